@@ -15,3 +15,12 @@ from .api import (  # noqa: F401
     workspace,
     workspace_size,
 )
+from .paged import (  # noqa: F401
+    attention_decode_latent,
+    attention_decode_paged,
+    pages_compact,
+    pages_copy,
+    pages_extend,
+    pages_fork,
+    pages_free,
+)

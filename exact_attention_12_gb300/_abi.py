@@ -15,6 +15,8 @@ ATTN_ERR_UNSUPPORTED = 2
 ATTN_ERR_CUDA = 3
 ATTN_ERR_TIMEOUT = 4
 ATTN_ERR_WORKSPACE = 5
+ATTN_ERR_PAGE = 6
+ATTN_ERR_FULL = 7
 
 ATTN_BF16 = 0
 ATTN_FP32 = 1
@@ -36,6 +38,30 @@ EXPORTS = {
     "attn_decode_workspace_size": (ctypes.c_size_t, [ctypes.c_void_p, ctypes.c_int32]),
     "attn_decode": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32] + [ctypes.c_void_p] * 6
                     + [ctypes.c_size_t, ctypes.c_void_p]),
+    "attn_decode_paged_workspace_size": (ctypes.c_size_t, [ctypes.c_void_p, ctypes.c_int32,
+                                                           ctypes.c_void_p]),
+    "attn_decode_paged": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32] + [ctypes.c_void_p] * 7
+                          + [ctypes.c_size_t, ctypes.c_void_p]),
+    "attn_decode_latent_workspace_size": (ctypes.c_size_t, [ctypes.c_void_p, ctypes.c_int32,
+                                                            ctypes.c_void_p]),
+    "attn_decode_latent": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32] + [ctypes.c_void_p] * 6
+                           + [ctypes.c_size_t, ctypes.c_void_p]),
+    "attn_pages_workspace_size": (ctypes.c_size_t, [ctypes.c_void_p, ctypes.c_int32]),
+    "attn_pages_copy": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
+                                       ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                                       ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "attn_pages_extend": (ctypes.c_int, [ctypes.c_void_p] * 3 + [ctypes.c_int32, ctypes.c_void_p,
+                                                                 ctypes.c_size_t,
+                                                                 ctypes.c_void_p]),
+    "attn_pages_fork": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                                       ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                                       ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                                       ctypes.c_void_p]),
+    "attn_pages_free": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                                       ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "attn_pages_compact": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                                          ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                                          ctypes.c_void_p]),
     "attn_selftest_timeout": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p]),
     "attn_debug_stall": (ctypes.c_int, [ctypes.c_int32, ctypes.c_uint64]),
     "attn_check": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
@@ -62,6 +88,33 @@ class AttnParams(ctypes.Structure):
         ("q_descale", ctypes.c_float), ("k_descale", ctypes.c_float),
         ("v_descale", ctypes.c_float), ("reserved2", ctypes.c_int32),
     ]
+
+
+class AttnPages(ctypes.Structure):
+    """Mirror of `attn_pages`."""
+
+    _fields_ = [
+        ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+        ("max_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32), ("shared_len", ctypes.c_int32),
+    ]
+
+
+class AttnPageTable(ctypes.Structure):
+    """Mirror of `attn_page_table`."""
+
+    _fields_ = [
+        ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("lens", ctypes.c_void_p),
+        ("refs", ctypes.c_void_p), ("rows", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+    ]
+
+
+class AttnPool(ctypes.Structure):
+    """Mirror of `attn_pool`."""
+
+    _fields_ = [("base", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("page_bytes", ctypes.c_int64)]
 
 
 class AttnError(RuntimeError):

@@ -10,6 +10,7 @@
 
 #include "attn.h"
 #include "attn_kernels.cuh"
+#include "attn_paged.cuh"
 
 namespace {
 
@@ -406,6 +407,13 @@ int attn::record_error(int status, const char* msg) {
   return static_cast<int>(fail(static_cast<attn_status>(status), "%s", msg));
 }
 
+int attn::encode_pages(CUtensorMap* map, const void* ptr, int num_pages, int heads, int page_size,
+                       int d, int64_t stride_p, int64_t stride_h, int64_t stride_n, int box_rows) {
+  return static_cast<int>(make_map(map, ptr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, num_pages, heads,
+                                   page_size, d, stride_p, stride_h, stride_n, 64, box_rows,
+                                   CU_TENSOR_MAP_SWIZZLE_128B));
+}
+
 extern "C" {
 
 size_t attn_workspace_size(const attn_params* p, int for_backward) {
@@ -790,6 +798,8 @@ const char* attn_status_string(attn_status s) {
     case ATTN_ERR_CUDA: return "CUDA error";
     case ATTN_ERR_TIMEOUT: return "device wait timed out";
     case ATTN_ERR_WORKSPACE: return "bad workspace";
+    case ATTN_ERR_PAGE: return "page index out of range";
+    case ATTN_ERR_FULL: return "no free page left";
   }
   return "unknown status";
 }

@@ -1,0 +1,541 @@
+// Decode step against a paged key/value cache.
+//
+// What it computes: the decode step of attn_decode.cu (query row t of
+// sequence b at position len_b - n_q + t attends the cached keys j < len_b,
+// j <= its position when causal; O = softmax(c q K^T) V, L = logsumexp) with
+// key j of sequence b in row j mod s of page table[b][j / s].
+//
+// Bound: HBM.  Every cached key and value is read once, 4 d bytes a key, for
+// 4 d rows operations: 1 to 64 operations a byte at 1 to 64 rows, below the
+// ridge of 277.  So what counts is that all SMs stream all the time:
+//   * the keys of all sequences are divided evenly over a fixed number of
+//     CTAs (two per SM) by their real lengths (attn_paged.cuh), which makes
+//     the step as fast for ragged batches as for even ones, and leaves at
+//     most two partial results per CTA however long the caches are;
+//   * each warp streams its own 32-key tiles of K and V by TMA through its
+//     own ring, a page's rows at a time, the page indices prefetched 32 tiles
+//     at a time, and the first tiles of the next segment are on their way
+//     before the write-out of the last one begins;
+//   * the two products are 16 x 8 x 16 warp MMAs: with at most 64 rows a
+//     128-row tcgen05 tile would be mostly padding, and the products' time is
+//     hidden behind the copies.  Above 16 rows MT = 2 or 4 warps share a tile,
+//     16 rows each.
+// Values of rows past the end of a sequence may be anything, infinities and
+// NaN included: their scores are replaced, not added to, and their value
+// rows are zeroed in shared memory before the product (0 * NaN is NaN).
+// P is rounded to bf16 for the second product (relative 2^-8 per element;
+// the row sums are of the unrounded fp32 values), m, l, O are fp32.
+#include "attn_paged.cuh"
+
+namespace attn {
+using namespace sm103;
+
+namespace {
+
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr int kSlots = 3;   // tiles worked on at a time by a CTA
+
+template <int D, int MT>
+struct PagedCfg {
+  static constexpr int kWarps = kSlots * MT;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kKeys = kPagedKeys;
+  static constexpr int kBoxes = D / 64;
+  static constexpr int kBoxBytes = kKeys * 128;
+  static constexpr int kTileBytes = kKeys * D * 2;
+  // four row tiles leave one CTA per SM, which then has twice the stages
+  static constexpr int kCtasPerSm = MT == 4 ? 1 : 2;
+  static constexpr int kStages = (D == 128 ? 2 : 4) * (MT == 4 ? 2 : 1);   // per slot
+  static constexpr int kRingBytes = 2 * kSlots * kStages * kTileBytes;
+  static constexpr int kRedStride = D + 8;   // floats; the pad spreads the rows over the banks
+  static constexpr int kRedBytes = 16 * kRedStride * 4;
+  static constexpr int kSmem = 1024 + kRingBytes + kRedBytes;
+  static_assert(kCtasPerSm * (kSmem + 1024 + 2560) <= 228 * 1024, "shared memory of an SM");
+};
+
+template <int D, int MT>
+struct PagedShared {
+  uint64_t full[kSlots * PagedCfg<D, MT>::kStages];
+  uint64_t empty[kSlots * PagedCfg<D, MT>::kStages];
+  float m[kSlots][MT * 16], l[kSlots][MT * 16];
+  int64_t sums[PagedCfg<D, MT>::kWarps];
+  PagedShare share;
+  int abort_flag;
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2,
+                                      uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(addr)
+               : "memory");
+}
+
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2,
+                                        uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(addr)
+               : "memory");
+}
+
+// c += a b, 16 x 8 x 16, bf16 inputs, fp32 accumulators
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// A row's final O (four columns) and L from its own partial (o, L) and the
+// shared prefix's.  L = log sum e^(L_s), O = sum e^(L_s - L) O_s.
+template <int D>
+__device__ __forceinline__ float fold_prefix(const PagedArgs& a, int64_t row, int c, float L,
+                                             float4& o) {
+  if (a.pre_splits == 0) return L;
+  const int64_t rows = static_cast<int64_t>(a.B) * a.H * a.n_q;
+  float top = L;
+  for (int s = 0; s < a.pre_splits; ++s) top = fmaxf(top, a.pre_l[s * rows + row]);
+  if (top == -INFINITY) return L;
+  const float w0 = __expf(L - top);   // L = -inf: weight 0
+  float sum = w0;
+  o.x *= w0;
+  o.y *= w0;
+  o.z *= w0;
+  o.w *= w0;
+  for (int s = 0; s < a.pre_splits; ++s) {
+    const float w = __expf(a.pre_l[s * rows + row] - top);
+    const float4 x = *reinterpret_cast<const float4*>(a.pre_o + (s * rows + row) * D + c);
+    sum += w;
+    o.x = fmaf(w, x.x, o.x);
+    o.y = fmaf(w, x.y, o.y);
+    o.z = fmaf(w, x.z, o.z);
+    o.w = fmaf(w, x.w, o.w);
+  }
+  const float inv = 1.f / sum;
+  o.x *= inv;
+  o.y *= inv;
+  o.z *= inv;
+  o.w *= inv;
+  return top + __logf(sum);
+}
+
+template <int D, int MT>
+__global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kCtasPerSm)
+    paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                 const PagedArgs a) {
+  using C = PagedCfg<D, MT>;
+  constexpr int ST = C::kStages, KT = C::kKeys, NT = D / 8;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  float* red = reinterpret_cast<float*>(smem + C::kRingBytes);   // [16][kRedStride]
+  __shared__ PagedShared<D, MT> sh;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int slot = warp / MT, mt = warp % MT;   // which tiles, which 16 rows
+  auto sK = [&](int st) { return smem + (slot * ST + st) * 2 * C::kTileBytes; };
+  auto sV = [&](int st) { return sK(st) + C::kTileBytes; };
+
+  if (threadIdx.x == 0) {
+    sh.abort_flag = 0;
+    for (int s = 0; s < kSlots * ST; ++s) {
+      mbar_init(&sh.full[s], 1);
+      mbar_init(&sh.empty[s], MT);
+    }
+    fence_mbar_init();
+    tma_prefetch_desc(&tk);
+    tma_prefetch_desc(&tv);
+  }
+  __syncthreads();
+  grid_dep_wait();
+  grid_dep_launch();
+  const PagedShare share = paged_share<C::kThreads, KT, kPagedOverhead>(
+      a, blockIdx.x, gridDim.x, sh.sums, &sh.share);
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.starts[a.B] = share.total;
+  const WaitCtx wc{&sh.abort_flag, a.status, a.timeout_ns};
+  const int box_rows = min(KT, 1 << a.page_shift);
+  bool ok = true;
+
+  // ---- the copies: tile u of this slot is tile t0 + slot + kSlots u of the
+  // piece; lane l of the issuing warp holds the page indices of tile
+  // 32 * (batch) + l (two where a tile spans two 16-key pages)
+  uint32_t issued = 0, done = 0;   // tiles of this slot issued / used, over all pieces
+  int page_of[2] = {0, 0};
+  auto slot_tiles = [&](const PagedPiece& p) {
+    const int n = p.t1 - p.t0 - slot;
+    return n > 0 ? (n + kSlots - 1) / kSlots : 0;
+  };
+  auto load_pages = [&](const PagedPiece& p, int u0, int nu) {
+    const int u = u0 + lane;
+    if (u < nu) {
+      const int key = a.first + (p.t0 + slot + kSlots * u) * KT;
+      const int32_t* row = a.table + p.b * a.table_stride;
+      page_of[0] = checked_page(row[key >> a.page_shift], a.num_pages, a.status);
+      // (a page of 16 keys: the tile's second half, where the sequence reaches it)
+      page_of[1] = box_rows == KT || key + box_rows >= p.len
+                       ? page_of[0]
+                       : checked_page(row[(key >> a.page_shift) + 1], a.num_pages, a.status);
+    }
+  };
+  auto issue = [&](const PagedPiece& p, int u) {   // the whole issuing warp
+    const int pg0 = __shfl_sync(0xffffffffu, page_of[0], u & 31);
+    const int pg1 = __shfl_sync(0xffffffffu, page_of[1], u & 31);
+    const int st = issued % ST;
+    if (MT > 1 && issued >= ST) {   // the slot's warps are done with the stage
+      ok = __all_sync(0xffffffffu, mbar_wait(&sh.empty[slot * ST + st], ((issued / ST) - 1) & 1, wc,
+                                             kSitePagedFree));
+      if (!ok) return;
+    }
+    if (lane == 0) {
+      uint64_t* bar = &sh.full[slot * ST + st];
+      const int row = (a.first + (p.t0 + slot + kSlots * u) * KT) & ((1 << a.page_shift) - 1);
+      fence_proxy_async_smem();
+      mbar_arrive_expect_tx(bar, 2 * C::kTileBytes);
+#pragma unroll
+      for (int x = 0; x < C::kBoxes; ++x) {
+        tma_load_4d(sK(st) + x * C::kBoxBytes, &tk, bar, x * 64, row, p.h, pg0);
+        tma_load_4d(sV(st) + x * C::kBoxBytes, &tv, bar, x * 64, row, p.h, pg0);
+        if (box_rows < KT) {
+          tma_load_4d(sK(st) + x * C::kBoxBytes + 16 * 128, &tk, bar, x * 64, 0, p.h, pg1);
+          tma_load_4d(sV(st) + x * C::kBoxBytes + 16 * 128, &tv, bar, x * 64, 0, p.h, pg1);
+        }
+      }
+    }
+    ++issued;
+  };
+  auto prefetch = [&](const PagedPiece& p) {   // the first tiles of a piece
+    if (mt != 0 || !p.valid) return;
+    const int nu = slot_tiles(p);
+    if (nu == 0) return;
+    load_pages(p, 0, nu);
+    for (int u = 0; ok && u < ST && u < nu; ++u) issue(p, u);
+  };
+
+  const int g = lane >> 2, q4 = lane & 3;
+  const int rows[2] = {mt * 16 + g, mt * 16 + g + 8};
+  const int lb = lane >> 3, lr = lane & 7;
+  const float c2 = a.scale_log2;
+
+  PagedPiece p = paged_piece<KT, kPagedOverhead>(a, share, share.b, 0, share.s, threadIdx.x == 0);
+  prefetch(p);
+  while (p.valid) {   // (the same pieces in every warp)
+    const int nu = slot_tiles(p);
+    // Q fragments of rows g and g + 8 of the warp's 16 (zero past the last row)
+    uint32_t qa[D / 16][4];
+    int lim[2];   // keys below lim are allowed
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = rows[i];
+      const bool live = r < a.rows;
+      const int hl = r / a.n_q, qt = r - hl * a.n_q;
+      const __nv_bfloat16* qr = a.q + p.b * a.stride_b + (p.h * a.group + hl) * a.stride_h +
+                                static_cast<int64_t>(qt) * a.stride_n;
+      lim[i] = !live ? 0 : (a.causal ? min(p.len, p.len - a.n_q + qt + 1) : p.len);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        qa[kk][i] = live ? *reinterpret_cast<const uint32_t*>(qr + kk * 16 + 2 * q4) : 0u;
+        qa[kk][i + 2] = live ? *reinterpret_cast<const uint32_t*>(qr + kk * 16 + 8 + 2 * q4) : 0u;
+      }
+    }
+    const int open = a.causal ? p.len - a.n_q + 1 : p.len;   // every row is allowed keys below it
+    float mrow[2] = {-INFINITY, -INFINITY}, lrow[2] = {0.f, 0.f};
+    float o[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+
+    for (int u = 0; ok && u < nu; ++u) {
+      const int st = done % ST;
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sh.full[slot * ST + st], (done / ST) & 1, wc,
+                                                   kSitePagedTile))))
+        break;
+      const uint32_t kb = smem_u32(sK(st)), vb = smem_u32(sV(st));
+      const int k0 = a.first + (p.t0 + slot + kSlots * u) * KT;
+      if (k0 + KT > p.len) {   // value rows past the end: zero
+        const int from = p.len - k0;
+        for (int i = lane; i < (KT - from) * (D / 8); i += 32) {
+          const int key = from + i / (D / 8), c8 = i % (D / 8);
+          *reinterpret_cast<uint4*>(sV(st) + (c8 >> 3) * C::kBoxBytes + key * 128 +
+                                    ((c8 & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        __syncwarp();
+      }
+      // S = Q K^T: per 16 columns of d one ldmatrix.x4 gives two key blocks of 8
+      float sc[KT / 8][4];
+#pragma unroll
+      for (int n = 0; n < KT / 8; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+        for (int n = 0; n < KT / 8; n += 2) {
+          const int key = 8 * n + 8 * (lb >> 1) + lr, col = 16 * kk + 8 * (lb & 1);
+          uint32_t b0, b1, b2, b3;
+          ldsm4(kb + (col >> 6) * C::kBoxBytes + key * 128 + ((((col & 63) >> 3) ^ (key & 7)) << 4),
+                b0, b1, b2, b3);
+          mma16816(sc[n], qa[kk], b0, b1);
+          mma16816(sc[n + 1], qa[kk], b2, b3);
+        }
+      if (k0 + KT > open) {
+#pragma unroll
+        for (int n = 0; n < KT / 8; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (k0 + 8 * n + 2 * q4 + (e & 1) >= lim[e >> 1]) sc[n][e] = -INFINITY;
+      }
+      float tmax[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int n = 0; n < KT / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) tmax[e >> 1] = fmaxf(tmax[e >> 1], sc[n][e]);
+      float alpha[2], base[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        tmax[i] = fmaxf(tmax[i], __shfl_xor_sync(0xffffffffu, tmax[i], 1));
+        tmax[i] = fmaxf(tmax[i], __shfl_xor_sync(0xffffffffu, tmax[i], 2));
+        const float mn = fmaxf(mrow[i], tmax[i]);
+        base[i] = mn == -INFINITY ? 0.f : mn * c2;   // -inf: no allowed key seen yet
+        alpha[i] = mrow[i] == -INFINITY ? 0.f : ex2_approx(mrow[i] * c2 - base[i]);
+        mrow[i] = mn;
+      }
+      // P = 2^(S c - m c) as bf16 A fragments; row sums from the same fp32 values
+      uint32_t pa[KT / 16][4];
+      float psum[2] = {0.f, 0.f};
+#pragma unroll
+      for (int n = 0; n < KT / 8; ++n) {
+        const float p0 = ex2_approx(fmaf(sc[n][0], c2, -base[0]));
+        const float p1 = ex2_approx(fmaf(sc[n][1], c2, -base[0]));
+        const float p2 = ex2_approx(fmaf(sc[n][2], c2, -base[1]));
+        const float p3 = ex2_approx(fmaf(sc[n][3], c2, -base[1]));
+        psum[0] += p0 + p1;
+        psum[1] += p2 + p3;
+        pa[n >> 1][(n & 1) * 2] = pack_bf16x2(p0, p1);
+        pa[n >> 1][(n & 1) * 2 + 1] = pack_bf16x2(p2, p3);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) lrow[i] = lrow[i] * alpha[i] + psum[i];
+      if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          o[n][0] *= alpha[0];
+          o[n][1] *= alpha[0];
+          o[n][2] *= alpha[1];
+          o[n][3] *= alpha[1];
+        }
+      }
+#pragma unroll
+      for (int kp = 0; kp < KT / 16; ++kp)
+#pragma unroll
+        for (int n = 0; n < NT; n += 2) {
+          const int key = 16 * kp + 8 * (lb & 1) + lr, col = 8 * n + 8 * (lb >> 1);
+          uint32_t b0, b1, b2, b3;
+          ldsm4_t(vb + (col >> 6) * C::kBoxBytes + key * 128 +
+                      ((((col & 63) >> 3) ^ (key & 7)) << 4),
+                  b0, b1, b2, b3);
+          mma16816(o[n], pa[kp], b0, b1);
+          mma16816(o[n + 1], pa[kp], b2, b3);
+        }
+      ++done;
+      __syncwarp();
+      if (MT > 1 && lane == 0) mbar_arrive(&sh.empty[slot * ST + st]);
+      if (mt == 0 && u + ST < nu) {   // refill the stage with the slot's tile u + ST
+        if (((u + ST) & 31) == 0) load_pages(p, u + ST, nu);
+        issue(p, u + ST);
+      }
+    }
+
+    const PagedPiece next = paged_next<KT, kPagedOverhead>(a, share, p, threadIdx.x == 0);
+    if (ok) prefetch(next);
+
+    // ---- the slots' states merged: m, l per row, then O through shared memory
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      lrow[i] += __shfl_xor_sync(0xffffffffu, lrow[i], 1);
+      lrow[i] += __shfl_xor_sync(0xffffffffu, lrow[i], 2);
+      if (q4 == 0) {
+        sh.m[slot][rows[i]] = mrow[i];
+        sh.l[slot][rows[i]] = lrow[i];
+      }
+    }
+    ok = __syncthreads_and(ok);
+    float scale[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float mx = -INFINITY, lt = 0.f;
+#pragma unroll
+      for (int w = 0; w < kSlots; ++w) mx = fmaxf(mx, sh.m[w][rows[i]]);
+#pragma unroll
+      for (int w = 0; w < kSlots; ++w) {
+        const float mw = sh.m[w][rows[i]];
+        if (mw != -INFINITY) lt += sh.l[w][rows[i]] * ex2_approx((mw - mx) * c2);
+      }
+      // this slot's weight, with the 1 / l folded in
+      scale[i] = mrow[i] == -INFINITY ? 0.f : ex2_approx((mrow[i] - mx) * c2) / lt;
+    }
+    const bool whole = p.whole();
+    const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (p.s < share.lo ? 0 : 1);
+    for (int m = 0; m < MT; ++m) {   // 16 rows at a time
+      for (int w = 0; w < kSlots; ++w) {   // in turn: the sum has a fixed order
+        if (slot == w && mt == m) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float2* dst = reinterpret_cast<float2*>(&red[(g + 8 * i) * C::kRedStride + 8 * n + 2 * q4]);
+              float2 x = make_float2(o[n][2 * i] * scale[i], o[n][2 * i + 1] * scale[i]);
+              if (w > 0) {
+                const float2 y = *dst;
+                x.x += y.x;
+                x.y += y.y;
+              }
+              *dst = x;
+            }
+        }
+        __syncthreads();
+      }
+      for (int e = threadIdx.x; e < min(16, a.rows - 16 * m) * (D / 4); e += C::kThreads) {
+        const int rr = e / (D / 4), c = 4 * (e - rr * (D / 4)), r = 16 * m + rr;
+        float mx = -INFINITY, lt = 0.f;
+#pragma unroll
+        for (int w = 0; w < kSlots; ++w) mx = fmaxf(mx, sh.m[w][r]);
+#pragma unroll
+        for (int w = 0; w < kSlots; ++w) {
+          const float mw = sh.m[w][r];
+          if (mw != -INFINITY) lt += sh.l[w][r] * ex2_approx((mw - mx) * c2);
+        }
+        float L = lt > 0.f ? (mx * c2 + __log2f(lt)) * kLn2 : -INFINITY;
+        float4 x = *reinterpret_cast<const float4*>(&red[rr * C::kRedStride + c]);
+        if (whole) {
+          const int hl = r / a.n_q, qt = r - hl * a.n_q, h = p.h * a.group + hl;
+          const int64_t row = (static_cast<int64_t>(p.b) * a.H + h) * a.n_q + qt;
+          L = fold_prefix<D>(a, row, c, L, x);
+          *reinterpret_cast<uint2*>(a.o + p.b * a.stride_b + h * a.stride_h +
+                                    static_cast<int64_t>(qt) * a.stride_n + c) =
+              make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+          if (c == 0) a.lse[row] = L;
+        } else {
+          *reinterpret_cast<float4*>(a.part_o + (part * a.rows + r) * D + c) = x;
+          if (c == 0) a.part_l[part * a.rows + r] = L;
+        }
+      }
+      __syncthreads();   // red (and after the last rows m, l) is free
+    }
+    if (!ok) break;
+    p = next;
+  }
+  if (!ok && mt == 0 && lane == 0) {   // let issued copies land before the CTA exits
+    for (uint32_t t = issued > ST ? issued - ST : 0; t < issued; ++t)
+      mbar_wait_drain(&sh.full[slot * ST + t % ST], (t / ST) & 1, a.timeout_ns);
+  }
+}
+
+// Segments that were cut: their pieces merged, four columns of a row per
+// thread.  A CTA per (segment, 128 of its rows x columns / 4).
+template <int D>
+__global__ void __launch_bounds__(128)
+    paged_merge_kernel(const PagedArgs a, int keys, int overhead, int launched) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int b = blockIdx.x / a.heads, h = blockIdx.x - b * a.heads;
+  const int64_t total = a.starts[a.B];
+  const int len = paged_len(a, b) - a.first;
+  const int n = len > 0 ? (len + keys - 1) / keys : 0;
+  if (n == 0) return;   // written by the CTA that owns it
+  const int64_t s = a.starts[b] + static_cast<int64_t>(h) * (n + overhead);
+  const int ctas = paged_ctas(total, launched);
+  auto owner = [&](int64_t unit) {
+    int i = static_cast<int>(unit * ctas / total);
+    while (total * (i + 1) / ctas <= unit) ++i;
+    while (total * i / ctas > unit) --i;
+    return i;
+  };
+  const int i0 = owner(s + overhead), i1 = owner(s + overhead + n - 1);
+  if (i0 == i1) return;   // finished by that CTA
+  const int rows = min(a.rows, a.all_rows - h * a.rows);
+  const int e = blockIdx.y * 128 + threadIdx.x;
+  const int r = e / (D / 4), c = 4 * (e - r * (D / 4));
+  if (r >= rows) return;
+  // the CTAs between hold one piece each, of a segment begun before them
+  auto slot_of = [&](int i) {
+    return 2 * static_cast<int64_t>(i) + (i == i0 && s >= total * i0 / ctas ? 1 : 0);
+  };
+  float top = -INFINITY;
+#pragma unroll 4
+  for (int i = i0; i <= i1; ++i) top = fmaxf(top, a.part_l[slot_of(i) * a.rows + r]);
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  float L = -INFINITY;
+  if (top > -INFINITY) {
+    float sum = 0.f;
+#pragma unroll 4
+    for (int i = i0; i <= i1; ++i) {
+      const int64_t at = slot_of(i) * a.rows + r;
+      const float w = __expf(a.part_l[at] - top);
+      const float4 y = *reinterpret_cast<const float4*>(a.part_o + at * D + c);
+      sum += w;
+      x.x = fmaf(w, y.x, x.x);
+      x.y = fmaf(w, y.y, x.y);
+      x.z = fmaf(w, y.z, x.z);
+      x.w = fmaf(w, y.w, x.w);
+    }
+    const float inv = 1.f / sum;
+    x.x *= inv;
+    x.y *= inv;
+    x.z *= inv;
+    x.w *= inv;
+    L = top + __logf(sum);
+  }
+  const int64_t row0 = static_cast<int64_t>(b) * a.all_rows;
+  const int hr = h * a.rows + r;   // row of the sequence: head * n_q + query
+  L = fold_prefix<D>(a, row0 + hr, c, L, x);
+  const int hq = hr / a.n_q, qt = hr - hq * a.n_q;
+  *reinterpret_cast<uint2*>(a.o + b * a.stride_b + hq * a.stride_h +
+                            static_cast<int64_t>(qt) * a.stride_n + c) =
+      make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+  if (c == 0) a.lse[row0 + hr] = L;
+}
+
+template <int D, int MT>
+cudaError_t launch_mt(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, int ctas,
+                      cudaStream_t s) {
+  using C = PagedCfg<D, MT>;
+  static std::atomic<uint64_t> set_up{0};
+  int dev = 0;
+  bool todo = false;
+  cudaError_t e = needs_setup(set_up, &dev, &todo);
+  if (e != cudaSuccess) return e;
+  if (todo) {
+    e = cudaFuncSetAttribute(paged_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             C::kSmem);
+    if (e != cudaSuccess) return e;
+    mark_done(set_up, dev);
+  }
+  return launch_pdl(paged_kernel<D, MT>, dim3(ctas), dim3(C::kThreads), C::kSmem, s, tk, tv, a);
+}
+
+template <int D>
+cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, int ctas,
+                     cudaStream_t s) {
+  if (a.rows <= 16) return launch_mt<D, 1>(tk, tv, a, ctas, s);
+  if (a.rows <= 32) return launch_mt<D, 2>(tk, tv, a, ctas, s);
+  return launch_mt<D, 4>(tk, tv, a, ctas, s);
+}
+
+}  // namespace
+
+cudaError_t launch_paged(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, int ctas,
+                         cudaStream_t s) {
+  return a.d == 64 ? launch_d<64>(tk, tv, a, ctas, s) : launch_d<128>(tk, tv, a, ctas, s);
+}
+
+cudaError_t launch_paged_merge(const PagedArgs& a, int keys, int overhead, int ctas,
+                               cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>(a.B * a.heads),
+                  static_cast<unsigned>((a.rows * (a.d / 4) + 127) / 128));
+  auto kernel = a.d == 64    ? paged_merge_kernel<64>
+                : a.d == 128 ? paged_merge_kernel<128>
+                : a.d == 256 ? paged_merge_kernel<256>
+                             : paged_merge_kernel<512>;
+  return launch_pdl(kernel, grid, dim3(128), 0, s, a, keys, overhead, ctas);
+}
+
+}  // namespace attn

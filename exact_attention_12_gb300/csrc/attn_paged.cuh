@@ -1,0 +1,252 @@
+// Kernel argument blocks, launchers and the work split of the kernels that
+// read a paged key/value cache: the paged decode step (attn_paged.cu), its
+// shared prefix (attn_prefix.cu) and the latent decode step (attn_latent.cu).
+#pragma once
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "attn_kernels.cuh"
+#include "sm103.cuh"
+
+namespace attn {
+
+// Device status code of a page index outside the cache (equals ATTN_ERR_PAGE
+// in attn.h).  The page reads as zeros.
+constexpr int kStatusPage = 6;
+
+// The split of a decode step over its CTAs.  The problem is a list of
+// segments, one per (sequence, head group), sequence by sequence; a segment
+// of n key tiles costs n + overhead units (its set-up and write-out, in
+// tiles).  CTA i of G takes the units [i T / G, (i + 1) T / G) of the T in
+// all: every CTA gets the same share whatever the lengths are, and no CTA is
+// launched for keys a short sequence does not have.  A segment that falls to
+// one CTA is finished by it; one that is cut leaves a partial (O, L) per CTA,
+// merged afterwards by the logsumexp rule.  A CTA cuts at most its first and
+// its last segment, so it has two partial slots: slot 0 for a segment that
+// began before the CTA's range, slot 1 for one that begins in it.
+struct PagedArgs {
+  int B, H, heads;                // heads: segments per sequence
+  int group;                      // query heads per segment
+  int n_q, rows;                  // query rows per segment: group * n_q (the last latent
+                                  // segment of a sequence may have fewer)
+  int all_rows;                   // latent: H * n_q
+  int causal, d;
+  const int32_t* key_lens;        // [B]
+  const int32_t* table;           // [B][table_stride]
+  int64_t table_stride;
+  int cap;                        // keys a row of the table can name
+  int page_shift, num_pages;
+  int first;                      // keys below it are left out (they are the shared prefix)
+  float scale_log2;
+  const __nv_bfloat16* q;
+  int64_t stride_b, stride_h, stride_n;      // q (and o, but for latent)
+  __nv_bfloat16* o;
+  float* lse;                     // [B][H][n_q]
+  int64_t* starts;                // workspace [B + 1]: the first unit of each sequence, then T
+  float* part_o;                  // workspace [2 G][rows][d]
+  float* part_l;                  // workspace [2 G][rows]
+  // the shared prefix's partials (pre_splits = 0: none)
+  const float* pre_o;             // workspace [pre_splits][B*H*n_q][d]
+  const float* pre_l;             // workspace [pre_splits][B*H*n_q]
+  int pre_splits;
+  int* status;
+  uint64_t timeout_ns;
+};
+
+struct PrefixArgs {
+  int B, H, H_kv, group, n_q, causal, d;
+  const int32_t* key_lens;
+  const int32_t* table;           // row 0 names the prefix
+  int cap;                        // keys a row of the table can name
+  int page_shift, num_pages;
+  int shared_len;
+  int splits, tiles;              // pieces of the prefix; 128-key tiles in all
+  int rows;                       // B * group * n_q: query rows of one key/value head
+  float scale_log2;
+  const __nv_bfloat16* q;
+  int64_t stride_b, stride_h, stride_n;
+  float* pre_o;
+  float* pre_l;
+  int* status;
+  uint64_t timeout_ns;
+};
+
+constexpr int kPagedKeys = 32;        // keys per tile of the paged decode kernel
+constexpr int kPagedOverhead = 4;     // a segment's fixed cost in such tiles
+constexpr int kPagedMinUnits = 6;     // units a CTA takes at least
+constexpr int kLatentKeys = 64;       // keys per tile of the latent kernel
+constexpr int kLatentOverhead = 3;
+constexpr int kLatentRows = 64;       // query rows of one CTA
+constexpr int kLatentRope = 64;       // columns of a latent vector that are not values
+
+enum PagedSite : int {
+  kSitePagedTile = 60, kSitePagedFree, kSitePrefixQ, kSitePrefixK, kSitePrefixV, kSitePrefixS,
+  kSitePrefixP, kSitePrefixFree, kSitePrefixDone,
+  kSiteLatentTile = 70, kSiteLatentS, kSiteLatentP, kSiteLatentFree, kSiteLatentDone, kSiteLatentQ,
+  kSitePageIndex = 80
+};
+
+__device__ __forceinline__ int paged_len(const PagedArgs& a, int b) {
+  return min(max(a.key_lens[b], 0), a.cap);
+}
+
+// Key tiles of one segment of sequence b.
+template <int KEYS>
+__device__ __forceinline__ int paged_tiles(const PagedArgs& a, int b) {
+  const int n = paged_len(a, b) - a.first;
+  return n > 0 ? (n + KEYS - 1) / KEYS : 0;
+}
+
+// The page that holds key `key` of a table row; an index outside the cache is
+// recorded and read as the (all-zero) page past the last one.
+__device__ __forceinline__ int checked_page(int page, int num_pages, int* status) {
+  if (static_cast<unsigned>(page) < static_cast<unsigned>(num_pages)) return page;
+  if (status != nullptr && atomicCAS(status, 0, kStatusPage) == 0)
+    atomicExch(status + 1, kSitePageIndex);
+  return max(num_pages, 1);   // (the tensor map of an empty cache has one page)
+}
+
+// CTAs that share T units when `launched` are there.
+__device__ __forceinline__ int paged_ctas(int64_t total, int launched) {
+  const int64_t most = total / kPagedMinUnits;
+  return most >= launched ? launched : max(1, static_cast<int>(most));
+}
+
+// A CTA's share [lo, hi) of the T units, and where it starts.
+struct PagedShare {
+  int64_t lo, hi, total;
+  int b;          // the sequence that holds unit lo
+  int64_t s;      // its first unit
+};
+
+// All threads of the CTA; `sums` has THREADS / 32 entries of shared memory.
+// Thread t adds up a run of consecutive sequences, the runs' sums are
+// scanned, and the thread whose run holds unit lo walks it.
+template <int THREADS, int KEYS, int OVERHEAD>
+__device__ __forceinline__ PagedShare paged_share(const PagedArgs& a, int cta, int launched,
+                                                  int64_t* sums, PagedShare* out) {
+  const int per = (a.B + THREADS - 1) / THREADS;
+  const int b0 = min(static_cast<int>(threadIdx.x) * per, a.B), b1 = min(b0 + per, a.B);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b)
+    mine += static_cast<int64_t>(a.heads) * (paged_tiles<KEYS>(a, b) + OVERHEAD);
+  // inclusive scan over the warp, then over the warps
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  if (lane == 31) sums[warp] = inc;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) before += sums[w];
+    total += sums[w];
+  }
+  inc += before;
+  PagedShare sh;
+  sh.total = total;
+  const int ctas = paged_ctas(total, launched);
+  if (cta >= ctas) {   // (uniform over the CTA)
+    sh.lo = sh.hi = sh.s = total;
+    sh.b = a.B;
+    return sh;
+  }
+  sh.lo = total * cta / ctas;
+  sh.hi = total * (cta + 1) / ctas;
+  if (inc - mine <= sh.lo && sh.lo < inc) {
+    int64_t s = inc - mine;
+    int b = b0;
+    for (;; ++b) {
+      const int64_t c = static_cast<int64_t>(a.heads) * (paged_tiles<KEYS>(a, b) + OVERHEAD);
+      if (sh.lo < s + c || b + 1 >= b1) break;
+      s += c;
+    }
+    out->b = b;
+    out->s = s;
+  }
+  __syncthreads();
+  sh.b = out->b;
+  sh.s = out->s;
+  return sh;
+}
+
+// One CTA's piece of a segment: key tiles [t0, t1) of the n tiles of segment
+// (b, h), whose first unit is s.
+struct PagedPiece {
+  int b, h, n, len;
+  int64_t s;
+  int t0, t1;
+  bool valid;
+  // this CTA alone has the segment
+  __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == n; }
+};
+
+template <int OVERHEAD>
+__device__ __forceinline__ void paged_clip(PagedPiece& p, const PagedShare& sh) {
+  const int64_t first = p.s + OVERHEAD;   // unit of tile 0
+  p.t0 = sh.lo > first ? static_cast<int>(min(sh.lo - first, static_cast<int64_t>(p.n))) : 0;
+  p.t1 = static_cast<int>(max(static_cast<int64_t>(0), min(sh.hi - first, static_cast<int64_t>(p.n))));
+}
+
+// The first piece at or after segment (b, h) at unit s that gives this CTA
+// something to do: tiles, or the rows of an empty segment that begins here.
+// `note`: record the sequences' first units that lie in this CTA's range.
+template <int KEYS, int OVERHEAD>
+__device__ __forceinline__ PagedPiece paged_piece(const PagedArgs& a, const PagedShare& sh, int b,
+                                                  int h, int64_t s, bool note) {
+  PagedPiece p;
+  p.valid = false;
+  p.b = b;
+  p.h = h;
+  p.s = s;
+  if (b >= a.B) return p;
+  p.len = paged_len(a, b);
+  p.n = paged_tiles<KEYS>(a, b);
+  while (p.s < sh.hi) {
+    if (note && p.h == 0 && p.s >= sh.lo) a.starts[p.b] = p.s;
+    paged_clip<OVERHEAD>(p, sh);
+    if (p.t1 > p.t0 || (p.n == 0 && p.s >= sh.lo)) {
+      p.valid = true;
+      return p;
+    }
+    p.s += p.n + OVERHEAD;
+    if (++p.h == a.heads) {
+      p.h = 0;
+      if (++p.b == a.B) return p;
+      p.len = paged_len(a, p.b);
+      p.n = paged_tiles<KEYS>(a, p.b);
+    }
+  }
+  return p;
+}
+
+template <int KEYS, int OVERHEAD>
+__device__ __forceinline__ PagedPiece paged_next(const PagedArgs& a, const PagedShare& sh,
+                                                 const PagedPiece& p, bool note) {
+  int b = p.b, h = p.h + 1;
+  if (h == a.heads) {
+    h = 0;
+    ++b;
+  }
+  return paged_piece<KEYS, OVERHEAD>(a, sh, b, h, p.s + p.n + OVERHEAD, note);
+}
+
+cudaError_t launch_paged(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, int ctas,
+                         cudaStream_t s);
+cudaError_t launch_prefix(const CUtensorMap& tk, const CUtensorMap& tv, const PrefixArgs& a,
+                          cudaStream_t s);
+cudaError_t launch_latent(const CUtensorMap& tc, const PagedArgs& a, int ctas, cudaStream_t s);
+cudaError_t launch_paged_merge(const PagedArgs& a, int keys, int overhead, int ctas,
+                               cudaStream_t s);
+
+// Tensor map of a paged cache for the host code (an attn_status).
+int encode_pages(CUtensorMap* map, const void* ptr, int num_pages, int heads, int page_size, int d,
+                 int64_t stride_p, int64_t stride_h, int64_t stride_n, int box_rows);
+
+}  // namespace attn

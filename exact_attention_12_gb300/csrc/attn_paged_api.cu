@@ -1,0 +1,329 @@
+// Host side of the paged decode steps (attn_decode_paged, attn_decode_latent
+// in include/attn.h): argument checks, workspace layout, launches.
+#include <cmath>
+#include <cstdio>
+
+#include "attn.h"
+#include "attn_paged.cuh"
+
+namespace {
+
+using attn::PagedArgs;
+
+constexpr size_t kHeaderBytes = 256;
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+constexpr float kLog2e = 1.4426950408889634f;
+
+attn_status fail(attn_status s, const char* msg) {
+  return static_cast<attn_status>(attn::record_error(s, msg));
+}
+
+size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+    sms = 148;
+  return sms;
+}
+
+int log2_of(int x) {
+  int s = 0;
+  while ((1 << s) < x) ++s;
+  return s;
+}
+
+attn_status validate(const attn_params* p, int32_t n_q, const attn_pages* g, bool latent) {
+  if (p == nullptr || g == nullptr) return fail(ATTN_ERR_INVALID_ARG, "params or pages is NULL");
+  if (p->B < 0 || p->H < 0 || p->N < 0) return fail(ATTN_ERR_INVALID_ARG, "negative shape");
+  if (p->reserved != 0 || p->reserved2 != 0)
+    return fail(ATTN_ERR_INVALID_ARG, "reserved field must be 0");
+  if (p->dtype != ATTN_BF16)
+    return fail(p->dtype == ATTN_FP32 || p->dtype == ATTN_FP8_E4M3 ? ATTN_ERR_UNSUPPORTED
+                                                                   : ATTN_ERR_INVALID_ARG,
+                "paged decode is implemented for bf16");
+  if (latent ? (p->d != 256 && p->d != 512) : (p->d != 64 && p->d != 128))
+    return fail(ATTN_ERR_UNSUPPORTED, latent ? "latent decode: d must be 256 or 512"
+                                             : "paged decode: d must be 64 or 128");
+  if (!std::isfinite(p->scale) || !(p->scale > 0.f))
+    return fail(ATTN_ERR_INVALID_ARG, "scale must be positive and finite");
+  if (p->dropout_p != 0.f || p->block_mask != nullptr)
+    return fail(ATTN_ERR_UNSUPPORTED, "decode takes no dropout and no block mask");
+  if (p->key_lens == nullptr)
+    return fail(ATTN_ERR_INVALID_ARG, "decode needs key_lens (cache lengths)");
+  if (n_q < 1) return fail(ATTN_ERR_INVALID_ARG, "n_q must be >= 1");
+  const int H_kv = latent ? 1 : (p->H_kv == 0 ? p->H : p->H_kv);
+  if (latent ? (p->H_kv != 0 && p->H_kv != 1)
+             : (p->H_kv < 0 || (p->H > 0 && (H_kv < 1 || p->H % H_kv != 0))))
+    return fail(ATTN_ERR_INVALID_ARG, latent ? "latent decode: H_kv must be 0 or 1"
+                                             : "H_kv must divide H");
+  if (!latent && p->H > 0 && static_cast<int64_t>(p->H / H_kv) * n_q > attn::kDecMaxRows)
+    return fail(ATTN_ERR_UNSUPPORTED, "(H / H_kv) * n_q exceeds 64");
+  if (static_cast<int64_t>(p->H) * n_q > 32768 ||
+      static_cast<int64_t>(p->B) * p->H * n_q > (1 << 30))
+    return fail(ATTN_ERR_UNSUPPORTED, "more than 32768 query rows per sequence or 2^30 in all");
+  // pages
+  if (g->max_pages < 0 || g->num_pages < 0 || g->table_stride < g->max_pages)
+    return fail(ATTN_ERR_INVALID_ARG, "pages: negative size, or table_stride < max_pages");
+  if (g->page_size < 16 || g->page_size > 32768 || (g->page_size & (g->page_size - 1)) != 0)
+    return fail(ATTN_ERR_INVALID_ARG, "page_size must be a power of two, 16 to 32768");
+  const int64_t cap = static_cast<int64_t>(g->max_pages) * g->page_size;
+  if (cap > (int64_t{1} << 30)) return fail(ATTN_ERR_UNSUPPORTED, "more than 2^30 keys per row");
+  if (cap != p->N) return fail(ATTN_ERR_INVALID_ARG, "N must be max_pages * page_size");
+  if (cap > 0 && p->B > 0 && g->table == nullptr)
+    return fail(ATTN_ERR_INVALID_ARG, "page table is NULL");
+  if (g->shared_len < 0 || g->shared_len > cap || g->shared_len % g->page_size != 0)
+    return fail(ATTN_ERR_INVALID_ARG, "shared_len must be a multiple of page_size, at most N");
+  if (latent && g->shared_len != 0)
+    return fail(ATTN_ERR_UNSUPPORTED, "latent decode takes no shared prefix");
+  // strides
+  const int cols = latent ? p->d + attn::kLatentRope : p->d;
+  const int64_t st[6] = {p->stride_b,    p->stride_h, p->stride_n, p->kv_stride_b,
+                         p->kv_stride_n, latent ? 8 : p->kv_stride_h};
+  for (int64_t s : st)
+    if (s <= 0 || s % 8 != 0)
+      return fail(ATTN_ERR_INVALID_ARG, "strides must be positive multiples of 8 elements");
+  if (p->kv_stride_n < cols || p->stride_n < cols)
+    return fail(ATTN_ERR_INVALID_ARG, "rows overlap: stride_n is below the row's columns");
+  return ATTN_OK;
+}
+
+attn_status check_ptrs(std::initializer_list<const void*> ptrs) {
+  for (const void* ptr : ptrs) {
+    if (ptr == nullptr) return fail(ATTN_ERR_INVALID_ARG, "tensor argument is NULL");
+    if ((reinterpret_cast<uintptr_t>(ptr) & 15u) != 0)
+      return fail(ATTN_ERR_INVALID_ARG, "tensor argument is not 16-byte aligned");
+  }
+  return ATTN_OK;
+}
+
+attn_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
+  if (ws == nullptr) return fail(ATTN_ERR_WORKSPACE, "workspace is NULL");
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+    return fail(ATTN_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  if (ws_bytes < need) {
+    char msg[96];
+    snprintf(msg, sizeof(msg), "workspace too small: %zu < %zu bytes", ws_bytes, need);
+    return fail(ATTN_ERR_WORKSPACE, msg);
+  }
+  return ATTN_OK;
+}
+
+bool empty(const attn_params* p) { return p->B == 0 || p->H == 0; }
+
+struct Layout {
+  size_t starts = 0, part_o = 0, part_l = 0, pre_o = 0, pre_l = 0, total = 0;
+  int ctas = 0;                            // of the decode kernel (latent: per row group)
+  int heads = 0, group = 0, rows = 0;      // segments per sequence, heads and rows of one
+  int first = 0, splits = 0, tiles = 0;    // the shared prefix
+};
+
+Layout layout(const attn_params* p, int32_t n_q, const attn_pages* g, bool latent) {
+  Layout L;
+  const int64_t sms = sm_count();
+  const int64_t rows_all = static_cast<int64_t>(p->B) * p->H * n_q;
+  const int H_kv = p->H_kv == 0 ? p->H : p->H_kv;
+  int64_t most;   // CTAs that have the smallest share worth a CTA at full caches
+  if (latent) {
+    const int64_t groups = (static_cast<int64_t>(p->H) * n_q + attn::kLatentRows - 1) / attn::kLatentRows;
+    L.heads = 1;
+    L.group = p->H;
+    L.rows = static_cast<int>(groups * attn::kLatentRows);
+    most = sms / groups;
+  } else {
+    L.heads = H_kv;
+    L.group = H_kv > 0 ? p->H / H_kv : 1;
+    L.rows = L.group * n_q;
+    most = L.rows > 32 ? sms : 2 * sms;
+    // the prefix apart: only where two sequences share it
+    L.first = p->B > 1 ? g->shared_len : 0;
+  }
+  const int keys = latent ? attn::kLatentKeys : attn::kPagedKeys;
+  const int64_t tiles = (static_cast<int64_t>(p->N) - L.first + keys - 1) / keys;
+  const int64_t units = static_cast<int64_t>(p->B) * L.heads *
+                        (tiles + (latent ? attn::kLatentOverhead : attn::kPagedOverhead));
+  const int64_t want = units / attn::kPagedMinUnits;
+  if (most > want) most = want;
+  L.ctas = static_cast<int>(most < 1 ? 1 : most);
+  if (L.first > 0) {
+    // pieces of the prefix: as many as fill the SMs once, two key tiles each
+    // at least, 16 at most
+    L.tiles = (L.first + attn::kTile - 1) / attn::kTile;
+    const int64_t stack = static_cast<int64_t>(p->B) * L.group * n_q;
+    const int64_t blocks = (stack + 2 * attn::kTile - 1) / (2 * attn::kTile) * L.heads;
+    int64_t k = blocks > 0 ? sms / blocks : 1;
+    if (k > L.tiles / 2) k = L.tiles / 2;
+    if (k > 16) k = 16;
+    L.splits = k < 1 ? 1 : static_cast<int>(k);
+  }
+  size_t off = kHeaderBytes;
+  L.starts = off;
+  off = round_up(off + (static_cast<size_t>(p->B) + 1) * sizeof(int64_t), 256);
+  L.part_o = off;
+  off = round_up(off + 2 * static_cast<size_t>(L.ctas) * L.rows * p->d * sizeof(float), 256);
+  L.part_l = off;
+  off = round_up(off + 2 * static_cast<size_t>(L.ctas) * L.rows * sizeof(float), 256);
+  if (L.splits > 0) {
+    L.pre_o = off;
+    off = round_up(off + static_cast<size_t>(L.splits) * rows_all * p->d * sizeof(float), 256);
+    L.pre_l = off;
+    off = round_up(off + static_cast<size_t>(L.splits) * rows_all * sizeof(float), 256);
+  }
+  L.total = off;
+  return L;
+}
+
+PagedArgs args_of(const attn_params* p, int32_t n_q, const attn_pages* g, const Layout& L,
+                  const void* q, void* o, float* lse, void* ws) {
+  char* w = static_cast<char*>(ws);
+  PagedArgs a{};
+  a.B = p->B;
+  a.H = p->H;
+  a.heads = L.heads;
+  a.group = L.group;
+  a.n_q = n_q;
+  a.rows = L.rows;
+  a.all_rows = p->H * n_q;
+  a.causal = p->causal != 0;
+  a.d = p->d;
+  a.key_lens = p->key_lens;
+  a.table = g->table;
+  a.table_stride = g->table_stride;
+  a.cap = p->N;
+  a.page_shift = log2_of(g->page_size);
+  a.num_pages = g->num_pages;
+  a.first = L.first;
+  a.scale_log2 = p->scale * kLog2e;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.stride_b = p->stride_b;
+  a.stride_h = p->stride_h;
+  a.stride_n = p->stride_n;
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  a.starts = reinterpret_cast<int64_t*>(w + L.starts);
+  a.part_o = reinterpret_cast<float*>(w + L.part_o);
+  a.part_l = reinterpret_cast<float*>(w + L.part_l);
+  a.pre_splits = L.splits;
+  a.pre_o = reinterpret_cast<const float*>(w + L.pre_o);
+  a.pre_l = reinterpret_cast<const float*>(w + L.pre_l);
+  a.status = reinterpret_cast<int*>(w);
+  a.timeout_ns = kTimeoutNs;
+  return a;
+}
+
+attn_status launched(cudaError_t e, const char* what) {
+  if (e == cudaSuccess) return ATTN_OK;
+  char msg[256];
+  snprintf(msg, sizeof(msg), "%s: %s", what, cudaGetErrorString(e));
+  return fail(ATTN_ERR_CUDA, msg);
+}
+
+// A tensor map of a cache without pages is never read; it needs some extent.
+int at_least_1(int n) { return n < 1 ? 1 : n; }
+
+int box_rows(const attn_pages* g, int keys) { return g->page_size < keys ? g->page_size : keys; }
+
+}  // namespace
+
+extern "C" {
+
+size_t attn_decode_paged_workspace_size(const attn_params* p, int32_t n_q,
+                                        const attn_pages* pages) {
+  if (validate(p, n_q, pages, false) != ATTN_OK) return 0;
+  return layout(p, n_q, pages, false).total;
+}
+
+attn_status attn_decode_paged(const attn_params* p, int32_t n_q, const attn_pages* pages,
+                              const void* q, const void* k, const void* v, void* o, float* lse,
+                              void* ws, size_t ws_bytes, void* stream) {
+  attn_status st = validate(p, n_q, pages, false);
+  if (st != ATTN_OK) return st;
+  const Layout L = layout(p, n_q, pages, false);
+  if ((st = check_ws(ws, ws_bytes, L.total)) != ATTN_OK) return st;
+  if (empty(p)) return ATTN_OK;
+  if ((st = check_ptrs({q, k, v, o, lse})) != ATTN_OK) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const PagedArgs a = args_of(p, n_q, pages, L, q, o, lse, ws);
+  const auto map = [&](CUtensorMap* m, const void* ptr, int keys) {
+    return static_cast<attn_status>(attn::encode_pages(
+        m, ptr, at_least_1(pages->num_pages), L.heads, pages->page_size, p->d, p->kv_stride_b,
+        p->kv_stride_h, p->kv_stride_n, box_rows(pages, keys)));
+  };
+  CUtensorMap tk, tv;
+  if (L.first > 0) {
+    if ((st = map(&tk, k, attn::kTile)) != ATTN_OK || (st = map(&tv, v, attn::kTile)) != ATTN_OK)
+      return st;
+    attn::PrefixArgs f{};
+    f.B = p->B;
+    f.H = p->H;
+    f.H_kv = L.heads;
+    f.group = L.group;
+    f.n_q = n_q;
+    f.causal = a.causal;
+    f.d = p->d;
+    f.key_lens = p->key_lens;
+    f.table = pages->table;
+    f.cap = a.cap;
+    f.page_shift = a.page_shift;
+    f.num_pages = pages->num_pages;
+    f.shared_len = L.first;
+    f.splits = L.splits;
+    f.tiles = L.tiles;
+    f.rows = p->B * L.group * n_q;
+    f.scale_log2 = a.scale_log2;
+    f.q = a.q;
+    f.stride_b = a.stride_b;
+    f.stride_h = a.stride_h;
+    f.stride_n = a.stride_n;
+    f.pre_o = const_cast<float*>(a.pre_o);
+    f.pre_l = const_cast<float*>(a.pre_l);
+    f.status = a.status;
+    f.timeout_ns = a.timeout_ns;
+    if ((st = launched(attn::launch_prefix(tk, tv, f, s), "shared prefix launch")) != ATTN_OK)
+      return st;
+  }
+  if ((st = map(&tk, k, attn::kPagedKeys)) != ATTN_OK ||
+      (st = map(&tv, v, attn::kPagedKeys)) != ATTN_OK)
+    return st;
+  if ((st = launched(attn::launch_paged(tk, tv, a, L.ctas, s), "paged decode launch")) != ATTN_OK)
+    return st;
+  if (L.ctas == 1) return ATTN_OK;   // one CTA cuts nothing
+  return launched(attn::launch_paged_merge(a, attn::kPagedKeys, attn::kPagedOverhead, L.ctas, s),
+                  "paged merge launch");
+}
+
+size_t attn_decode_latent_workspace_size(const attn_params* p, int32_t n_q,
+                                         const attn_pages* pages) {
+  if (validate(p, n_q, pages, true) != ATTN_OK) return 0;
+  return layout(p, n_q, pages, true).total;
+}
+
+attn_status attn_decode_latent(const attn_params* p, int32_t n_q, const attn_pages* pages,
+                               const void* q, const void* c, void* o, float* lse, void* ws,
+                               size_t ws_bytes, void* stream) {
+  attn_status st = validate(p, n_q, pages, true);
+  if (st != ATTN_OK) return st;
+  const Layout L = layout(p, n_q, pages, true);
+  if ((st = check_ws(ws, ws_bytes, L.total)) != ATTN_OK) return st;
+  if (empty(p)) return ATTN_OK;
+  if ((st = check_ptrs({q, c, o, lse})) != ATTN_OK) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  PagedArgs a = args_of(p, n_q, pages, L, q, o, lse, ws);
+  CUtensorMap tc;
+  st = static_cast<attn_status>(attn::encode_pages(
+      &tc, c, at_least_1(pages->num_pages), 1, pages->page_size, p->d + attn::kLatentRope,
+      p->kv_stride_b, p->kv_stride_b, p->kv_stride_n, box_rows(pages, attn::kLatentKeys)));
+  if (st != ATTN_OK) return st;
+  if ((st = launched(attn::launch_latent(tc, a, L.ctas, s), "latent decode launch")) != ATTN_OK)
+    return st;
+  if (L.ctas == 1) return ATTN_OK;
+  // the merge writes o, which is contiguous
+  a.stride_n = p->d;
+  a.stride_h = static_cast<int64_t>(n_q) * p->d;
+  a.stride_b = static_cast<int64_t>(p->H) * n_q * p->d;
+  return launched(attn::launch_paged_merge(a, attn::kLatentKeys, attn::kLatentOverhead, L.ctas, s),
+                  "latent merge launch");
+}
+
+}  // extern "C"

@@ -1,0 +1,291 @@
+"""Python binding of the paged-cache calls: argument marshalling only.
+
+As in api.py every step of the computation runs in the CUDA library, on the
+current stream of the tensors' device.  A decode step on a short cache takes
+a few microseconds on the device, so the calls here do little per call: one
+structure is filled and one library function called, and the workspace's size
+is asked for only when the one at hand is too small.
+"""
+
+import ctypes
+import math
+
+import torch
+
+from . import _abi
+from ._abi import AttnPages, AttnPageTable, AttnParams, AttnPool, check_status, lib
+from .api import workspace
+
+_ROPE = 64   # columns of a latent vector beside its d_v value columns
+
+
+def _call(device, ws, size_of, call, what):
+    """call(ws pointer, bytes, stream) on `device`, with the caller's workspace
+    or the device's shared one, grown when the call says it is too small."""
+    if device.type != "cuda":
+        raise ValueError(f"{what}: tensors must be on a CUDA device")
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return _call(device, ws, size_of, call, what)
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if ws is not None:
+        if ws.device != device or not ws.is_contiguous():
+            raise ValueError(f"{what}: ws must be contiguous, on the tensors' device")
+        check_status(call(ws.data_ptr(), ws.numel() * ws.element_size(), stream), what)
+        return
+    w = workspace(device, 256)
+    st = call(w.data_ptr(), w.numel(), stream)
+    if st == _abi.ATTN_ERR_WORKSPACE:
+        w = workspace(device, size_of())
+        st = call(w.data_ptr(), w.numel(), stream)
+    check_status(st, what)
+
+
+def _int32(t, device, dim, what):
+    if t.dtype != torch.int32 or t.device != device or t.dim() != dim \
+            or (t.numel() > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{what} must be a {dim}-dimensional int32 tensor on the tensors' device, "
+                         "contiguous along its last axis")
+
+
+def _decode_args(q, pages, table, cache_lens, scale, causal, shared_len, d, H_kv, strides):
+    """attn_params and attn_pages of a paged decode step; strides: of a page
+    buffer, between pages, heads and keys."""
+    B, H, n_q, _ = q.shape
+    _int32(table, q.device, 2, "page_table")
+    _int32(cache_lens, q.device, 1, "cache_lens")
+    if table.shape[0] != B or cache_lens.shape[0] != B:
+        raise ValueError("page_table and cache_lens must have a row per sequence of q")
+    page_size, max_pages = pages.shape[-2], table.shape[1]
+    qs = q.stride()
+    p = AttnParams(B, H, max_pages * page_size, d, _abi.ATTN_BF16, scale, 1 if causal else 0, 0.0,
+                   0, 0, cache_lens.data_ptr(), None, 0, qs[0], qs[1], qs[2], H_kv, 0, *strides,
+                   0.0, 0.0, 0.0, 0)
+    g = AttnPages(table.data_ptr(), table.stride(0) if B > 1 else max_pages, max_pages, page_size,
+                  pages.shape[0], int(shared_len))
+    return p, g
+
+
+def _strides(t):
+    """Strides of a bf16 tensor whose axes of one element, over which nothing
+    strides, are given the value that the library's checks pass."""
+    s = list(t.stride())
+    if s[-1] != 1 and t.shape[-1] > 1:
+        raise ValueError("the last axis must be contiguous")
+    inner = t.shape[-1]
+    for i in range(t.dim() - 2, -1, -1):
+        if t.shape[i] <= 1:
+            s[i] = inner
+        inner = max(inner, s[i] * max(t.shape[i], 1))
+    return s
+
+
+def _check_bf16(*ts):
+    for t in ts:
+        if t.dtype != torch.bfloat16 or t.device != ts[0].device:
+            raise TypeError("tensors must be bf16 on one device")
+
+
+def attention_decode_paged(q, k_pages, v_pages, page_table, cache_lens, *, scale=None, causal=True,
+                           shared_len=0, out=None, lse=None, ws=None):
+    """The decode step of attention_decode against a paged cache (see
+    attn_decode_paged in include/attn.h).
+
+    q: [B, H, n_q, d] bf16; k_pages, v_pages: [num_pages, H_kv, page_size, d]
+    bf16, with like strides, H_kv dividing H and page_size a power of two from
+    16 on; page_table: int32 [B, max_pages]: key j of sequence b is row
+    j % page_size of page page_table[b, j // page_size]; cache_lens: int32 [B].
+    shared_len: a multiple of page_size; the first shared_len keys of all
+    sequences lie in the same pages (row 0's are read) and are attended once
+    for the whole batch.  Returns (o, lse) with o like q and lse fp32
+    [B, H, n_q].  A page index outside the cache is reported by check().
+    """
+    _check_bf16(q, k_pages, v_pages)
+    if q.dim() != 4 or k_pages.dim() != 4 or k_pages.shape != v_pages.shape \
+            or k_pages.shape[3] != q.shape[3]:
+        raise ValueError("q must be [B, H, n_q, d], k_pages and v_pages "
+                         "[num_pages, H_kv, page_size, d]")
+    B, H, n_q, d = q.shape
+    H_kv = k_pages.shape[1]
+    if H_kv < 1 or H % H_kv:
+        raise ValueError("H_kv must divide q's H")
+    ks = _strides(k_pages)
+    if ks != _strides(v_pages):
+        raise ValueError("k_pages and v_pages must share strides")
+    if out is None:
+        out = torch.empty_strided(q.shape, q.stride(), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.stride() != q.stride() or out.dtype != q.dtype \
+            or out.device != q.device:
+        raise ValueError("out must be like q")
+    lse = _lse(lse, q)
+    p, g = _decode_args(q, k_pages, page_table, cache_lens,
+                        1.0 / math.sqrt(d) if scale is None else float(scale), causal, shared_len,
+                        d, H_kv, ks[:3])
+    p.stride_b, p.stride_h, p.stride_n = _strides(q)[:3]
+    fn = lib().attn_decode_paged
+    pp, gp = ctypes.byref(p), ctypes.byref(g)
+    ptrs = (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), lse.data_ptr())
+    _call(q.device, ws, lambda: _size(lib().attn_decode_paged_workspace_size(pp, n_q, gp)),
+          lambda w, n, s: fn(pp, n_q, gp, *ptrs, w, n, s), "attn_decode_paged")
+    return out, lse
+
+
+def attention_decode_latent(q, c_pages, page_table, cache_lens, *, scale, d_v=512, causal=True,
+                            out=None, lse=None, ws=None):
+    """The decode step of latent attention in its absorbed form, against a
+    paged cache of latent vectors (see attn_decode_latent in include/attn.h).
+
+    q: [B, H, n_q, d_v + 64] bf16; c_pages: [num_pages, page_size, d_v + 64]
+    bf16: a cached vector is the key of every head, its first d_v columns (256
+    or 512) the value; page_table, cache_lens as in attention_decode_paged.
+    `scale` has no default: it belongs to the heads' width before the
+    projections were folded in.  Returns (o, lse): o [B, H, n_q, d_v] bf16,
+    contiguous, and lse fp32 [B, H, n_q].
+    """
+    _check_bf16(q, c_pages)
+    if q.dim() != 4 or c_pages.dim() != 3 or q.shape[3] != d_v + _ROPE \
+            or c_pages.shape[2] != d_v + _ROPE:
+        raise ValueError(f"q must be [B, H, n_q, d_v + {_ROPE}], c_pages "
+                         f"[num_pages, page_size, d_v + {_ROPE}]")
+    B, H, n_q, _ = q.shape
+    if out is None:
+        out = torch.empty((B, H, n_q, d_v), dtype=q.dtype, device=q.device)
+    elif out.shape != (B, H, n_q, d_v) or not out.is_contiguous() or out.dtype != q.dtype \
+            or out.device != q.device:
+        raise ValueError("out must be a contiguous bf16 [B, H, n_q, d_v] on q's device")
+    lse = _lse(lse, q)
+    cs = _strides(c_pages)
+    p, g = _decode_args(q, c_pages, page_table, cache_lens, float(scale), causal, 0, d_v, 1,
+                        (cs[0], cs[0], cs[1]))
+    p.stride_b, p.stride_h, p.stride_n = _strides(q)[:3]
+    fn = lib().attn_decode_latent
+    pp, gp = ctypes.byref(p), ctypes.byref(g)
+    ptrs = (q.data_ptr(), c_pages.data_ptr(), out.data_ptr(), lse.data_ptr())
+    _call(q.device, ws, lambda: _size(lib().attn_decode_latent_workspace_size(pp, n_q, gp)),
+          lambda w, n, s: fn(pp, n_q, gp, *ptrs, w, n, s), "attn_decode_latent")
+    return out, lse
+
+
+def _lse(lse, q):
+    if lse is None:
+        return torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    if lse.shape != q.shape[:3] or not lse.is_contiguous() or lse.dtype != torch.float32 \
+            or lse.device != q.device:
+        raise ValueError("lse must be a contiguous fp32 [B, H, n_q] on q's device")
+    return lse
+
+
+def _size(n):
+    if n == 0:
+        check_status(_abi.ATTN_ERR_INVALID_ARG, "workspace size")
+    return n
+
+
+# ------------------------------------------------------------------- upkeep --
+
+def _table_args(page_table, cache_lens, refs, page_size):
+    dev = refs.device
+    _int32(page_table, dev, 2, "page_table")
+    _int32(cache_lens, dev, 1, "cache_lens")
+    _int32(refs, dev, 1, "refs")
+    rows, max_pages = page_table.shape
+    if cache_lens.shape[0] != rows:
+        raise ValueError("cache_lens must have an entry per row of page_table")
+    return AttnPageTable(page_table.data_ptr(), page_table.stride(0) if rows > 1 else max_pages,
+                         cache_lens.data_ptr(), refs.data_ptr(), rows, max_pages, int(page_size),
+                         refs.shape[0])
+
+
+def _pool_args(pools, num_pages, device):
+    """attn_pool of each page buffer [num_pages, ...]: a page's elements must
+    fill one contiguous block, in whatever order its axes have."""
+    got = (AttnPool * max(1, len(pools)))()
+    for a, t in zip(got, pools):
+        if t.device != device or t.dim() < 2 or t.shape[0] != num_pages:
+            raise ValueError("pools must be tensors [num_pages, ...] on the table's device")
+        n = 1
+        if not t[0:1].is_contiguous():   # (a permuted page: its axes in the order of the strides)
+            for stride, size in sorted(zip(t.stride()[1:], t.shape[1:])):
+                if size != 1 and stride != n:
+                    raise ValueError("a page must be one contiguous block of memory")
+                n *= size
+        page_bytes = math.prod(t.shape[1:]) * t.element_size()
+        a.base, a.page_bytes = t.data_ptr(), page_bytes
+        a.page_stride = t.stride(0) * t.element_size() if num_pages > 1 else page_bytes
+    return got
+
+
+def _list(t, device, what):
+    _int32(t, device, 1, what)
+    return t.data_ptr(), t.shape[0]
+
+
+def pages_copy(pools, src, dst, *, ws=None):
+    """Page dst[i] of every page buffer in `pools` ([num_pages, ...] tensors)
+    becomes a copy of page src[i]; src, dst: int32 on the device, dst without
+    repeats and apart from src."""
+    if not pools:
+        return
+    dev, num_pages = pools[0].device, pools[0].shape[0]
+    arr = _pool_args(pools, num_pages, dev)
+    s, n = _list(src, dev, "src")
+    d, m = _list(dst, dev, "dst")
+    if n != m:
+        raise ValueError("src and dst must have the same length")
+    fn = lib().attn_pages_copy
+    _call(dev, ws, lambda: 256,
+          lambda w, nb, st: fn(arr, len(pools), num_pages, s, d, n, w, nb, st), "attn_pages_copy")
+
+
+def pages_extend(page_table, cache_lens, refs, seqs, new_lens, *, page_size, ws=None):
+    """Sequence seqs[i] grows to new_lens[i] keys, taking the lowest free pages
+    (see attn_pages_extend).  page_table int32 [rows, max_pages], cache_lens
+    int32 [rows], refs int32 [num_pages], in place."""
+    t = _table_args(page_table, cache_lens, refs, page_size)
+    s, n = _list(seqs, refs.device, "seqs")
+    d, m = _list(new_lens, refs.device, "new_lens")
+    if n != m:
+        raise ValueError("seqs and new_lens must have the same length")
+    tp, fn = ctypes.byref(t), lib().attn_pages_extend
+    _call(refs.device, ws, lambda: _size(lib().attn_pages_workspace_size(tp, n)),
+          lambda w, nb, st: fn(tp, s, d, n, w, nb, st), "attn_pages_extend")
+
+
+def pages_fork(pools, page_table, cache_lens, refs, parents, children, *, page_size, ws=None):
+    """Row children[i] (empty) becomes a copy of sequence parents[i]: full
+    pages shared, a part-filled last page copied in every buffer of `pools`
+    (see attn_pages_fork).  Returns the new pages, int32 like parents: -1 where
+    none was needed, -2 where the fork was not made."""
+    t = _table_args(page_table, cache_lens, refs, page_size)
+    arr = _pool_args(pools, refs.shape[0], refs.device)
+    a, n = _list(parents, refs.device, "parents")
+    b, m = _list(children, refs.device, "children")
+    if n != m:
+        raise ValueError("parents and children must have the same length")
+    new = torch.empty(n, dtype=torch.int32, device=refs.device)
+    tp, fn, np_ = ctypes.byref(t), lib().attn_pages_fork, new.data_ptr()
+    _call(refs.device, ws, lambda: _size(lib().attn_pages_workspace_size(tp, n)),
+          lambda w, nb, st: fn(tp, arr, len(pools), a, b, n, np_, w, nb, st), "attn_pages_fork")
+    return new
+
+
+def pages_free(page_table, cache_lens, refs, seqs, *, page_size, ws=None):
+    """The sequences `seqs` give back their pages (see attn_pages_free)."""
+    t = _table_args(page_table, cache_lens, refs, page_size)
+    s, n = _list(seqs, refs.device, "seqs")
+    tp, fn = ctypes.byref(t), lib().attn_pages_free
+    _call(refs.device, ws, lambda: 256, lambda w, nb, st: fn(tp, s, n, w, nb, st),
+          "attn_pages_free")
+
+
+def pages_compact(pools, page_table, cache_lens, refs, *, page_size, ws=None):
+    """Moves the pages in use to the front of the buffers `pools`, tables and
+    counts with them (see attn_pages_compact).  Returns where each page now is,
+    int32 [num_pages], -1 for a free one."""
+    t = _table_args(page_table, cache_lens, refs, page_size)
+    arr = _pool_args(pools, refs.shape[0], refs.device)
+    moved = torch.empty_like(refs)
+    tp, fn, mp = ctypes.byref(t), lib().attn_pages_compact, moved.data_ptr()
+    _call(refs.device, ws, lambda: _size(lib().attn_pages_workspace_size(tp, 0)),
+          lambda w, nb, st: fn(tp, arr, len(pools), mp, w, nb, st), "attn_pages_compact")
+    return moved

@@ -82,7 +82,10 @@ typedef enum {
   ATTN_ERR_UNSUPPORTED = 2,   /* valid but not implemented (e.g. fp32 bwd) */
   ATTN_ERR_CUDA = 3,          /* a CUDA runtime/driver call failed */
   ATTN_ERR_TIMEOUT = 4,       /* a kernel wait gave up (device status) */
-  ATTN_ERR_WORKSPACE = 5      /* workspace missing, misaligned or too small */
+  ATTN_ERR_WORKSPACE = 5,     /* workspace missing, misaligned or too small */
+  ATTN_ERR_PAGE = 6,          /* a page table or list in device memory held an
+                                 index outside its range (device status) */
+  ATTN_ERR_FULL = 7           /* a cache had no free page left (device status) */
 } attn_status;
 
 typedef enum { ATTN_BF16 = 0, ATTN_FP32 = 1, ATTN_FP8_E4M3 = 2 } attn_dtype;
@@ -234,6 +237,132 @@ attn_status attn_decode(const attn_params* p, int32_t n_q, const void* q, const 
                         const void* v, void* o, float* lse, void* ws, size_t ws_bytes,
                         void* stream);
 
+/* ------------------------------------------------------------------------
+ * Paged key/value caches.  A serving program keeps the caches of many
+ * sequences in pages of equal size that are handed out as sequences grow, so
+ * that no sequence needs a contiguous, full-length buffer (the KV cache of
+ * "3.3 Hiểu sâu cơ chế Self-Attention", §9, has no pages; these calls have
+ * no counterpart there).
+ *
+ * Key j of sequence b lies in row j mod page_size of page
+ * table[b * table_stride + j / page_size].  Only the entries that hold cached
+ * keys, ceil(len / page_size) of a row, are read.  An entry outside
+ * [0, num_pages) is never followed: its page reads as zeros and the
+ * workspace's status becomes ATTN_ERR_PAGE, which attn_check reports. */
+typedef struct attn_pages {
+  const int32_t* table;      /* device [B][table_stride] */
+  int64_t table_stride;      /* entries between the rows of two sequences */
+  int32_t max_pages;         /* entries of a row that may be used */
+  int32_t page_size;         /* keys per page: a power of two, 16 to 32768 */
+  int32_t num_pages;         /* pages in the cache */
+  int32_t shared_len;        /* leading keys that all sequences share (below); 0: none */
+} attn_pages;
+
+/* Decode step against a paged cache: attn_decode with
+ *   k, v    [num_pages, H_kv, page_size, d] bf16, where kv_stride_b is the
+ *           stride between pages (all three key/value strides are required)
+ *   p->N    must be max_pages * page_size
+ * and the same query rows, masks, limits and outputs.  Rows of a page past
+ * the end of its sequence are not used, whatever they hold.
+ *
+ * shared_len > 0: the first shared_len / page_size entries of every table row
+ * name the same pages (a fork of one prompt, a common system prompt), of
+ * which row 0 is read.  Their keys are attended once for all sequences, the
+ * rest per sequence, and the two are merged by the logsumexp rule; the result
+ * is that of shared_len = 0 up to rounding.  shared_len must be a multiple
+ * of page_size and at most p->N.  A cache_lens[b] below shared_len is allowed:
+ * that sequence attends its own first keys only; the keys and values of the
+ * shared pages that other sequences use must then be finite. */
+size_t attn_decode_paged_workspace_size(const attn_params* p, int32_t n_q,
+                                        const attn_pages* pages);
+attn_status attn_decode_paged(const attn_params* p, int32_t n_q, const attn_pages* pages,
+                              const void* q, const void* k, const void* v, void* o, float* lse,
+                              void* ws, size_t ws_bytes, void* stream);
+
+/* Decode step of latent attention, absorbed form: every cached token is one
+ * vector of d + 64 columns that is the key of all heads as it stands and
+ * whose first d columns are their value,
+ *   S = scale * q c^T,  O = softmax(S) c[:, 0:d],  L = logsumexp(S)
+ * (the per-head up-projections of keys and values are folded into q and into
+ * what follows O; the last 64 columns carry the position).
+ *   p->d    value columns: 256 or 512;  p->N = max_pages * page_size;
+ *           p->H_kv 0 or 1
+ *   q       [B, H, n_q, d + 64] bf16 with the query strides
+ *   c       [num_pages, page_size, d + 64] bf16; kv_stride_b between pages,
+ *           kv_stride_n between tokens (kv_stride_h is ignored)
+ *   o       [B, H, n_q, d] bf16, contiguous;  lse fp32 [B, H, n_q]
+ * key_lens, causal and the query positions are those of attn_decode; H * n_q
+ * is not limited.  pages->shared_len must be 0. */
+size_t attn_decode_latent_workspace_size(const attn_params* p, int32_t n_q,
+                                         const attn_pages* pages);
+attn_status attn_decode_latent(const attn_params* p, int32_t n_q, const attn_pages* pages,
+                               const void* q, const void* c, void* o, float* lse, void* ws,
+                               size_t ws_bytes, void* stream);
+
+/* Upkeep of a paged cache, on the device: no call synchronises or reads
+ * anything back.  The state is a table of pages, a length per sequence (row)
+ * and a reference count per page; a page with count 0 is free.  A row holds
+ * ceil(len / page_size) pages, its further entries mean nothing.  Lists are
+ * int32 device arrays.  What a list or the state holds wrongly is skipped and
+ * recorded in the workspace's status (ATTN_ERR_PAGE; ATTN_ERR_FULL where a
+ * cache has too few free pages), which attn_check reports. */
+typedef struct attn_page_table {
+  int32_t* table;            /* [rows][table_stride] */
+  int64_t table_stride;
+  int32_t* lens;             /* [rows] */
+  int32_t* refs;             /* [num_pages] */
+  int32_t rows, max_pages, page_size, num_pages;
+} attn_page_table;
+
+/* One buffer of pages (keys or values of one layer, latent vectors, ...): a
+ * page's page_bytes are contiguous.  base 16-byte aligned, both sizes
+ * multiples of 16. */
+typedef struct attn_pool {
+  void* base;
+  int64_t page_stride, page_bytes;
+} attn_pool;
+
+/* Workspace of every call below for lists of up to n entries (the header
+ * rules of the other calls apply); attn_pages_copy needs 256 bytes. */
+size_t attn_pages_workspace_size(const attn_page_table* t, int32_t n);
+
+/* Page dst[i] of every pool becomes a copy of page src[i].  Where a dst is
+ * also another pair's src or dst, what it and the copies of it hold is
+ * unspecified. */
+attn_status attn_pages_copy(const attn_pool* pools, int32_t n_pools, int32_t num_pages,
+                            const int32_t* src, const int32_t* dst, int32_t n, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/* Sequence seqs[i] grows to new_lens[i] keys (not below its length): the
+ * pages it needs are the lowest free ones, in the list's order.  A sequence
+ * for which too few are left stays as it was, and so do those after it that
+ * need pages.  Of a row that is named twice the first entry counts. */
+attn_status attn_pages_extend(const attn_page_table* t, const int32_t* seqs,
+                              const int32_t* new_lens, int32_t n, void* ws, size_t ws_bytes,
+                              void* stream);
+
+/* Row children[i], which must be empty (length 0), becomes a copy of sequence
+ * parents[i]: full pages are shared (their counts grow), a part-filled last
+ * page is copied, in every pool, to the lowest free page.  new_pages[i]
+ * (device, output) is that page, -1 if none was needed, -2 if the fork was
+ * not made.  Of a child that is named twice the first entry counts; all
+ * entries see the state before the call. */
+attn_status attn_pages_fork(const attn_page_table* t, const attn_pool* pools, int32_t n_pools,
+                            const int32_t* parents, const int32_t* children, int32_t n,
+                            int32_t* new_pages, void* ws, size_t ws_bytes, void* stream);
+
+/* The sequences give back their pages: counts fall, the entries they held
+ * become -1, the lengths 0.  Freeing an empty row does nothing. */
+attn_status attn_pages_free(const attn_page_table* t, const int32_t* seqs, int32_t n, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/* Moves the pages in use to the places [0, pages in use): those behind, in
+ * ascending order, to the free ones before, in ascending order, in every
+ * pool; tables and counts follow.  moved[p] (device [num_pages], output) is
+ * where page p now is, -1 for a page that was free. */
+attn_status attn_pages_compact(const attn_page_table* t, const attn_pool* pools, int32_t n_pools,
+                               int32_t* moved, void* ws, size_t ws_bytes, void* stream);
+
 /* Diagnostic: runs the kernels' time-out path on purpose.  Enqueues one warp
  * that waits on a barrier nothing arrives at, giving up after `limit_ns`
  * (clamped to [1 ms, 2 s]); it records ATTN_ERR_TIMEOUT in the workspace's
@@ -267,7 +396,7 @@ typedef enum {
 attn_status attn_debug_stall(int32_t which, uint64_t limit_ns);
 
 /* Synchronises `stream`, returns the workspace's device status (ATTN_OK or
- * ATTN_ERR_TIMEOUT) and clears it.  ws = NULL: the status of
+ * ATTN_ERR_TIMEOUT, ATTN_ERR_PAGE or ATTN_ERR_FULL) and clears it.  ws = NULL: the status of
  * attn_bwd_noalloc's built-in scratch on the current device. */
 attn_status attn_check(void* ws, void* stream);
 
