@@ -20,19 +20,20 @@
 // because the other way round the accumulator of 128 rows x 512 columns would
 // fill TMEM, and q alone would take 147 KB of shared memory.  So O^T takes
 // d_v / 128 * 64 TMEM columns, q 72 KB, and two 64-key tiles of 72 KB are in
-// flight, each read from global memory once and used as both operands.  (The
-// MMA of S^T has M = 128: its rows 64-127 are whatever lies behind the tile,
-// and nothing reads them.)  H * n_q rows are cut into groups of 64; the CTAs
+// flight, each read from global memory once and used as both operands.  H * n_q rows are cut into groups of 64; the CTAs
 // of a sequence's groups run side by side on the same keys, so that the
 // second read of a tile finds it in L2.  The keys are divided over the CTAs
 // as in the paged decode step.
-//   warps 0, 1, 4, 5   softmax: thread = key, 32 of the 64 columns each; a
-//                      column's max is a warp reduction; the row sums stay in
-//                      registers, a partial per key lane, until the end
-//   warps 0-7          load q, rescale O^T when some column's max has grown
-//                      by 2^8, write O
-//   warp 8             copies (a lane per page), warp 9 MMA issue: the scores of
-//                      the next tile run under this tile's softmax
+//   warps 0-7  load q; softmax of 16 keys x 32 columns each, in the MMA's
+//              fragment layout; the sums stay in registers, a partial per
+//              thread, until the end; rescale O^T when some column's max has
+//              grown by 2^8; write O
+//   warp 8     copies (a lane per page)
+//   warp 9     MMA issue: the scores of the next tile run under this tile's
+//              softmax
+// A tile is copied, waited for and released in groups of columns, so that its
+// scores begin while the rest is on the way, and the next copies while its
+// last products run: two 72 KB tiles are few for 1.6 us of latency.
 // P is rounded to bf16 for the second product (relative 2^-8 per element);
 // m, l, O are fp32.  Rows past the end of a sequence are zeroed in shared
 // memory before they are used as values (0 * NaN is NaN).
@@ -44,6 +45,7 @@ using namespace sm103;
 namespace {
 
 constexpr float kLn2 = 0.693147180559945309f;
+constexpr int kAhead = 1;   // tiles between a tile's way to L2 and its copy
 
 template <int DV>
 struct LatentCfg {
@@ -53,28 +55,59 @@ struct LatentCfg {
   static constexpr int kTileBytes = kBoxes * kBoxBytes;   // a key tile, and q
   static constexpr int kStages = DV == 512 ? 2 : 4;
   static constexpr int kBlocks = DV / 128;                // 128-row blocks of O^T
+  // what is copied, waited for and released together: the 64 key-only columns
+  // (group 0), then 128 columns = a block of O^T (groups 1 ..)
+  static constexpr int kGroups = kBlocks + 1;
   static constexpr int kPBytes = kLatentKeys * 128;
-  static constexpr int kSmem = 1024 + (1 + kStages) * kTileBytes + kPBytes;
+  static constexpr int kSmem = (1 + kStages) * kTileBytes + kPBytes;
+  static constexpr int kCtl = 3072;                       // LatentCtl, in whole kilobytes
+  static_assert(kSmem + kCtl <= 227 * 1024, "shared memory of a CTA");
   static constexpr int kThreads = 320;
   // S^T of tile t at 64 (t mod 2), block i of O^T at 128 + 64 i
   static constexpr uint32_t kOCol = 128;
 };
 
+// (aligned, so that what follows it, the dynamic shared memory, is too)
 template <int ST>
-struct LatentCtl {
-  uint64_t full[ST], empty[ST], sfull[2], pfull, pvdone, qfull, final_bar;
-  float wmax[2][2][64];     // [tile mod 2][32-key half][column]
-  float lsum[2][64];
+struct __align__(1024) LatentCtl {
+  uint64_t full[ST][5], empty[ST][5], sfull[2], pfull, pvdone, qfull, final_bar;
+  // [tile mod 2][16-key quarter][column]: the tile's maxima; behind the last
+  // tile of a piece, in the buffer of the next, the columns' sums
+  float wmax[2][4][64];
   int64_t sums[10];
   PagedShare share;
   uint32_t tmem_base;
   int abort_flag;
 };
 
-__device__ __forceinline__ float warp_max(float x) {
-  float r;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
-  return r;
+// 16 bytes global -> shared, asynchronously.
+__device__ __forceinline__ void copy16_async(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)),
+               "l"(reinterpret_cast<uint64_t>(src))
+               : "memory");
+}
+
+// `bytes` (a multiple of 16) at a 16-byte aligned address into L2.
+__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(src)),
+               "r"(bytes)
+               : "memory");
+}
+
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// 16 TMEM lanes x 32 columns: thread 4 g + q receives, for i = 0 .. 15, row
+// g + 8 ((i / 2) mod 2), column 8 (i / 4) + 2 q + i mod 2.
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
 }
 
 template <int DV>
@@ -82,25 +115,32 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
     latent_kernel(const __grid_constant__ CUtensorMap tc, const PagedArgs a, int groups) {
   using C = LatentCfg<DV>;
   constexpr int ST = C::kStages, KT = kLatentKeys;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ LatentCtl<ST> ctl;
+  static_assert(sizeof(LatentCtl<ST>) == C::kCtl, "the size that the limit is checked with");
+  if ((smem_u32(smem) & 1023u) != 0) {   // swizzled tiles need 1024-byte alignment
+    grid_dep_wait();
+    if (threadIdx.x == 0 && atomicCAS(a.status, 0, kStatusSmemAlign) == 0)
+      atomicExch(a.status + 1, kSiteLatentSmem);
+    return;
+  }
   uint8_t* sQ = smem;
   uint8_t* sC = smem + C::kTileBytes;
   uint8_t* sP = sC + ST * C::kTileBytes;
-  __shared__ LatentCtl<ST> ctl;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+  const int lane = threadIdx.x & 31;
   const int r0 = static_cast<int>(blockIdx.x % groups) * kLatentRows;   // first query row
   const int cta = blockIdx.x / groups, ctas = gridDim.x / groups;
   const int live = min(kLatentRows, a.all_rows - r0);
 
   if (threadIdx.x == 0) {
     ctl.abort_flag = 0;
-    for (int s = 0; s < ST; ++s) {
-      mbar_init(&ctl.full[s], 1);
-      mbar_init(&ctl.empty[s], 1);
-    }
+    for (int s = 0; s < ST; ++s)
+      for (int x = 0; x < C::kGroups; ++x) {
+        mbar_init(&ctl.full[s][x], 1);
+        mbar_init(&ctl.empty[s][x], 1);
+      }
     mbar_init(&ctl.sfull[0], 1);
     mbar_init(&ctl.sfull[1], 1);
     mbar_init(&ctl.pfull, 8);
@@ -114,31 +154,54 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
     tmem_alloc(&ctl.tmem_base, 512);
     tmem_relinquish();
   }
-  // P's columns past the live rows stay zero; their maxima -inf
+  // q's rows and P's columns past the live rows stay zero; their maxima -inf
+  for (int i = threadIdx.x; i < C::kTileBytes / 16; i += C::kThreads)
+    reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0u, 0u, 0u, 0u);
   for (int i = threadIdx.x; i < C::kPBytes / 16; i += C::kThreads)
     reinterpret_cast<uint4*>(sP)[i] = make_uint4(0u, 0u, 0u, 0u);
-  for (int i = threadIdx.x; i < 256; i += C::kThreads) (&ctl.wmax[0][0][0])[i] = -INFINITY;
-  for (int i = threadIdx.x; i < 128; i += C::kThreads) (&ctl.lsum[0][0])[i] = 0.f;
+  for (int i = threadIdx.x; i < 512; i += C::kThreads) (&ctl.wmax[0][0][0])[i] = -INFINITY;
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   grid_dep_wait();
   grid_dep_launch();
-  const uint32_t tmem = ctl.tmem_base;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.tmem_base, 0);
   const PagedShare share =
       paged_share<C::kThreads, KT, kLatentOverhead>(a, cta, ctas, ctl.sums, &ctl.share);
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.starts[a.B] = share.total;
   const WaitCtx wc{&ctl.abort_flag, a.status, a.timeout_ns};
-  PagedPiece p = paged_piece<KT, kLatentOverhead>(a, share, share.b, 0, share.s,
-                                                  threadIdx.x == 0 && r0 == 0);
+  PagedPiece p = paged_piece<KT, kLatentOverhead>(a, share, share.b, 0, share.s);
 
   if (warp == 8) {
     // ------------------------------------------------------------ copies
     const int rows = min(KT, 1 << a.page_shift), parts = KT / rows;
     bool ok = true;
     uint32_t T = 0;   // tiles issued, over all pieces
-    for (; ok && p.valid; p = paged_next<KT, kLatentOverhead>(a, share, p, false)) {
+    PagedPiece nx = p;
+    // Tile t of piece p, or past its end of the piece behind it, on its way to
+    // L2: the two tiles in shared memory are too few to cover the latency of
+    // HBM, and their copies go through a tile's memory 256 bytes of a token at
+    // a time, where this reads it in one run.
+    auto ahead = [&](int t) {
+      int b = p.b, len = p.len;
+      if (t >= p.t1) {
+        if (!nx.valid) return;
+        t += nx.t0 - p.t1;
+        if (t >= nx.t1) return;
+        b = nx.b;
+        len = nx.len;
+      }
+      const int key = t * KT + lane * rows;
+      if (lane >= parts || key >= len) return;
+      const int page = a.table[b * a.table_stride + (key >> a.page_shift)];
+      if (static_cast<unsigned>(page) < static_cast<unsigned>(a.num_pages))
+        prefetch_l2(a.pages + page * a.stride_page + (key & ((1 << a.page_shift) - 1)) * C::kCols,
+                    rows * C::kCols * 2);
+    };
+    // (the other row groups' CTAs read the same tiles)
+    const bool fetch = a.dense && r0 == 0;
+    for (; ok && p.valid; p = nx) {
+      nx = paged_next<KT, kLatentOverhead>(a, share, p);
       const int32_t* row = a.table + p.b * a.table_stride;
       for (int t = p.t0; t < p.t1; ++t, ++T) {
         const int s = T % ST;
@@ -147,138 +210,171 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
         const int at = key < p.len ? key : t * KT;
         int page = 0;
         if (lane < parts) page = checked_page(row[at >> a.page_shift], a.num_pages, a.status);
-        if (T >= ST && !(ok = __all_sync(0xffffffffu, mbar_wait(&ctl.empty[s], ((T / ST) - 1) & 1,
-                                                                wc, kSiteLatentFree))))
-          break;
-        if (lane == 0) mbar_arrive_expect_tx(&ctl.full[s], C::kTileBytes);
-        __syncwarp();
-        if (lane < parts) {
+        // the key-only columns first: they are released first
 #pragma unroll
-          for (int x = 0; x < C::kBoxes; ++x)
-            tma_load_4d(sC + s * C::kTileBytes + x * C::kBoxBytes + lane * rows * 128, &tc,
-                        &ctl.full[s], x * 64, at & ((1 << a.page_shift) - 1), 0, page);
+        for (int x = 0; x < C::kGroups; ++x) {
+          if (T >= ST && !(ok = __all_sync(0xffffffffu, mbar_wait(&ctl.empty[s][x], ((T / ST) - 1) & 1,
+                                                                  wc, kSiteLatentFree))))
+            break;
+          const int box = x == 0 ? C::kBoxes - 1 : 2 * (x - 1), boxes = x == 0 ? 1 : 2;
+          if (lane == 0) mbar_arrive_expect_tx(&ctl.full[s][x], boxes * C::kBoxBytes);
+          __syncwarp();
+          if (lane < parts)
+            for (int k = box; k < box + boxes; ++k)
+              tma_load_4d(sC + s * C::kTileBytes + k * C::kBoxBytes + lane * rows * 128, &tc,
+                          &ctl.full[s][x], k * 64, at & ((1 << a.page_shift) - 1), 0, page);
         }
+        if (!ok) break;
+        // (a CTA's first tiles themselves go out before any of this)
+        if (fetch && T + 1 >= ST)
+          for (int k = T + 1 == ST ? 1 : kAhead; k <= kAhead; ++k) ahead(t + k);
       }
     }
     if (!ok && lane == 0)   // let issued copies land before the CTA exits
-      for (uint32_t u = T > ST ? T - ST : 0; u < T; ++u)
-        mbar_wait_drain(&ctl.full[u % ST], (u / ST) & 1, a.timeout_ns);
+      for (uint32_t u = T > ST ? T - ST : 0; u <= T; ++u)   // (of tile T some groups, perhaps)
+        for (int x = 0; x < C::kGroups; ++x)
+          if (u < T || mbar_test(&ctl.empty[u % ST][x], ((u / ST) - 1) & 1))
+            mbar_wait_drain(&ctl.full[u % ST][x], (u / ST) & 1, a.timeout_ns);
   } else if (warp == 9) {
     // --------------------------------------------------------- MMA issue
-    constexpr uint32_t kIdS = idesc_bf16(128, kLatentRows, false, false);
+    // One elected lane issues, in code that the whole warp runs, from values
+    // that are known to be the same in all its lanes (the shuffles): the
+    // operands' descriptors then stay in uniform registers, and an MMA goes out
+    // every 31 cycles (64 x 64 x 16) or 46 (128 x 64 x 16) instead of every 58.
+    constexpr uint32_t kIdS = idesc_bf16(64, kLatentRows, false, false);
     constexpr uint32_t kIdO = idesc_bf16(128, kLatentRows, true, true);
+    const bool one = elect_one_lane();
     const uint64_t dq = smem_desc(smem_u32(sQ), 16, 1024);
     const uint64_t dp = smem_desc(smem_u32(sP), 16, 1024);
     bool ok = true;
     uint32_t T = 0;   // tiles before this piece
     int k = 0;        // pieces with tiles
-    for (; ok && p.valid; p = paged_next<KT, kLatentOverhead>(a, share, p, false)) {
-      const int n = p.t1 - p.t0;
+    for (; ok && __shfl_sync(0xffffffffu, p.valid, 0);
+         p = paged_next<KT, kLatentOverhead>(a, share, p)) {
+      const int n = __shfl_sync(0xffffffffu, p.t1 - p.t0, 0);
+      const int left = __shfl_sync(0xffffffffu, p.len - p.t0 * KT, 0);
       if (n == 0) continue;
-      // S^T of the piece's tile i (the tile has landed): zero what lies past
-      // the sequence's end, then issue
-      auto scores = [&](int i) {
+      // S^T of the piece's tile i, group by group as they land; what lies past
+      // the sequence's end is zeroed (it would be a value row)
+      // which groups of tile i have landed: all of them?
+      auto landed = [&](int i) {
+        const uint32_t u = T + i;
+        return __all_sync(0xffffffffu, lane >= C::kGroups ||
+                                           mbar_test(&ctl.full[u % ST][lane], (u / ST) & 1)) != 0;
+      };
+      auto scores = [&](int i, bool all) {
         const uint32_t u = T + i, s = u % ST;
         uint8_t* tile = sC + s * C::kTileBytes;
-        const int from = p.len - (p.t0 + i) * KT;
-        if (from < KT) {
-          for (int e = lane; e < (KT - from) * C::kBoxes * 8; e += 32) {
-            const int j = from + e / (C::kBoxes * 8), c = e % (C::kBoxes * 8);
-            *reinterpret_cast<uint4*>(tile + (c >> 3) * C::kBoxBytes + j * 128 + ((c & 7) << 4)) =
-                make_uint4(0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        tc_fence_after();
-        if (lane == 0) {
-          const uint64_t dc = smem_desc(smem_u32(tile), 16, 1024);
+        const int from = left - i * KT;
+        const uint64_t dc = smem_desc(smem_u32(tile), 16, 1024);
 #pragma unroll
-          for (int kk = 0; kk < C::kCols / 16; ++kk) {
-            const uint64_t off = static_cast<uint64_t>(((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4);
-            mma_ss(tmem + 64 * (u & 1), dc + off, dq + off, kIdS, kk > 0 ? 1u : 0u);
+        for (int x = 0; x < C::kGroups; ++x) {
+          if (!all) {
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&ctl.full[s][x], (u / ST) & 1, wc,
+                                                         kSiteLatentTile))))
+              return;
+            tc_fence_after();
           }
+          const int box = x == 0 ? C::kBoxes - 1 : 2 * (x - 1), boxes = x == 0 ? 1 : 2;
+          if (from < KT) {
+            for (int e = lane; e < (KT - from) * boxes * 8; e += 32) {
+              const int j = from + e / (boxes * 8), c = box * 8 + e % (boxes * 8);
+              *reinterpret_cast<uint4*>(tile + (c >> 3) * C::kBoxBytes + j * 128 + ((c & 7) << 4)) =
+                  make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (one) {
+#pragma unroll
+            for (int kk = 4 * box; kk < 4 * (box + boxes); ++kk) {
+              const uint64_t off =
+                  static_cast<uint64_t>(((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4);
+              mma_ss(tmem + 64 * (u & 1), dc + off, dq + off, kIdS, x > 0 || (kk & 3) > 0 ? 1u : 0u);
+            }
+          }
+        }
+        if (one) {
+          mma_commit(&ctl.empty[s][0]);
           mma_commit(&ctl.sfull[u & 1]);
         }
         __syncwarp();
       };
-      auto landed = [&](int i, bool wait) {
-        const uint32_t u = T + i;
-        if (!wait)
-          return __all_sync(0xffffffffu, mbar_test(&ctl.full[u % ST], (u / ST) & 1)) != 0;
-        return (ok = __all_sync(0xffffffffu, mbar_wait(&ctl.full[u % ST], (u / ST) & 1, wc,
-                                                       kSiteLatentTile)));
-      };
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(&ctl.qfull, k & 1, wc, kSiteLatentQ)))) break;
-      if (!landed(0, true)) break;
-      scores(0);
-      for (int i = 0; i < n; ++i) {
-        // the next tile's scores first if it has landed; P of this tile does
-        // not wait for it
+      tc_fence_after();
+      scores(0, landed(0));
+      for (int i = 0; ok && i < n; ++i) {
+        // the next tile's scores first if it has landed; P of this tile
+        // does not wait for it
+        const uint32_t u = T + i, s = u % ST;
         bool next = i + 1 < n;
-        if (next && landed(i + 1, false)) {
-          scores(i + 1);
+        if (next && landed(i + 1)) {
+          scores(i + 1, true);
           next = false;
         }
-        const uint32_t u = T + i, s = u % ST;
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&ctl.pfull, u & 1, wc, kSiteLatentP)))) break;
+        if (!ok || !(ok = __all_sync(0xffffffffu, mbar_wait(&ctl.pfull, u & 1, wc, kSiteLatentP))))
+          break;
         tc_fence_after();
-        if (lane == 0) {   // O^T += c^T P^T, 128 value columns at a time
 #pragma unroll
-          for (int blk = 0; blk < C::kBlocks; ++blk) {
-            const uint64_t dv = smem_desc(smem_u32(sC + s * C::kTileBytes + 2 * blk * C::kBoxBytes),
-                                          C::kBoxBytes, 1024);
+        for (int blk = 0; blk < C::kBlocks; ++blk) {   // O^T += c^T P^T, 128 value columns at a time
+          const uint64_t dv = smem_desc(smem_u32(sC + s * C::kTileBytes + 2 * blk * C::kBoxBytes),
+                                        C::kBoxBytes, 1024);
+          if (one) {
 #pragma unroll
             for (int kk = 0; kk < KT / 16; ++kk) {
               const uint64_t off = static_cast<uint64_t>((kk * 2048) >> 4);
               mma_ss(tmem + C::kOCol + 64 * blk, dv + off, dp + off, kIdO, i > 0 || kk > 0 ? 1u : 0u);
             }
+            mma_commit(&ctl.empty[s][1 + blk]);
           }
-          mma_commit(&ctl.empty[s]);
-          mma_commit(&ctl.pvdone);
         }
+        if (one) mma_commit(&ctl.pvdone);
         __syncwarp();
-        if (next) {
-          if (!landed(i + 1, true)) break;
-          scores(i + 1);
-        }
+        if (next) scores(i + 1, false);
       }
       T += n;
       ++k;
     }
-    if (lane == 0) {
+    if (one) {
       mma_commit(&ctl.final_bar);   // every MMA of this CTA done before TMEM is freed
       mbar_wait_drain(&ctl.final_bar, 0, a.timeout_ns);
     }
     __syncwarp();
   } else {
     // ------------------------------------------- q, softmax, rescale, output
-    const bool soft = (warp & 2) == 0 && ((warp >> 2) == 0 || live > 32);
-    const int key_row = (warp & 1) * 32 + lane;    // softmax: this thread's key of a tile
-    const int half = warp >> 2;                    // ... and columns 32 half .. 32 half + 31
+    // softmax: 16 keys and 32 of the columns a warp, in the MMA's fragment
+    // layout: keys g, g + 8 and columns 8 b + 2 q, + 1 (b = 0 .. 3) a thread
+    const int quad = warp & 3, half = warp >> 2;
+    const bool soft = half == 0 || live > 32;
+    const int g = lane >> 2, q4 = lane & 3;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const float c2 = a.scale_log2;
     bool ok = true;
     uint32_t T = 0;
-    for (; p.valid; p = paged_next<KT, kLatentOverhead>(a, share, p, threadIdx.x == 0 && r0 == 0)) {
+    MergeNote note{-1, 0, 0, 0};
+    // q rows r0 .. of the piece's sequence, K-major (asynchronous copies: all
+    // are in flight together)
+    auto load_q = [&](const PagedPiece& w) {
+      if (!w.valid || w.t0 == w.t1) return;
+      for (int r = warp; r < live; r += 8) {
+        const int h = (r0 + r) / a.n_q, qt = (r0 + r) - h * a.n_q;
+        const __nv_bfloat16* src = a.q + w.b * a.stride_b + h * a.stride_h +
+                                   static_cast<int64_t>(qt) * a.stride_n;
+        for (int c = lane; c < C::kBoxes * 8; c += 32)
+          copy16_async(sQ + (c >> 3) * C::kBoxBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                       src + c * 8);
+      }
+    };
+    load_q(p);
+    for (PagedPiece nx = p; p.valid; p = nx) {
+      nx = paged_next<KT, kLatentOverhead>(a, share, p);
       const int n = p.t1 - p.t0;
       float mref[2] = {-INFINITY, -INFINITY};   // columns lane, lane + 32: reference maxima
-      float mc[32], l[32];                      // softmax: this half's columns
+      float mc[8], l[8];                        // softmax: this thread's columns
 #pragma unroll
-      for (int j = 0; j < 32; ++j) mc[j] = l[j] = 0.f;
+      for (int j = 0; j < 8; ++j) mc[j] = l[j] = 0.f;
       if (n > 0) {
-        // q rows r0 .. r0 + 63 of the sequence (zero past the last), K-major
-        for (int e = threadIdx.x; e < kLatentRows * C::kBoxes * 8; e += 256) {
-          const int r = e / (C::kBoxes * 8), c = e - r * (C::kBoxes * 8);
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (r < live) {
-            const int h = (r0 + r) / a.n_q, qt = (r0 + r) - h * a.n_q;
-            v = *reinterpret_cast<const uint4*>(a.q + p.b * a.stride_b + h * a.stride_h +
-                                                static_cast<int64_t>(qt) * a.stride_n + c * 8);
-          }
-          *reinterpret_cast<uint4*>(sQ + (c >> 3) * C::kBoxBytes + r * 128 +
-                                    (((c & 7) ^ (r & 7)) << 4)) = v;
-        }
+        copies_wait();
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl.qfull);
@@ -286,37 +382,46 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
       const int open = a.causal ? p.len - a.n_q + 1 : p.len;   // every row is allowed keys below it
       for (int i = 0; i < n; ++i, ++T) {
         const int buf = T & 1;
-        uint32_t sr[32];
+        uint32_t sr[16];
         if (soft) {
           if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&ctl.sfull[buf], (T >> 1) & 1, wc,
                                                          kSiteLatentS));
           tc_fence_after();
-          tmem_ld32(tmem + lanes + 64 * buf + 32 * half, sr);
+          tmem_ld_16x32(tmem + lanes + 64 * buf + 32 * half, sr);
           tmem_wait_ld();
-          const int k0 = (p.t0 + i) * KT, kj = k0 + key_row;
+          const int k0 = (p.t0 + i) * KT;
           if (k0 + KT > open) {
-            int qt = (r0 + 32 * half) % a.n_q;
+            const int kj = k0 + 16 * quad + g;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
+            for (int j = 0; j < 16; ++j) {
+              const int qt = (r0 + 32 * half + 8 * (j >> 2) + 2 * q4 + (j & 1)) % a.n_q;
               const int lim = a.causal ? p.len - a.n_q + qt + 1 : p.len;
-              if (kj >= lim) sr[j] = __float_as_uint(-INFINITY);
-              if (++qt == a.n_q) qt = 0;
+              if (kj + 8 * ((j >> 1) & 1) >= lim) sr[j] = __float_as_uint(-INFINITY);
             }
           }
-          float top = -INFINITY;
+          float top[8];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float x = warp_max(__uint_as_float(sr[j]));
-            if (lane == j) top = x;
+          for (int j = 0; j < 8; ++j) {
+            const int at = 4 * (j >> 1) + (j & 1);
+            top[j] = fmaxf(__uint_as_float(sr[at]), __uint_as_float(sr[at + 2]));
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1)
+              top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
           }
-          ctl.wmax[buf][warp & 1][32 * half + lane] = top;
+          if (g == 0) {
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+              *reinterpret_cast<float2*>(&ctl.wmax[buf][quad][32 * half + 8 * b + 2 * q4]) =
+                  make_float2(top[2 * b], top[2 * b + 1]);
+          }
         }
         named_barrier_sync(1, 256);
         float alpha[2];
         bool grown[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float x = fmaxf(ctl.wmax[buf][0][lane + 32 * e], ctl.wmax[buf][1][lane + 32 * e]);
+          const float x = fmaxf(fmaxf(ctl.wmax[buf][0][lane + 32 * e], ctl.wmax[buf][1][lane + 32 * e]),
+                                fmaxf(ctl.wmax[buf][2][lane + 32 * e], ctl.wmax[buf][3][lane + 32 * e]));
           grown[e] = x > mref[e] && (mref[e] == -INFINITY || (x - mref[e]) * c2 > kRescaleTau);
           alpha[e] = grown[e] ? ex2_approx((mref[e] - x) * c2) : 1.f;
           if (grown[e]) mref[e] = x;
@@ -330,9 +435,10 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
             const float al = half ? alpha[1] : alpha[0], mr = half ? mref[1] : mref[0];
             const float mrc = mr == -INFINITY ? 0.f : mr * c2;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              l[j] *= __shfl_sync(0xffffffffu, al, j);
-              mc[j] = __shfl_sync(0xffffffffu, mrc, j);
+            for (int j = 0; j < 8; ++j) {
+              const int from = 8 * (j >> 1) + 2 * q4 + (j & 1);
+              l[j] *= __shfl_sync(0xffffffffu, al, from);
+              mc[j] = __shfl_sync(0xffffffffu, mrc, from);
             }
           }
           if (i > 0) {
@@ -353,21 +459,20 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
             tmem_wait_st();
           }
         }
-        if (soft) {   // P^T row of this thread's key: 32 columns, 64 bytes
+        if (soft) {   // P^T: two columns of keys g and g + 8 at a time
 #pragma unroll
-          for (int c8 = 0; c8 < 4; ++c8) {
-            uint32_t w[4];
+          for (int b = 0; b < 4; ++b) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int j = 8 * c8 + 2 * q;
-              const float p0 = ex2_approx(fmaf(__uint_as_float(sr[j]), c2, -mc[j]));
-              const float p1 = ex2_approx(fmaf(__uint_as_float(sr[j + 1]), c2, -mc[j + 1]));
-              l[j] += p0;
-              l[j + 1] += p1;
-              w[q] = pack_bf16x2(p0, p1);
+            for (int e = 0; e < 2; ++e) {
+              const int row = 16 * quad + g + 8 * e;
+              const float p0 = ex2_approx(fmaf(__uint_as_float(sr[4 * b + 2 * e]), c2, -mc[2 * b]));
+              const float p1 =
+                  ex2_approx(fmaf(__uint_as_float(sr[4 * b + 2 * e + 1]), c2, -mc[2 * b + 1]));
+              l[2 * b] += p0;
+              l[2 * b + 1] += p1;
+              *reinterpret_cast<uint32_t*>(sP + row * 128 + (((4 * half + b) ^ (row & 7)) << 4) +
+                                           4 * q4) = pack_bf16x2(p0, p1);
             }
-            *reinterpret_cast<uint4*>(sP + key_row * 128 + (((4 * half + c8) ^ (key_row & 7)) << 4)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
           }
           fence_proxy_async_smem();
         }
@@ -376,17 +481,21 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
         if (lane == 0) mbar_arrive(&ctl.pfull);
       }
 
-      // ---- O = O^T / l and L of the piece
+      // ---- O = O^T / l and L of the piece; every score MMA of the piece is
+      // complete (a warp waited for the last before the last barrier), so the
+      // next piece's q can come
+      load_q(nx);
       if (n > 0 && soft) {
-        float mine = 0.f;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          float x = l[j];
+        for (int j = 0; j < 8; ++j)
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-          if (lane == j) mine = x;
+          for (int o = 4; o < 32; o <<= 1) l[j] += __shfl_xor_sync(0xffffffffu, l[j], o);
+        if (g == 0) {
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            *reinterpret_cast<float2*>(&ctl.wmax[T & 1][quad][32 * half + 8 * b + 2 * q4]) =
+                make_float2(l[2 * b], l[2 * b + 1]);
         }
-        ctl.lsum[warp & 1][32 * half + lane] = mine;
       }
       if (n > 0 && ok) {
         ok = __all_sync(0xffffffffu, mbar_wait(&ctl.pvdone, (T - 1) & 1, wc, kSiteLatentDone));
@@ -396,11 +505,14 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
       float inv[2], L[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float s = n > 0 ? ctl.lsum[0][lane + 32 * e] + ctl.lsum[1][lane + 32 * e] : 0.f;
+        const float(*sum)[64] = ctl.wmax[T & 1];
+        const int c = lane + 32 * e;
+        const float s = n > 0 ? (sum[0][c] + sum[1][c]) + (sum[2][c] + sum[3][c]) : 0.f;
         inv[e] = s != 0.f ? 1.f / s : 0.f;
         L[e] = s != 0.f ? (mref[e] * c2 + __log2f(s)) * kLn2 : -INFINITY;
       }
       const bool whole = p.whole();
+      if (p.t0 == 0 && !whole) note = paged_note<kLatentOverhead>(share, p);
       const int64_t part = 2 * static_cast<int64_t>(cta) + (p.s < share.lo ? 0 : 1);
       if (warp == 0) {
 #pragma unroll
@@ -416,43 +528,45 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
       for (int bb = 0; bb < C::kBlocks / 2; ++bb) {
         const int blk = half * (C::kBlocks / 2) + bb;
         const int dim = 128 * blk + (warp & 3) * 32 + lane;
+        // 16 rows (columns of O^T) at a time
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if (32 * e >= live) break;
-          uint32_t o[32];
+        for (int e = 0; e < 4; ++e) {
+          if (16 * e >= live) break;
+          uint32_t o[16];
           if (n > 0) {
-            tmem_ld32(tmem + lanes + C::kOCol + 64 * blk + 32 * e, o);
+            tmem_ld16(tmem + lanes + C::kOCol + 64 * blk + 16 * e, o);
             tmem_wait_ld();
           }
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float w = __shfl_sync(0xffffffffu, inv[e], j);
+          for (int j = 0; j < 16; ++j) {
+            const float w = __shfl_sync(0xffffffffu, inv[e >> 1], 16 * (e & 1) + j);
             o[j] = n > 0 && w != 0.f ? __float_as_uint(__uint_as_float(o[j]) * w) : 0u;
           }
           if (whole) {
             // lanes 2 i, 2 i + 1 trade: the even one stores its two columns of
             // row j, the odd one those of row j + 1
+            __nv_bfloat16* to = a.o + (static_cast<int64_t>(p.b) * a.all_rows + r0 + 16 * e) * DV +
+                                (dim & ~1);
 #pragma unroll
-            for (int j = 0; j < 32; j += 2) {
+            for (int j = 0; j < 16; j += 2) {
               const uint32_t give = (lane & 1) ? o[j] : o[j + 1];
               const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 1);
               const uint32_t v = (lane & 1) ? pack_bf16x2(__uint_as_float(got), __uint_as_float(o[j + 1]))
                                             : pack_bf16x2(__uint_as_float(o[j]), __uint_as_float(got));
-              const int r = 32 * e + j + (lane & 1);
-              if (r < live)
-                *reinterpret_cast<uint32_t*>(
-                    a.o + (static_cast<int64_t>(p.b) * a.all_rows + r0 + r) * DV + (dim & ~1)) = v;
+              const int r = j + (lane & 1);
+              if (16 * e + r < live) *reinterpret_cast<uint32_t*>(to + r * DV) = v;
             }
           } else {
+            float* to = a.part_o + (part * a.rows + r0 + 16 * e) * DV + dim;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (32 * e + j < live)
-                a.part_o[(part * a.rows + r0 + 32 * e + j) * DV + dim] = __uint_as_float(o[j]);
+            for (int j = 0; j < 16; ++j)
+              if (16 * e + j < live) to[j * DV] = __uint_as_float(o[j]);
           }
         }
       }
       tc_fence_before();
     }
+    if (threadIdx.x == 0 && r0 == 0) a.notes[cta] = note;
   }
 
   tc_fence_before();

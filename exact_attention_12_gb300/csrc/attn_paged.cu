@@ -88,39 +88,6 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// A row's final O (four columns) and L from its own partial (o, L) and the
-// shared prefix's.  L = log sum e^(L_s), O = sum e^(L_s - L) O_s.
-template <int D>
-__device__ __forceinline__ float fold_prefix(const PagedArgs& a, int64_t row, int c, float L,
-                                             float4& o) {
-  if (a.pre_splits == 0) return L;
-  const int64_t rows = static_cast<int64_t>(a.B) * a.H * a.n_q;
-  float top = L;
-  for (int s = 0; s < a.pre_splits; ++s) top = fmaxf(top, a.pre_l[s * rows + row]);
-  if (top == -INFINITY) return L;
-  const float w0 = __expf(L - top);   // L = -inf: weight 0
-  float sum = w0;
-  o.x *= w0;
-  o.y *= w0;
-  o.z *= w0;
-  o.w *= w0;
-  for (int s = 0; s < a.pre_splits; ++s) {
-    const float w = __expf(a.pre_l[s * rows + row] - top);
-    const float4 x = *reinterpret_cast<const float4*>(a.pre_o + (s * rows + row) * D + c);
-    sum += w;
-    o.x = fmaf(w, x.x, o.x);
-    o.y = fmaf(w, x.y, o.y);
-    o.z = fmaf(w, x.z, o.z);
-    o.w = fmaf(w, x.w, o.w);
-  }
-  const float inv = 1.f / sum;
-  o.x *= inv;
-  o.y *= inv;
-  o.z *= inv;
-  o.w *= inv;
-  return top + __logf(sum);
-}
-
 template <int D, int MT>
 __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kCtasPerSm)
     paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
@@ -153,7 +120,7 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
   grid_dep_launch();
   const PagedShare share = paged_share<C::kThreads, KT, kPagedOverhead>(
       a, blockIdx.x, gridDim.x, sh.sums, &sh.share);
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.starts[a.B] = share.total;
+  MergeNote note{-1, 0, 0, 0};
   const WaitCtx wc{&sh.abort_flag, a.status, a.timeout_ns};
   const int box_rows = min(KT, 1 << a.page_shift);
   bool ok = true;
@@ -218,7 +185,7 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
   const int lb = lane >> 3, lr = lane & 7;
   const float c2 = a.scale_log2;
 
-  PagedPiece p = paged_piece<KT, kPagedOverhead>(a, share, share.b, 0, share.s, threadIdx.x == 0);
+  PagedPiece p = paged_piece<KT, kPagedOverhead>(a, share, share.b, 0, share.s);
   prefetch(p);
   while (p.valid) {   // (the same pieces in every warp)
     const int nu = slot_tiles(p);
@@ -344,7 +311,7 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
       }
     }
 
-    const PagedPiece next = paged_next<KT, kPagedOverhead>(a, share, p, threadIdx.x == 0);
+    const PagedPiece next = paged_next<KT, kPagedOverhead>(a, share, p);
     if (ok) prefetch(next);
 
     // ---- the slots' states merged: m, l per row, then O through shared memory
@@ -373,6 +340,10 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
       scale[i] = mrow[i] == -INFINITY ? 0.f : ex2_approx((mrow[i] - mx) * c2) / lt;
     }
     const bool whole = p.whole();
+    const bool apart = a.pre_splits > 0;   // a prefix is merged afterwards
+    if (p.t0 == 0 && !whole) note = paged_note<kPagedOverhead>(share, p);
+    if (apart && p.t0 == 0 && threadIdx.x == 0)
+      a.notes[p.b * a.heads + p.h] = whole ? MergeNote{p.b, p.h, 0, -1} : note;
     const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (p.s < share.lo ? 0 : 1);
     for (int m = 0; m < MT; ++m) {   // 16 rows at a time
       for (int w = 0; w < kSlots; ++w) {   // in turn: the sum has a fixed order
@@ -408,7 +379,12 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
         if (whole) {
           const int hl = r / a.n_q, qt = r - hl * a.n_q, h = p.h * a.group + hl;
           const int64_t row = (static_cast<int64_t>(p.b) * a.H + h) * a.n_q + qt;
-          L = fold_prefix<D>(a, row, c, L, x);
+          if (apart) {
+            const int64_t at = a.pre_splits * (static_cast<int64_t>(a.B) * a.all_rows) + row;
+            *reinterpret_cast<float4*>(a.pre_o + at * D + c) = x;
+            if (c == 0) a.pre_l[at] = L;
+            continue;
+          }
           *reinterpret_cast<uint2*>(a.o + p.b * a.stride_b + h * a.stride_h +
                                     static_cast<int64_t>(qt) * a.stride_n + c) =
               make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
@@ -423,75 +399,111 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
     if (!ok) break;
     p = next;
   }
+  if (a.pre_splits == 0 && threadIdx.x == 0) a.notes[blockIdx.x] = note;
   if (!ok && mt == 0 && lane == 0) {   // let issued copies land before the CTA exits
     for (uint32_t t = issued > ST ? issued - ST : 0; t < issued; ++t)
       mbar_wait_drain(&sh.full[slot * ST + t % ST], (t / ST) & 1, a.timeout_ns);
   }
 }
 
-// Segments that were cut: their pieces merged, four columns of a row per
-// thread.  A CTA per (segment, 128 of its rows x columns / 4).
-template <int D>
-__global__ void __launch_bounds__(128)
-    paged_merge_kernel(const PagedArgs a, int keys, int overhead, int launched) {
-  grid_dep_wait();
-  grid_dep_launch();
-  const int b = blockIdx.x / a.heads, h = blockIdx.x - b * a.heads;
-  const int64_t total = a.starts[a.B];
-  const int len = paged_len(a, b) - a.first;
-  const int n = len > 0 ? (len + keys - 1) / keys : 0;
-  if (n == 0) return;   // written by the CTA that owns it
-  const int64_t s = a.starts[b] + static_cast<int64_t>(h) * (n + overhead);
-  const int ctas = paged_ctas(total, launched);
-  auto owner = [&](int64_t unit) {
-    int i = static_cast<int>(unit * ctas / total);
-    while (total * (i + 1) / ctas <= unit) ++i;
-    while (total * i / ctas > unit) --i;
-    return i;
-  };
-  const int i0 = owner(s + overhead), i1 = owner(s + overhead + n - 1);
-  if (i0 == i1) return;   // finished by that CTA
-  const int rows = min(a.rows, a.all_rows - h * a.rows);
-  const int e = blockIdx.y * 128 + threadIdx.x;
-  const int r = e / (D / 4), c = 4 * (e - r * (D / 4));
-  if (r >= rows) return;
-  // the CTAs between hold one piece each, of a segment begun before them
-  auto slot_of = [&](int i) {
-    return 2 * static_cast<int64_t>(i) + (i == i0 && s >= total * i0 / ctas ? 1 : 0);
-  };
+// Four columns of a row's O and its L, merged from `n` partials: the i-th has
+// its L at part_l[at(i)] and its columns at part_o[at(i) * D + c] of the arrays
+// that `from` names.  L = log sum e^(L_i), O = sum e^(L_i - L) O_i.
+template <int D, typename From>
+__device__ __forceinline__ void merge_row(int n, int c, const From& from, float4& x, float& L) {
+  x = make_float4(0.f, 0.f, 0.f, 0.f);
   float top = -INFINITY;
 #pragma unroll 4
-  for (int i = i0; i <= i1; ++i) top = fmaxf(top, a.part_l[slot_of(i) * a.rows + r]);
-  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-  float L = -INFINITY;
-  if (top > -INFINITY) {
-    float sum = 0.f;
+  for (int i = 0; i < n; ++i) top = fmaxf(top, *from(i).l);
+  L = top;
+  if (top == -INFINITY) return;
+  float sum = 0.f;
 #pragma unroll 4
-    for (int i = i0; i <= i1; ++i) {
-      const int64_t at = slot_of(i) * a.rows + r;
-      const float w = __expf(a.part_l[at] - top);
-      const float4 y = *reinterpret_cast<const float4*>(a.part_o + at * D + c);
-      sum += w;
-      x.x = fmaf(w, y.x, x.x);
-      x.y = fmaf(w, y.y, x.y);
-      x.z = fmaf(w, y.z, x.z);
-      x.w = fmaf(w, y.w, x.w);
-    }
-    const float inv = 1.f / sum;
-    x.x *= inv;
-    x.y *= inv;
-    x.z *= inv;
-    x.w *= inv;
-    L = top + __logf(sum);
+  for (int i = 0; i < n; ++i) {
+    const auto part = from(i);
+    const float w = __expf(*part.l - top);
+    const float4 y = *reinterpret_cast<const float4*>(part.o + c);
+    sum += w;
+    x.x = fmaf(w, y.x, x.x);
+    x.y = fmaf(w, y.y, x.y);
+    x.z = fmaf(w, y.z, x.z);
+    x.w = fmaf(w, y.w, x.w);
   }
-  const int64_t row0 = static_cast<int64_t>(b) * a.all_rows;
-  const int hr = h * a.rows + r;   // row of the sequence: head * n_q + query
-  L = fold_prefix<D>(a, row0 + hr, c, L, x);
-  const int hq = hr / a.n_q, qt = hr - hq * a.n_q;
-  *reinterpret_cast<uint2*>(a.o + b * a.stride_b + hq * a.stride_h +
+  const float inv = 1.f / sum;
+  x.x *= inv;
+  x.y *= inv;
+  x.z *= inv;
+  x.w *= inv;
+  L = top + __logf(sum);
+}
+
+struct Partial {
+  const float *o, *l;
+};
+
+// Row hr (head * n_q + query) of sequence b.
+__device__ __forceinline__ void write_row(const PagedArgs& a, int b, int hr, int c, const float4& x,
+                                          float L) {
+  const int h = hr / a.n_q, qt = hr - h * a.n_q;
+  *reinterpret_cast<uint2*>(a.o + b * a.stride_b + h * a.stride_h +
                             static_cast<int64_t>(qt) * a.stride_n + c) =
       make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-  if (c == 0) a.lse[row0 + hr] = L;
+  if (c == 0) a.lse[static_cast<int64_t>(b) * a.all_rows + hr] = L;
+}
+
+// Segments that were cut: their pieces merged, four columns of a row per
+// thread.  A CTA per (CTA that may have left a note, 128 x 4 elements).
+template <int D>
+__global__ void __launch_bounds__(128) paged_merge_kernel(const PagedArgs a) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int4 raw = *reinterpret_cast<const int4*>(a.notes + blockIdx.x);
+  const MergeNote note{raw.x, raw.y, raw.z, raw.w};
+  if (note.b < 0) return;
+  const int e = blockIdx.y * 128 + threadIdx.x;
+  const int r = e / (D / 4), c = 4 * (e % (D / 4));
+  const int hr = note.h * a.rows + r;
+  if (r >= a.rows || hr >= a.all_rows) return;
+  auto piece = [&](int i) {
+    const int64_t at =
+        static_cast<int64_t>(i == 0 ? note.slot : (note.slot & ~1) + 2 * i) * a.rows + r;
+    return Partial{a.part_o + at * D, a.part_l + at};
+  };
+  float4 x;
+  float L;
+  merge_row<D>(note.more + 1, c, piece, x, L);
+  write_row(a, note.b, hr, c, x, L);
+}
+
+// With a shared prefix: every row from the prefix's pieces and its own
+// segment, in one piece or cut.  A CTA per (segment, 128 x 4 elements).
+template <int D>
+__global__ void __launch_bounds__(128) paged_finish_kernel(const PagedArgs a) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int4 raw = *reinterpret_cast<const int4*>(a.notes + blockIdx.x);
+  const MergeNote note{raw.x, raw.y, raw.z, raw.w};
+  const int e = blockIdx.y * 128 + threadIdx.x;
+  const int r = e / (D / 4), c = 4 * (e % (D / 4));
+  if (r >= a.rows) return;
+  const int hr = note.h * a.rows + r;
+  const int64_t row = static_cast<int64_t>(note.b) * a.all_rows + hr;
+  const int64_t all = static_cast<int64_t>(a.B) * a.all_rows;
+  const int pre = a.pre_splits + (note.more < 0 ? 1 : 0);
+  auto part = [&](int i) {
+    if (i < pre) {
+      const int64_t at = i * all + row;
+      return Partial{a.pre_o + at * D, a.pre_l + at};
+    }
+    i -= pre;
+    const int64_t at =
+        static_cast<int64_t>(i == 0 ? note.slot : (note.slot & ~1) + 2 * i) * a.rows + r;
+    return Partial{a.part_o + at * D, a.part_l + at};
+  };
+  float4 x;
+  float L;
+  merge_row<D>(pre + note.more + 1, c, part, x, L);
+  write_row(a, note.b, hr, c, x, L);
 }
 
 template <int D, int MT>
@@ -527,15 +539,21 @@ cudaError_t launch_paged(const CUtensorMap& tk, const CUtensorMap& tv, const Pag
   return a.d == 64 ? launch_d<64>(tk, tv, a, ctas, s) : launch_d<128>(tk, tv, a, ctas, s);
 }
 
-cudaError_t launch_paged_merge(const PagedArgs& a, int keys, int overhead, int ctas,
-                               cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(a.B * a.heads),
-                  static_cast<unsigned>((a.rows * (a.d / 4) + 127) / 128));
+cudaError_t launch_paged_merge(const PagedArgs& a, int ctas, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>(ctas),
+                  static_cast<unsigned>((min(a.rows, a.all_rows) * (a.d / 4) + 127) / 128));
   auto kernel = a.d == 64    ? paged_merge_kernel<64>
                 : a.d == 128 ? paged_merge_kernel<128>
                 : a.d == 256 ? paged_merge_kernel<256>
                              : paged_merge_kernel<512>;
-  return launch_pdl(kernel, grid, dim3(128), 0, s, a, keys, overhead, ctas);
+  return launch_pdl(kernel, grid, dim3(128), 0, s, a);
+}
+
+cudaError_t launch_paged_finish(const PagedArgs& a, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>(a.B * a.heads),
+                  static_cast<unsigned>((a.rows * (a.d / 4) + 127) / 128));
+  return launch_pdl(a.d == 64 ? paged_finish_kernel<64> : paged_finish_kernel<128>, grid, dim3(128),
+                    0, s, a);
 }
 
 }  // namespace attn

@@ -19,13 +19,22 @@ constexpr int kStatusPage = 6;
 // The split of a decode step over its CTAs.  The problem is a list of
 // segments, one per (sequence, head group), sequence by sequence; a segment
 // of n key tiles costs n + overhead units (its set-up and write-out, in
-// tiles).  CTA i of G takes the units [i T / G, (i + 1) T / G) of the T in
-// all: every CTA gets the same share whatever the lengths are, and no CTA is
-// launched for keys a short sequence does not have.  A segment that falls to
-// one CTA is finished by it; one that is cut leaves a partial (O, L) per CTA,
-// merged afterwards by the logsumexp rule.  A CTA cuts at most its first and
-// its last segment, so it has two partial slots: slot 0 for a segment that
-// began before the CTA's range, slot 1 for one that begins in it.
+// tiles).  The units are dealt to the CTAs in equal runs (of all CTAs
+// launched, or of fewer when the lengths leave less than kPagedMinUnits each;
+// the others return): every CTA gets the same share whatever the lengths are,
+// and none waits for keys a short sequence does not have.  A segment that
+// falls to one CTA is finished by it; one that is cut leaves a partial (O, L)
+// per CTA, merged afterwards by the logsumexp rule.  A CTA cuts at most its
+// first and its last segment, so it has two partial slots: slot 0 for a
+// segment that began before the CTA's run, slot 1 for one that begins in it.
+// The CTA that holds a cut segment's first tile leaves a note of the merge.
+struct MergeNote {
+  int b, h;      // the segment; b < 0: nothing to merge
+  int slot;      // partial slot of the first piece, 2 CTA + 0 or 1; the next
+                 // CTAs' pieces are in their slot 0
+  int more;      // how many CTAs follow
+};
+
 struct PagedArgs {
   int B, H, heads;                // heads: segments per sequence
   int group;                      // query heads per segment
@@ -44,12 +53,17 @@ struct PagedArgs {
   int64_t stride_b, stride_h, stride_n;      // q (and o, but for latent)
   __nv_bfloat16* o;
   float* lse;                     // [B][H][n_q]
-  int64_t* starts;                // workspace [B + 1]: the first unit of each sequence, then T
+  // latent: the cache, for copies that go without its tensor map
+  const __nv_bfloat16* pages;
+  int64_t stride_page;
+  int dense;                      // a page's rows follow one another without gaps
+  MergeNote* notes;               // workspace [G]; with a prefix one per segment, [B * heads]
   float* part_o;                  // workspace [2 G][rows][d]
   float* part_l;                  // workspace [2 G][rows]
-  // the shared prefix's partials (pre_splits = 0: none)
-  const float* pre_o;             // workspace [pre_splits][B*H*n_q][d]
-  const float* pre_l;             // workspace [pre_splits][B*H*n_q]
+  // a shared prefix: its pieces' partials and, behind them, those of the
+  // segments that one CTA has finished (pre_splits = 0: no prefix)
+  float* pre_o;                   // workspace [pre_splits + 1][B*H*n_q][d]
+  float* pre_l;                   // workspace [pre_splits + 1][B*H*n_q]
   int pre_splits;
   int* status;
   uint64_t timeout_ns;
@@ -85,6 +99,7 @@ enum PagedSite : int {
   kSitePagedTile = 60, kSitePagedFree, kSitePrefixQ, kSitePrefixK, kSitePrefixV, kSitePrefixS,
   kSitePrefixP, kSitePrefixFree, kSitePrefixDone,
   kSiteLatentTile = 70, kSiteLatentS, kSiteLatentP, kSiteLatentFree, kSiteLatentDone, kSiteLatentQ,
+  kSiteLatentSmem,
   kSitePageIndex = 80
 };
 
@@ -114,11 +129,25 @@ __device__ __forceinline__ int paged_ctas(int64_t total, int launched) {
   return most >= launched ? launched : max(1, static_cast<int>(most));
 }
 
-// A CTA's share [lo, hi) of the T units, and where it starts.
+// a / b for a >= 0, b > 0; a long division is 100 instructions, and hardly
+// ever needed.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 31) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
+// A CTA's run [lo, hi) of the units, and where it starts.
 struct PagedShare {
-  int64_t lo, hi, total;
+  int64_t lo, hi;
+  int64_t q;      // units of a CTA: q + 1 of the first `extra` CTAs, q of the others
+  int extra, cta;
   int b;          // the sequence that holds unit lo
   int64_t s;      // its first unit
+  // The CTA whose run holds `unit`.
+  __device__ __forceinline__ int owner(int64_t unit) const {
+    const int64_t big = extra * (q + 1);
+    return static_cast<int>(unit < big ? quotient(unit, q + 1) : extra + quotient(unit - big, q));
+  }
 };
 
 // All threads of the CTA; `sums` has THREADS / 32 entries of shared memory.
@@ -150,15 +179,18 @@ __device__ __forceinline__ PagedShare paged_share(const PagedArgs& a, int cta, i
   }
   inc += before;
   PagedShare sh;
-  sh.total = total;
-  const int ctas = paged_ctas(total, launched);
+  const int64_t most = quotient(total, kPagedMinUnits);
+  const int ctas = most >= launched ? launched : max(1, static_cast<int>(most));
+  sh.cta = cta;
+  sh.q = quotient(total, ctas);
+  sh.extra = static_cast<int>(total - sh.q * ctas);
   if (cta >= ctas) {   // (uniform over the CTA)
     sh.lo = sh.hi = sh.s = total;
     sh.b = a.B;
     return sh;
   }
-  sh.lo = total * cta / ctas;
-  sh.hi = total * (cta + 1) / ctas;
+  sh.lo = sh.q * cta + min(cta, sh.extra);
+  sh.hi = sh.lo + sh.q + (cta < sh.extra ? 1 : 0);
   if (inc - mine <= sh.lo && sh.lo < inc) {
     int64_t s = inc - mine;
     int b = b0;
@@ -196,10 +228,9 @@ __device__ __forceinline__ void paged_clip(PagedPiece& p, const PagedShare& sh) 
 
 // The first piece at or after segment (b, h) at unit s that gives this CTA
 // something to do: tiles, or the rows of an empty segment that begins here.
-// `note`: record the sequences' first units that lie in this CTA's range.
 template <int KEYS, int OVERHEAD>
 __device__ __forceinline__ PagedPiece paged_piece(const PagedArgs& a, const PagedShare& sh, int b,
-                                                  int h, int64_t s, bool note) {
+                                                  int h, int64_t s) {
   PagedPiece p;
   p.valid = false;
   p.b = b;
@@ -209,7 +240,6 @@ __device__ __forceinline__ PagedPiece paged_piece(const PagedArgs& a, const Page
   p.len = paged_len(a, b);
   p.n = paged_tiles<KEYS>(a, b);
   while (p.s < sh.hi) {
-    if (note && p.h == 0 && p.s >= sh.lo) a.starts[p.b] = p.s;
     paged_clip<OVERHEAD>(p, sh);
     if (p.t1 > p.t0 || (p.n == 0 && p.s >= sh.lo)) {
       p.valid = true;
@@ -228,13 +258,20 @@ __device__ __forceinline__ PagedPiece paged_piece(const PagedArgs& a, const Page
 
 template <int KEYS, int OVERHEAD>
 __device__ __forceinline__ PagedPiece paged_next(const PagedArgs& a, const PagedShare& sh,
-                                                 const PagedPiece& p, bool note) {
+                                                 const PagedPiece& p) {
   int b = p.b, h = p.h + 1;
   if (h == a.heads) {
     h = 0;
     ++b;
   }
-  return paged_piece<KEYS, OVERHEAD>(a, sh, b, h, p.s + p.n + OVERHEAD, note);
+  return paged_piece<KEYS, OVERHEAD>(a, sh, b, h, p.s + p.n + OVERHEAD);
+}
+
+// The note of the merge that begins with piece p.
+template <int OVERHEAD>
+__device__ __forceinline__ MergeNote paged_note(const PagedShare& sh, const PagedPiece& p) {
+  return MergeNote{p.b, p.h, 2 * sh.cta + (p.s < sh.lo ? 0 : 1),
+                   sh.owner(p.s + OVERHEAD + p.n - 1) - sh.cta};
 }
 
 cudaError_t launch_paged(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, int ctas,
@@ -242,8 +279,8 @@ cudaError_t launch_paged(const CUtensorMap& tk, const CUtensorMap& tv, const Pag
 cudaError_t launch_prefix(const CUtensorMap& tk, const CUtensorMap& tv, const PrefixArgs& a,
                           cudaStream_t s);
 cudaError_t launch_latent(const CUtensorMap& tc, const PagedArgs& a, int ctas, cudaStream_t s);
-cudaError_t launch_paged_merge(const PagedArgs& a, int keys, int overhead, int ctas,
-                               cudaStream_t s);
+cudaError_t launch_paged_merge(const PagedArgs& a, int ctas, cudaStream_t s);
+cudaError_t launch_paged_finish(const PagedArgs& a, cudaStream_t s);
 
 // Tensor map of a paged cache for the host code (an attn_status).
 int encode_pages(CUtensorMap* map, const void* ptr, int num_pages, int heads, int page_size, int d,

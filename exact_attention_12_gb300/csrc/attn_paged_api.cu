@@ -113,7 +113,7 @@ attn_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
 bool empty(const attn_params* p) { return p->B == 0 || p->H == 0; }
 
 struct Layout {
-  size_t starts = 0, part_o = 0, part_l = 0, pre_o = 0, pre_l = 0, total = 0;
+  size_t notes = 0, part_o = 0, part_l = 0, pre_o = 0, pre_l = 0, total = 0;
   int ctas = 0;                            // of the decode kernel (latent: per row group)
   int heads = 0, group = 0, rows = 0;      // segments per sequence, heads and rows of one
   int first = 0, splits = 0, tiles = 0;    // the shared prefix
@@ -158,17 +158,19 @@ Layout layout(const attn_params* p, int32_t n_q, const attn_pages* g, bool laten
     L.splits = k < 1 ? 1 : static_cast<int>(k);
   }
   size_t off = kHeaderBytes;
-  L.starts = off;
-  off = round_up(off + (static_cast<size_t>(p->B) + 1) * sizeof(int64_t), 256);
+  L.notes = off;
+  off = round_up(off + (L.first > 0 ? static_cast<size_t>(p->B) * L.heads : L.ctas) *
+                           sizeof(attn::MergeNote),
+                 256);
   L.part_o = off;
   off = round_up(off + 2 * static_cast<size_t>(L.ctas) * L.rows * p->d * sizeof(float), 256);
   L.part_l = off;
   off = round_up(off + 2 * static_cast<size_t>(L.ctas) * L.rows * sizeof(float), 256);
   if (L.splits > 0) {
     L.pre_o = off;
-    off = round_up(off + static_cast<size_t>(L.splits) * rows_all * p->d * sizeof(float), 256);
+    off = round_up(off + static_cast<size_t>(L.splits + 1) * rows_all * p->d * sizeof(float), 256);
     L.pre_l = off;
-    off = round_up(off + static_cast<size_t>(L.splits) * rows_all * sizeof(float), 256);
+    off = round_up(off + static_cast<size_t>(L.splits + 1) * rows_all * sizeof(float), 256);
   }
   L.total = off;
   return L;
@@ -201,12 +203,12 @@ PagedArgs args_of(const attn_params* p, int32_t n_q, const attn_pages* g, const 
   a.stride_n = p->stride_n;
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;
-  a.starts = reinterpret_cast<int64_t*>(w + L.starts);
+  a.notes = reinterpret_cast<attn::MergeNote*>(w + L.notes);
   a.part_o = reinterpret_cast<float*>(w + L.part_o);
   a.part_l = reinterpret_cast<float*>(w + L.part_l);
   a.pre_splits = L.splits;
-  a.pre_o = reinterpret_cast<const float*>(w + L.pre_o);
-  a.pre_l = reinterpret_cast<const float*>(w + L.pre_l);
+  a.pre_o = reinterpret_cast<float*>(w + L.pre_o);
+  a.pre_l = reinterpret_cast<float*>(w + L.pre_l);
   a.status = reinterpret_cast<int*>(w);
   a.timeout_ns = kTimeoutNs;
   return a;
@@ -276,8 +278,8 @@ attn_status attn_decode_paged(const attn_params* p, int32_t n_q, const attn_page
     f.stride_b = a.stride_b;
     f.stride_h = a.stride_h;
     f.stride_n = a.stride_n;
-    f.pre_o = const_cast<float*>(a.pre_o);
-    f.pre_l = const_cast<float*>(a.pre_l);
+    f.pre_o = a.pre_o;
+    f.pre_l = a.pre_l;
     f.status = a.status;
     f.timeout_ns = a.timeout_ns;
     if ((st = launched(attn::launch_prefix(tk, tv, f, s), "shared prefix launch")) != ATTN_OK)
@@ -288,9 +290,9 @@ attn_status attn_decode_paged(const attn_params* p, int32_t n_q, const attn_page
     return st;
   if ((st = launched(attn::launch_paged(tk, tv, a, L.ctas, s), "paged decode launch")) != ATTN_OK)
     return st;
+  if (L.first > 0) return launched(attn::launch_paged_finish(a, s), "shared prefix merge launch");
   if (L.ctas == 1) return ATTN_OK;   // one CTA cuts nothing
-  return launched(attn::launch_paged_merge(a, attn::kPagedKeys, attn::kPagedOverhead, L.ctas, s),
-                  "paged merge launch");
+  return launched(attn::launch_paged_merge(a, L.ctas, s), "paged merge launch");
 }
 
 size_t attn_decode_latent_workspace_size(const attn_params* p, int32_t n_q,
@@ -310,6 +312,9 @@ attn_status attn_decode_latent(const attn_params* p, int32_t n_q, const attn_pag
   if ((st = check_ptrs({q, c, o, lse})) != ATTN_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   PagedArgs a = args_of(p, n_q, pages, L, q, o, lse, ws);
+  a.pages = static_cast<const __nv_bfloat16*>(c);
+  a.stride_page = p->kv_stride_b;
+  a.dense = p->kv_stride_n == p->d + attn::kLatentRope;
   CUtensorMap tc;
   st = static_cast<attn_status>(attn::encode_pages(
       &tc, c, at_least_1(pages->num_pages), 1, pages->page_size, p->d + attn::kLatentRope,
@@ -322,8 +327,7 @@ attn_status attn_decode_latent(const attn_params* p, int32_t n_q, const attn_pag
   a.stride_n = p->d;
   a.stride_h = static_cast<int64_t>(n_q) * p->d;
   a.stride_b = static_cast<int64_t>(p->H) * n_q * p->d;
-  return launched(attn::launch_paged_merge(a, attn::kLatentKeys, attn::kLatentOverhead, L.ctas, s),
-                  "latent merge launch");
+  return launched(attn::launch_paged_merge(a, L.ctas, s), "latent merge launch");
 }
 
 }  // extern "C"

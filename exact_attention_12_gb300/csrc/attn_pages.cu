@@ -27,8 +27,7 @@ using namespace sm103;
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanPer = 8;                              // pages per thread and batch
-constexpr int kPlanBatch = kPlanThreads * kPlanPer;
+constexpr int kPlanBatch = kPlanThreads * 32;            // pages looked at together
 constexpr int kCopyThreads = 256;
 constexpr int kCopyBytes = kCopyThreads * 16 * 4;        // a copy piece
 constexpr int kPoolsPerLaunch = 64;
@@ -99,24 +98,37 @@ __device__ __forceinline__ T block_rank(T x, T* scratch, T* total) {
   return before + inc - x;
 }
 
+// Which of the 32 pages from base + 32 * thread on are in use (a bit each; 0
+// past the last page).  The warp reads its 1024 counts in order, 32 at a time.
+__device__ __forceinline__ uint32_t used_mask(const Table& t, int base) {
+  const int lane = threadIdx.x & 31, first = base + (threadIdx.x >> 5) * 1024;
+  uint32_t mask = 0;
+  if (first >= t.num_pages) return 0;   // (uniform over the warp)
+#pragma unroll 16
+  for (int k = 0; k < 32; ++k) {
+    const int i = first + 32 * k + lane;
+    const uint32_t word = __ballot_sync(0xffffffffu, i < t.num_pages && t.refs[i] != 0);
+    if (lane == k) mask = word;
+  }
+  return mask;
+}
+
+// The bits of a thread's 32 pages that lie below page `end`.
+__device__ __forceinline__ uint32_t below(int base, int end) {
+  const int n = end - base - 32 * static_cast<int>(threadIdx.x);
+  return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
+}
+
 // The lowest `need` free pages into `list`, ascending; how many there are (at
-// most `need`).  The whole block; a thread takes kPlanPer consecutive pages.
+// most `need`).  The whole block.
 __device__ int lowest_free(const Table& t, int need, int32_t* list, int* scratch) {
   int found = 0;
   for (int base = 0; base < t.num_pages && found < need; base += kPlanBatch) {
-    const int i0 = base + static_cast<int>(threadIdx.x) * kPlanPer;
-    int mask = 0;
-#pragma unroll
-    for (int k = 0; k < kPlanPer; ++k)
-      if (i0 + k < t.num_pages && t.refs[i0 + k] == 0) mask |= 1 << k;
+    uint32_t free = ~used_mask(t, base) & below(base, t.num_pages);
     int total;
-    int at = found + block_rank(__popc(mask), scratch, &total);
-#pragma unroll
-    for (int k = 0; k < kPlanPer; ++k)
-      if ((mask >> k) & 1) {
-        if (at < need) list[at] = i0 + k;
-        ++at;
-      }
+    int at = found + block_rank(__popc(free), scratch, &total);
+    for (; free != 0 && at < need; free &= free - 1)
+      list[at++] = base + 32 * static_cast<int>(threadIdx.x) + __ffs(free) - 1;
     found += total;
   }
   __syncthreads();   // list is visible to the block
@@ -345,39 +357,39 @@ __global__ void __launch_bounds__(kPlanThreads)
   grid_dep_wait();
   grid_dep_launch();
   __shared__ int scratch[33];
+  __shared__ uint32_t ranks[33];
   const int P = t.num_pages;
   int used = 0;
+  uint32_t mask = 0;   // (of the only batch, where there is one)
   for (int base = 0; base < P; base += kPlanBatch) {
-    const int i0 = base + static_cast<int>(threadIdx.x) * kPlanPer;
-    int mine = 0;
-#pragma unroll
-    for (int k = 0; k < kPlanPer; ++k) mine += i0 + k < P && t.refs[i0 + k] != 0;
+    mask = used_mask(t, base);
     int total;
-    block_rank(mine, scratch, &total);
+    block_rank(__popc(mask), scratch, &total);
     used += total;
   }
+  const int lane = threadIdx.x & 31;
   int n_holes = 0, n_movers = 0;
   for (int base = 0; base < P; base += kPlanBatch) {
-    const int i0 = base + static_cast<int>(threadIdx.x) * kPlanPer;
-    int hole = 0, mover = 0;
-#pragma unroll
-    for (int k = 0; k < kPlanPer; ++k) {
-      const int i = i0 + k;
-      if (i >= P) break;
-      const bool live = t.refs[i] != 0;
-      if (!live && i < used) hole |= 1 << k;
-      if (live && i >= used) mover |= 1 << k;
-      moved[i] = live ? i : -1;
-    }
-    int total;
-    int at = n_holes + block_rank(__popc(hole), scratch, &total);
-    n_holes += total;
-    for (int k = 0; k < kPlanPer; ++k)
-      if ((hole >> k) & 1) holes[at++] = i0 + k;
-    at = n_movers + block_rank(__popc(mover), scratch, &total);
-    n_movers += total;
-    for (int k = 0; k < kPlanPer; ++k)
-      if ((mover >> k) & 1) movers[at++] = i0 + k;
+    if (P > kPlanBatch) mask = used_mask(t, base);
+    const int i0 = base + 32 * static_cast<int>(threadIdx.x);
+    uint32_t hole = ~mask & below(base, used), mover = mask & ~below(base, used);
+    // both ranks in one scan: the counts of a batch fit 16 bits each
+    uint32_t total;
+    const uint32_t rank = block_rank(
+        static_cast<uint32_t>(__popc(hole) | __popc(mover) << 16), ranks, &total);
+    int at = n_holes + static_cast<int>(rank & 0xffffu);
+    for (; hole != 0; hole &= hole - 1) holes[at++] = i0 + __ffs(hole) - 1;
+    at = n_movers + static_cast<int>(rank >> 16);
+    for (; mover != 0; mover &= mover - 1) movers[at++] = i0 + __ffs(mover) - 1;
+    n_holes += static_cast<int>(total & 0xffffu);
+    n_movers += static_cast<int>(total >> 16);
+    const int first = base + (threadIdx.x >> 5) * 1024;
+    if (first < P)
+      for (int k = 0; k < 32; ++k) {
+        const uint32_t word = __shfl_sync(0xffffffffu, mask, k);
+        const int i = first + 32 * k + lane;
+        if (i < P) moved[i] = (word >> lane) & 1u ? i : -1;
+      }
   }
   __syncthreads();
   for (int i = threadIdx.x; i < n_movers; i += kPlanThreads) {

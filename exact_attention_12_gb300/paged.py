@@ -13,10 +13,18 @@ import math
 import torch
 
 from . import _abi
-from ._abi import AttnPages, AttnPageTable, AttnParams, AttnPool, check_status, lib
+from ._abi import AttnPages, AttnPageTable, AttnParams, check_status, lib
 from .api import workspace
 
 _ROPE = 64   # columns of a latent vector beside its d_v value columns
+
+
+def _public_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# the current stream's handle without the stream object around it (2 us)
+_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_stream)
 
 
 def _call(device, ws, size_of, call, what):
@@ -27,7 +35,7 @@ def _call(device, ws, size_of, call, what):
     if torch.cuda.current_device() != device.index:
         with torch.cuda.device(device):
             return _call(device, ws, size_of, call, what)
-    stream = torch.cuda.current_stream(device).cuda_stream
+    stream = _stream(device.index)
     if ws is not None:
         if ws.device != device or not ws.is_contiguous():
             raise ValueError(f"{what}: ws must be contiguous, on the tensors' device")
@@ -38,45 +46,45 @@ def _call(device, ws, size_of, call, what):
     if st == _abi.ATTN_ERR_WORKSPACE:
         w = workspace(device, size_of())
         st = call(w.data_ptr(), w.numel(), stream)
-    check_status(st, what)
+    if st:
+        check_status(st, what)
 
 
 def _int32(t, device, dim, what):
     if t.dtype != torch.int32 or t.device != device or t.dim() != dim \
-            or (t.numel() > 1 and t.stride(-1) != 1):
+            or not (t.is_contiguous() or t.stride(-1) == 1):
         raise ValueError(f"{what} must be a {dim}-dimensional int32 tensor on the tensors' device, "
                          "contiguous along its last axis")
 
 
-def _decode_args(q, pages, table, cache_lens, scale, causal, shared_len, d, H_kv, strides):
-    """attn_params and attn_pages of a paged decode step; strides: of a page
-    buffer, between pages, heads and keys."""
-    B, H, n_q, _ = q.shape
-    _int32(table, q.device, 2, "page_table")
-    _int32(cache_lens, q.device, 1, "cache_lens")
-    if table.shape[0] != B or cache_lens.shape[0] != B:
-        raise ValueError("page_table and cache_lens must have a row per sequence of q")
-    page_size, max_pages = pages.shape[-2], table.shape[1]
-    qs = q.stride()
-    p = AttnParams(B, H, max_pages * page_size, d, _abi.ATTN_BF16, scale, 1 if causal else 0, 0.0,
-                   0, 0, cache_lens.data_ptr(), None, 0, qs[0], qs[1], qs[2], H_kv, 0, *strides,
-                   0.0, 0.0, 0.0, 0)
-    g = AttnPages(table.data_ptr(), table.stride(0) if B > 1 else max_pages, max_pages, page_size,
-                  pages.shape[0], int(shared_len))
-    return p, g
+def _table(table, cache_lens, B, device):
+    """Pointers, row stride and width of a page table with B rows."""
+    _int32(table, device, 2, "page_table")
+    _int32(cache_lens, device, 1, "cache_lens")
+    rows, width = table.shape
+    if rows != B or cache_lens.shape[0] != B:
+        raise ValueError("page_table and cache_lens must have a row per sequence")
+    return table.data_ptr(), (table.stride(0) if rows > 1 else width), width, cache_lens.data_ptr()
 
 
 def _strides(t):
-    """Strides of a bf16 tensor whose axes of one element, over which nothing
-    strides, are given the value that the library's checks pass."""
-    s = list(t.stride())
-    if s[-1] != 1 and t.shape[-1] > 1:
-        raise ValueError("the last axis must be contiguous")
-    inner = t.shape[-1]
-    for i in range(t.dim() - 2, -1, -1):
-        if t.shape[i] <= 1:
+    """Strides of a tensor; an axis of one element, over which nothing strides,
+    has the value it has in a contiguous tensor."""
+    shape = t.shape
+    if not t.is_contiguous():
+        s = list(t.stride())
+        if s[-1] != 1 and shape[-1] > 1:
+            raise ValueError("the last axis must be contiguous")
+    else:
+        s = [1] * len(shape)
+        for i in range(len(shape) - 2, -1, -1):
+            s[i] = s[i + 1] * shape[i + 1]
+        return s
+    inner = shape[-1]
+    for i in range(len(shape) - 2, -1, -1):
+        if shape[i] <= 1:
             s[i] = inner
-        inner = max(inner, s[i] * max(t.shape[i], 1))
+        inner = max(inner, s[i] * shape[i])
     return s
 
 
@@ -101,31 +109,35 @@ def attention_decode_paged(q, k_pages, v_pages, page_table, cache_lens, *, scale
     [B, H, n_q].  A page index outside the cache is reported by check().
     """
     _check_bf16(q, k_pages, v_pages)
-    if q.dim() != 4 or k_pages.dim() != 4 or k_pages.shape != v_pages.shape \
-            or k_pages.shape[3] != q.shape[3]:
+    shape, pages = q.shape, k_pages.shape
+    if len(shape) != 4 or len(pages) != 4 or pages != v_pages.shape or pages[3] != shape[3]:
         raise ValueError("q must be [B, H, n_q, d], k_pages and v_pages "
                          "[num_pages, H_kv, page_size, d]")
-    B, H, n_q, d = q.shape
-    H_kv = k_pages.shape[1]
+    B, H, n_q, d = shape
+    num_pages, H_kv, page_size, _ = pages
     if H_kv < 1 or H % H_kv:
         raise ValueError("H_kv must divide q's H")
     ks = _strides(k_pages)
     if ks != _strides(v_pages):
         raise ValueError("k_pages and v_pages must share strides")
+    qs = _strides(q)
+    device = q.device
     if out is None:
-        out = torch.empty_strided(q.shape, q.stride(), dtype=q.dtype, device=q.device)
-    elif out.shape != q.shape or out.stride() != q.stride() or out.dtype != q.dtype \
-            or out.device != q.device:
+        out = torch.empty_like(q) if q.is_contiguous() else torch.empty_strided(
+            shape, q.stride(), dtype=q.dtype, device=device)
+    elif out.shape != shape or _strides(out) != qs or out.dtype != q.dtype \
+            or out.device != device:
         raise ValueError("out must be like q")
-    lse = _lse(lse, q)
-    p, g = _decode_args(q, k_pages, page_table, cache_lens,
-                        1.0 / math.sqrt(d) if scale is None else float(scale), causal, shared_len,
-                        d, H_kv, ks[:3])
-    p.stride_b, p.stride_h, p.stride_n = _strides(q)[:3]
+    lse = _lse(lse, shape, device)
+    table, row, width, lens = _table(page_table, cache_lens, B, device)
+    p = AttnParams(B, H, width * page_size, d, _abi.ATTN_BF16,
+                   d ** -0.5 if scale is None else scale, 1 if causal else 0, 0.0, 0, 0, lens,
+                   None, 0, qs[0], qs[1], qs[2], H_kv, 0, ks[0], ks[1], ks[2])
+    g = AttnPages(table, row, width, page_size, num_pages, shared_len)
     fn = lib().attn_decode_paged
     pp, gp = ctypes.byref(p), ctypes.byref(g)
     ptrs = (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), lse.data_ptr())
-    _call(q.device, ws, lambda: _size(lib().attn_decode_paged_workspace_size(pp, n_q, gp)),
+    _call(device, ws, lambda: _size(lib().attn_decode_paged_workspace_size(pp, n_q, gp)),
           lambda w, n, s: fn(pp, n_q, gp, *ptrs, w, n, s), "attn_decode_paged")
     return out, lse
 
@@ -143,34 +155,37 @@ def attention_decode_latent(q, c_pages, page_table, cache_lens, *, scale, d_v=51
     contiguous, and lse fp32 [B, H, n_q].
     """
     _check_bf16(q, c_pages)
-    if q.dim() != 4 or c_pages.dim() != 3 or q.shape[3] != d_v + _ROPE \
-            or c_pages.shape[2] != d_v + _ROPE:
+    shape, pages, cols = q.shape, c_pages.shape, d_v + _ROPE
+    if len(shape) != 4 or len(pages) != 3 or shape[3] != cols or pages[2] != cols:
         raise ValueError(f"q must be [B, H, n_q, d_v + {_ROPE}], c_pages "
                          f"[num_pages, page_size, d_v + {_ROPE}]")
-    B, H, n_q, _ = q.shape
+    B, H, n_q, _ = shape
+    num_pages, page_size, _ = pages
+    device = q.device
     if out is None:
-        out = torch.empty((B, H, n_q, d_v), dtype=q.dtype, device=q.device)
+        out = torch.empty((B, H, n_q, d_v), dtype=q.dtype, device=device)
     elif out.shape != (B, H, n_q, d_v) or not out.is_contiguous() or out.dtype != q.dtype \
-            or out.device != q.device:
+            or out.device != device:
         raise ValueError("out must be a contiguous bf16 [B, H, n_q, d_v] on q's device")
-    lse = _lse(lse, q)
-    cs = _strides(c_pages)
-    p, g = _decode_args(q, c_pages, page_table, cache_lens, float(scale), causal, 0, d_v, 1,
-                        (cs[0], cs[0], cs[1]))
-    p.stride_b, p.stride_h, p.stride_n = _strides(q)[:3]
+    lse = _lse(lse, shape, device)
+    cs, qs = _strides(c_pages), _strides(q)
+    table, row, width, lens = _table(page_table, cache_lens, B, device)
+    p = AttnParams(B, H, width * page_size, d_v, _abi.ATTN_BF16, scale, 1 if causal else 0, 0.0, 0,
+                   0, lens, None, 0, qs[0], qs[1], qs[2], 1, 0, cs[0], cs[0], cs[1])
+    g = AttnPages(table, row, width, page_size, num_pages, 0)
     fn = lib().attn_decode_latent
     pp, gp = ctypes.byref(p), ctypes.byref(g)
     ptrs = (q.data_ptr(), c_pages.data_ptr(), out.data_ptr(), lse.data_ptr())
-    _call(q.device, ws, lambda: _size(lib().attn_decode_latent_workspace_size(pp, n_q, gp)),
+    _call(device, ws, lambda: _size(lib().attn_decode_latent_workspace_size(pp, n_q, gp)),
           lambda w, n, s: fn(pp, n_q, gp, *ptrs, w, n, s), "attn_decode_latent")
     return out, lse
 
 
-def _lse(lse, q):
+def _lse(lse, shape, device):
     if lse is None:
-        return torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
-    if lse.shape != q.shape[:3] or not lse.is_contiguous() or lse.dtype != torch.float32 \
-            or lse.device != q.device:
+        return torch.empty(shape[:3], dtype=torch.float32, device=device)
+    if lse.shape != shape[:3] or not lse.is_contiguous() or lse.dtype != torch.float32 \
+            or lse.device != device:
         raise ValueError("lse must be a contiguous fp32 [B, H, n_q] on q's device")
     return lse
 
@@ -184,35 +199,34 @@ def _size(n):
 # ------------------------------------------------------------------- upkeep --
 
 def _table_args(page_table, cache_lens, refs, page_size):
-    dev = refs.device
-    _int32(page_table, dev, 2, "page_table")
-    _int32(cache_lens, dev, 1, "cache_lens")
-    _int32(refs, dev, 1, "refs")
-    rows, max_pages = page_table.shape
-    if cache_lens.shape[0] != rows:
-        raise ValueError("cache_lens must have an entry per row of page_table")
-    return AttnPageTable(page_table.data_ptr(), page_table.stride(0) if rows > 1 else max_pages,
-                         cache_lens.data_ptr(), refs.data_ptr(), rows, max_pages, int(page_size),
-                         refs.shape[0])
+    _int32(refs, refs.device, 1, "refs")
+    rows = page_table.shape[0]
+    table, row, width, lens = _table(page_table, cache_lens, rows, refs.device)
+    return AttnPageTable(table, row, lens, refs.data_ptr(), rows, width, page_size, refs.shape[0])
 
 
 def _pool_args(pools, num_pages, device):
     """attn_pool of each page buffer [num_pages, ...]: a page's elements must
     fill one contiguous block, in whatever order its axes have."""
-    got = (AttnPool * max(1, len(pools)))()
-    for a, t in zip(got, pools):
-        if t.device != device or t.dim() < 2 or t.shape[0] != num_pages:
+    got = []
+    for t in pools:
+        shape = t.shape
+        if t.device != device or len(shape) < 2 or shape[0] != num_pages:
             raise ValueError("pools must be tensors [num_pages, ...] on the table's device")
-        n = 1
-        if not t[0:1].is_contiguous():   # (a permuted page: its axes in the order of the strides)
-            for stride, size in sorted(zip(t.stride()[1:], t.shape[1:])):
+        item = t.element_size()
+        page = math.prod(shape[1:])
+        if t.is_contiguous():
+            step = page
+        else:
+            n = 1   # the page's axes in the order of their strides
+            for stride, size in sorted(zip(t.stride()[1:], shape[1:])):
                 if size != 1 and stride != n:
                     raise ValueError("a page must be one contiguous block of memory")
                 n *= size
-        page_bytes = math.prod(t.shape[1:]) * t.element_size()
-        a.base, a.page_bytes = t.data_ptr(), page_bytes
-        a.page_stride = t.stride(0) * t.element_size() if num_pages > 1 else page_bytes
-    return got
+            step = t.stride(0) if num_pages > 1 else page
+        got += (t.data_ptr(), step * item, page * item)
+    # attn_pool is three 64-bit words
+    return (ctypes.c_int64 * max(1, len(got)))(*got)
 
 
 def _list(t, device, what):
@@ -262,7 +276,7 @@ def pages_fork(pools, page_table, cache_lens, refs, parents, children, *, page_s
     b, m = _list(children, refs.device, "children")
     if n != m:
         raise ValueError("parents and children must have the same length")
-    new = torch.empty(n, dtype=torch.int32, device=refs.device)
+    new = torch.empty_like(parents)
     tp, fn, np_ = ctypes.byref(t), lib().attn_pages_fork, new.data_ptr()
     _call(refs.device, ws, lambda: _size(lib().attn_pages_workspace_size(tp, n)),
           lambda w, nb, st: fn(tp, arr, len(pools), a, b, n, np_, w, nb, st), "attn_pages_fork")

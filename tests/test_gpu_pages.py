@@ -116,6 +116,22 @@ def test_large_cache_many_forks(ea):
     c.same()
 
 
+@pytest.mark.parametrize("P", [32768, 32769, 70001])
+def test_more_pages_than_a_plan_looks_at_together(ea, P):
+    rng = np.random.default_rng(P)
+    lens = [P // 7] * 3 + [0, P // 9, 77]
+    c = Cache(rng, 8, P // 5, P, 1, lens, pools=((1, 8),))
+    ea.pages_free(*c.state, _i([1]), page_size=1)
+    c.twin.free([1])
+    for rows, to in (([3, 6], [P // 11, 5]), ([7], [P // 6])):
+        ea.pages_extend(*c.state, _i(rows), _i(to), page_size=1)
+        c.twin.extend(rows, to)
+    moved = ea.pages_compact(c.pools, *c.state, page_size=1)
+    assert moved.cpu().tolist() == c.twin.compact(c.plain)
+    ea.check()
+    c.same()
+
+
 def test_a_full_cache_is_reported_and_left_whole(ea):
     from exact_attention_12_gb300 import _abi
     c = Cache(np.random.default_rng(3), 8, 4, 6, 16, [20, 17])   # 4 of 6 pages taken
