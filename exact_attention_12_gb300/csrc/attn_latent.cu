@@ -58,11 +58,19 @@ struct LatentCfg {
   // what is copied, waited for and released together: the 64 key-only columns
   // (group 0), then 128 columns = a block of O^T (groups 1 ..)
   static constexpr int kGroups = kBlocks + 1;
-  static constexpr int kPBytes = kLatentKeys * 128;
-  static constexpr int kSmem = (1 + kStages) * kTileBytes + kPBytes;
+  // P^T of a tile takes the place of its key-only columns (64 keys x 64 rows of
+  // bf16 either way): its scores are complete when P is written
+  static constexpr int kPOffset = (kBoxes - 1) * kBoxBytes;
+  static constexpr int kSmem = (1 + kStages) * kTileBytes;
   static constexpr int kCtl = 3072;                       // LatentCtl, in whole kilobytes
   static_assert(kSmem + kCtl <= 227 * 1024, "shared memory of a CTA");
-  static constexpr int kThreads = 320;
+  // warpgroups 0, 1: the eight warps of the softmax; warpgroup 2: copies, MMA
+  // issue, two idle warps.  Registers re-split after the start: 256 * 216 +
+  // 128 * 72 <= 384 * 168
+  static constexpr int kThreads = 384;
+  static constexpr uint32_t kRegsLaunch = 168, kRegsSoftmax = 216, kRegsOther = 72;
+  static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * kRegsLaunch,
+                "register re-split exceeds the launch allocation");
   // S^T of tile t at 64 (t mod 2), block i of O^T at 128 + 64 i
   static constexpr uint32_t kOCol = 128;
 };
@@ -70,11 +78,14 @@ struct LatentCfg {
 // (aligned, so that what follows it, the dynamic shared memory, is too)
 template <int ST>
 struct __align__(1024) LatentCtl {
-  uint64_t full[ST][5], empty[ST][5], sfull[2], pfull, pvdone, qfull, final_bar;
+  // pfull, pvdone of tile T: [T mod 2], because the softmax may be done with
+  // tile T + 1 before anyone has looked at tile T's (one barrier's phase would
+  // then be two on, which a parity cannot tell from none)
+  uint64_t full[ST][5], empty[ST][5], sfull[2], pfull[2], pvdone[2], qfull, final_bar;
   // [tile mod 2][16-key quarter][column]: the tile's maxima; behind the last
   // tile of a piece, in the buffer of the next, the columns' sums
   float wmax[2][4][64];
-  int64_t sums[10];
+  int sums[12];
   PagedShare share;
   uint32_t tmem_base;
   int abort_flag;
@@ -126,7 +137,6 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
   }
   uint8_t* sQ = smem;
   uint8_t* sC = smem + C::kTileBytes;
-  uint8_t* sP = sC + ST * C::kTileBytes;
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
@@ -143,8 +153,10 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
       }
     mbar_init(&ctl.sfull[0], 1);
     mbar_init(&ctl.sfull[1], 1);
-    mbar_init(&ctl.pfull, 8);
-    mbar_init(&ctl.pvdone, 1);
+    mbar_init(&ctl.pfull[0], 8);
+    mbar_init(&ctl.pfull[1], 8);
+    mbar_init(&ctl.pvdone[0], 1);
+    mbar_init(&ctl.pvdone[1], 1);
     mbar_init(&ctl.qfull, 8);
     mbar_init(&ctl.final_bar, 1);
     fence_mbar_init();
@@ -154,11 +166,10 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
     tmem_alloc(&ctl.tmem_base, 512);
     tmem_relinquish();
   }
-  // q's rows and P's columns past the live rows stay zero; their maxima -inf
+  // q's rows past the live ones stay zero; the maxima of a half without live
+  // rows -inf (what its columns of P and O^T hold reaches no other column)
   for (int i = threadIdx.x; i < C::kTileBytes / 16; i += C::kThreads)
     reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0u, 0u, 0u, 0u);
-  for (int i = threadIdx.x; i < C::kPBytes / 16; i += C::kThreads)
-    reinterpret_cast<uint4*>(sP)[i] = make_uint4(0u, 0u, 0u, 0u);
   for (int i = threadIdx.x; i < 512; i += C::kThreads) (&ctl.wmax[0][0][0])[i] = -INFINITY;
   fence_proxy_async_smem();
   tc_fence_before();
@@ -168,10 +179,12 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
   grid_dep_launch();
   const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.tmem_base, 0);
   const PagedShare share =
-      paged_share<C::kThreads, KT, kLatentOverhead>(a, cta, ctas, ctl.sums, &ctl.share);
+      paged_share<C::kThreads, KT, kLatentOverhead, kLatentMinUnits>(a, cta, ctas, ctl.sums, &ctl.share);
   const WaitCtx wc{&ctl.abort_flag, a.status, a.timeout_ns};
   PagedPiece p = paged_piece<KT, kLatentOverhead>(a, share, share.b, 0, share.s);
 
+  if (warp >= 8) {
+    regs_decrease<C::kRegsOther>();
   if (warp == 8) {
     // ------------------------------------------------------------ copies
     const int rows = min(KT, 1 << a.page_shift), parts = KT / rows;
@@ -210,9 +223,10 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
         const int at = key < p.len ? key : t * KT;
         int page = 0;
         if (lane < parts) page = checked_page(row[at >> a.page_shift], a.num_pages, a.status);
-        // the key-only columns first: they are released first
+        // the key-only columns last: P lies there until the last product
 #pragma unroll
-        for (int x = 0; x < C::kGroups; ++x) {
+        for (int y = 1; y <= C::kGroups; ++y) {
+          const int x = y % C::kGroups;
           if (T >= ST && !(ok = __all_sync(0xffffffffu, mbar_wait(&ctl.empty[s][x], ((T / ST) - 1) & 1,
                                                                   wc, kSiteLatentFree))))
             break;
@@ -245,7 +259,6 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
     constexpr uint32_t kIdO = idesc_bf16(128, kLatentRows, true, true);
     const bool one = elect_one_lane();
     const uint64_t dq = smem_desc(smem_u32(sQ), 16, 1024);
-    const uint64_t dp = smem_desc(smem_u32(sP), 16, 1024);
     bool ok = true;
     uint32_t T = 0;   // tiles before this piece
     int k = 0;        // pieces with tiles
@@ -268,7 +281,8 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
         const int from = left - i * KT;
         const uint64_t dc = smem_desc(smem_u32(tile), 16, 1024);
 #pragma unroll
-        for (int x = 0; x < C::kGroups; ++x) {
+        for (int y = 1; y <= C::kGroups; ++y) {
+          const int x = y % C::kGroups;
           if (!all) {
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&ctl.full[s][x], (u / ST) & 1, wc,
                                                          kSiteLatentTile))))
@@ -290,14 +304,11 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
             for (int kk = 4 * box; kk < 4 * (box + boxes); ++kk) {
               const uint64_t off =
                   static_cast<uint64_t>(((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4);
-              mma_ss(tmem + 64 * (u & 1), dc + off, dq + off, kIdS, x > 0 || (kk & 3) > 0 ? 1u : 0u);
+              mma_ss(tmem + 64 * (u & 1), dc + off, dq + off, kIdS, x != 1 || kk > 0 ? 1u : 0u);
             }
           }
         }
-        if (one) {
-          mma_commit(&ctl.empty[s][0]);
-          mma_commit(&ctl.sfull[u & 1]);
-        }
+        if (one) mma_commit(&ctl.sfull[u & 1]);
         __syncwarp();
       };
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(&ctl.qfull, k & 1, wc, kSiteLatentQ)))) break;
@@ -312,9 +323,11 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
           scores(i + 1, true);
           next = false;
         }
-        if (!ok || !(ok = __all_sync(0xffffffffu, mbar_wait(&ctl.pfull, u & 1, wc, kSiteLatentP))))
+        if (!ok || !(ok = __all_sync(0xffffffffu, mbar_wait(&ctl.pfull[u & 1], (u >> 1) & 1, wc,
+                                                            kSiteLatentP))))
           break;
         tc_fence_after();
+        const uint64_t dp = smem_desc(smem_u32(sC + s * C::kTileBytes + C::kPOffset), 16, 1024);
 #pragma unroll
         for (int blk = 0; blk < C::kBlocks; ++blk) {   // O^T += c^T P^T, 128 value columns at a time
           const uint64_t dv = smem_desc(smem_u32(sC + s * C::kTileBytes + 2 * blk * C::kBoxBytes),
@@ -328,7 +341,10 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
             mma_commit(&ctl.empty[s][1 + blk]);
           }
         }
-        if (one) mma_commit(&ctl.pvdone);
+        if (one) {
+          mma_commit(&ctl.pvdone[u & 1]);
+          mma_commit(&ctl.empty[s][0]);
+        }
         __syncwarp();
         if (next) scores(i + 1, false);
       }
@@ -340,7 +356,9 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
       mbar_wait_drain(&ctl.final_bar, 0, a.timeout_ns);
     }
     __syncwarp();
+  }
   } else {
+    regs_increase<C::kRegsSoftmax>();
     // ------------------------------------------- q, softmax, rescale, output
     // softmax: 16 keys and 32 of the columns a warp, in the MMA's fragment
     // layout: keys g, g + 8 and columns 8 b + 2 q, + 1 (b = 0 .. 3) a thread
@@ -427,9 +445,6 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
           if (grown[e]) mref[e] = x;
         }
         const bool rescale = __any_sync(0xffffffffu, grown[0] || grown[1]);   // alike in every warp
-        if (i > 0 && ok)   // O^T holds the sum through the tile before; P is free
-          ok = __all_sync(0xffffffffu, mbar_wait(&ctl.pvdone, (T - 1) & 1, wc, kSiteLatentDone));
-        tc_fence_after();
         if (rescale) {
           if (soft) {
             const float al = half ? alpha[1] : alpha[0], mr = half ? mref[1] : mref[0];
@@ -442,6 +457,10 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
             }
           }
           if (i > 0) {
+            if (ok)   // O^T holds the sum through the tile before
+              ok = __all_sync(0xffffffffu, mbar_wait(&ctl.pvdone[(T - 1) & 1], ((T - 1) >> 1) & 1, wc,
+                                                     kSiteLatentDone));
+            tc_fence_after();
 #pragma unroll
             for (int bb = 0; bb < C::kBlocks / 2; ++bb) {
               const uint32_t col = tmem + lanes + C::kOCol + 64 * (half * (C::kBlocks / 2) + bb);
@@ -470,7 +489,7 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
                   ex2_approx(fmaf(__uint_as_float(sr[4 * b + 2 * e + 1]), c2, -mc[2 * b + 1]));
               l[2 * b] += p0;
               l[2 * b + 1] += p1;
-              *reinterpret_cast<uint32_t*>(sP + row * 128 + (((4 * half + b) ^ (row & 7)) << 4) +
+              *reinterpret_cast<uint32_t*>(sC + (T % ST) * C::kTileBytes + C::kPOffset + row * 128 + (((4 * half + b) ^ (row & 7)) << 4) +
                                            4 * q4) = pack_bf16x2(p0, p1);
             }
           }
@@ -478,7 +497,7 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.pfull);
+        if (lane == 0) mbar_arrive(&ctl.pfull[buf]);
       }
 
       // ---- O = O^T / l and L of the piece; every score MMA of the piece is
@@ -498,7 +517,8 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
         }
       }
       if (n > 0 && ok) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&ctl.pvdone, (T - 1) & 1, wc, kSiteLatentDone));
+        ok = __all_sync(0xffffffffu, mbar_wait(&ctl.pvdone[(T - 1) & 1], ((T - 1) >> 1) & 1, wc,
+                                                     kSiteLatentDone));
         tc_fence_after();
       }
       named_barrier_sync(1, 256);
@@ -588,6 +608,10 @@ cudaError_t launch_dv(const CUtensorMap& tc, const PagedArgs& a, int ctas, cudaS
   if (todo) {
     e = cudaFuncSetAttribute(latent_kernel<DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
+    // the register re-split inside the kernel assumes the launch allocation
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, latent_kernel<DV>)) != cudaSuccess) return e;
+    if (static_cast<uint32_t>(fa.numRegs) < C::kRegsLaunch) return cudaErrorInvalidConfiguration;
     mark_done(set_up, dev);
   }
   const int groups = a.rows / kLatentRows;

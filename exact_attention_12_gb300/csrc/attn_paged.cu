@@ -58,7 +58,7 @@ struct PagedShared {
   uint64_t full[kSlots * PagedCfg<D, MT>::kStages];
   uint64_t empty[kSlots * PagedCfg<D, MT>::kStages];
   float m[kSlots][MT * 16], l[kSlots][MT * 16];
-  int64_t sums[PagedCfg<D, MT>::kWarps];
+  int sums[PagedCfg<D, MT>::kWarps];
   PagedShare share;
   int abort_flag;
 };
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
   __syncthreads();
   grid_dep_wait();
   grid_dep_launch();
-  const PagedShare share = paged_share<C::kThreads, KT, kPagedOverhead>(
+  const PagedShare share = paged_share<C::kThreads, KT, kPagedOverhead, kPagedMinUnits>(
       a, blockIdx.x, gridDim.x, sh.sums, &sh.share);
   MergeNote note{-1, 0, 0, 0};
   const WaitCtx wc{&sh.abort_flag, a.status, a.timeout_ns};

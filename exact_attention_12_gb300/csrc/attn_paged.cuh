@@ -20,7 +20,7 @@ constexpr int kStatusPage = 6;
 // segments, one per (sequence, head group), sequence by sequence; a segment
 // of n key tiles costs n + overhead units (its set-up and write-out, in
 // tiles).  The units are dealt to the CTAs in equal runs (of all CTAs
-// launched, or of fewer when the lengths leave less than kPagedMinUnits each;
+// launched, or of fewer when the lengths leave less than MIN_UNITS each;
 // the others return): every CTA gets the same share whatever the lengths are,
 // and none waits for keys a short sequence does not have.  A segment that
 // falls to one CTA is finished by it; one that is cut leaves a partial (O, L)
@@ -88,10 +88,11 @@ struct PrefixArgs {
 };
 
 constexpr int kPagedKeys = 32;        // keys per tile of the paged decode kernel
-constexpr int kPagedOverhead = 4;     // a segment's fixed cost in such tiles
+constexpr int kPagedOverhead = 8;     // a segment's fixed cost in such tiles
 constexpr int kPagedMinUnits = 6;     // units a CTA takes at least
 constexpr int kLatentKeys = 64;       // keys per tile of the latent kernel
-constexpr int kLatentOverhead = 3;
+constexpr int kLatentOverhead = 2;
+constexpr int kLatentMinUnits = 2;
 constexpr int kLatentRows = 64;       // query rows of one CTA
 constexpr int kLatentRope = 64;       // columns of a latent vector that are not values
 
@@ -129,49 +130,42 @@ __device__ __forceinline__ int paged_ctas(int64_t total, int launched) {
   return most >= launched ? launched : max(1, static_cast<int>(most));
 }
 
-// a / b for a >= 0, b > 0; a long division is 100 instructions, and hardly
-// ever needed.
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-  if (((a | b) >> 31) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
-}
-
-// A CTA's run [lo, hi) of the units, and where it starts.
+// A CTA's run [lo, hi) of the units, and where it starts.  (All units together
+// are less than 2^31: the host sees to that.)
 struct PagedShare {
-  int64_t lo, hi;
-  int64_t q;      // units of a CTA: q + 1 of the first `extra` CTAs, q of the others
+  int lo, hi;
+  int q;          // units of a CTA: q + 1 of the first `extra` CTAs, q of the others
   int extra, cta;
   int b;          // the sequence that holds unit lo
-  int64_t s;      // its first unit
+  int s;          // its first unit
   // The CTA whose run holds `unit`.
-  __device__ __forceinline__ int owner(int64_t unit) const {
-    const int64_t big = extra * (q + 1);
-    return static_cast<int>(unit < big ? quotient(unit, q + 1) : extra + quotient(unit - big, q));
+  __device__ __forceinline__ int owner(int unit) const {
+    const int big = extra * (q + 1);
+    return unit < big ? unit / (q + 1) : extra + (unit - big) / q;
   }
 };
 
 // All threads of the CTA; `sums` has THREADS / 32 entries of shared memory.
 // Thread t adds up a run of consecutive sequences, the runs' sums are
 // scanned, and the thread whose run holds unit lo walks it.
-template <int THREADS, int KEYS, int OVERHEAD>
+template <int THREADS, int KEYS, int OVERHEAD, int MIN_UNITS>
 __device__ __forceinline__ PagedShare paged_share(const PagedArgs& a, int cta, int launched,
-                                                  int64_t* sums, PagedShare* out) {
+                                                  int* sums, PagedShare* out) {
   const int per = (a.B + THREADS - 1) / THREADS;
   const int b0 = min(static_cast<int>(threadIdx.x) * per, a.B), b1 = min(b0 + per, a.B);
-  int64_t mine = 0;
-  for (int b = b0; b < b1; ++b)
-    mine += static_cast<int64_t>(a.heads) * (paged_tiles<KEYS>(a, b) + OVERHEAD);
+  int mine = 0;
+  for (int b = b0; b < b1; ++b) mine += a.heads * (paged_tiles<KEYS>(a, b) + OVERHEAD);
   // inclusive scan over the warp, then over the warps
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t inc = mine;
+  int inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
+    const int x = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += x;
   }
   if (lane == 31) sums[warp] = inc;
   __syncthreads();
-  int64_t before = 0, total = 0;
+  int before = 0, total = 0;
 #pragma unroll
   for (int w = 0; w < THREADS / 32; ++w) {
     if (w < warp) before += sums[w];
@@ -179,11 +173,10 @@ __device__ __forceinline__ PagedShare paged_share(const PagedArgs& a, int cta, i
   }
   inc += before;
   PagedShare sh;
-  const int64_t most = quotient(total, kPagedMinUnits);
-  const int ctas = most >= launched ? launched : max(1, static_cast<int>(most));
+  const int ctas = max(1, min(launched, total / MIN_UNITS));
   sh.cta = cta;
-  sh.q = quotient(total, ctas);
-  sh.extra = static_cast<int>(total - sh.q * ctas);
+  sh.q = total / ctas;
+  sh.extra = total - sh.q * ctas;
   if (cta >= ctas) {   // (uniform over the CTA)
     sh.lo = sh.hi = sh.s = total;
     sh.b = a.B;
@@ -192,10 +185,9 @@ __device__ __forceinline__ PagedShare paged_share(const PagedArgs& a, int cta, i
   sh.lo = sh.q * cta + min(cta, sh.extra);
   sh.hi = sh.lo + sh.q + (cta < sh.extra ? 1 : 0);
   if (inc - mine <= sh.lo && sh.lo < inc) {
-    int64_t s = inc - mine;
-    int b = b0;
+    int s = inc - mine, b = b0;
     for (;; ++b) {
-      const int64_t c = static_cast<int64_t>(a.heads) * (paged_tiles<KEYS>(a, b) + OVERHEAD);
+      const int c = a.heads * (paged_tiles<KEYS>(a, b) + OVERHEAD);
       if (sh.lo < s + c || b + 1 >= b1) break;
       s += c;
     }
@@ -212,7 +204,7 @@ __device__ __forceinline__ PagedShare paged_share(const PagedArgs& a, int cta, i
 // (b, h), whose first unit is s.
 struct PagedPiece {
   int b, h, n, len;
-  int64_t s;
+  int s;
   int t0, t1;
   bool valid;
   // this CTA alone has the segment
@@ -221,16 +213,16 @@ struct PagedPiece {
 
 template <int OVERHEAD>
 __device__ __forceinline__ void paged_clip(PagedPiece& p, const PagedShare& sh) {
-  const int64_t first = p.s + OVERHEAD;   // unit of tile 0
-  p.t0 = sh.lo > first ? static_cast<int>(min(sh.lo - first, static_cast<int64_t>(p.n))) : 0;
-  p.t1 = static_cast<int>(max(static_cast<int64_t>(0), min(sh.hi - first, static_cast<int64_t>(p.n))));
+  const int first = p.s + OVERHEAD;   // unit of tile 0
+  p.t0 = max(0, min(sh.lo - first, p.n));
+  p.t1 = max(0, min(sh.hi - first, p.n));
 }
 
 // The first piece at or after segment (b, h) at unit s that gives this CTA
 // something to do: tiles, or the rows of an empty segment that begins here.
 template <int KEYS, int OVERHEAD>
 __device__ __forceinline__ PagedPiece paged_piece(const PagedArgs& a, const PagedShare& sh, int b,
-                                                  int h, int64_t s) {
+                                                  int h, int s) {
   PagedPiece p;
   p.valid = false;
   p.b = b;

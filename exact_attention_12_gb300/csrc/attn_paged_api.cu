@@ -75,6 +75,9 @@ attn_status validate(const attn_params* p, int32_t n_q, const attn_pages* g, boo
     return fail(ATTN_ERR_INVALID_ARG, "page table is NULL");
   if (g->shared_len < 0 || g->shared_len > cap || g->shared_len % g->page_size != 0)
     return fail(ATTN_ERR_INVALID_ARG, "shared_len must be a multiple of page_size, at most N");
+  if (p->B * (latent ? 1 : H_kv) * (cap / (latent ? attn::kLatentKeys : attn::kPagedKeys) +
+                                    attn::kPagedOverhead + 1) >= (int64_t{1} << 31))
+    return fail(ATTN_ERR_UNSUPPORTED, "B * H_kv * N / 32 must stay below 2^31");
   if (latent && g->shared_len != 0)
     return fail(ATTN_ERR_UNSUPPORTED, "latent decode takes no shared prefix");
   // strides
@@ -143,7 +146,7 @@ Layout layout(const attn_params* p, int32_t n_q, const attn_pages* g, bool laten
   const int64_t tiles = (static_cast<int64_t>(p->N) - L.first + keys - 1) / keys;
   const int64_t units = static_cast<int64_t>(p->B) * L.heads *
                         (tiles + (latent ? attn::kLatentOverhead : attn::kPagedOverhead));
-  const int64_t want = units / attn::kPagedMinUnits;
+  const int64_t want = units / (latent ? attn::kLatentMinUnits : attn::kPagedMinUnits);
   if (most > want) most = want;
   L.ctas = static_cast<int>(most < 1 ? 1 : most);
   if (L.first > 0) {

@@ -27,25 +27,29 @@ def _public_stream(index):
 _stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_stream)
 
 
-def _call(device, ws, size_of, call, what):
-    """call(ws pointer, bytes, stream) on `device`, with the caller's workspace
-    or the device's shared one, grown when the call says it is too small."""
-    if device.type != "cuda":
+def _call(fn, size_fn, size_args, args, device, ws, what):
+    """fn(*args, ws pointer, bytes, stream) on `device`, with the caller's
+    workspace or the device's shared one, which grows (to what `size_fn` says)
+    when the call finds it too small."""
+    index = device.index
+    if index is None or device.type != "cuda":
         raise ValueError(f"{what}: tensors must be on a CUDA device")
-    if torch.cuda.current_device() != device.index:
+    if torch.cuda.current_device() != index:
         with torch.cuda.device(device):
-            return _call(device, ws, size_of, call, what)
-    stream = _stream(device.index)
-    if ws is not None:
+            return _call(fn, size_fn, size_args, args, device, ws, what)
+    if ws is None:
+        w = workspace(device, 256)
+        st = fn(*args, w.data_ptr(), w.numel(), _stream(index))
+        if st == _abi.ATTN_ERR_WORKSPACE:
+            need = size_fn(*size_args) if size_fn else 256
+            if need == 0:
+                check_status(_abi.ATTN_ERR_INVALID_ARG, what)
+            w = workspace(device, need)
+            st = fn(*args, w.data_ptr(), w.numel(), _stream(index))
+    else:
         if ws.device != device or not ws.is_contiguous():
             raise ValueError(f"{what}: ws must be contiguous, on the tensors' device")
-        check_status(call(ws.data_ptr(), ws.numel() * ws.element_size(), stream), what)
-        return
-    w = workspace(device, 256)
-    st = call(w.data_ptr(), w.numel(), stream)
-    if st == _abi.ATTN_ERR_WORKSPACE:
-        w = workspace(device, size_of())
-        st = call(w.data_ptr(), w.numel(), stream)
+        st = fn(*args, ws.data_ptr(), ws.numel() * ws.element_size(), _stream(index))
     if st:
         check_status(st, what)
 
@@ -88,12 +92,6 @@ def _strides(t):
     return s
 
 
-def _check_bf16(*ts):
-    for t in ts:
-        if t.dtype != torch.bfloat16 or t.device != ts[0].device:
-            raise TypeError("tensors must be bf16 on one device")
-
-
 def attention_decode_paged(q, k_pages, v_pages, page_table, cache_lens, *, scale=None, causal=True,
                            shared_len=0, out=None, lse=None, ws=None):
     """The decode step of attention_decode against a paged cache (see
@@ -108,8 +106,10 @@ def attention_decode_paged(q, k_pages, v_pages, page_table, cache_lens, *, scale
     for the whole batch.  Returns (o, lse) with o like q and lse fp32
     [B, H, n_q].  A page index outside the cache is reported by check().
     """
-    _check_bf16(q, k_pages, v_pages)
-    shape, pages = q.shape, k_pages.shape
+    device, shape, pages = q.device, q.shape, k_pages.shape
+    if not q.dtype == k_pages.dtype == v_pages.dtype == torch.bfloat16 \
+            or k_pages.device != device or v_pages.device != device:
+        raise TypeError("q, k_pages and v_pages must be bf16 on one device")
     if len(shape) != 4 or len(pages) != 4 or pages != v_pages.shape or pages[3] != shape[3]:
         raise ValueError("q must be [B, H, n_q, d], k_pages and v_pages "
                          "[num_pages, H_kv, page_size, d]")
@@ -117,11 +117,13 @@ def attention_decode_paged(q, k_pages, v_pages, page_table, cache_lens, *, scale
     num_pages, H_kv, page_size, _ = pages
     if H_kv < 1 or H % H_kv:
         raise ValueError("H_kv must divide q's H")
-    ks = _strides(k_pages)
-    if ks != _strides(v_pages):
-        raise ValueError("k_pages and v_pages must share strides")
+    if k_pages.is_contiguous() and v_pages.is_contiguous():
+        ks = (H_kv * page_size * d, page_size * d, d)
+    else:
+        ks = _strides(k_pages)
+        if ks != _strides(v_pages):
+            raise ValueError("k_pages and v_pages must share strides")
     qs = _strides(q)
-    device = q.device
     if out is None:
         out = torch.empty_like(q) if q.is_contiguous() else torch.empty_strided(
             shape, q.stride(), dtype=q.dtype, device=device)
@@ -134,11 +136,10 @@ def attention_decode_paged(q, k_pages, v_pages, page_table, cache_lens, *, scale
                    d ** -0.5 if scale is None else scale, 1 if causal else 0, 0.0, 0, 0, lens,
                    None, 0, qs[0], qs[1], qs[2], H_kv, 0, ks[0], ks[1], ks[2])
     g = AttnPages(table, row, width, page_size, num_pages, shared_len)
-    fn = lib().attn_decode_paged
-    pp, gp = ctypes.byref(p), ctypes.byref(g)
-    ptrs = (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), lse.data_ptr())
-    _call(device, ws, lambda: _size(lib().attn_decode_paged_workspace_size(pp, n_q, gp)),
-          lambda w, n, s: fn(pp, n_q, gp, *ptrs, w, n, s), "attn_decode_paged")
+    c, pp, gp = lib(), ctypes.byref(p), ctypes.byref(g)
+    _call(c.attn_decode_paged, c.attn_decode_paged_workspace_size, (pp, n_q, gp),
+          (pp, n_q, gp, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(),
+           lse.data_ptr()), device, ws, "attn_decode_paged")
     return out, lse
 
 
@@ -154,14 +155,14 @@ def attention_decode_latent(q, c_pages, page_table, cache_lens, *, scale, d_v=51
     projections were folded in.  Returns (o, lse): o [B, H, n_q, d_v] bf16,
     contiguous, and lse fp32 [B, H, n_q].
     """
-    _check_bf16(q, c_pages)
-    shape, pages, cols = q.shape, c_pages.shape, d_v + _ROPE
+    device, shape, pages, cols = q.device, q.shape, c_pages.shape, d_v + _ROPE
+    if not q.dtype == c_pages.dtype == torch.bfloat16 or c_pages.device != device:
+        raise TypeError("q and c_pages must be bf16 on one device")
     if len(shape) != 4 or len(pages) != 3 or shape[3] != cols or pages[2] != cols:
         raise ValueError(f"q must be [B, H, n_q, d_v + {_ROPE}], c_pages "
                          f"[num_pages, page_size, d_v + {_ROPE}]")
     B, H, n_q, _ = shape
     num_pages, page_size, _ = pages
-    device = q.device
     if out is None:
         out = torch.empty((B, H, n_q, d_v), dtype=q.dtype, device=device)
     elif out.shape != (B, H, n_q, d_v) or not out.is_contiguous() or out.dtype != q.dtype \
@@ -173,11 +174,10 @@ def attention_decode_latent(q, c_pages, page_table, cache_lens, *, scale, d_v=51
     p = AttnParams(B, H, width * page_size, d_v, _abi.ATTN_BF16, scale, 1 if causal else 0, 0.0, 0,
                    0, lens, None, 0, qs[0], qs[1], qs[2], 1, 0, cs[0], cs[0], cs[1])
     g = AttnPages(table, row, width, page_size, num_pages, 0)
-    fn = lib().attn_decode_latent
-    pp, gp = ctypes.byref(p), ctypes.byref(g)
-    ptrs = (q.data_ptr(), c_pages.data_ptr(), out.data_ptr(), lse.data_ptr())
-    _call(device, ws, lambda: _size(lib().attn_decode_latent_workspace_size(pp, n_q, gp)),
-          lambda w, n, s: fn(pp, n_q, gp, *ptrs, w, n, s), "attn_decode_latent")
+    c, pp, gp = lib(), ctypes.byref(p), ctypes.byref(g)
+    _call(c.attn_decode_latent, c.attn_decode_latent_workspace_size, (pp, n_q, gp),
+          (pp, n_q, gp, q.data_ptr(), c_pages.data_ptr(), out.data_ptr(), lse.data_ptr()), device,
+          ws, "attn_decode_latent")
     return out, lse
 
 
@@ -188,12 +188,6 @@ def _lse(lse, shape, device):
             or lse.device != device:
         raise ValueError("lse must be a contiguous fp32 [B, H, n_q] on q's device")
     return lse
-
-
-def _size(n):
-    if n == 0:
-        check_status(_abi.ATTN_ERR_INVALID_ARG, "workspace size")
-    return n
 
 
 # ------------------------------------------------------------------- upkeep --
@@ -246,9 +240,8 @@ def pages_copy(pools, src, dst, *, ws=None):
     d, m = _list(dst, dev, "dst")
     if n != m:
         raise ValueError("src and dst must have the same length")
-    fn = lib().attn_pages_copy
-    _call(dev, ws, lambda: 256,
-          lambda w, nb, st: fn(arr, len(pools), num_pages, s, d, n, w, nb, st), "attn_pages_copy")
+    _call(lib().attn_pages_copy, None, (), (arr, len(pools), num_pages, s, d, n), dev, ws,
+          "attn_pages_copy")
 
 
 def pages_extend(page_table, cache_lens, refs, seqs, new_lens, *, page_size, ws=None):
@@ -260,9 +253,9 @@ def pages_extend(page_table, cache_lens, refs, seqs, new_lens, *, page_size, ws=
     d, m = _list(new_lens, refs.device, "new_lens")
     if n != m:
         raise ValueError("seqs and new_lens must have the same length")
-    tp, fn = ctypes.byref(t), lib().attn_pages_extend
-    _call(refs.device, ws, lambda: _size(lib().attn_pages_workspace_size(tp, n)),
-          lambda w, nb, st: fn(tp, s, d, n, w, nb, st), "attn_pages_extend")
+    c, tp = lib(), ctypes.byref(t)
+    _call(c.attn_pages_extend, c.attn_pages_workspace_size, (tp, n), (tp, s, d, n), refs.device, ws,
+          "attn_pages_extend")
 
 
 def pages_fork(pools, page_table, cache_lens, refs, parents, children, *, page_size, ws=None):
@@ -277,9 +270,9 @@ def pages_fork(pools, page_table, cache_lens, refs, parents, children, *, page_s
     if n != m:
         raise ValueError("parents and children must have the same length")
     new = torch.empty_like(parents)
-    tp, fn, np_ = ctypes.byref(t), lib().attn_pages_fork, new.data_ptr()
-    _call(refs.device, ws, lambda: _size(lib().attn_pages_workspace_size(tp, n)),
-          lambda w, nb, st: fn(tp, arr, len(pools), a, b, n, np_, w, nb, st), "attn_pages_fork")
+    c, tp = lib(), ctypes.byref(t)
+    _call(c.attn_pages_fork, c.attn_pages_workspace_size, (tp, n),
+          (tp, arr, len(pools), a, b, n, new.data_ptr()), refs.device, ws, "attn_pages_fork")
     return new
 
 
@@ -287,8 +280,7 @@ def pages_free(page_table, cache_lens, refs, seqs, *, page_size, ws=None):
     """The sequences `seqs` give back their pages (see attn_pages_free)."""
     t = _table_args(page_table, cache_lens, refs, page_size)
     s, n = _list(seqs, refs.device, "seqs")
-    tp, fn = ctypes.byref(t), lib().attn_pages_free
-    _call(refs.device, ws, lambda: 256, lambda w, nb, st: fn(tp, s, n, w, nb, st),
+    _call(lib().attn_pages_free, None, (), (ctypes.byref(t), s, n), refs.device, ws,
           "attn_pages_free")
 
 
@@ -299,7 +291,7 @@ def pages_compact(pools, page_table, cache_lens, refs, *, page_size, ws=None):
     t = _table_args(page_table, cache_lens, refs, page_size)
     arr = _pool_args(pools, refs.shape[0], refs.device)
     moved = torch.empty_like(refs)
-    tp, fn, mp = ctypes.byref(t), lib().attn_pages_compact, moved.data_ptr()
-    _call(refs.device, ws, lambda: _size(lib().attn_pages_workspace_size(tp, 0)),
-          lambda w, nb, st: fn(tp, arr, len(pools), mp, w, nb, st), "attn_pages_compact")
+    c, tp = lib(), ctypes.byref(t)
+    _call(c.attn_pages_compact, c.attn_pages_workspace_size, (tp, 0),
+          (tp, arr, len(pools), moved.data_ptr()), refs.device, ws, "attn_pages_compact")
     return moved

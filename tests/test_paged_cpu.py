@@ -79,7 +79,8 @@ def _status(abi, p, g, n_q, latent=False, ws=0x1000, nb=1 << 40, ptr=0x1000):
     (dict(stride_n=60), 1), (dict(stride_n=56), 1), (dict(kv_stride_n=56), 1),
     (dict(kv_stride_h=0), 1), (dict(kv_stride_b=-64), 1), (dict(stride_h=4), 1),
     (dict(max_pages=1 << 16, table_stride=1 << 16, page_size=32768, N=0), 2),
-    (dict(B=1 << 29, n_q=2), 2),
+    (dict(B=1 << 29, n_q=2), 2), (dict(B=1 << 20, max_pages=1 << 15, table_stride=1 << 15,
+                                       N=1 << 20), 2),
 ])
 def test_paged_decode_refusals(abi, kw, status):
     p, g, n_q = _decode(abi, **kw)
