@@ -44,7 +44,6 @@ using namespace sm103;
 
 namespace {
 
-constexpr float kLn2 = 0.693147180559945309f;
 constexpr int kAhead = 1;   // tiles between a tile's way to L2 and its copy
 
 template <int DV>
@@ -529,10 +528,12 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
         const int c = lane + 32 * e;
         const float s = n > 0 ? (sum[0][c] + sum[1][c]) + (sum[2][c] + sum[3][c]) : 0.f;
         inv[e] = s != 0.f ? 1.f / s : 0.f;
-        L[e] = s != 0.f ? (mref[e] * c2 + __log2f(s)) * kLn2 : -INFINITY;
+        L[e] = s != 0.f ? fmaf(mref[e], a.scale, logf(s)) : -INFINITY;
       }
       const bool whole = p.whole();
       if (p.t0 == 0 && !whole) note = paged_note<kLatentOverhead>(share, p);
+      if (a.by_segment && p.t0 == 0 && threadIdx.x == 0 && r0 == 0)
+        a.notes[p.b] = whole ? MergeNote{p.b, 0, 0, -1} : note;
       const int64_t part = 2 * static_cast<int64_t>(cta) + (p.s < share.lo ? 0 : 1);
       if (warp == 0) {
 #pragma unroll
@@ -586,7 +587,7 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
       }
       tc_fence_before();
     }
-    if (threadIdx.x == 0 && r0 == 0) a.notes[cta] = note;
+    if (!a.by_segment && threadIdx.x == 0 && r0 == 0) a.notes[cta] = note;
   }
 
   tc_fence_before();

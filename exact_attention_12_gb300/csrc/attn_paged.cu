@@ -32,7 +32,6 @@ using namespace sm103;
 
 namespace {
 
-constexpr float kLn2 = 0.693147180559945309f;
 constexpr int kSlots = 3;   // tiles worked on at a time by a CTA
 
 template <int D, int MT>
@@ -342,7 +341,7 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
     const bool whole = p.whole();
     const bool apart = a.pre_splits > 0;   // a prefix is merged afterwards
     if (p.t0 == 0 && !whole) note = paged_note<kPagedOverhead>(share, p);
-    if (apart && p.t0 == 0 && threadIdx.x == 0)
+    if (a.by_segment && p.t0 == 0 && threadIdx.x == 0)
       a.notes[p.b * a.heads + p.h] = whole ? MergeNote{p.b, p.h, 0, -1} : note;
     const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (p.s < share.lo ? 0 : 1);
     for (int m = 0; m < MT; ++m) {   // 16 rows at a time
@@ -366,32 +365,34 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
       }
       for (int e = threadIdx.x; e < min(16, a.rows - 16 * m) * (D / 4); e += C::kThreads) {
         const int rr = e / (D / 4), c = 4 * (e - rr * (D / 4)), r = 16 * m + rr;
-        float mx = -INFINITY, lt = 0.f;
+        auto logsumexp = [&] {
+          float mx = -INFINITY, lt = 0.f;
 #pragma unroll
-        for (int w = 0; w < kSlots; ++w) mx = fmaxf(mx, sh.m[w][r]);
+          for (int w = 0; w < kSlots; ++w) mx = fmaxf(mx, sh.m[w][r]);
 #pragma unroll
-        for (int w = 0; w < kSlots; ++w) {
-          const float mw = sh.m[w][r];
-          if (mw != -INFINITY) lt += sh.l[w][r] * ex2_approx((mw - mx) * c2);
-        }
-        float L = lt > 0.f ? (mx * c2 + __log2f(lt)) * kLn2 : -INFINITY;
-        float4 x = *reinterpret_cast<const float4*>(&red[rr * C::kRedStride + c]);
+          for (int w = 0; w < kSlots; ++w) {
+            const float mw = sh.m[w][r];
+            if (mw != -INFINITY) lt += sh.l[w][r] * ex2_approx((mw - mx) * c2);
+          }
+          return lt == 0.f ? -INFINITY : fmaf(mx, a.scale, logf(lt));
+        };
+        const float4 x = *reinterpret_cast<const float4*>(&red[rr * C::kRedStride + c]);
         if (whole) {
           const int hl = r / a.n_q, qt = r - hl * a.n_q, h = p.h * a.group + hl;
           const int64_t row = (static_cast<int64_t>(p.b) * a.H + h) * a.n_q + qt;
           if (apart) {
             const int64_t at = a.pre_splits * (static_cast<int64_t>(a.B) * a.all_rows) + row;
             *reinterpret_cast<float4*>(a.pre_o + at * D + c) = x;
-            if (c == 0) a.pre_l[at] = L;
+            if (c == 0) a.pre_l[at] = logsumexp();
             continue;
           }
           *reinterpret_cast<uint2*>(a.o + p.b * a.stride_b + h * a.stride_h +
                                     static_cast<int64_t>(qt) * a.stride_n + c) =
               make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-          if (c == 0) a.lse[row] = L;
+          if (c == 0) a.lse[row] = logsumexp();
         } else {
           *reinterpret_cast<float4*>(a.part_o + (part * a.rows + r) * D + c) = x;
-          if (c == 0) a.part_l[part * a.rows + r] = L;
+          if (c == 0) a.part_l[part * a.rows + r] = logsumexp();
         }
       }
       __syncthreads();   // red (and after the last rows m, l) is free
@@ -399,111 +400,145 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
     if (!ok) break;
     p = next;
   }
-  if (a.pre_splits == 0 && threadIdx.x == 0) a.notes[blockIdx.x] = note;
+  if (!a.by_segment && threadIdx.x == 0) a.notes[blockIdx.x] = note;
   if (!ok && mt == 0 && lane == 0) {   // let issued copies land before the CTA exits
     for (uint32_t t = issued > ST ? issued - ST : 0; t < issued; ++t)
       mbar_wait_drain(&sh.full[slot * ST + t % ST], (t / ST) & 1, a.timeout_ns);
   }
 }
 
-// Four columns of a row's O and its L, merged from `n` partials: the i-th has
-// its L at part_l[at(i)] and its columns at part_o[at(i) * D + c] of the arrays
-// that `from` names.  L = log sum e^(L_i), O = sum e^(L_i - L) O_i.
-template <int D, typename From>
-__device__ __forceinline__ void merge_row(int n, int c, const From& from, float4& x, float& L) {
+struct Partial {
+  const float *o, *l;   // a row's columns; its L
+};
+
+constexpr int kMergeThreads = 256;
+
+// Four columns of a row's O merged from `n` partials, O = sum e^(L_i - L) O_i,
+// and the parts of L = log sum e^(L_i) = top + log(sum).  GROUPS threads share an item (threads
+// kMergeThreads / GROUPS apart), each takes every GROUPS-th partial; the first
+// has the result.  `live`: the item exists.  The whole CTA.
+template <int GROUPS, typename From>
+__device__ __forceinline__ void merge_row(bool live, int n, const From& from, float4& x, float& top,
+                                          float& sum) {
+  constexpr int kItems = kMergeThreads / GROUPS;
+  __shared__ float tops[GROUPS > 1 ? kMergeThreads : 1], sums[GROUPS > 1 ? kMergeThreads : 1];
+  __shared__ float4 xs[GROUPS > 1 ? kMergeThreads : 1];
+  const int group = threadIdx.x / kItems, item = threadIdx.x % kItems;
+  if (!live) n = 0;
   x = make_float4(0.f, 0.f, 0.f, 0.f);
-  float top = -INFINITY;
+  top = -INFINITY;
+  sum = 0.f;
 #pragma unroll 4
-  for (int i = 0; i < n; ++i) top = fmaxf(top, *from(i).l);
-  L = top;
-  if (top == -INFINITY) return;
-  float sum = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const auto part = from(i);
-    const float w = __expf(*part.l - top);
-    const float4 y = *reinterpret_cast<const float4*>(part.o + c);
-    sum += w;
-    x.x = fmaf(w, y.x, x.x);
-    x.y = fmaf(w, y.y, x.y);
-    x.z = fmaf(w, y.z, x.z);
-    x.w = fmaf(w, y.w, x.w);
+  for (int i = group; i < n; i += GROUPS) top = fmaxf(top, *from(i).l);
+  if constexpr (GROUPS > 1) {
+    tops[threadIdx.x] = top;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < GROUPS; ++k) top = fmaxf(top, tops[item + k * kItems]);
   }
-  const float inv = 1.f / sum;
+  if (top > -INFINITY) {
+#pragma unroll 4
+    for (int i = group; i < n; i += GROUPS) {
+      const Partial part = from(i);
+      const float w = __expf(*part.l - top);
+      const float4 y = *reinterpret_cast<const float4*>(part.o);
+      sum += w;
+      x.x = fmaf(w, y.x, x.x);
+      x.y = fmaf(w, y.y, x.y);
+      x.z = fmaf(w, y.z, x.z);
+      x.w = fmaf(w, y.w, x.w);
+    }
+  }
+  if constexpr (GROUPS > 1) {
+    sums[threadIdx.x] = sum;
+    xs[threadIdx.x] = x;
+    __syncthreads();
+    if (group == 0) {
+#pragma unroll
+      for (int k = 1; k < GROUPS; ++k) {
+        const float4 y = xs[item + k * kItems];
+        sum += sums[item + k * kItems];
+        x.x += y.x;
+        x.y += y.y;
+        x.z += y.z;
+        x.w += y.w;
+      }
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   x.x *= inv;
   x.y *= inv;
   x.z *= inv;
   x.w *= inv;
-  L = top + __logf(sum);
 }
-
-struct Partial {
-  const float *o, *l;
-};
 
 // Row hr (head * n_q + query) of sequence b.
 __device__ __forceinline__ void write_row(const PagedArgs& a, int b, int hr, int c, const float4& x,
-                                          float L) {
+                                          float top, float sum) {
   const int h = hr / a.n_q, qt = hr - h * a.n_q;
   *reinterpret_cast<uint2*>(a.o + b * a.stride_b + h * a.stride_h +
                             static_cast<int64_t>(qt) * a.stride_n + c) =
       make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-  if (c == 0) a.lse[static_cast<int64_t>(b) * a.all_rows + hr] = L;
+  if (c == 0)
+    a.lse[static_cast<int64_t>(b) * a.all_rows + hr] = sum == 0.f ? -INFINITY : top + logf(sum);
 }
 
-// Segments that were cut: their pieces merged, four columns of a row per
-// thread.  A CTA per (CTA that may have left a note, 128 x 4 elements).
-template <int D>
-__global__ void __launch_bounds__(128) paged_merge_kernel(const PagedArgs a) {
+// Segments that were cut: their pieces merged, four columns of a row per item.
+// A CTA per (note, kMergeThreads / GROUPS items).  Bound by the latency of its
+// loads (the pieces come from L2) and by the launch of CTAs that find nothing
+// to do, hence notes per segment where there are fewer of those, and four
+// threads per item where a segment has many pieces.
+template <int D, int GROUPS>
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedArgs a) {
+  constexpr int kItems = kMergeThreads / GROUPS;
   grid_dep_wait();
   grid_dep_launch();
   const int4 raw = *reinterpret_cast<const int4*>(a.notes + blockIdx.x);
   const MergeNote note{raw.x, raw.y, raw.z, raw.w};
-  if (note.b < 0) return;
-  const int e = blockIdx.y * 128 + threadIdx.x;
-  const int r = e / (D / 4), c = 4 * (e % (D / 4));
-  const int hr = note.h * a.rows + r;
-  if (r >= a.rows || hr >= a.all_rows) return;
+  if (note.b < 0 || note.more < 0) return;   // (uniform over the CTA)
+  const int e = blockIdx.y * kItems + threadIdx.x % kItems;
+  const int r = e / (D / 4), c = 4 * (e % (D / 4)), hr = note.h * a.rows + r;
+  const bool live = r < a.rows && hr < a.all_rows;
   auto piece = [&](int i) {
     const int64_t at =
         static_cast<int64_t>(i == 0 ? note.slot : (note.slot & ~1) + 2 * i) * a.rows + r;
-    return Partial{a.part_o + at * D, a.part_l + at};
+    return Partial{a.part_o + at * D + c, a.part_l + at};
   };
   float4 x;
-  float L;
-  merge_row<D>(note.more + 1, c, piece, x, L);
-  write_row(a, note.b, hr, c, x, L);
+  float top, sum;
+  merge_row<GROUPS>(live, note.more + 1, piece, x, top, sum);
+  if (live && threadIdx.x < kItems) write_row(a, note.b, hr, c, x, top, sum);
 }
 
 // With a shared prefix: every row from the prefix's pieces and its own
-// segment, in one piece or cut.  A CTA per (segment, 128 x 4 elements).
-template <int D>
-__global__ void __launch_bounds__(128) paged_finish_kernel(const PagedArgs a) {
+// segment, in one piece or cut.  A CTA per (segment, kMergeThreads / GROUPS items).
+template <int D, int GROUPS>
+__global__ void __launch_bounds__(kMergeThreads) paged_finish_kernel(const PagedArgs a) {
+  constexpr int kItems = kMergeThreads / GROUPS;
   grid_dep_wait();
   grid_dep_launch();
   const int4 raw = *reinterpret_cast<const int4*>(a.notes + blockIdx.x);
   const MergeNote note{raw.x, raw.y, raw.z, raw.w};
-  const int e = blockIdx.y * 128 + threadIdx.x;
-  const int r = e / (D / 4), c = 4 * (e % (D / 4));
-  if (r >= a.rows) return;
-  const int hr = note.h * a.rows + r;
+  const int e = blockIdx.y * kItems + threadIdx.x % kItems;
+  const int r = e / (D / 4), c = 4 * (e % (D / 4)), hr = note.h * a.rows + r;
+  const bool live = r < a.rows;
   const int64_t row = static_cast<int64_t>(note.b) * a.all_rows + hr;
   const int64_t all = static_cast<int64_t>(a.B) * a.all_rows;
   const int pre = a.pre_splits + (note.more < 0 ? 1 : 0);
   auto part = [&](int i) {
     if (i < pre) {
       const int64_t at = i * all + row;
-      return Partial{a.pre_o + at * D, a.pre_l + at};
+      return Partial{a.pre_o + at * D + c, a.pre_l + at};
     }
     i -= pre;
     const int64_t at =
         static_cast<int64_t>(i == 0 ? note.slot : (note.slot & ~1) + 2 * i) * a.rows + r;
-    return Partial{a.part_o + at * D, a.part_l + at};
+    return Partial{a.part_o + at * D + c, a.part_l + at};
   };
   float4 x;
-  float L;
-  merge_row<D>(pre + note.more + 1, c, part, x, L);
-  write_row(a, note.b, hr, c, x, L);
+  float top, sum;
+  merge_row<GROUPS>(live, pre + note.more + 1, part, x, top, sum);
+  if (live && threadIdx.x < kItems) write_row(a, note.b, hr, c, x, top, sum);
 }
 
 template <int D, int MT>
@@ -539,21 +574,31 @@ cudaError_t launch_paged(const CUtensorMap& tk, const CUtensorMap& tv, const Pag
   return a.d == 64 ? launch_d<64>(tk, tv, a, ctas, s) : launch_d<128>(tk, tv, a, ctas, s);
 }
 
-cudaError_t launch_paged_merge(const PagedArgs& a, int ctas, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(ctas),
-                  static_cast<unsigned>((min(a.rows, a.all_rows) * (a.d / 4) + 127) / 128));
-  auto kernel = a.d == 64    ? paged_merge_kernel<64>
-                : a.d == 128 ? paged_merge_kernel<128>
-                : a.d == 256 ? paged_merge_kernel<256>
-                             : paged_merge_kernel<512>;
-  return launch_pdl(kernel, grid, dim3(128), 0, s, a);
+cudaError_t launch_paged_merge(const PagedArgs& a, int notes, cudaStream_t s) {
+  // Four threads an item while the items are too few to fill the GPU: 16
+  // sequences of 4096 latent vectors, 16 heads (32 K items of 10 pieces) 26.2
+  // against 28.6 us a step, but with 64 heads (131 K items) 39.6 against 36.4.
+  const int64_t items = static_cast<int64_t>(notes) * min(a.rows, a.all_rows) * (a.d / 4);
+  const bool groups = items <= (1 << 16);
+  const int per = groups ? kMergeThreads / 4 : kMergeThreads;
+  const dim3 grid(static_cast<unsigned>(notes),
+                  static_cast<unsigned>((min(a.rows, a.all_rows) * (a.d / 4) + per - 1) / per));
+  auto kernel = a.d == 64    ? (groups ? paged_merge_kernel<64, 4> : paged_merge_kernel<64, 1>)
+                : a.d == 128 ? (groups ? paged_merge_kernel<128, 4> : paged_merge_kernel<128, 1>)
+                : a.d == 256 ? (groups ? paged_merge_kernel<256, 4> : paged_merge_kernel<256, 1>)
+                             : (groups ? paged_merge_kernel<512, 4> : paged_merge_kernel<512, 1>);
+  return launch_pdl(kernel, grid, dim3(kMergeThreads), 0, s, a);
 }
 
 cudaError_t launch_paged_finish(const PagedArgs& a, cudaStream_t s) {
+  // (109 against 115 us a step with 9 pieces of the prefix and 131 K items)
+  const bool groups = a.pre_splits >= 3;
+  const int per = groups ? kMergeThreads / 4 : kMergeThreads;
   const dim3 grid(static_cast<unsigned>(a.B * a.heads),
-                  static_cast<unsigned>((a.rows * (a.d / 4) + 127) / 128));
-  return launch_pdl(a.d == 64 ? paged_finish_kernel<64> : paged_finish_kernel<128>, grid, dim3(128),
-                    0, s, a);
+                  static_cast<unsigned>((a.rows * (a.d / 4) + per - 1) / per));
+  auto kernel = a.d == 64 ? (groups ? paged_finish_kernel<64, 4> : paged_finish_kernel<64, 1>)
+                          : (groups ? paged_finish_kernel<128, 4> : paged_finish_kernel<128, 1>);
+  return launch_pdl(kernel, grid, dim3(kMergeThreads), 0, s, a);
 }
 
 }  // namespace attn

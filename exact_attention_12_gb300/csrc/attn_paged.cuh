@@ -29,7 +29,7 @@ constexpr int kStatusPage = 6;
 // segment that began before the CTA's run, slot 1 for one that begins in it.
 // The CTA that holds a cut segment's first tile leaves a note of the merge.
 struct MergeNote {
-  int b, h;      // the segment; b < 0: nothing to merge
+  int b, h;      // the segment; b < 0: nothing to merge (per segment: more < 0)
   int slot;      // partial slot of the first piece, 2 CTA + 0 or 1; the next
                  // CTAs' pieces are in their slot 0
   int more;      // how many CTAs follow
@@ -48,7 +48,7 @@ struct PagedArgs {
   int cap;                        // keys a row of the table can name
   int page_shift, num_pages;
   int first;                      // keys below it are left out (they are the shared prefix)
-  float scale_log2;
+  float scale, scale_log2;        // c, c log2(e)
   const __nv_bfloat16* q;
   int64_t stride_b, stride_h, stride_n;      // q (and o, but for latent)
   __nv_bfloat16* o;
@@ -57,7 +57,8 @@ struct PagedArgs {
   const __nv_bfloat16* pages;
   int64_t stride_page;
   int dense;                      // a page's rows follow one another without gaps
-  MergeNote* notes;               // workspace [G]; with a prefix one per segment, [B * heads]
+  MergeNote* notes;               // workspace: one per segment, or one per CTA, as
+  int by_segment;                 // fewer are (with a prefix always per segment)
   float* part_o;                  // workspace [2 G][rows][d]
   float* part_l;                  // workspace [2 G][rows]
   // a shared prefix: its pieces' partials and, behind them, those of the
@@ -78,7 +79,7 @@ struct PrefixArgs {
   int shared_len;
   int splits, tiles;              // pieces of the prefix; 128-key tiles in all
   int rows;                       // B * group * n_q: query rows of one key/value head
-  float scale_log2;
+  float scale, scale_log2;        // c, c log2(e)
   const __nv_bfloat16* q;
   int64_t stride_b, stride_h, stride_n;
   float* pre_o;
@@ -271,7 +272,7 @@ cudaError_t launch_paged(const CUtensorMap& tk, const CUtensorMap& tv, const Pag
 cudaError_t launch_prefix(const CUtensorMap& tk, const CUtensorMap& tv, const PrefixArgs& a,
                           cudaStream_t s);
 cudaError_t launch_latent(const CUtensorMap& tc, const PagedArgs& a, int ctas, cudaStream_t s);
-cudaError_t launch_paged_merge(const PagedArgs& a, int ctas, cudaStream_t s);
+cudaError_t launch_paged_merge(const PagedArgs& a, int notes, cudaStream_t s);
 cudaError_t launch_paged_finish(const PagedArgs& a, cudaStream_t s);
 
 // Tensor map of a paged cache for the host code (an attn_status).

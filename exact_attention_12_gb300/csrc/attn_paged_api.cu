@@ -118,9 +118,15 @@ bool empty(const attn_params* p) { return p->B == 0 || p->H == 0; }
 struct Layout {
   size_t notes = 0, part_o = 0, part_l = 0, pre_o = 0, pre_l = 0, total = 0;
   int ctas = 0;                            // of the decode kernel (latent: per row group)
+  int n_notes = 0;                         // of merges: one per segment or per CTA
+  bool by_segment = false;
   int heads = 0, group = 0, rows = 0;      // segments per sequence, heads and rows of one
   int first = 0, splits = 0, tiles = 0;    // the shared prefix
 };
+
+int64_t segments_of(const attn_params* p, const Layout& L) {
+  return static_cast<int64_t>(p->B) * L.heads;
+}
 
 Layout layout(const attn_params* p, int32_t n_q, const attn_pages* g, bool latent) {
   Layout L;
@@ -160,11 +166,12 @@ Layout layout(const attn_params* p, int32_t n_q, const attn_pages* g, bool laten
     if (k > 16) k = 16;
     L.splits = k < 1 ? 1 : static_cast<int>(k);
   }
+  const int64_t segments = segments_of(p, L);
+  L.by_segment = L.first > 0 || segments <= L.ctas;
+  L.n_notes = L.by_segment ? static_cast<int>(segments) : L.ctas;
   size_t off = kHeaderBytes;
   L.notes = off;
-  off = round_up(off + (L.first > 0 ? static_cast<size_t>(p->B) * L.heads : L.ctas) *
-                           sizeof(attn::MergeNote),
-                 256);
+  off = round_up(off + static_cast<size_t>(L.n_notes) * sizeof(attn::MergeNote), 256);
   L.part_o = off;
   off = round_up(off + 2 * static_cast<size_t>(L.ctas) * L.rows * p->d * sizeof(float), 256);
   L.part_l = off;
@@ -199,6 +206,7 @@ PagedArgs args_of(const attn_params* p, int32_t n_q, const attn_pages* g, const 
   a.page_shift = log2_of(g->page_size);
   a.num_pages = g->num_pages;
   a.first = L.first;
+  a.scale = p->scale;
   a.scale_log2 = p->scale * kLog2e;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.stride_b = p->stride_b;
@@ -207,6 +215,7 @@ PagedArgs args_of(const attn_params* p, int32_t n_q, const attn_pages* g, const 
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;
   a.notes = reinterpret_cast<attn::MergeNote*>(w + L.notes);
+  a.by_segment = L.by_segment;
   a.part_o = reinterpret_cast<float*>(w + L.part_o);
   a.part_l = reinterpret_cast<float*>(w + L.part_l);
   a.pre_splits = L.splits;
@@ -276,6 +285,7 @@ attn_status attn_decode_paged(const attn_params* p, int32_t n_q, const attn_page
     f.splits = L.splits;
     f.tiles = L.tiles;
     f.rows = p->B * L.group * n_q;
+    f.scale = a.scale;
     f.scale_log2 = a.scale_log2;
     f.q = a.q;
     f.stride_b = a.stride_b;
@@ -295,7 +305,7 @@ attn_status attn_decode_paged(const attn_params* p, int32_t n_q, const attn_page
     return st;
   if (L.first > 0) return launched(attn::launch_paged_finish(a, s), "shared prefix merge launch");
   if (L.ctas == 1) return ATTN_OK;   // one CTA cuts nothing
-  return launched(attn::launch_paged_merge(a, L.ctas, s), "paged merge launch");
+  return launched(attn::launch_paged_merge(a, L.n_notes, s), "paged merge launch");
 }
 
 size_t attn_decode_latent_workspace_size(const attn_params* p, int32_t n_q,
@@ -330,7 +340,7 @@ attn_status attn_decode_latent(const attn_params* p, int32_t n_q, const attn_pag
   a.stride_n = p->d;
   a.stride_h = static_cast<int64_t>(n_q) * p->d;
   a.stride_b = static_cast<int64_t>(p->H) * n_q * p->d;
-  return launched(attn::launch_paged_merge(a, L.ctas, s), "latent merge launch");
+  return launched(attn::launch_paged_merge(a, L.n_notes, s), "latent merge launch");
 }
 
 }  // extern "C"

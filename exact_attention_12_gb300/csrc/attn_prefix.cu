@@ -35,7 +35,6 @@ using namespace sm103;
 
 namespace {
 
-constexpr float kLn2 = 0.693147180559945309f;
 
 template <int D>
 struct PrefixCfg {
@@ -390,7 +389,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
                        : make_float4(0.f, 0.f, 0.f, 0.f);
       }
     }
-    if (live) a.pre_l[out] = some ? (m_used * c2 + __log2f(l_sum)) * kLn2 : -INFINITY;
+    if (live) a.pre_l[out] = some ? fmaf(m_used, a.scale, logf(l_sum)) : -INFINITY;
   }
 
   tc_fence_before();
