@@ -84,6 +84,7 @@ struct __align__(1024) LatentCtl {
   // [tile mod 2][16-key quarter][column]: the tile's maxima; behind the last
   // tile of a piece, in the buffer of the next, the columns' sums
   float wmax[2][4][64];
+  float L[64];              // of the rows, for the cluster
   int sums[12];
   PagedShare share;
   uint32_t tmem_base;
@@ -120,7 +121,8 @@ __device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t* r) {
       : "r"(taddr));
 }
 
-template <int DV>
+// CLUSTER: a sequence per cluster (a.cluster CTAs), else the balanced split.
+template <int DV, bool CLUSTER>
 __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
     latent_kernel(const __grid_constant__ CUtensorMap tc, const PagedArgs a, int groups) {
   using C = LatentCfg<DV>;
@@ -139,8 +141,11 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
-  const int r0 = static_cast<int>(blockIdx.x % groups) * kLatentRows;   // first query row
-  const int cta = blockIdx.x / groups, ctas = gridDim.x / groups;
+  // row groups side by side; of clusters, the clusters
+  const int unit = CLUSTER ? blockIdx.x / a.cluster : blockIdx.x;
+  const int r0 = unit % groups * kLatentRows;   // first query row
+  const int cta = unit / groups, ctas = gridDim.x / groups;
+  const int rank = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
   const int live = min(kLatentRows, a.all_rows - r0);
 
   if (threadIdx.x == 0) {
@@ -177,10 +182,20 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
   grid_dep_wait();
   grid_dep_launch();
   const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.tmem_base, 0);
-  const PagedShare share =
-      paged_share<C::kThreads, KT, kLatentOverhead, kLatentMinUnits>(a, cta, ctas, ctl.sums, &ctl.share);
+  PagedShare share{};
+  if constexpr (!CLUSTER)
+    share = paged_share<C::kThreads, KT, kLatentOverhead, kLatentMinUnits>(a, cta, ctas, ctl.sums,
+                                                                           &ctl.share);
   const WaitCtx wc{&ctl.abort_flag, a.status, a.timeout_ns};
-  PagedPiece p = paged_piece<KT, kLatentOverhead>(a, share, share.b, 0, share.s);
+  PagedPiece p;
+  if constexpr (CLUSTER) p = paged_part<KT>(a, cta, 0, rank);
+  else p = paged_piece<KT, kLatentOverhead>(a, share, share.b, 0, share.s);
+  auto next_of = [&](const PagedPiece& w) {
+    PagedPiece x = w;
+    if constexpr (CLUSTER) x.valid = false;
+    else x = paged_next<KT, kLatentOverhead>(a, share, w);
+    return x;
+  };
 
   if (warp >= 8) {
     regs_decrease<C::kRegsOther>();
@@ -213,7 +228,7 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
     // (the other row groups' CTAs read the same tiles)
     const bool fetch = a.dense && r0 == 0;
     for (; ok && p.valid; p = nx) {
-      nx = paged_next<KT, kLatentOverhead>(a, share, p);
+      nx = next_of(p);
       const int32_t* row = a.table + p.b * a.table_stride;
       for (int t = p.t0; t < p.t1; ++t, ++T) {
         const int s = T % ST;
@@ -262,7 +277,7 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
     uint32_t T = 0;   // tiles before this piece
     int k = 0;        // pieces with tiles
     for (; ok && __shfl_sync(0xffffffffu, p.valid, 0);
-         p = paged_next<KT, kLatentOverhead>(a, share, p)) {
+         p = next_of(p)) {
       const int n = __shfl_sync(0xffffffffu, p.t1 - p.t0, 0);
       const int left = __shfl_sync(0xffffffffu, p.len - p.t0 * KT, 0);
       if (n == 0) continue;
@@ -384,7 +399,7 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
     };
     load_q(p);
     for (PagedPiece nx = p; p.valid; p = nx) {
-      nx = paged_next<KT, kLatentOverhead>(a, share, p);
+      nx = next_of(p);
       const int n = p.t1 - p.t0;
       float mref[2] = {-INFINITY, -INFINITY};   // columns lane, lane + 32: reference maxima
       float mc[8], l[8];                        // softmax: this thread's columns
@@ -530,17 +545,20 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
         inv[e] = s != 0.f ? 1.f / s : 0.f;
         L[e] = s != 0.f ? fmaf(mref[e], a.scale, logf(s)) : -INFINITY;
       }
-      const bool whole = p.whole();
-      if (p.t0 == 0 && !whole) note = paged_note<kLatentOverhead>(share, p);
-      if (a.by_segment && p.t0 == 0 && threadIdx.x == 0 && r0 == 0)
-        a.notes[p.b] = whole ? MergeNote{p.b, 0, 0, -1} : note;
+      const bool whole = !CLUSTER && p.whole();
+      if constexpr (!CLUSTER) {
+        if (p.t0 == 0 && !whole) note = paged_note<kLatentOverhead>(share, p);
+        if (a.by_segment && p.t0 == 0 && threadIdx.x == 0 && r0 == 0)
+          a.notes[p.b] = whole ? MergeNote{p.b, 0, 0, -1} : note;
+      }
       const int64_t part = 2 * static_cast<int64_t>(cta) + (p.s < share.lo ? 0 : 1);
       if (warp == 0) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int r = r0 + lane + 32 * e;
           if (lane + 32 * e < live) {
-            if (whole) a.lse[static_cast<int64_t>(p.b) * a.all_rows + r] = L[e];
+            if (CLUSTER) ctl.L[lane + 32 * e] = L[e];
+            else if (whole) a.lse[static_cast<int64_t>(p.b) * a.all_rows + r] = L[e];
             else a.part_l[part * a.rows + r] = L[e];
           }
         }
@@ -578,7 +596,9 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
               if (16 * e + r < live) *reinterpret_cast<uint32_t*>(to + r * DV) = v;
             }
           } else {
-            float* to = a.part_o + (part * a.rows + r0 + 16 * e) * DV + dim;
+            // (a cluster's CTA: to where its tiles were)
+            float* to = CLUSTER ? reinterpret_cast<float*>(sC) + 16 * e * DV + dim
+                                : a.part_o + (part * a.rows + r0 + 16 * e) * DV + dim;
 #pragma unroll
             for (int j = 0; j < 16; ++j)
               if (16 * e + j < live) to[j * DV] = __uint_as_float(o[j]);
@@ -587,7 +607,35 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
       }
       tc_fence_before();
     }
-    if (!a.by_segment && threadIdx.x == 0 && r0 == 0) a.notes[cta] = note;
+    if (!CLUSTER && !a.by_segment && threadIdx.x == 0 && r0 == 0) a.notes[cta] = note;
+  }
+  if constexpr (CLUSTER) {
+    // the cluster's rows merged: each CTA writes a part of the items
+    static_assert(kLatentRows * DV * 4 <= ST * C::kTileBytes, "a CTA's O fits where its tiles were");
+    __syncwarp();
+    cluster_sync();
+    const float* o = reinterpret_cast<const float*>(sC);
+    for (int e = rank * C::kThreads + threadIdx.x; e < live * (DV / 4);
+         e += a.cluster * C::kThreads) {
+      const int r = e / (DV / 4), c = 4 * (e - r * (DV / 4));
+      float top = -INFINITY, sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int k = 0; k < a.cluster; ++k) top = fmaxf(top, cluster_ld(cluster_addr(&ctl.L[r], k)));
+      if (top > -INFINITY)
+        for (int k = 0; k < a.cluster; ++k) {
+          float y[4];
+          cluster_ld4(cluster_addr(o + r * DV + c, k), y);
+          const float w = __expf(cluster_ld(cluster_addr(&ctl.L[r], k)) - top);
+          sum += w;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = fmaf(w, y[i], x[i]);
+        }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const int64_t row = static_cast<int64_t>(cta) * a.all_rows + r0 + r;
+      *reinterpret_cast<uint2*>(a.o + row * DV + c) =
+          make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
+      if (c == 0) a.lse[row] = sum == 0.f ? -INFINITY : top + logf(sum);
+    }
+    cluster_sync();   // the others have read this CTA's rows
   }
 
   tc_fence_before();
@@ -598,7 +646,7 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
   }
 }
 
-template <int DV>
+template <int DV, bool CLUSTER>
 cudaError_t launch_dv(const CUtensorMap& tc, const PagedArgs& a, int ctas, cudaStream_t s) {
   using C = LatentCfg<DV>;
   static std::atomic<uint64_t> set_up{0};
@@ -607,23 +655,30 @@ cudaError_t launch_dv(const CUtensorMap& tc, const PagedArgs& a, int ctas, cudaS
   cudaError_t e = needs_setup(set_up, &dev, &todo);
   if (e != cudaSuccess) return e;
   if (todo) {
-    e = cudaFuncSetAttribute(latent_kernel<DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    e = cudaFuncSetAttribute(latent_kernel<DV, CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             C::kSmem);
     if (e != cudaSuccess) return e;
     // the register re-split inside the kernel assumes the launch allocation
     cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, latent_kernel<DV>)) != cudaSuccess) return e;
+    if ((e = cudaFuncGetAttributes(&fa, latent_kernel<DV, CLUSTER>)) != cudaSuccess) return e;
     if (static_cast<uint32_t>(fa.numRegs) < C::kRegsLaunch) return cudaErrorInvalidConfiguration;
     mark_done(set_up, dev);
   }
   const int groups = a.rows / kLatentRows;
-  return launch_pdl(latent_kernel<DV>, dim3(ctas * groups), dim3(C::kThreads), C::kSmem, s, tc, a,
-                    groups);
+  if (CLUSTER)
+    return launch_clusters(latent_kernel<DV, CLUSTER>,
+                           dim3(static_cast<unsigned>(a.B * groups * a.cluster)), dim3(C::kThreads),
+                           C::kSmem, a.cluster, s, tc, a, groups);
+  return launch_pdl(latent_kernel<DV, CLUSTER>, dim3(ctas * groups), dim3(C::kThreads), C::kSmem, s,
+                    tc, a, groups);
 }
 
 }  // namespace
 
 cudaError_t launch_latent(const CUtensorMap& tc, const PagedArgs& a, int ctas, cudaStream_t s) {
-  return a.d == 256 ? launch_dv<256>(tc, a, ctas, s) : launch_dv<512>(tc, a, ctas, s);
+  if (a.cluster > 0)
+    return a.d == 256 ? launch_dv<256, true>(tc, a, ctas, s) : launch_dv<512, true>(tc, a, ctas, s);
+  return a.d == 256 ? launch_dv<256, false>(tc, a, ctas, s) : launch_dv<512, false>(tc, a, ctas, s);
 }
 
 }  // namespace attn

@@ -57,6 +57,7 @@ struct PagedShared {
   uint64_t full[kSlots * PagedCfg<D, MT>::kStages];
   uint64_t empty[kSlots * PagedCfg<D, MT>::kStages];
   float m[kSlots][MT * 16], l[kSlots][MT * 16];
+  float L[16];   // of the rows in `red`, for the cluster
   int sums[PagedCfg<D, MT>::kWarps];
   PagedShare share;
   int abort_flag;
@@ -87,7 +88,8 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int D, int MT>
+// CLUSTER: a segment per cluster (a.cluster CTAs), else the balanced split.
+template <int D, int MT, bool CLUSTER>
 __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kCtasPerSm)
     paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                  const PagedArgs a) {
@@ -117,8 +119,10 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
   __syncthreads();
   grid_dep_wait();
   grid_dep_launch();
-  const PagedShare share = paged_share<C::kThreads, KT, kPagedOverhead, kPagedMinUnits>(
-      a, blockIdx.x, gridDim.x, sh.sums, &sh.share);
+  PagedShare share{};
+  if constexpr (!CLUSTER)
+    share = paged_share<C::kThreads, KT, kPagedOverhead, kPagedMinUnits>(a, blockIdx.x, gridDim.x,
+                                                                         sh.sums, &sh.share);
   MergeNote note{-1, 0, 0, 0};
   const WaitCtx wc{&sh.abort_flag, a.status, a.timeout_ns};
   const int box_rows = min(KT, 1 << a.page_shift);
@@ -184,7 +188,14 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
   const int lb = lane >> 3, lr = lane & 7;
   const float c2 = a.scale_log2;
 
-  PagedPiece p = paged_piece<KT, kPagedOverhead>(a, share, share.b, 0, share.s);
+  const int rank = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
+  PagedPiece p;
+  if constexpr (CLUSTER) {
+    const int segment = blockIdx.x / a.cluster, b = segment / a.heads;
+    p = paged_part<KT>(a, b, segment - b * a.heads, rank);
+  } else {
+    p = paged_piece<KT, kPagedOverhead>(a, share, share.b, 0, share.s);
+  }
   prefetch(p);
   while (p.valid) {   // (the same pieces in every warp)
     const int nu = slot_tiles(p);
@@ -310,8 +321,13 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
       }
     }
 
-    const PagedPiece next = paged_next<KT, kPagedOverhead>(a, share, p);
-    if (ok) prefetch(next);
+    PagedPiece next = p;
+    if constexpr (CLUSTER) {
+      next.valid = false;
+    } else {
+      next = paged_next<KT, kPagedOverhead>(a, share, p);
+      if (ok) prefetch(next);
+    }
 
     // ---- the slots' states merged: m, l per row, then O through shared memory
 #pragma unroll
@@ -340,9 +356,11 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
     }
     const bool whole = p.whole();
     const bool apart = a.pre_splits > 0;   // a prefix is merged afterwards
-    if (p.t0 == 0 && !whole) note = paged_note<kPagedOverhead>(share, p);
-    if (a.by_segment && p.t0 == 0 && threadIdx.x == 0)
-      a.notes[p.b * a.heads + p.h] = whole ? MergeNote{p.b, p.h, 0, -1} : note;
+    if constexpr (!CLUSTER) {
+      if (p.t0 == 0 && !whole) note = paged_note<kPagedOverhead>(share, p);
+      if (a.by_segment && p.t0 == 0 && threadIdx.x == 0)
+        a.notes[p.b * a.heads + p.h] = whole ? MergeNote{p.b, p.h, 0, -1} : note;
+    }
     const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (p.s < share.lo ? 0 : 1);
     for (int m = 0; m < MT; ++m) {   // 16 rows at a time
       for (int w = 0; w < kSlots; ++w) {   // in turn: the sum has a fixed order
@@ -363,44 +381,87 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
         }
         __syncthreads();
       }
-      for (int e = threadIdx.x; e < min(16, a.rows - 16 * m) * (D / 4); e += C::kThreads) {
-        const int rr = e / (D / 4), c = 4 * (e - rr * (D / 4)), r = 16 * m + rr;
-        auto logsumexp = [&] {
-          float mx = -INFINITY, lt = 0.f;
+      const int live = min(16, a.rows - 16 * m);
+      auto logsumexp = [&](int r) {
+        float mx = -INFINITY, lt = 0.f;
 #pragma unroll
-          for (int w = 0; w < kSlots; ++w) mx = fmaxf(mx, sh.m[w][r]);
+        for (int w = 0; w < kSlots; ++w) mx = fmaxf(mx, sh.m[w][r]);
 #pragma unroll
-          for (int w = 0; w < kSlots; ++w) {
-            const float mw = sh.m[w][r];
-            if (mw != -INFINITY) lt += sh.l[w][r] * ex2_approx((mw - mx) * c2);
-          }
-          return lt == 0.f ? -INFINITY : fmaf(mx, a.scale, logf(lt));
-        };
-        const float4 x = *reinterpret_cast<const float4*>(&red[rr * C::kRedStride + c]);
-        if (whole) {
+        for (int w = 0; w < kSlots; ++w) {
+          const float mw = sh.m[w][r];
+          if (mw != -INFINITY) lt += sh.l[w][r] * ex2_approx((mw - mx) * c2);
+        }
+        return lt == 0.f ? -INFINITY : fmaf(mx, a.scale, logf(lt));
+      };
+      if constexpr (CLUSTER) {
+        // the cluster's rows, and a prefix's pieces, merged: each CTA writes a
+        // part of the items
+        if (threadIdx.x < live) sh.L[threadIdx.x] = logsumexp(16 * m + threadIdx.x);
+        cluster_sync();
+        for (int e = rank * C::kThreads + threadIdx.x; e < live * (D / 4);
+             e += a.cluster * C::kThreads) {
+          const int rr = e / (D / 4), c = 4 * (e - rr * (D / 4)), r = 16 * m + rr;
           const int hl = r / a.n_q, qt = r - hl * a.n_q, h = p.h * a.group + hl;
           const int64_t row = (static_cast<int64_t>(p.b) * a.H + h) * a.n_q + qt;
-          if (apart) {
-            const int64_t at = a.pre_splits * (static_cast<int64_t>(a.B) * a.all_rows) + row;
-            *reinterpret_cast<float4*>(a.pre_o + at * D + c) = x;
-            if (c == 0) a.pre_l[at] = logsumexp();
-            continue;
+          const int64_t all = static_cast<int64_t>(a.B) * a.all_rows;
+          float top = -INFINITY, sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int k = 0; k < a.cluster; ++k)
+            top = fmaxf(top, cluster_ld(cluster_addr(&sh.L[rr], k)));
+          for (int k = 0; k < a.pre_splits; ++k) top = fmaxf(top, a.pre_l[k * all + row]);
+          auto add = [&](float L, const float* y) {
+            const float w = __expf(L - top);
+            sum += w;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = fmaf(w, y[i], x[i]);
+          };
+          if (top > -INFINITY) {
+            for (int k = 0; k < a.cluster; ++k) {
+              float y[4];
+              cluster_ld4(cluster_addr(&red[rr * C::kRedStride + c], k), y);
+              add(cluster_ld(cluster_addr(&sh.L[rr], k)), y);
+            }
+            for (int k = 0; k < a.pre_splits; ++k) {
+              const float4 y = *reinterpret_cast<const float4*>(a.pre_o + (k * all + row) * D + c);
+              const float z[4] = {y.x, y.y, y.z, y.w};
+              add(a.pre_l[k * all + row], z);
+            }
           }
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
           *reinterpret_cast<uint2*>(a.o + p.b * a.stride_b + h * a.stride_h +
                                     static_cast<int64_t>(qt) * a.stride_n + c) =
-              make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-          if (c == 0) a.lse[row] = logsumexp();
-        } else {
-          *reinterpret_cast<float4*>(a.part_o + (part * a.rows + r) * D + c) = x;
-          if (c == 0) a.part_l[part * a.rows + r] = logsumexp();
+              make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
+          if (c == 0) a.lse[row] = sum == 0.f ? -INFINITY : top + logf(sum);
         }
+        cluster_sync();   // the others have read this CTA's rows
+      } else {
+        for (int e = threadIdx.x; e < live * (D / 4); e += C::kThreads) {
+          const int rr = e / (D / 4), c = 4 * (e - rr * (D / 4)), r = 16 * m + rr;
+          const float4 x = *reinterpret_cast<const float4*>(&red[rr * C::kRedStride + c]);
+          if (whole) {
+            const int hl = r / a.n_q, qt = r - hl * a.n_q, h = p.h * a.group + hl;
+            const int64_t row = (static_cast<int64_t>(p.b) * a.H + h) * a.n_q + qt;
+            if (apart) {
+              const int64_t at = a.pre_splits * (static_cast<int64_t>(a.B) * a.all_rows) + row;
+              *reinterpret_cast<float4*>(a.pre_o + at * D + c) = x;
+              if (c == 0) a.pre_l[at] = logsumexp(r);
+              continue;
+            }
+            *reinterpret_cast<uint2*>(a.o + p.b * a.stride_b + h * a.stride_h +
+                                      static_cast<int64_t>(qt) * a.stride_n + c) =
+                make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+            if (c == 0) a.lse[row] = logsumexp(r);
+          } else {
+            *reinterpret_cast<float4*>(a.part_o + (part * a.rows + r) * D + c) = x;
+            if (c == 0) a.part_l[part * a.rows + r] = logsumexp(r);
+          }
+        }
+        __syncthreads();   // red (and after the last rows m, l) is free
       }
-      __syncthreads();   // red (and after the last rows m, l) is free
     }
     if (!ok) break;
     p = next;
   }
-  if (!a.by_segment && threadIdx.x == 0) a.notes[blockIdx.x] = note;
+  if (!CLUSTER && !a.by_segment && threadIdx.x == 0) a.notes[blockIdx.x] = note;
   if (!ok && mt == 0 && lane == 0) {   // let issued copies land before the CTA exits
     for (uint32_t t = issued > ST ? issued - ST : 0; t < issued; ++t)
       mbar_wait_drain(&sh.full[slot * ST + t % ST], (t / ST) & 1, a.timeout_ns);
@@ -541,7 +602,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_finish_kernel(const Paged
   if (live && threadIdx.x < kItems) write_row(a, note.b, hr, c, x, top, sum);
 }
 
-template <int D, int MT>
+template <int D, int MT, bool CLUSTER>
 cudaError_t launch_mt(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, int ctas,
                       cudaStream_t s) {
   using C = PagedCfg<D, MT>;
@@ -551,27 +612,34 @@ cudaError_t launch_mt(const CUtensorMap& tk, const CUtensorMap& tv, const PagedA
   cudaError_t e = needs_setup(set_up, &dev, &todo);
   if (e != cudaSuccess) return e;
   if (todo) {
-    e = cudaFuncSetAttribute(paged_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             C::kSmem);
+    e = cudaFuncSetAttribute(paged_kernel<D, MT, CLUSTER>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     mark_done(set_up, dev);
   }
-  return launch_pdl(paged_kernel<D, MT>, dim3(ctas), dim3(C::kThreads), C::kSmem, s, tk, tv, a);
+  if (CLUSTER)
+    return launch_clusters(paged_kernel<D, MT, CLUSTER>,
+                           dim3(static_cast<unsigned>(a.B * a.heads * a.cluster)), dim3(C::kThreads),
+                           C::kSmem, a.cluster, s, tk, tv, a);
+  return launch_pdl(paged_kernel<D, MT, CLUSTER>, dim3(ctas), dim3(C::kThreads), C::kSmem, s, tk, tv,
+                    a);
 }
 
-template <int D>
+template <int D, bool CLUSTER>
 cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, int ctas,
                      cudaStream_t s) {
-  if (a.rows <= 16) return launch_mt<D, 1>(tk, tv, a, ctas, s);
-  if (a.rows <= 32) return launch_mt<D, 2>(tk, tv, a, ctas, s);
-  return launch_mt<D, 4>(tk, tv, a, ctas, s);
+  if (a.rows <= 16) return launch_mt<D, 1, CLUSTER>(tk, tv, a, ctas, s);
+  if (a.rows <= 32) return launch_mt<D, 2, CLUSTER>(tk, tv, a, ctas, s);
+  return launch_mt<D, 4, CLUSTER>(tk, tv, a, ctas, s);
 }
 
 }  // namespace
 
 cudaError_t launch_paged(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, int ctas,
                          cudaStream_t s) {
-  return a.d == 64 ? launch_d<64>(tk, tv, a, ctas, s) : launch_d<128>(tk, tv, a, ctas, s);
+  if (a.cluster > 0)
+    return a.d == 64 ? launch_d<64, true>(tk, tv, a, ctas, s) : launch_d<128, true>(tk, tv, a, ctas, s);
+  return a.d == 64 ? launch_d<64, false>(tk, tv, a, ctas, s) : launch_d<128, false>(tk, tv, a, ctas, s);
 }
 
 cudaError_t launch_paged_merge(const PagedArgs& a, int notes, cudaStream_t s) {

@@ -35,6 +35,10 @@ struct MergeNote {
   int more;      // how many CTAs follow
 };
 
+// Where the caches are short there is nothing to balance, and the merge's own
+// launch costs as much as the keys: then a segment falls to a cluster of CTAs,
+// each takes an equal part of its tiles, and they merge through their shared
+// memory (PagedArgs::cluster > 0; the note and the partials stay unused).
 struct PagedArgs {
   int B, H, heads;                // heads: segments per sequence
   int group;                      // query heads per segment
@@ -59,6 +63,7 @@ struct PagedArgs {
   int dense;                      // a page's rows follow one another without gaps
   MergeNote* notes;               // workspace: one per segment, or one per CTA, as
   int by_segment;                 // fewer are (with a prefix always per segment)
+  int cluster;                    // CTAs of a segment's cluster; 0: the work split above
   float* part_o;                  // workspace [2 G][rows][d]
   float* part_l;                  // workspace [2 G][rows]
   // a shared prefix: its pieces' partials and, behind them, those of the
@@ -94,6 +99,8 @@ constexpr int kPagedMinUnits = 6;     // units a CTA takes at least
 constexpr int kLatentKeys = 64;       // keys per tile of the latent kernel
 constexpr int kLatentOverhead = 2;
 constexpr int kLatentMinUnits = 2;
+constexpr int kPagedClusterTiles = 24;   // tiles of a cluster's CTA at most, at full caches
+constexpr int kLatentClusterTiles = 4;
 constexpr int kLatentRows = 64;       // query rows of one CTA
 constexpr int kLatentRope = 64;       // columns of a latent vector that are not values
 
@@ -260,11 +267,47 @@ __device__ __forceinline__ PagedPiece paged_next(const PagedArgs& a, const Paged
   return paged_piece<KEYS, OVERHEAD>(a, sh, b, h, p.s + p.n + OVERHEAD);
 }
 
+// A cluster's CTA `rank`: its part of segment (b, h).
+template <int KEYS>
+__device__ __forceinline__ PagedPiece paged_part(const PagedArgs& a, int b, int h, int rank) {
+  PagedPiece p;
+  p.b = b;
+  p.h = h;
+  p.len = paged_len(a, b);
+  p.n = paged_tiles<KEYS>(a, b);
+  p.s = 0;
+  p.t0 = static_cast<int>(static_cast<int64_t>(p.n) * rank / a.cluster);
+  p.t1 = static_cast<int>(static_cast<int64_t>(p.n) * (rank + 1) / a.cluster);
+  p.valid = true;
+  return p;
+}
+
 // The note of the merge that begins with piece p.
 template <int OVERHEAD>
 __device__ __forceinline__ MergeNote paged_note(const PagedShare& sh, const PagedPiece& p) {
   return MergeNote{p.b, p.h, 2 * sh.cta + (p.s < sh.lo ? 0 : 1),
                    sh.owner(p.s + OVERHEAD + p.n - 1) - sh.cta};
+}
+
+// launch_pdl with clusters of `cluster` CTAs.
+template <typename... P, typename... A>
+inline cudaError_t launch_clusters(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
+                                   unsigned cluster, cudaStream_t s, A&&... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
 
 cudaError_t launch_paged(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, int ctas,

@@ -120,6 +120,7 @@ struct Layout {
   int ctas = 0;                            // of the decode kernel (latent: per row group)
   int n_notes = 0;                         // of merges: one per segment or per CTA
   bool by_segment = false;
+  int cluster = 0;
   int heads = 0, group = 0, rows = 0;      // segments per sequence, heads and rows of one
   int first = 0, splits = 0, tiles = 0;    // the shared prefix
 };
@@ -153,6 +154,7 @@ Layout layout(const attn_params* p, int32_t n_q, const attn_pages* g, bool laten
   const int64_t units = static_cast<int64_t>(p->B) * L.heads *
                         (tiles + (latent ? attn::kLatentOverhead : attn::kPagedOverhead));
   const int64_t want = units / (latent ? attn::kLatentMinUnits : attn::kPagedMinUnits);
+  const int64_t room = most;
   if (most > want) most = want;
   L.ctas = static_cast<int>(most < 1 ? 1 : most);
   if (L.first > 0) {
@@ -166,7 +168,17 @@ Layout layout(const attn_params* p, int32_t n_q, const attn_pages* g, bool laten
     if (k > 16) k = 16;
     L.splits = k < 1 ? 1 : static_cast<int>(k);
   }
+  // short caches: a cluster per segment, of as many CTAs as the GPU holds at
+  // once and as have a tile for each slot (latent: a tile), if that leaves each
+  // few tiles
   const int64_t segments = segments_of(p, L);
+  {
+    int c = 8;
+    while (c > 1 && (segments * c > room || c > (tiles + (latent ? 0 : 2)) / (latent ? 1 : 3))) c /= 2;
+    if (tiles <= static_cast<int64_t>(c) *
+                     (latent ? attn::kLatentClusterTiles : attn::kPagedClusterTiles))
+      L.cluster = c;
+  }
   L.by_segment = L.first > 0 || segments <= L.ctas;
   L.n_notes = L.by_segment ? static_cast<int>(segments) : L.ctas;
   size_t off = kHeaderBytes;
@@ -216,6 +228,7 @@ PagedArgs args_of(const attn_params* p, int32_t n_q, const attn_pages* g, const 
   a.lse = lse;
   a.notes = reinterpret_cast<attn::MergeNote*>(w + L.notes);
   a.by_segment = L.by_segment;
+  a.cluster = L.cluster;
   a.part_o = reinterpret_cast<float*>(w + L.part_o);
   a.part_l = reinterpret_cast<float*>(w + L.part_l);
   a.pre_splits = L.splits;
@@ -303,6 +316,7 @@ attn_status attn_decode_paged(const attn_params* p, int32_t n_q, const attn_page
     return st;
   if ((st = launched(attn::launch_paged(tk, tv, a, L.ctas, s), "paged decode launch")) != ATTN_OK)
     return st;
+  if (L.cluster > 0) return ATTN_OK;   // merged already
   if (L.first > 0) return launched(attn::launch_paged_finish(a, s), "shared prefix merge launch");
   if (L.ctas == 1) return ATTN_OK;   // one CTA cuts nothing
   return launched(attn::launch_paged_merge(a, L.n_notes, s), "paged merge launch");
@@ -335,7 +349,7 @@ attn_status attn_decode_latent(const attn_params* p, int32_t n_q, const attn_pag
   if (st != ATTN_OK) return st;
   if ((st = launched(attn::launch_latent(tc, a, L.ctas, s), "latent decode launch")) != ATTN_OK)
     return st;
-  if (L.ctas == 1) return ATTN_OK;
+  if (L.ctas == 1 || L.cluster > 0) return ATTN_OK;
   // the merge writes o, which is contiguous
   a.stride_n = p->d;
   a.stride_h = static_cast<int64_t>(n_q) * p->d;

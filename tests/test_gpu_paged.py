@@ -26,9 +26,15 @@ def ea():
     return ea
 
 
-def _table(rng, lens, page, spare=2, shared=0):
-    """A random table for these lengths: unused entries are far out of range."""
-    most = max(1, shared // page, max(-(-n // page) for n in lens)) + 1
+# A table with room for many more keys than are cached: short caches then go
+# through the balanced split of the keys instead of clusters.
+WIDE = 20000
+
+
+def _table(rng, lens, page, spare=2, shared=0, room=0):
+    """A random table for these lengths, and `room` keys: unused entries are
+    far out of range."""
+    most = max(1, shared // page, room // page, max(-(-n // page) for n in lens)) + 1
     P = sum(-(-n // page) for n in lens) + shared // page + spare
     free = list(rng.permutation(P))
     pre = [free.pop() for _ in range(shared // page)]
@@ -74,11 +80,12 @@ def _hold(o, lse, want, what=""):
     assert max_abs(lse.cpu().numpy(), L) <= L_MAX_ABS, what
 
 
-def _run(ea, lens, H, H_kv, n_q, d, page, causal=True, shared=0, seed=0, layout="hnd", scale=None):
+def _run(ea, lens, H, H_kv, n_q, d, page, causal=True, shared=0, seed=0, layout="hnd", scale=None,
+         room=0):
     rng = np.random.default_rng(seed)
     g = torch.Generator().manual_seed(seed)
     B = len(lens)
-    table, P = _table(rng, lens, page, shared=shared)
+    table, P = _table(rng, lens, page, shared=shared, room=room)
     shape = (P, H_kv, page, d)
     k, kd = _pages(g, shape, table, lens, layout)
     v, vd = _pages(g, shape, table, lens, layout)
@@ -98,14 +105,17 @@ def _run(ea, lens, H, H_kv, n_q, d, page, causal=True, shared=0, seed=0, layout=
 @pytest.mark.parametrize("H,H_kv,n_q", [(2, 2, 1), (8, 2, 1), (16, 1, 1), (6, 2, 8), (10, 2, 8),
                                          (64, 1, 1)])
 @pytest.mark.parametrize("d", [64, 128])
-def test_rows_and_widths(ea, H, H_kv, n_q, d):
-    _run(ea, [300, 1, 33, 0, 129], H, H_kv, n_q, d, 16, seed=H + d)
+@pytest.mark.parametrize("room", [0, WIDE])
+def test_rows_and_widths(ea, H, H_kv, n_q, d, room):
+    _run(ea, [300, 1, 33, 0, 129], H, H_kv, n_q, d, 16, seed=H + d, room=room)
 
 
 @pytest.mark.parametrize("page", [16, 32, 64, 128, 512])
 @pytest.mark.parametrize("causal", [True, False])
-def test_page_sizes(ea, page, causal):
-    _run(ea, [0, 1, 15, 16, 17, 31, 32, 33, 512, 513, 700], 4, 2, 3, 64, page, causal, seed=page)
+@pytest.mark.parametrize("room", [0, WIDE])
+def test_page_sizes(ea, page, causal, room):
+    _run(ea, [0, 1, 15, 16, 17, 31, 32, 33, 512, 513, 700], 4, 2, 3, 64, page, causal, seed=page,
+         room=room)
 
 
 @pytest.mark.parametrize("layout", ["nhd", "padded"])
@@ -113,8 +123,9 @@ def test_layouts(ea, layout):
     _run(ea, [200, 77], 8, 4, 1, 128, 32, layout=layout, seed=3)
 
 
-def test_empty_sequences(ea):
-    o, lse = _run(ea, [0, 0, 0], 4, 2, 2, 64, 16)
+@pytest.mark.parametrize("room", [0, WIDE])
+def test_empty_sequences(ea, room):
+    o, lse = _run(ea, [0, 0, 0], 4, 2, 2, 64, 16, room=room)
     assert torch.all(o == 0) and torch.all(torch.isneginf(lse))
 
 
@@ -135,22 +146,25 @@ def test_large_scores(ea):
     (2, 2, 2, 1, 64, 16, 16), (5, 8, 2, 1, 128, 16, 1040), (3, 4, 1, 5, 64, 64, 128),
     (40, 16, 2, 1, 128, 32, 512), (70, 8, 1, 2, 64, 256, 256), (9, 32, 1, 2, 128, 128, 2048)])
 @pytest.mark.parametrize("causal", [True, False])
-def test_shared_prefix(ea, B, H, H_kv, n_q, d, page, shared, causal):
+@pytest.mark.parametrize("room", [0, WIDE])
+def test_shared_prefix(ea, B, H, H_kv, n_q, d, page, shared, causal, room):
     rng = np.random.default_rng(B)
     lens = [int(shared + x) for x in rng.integers(n_q, 150, B)]
-    _run(ea, lens, H, H_kv, n_q, d, page, causal, shared, seed=B + d)
+    _run(ea, lens, H, H_kv, n_q, d, page, causal, shared, seed=B + d, room=room)
 
 
-def test_shared_prefix_is_all_there_is(ea):
+@pytest.mark.parametrize("room", [0, WIDE])
+def test_shared_prefix_is_all_there_is(ea, room):
     # nothing of their own; and the newest queries reach back into the prefix
-    _run(ea, [256, 256, 257, 300], 4, 2, 3, 64, 64, True, 256, seed=5)
+    _run(ea, [256, 256, 257, 300], 4, 2, 3, 64, 64, True, 256, seed=5, room=room)
 
 
 @pytest.mark.parametrize("lens", [[100, 300, 0, 513], [100, 90, 1, 0]])
-def test_sequences_shorter_than_the_prefix(ea, lens):
+@pytest.mark.parametrize("room", [0, WIDE])
+def test_sequences_shorter_than_the_prefix(ea, lens, room):
     # a sequence that ends inside the prefix attends its own keys; where all do, the rows
     # behind the longest hold NaN
-    _run(ea, lens, 4, 2, 2, 128, 64, True, 512, seed=6)
+    _run(ea, lens, 4, 2, 2, 128, 64, True, 512, seed=6, room=room)
 
 
 def test_shared_equals_unshared(ea):
@@ -167,10 +181,10 @@ def test_shared_equals_unshared(ea):
     assert (a[1] - b[1]).abs().max() <= L_MAX_ABS
 
 
-def _run_latent(ea, lens, H, n_q, d_v, page, causal=True, seed=0, scale=0.04, padded=False):
+def _run_latent(ea, lens, H, n_q, d_v, page, causal=True, seed=0, scale=0.04, padded=False, room=0):
     rng = np.random.default_rng(seed)
     g = torch.Generator().manual_seed(seed)
-    table, P = _table(rng, lens, page)
+    table, P = _table(rng, lens, page, room=room)
     D = d_v + 64
     c = _poison(torch.randn(P, page, D, generator=g).to(torch.bfloat16), table, lens, page)
     cd = c.cuda()
@@ -191,22 +205,25 @@ def _run_latent(ea, lens, H, n_q, d_v, page, causal=True, seed=0, scale=0.04, pa
 @pytest.mark.parametrize("H,n_q", [(1, 1), (16, 1), (20, 2), (33, 1), (64, 1), (65, 1), (128, 1),
                                    (24, 8)])
 @pytest.mark.parametrize("d_v", [256, 512])
-def test_latent_rows(ea, H, n_q, d_v):
-    _run_latent(ea, [130, 0, 1, 64], H, n_q, d_v, 32, seed=H)
+@pytest.mark.parametrize("room", [0, WIDE])
+def test_latent_rows(ea, H, n_q, d_v, room):
+    _run_latent(ea, [130, 0, 1, 64], H, n_q, d_v, 32, seed=H, room=room)
 
 
 @pytest.mark.parametrize("page", [16, 32, 64, 256])
 @pytest.mark.parametrize("causal", [True, False])
-def test_latent_pages(ea, page, causal):
-    _run_latent(ea, [0, 1, 15, 16, 17, 63, 64, 65, 400], 8, 3, 512, page, causal, seed=page)
+@pytest.mark.parametrize("room", [0, WIDE])
+def test_latent_pages(ea, page, causal, room):
+    _run_latent(ea, [0, 1, 15, 16, 17, 63, 64, 65, 400], 8, 3, 512, page, causal, seed=page, room=room)
 
 
 def test_latent_long_and_ragged(ea):
     _run_latent(ea, [5000, 3, 700, 0, 0, 90], 16, 1, 512, 64, seed=2)
 
 
-def test_latent_padded_pages_and_large_scores(ea):
-    _run_latent(ea, [300, 129], 16, 1, 512, 16, seed=4, scale=1.0, padded=True)
+@pytest.mark.parametrize("room", [0, WIDE])
+def test_latent_padded_pages_and_large_scores(ea, room):
+    _run_latent(ea, [300, 129], 16, 1, 512, 16, seed=4, scale=1.0, padded=True, room=room)
 
 
 def test_q_views(ea):
@@ -255,7 +272,8 @@ def test_bad_page_is_reported_and_reads_as_zeros(ea):
         ea.check()
 
 
-def test_replayed_graph_follows_lengths_and_tables(ea):
+@pytest.mark.parametrize("room", [0, WIDE])
+def test_replayed_graph_follows_lengths_and_tables(ea, room):
     """Captured once, replayed with other lengths, pages and queries."""
     g = torch.Generator().manual_seed(4)
     B, page, most = 4, 32, 12
@@ -264,7 +282,8 @@ def test_replayed_graph_follows_lengths_and_tables(ea):
     c = torch.randn(P, page, 576, generator=g).to(torch.bfloat16).cuda()
     q = torch.zeros(B, 4, 1, 64, dtype=torch.bfloat16, device="cuda")
     qc = torch.zeros(B, 8, 1, 576, dtype=torch.bfloat16, device="cuda")
-    table = torch.arange(P, dtype=torch.int32).view(B, most).cuda()
+    table = torch.full((B, max(most, room // page)), -1, dtype=torch.int32).cuda()
+    table[:, :most] = torch.arange(P).view(B, most)
     lens = torch.full((B,), page * most, dtype=torch.int32).cuda()
 
     def step():
@@ -285,7 +304,7 @@ def test_replayed_graph_follows_lengths_and_tables(ea):
         t[:, :2] = t[0, :2].clone()
         q.copy_(torch.randn(q.shape, generator=r))
         qc.copy_(torch.randn(qc.shape, generator=r))
-        table.copy_(t)
+        table[:, :most] = t.cuda()
         lens.copy_(torch.tensor(n, dtype=torch.int32))
         graph.replay()
         torch.cuda.synchronize()
