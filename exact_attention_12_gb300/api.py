@@ -32,7 +32,7 @@ def workspace(device, nbytes):
     of the process, because a CUDA graph captured earlier still holds its
     address.
     """
-    dev = torch.device(device)
+    dev = device if isinstance(device, torch.device) else torch.device(device)
     key = (dev.type, dev.index)
     t = _workspaces.get(key)
     if t is None or t.numel() < nbytes:

@@ -7,14 +7,20 @@ structure is filled and one library function called, and the workspace's size
 is asked for only when the one at hand is too small.
 """
 
-import ctypes
 import math
+import struct
 
 import torch
 
 from . import _abi
-from ._abi import AttnPages, AttnPageTable, AttnParams, check_status, lib
+from ._abi import check_status, lib
 from .api import workspace
+
+# The C structures (attn_params, attn_pages, attn_page_table) as bytes, which
+# ctypes passes as a pointer: a third of the time of filling a ctypes.Structure.
+_PARAMS = struct.Struct("@5ifif2Q2P4q2i3q3fi").pack
+_PAGES = struct.Struct("@Pq4i").pack
+_TABLE = struct.Struct("@PqPP4i").pack
 
 _ROPE = 64   # columns of a latent vector beside its d_v value columns
 
@@ -37,19 +43,20 @@ def _call(fn, size_fn, size_args, args, device, ws, what):
     if torch.cuda.current_device() != index:
         with torch.cuda.device(device):
             return _call(fn, size_fn, size_args, args, device, ws, what)
+    stream = _stream(index)
     if ws is None:
         w = workspace(device, 256)
-        st = fn(*args, w.data_ptr(), w.numel(), _stream(index))
+        st = fn(*args, w.data_ptr(), w.numel(), stream)
         if st == _abi.ATTN_ERR_WORKSPACE:
             need = size_fn(*size_args) if size_fn else 256
             if need == 0:
                 check_status(_abi.ATTN_ERR_INVALID_ARG, what)
             w = workspace(device, need)
-            st = fn(*args, w.data_ptr(), w.numel(), _stream(index))
+            st = fn(*args, w.data_ptr(), w.numel(), stream)
     else:
         if ws.device != device or not ws.is_contiguous():
             raise ValueError(f"{what}: ws must be contiguous, on the tensors' device")
-        st = fn(*args, ws.data_ptr(), ws.numel() * ws.element_size(), _stream(index))
+        st = fn(*args, ws.data_ptr(), ws.numel() * ws.element_size(), stream)
     if st:
         check_status(st, what)
 
@@ -132,13 +139,12 @@ def attention_decode_paged(q, k_pages, v_pages, page_table, cache_lens, *, scale
         raise ValueError("out must be like q")
     lse = _lse(lse, shape, device)
     table, row, width, lens = _table(page_table, cache_lens, B, device)
-    p = AttnParams(B, H, width * page_size, d, _abi.ATTN_BF16,
-                   d ** -0.5 if scale is None else scale, 1 if causal else 0, 0.0, 0, 0, lens,
-                   None, 0, qs[0], qs[1], qs[2], H_kv, 0, ks[0], ks[1], ks[2])
-    g = AttnPages(table, row, width, page_size, num_pages, shared_len)
-    c, pp, gp = lib(), ctypes.byref(p), ctypes.byref(g)
-    _call(c.attn_decode_paged, c.attn_decode_paged_workspace_size, (pp, n_q, gp),
-          (pp, n_q, gp, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(),
+    p = _PARAMS(B, H, width * page_size, d, 0, d ** -0.5 if scale is None else scale,
+                1 if causal else 0, 0.0, 0, 0, lens, 0, 0, *qs[:3], H_kv, 0, *ks[:3], 0.0, 0.0, 0.0, 0)
+    g = _PAGES(table, row, width, page_size, num_pages, shared_len)
+    c = lib()
+    _call(c.attn_decode_paged, c.attn_decode_paged_workspace_size, (p, n_q, g),
+          (p, n_q, g, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(),
            lse.data_ptr()), device, ws, "attn_decode_paged")
     return out, lse
 
@@ -171,12 +177,12 @@ def attention_decode_latent(q, c_pages, page_table, cache_lens, *, scale, d_v=51
     lse = _lse(lse, shape, device)
     cs, qs = _strides(c_pages), _strides(q)
     table, row, width, lens = _table(page_table, cache_lens, B, device)
-    p = AttnParams(B, H, width * page_size, d_v, _abi.ATTN_BF16, scale, 1 if causal else 0, 0.0, 0,
-                   0, lens, None, 0, qs[0], qs[1], qs[2], 1, 0, cs[0], cs[0], cs[1])
-    g = AttnPages(table, row, width, page_size, num_pages, 0)
-    c, pp, gp = lib(), ctypes.byref(p), ctypes.byref(g)
-    _call(c.attn_decode_latent, c.attn_decode_latent_workspace_size, (pp, n_q, gp),
-          (pp, n_q, gp, q.data_ptr(), c_pages.data_ptr(), out.data_ptr(), lse.data_ptr()), device,
+    p = _PARAMS(B, H, width * page_size, d_v, 0, scale, 1 if causal else 0, 0.0, 0, 0, lens, 0, 0,
+                *qs[:3], 1, 0, cs[0], cs[0], cs[1], 0.0, 0.0, 0.0, 0)
+    g = _PAGES(table, row, width, page_size, num_pages, 0)
+    c = lib()
+    _call(c.attn_decode_latent, c.attn_decode_latent_workspace_size, (p, n_q, g),
+          (p, n_q, g, q.data_ptr(), c_pages.data_ptr(), out.data_ptr(), lse.data_ptr()), device,
           ws, "attn_decode_latent")
     return out, lse
 
@@ -196,7 +202,7 @@ def _table_args(page_table, cache_lens, refs, page_size):
     _int32(refs, refs.device, 1, "refs")
     rows = page_table.shape[0]
     table, row, width, lens = _table(page_table, cache_lens, rows, refs.device)
-    return AttnPageTable(table, row, lens, refs.data_ptr(), rows, width, page_size, refs.shape[0])
+    return _TABLE(table, row, lens, refs.data_ptr(), rows, width, page_size, refs.shape[0])
 
 
 def _pool_args(pools, num_pages, device):
@@ -219,8 +225,7 @@ def _pool_args(pools, num_pages, device):
                 n *= size
             step = t.stride(0) if num_pages > 1 else page
         got += (t.data_ptr(), step * item, page * item)
-    # attn_pool is three 64-bit words
-    return (ctypes.c_int64 * max(1, len(got)))(*got)
+    return struct.pack(f"@{len(got)}q", *got)   # attn_pool: three 64-bit words
 
 
 def _list(t, device, what):
@@ -253,8 +258,8 @@ def pages_extend(page_table, cache_lens, refs, seqs, new_lens, *, page_size, ws=
     d, m = _list(new_lens, refs.device, "new_lens")
     if n != m:
         raise ValueError("seqs and new_lens must have the same length")
-    c, tp = lib(), ctypes.byref(t)
-    _call(c.attn_pages_extend, c.attn_pages_workspace_size, (tp, n), (tp, s, d, n), refs.device, ws,
+    c = lib()
+    _call(c.attn_pages_extend, c.attn_pages_workspace_size, (t, n), (t, s, d, n), refs.device, ws,
           "attn_pages_extend")
 
 
@@ -270,9 +275,9 @@ def pages_fork(pools, page_table, cache_lens, refs, parents, children, *, page_s
     if n != m:
         raise ValueError("parents and children must have the same length")
     new = torch.empty_like(parents)
-    c, tp = lib(), ctypes.byref(t)
-    _call(c.attn_pages_fork, c.attn_pages_workspace_size, (tp, n),
-          (tp, arr, len(pools), a, b, n, new.data_ptr()), refs.device, ws, "attn_pages_fork")
+    c = lib()
+    _call(c.attn_pages_fork, c.attn_pages_workspace_size, (t, n),
+          (t, arr, len(pools), a, b, n, new.data_ptr()), refs.device, ws, "attn_pages_fork")
     return new
 
 
@@ -280,7 +285,7 @@ def pages_free(page_table, cache_lens, refs, seqs, *, page_size, ws=None):
     """The sequences `seqs` give back their pages (see attn_pages_free)."""
     t = _table_args(page_table, cache_lens, refs, page_size)
     s, n = _list(seqs, refs.device, "seqs")
-    _call(lib().attn_pages_free, None, (), (ctypes.byref(t), s, n), refs.device, ws,
+    _call(lib().attn_pages_free, None, (), (t, s, n), refs.device, ws,
           "attn_pages_free")
 
 
@@ -291,7 +296,7 @@ def pages_compact(pools, page_table, cache_lens, refs, *, page_size, ws=None):
     t = _table_args(page_table, cache_lens, refs, page_size)
     arr = _pool_args(pools, refs.shape[0], refs.device)
     moved = torch.empty_like(refs)
-    c, tp = lib(), ctypes.byref(t)
-    _call(c.attn_pages_compact, c.attn_pages_workspace_size, (tp, 0),
-          (tp, arr, len(pools), moved.data_ptr()), refs.device, ws, "attn_pages_compact")
+    c = lib()
+    _call(c.attn_pages_compact, c.attn_pages_workspace_size, (t, 0),
+          (t, arr, len(pools), moved.data_ptr()), refs.device, ws, "attn_pages_compact")
     return moved

@@ -43,6 +43,19 @@ def test_struct_layouts(abi, tmp_path, cls, name):
         assert int(got[n]) == getattr(c, n).offset, n
 
 
+@pytest.mark.parametrize("fmt,cls", [("_PARAMS", "AttnParams"), ("_PAGES", "AttnPages"),
+                                     ("_TABLE", "AttnPageTable")])
+def test_packed_structures_are_the_declared_ones(abi, fmt, cls):
+    # the binding packs the structures as bytes: the same as the ctypes mirror filled in order
+    from exact_attention_12_gb300 import paged as binding
+    c = getattr(abi, cls)
+    values = [float(i + 1) if t is ctypes.c_float else i + 1 for i, (_, t) in enumerate(c._fields_)]
+    got = getattr(binding, fmt)(*values)
+    assert len(got) == ctypes.sizeof(c)
+    s = c.from_buffer_copy(got)
+    assert [getattr(s, n) for n, _ in c._fields_] == values
+
+
 def _decode(abi, latent=False, **kw):
     p, g = abi.AttnParams(), abi.AttnPages()
     d = 512 if latent else 64
