@@ -51,9 +51,20 @@ struct PrefixCfg {
                 "register re-split exceeds the launch allocation");
 };
 
+// 16 bytes global -> shared, asynchronously; zeros where nothing is `there`.
+__device__ __forceinline__ void copy16_async(void* dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(there ? 16 : 0)
+               : "memory");
+}
+
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 template <int ST>
 struct PrefixCtl {
-  uint64_t qfull, kfull[ST], vfull[ST], kvempty[ST];
+  uint64_t qfull, kfull[ST], vfull[ST], kempty[ST], vempty[ST];
   uint64_t sfull[2], pfull[2], done, final_bar;
   uint32_t tmem_base;
   int abort_flag;
@@ -73,7 +84,8 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
   uint8_t* sV = sK + ST * C::kTileBytes;
   __shared__ PrefixCtl<ST> ctl;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+  const int lane = threadIdx.x & 31;
   const int hk = blockIdx.x % a.H_kv, pair = blockIdx.x / a.H_kv, piece = blockIdx.y;
   const int r0 = pair * 2 * kTile;
   const bool two = r0 + kTile < a.rows;   // there is a second query tile
@@ -86,7 +98,8 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
     for (int s = 0; s < ST; ++s) {
       mbar_init(&ctl.kfull[s], 1);
       mbar_init(&ctl.vfull[s], 1);
-      mbar_init(&ctl.kvempty[s], 1);
+      mbar_init(&ctl.kempty[s], 1);
+      mbar_init(&ctl.vempty[s], 1);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&ctl.sfull[x], 1);
@@ -105,7 +118,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
   tc_fence_after();
   grid_dep_wait();
   grid_dep_launch();
-  const uint32_t tmem = ctl.tmem_base;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.tmem_base, 0);
   const WaitCtx wc{&ctl.abort_flag, a.status, a.timeout_ns};
   const int wg = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) / 128, 0);
 
@@ -130,9 +143,10 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         const bool mine = lane < parts && key < end;   // this lane's page of the tile
         int page = 0;
         if (mine) page = checked_page(a.table[key >> a.page_shift], a.num_pages, a.status);
-        if (t >= ST &&
-            !(ok = __all_sync(0xffffffffu, mbar_wait(&ctl.kvempty[s], ((t / ST) - 1) & 1, wc,
-                                                     kSitePrefixFree))))
+        // (the keys are free once both tiles' scores are complete, a tile's
+        // products before the values)
+        if (t >= ST && !(ok = __all_sync(0xffffffffu, mbar_wait(&ctl.kempty[s], ((t / ST) - 1) & 1, wc,
+                                                                kSitePrefixFree))))
           break;
         uint8_t* dk = sK + s * C::kTileBytes;
         uint8_t* dv = sV + s * C::kTileBytes;
@@ -147,6 +161,9 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
             tma_load_4d(dk + x * C::kBoxBytes + lane * rows * 128, &tk, &ctl.kfull[s], x * 64, row,
                         hk, page);
         }
+        if (t >= ST && !(ok = __all_sync(0xffffffffu, mbar_wait(&ctl.vempty[s], ((t / ST) - 1) & 1, wc,
+                                                                kSitePrefixFree))))
+          break;
         // value rows past `end` that no copy writes are zeroed before the
         // barrier's arrive, those inside a copied page after the copy (below)
         if (copies < parts) {
@@ -172,6 +189,9 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
           mbar_wait_drain(&ctl.kfull[u % ST], (u / ST) & 1, a.timeout_ns);
           mbar_wait_drain(&ctl.vfull[u % ST], (u / ST) & 1, a.timeout_ns);
         }
+        // (tile t's keys perhaps, which have gone out when kempty was passed)
+        if (mbar_test(&ctl.kempty[t % ST], ((t / ST) - 1) & 1))
+          mbar_wait_drain(&ctl.kfull[t % ST], (t / ST) & 1, a.timeout_ns);
       }
     } else if (warp == 9) {
       // ------------------------------------------------------- MMA issue
@@ -181,26 +201,35 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
       for (int o = 16; o > 0; o >>= 1) end = max(end, __shfl_xor_sync(0xffffffffu, end, o));
       end = min(end, a.shared_len);
       const int rows = min(kTile, 1 << a.page_shift);
+      // One elected lane issues, in code that the whole warp runs, so that the
+      // descriptors stay in uniform registers: a group of eight MMAs goes out
+      // in 520 cycles instead of 900, which had bound the kernel.
       constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);
       constexpr uint32_t kIdO = idesc_bf16(128, D, false, true);
+      const bool one = elect_one_lane();
       auto scores = [&](int x, int s) {
         const uint64_t dq = smem_desc(smem_u32(sQ + x * C::kTileBytes), 16, 1024);
         const uint64_t dk = smem_desc(smem_u32(sK + s * C::kTileBytes), 16, 1024);
+        if (one) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t off = static_cast<uint64_t>(((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4);
-          mma_ss(tmem + C::kSCol + 128 * x, dq + off, dk + off, kIdS, kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t off = static_cast<uint64_t>(((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4);
+            mma_ss(tmem + C::kSCol + 128 * x, dq + off, dk + off, kIdS, kk > 0 ? 1u : 0u);
+          }
+          mma_commit(&ctl.sfull[x]);
         }
-        mma_commit(&ctl.sfull[x]);
       };
-      // the whole warp walks the tiles (it zeroes value rows); lane 0 issues
+      // the whole warp walks the tiles (it zeroes value rows)
       const int tiles_x[2] = {n, two ? n : 0};
       bool ok = n == 0 || __all_sync(0xffffffffu, mbar_wait(&ctl.qfull, 0, wc, kSitePrefixQ));
       if (ok && n > 0) {
         ok = __all_sync(0xffffffffu, mbar_wait(&ctl.kfull[0], 0, wc, kSitePrefixK));
         tc_fence_after();
-        if (ok && lane == 0)
-          for (int x = 0; x < (two ? 2 : 1); ++x) scores(x, 0);
+        if (ok) {
+          scores(0, 0);
+          if (two) scores(1, 0);
+          if (one) mma_commit(&ctl.kempty[0]);
+        }
       }
       for (int t = 0; ok && t < n; ++t) {
         const int s = t % ST, s1 = (t + 1) % ST;
@@ -227,13 +256,13 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
           ok = __all_sync(0xffffffffu, mbar_wait(&ctl.pfull[x], t & 1, wc, kSitePrefixP));
           if (!ok) break;
           tc_fence_after();
-          if (lane == 0) {   // O_X += P_X V
-            const uint64_t dv = smem_desc(smem_u32(sV + s * C::kTileBytes), C::kBoxBytes, 1024);
+          const uint64_t dv = smem_desc(smem_u32(sV + s * C::kTileBytes), C::kBoxBytes, 1024);
+          if (one) {   // O_X += P_X V
 #pragma unroll
             for (int kk = 0; kk < kTile / 16; ++kk)
               mma_ts(tmem + C::kOCol + D * x, tmem + C::kSCol + 128 * x + kk * 8,
                      dv + static_cast<uint64_t>((kk * 2048) >> 4), kIdO, t > 0 || kk > 0 ? 1u : 0u);
-            if (x == (two ? 1 : 0)) mma_commit(&ctl.kvempty[s]);
+            if (x == (two ? 1 : 0)) mma_commit(&ctl.vempty[s]);
           }
           if (more) {
             if (!k_ready) {
@@ -242,11 +271,12 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
               if (!ok) break;
               tc_fence_after();
             }
-            if (lane == 0) scores(x, s1);   // S_X of the next key tile
+            scores(x, s1);   // S_X of the next key tile
+            if (one && x == (two ? 1 : 0)) mma_commit(&ctl.kempty[s1]);
           }
         }
       }
-      if (lane == 0) {
+      if (one) {
         if (ok) mma_commit(&ctl.done);
         mma_commit(&ctl.final_bar);   // every MMA of this CTA done before TMEM is freed
         mbar_wait_drain(&ctl.final_bar, 0, a.timeout_ns);
@@ -265,13 +295,21 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
     const int rem = live ? r - b * per : 0;
     const int hl = rem / a.n_q, qt = rem - hl * a.n_q, h = hk * a.group + hl;
     {
-      const uint4* src = reinterpret_cast<const uint4*>(a.q + b * a.stride_b + h * a.stride_h +
-                                                        static_cast<int64_t>(qt) * a.stride_n);
-      uint8_t* dst = sQ + x * C::kTileBytes + row * 128;
+      // the warp's 32 rows, kPerRow lanes a row (asynchronous copies: all are
+      // in flight together); rows past the last are zero
+      constexpr int kPerRow = D / 8, kAtOnce = 32 / kPerRow;
+      const int64_t mine = b * a.stride_b + h * a.stride_h + static_cast<int64_t>(qt) * a.stride_n;
+      uint8_t* dst = sQ + x * C::kTileBytes + (warp & 3) * 32 * 128;
+      const int c8 = lane % kPerRow;
 #pragma unroll
-      for (int c8 = 0; c8 < D / 8; ++c8)
-        *reinterpret_cast<uint4*>(dst + (c8 >> 3) * C::kBoxBytes + (((c8 & 7) ^ (row & 7)) << 4)) =
-            live ? src[c8] : make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < kPerRow; ++i) {
+        const int rr = i * kAtOnce + lane / kPerRow;
+        const int64_t from = __shfl_sync(0xffffffffu, mine, rr);
+        const bool there = __shfl_sync(0xffffffffu, live ? 1 : 0, rr) != 0;
+        copy16_async(dst + (c8 >> 3) * C::kBoxBytes + rr * 128 + (((c8 & 7) ^ (rr & 7)) << 4),
+                     a.q + from + c8 * 8, there);
+      }
+      copies_wait();
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.qfull);
@@ -372,6 +410,14 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
     const float inv = some ? 1.f / l_sum : 0.f;
     const int64_t rows_all = static_cast<int64_t>(a.B) * a.H * a.n_q;
     const int64_t out = piece * rows_all + (static_cast<int64_t>(b) * a.H + h) * a.n_q + qt;
+    // O through shared memory (q, k, v are done with), so that a row goes out in
+    // one piece: a thread's own stores of its row had taken 5 us
+    constexpr int kStride = D + 4;   // floats; the pad spreads the rows over the banks
+    static_assert(256 * kStride * 4 <= C::kSmem - 1024, "O fits where the operands were");
+    float* mine_o = reinterpret_cast<float*>(smem) + warp * 32 * kStride;
+    // (every warp of the two groups is past its last use of them: `done` covers
+    // the products; a group without a tile has none)
+    named_barrier_sync(1, 256);
 #pragma unroll
     for (int c = 0; c < D; c += 32) {
       uint32_t o[32];
@@ -379,15 +425,24 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         tmem_ld32(oc + c, o);
         tmem_wait_ld();
       }
-      if (live) {
-        float4* dst = reinterpret_cast<float4*>(a.pre_o + out * D + c);
+      float4* dst = reinterpret_cast<float4*>(mine_o + lane * kStride + c);
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-          dst[u] = mine > 0 && some
-                       ? make_float4(__uint_as_float(o[4 * u]) * inv, __uint_as_float(o[4 * u + 1]) * inv,
-                                     __uint_as_float(o[4 * u + 2]) * inv, __uint_as_float(o[4 * u + 3]) * inv)
-                       : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
+      for (int u = 0; u < 8; ++u)
+        dst[u] = mine > 0 && some
+                     ? make_float4(__uint_as_float(o[4 * u]) * inv, __uint_as_float(o[4 * u + 1]) * inv,
+                                   __uint_as_float(o[4 * u + 2]) * inv, __uint_as_float(o[4 * u + 3]) * inv)
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    __syncwarp();
+    constexpr int kLanes = D / 4;   // float4 lanes a row
+#pragma unroll 4
+    for (int i = 0; i < kLanes; ++i) {
+      const int rr = i * (32 / kLanes) + lane / kLanes, c = lane % kLanes;
+      const int64_t to = __shfl_sync(0xffffffffu, out, rr);
+      const bool there = __shfl_sync(0xffffffffu, live ? 1 : 0, rr) != 0;
+      if (there)
+        *reinterpret_cast<float4*>(a.pre_o + to * D + 4 * c) =
+            *reinterpret_cast<const float4*>(mine_o + rr * kStride + 4 * c);
     }
     if (live) a.pre_l[out] = some ? fmaf(m_used, a.scale, logf(l_sum)) : -INFINITY;
   }
