@@ -27,7 +27,6 @@ using namespace sm103;
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanBatch = kPlanThreads * 32;            // pages looked at together
 constexpr int kCopyThreads = 256;
 constexpr int kCopyBytes = kCopyThreads * 16 * 4;        // a copy piece
 constexpr int kPoolsPerLaunch = 64;
@@ -98,37 +97,48 @@ __device__ __forceinline__ T block_rank(T x, T* scratch, T* total) {
   return before + inc - x;
 }
 
-// Which of the 32 pages from base + 32 * thread on are in use (a bit each; 0
-// past the last page).  The warp reads its 1024 counts in order, 32 at a time.
-__device__ __forceinline__ uint32_t used_mask(const Table& t, int base) {
-  const int lane = threadIdx.x & 31, first = base + (threadIdx.x >> 5) * 1024;
-  uint32_t mask = 0;
-  if (first >= t.num_pages) return 0;   // (uniform over the warp)
-#pragma unroll 16
-  for (int k = 0; k < 32; ++k) {
-    const int i = first + 32 * k + lane;
-    const uint32_t word = __ballot_sync(0xffffffffu, i < t.num_pages && t.refs[i] != 0);
-    if (lane == k) mask = word;
+// The pages that a plan looks at together: a warp has `words` runs of 32 (up to
+// 32 of them, so that all warps have their share of a small cache), lane l of
+// it run l.
+struct Batch {
+  int words;
+  __device__ explicit Batch(int num_pages)
+      : words(min(32, (num_pages + kPlanThreads - 1) / kPlanThreads)) {}
+  __device__ int size() const { return kPlanThreads * words; }
+  // The first page of this thread's run, if it has one.
+  __device__ int first(int base) const {
+    return base + 32 * (static_cast<int>(threadIdx.x >> 5) * words + static_cast<int>(threadIdx.x & 31));
   }
-  return mask;
-}
-
-// The bits of a thread's 32 pages that lie below page `end`.
-__device__ __forceinline__ uint32_t below(int base, int end) {
-  const int n = end - base - 32 * static_cast<int>(threadIdx.x);
-  return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
-}
+  // Which of its pages are in use, a bit each (0 past the last page).  The warp
+  // reads its counts in order, 32 at a time.
+  __device__ uint32_t used(const Table& t, int base) const {
+    const int lane = threadIdx.x & 31, start = base + 32 * static_cast<int>(threadIdx.x >> 5) * words;
+    uint32_t mask = 0;
+#pragma unroll 8
+    for (int k = 0; k < words; ++k) {
+      const int i = start + 32 * k + lane;
+      const uint32_t word = __ballot_sync(0xffffffffu, i < t.num_pages && t.refs[i] != 0);
+      if (lane == k) mask = word;
+    }
+    return mask;
+  }
+  // The bits of its pages that lie below page `end`.
+  __device__ uint32_t below(int base, int end) const {
+    const int n = static_cast<int>(threadIdx.x & 31) < words ? end - first(base) : 0;
+    return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
+  }
+};
 
 // The lowest `need` free pages into `list`, ascending; how many there are (at
 // most `need`).  The whole block.
 __device__ int lowest_free(const Table& t, int need, int32_t* list, int* scratch) {
+  const Batch batch(t.num_pages);
   int found = 0;
-  for (int base = 0; base < t.num_pages && found < need; base += kPlanBatch) {
-    uint32_t free = ~used_mask(t, base) & below(base, t.num_pages);
+  for (int base = 0; base < t.num_pages && found < need; base += batch.size()) {
+    uint32_t free = ~batch.used(t, base) & batch.below(base, t.num_pages);
     int total;
     int at = found + block_rank(__popc(free), scratch, &total);
-    for (; free != 0 && at < need; free &= free - 1)
-      list[at++] = base + 32 * static_cast<int>(threadIdx.x) + __ffs(free) - 1;
+    for (; free != 0 && at < need; free &= free - 1) list[at++] = batch.first(base) + __ffs(free) - 1;
     found += total;
   }
   __syncthreads();   // list is visible to the block
@@ -359,20 +369,22 @@ __global__ void __launch_bounds__(kPlanThreads)
   __shared__ int scratch[33];
   __shared__ uint32_t ranks[33];
   const int P = t.num_pages;
+  const Batch batch(P);
   int used = 0;
   uint32_t mask = 0;   // (of the only batch, where there is one)
-  for (int base = 0; base < P; base += kPlanBatch) {
-    mask = used_mask(t, base);
+  for (int base = 0; base < P; base += batch.size()) {
+    mask = batch.used(t, base);
     int total;
     block_rank(__popc(mask), scratch, &total);
     used += total;
   }
   const int lane = threadIdx.x & 31;
   int n_holes = 0, n_movers = 0;
-  for (int base = 0; base < P; base += kPlanBatch) {
-    if (P > kPlanBatch) mask = used_mask(t, base);
-    const int i0 = base + 32 * static_cast<int>(threadIdx.x);
-    uint32_t hole = ~mask & below(base, used), mover = mask & ~below(base, used);
+  for (int base = 0; base < P; base += batch.size()) {
+    if (P > batch.size()) mask = batch.used(t, base);
+    const int i0 = batch.first(base);
+    const uint32_t low = batch.below(base, used);
+    uint32_t hole = ~mask & low, mover = mask & ~low;
     // both ranks in one scan: the counts of a batch fit 16 bits each
     uint32_t total;
     const uint32_t rank = block_rank(
@@ -383,13 +395,12 @@ __global__ void __launch_bounds__(kPlanThreads)
     for (; mover != 0; mover &= mover - 1) movers[at++] = i0 + __ffs(mover) - 1;
     n_holes += static_cast<int>(total & 0xffffu);
     n_movers += static_cast<int>(total >> 16);
-    const int first = base + (threadIdx.x >> 5) * 1024;
-    if (first < P)
-      for (int k = 0; k < 32; ++k) {
-        const uint32_t word = __shfl_sync(0xffffffffu, mask, k);
-        const int i = first + 32 * k + lane;
-        if (i < P) moved[i] = (word >> lane) & 1u ? i : -1;
-      }
+    const int start = base + 32 * static_cast<int>(threadIdx.x >> 5) * batch.words;
+    for (int k = 0; k < batch.words; ++k) {
+      const uint32_t word = __shfl_sync(0xffffffffu, mask, k);
+      const int i = start + 32 * k + lane;
+      if (i < P) moved[i] = (word >> lane) & 1u ? i : -1;
+    }
   }
   __syncthreads();
   for (int i = threadIdx.x; i < n_movers; i += kPlanThreads) {
