@@ -37,6 +37,15 @@
 // P is rounded to bf16 for the second product (relative 2^-8 per element);
 // m, l, O are fp32.  Rows past the end of a sequence are zeroed in shared
 // memory before they are used as values (0 * NaN is NaN).
+//
+// Measured (d_v = 512, whole steps replayed from a CUDA graph): up to 64 rows
+// the kernel streams at the copy rate once it runs (16 sequences, 16 heads:
+// 16384 more tokens each cost 44 us = 6.8 TB/s); what remains is 12 us of
+// set-up, first and last tiles and the merge (4096 tokens each: 27 us).  With
+// 128 rows each tile is worked on by two CTAs, and shared memory bounds it: a
+// tile's operand reads, its copy and P take 2600 cycles of its bandwidth, its
+// MMAs 2000, and a tile takes 3200 (64 sequences of 4096-8192 tokens: 175 us,
+// where the tokens' bytes need 69 and the operations 58).
 #include "attn_paged.cuh"
 
 namespace attn {
@@ -90,24 +99,6 @@ struct __align__(1024) LatentCtl {
   uint32_t tmem_base;
   int abort_flag;
 };
-
-// 16 bytes global -> shared, asynchronously.
-__device__ __forceinline__ void copy16_async(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)),
-               "l"(reinterpret_cast<uint64_t>(src))
-               : "memory");
-}
-
-// `bytes` (a multiple of 16) at a 16-byte aligned address into L2.
-__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(src)),
-               "r"(bytes)
-               : "memory");
-}
-
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_all;" ::: "memory");
-}
 
 // 16 TMEM lanes x 32 columns: thread 4 g + q receives, for i = 0 .. 15, row
 // g + 8 ((i / 2) mod 2), column 8 (i / 4) + 2 q + i mod 2.
@@ -394,7 +385,7 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
                                    static_cast<int64_t>(qt) * a.stride_n;
         for (int c = lane; c < C::kBoxes * 8; c += 32)
           copy16_async(sQ + (c >> 3) * C::kBoxBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-                       src + c * 8);
+                       src + c * 8, true);
       }
     };
     load_q(p);
@@ -503,8 +494,9 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
                   ex2_approx(fmaf(__uint_as_float(sr[4 * b + 2 * e + 1]), c2, -mc[2 * b + 1]));
               l[2 * b] += p0;
               l[2 * b + 1] += p1;
-              *reinterpret_cast<uint32_t*>(sC + (T % ST) * C::kTileBytes + C::kPOffset + row * 128 + (((4 * half + b) ^ (row & 7)) << 4) +
-                                           4 * q4) = pack_bf16x2(p0, p1);
+              *reinterpret_cast<uint32_t*>(sC + (T % ST) * C::kTileBytes + C::kPOffset + row * 128 +
+                                           (((4 * half + b) ^ (row & 7)) << 4) + 4 * q4) =
+                  pack_bf16x2(p0, p1);
             }
           }
           fence_proxy_async_smem();

