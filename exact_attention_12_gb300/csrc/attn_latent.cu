@@ -20,10 +20,13 @@
 // because the other way round the accumulator of 128 rows x 512 columns would
 // fill TMEM, and q alone would take 147 KB of shared memory.  So O^T takes
 // d_v / 128 * 64 TMEM columns, q 72 KB, and two 64-key tiles of 72 KB are in
-// flight, each read from global memory once and used as both operands.  H * n_q rows are cut into groups of 64; the CTAs
-// of a sequence's groups run side by side on the same keys, so that the
-// second read of a tile finds it in L2.  The keys are divided over the CTAs
-// as in the paged decode step.
+// flight, each used as both operands.  H * n_q rows are cut into groups of 64;
+// the CTAs of a sequence's groups run side by side on the same keys.  Where
+// the groups are even in number, two of them form a cluster, and each copies
+// half of a tile's value columns into both (multicast), which halves what L2
+// has to deliver; a column group's place is free again when both are done with
+// it (64 sequences of 4096-8192 tokens, 128 heads: 177 -> 169 us).  The keys
+// are divided over the CTAs as in the paged decode step.
 //   warps 0-7  load q; softmax of 16 keys x 32 columns each, in the MMA's
 //              fragment layout; the sums stay in registers, a partial per
 //              thread, until the end; rescale O^T when some column's max has
@@ -44,7 +47,7 @@
 // set-up, first and last tiles and the merge (4096 tokens each: 27 us).  With
 // 128 rows each tile is worked on by two CTAs, and shared memory bounds it: a
 // tile's operand reads, its copy and P take 2600 cycles of its bandwidth, its
-// MMAs 2000, and a tile takes 3200 (64 sequences of 4096-8192 tokens: 175 us,
+// MMAs 2000, and a tile takes 3000 (64 sequences of 4096-8192 tokens: 169 us,
 // where the tokens' bytes need 69 and the operations 58).
 #include "attn_paged.cuh"
 
@@ -112,11 +115,18 @@ __device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t* r) {
       : "r"(taddr));
 }
 
-// CLUSTER: a sequence per cluster (a.cluster CTAs), else the balanced split.
-template <int DV, bool CLUSTER>
+// How a launch uses clusters.
+//   kAlone  none: the balanced split
+//   kPair   the balanced split, two row groups of the same tiles a cluster: each
+//           CTA copies half of a tile's value columns into both
+//   kSeq    a sequence per cluster (a.cluster CTAs)
+enum LatentMode { kAlone, kPair, kSeq };
+
+template <int DV, LatentMode MODE>
 __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
     latent_kernel(const __grid_constant__ CUtensorMap tc, const PagedArgs a, int groups) {
   using C = LatentCfg<DV>;
+  constexpr bool CLUSTER = MODE == kSeq, PAIR = MODE == kPair;
   constexpr int ST = C::kStages, KT = kLatentKeys;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ LatentCtl<ST> ctl;
@@ -136,7 +146,7 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
   const int unit = CLUSTER ? blockIdx.x / a.cluster : blockIdx.x;
   const int r0 = unit % groups * kLatentRows;   // first query row
   const int cta = unit / groups, ctas = gridDim.x / groups;
-  const int rank = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
+  const int rank = MODE == kAlone ? 0 : static_cast<int>(cluster_rank());
   const int live = min(kLatentRows, a.all_rows - r0);
 
   if (threadIdx.x == 0) {
@@ -144,7 +154,8 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
     for (int s = 0; s < ST; ++s)
       for (int x = 0; x < C::kGroups; ++x) {
         mbar_init(&ctl.full[s][x], 1);
-        mbar_init(&ctl.empty[s][x], 1);
+        // (a pair's value columns are free when both CTAs are done with them)
+        mbar_init(&ctl.empty[s][x], PAIR && x > 0 ? 2 : 1);
       }
     mbar_init(&ctl.sfull[0], 1);
     mbar_init(&ctl.sfull[1], 1);
@@ -169,6 +180,7 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();   // the other CTA's barriers are ready
   tc_fence_after();
   grid_dep_wait();
   grid_dep_launch();
@@ -238,10 +250,16 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
           const int box = x == 0 ? C::kBoxes - 1 : 2 * (x - 1), boxes = x == 0 ? 1 : 2;
           if (lane == 0) mbar_arrive_expect_tx(&ctl.full[s][x], boxes * C::kBoxBytes);
           __syncwarp();
-          if (lane < parts)
+          if (PAIR && x > 0) {
+            if (lane < parts)
+              tma_load_4d_multicast(
+                  sC + s * C::kTileBytes + (box + rank) * C::kBoxBytes + lane * rows * 128, &tc,
+                  &ctl.full[s][x], (box + rank) * 64, at & ((1 << a.page_shift) - 1), 0, page, 3);
+          } else if (lane < parts) {
             for (int k = box; k < box + boxes; ++k)
               tma_load_4d(sC + s * C::kTileBytes + k * C::kBoxBytes + lane * rows * 128, &tc,
                           &ctl.full[s][x], k * 64, at & ((1 << a.page_shift) - 1), 0, page);
+          }
         }
         if (!ok) break;
         // (a CTA's first tiles themselves go out before any of this)
@@ -343,7 +361,8 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
               const uint64_t off = static_cast<uint64_t>((kk * 2048) >> 4);
               mma_ss(tmem + C::kOCol + 64 * blk, dv + off, dp + off, kIdO, i > 0 || kk > 0 ? 1u : 0u);
             }
-            mma_commit(&ctl.empty[s][1 + blk]);
+            if constexpr (PAIR) mma_commit_multicast(&ctl.empty[s][1 + blk], 3);
+            else mma_commit(&ctl.empty[s][1 + blk]);
           }
         }
         if (one) {
@@ -630,6 +649,10 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
     cluster_sync();   // the others have read this CTA's rows
   }
 
+  if constexpr (PAIR) {   // neither CTA leaves while the other's copies or commits may come
+    __syncwarp();
+    cluster_sync();
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == 9) {
@@ -638,7 +661,7 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
   }
 }
 
-template <int DV, bool CLUSTER>
+template <int DV, LatentMode MODE>
 cudaError_t launch_dv(const CUtensorMap& tc, const PagedArgs& a, int ctas, cudaStream_t s) {
   using C = LatentCfg<DV>;
   static std::atomic<uint64_t> set_up{0};
@@ -647,30 +670,36 @@ cudaError_t launch_dv(const CUtensorMap& tc, const PagedArgs& a, int ctas, cudaS
   cudaError_t e = needs_setup(set_up, &dev, &todo);
   if (e != cudaSuccess) return e;
   if (todo) {
-    e = cudaFuncSetAttribute(latent_kernel<DV, CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(latent_kernel<DV, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              C::kSmem);
     if (e != cudaSuccess) return e;
     // the register re-split inside the kernel assumes the launch allocation
     cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, latent_kernel<DV, CLUSTER>)) != cudaSuccess) return e;
+    if ((e = cudaFuncGetAttributes(&fa, latent_kernel<DV, MODE>)) != cudaSuccess) return e;
     if (static_cast<uint32_t>(fa.numRegs) < C::kRegsLaunch) return cudaErrorInvalidConfiguration;
     mark_done(set_up, dev);
   }
   const int groups = a.rows / kLatentRows;
-  if (CLUSTER)
-    return launch_clusters(latent_kernel<DV, CLUSTER>,
+  if (MODE == kSeq)
+    return launch_clusters(latent_kernel<DV, MODE>,
                            dim3(static_cast<unsigned>(a.B * groups * a.cluster)), dim3(C::kThreads),
                            C::kSmem, a.cluster, s, tc, a, groups);
-  return launch_pdl(latent_kernel<DV, CLUSTER>, dim3(ctas * groups), dim3(C::kThreads), C::kSmem, s,
+  if (MODE == kPair)
+    return launch_clusters(latent_kernel<DV, MODE>, dim3(ctas * groups), dim3(C::kThreads), C::kSmem,
+                           2, s, tc, a, groups);
+  return launch_pdl(latent_kernel<DV, MODE>, dim3(ctas * groups), dim3(C::kThreads), C::kSmem, s,
                     tc, a, groups);
 }
 
 }  // namespace
 
 cudaError_t launch_latent(const CUtensorMap& tc, const PagedArgs& a, int ctas, cudaStream_t s) {
+  const bool wide = a.d == 512;
   if (a.cluster > 0)
-    return a.d == 256 ? launch_dv<256, true>(tc, a, ctas, s) : launch_dv<512, true>(tc, a, ctas, s);
-  return a.d == 256 ? launch_dv<256, false>(tc, a, ctas, s) : launch_dv<512, false>(tc, a, ctas, s);
+    return wide ? launch_dv<512, kSeq>(tc, a, ctas, s) : launch_dv<256, kSeq>(tc, a, ctas, s);
+  if (a.rows / kLatentRows % 2 == 0)
+    return wide ? launch_dv<512, kPair>(tc, a, ctas, s) : launch_dv<256, kPair>(tc, a, ctas, s);
+  return wide ? launch_dv<512, kAlone>(tc, a, ctas, s) : launch_dv<256, kAlone>(tc, a, ctas, s);
 }
 
 }  // namespace attn

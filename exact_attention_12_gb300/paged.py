@@ -68,13 +68,15 @@ def _int32(t, device, dim, what):
                          "contiguous along its last axis")
 
 
-def _table(table, cache_lens, B, device):
+def _table(table, cache_lens, B, device, page_size):
     """Pointers, row stride and width of a page table with B rows."""
     _int32(table, device, 2, "page_table")
     _int32(cache_lens, device, 1, "cache_lens")
     rows, width = table.shape
     if rows != B or cache_lens.shape[0] != B:
         raise ValueError("page_table and cache_lens must have a row per sequence")
+    if width * page_size > 1 << 30:
+        raise ValueError("page_table: more than 2^30 keys per row")
     return table.data_ptr(), (table.stride(0) if rows > 1 else width), width, cache_lens.data_ptr()
 
 
@@ -138,7 +140,7 @@ def attention_decode_paged(q, k_pages, v_pages, page_table, cache_lens, *, scale
             or out.device != device:
         raise ValueError("out must be like q")
     lse = _lse(lse, shape, device)
-    table, row, width, lens = _table(page_table, cache_lens, B, device)
+    table, row, width, lens = _table(page_table, cache_lens, B, device, page_size)
     p = _PARAMS(B, H, width * page_size, d, 0, d ** -0.5 if scale is None else scale,
                 1 if causal else 0, 0.0, 0, 0, lens, 0, 0, *qs[:3], H_kv, 0, *ks[:3], 0.0, 0.0, 0.0, 0)
     g = _PAGES(table, row, width, page_size, num_pages, shared_len)
@@ -176,7 +178,7 @@ def attention_decode_latent(q, c_pages, page_table, cache_lens, *, scale, d_v=51
         raise ValueError("out must be a contiguous bf16 [B, H, n_q, d_v] on q's device")
     lse = _lse(lse, shape, device)
     cs, qs = _strides(c_pages), _strides(q)
-    table, row, width, lens = _table(page_table, cache_lens, B, device)
+    table, row, width, lens = _table(page_table, cache_lens, B, device, page_size)
     p = _PARAMS(B, H, width * page_size, d_v, 0, scale, 1 if causal else 0, 0.0, 0, 0, lens, 0, 0,
                 *qs[:3], 1, 0, cs[0], cs[0], cs[1], 0.0, 0.0, 0.0, 0)
     g = _PAGES(table, row, width, page_size, num_pages, 0)
@@ -201,7 +203,7 @@ def _lse(lse, shape, device):
 def _table_args(page_table, cache_lens, refs, page_size):
     _int32(refs, refs.device, 1, "refs")
     rows = page_table.shape[0]
-    table, row, width, lens = _table(page_table, cache_lens, rows, refs.device)
+    table, row, width, lens = _table(page_table, cache_lens, rows, refs.device, page_size)
     return _TABLE(table, row, lens, refs.data_ptr(), rows, width, page_size, refs.shape[0])
 
 

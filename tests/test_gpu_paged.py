@@ -240,6 +240,39 @@ def test_q_views(ea):
     _hold(o, lse, oracle.paged_decode(np64(q), np64(k), np64(v), table, lens, 0.125))
 
 
+def test_caches_beyond_32_bit_offsets(ea):
+    # pages whose elements lie past 2^31; all but the used ones hold whatever was there
+    g = torch.Generator().manual_seed(9)
+    P, page = 270000, 64
+    pool = torch.empty(P, 1, page, 128, dtype=torch.bfloat16, device="cuda")   # 4.4 GB
+    used = [P - 1, 0, P - 2, 262144, 131072, P // 2]
+    x = torch.randn(6, 1, page, 128, generator=g).to(torch.bfloat16)
+    pool[torch.tensor(used).cuda()] = x.cuda()
+    table = torch.tensor([used[:3], used[3:]], dtype=torch.int32)
+    small = np.array([[0, 1, 2], [3, 4, 5]])
+    lens = torch.tensor([150, 192], dtype=torch.int32)
+    q = torch.randn(2, 4, 1, 128, generator=g).to(torch.bfloat16)
+    for shared in (0, 64):
+        if shared:
+            table[1, 0], small[1, 0] = table[0, 0], 0
+        o, lse = ea.attention_decode_paged(q.cuda(), pool, pool, table.cuda(), lens.cuda(),
+                                           shared_len=shared)
+        ea.check()
+        _hold(o, lse, oracle.paged_decode(np64(q), np64(x), np64(x), small, lens, 128 ** -0.5))
+    ea.pages_copy([pool], torch.tensor([P - 1], dtype=torch.int32).cuda(),
+                  torch.tensor([P - 9], dtype=torch.int32).cuda())
+    assert torch.equal(pool[P - 9].cpu(), x[0])
+    c = pool.view(-1)[:P * page * 128 // (page * 576) * page * 576].view(-1, page, 576)
+    used = [c.shape[0] - 1, 7, c.shape[0] - 3]
+    y = torch.randn(3, page, 576, generator=g).to(torch.bfloat16)
+    c[torch.tensor(used).cuda()] = y.cuda()
+    qc = torch.randn(1, 16, 1, 576, generator=g).to(torch.bfloat16)
+    o, lse = ea.attention_decode_latent(qc.cuda(), c, torch.tensor([used], dtype=torch.int32).cuda(),
+                                        torch.tensor([170], dtype=torch.int32).cuda(), scale=0.04)
+    ea.check()
+    _hold(o, lse, oracle.latent_decode(np64(qc), np64(y), [[0, 1, 2]], [170], 0.04, 512))
+
+
 def test_bad_page_is_reported_and_reads_as_zeros(ea):
     from exact_attention_12_gb300 import _abi
     g = torch.Generator().manual_seed(3)

@@ -196,6 +196,7 @@ def test_binding_refusals():
                     (dict(q=q[:, :3]), ValueError), (dict(page_table=t.long()), ValueError),
                     (dict(page_table=t[:1]), ValueError), (dict(cache_lens=n[:1]), ValueError),
                     (dict(page_table=t.repeat(1, 2)[:, ::2]), ValueError),
+                    (dict(page_table=t.repeat(1, 1 << 25)), ValueError),
                     (dict(v_pages=k.transpose(1, 2).contiguous().transpose(1, 2)), ValueError),
                     (dict(out=q.float()), ValueError), (dict(lse=torch.zeros(2, 4)), ValueError),
                     (dict(), ValueError)]:   # the last: not on a GPU
