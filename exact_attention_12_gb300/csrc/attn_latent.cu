@@ -97,8 +97,6 @@ struct __align__(1024) LatentCtl {
   // tile of a piece, in the buffer of the next, the columns' sums
   float wmax[2][4][64];
   float L[64];              // of the rows, for the cluster
-  int sums[12];
-  PagedShare share;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -187,8 +185,7 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
   const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.tmem_base, 0);
   PagedShare share{};
   if constexpr (!CLUSTER)
-    share = paged_share<C::kThreads, KT, kLatentOverhead, kLatentMinUnits>(a, cta, ctas, ctl.sums,
-                                                                           &ctl.share);
+    share = paged_share<KT, kLatentOverhead, kLatentMinUnits>(a, cta, ctas);
   const WaitCtx wc{&ctl.abort_flag, a.status, a.timeout_ns};
   PagedPiece p;
   if constexpr (CLUSTER) p = paged_part<KT>(a, cta, 0, rank);

@@ -65,8 +65,6 @@ struct PagedShared {
   uint64_t empty[kSlots * PagedCfg<D, MT>::kStages];
   float m[kSlots][MT * 16], l[kSlots][MT * 16];
   float L[16];   // of the rows in `red`, for the cluster
-  int sums[PagedCfg<D, MT>::kWarps];
-  PagedShare share;
   int abort_flag;
 };
 
@@ -128,8 +126,7 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
   grid_dep_launch();
   PagedShare share{};
   if constexpr (!CLUSTER)
-    share = paged_share<C::kThreads, KT, kPagedOverhead, kPagedMinUnits>(a, blockIdx.x, gridDim.x,
-                                                                         sh.sums, &sh.share);
+    share = paged_share<KT, kPagedOverhead, kPagedMinUnits>(a, blockIdx.x, gridDim.x);
   MergeNote note{-1, 0, 0, 0};
   const WaitCtx wc{&sh.abort_flag, a.status, a.timeout_ns};
   const int box_rows = min(KT, 1 << a.page_shift);

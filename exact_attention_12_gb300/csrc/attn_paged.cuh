@@ -160,33 +160,25 @@ struct PagedShare {
   }
 };
 
-// All threads of the CTA; `sums` has THREADS / 32 entries of shared memory.
-// Thread t adds up a run of consecutive sequences, the runs' sums are
-// scanned, and the thread whose run holds unit lo walks it.
-template <int THREADS, int KEYS, int OVERHEAD, int MIN_UNITS>
-__device__ __forceinline__ PagedShare paged_share(const PagedArgs& a, int cta, int launched,
-                                                  int* sums, PagedShare* out) {
-  const int per = (a.B + THREADS - 1) / THREADS;
-  const int b0 = min(static_cast<int>(threadIdx.x) * per, a.B), b1 = min(b0 + per, a.B);
+// Every warp by itself (each needs the answer, and barriers would cost more
+// than the lengths that are read again).  Lane l adds up a run of consecutive
+// sequences, the runs' sums are scanned, and the lane whose run holds unit lo
+// walks it.
+template <int KEYS, int OVERHEAD, int MIN_UNITS>
+__device__ __forceinline__ PagedShare paged_share(const PagedArgs& a, int cta, int launched) {
+  const int lane = threadIdx.x & 31;
+  const int per = (a.B + 31) / 32;
+  const int b0 = min(lane * per, a.B), b1 = min(b0 + per, a.B);
   int mine = 0;
+#pragma unroll 4
   for (int b = b0; b < b1; ++b) mine += a.heads * (paged_tiles<KEYS>(a, b) + OVERHEAD);
-  // inclusive scan over the warp, then over the warps
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int x = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += x;
   }
-  if (lane == 31) sums[warp] = inc;
-  __syncthreads();
-  int before = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) {
-    if (w < warp) before += sums[w];
-    total += sums[w];
-  }
-  inc += before;
+  const int total = __shfl_sync(0xffffffffu, inc, 31);
   PagedShare sh;
   const int ctas = max(1, min(launched, total / MIN_UNITS));
   sh.cta = cta;
@@ -199,19 +191,17 @@ __device__ __forceinline__ PagedShare paged_share(const PagedArgs& a, int cta, i
   }
   sh.lo = sh.q * cta + min(cta, sh.extra);
   sh.hi = sh.lo + sh.q + (cta < sh.extra ? 1 : 0);
-  if (inc - mine <= sh.lo && sh.lo < inc) {
-    int s = inc - mine, b = b0;
-    for (;; ++b) {
+  const bool here = inc - mine <= sh.lo && sh.lo < inc;
+  int s = inc - mine, b = b0;
+  if (here)
+    for (; b + 1 < b1; ++b) {
       const int c = a.heads * (paged_tiles<KEYS>(a, b) + OVERHEAD);
-      if (sh.lo < s + c || b + 1 >= b1) break;
+      if (sh.lo < s + c) break;
       s += c;
     }
-    out->b = b;
-    out->s = s;
-  }
-  __syncthreads();
-  sh.b = out->b;
-  sh.s = out->s;
+  const int from = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+  sh.b = __shfl_sync(0xffffffffu, b, from);
+  sh.s = __shfl_sync(0xffffffffu, s, from);
   return sh;
 }
 
