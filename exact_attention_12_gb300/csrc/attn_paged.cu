@@ -165,15 +165,16 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
     if (lane == 0) {
       uint64_t* bar = &sh.full[slot * ST + st];
       const int row = (a.first + (p.t0 + slot + kSlots * u) * KT) & ((1 << a.page_shift) - 1);
+      const int head = p.h / a.blocks;
       fence_proxy_async_smem();
       mbar_arrive_expect_tx(bar, 2 * C::kTileBytes);
 #pragma unroll
       for (int x = 0; x < C::kBoxes; ++x) {
-        tma_load_4d(sK(st) + x * C::kBoxBytes, &tk, bar, x * 64, row, p.h, pg0);
-        tma_load_4d(sV(st) + x * C::kBoxBytes, &tv, bar, x * 64, row, p.h, pg0);
+        tma_load_4d(sK(st) + x * C::kBoxBytes, &tk, bar, x * 64, row, head, pg0);
+        tma_load_4d(sV(st) + x * C::kBoxBytes, &tv, bar, x * 64, row, head, pg0);
         if (box_rows < KT) {
-          tma_load_4d(sK(st) + x * C::kBoxBytes + 16 * 128, &tk, bar, x * 64, 0, p.h, pg1);
-          tma_load_4d(sV(st) + x * C::kBoxBytes + 16 * 128, &tv, bar, x * 64, 0, p.h, pg1);
+          tma_load_4d(sK(st) + x * C::kBoxBytes + 16 * 128, &tk, bar, x * 64, 0, head, pg1);
+          tma_load_4d(sV(st) + x * C::kBoxBytes + 16 * 128, &tv, bar, x * 64, 0, head, pg1);
         }
       }
     }
@@ -206,13 +207,14 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
     // Q fragments of rows g and g + 8 of the warp's 16 (zero past the last row)
     uint32_t qa[D / 16][4];
     int lim[2];   // keys below lim are allowed
+    const int row0 = segment_row(a, p.h), nrows = segment_rows(a, p.h);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = rows[i];
-      const bool live = r < a.rows;
-      const int hl = r / a.n_q, qt = r - hl * a.n_q;
-      const __nv_bfloat16* qr = a.q + p.b * a.stride_b + (p.h * a.group + hl) * a.stride_h +
-                                static_cast<int64_t>(qt) * a.stride_n;
+      const bool live = r < nrows;
+      const int h = (row0 + r) / a.n_q, qt = row0 + r - h * a.n_q;
+      const __nv_bfloat16* qr =
+          a.q + p.b * a.stride_b + h * a.stride_h + static_cast<int64_t>(qt) * a.stride_n;
       lim[i] = !live ? 0 : (a.causal ? min(p.len, p.len - a.n_q + qt + 1) : p.len);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
@@ -385,7 +387,7 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
         }
         __syncthreads();
       }
-      const int live = min(16, a.rows - 16 * m);
+      const int live = min(16, nrows - 16 * m);   // (none, perhaps)
       auto logsumexp = [&](int r) {
         float mx = -INFINITY, lt = 0.f;
 #pragma unroll
@@ -405,8 +407,8 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
         for (int e = rank * C::kThreads + threadIdx.x; e < live * (D / 4);
              e += a.cluster * C::kThreads) {
           const int rr = e / (D / 4), c = 4 * (e - rr * (D / 4)), r = 16 * m + rr;
-          const int hl = r / a.n_q, qt = r - hl * a.n_q, h = p.h * a.group + hl;
-          const int64_t row = (static_cast<int64_t>(p.b) * a.H + h) * a.n_q + qt;
+          const int h = (row0 + r) / a.n_q, qt = row0 + r - h * a.n_q;
+          const int64_t row = static_cast<int64_t>(p.b) * a.all_rows + row0 + r;
           const int64_t all = static_cast<int64_t>(a.B) * a.all_rows;
           float top = -INFINITY, sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
           for (int k = 0; k < a.cluster; ++k)
@@ -442,8 +444,8 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
           const int rr = e / (D / 4), c = 4 * (e - rr * (D / 4)), r = 16 * m + rr;
           const float4 x = *reinterpret_cast<const float4*>(&red[rr * C::kRedStride + c]);
           if (whole) {
-            const int hl = r / a.n_q, qt = r - hl * a.n_q, h = p.h * a.group + hl;
-            const int64_t row = (static_cast<int64_t>(p.b) * a.H + h) * a.n_q + qt;
+            const int h = (row0 + r) / a.n_q, qt = row0 + r - h * a.n_q;
+            const int64_t row = static_cast<int64_t>(p.b) * a.all_rows + row0 + r;
             if (apart) {
               const int64_t at = a.pre_splits * (static_cast<int64_t>(a.B) * a.all_rows) + row;
               *reinterpret_cast<float4*>(a.pre_o + at * D + c) = x;
@@ -562,8 +564,8 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
   const MergeNote note{raw.x, raw.y, raw.z, raw.w};
   if (note.b < 0 || note.more < 0) return;   // (uniform over the CTA)
   const int e = blockIdx.y * kItems + threadIdx.x % kItems;
-  const int r = e / (D / 4), c = 4 * (e % (D / 4)), hr = note.h * a.rows + r;
-  const bool live = r < a.rows && hr < a.all_rows;
+  const int r = e / (D / 4), c = 4 * (e % (D / 4)), hr = segment_row(a, note.h) + r;
+  const bool live = r < segment_rows(a, note.h);
   auto piece = [&](int i) {
     const int64_t at =
         static_cast<int64_t>(i == 0 ? note.slot : (note.slot & ~1) + 2 * i) * a.rows + r;
@@ -585,8 +587,8 @@ __global__ void __launch_bounds__(kMergeThreads) paged_finish_kernel(const Paged
   const int4 raw = *reinterpret_cast<const int4*>(a.notes + blockIdx.x);
   const MergeNote note{raw.x, raw.y, raw.z, raw.w};
   const int e = blockIdx.y * kItems + threadIdx.x % kItems;
-  const int r = e / (D / 4), c = 4 * (e % (D / 4)), hr = note.h * a.rows + r;
-  const bool live = r < a.rows;
+  const int r = e / (D / 4), c = 4 * (e % (D / 4)), hr = segment_row(a, note.h) + r;
+  const bool live = r < segment_rows(a, note.h);
   const int64_t row = static_cast<int64_t>(note.b) * a.all_rows + hr;
   const int64_t all = static_cast<int64_t>(a.B) * a.all_rows;
   const int pre = a.pre_splits + (note.more < 0 ? 1 : 0);

@@ -40,11 +40,10 @@ struct MergeNote {
 // each takes an equal part of its tiles, and they merge through their shared
 // memory (PagedArgs::cluster > 0; the note and the partials stay unused).
 struct PagedArgs {
-  int B, H, heads;                // heads: segments per sequence
-  int group;                      // query heads per segment
-  int n_q, rows;                  // query rows per segment: group * n_q (the last latent
-                                  // segment of a sequence may have fewer)
-  int all_rows;                   // latent: H * n_q
+  int B, H, heads;                // heads: segments per sequence, H_kv * blocks
+  int blocks;                     // segments per key/value head (1 up to 64 query rows)
+  int n_q, rows;                  // query rows per segment (the last of a head may have fewer)
+  int head_rows, all_rows;        // of a key/value head, (H / H_kv) * n_q; of a sequence
   int causal, d;
   const int32_t* key_lens;        // [B]
   const int32_t* table;           // [B][table_stride]
@@ -74,6 +73,17 @@ struct PagedArgs {
   int* status;
   uint64_t timeout_ns;
 };
+
+// Where segment h of a sequence begins among the sequence's rows (head * n_q +
+// query), and how many it has.
+__device__ __forceinline__ int segment_row(const PagedArgs& a, int h) {
+  const int head = h / a.blocks;
+  return head * a.head_rows + (h - head * a.blocks) * a.rows;
+}
+
+__device__ __forceinline__ int segment_rows(const PagedArgs& a, int h) {
+  return min(a.rows, a.head_rows - h % a.blocks * a.rows);
+}
 
 struct PrefixArgs {
   int B, H, H_kv, group, n_q, causal, d;

@@ -58,8 +58,6 @@ attn_status validate(const attn_params* p, int32_t n_q, const attn_pages* g, boo
              : (p->H_kv < 0 || (p->H > 0 && (H_kv < 1 || p->H % H_kv != 0))))
     return fail(ATTN_ERR_INVALID_ARG, latent ? "latent decode: H_kv must be 0 or 1"
                                              : "H_kv must divide H");
-  if (!latent && p->H > 0 && static_cast<int64_t>(p->H / H_kv) * n_q > attn::kDecMaxRows)
-    return fail(ATTN_ERR_UNSUPPORTED, "(H / H_kv) * n_q exceeds 64");
   if (static_cast<int64_t>(p->H) * n_q > 32768 ||
       static_cast<int64_t>(p->B) * p->H * n_q > (1 << 30))
     return fail(ATTN_ERR_UNSUPPORTED, "more than 32768 query rows per sequence or 2^30 in all");
@@ -75,9 +73,10 @@ attn_status validate(const attn_params* p, int32_t n_q, const attn_pages* g, boo
     return fail(ATTN_ERR_INVALID_ARG, "page table is NULL");
   if (g->shared_len < 0 || g->shared_len > cap || g->shared_len % g->page_size != 0)
     return fail(ATTN_ERR_INVALID_ARG, "shared_len must be a multiple of page_size, at most N");
-  if (p->B * (latent ? 1 : H_kv) * (cap / (latent ? attn::kLatentKeys : attn::kPagedKeys) +
+  const int64_t blocks = latent ? 1 : H_kv > 0 ? (static_cast<int64_t>(p->H / H_kv) * n_q + 63) / 64 * H_kv : 0;
+  if (p->B * blocks * (cap / (latent ? attn::kLatentKeys : attn::kPagedKeys) +
                                     attn::kPagedOverhead + 1) >= (int64_t{1} << 31))
-    return fail(ATTN_ERR_UNSUPPORTED, "B * H_kv * N / 32 must stay below 2^31");
+    return fail(ATTN_ERR_UNSUPPORTED, "B * H_kv * N / 32 (times H / H_kv * n_q / 64) must stay below 2^31");
   if (latent && g->shared_len != 0)
     return fail(ATTN_ERR_UNSUPPORTED, "latent decode takes no shared prefix");
   // strides
@@ -113,6 +112,8 @@ attn_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
   return ATTN_OK;
 }
 
+int kv_heads(const attn_params* p) { return p->H_kv == 0 ? p->H : p->H_kv; }
+
 bool empty(const attn_params* p) { return p->B == 0 || p->H == 0; }
 
 struct Layout {
@@ -121,7 +122,8 @@ struct Layout {
   int n_notes = 0;                         // of merges: one per segment or per CTA
   bool by_segment = false;
   int cluster = 0;
-  int heads = 0, group = 0, rows = 0;      // segments per sequence, heads and rows of one
+  int heads = 0, blocks = 1, rows = 0;     // segments per sequence and key/value head, rows of one
+  int head_rows = 0;                       // rows of a key/value head
   int first = 0, splits = 0, tiles = 0;    // the shared prefix
 };
 
@@ -138,13 +140,16 @@ Layout layout(const attn_params* p, int32_t n_q, const attn_pages* g, bool laten
   if (latent) {
     const int64_t groups = (static_cast<int64_t>(p->H) * n_q + attn::kLatentRows - 1) / attn::kLatentRows;
     L.heads = 1;
-    L.group = p->H;
+    L.head_rows = p->H * n_q;
     L.rows = static_cast<int>(groups * attn::kLatentRows);
     most = sms / groups;
   } else {
-    L.heads = H_kv;
-    L.group = H_kv > 0 ? p->H / H_kv : 1;
-    L.rows = L.group * n_q;
+    // more than 64 rows of a key/value head: in equal blocks, each of which
+    // reads the keys
+    L.head_rows = H_kv > 0 ? p->H / H_kv * n_q : n_q;
+    L.blocks = (L.head_rows + attn::kDecMaxRows - 1) / attn::kDecMaxRows;
+    L.rows = L.blocks > 0 ? (L.head_rows + L.blocks - 1) / L.blocks : 0;
+    L.heads = H_kv * L.blocks;
     most = L.rows > 32 ? sms : 2 * sms;
     // the prefix apart: only where two sequences share it
     L.first = p->B > 1 ? g->shared_len : 0;
@@ -161,9 +166,9 @@ Layout layout(const attn_params* p, int32_t n_q, const attn_pages* g, bool laten
     // pieces of the prefix: as many as fill the SMs once, two key tiles each
     // at least, 16 at most
     L.tiles = (L.first + attn::kTile - 1) / attn::kTile;
-    const int64_t stack = static_cast<int64_t>(p->B) * L.group * n_q;
-    const int64_t blocks = (stack + 2 * attn::kTile - 1) / (2 * attn::kTile) * L.heads;
-    int64_t k = blocks > 0 ? sms / blocks : 1;
+    const int64_t stack = static_cast<int64_t>(p->B) * L.head_rows;
+    const int64_t units2 = (stack + 2 * attn::kTile - 1) / (2 * attn::kTile) * H_kv;
+    int64_t k = units2 > 0 ? sms / units2 : 1;
     if (k > L.tiles / 2) k = L.tiles / 2;
     if (k > 16) k = 16;
     L.splits = k < 1 ? 1 : static_cast<int>(k);
@@ -205,7 +210,8 @@ PagedArgs args_of(const attn_params* p, int32_t n_q, const attn_pages* g, const 
   a.B = p->B;
   a.H = p->H;
   a.heads = L.heads;
-  a.group = L.group;
+  a.blocks = L.blocks;
+  a.head_rows = L.head_rows;
   a.n_q = n_q;
   a.rows = L.rows;
   a.all_rows = p->H * n_q;
@@ -274,7 +280,7 @@ attn_status attn_decode_paged(const attn_params* p, int32_t n_q, const attn_page
   const PagedArgs a = args_of(p, n_q, pages, L, q, o, lse, ws);
   const auto map = [&](CUtensorMap* m, const void* ptr, int keys) {
     return static_cast<attn_status>(attn::encode_pages(
-        m, ptr, at_least_1(pages->num_pages), L.heads, pages->page_size, p->d, p->kv_stride_b,
+        m, ptr, at_least_1(pages->num_pages), kv_heads(p), pages->page_size, p->d, p->kv_stride_b,
         p->kv_stride_h, p->kv_stride_n, box_rows(pages, keys)));
   };
   CUtensorMap tk, tv;
@@ -284,8 +290,8 @@ attn_status attn_decode_paged(const attn_params* p, int32_t n_q, const attn_page
     attn::PrefixArgs f{};
     f.B = p->B;
     f.H = p->H;
-    f.H_kv = L.heads;
-    f.group = L.group;
+    f.H_kv = kv_heads(p);
+    f.group = p->H / f.H_kv;
     f.n_q = n_q;
     f.causal = a.causal;
     f.d = p->d;
@@ -297,7 +303,7 @@ attn_status attn_decode_paged(const attn_params* p, int32_t n_q, const attn_page
     f.shared_len = L.first;
     f.splits = L.splits;
     f.tiles = L.tiles;
-    f.rows = p->B * L.group * n_q;
+    f.rows = p->B * L.head_rows;
     f.scale = a.scale;
     f.scale_log2 = a.scale_log2;
     f.q = a.q;

@@ -263,8 +263,9 @@ typedef struct attn_pages {
  *   k, v    [num_pages, H_kv, page_size, d] bf16, where kv_stride_b is the
  *           stride between pages (all three key/value strides are required)
  *   p->N    must be max_pages * page_size
- * and the same query rows, masks, limits and outputs.  Rows of a page past
- * the end of its sequence are not used, whatever they hold.
+ * and the same query rows, masks and outputs.  (H / H_kv) * n_q is not
+ * limited to 64 here; the cache is read once per 64 of these rows.  Rows of a
+ * page past the end of its sequence are not used, whatever they hold.
  *
  * shared_len > 0: the first shared_len / page_size entries of every table row
  * name the same pages (a fork of one prompt, a common system prompt), of

@@ -101,9 +101,10 @@ def _run(ea, lens, H, H_kv, n_q, d, page, causal=True, shared=0, seed=0, layout=
     return o, lse
 
 
-# rows per key/value head: 1, 4, 16, 24, 40, 64 -- each row-tile count
+# rows per key/value head: 1, 4, 16, 24, 40, 64 -- each row-tile count -- and
+# 65, 100, 128, 200, in blocks
 @pytest.mark.parametrize("H,H_kv,n_q", [(2, 2, 1), (8, 2, 1), (16, 1, 1), (6, 2, 8), (10, 2, 8),
-                                         (64, 1, 1)])
+                                         (64, 1, 1), (65, 1, 1), (40, 2, 5), (128, 1, 1), (8, 1, 25)])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("room", [0, WIDE])
 def test_rows_and_widths(ea, H, H_kv, n_q, d, room):
@@ -144,7 +145,7 @@ def test_large_scores(ea):
 
 @pytest.mark.parametrize("B,H,H_kv,n_q,d,page,shared", [
     (2, 2, 2, 1, 64, 16, 16), (5, 8, 2, 1, 128, 16, 1040), (3, 4, 1, 5, 64, 64, 128),
-    (40, 16, 2, 1, 128, 32, 512), (70, 8, 1, 2, 64, 256, 256), (9, 32, 1, 2, 128, 128, 2048)])
+    (40, 16, 2, 1, 128, 32, 512), (3, 48, 2, 4, 64, 32, 256), (70, 8, 1, 2, 64, 256, 256), (9, 32, 1, 2, 128, 128, 2048)])
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("room", [0, WIDE])
 def test_shared_prefix(ea, B, H, H_kv, n_q, d, page, shared, causal, room):

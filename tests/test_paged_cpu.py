@@ -84,7 +84,7 @@ def _status(abi, p, g, n_q, latent=False, ws=0x1000, nb=1 << 40, ptr=0x1000):
 @pytest.mark.parametrize("kw,status", [
     (dict(d=96), 2), (dict(dtype=1), 2), (dict(dtype=9), 1), (dict(scale=0.0), 1),
     (dict(scale=float("nan")), 1), (dict(dropout_p=0.1), 2), (dict(block_mask=0x1000), 2),
-    (dict(key_lens=None), 1), (dict(n_q=0), 1), (dict(H_kv=3), 1), (dict(n_q=33), 2),
+    (dict(key_lens=None), 1), (dict(n_q=0), 1), (dict(H_kv=3), 1), (dict(n_q=9000), 2),
     (dict(B=-1), 1), (dict(reserved=1), 1), (dict(N=255), 1), (dict(table=None), 1),
     (dict(page_size=24, N=192), 1), (dict(page_size=8, N=64), 1), (dict(page_size=0, N=0), 1),
     (dict(max_pages=-1), 1), (dict(num_pages=-1), 1), (dict(table_stride=7), 1),
