@@ -25,12 +25,18 @@ _TABLE = struct.Struct("@PqPP4i").pack
 _ROPE = 64   # columns of a latent vector beside its d_v value columns
 
 
+_empty, _empty_like, _bf16, _f32, _i32 = (torch.empty, torch.empty_like, torch.bfloat16,
+                                          torch.float32, torch.int32)
+
+
 def _public_stream(index):
     return torch.cuda.current_stream(index).cuda_stream
 
 
-# the current stream's handle without the stream object around it (2 us)
+# the current stream's handle without the stream object around it (2 us), and
+# the current device without a look at whether CUDA is initialised
 _stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_stream)
+_current = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _call(fn, size_fn, size_args, args, device, ws, what):
@@ -40,7 +46,7 @@ def _call(fn, size_fn, size_args, args, device, ws, what):
     index = device.index
     if index is None or device.type != "cuda":
         raise ValueError(f"{what}: tensors must be on a CUDA device")
-    if torch.cuda.current_device() != index:
+    if _current() != index:
         with torch.cuda.device(device):
             return _call(fn, size_fn, size_args, args, device, ws, what)
     stream = _stream(index)
@@ -61,17 +67,17 @@ def _call(fn, size_fn, size_args, args, device, ws, what):
         check_status(st, what)
 
 
-def _int32(t, device, dim, what):
-    if t.dtype != torch.int32 or t.device != device or t.dim() != dim \
+def _int32(t, index, dim, what):
+    if t.dtype is not _i32 or t.get_device() != index or t.dim() != dim \
             or not (t.is_contiguous() or t.stride(-1) == 1):
         raise ValueError(f"{what} must be a {dim}-dimensional int32 tensor on the tensors' device, "
                          "contiguous along its last axis")
 
 
-def _table(table, cache_lens, B, device, page_size):
+def _table(table, cache_lens, B, index, page_size):
     """Pointers, row stride and width of a page table with B rows."""
-    _int32(table, device, 2, "page_table")
-    _int32(cache_lens, device, 1, "cache_lens")
+    _int32(table, index, 2, "page_table")
+    _int32(cache_lens, index, 1, "cache_lens")
     rows, width = table.shape
     if rows != B or cache_lens.shape[0] != B:
         raise ValueError("page_table and cache_lens must have a row per sequence")
@@ -115,9 +121,9 @@ def attention_decode_paged(q, k_pages, v_pages, page_table, cache_lens, *, scale
     for the whole batch.  Returns (o, lse) with o like q and lse fp32
     [B, H, n_q].  A page index outside the cache is reported by check().
     """
-    device, shape, pages = q.device, q.shape, k_pages.shape
-    if not q.dtype == k_pages.dtype == v_pages.dtype == torch.bfloat16 \
-            or k_pages.device != device or v_pages.device != device:
+    shape, pages, index = q.shape, k_pages.shape, q.get_device()
+    if not (q.dtype is k_pages.dtype is v_pages.dtype is _bf16) \
+            or not index == k_pages.get_device() == v_pages.get_device():
         raise TypeError("q, k_pages and v_pages must be bf16 on one device")
     if len(shape) != 4 or len(pages) != 4 or pages != v_pages.shape or pages[3] != shape[3]:
         raise ValueError("q must be [B, H, n_q, d], k_pages and v_pages "
@@ -132,17 +138,19 @@ def attention_decode_paged(q, k_pages, v_pages, page_table, cache_lens, *, scale
         ks = _strides(k_pages)
         if ks != _strides(v_pages):
             raise ValueError("k_pages and v_pages must share strides")
-    qs = _strides(q)
+    device = q.device
+    dense = q.is_contiguous()
+    qs = (H * n_q * d, n_q * d, d) if dense else _strides(q)[:3]
     if out is None:
-        out = torch.empty_like(q) if q.is_contiguous() else torch.empty_strided(
-            shape, q.stride(), dtype=q.dtype, device=device)
-    elif out.shape != shape or _strides(out) != qs or out.dtype != q.dtype \
-            or out.device != device:
+        out = _empty_like(q) if dense else torch.empty_strided(shape, q.stride(), dtype=_bf16,
+                                                               device=device)
+    elif out.shape != shape or _strides(out) != _strides(q) or out.dtype is not _bf16 \
+            or out.get_device() != index:
         raise ValueError("out must be like q")
     lse = _lse(lse, shape, device)
-    table, row, width, lens = _table(page_table, cache_lens, B, device, page_size)
+    table, row, width, lens = _table(page_table, cache_lens, B, index, page_size)
     p = _PARAMS(B, H, width * page_size, d, 0, d ** -0.5 if scale is None else scale,
-                1 if causal else 0, 0.0, 0, 0, lens, 0, 0, *qs[:3], H_kv, 0, *ks[:3], 0.0, 0.0, 0.0, 0)
+                1 if causal else 0, 0.0, 0, 0, lens, 0, 0, *qs, H_kv, 0, *ks[:3], 0.0, 0.0, 0.0, 0)
     g = _PAGES(table, row, width, page_size, num_pages, shared_len)
     c = lib()
     _call(c.attn_decode_paged, c.attn_decode_paged_workspace_size, (p, n_q, g),
@@ -164,7 +172,8 @@ def attention_decode_latent(q, c_pages, page_table, cache_lens, *, scale, d_v=51
     contiguous, and lse fp32 [B, H, n_q].
     """
     device, shape, pages, cols = q.device, q.shape, c_pages.shape, d_v + _ROPE
-    if not q.dtype == c_pages.dtype == torch.bfloat16 or c_pages.device != device:
+    index = q.get_device()
+    if not (q.dtype is c_pages.dtype is _bf16) or c_pages.get_device() != index:
         raise TypeError("q and c_pages must be bf16 on one device")
     if len(shape) != 4 or len(pages) != 3 or shape[3] != cols or pages[2] != cols:
         raise ValueError(f"q must be [B, H, n_q, d_v + {_ROPE}], c_pages "
@@ -172,13 +181,13 @@ def attention_decode_latent(q, c_pages, page_table, cache_lens, *, scale, d_v=51
     B, H, n_q, _ = shape
     num_pages, page_size, _ = pages
     if out is None:
-        out = torch.empty((B, H, n_q, d_v), dtype=q.dtype, device=device)
-    elif out.shape != (B, H, n_q, d_v) or not out.is_contiguous() or out.dtype != q.dtype \
-            or out.device != device:
+        out = _empty((B, H, n_q, d_v), dtype=_bf16, device=device)
+    elif out.shape != (B, H, n_q, d_v) or not out.is_contiguous() or out.dtype is not _bf16 \
+            or out.get_device() != index:
         raise ValueError("out must be a contiguous bf16 [B, H, n_q, d_v] on q's device")
     lse = _lse(lse, shape, device)
     cs, qs = _strides(c_pages), _strides(q)
-    table, row, width, lens = _table(page_table, cache_lens, B, device, page_size)
+    table, row, width, lens = _table(page_table, cache_lens, B, index, page_size)
     p = _PARAMS(B, H, width * page_size, d_v, 0, scale, 1 if causal else 0, 0.0, 0, 0, lens, 0, 0,
                 *qs[:3], 1, 0, cs[0], cs[0], cs[1], 0.0, 0.0, 0.0, 0)
     g = _PAGES(table, row, width, page_size, num_pages, 0)
@@ -191,8 +200,8 @@ def attention_decode_latent(q, c_pages, page_table, cache_lens, *, scale, d_v=51
 
 def _lse(lse, shape, device):
     if lse is None:
-        return torch.empty(shape[:3], dtype=torch.float32, device=device)
-    if lse.shape != shape[:3] or not lse.is_contiguous() or lse.dtype != torch.float32 \
+        return _empty(shape[:3], dtype=_f32, device=device)
+    if lse.shape != shape[:3] or not lse.is_contiguous() or lse.dtype is not _f32 \
             or lse.device != device:
         raise ValueError("lse must be a contiguous fp32 [B, H, n_q] on q's device")
     return lse
@@ -201,9 +210,10 @@ def _lse(lse, shape, device):
 # ------------------------------------------------------------------- upkeep --
 
 def _table_args(page_table, cache_lens, refs, page_size):
-    _int32(refs, refs.device, 1, "refs")
+    index = refs.get_device()
+    _int32(refs, index, 1, "refs")
     rows = page_table.shape[0]
-    table, row, width, lens = _table(page_table, cache_lens, rows, refs.device, page_size)
+    table, row, width, lens = _table(page_table, cache_lens, rows, index, page_size)
     return _TABLE(table, row, lens, refs.data_ptr(), rows, width, page_size, refs.shape[0])
 
 
@@ -231,7 +241,7 @@ def _pool_args(pools, num_pages, device):
 
 
 def _list(t, device, what):
-    _int32(t, device, 1, what)
+    _int32(t, -1 if device.type == "cpu" else device.index, 1, what)
     return t.data_ptr(), t.shape[0]
 
 
