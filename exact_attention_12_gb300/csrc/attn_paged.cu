@@ -122,7 +122,13 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
     tma_prefetch_desc(&tv);
   }
   __syncthreads();
-  grid_dep_wait();
+  // With a prefix the kernel before this one attends it, and only the merge
+  // needs its results: so the wait for it comes at the end, and this kernel's
+  // CTAs run beside it as SMs fall free.  (That all kernels before it are
+  // complete is known here: each of its CTAs had waited for them before it let
+  // this kernel start.)
+  const bool late = a.pre_splits > 0;
+  if (!late) grid_dep_wait();
   grid_dep_launch();
   PagedShare share{};
   if constexpr (!CLUSTER)
@@ -403,6 +409,7 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
         // the cluster's rows, and a prefix's pieces, merged: each CTA writes a
         // part of the items
         if (threadIdx.x < live) sh.L[threadIdx.x] = logsumexp(16 * m + threadIdx.x);
+        if (late) grid_dep_wait();
         cluster_sync();
         for (int e = rank * C::kThreads + threadIdx.x; e < live * (D / 4);
              e += a.cluster * C::kThreads) {
@@ -468,6 +475,7 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
     p = next;
   }
   if (!CLUSTER && !a.by_segment && threadIdx.x == 0) a.notes[blockIdx.x] = note;
+  if (!CLUSTER && late) grid_dep_wait();   // the merge waits for this kernel only
   if (!ok && mt == 0 && lane == 0) {   // let issued copies land before the CTA exits
     for (uint32_t t = issued > ST ? issued - ST : 0; t < issued; ++t)
       mbar_wait_drain(&sh.full[slot * ST + t % ST], (t / ST) & 1, a.timeout_ns);
