@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
     share = paged_share<KT, kLatentOverhead, kLatentMinUnits>(a, cta, ctas);
   const WaitCtx wc{&ctl.abort_flag, a.status, a.timeout_ns};
   PagedPiece p;
-  if constexpr (CLUSTER) p = paged_part<KT>(a, cta, 0, rank);
+  if constexpr (CLUSTER) p = paged_part<KT>(a, cta, 0, rank, a.cluster);
   else p = paged_piece<KT, kLatentOverhead>(a, share, share.b, 0, share.s);
   auto next_of = [&](const PagedPiece& w) {
     PagedPiece x = w;

@@ -93,12 +93,19 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// CLUSTER: a segment per cluster (a.cluster CTAs), else the balanced split.
-template <int D, int MT, bool CLUSTER>
+// How the segments are given out.
+//   kSplit    the balanced split
+//   kCluster  a segment per cluster (a.cluster CTAs), merged in shared memory
+//   kSolo     a segment per slot, which has nobody to merge with: for many short
+//             sequences (64 of 50-200 keys, 8 heads: 12.5 against 18.8 us)
+enum PagedMode { kSplit, kCluster, kSolo };
+
+template <int D, int MT, PagedMode MODE>
 __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kCtasPerSm)
     paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                  const PagedArgs a) {
   using C = PagedCfg<D, MT>;
+  constexpr bool CLUSTER = MODE == kCluster, SOLO = MODE == kSolo;
   constexpr int ST = C::kStages, KT = C::kKeys, NT = D / 8;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -131,7 +138,7 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
   if (!late) grid_dep_wait();
   grid_dep_launch();
   PagedShare share{};
-  if constexpr (!CLUSTER)
+  if constexpr (MODE == kSplit)
     share = paged_share<KT, kPagedOverhead, kPagedMinUnits>(a, blockIdx.x, gridDim.x);
   MergeNote note{-1, 0, 0, 0};
   const WaitCtx wc{&sh.abort_flag, a.status, a.timeout_ns};
@@ -139,18 +146,20 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
   bool ok = true;
 
   // ---- the copies: tile u of this slot is tile t0 + slot + kSlots u of the
-  // piece; lane l of the issuing warp holds the page indices of tile
+  // piece (of a segment of its own: tile u); lane l of the issuing warp holds the page indices of tile
   // 32 * (batch) + l (two where a tile spans two 16-key pages)
   uint32_t issued = 0, done = 0;   // tiles of this slot issued / used, over all pieces
   int page_of[2] = {0, 0};
+  constexpr int kStep = SOLO ? 1 : kSlots;
+  const int first_tile = SOLO ? 0 : slot;
   auto slot_tiles = [&](const PagedPiece& p) {
-    const int n = p.t1 - p.t0 - slot;
-    return n > 0 ? (n + kSlots - 1) / kSlots : 0;
+    const int n = p.t1 - p.t0 - first_tile;
+    return n > 0 ? (n + kStep - 1) / kStep : 0;
   };
   auto load_pages = [&](const PagedPiece& p, int u0, int nu) {
     const int u = u0 + lane;
     if (u < nu) {
-      const int key = a.first + (p.t0 + slot + kSlots * u) * KT;
+      const int key = a.first + (p.t0 + first_tile + kStep * u) * KT;
       const int32_t* row = a.table + p.b * a.table_stride;
       page_of[0] = checked_page(row[key >> a.page_shift], a.num_pages, a.status);
       // (a page of 16 keys: the tile's second half, where the sequence reaches it)
@@ -170,7 +179,7 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
     }
     if (lane == 0) {
       uint64_t* bar = &sh.full[slot * ST + st];
-      const int row = (a.first + (p.t0 + slot + kSlots * u) * KT) & ((1 << a.page_shift) - 1);
+      const int row = (a.first + (p.t0 + first_tile + kStep * u) * KT) & ((1 << a.page_shift) - 1);
       const int head = p.h / a.blocks;
       fence_proxy_async_smem();
       mbar_arrive_expect_tx(bar, 2 * C::kTileBytes);
@@ -203,7 +212,11 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
   PagedPiece p;
   if constexpr (CLUSTER) {
     const int segment = blockIdx.x / a.cluster, b = segment / a.heads;
-    p = paged_part<KT>(a, b, segment - b * a.heads, rank);
+    p = paged_part<KT>(a, b, segment - b * a.heads, rank, a.cluster);
+  } else if constexpr (SOLO) {
+    const int segment = blockIdx.x * kSlots + slot, b = segment / a.heads;
+    if (b < a.B) p = paged_part<KT>(a, b, segment - b * a.heads, 0, 1);
+    else p.valid = false;
   } else {
     p = paged_piece<KT, kPagedOverhead>(a, share, share.b, 0, share.s);
   }
@@ -240,7 +253,7 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
                                                    kSitePagedTile))))
         break;
       const uint32_t kb = smem_u32(sK(st)), vb = smem_u32(sV(st));
-      const int k0 = a.first + (p.t0 + slot + kSlots * u) * KT;
+      const int k0 = a.first + (p.t0 + first_tile + kStep * u) * KT;
       if (k0 + KT > p.len) {   // value rows past the end: zero
         const int from = p.len - k0;
         for (int i = lane; i < (KT - from) * (D / 8); i += 32) {
@@ -334,148 +347,194 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
     }
 
     PagedPiece next = p;
-    if constexpr (CLUSTER) {
-      next.valid = false;
-    } else {
+    if constexpr (MODE == kSplit) {
       next = paged_next<KT, kPagedOverhead>(a, share, p);
       if (ok) prefetch(next);
+    } else {
+      next.valid = false;
     }
-
-    // ---- the slots' states merged: m, l per row, then O through shared memory
+    if constexpr (SOLO) {
+      // rows g, g + 8 straight from the registers, with a prefix's pieces
+      if (late) grid_dep_wait();
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      lrow[i] += __shfl_xor_sync(0xffffffffu, lrow[i], 1);
-      lrow[i] += __shfl_xor_sync(0xffffffffu, lrow[i], 2);
-      if (q4 == 0) {
-        sh.m[slot][rows[i]] = mrow[i];
-        sh.l[slot][rows[i]] = lrow[i];
-      }
-    }
-    ok = __syncthreads_and(ok);
-    float scale[2];
+      for (int i = 0; i < 2; ++i) {
+        float l = lrow[i];
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        if (rows[i] >= nrows) continue;
+        const int h = (row0 + rows[i]) / a.n_q, qt = row0 + rows[i] - h * a.n_q;
+        const int64_t row = static_cast<int64_t>(p.b) * a.all_rows + row0 + rows[i];
+        const int64_t all = static_cast<int64_t>(a.B) * a.all_rows;
+        const float L = l == 0.f ? -INFINITY : fmaf(mrow[i], a.scale, logf(l));
+        float top = L;
+        for (int k = 0; k < a.pre_splits; ++k) top = fmaxf(top, a.pre_l[k * all + row]);
+        // (without a prefix the weight is 1)
+        float sum = top == -INFINITY ? 0.f : a.pre_splits > 0 ? __expf(L - top) : 1.f;
+        const float own = sum == 0.f ? 0.f : sum / l;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float mx = -INFINITY, lt = 0.f;
-#pragma unroll
-      for (int w = 0; w < kSlots; ++w) mx = fmaxf(mx, sh.m[w][rows[i]]);
-#pragma unroll
-      for (int w = 0; w < kSlots; ++w) {
-        const float mw = sh.m[w][rows[i]];
-        if (mw != -INFINITY) lt += sh.l[w][rows[i]] * ex2_approx((mw - mx) * c2);
-      }
-      // this slot's weight, with the 1 / l folded in
-      scale[i] = mrow[i] == -INFINITY ? 0.f : ex2_approx((mrow[i] - mx) * c2) / lt;
-    }
-    const bool whole = p.whole();
-    const bool apart = a.pre_splits > 0;   // a prefix is merged afterwards
-    if constexpr (!CLUSTER) {
-      if (p.t0 == 0 && !whole) note = paged_note<kPagedOverhead>(share, p);
-      if (a.by_segment && p.t0 == 0 && threadIdx.x == 0)
-        a.notes[p.b * a.heads + p.h] = whole ? MergeNote{p.b, p.h, 0, -1} : note;
-    }
-    const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (p.s < share.lo ? 0 : 1);
-    for (int m = 0; m < MT; ++m) {   // 16 rows at a time
-      for (int w = 0; w < kSlots; ++w) {   // in turn: the sum has a fixed order
-        if (slot == w && mt == m) {
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              float2* dst = reinterpret_cast<float2*>(&red[(g + 8 * i) * C::kRedStride + 8 * n + 2 * q4]);
-              float2 x = make_float2(o[n][2 * i] * scale[i], o[n][2 * i + 1] * scale[i]);
-              if (w > 0) {
-                const float2 y = *dst;
-                x.x += y.x;
-                x.y += y.y;
-              }
-              *dst = x;
-            }
+        for (int n = 0; n < NT; ++n) {
+          o[n][2 * i] *= own;
+          o[n][2 * i + 1] *= own;
         }
-        __syncthreads();
-      }
-      const int live = min(16, nrows - 16 * m);   // (none, perhaps)
-      auto logsumexp = [&](int r) {
-        float mx = -INFINITY, lt = 0.f;
-#pragma unroll
-        for (int w = 0; w < kSlots; ++w) mx = fmaxf(mx, sh.m[w][r]);
-#pragma unroll
-        for (int w = 0; w < kSlots; ++w) {
-          const float mw = sh.m[w][r];
-          if (mw != -INFINITY) lt += sh.l[w][r] * ex2_approx((mw - mx) * c2);
-        }
-        return lt == 0.f ? -INFINITY : fmaf(mx, a.scale, logf(lt));
-      };
-      if constexpr (CLUSTER) {
-        // the cluster's rows, and a prefix's pieces, merged: each CTA writes a
-        // part of the items
-        if (threadIdx.x < live) sh.L[threadIdx.x] = logsumexp(16 * m + threadIdx.x);
-        if (late) grid_dep_wait();
-        cluster_sync();
-        for (int e = rank * C::kThreads + threadIdx.x; e < live * (D / 4);
-             e += a.cluster * C::kThreads) {
-          const int rr = e / (D / 4), c = 4 * (e - rr * (D / 4)), r = 16 * m + rr;
-          const int h = (row0 + r) / a.n_q, qt = row0 + r - h * a.n_q;
-          const int64_t row = static_cast<int64_t>(p.b) * a.all_rows + row0 + r;
-          const int64_t all = static_cast<int64_t>(a.B) * a.all_rows;
-          float top = -INFINITY, sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
-          for (int k = 0; k < a.cluster; ++k)
-            top = fmaxf(top, cluster_ld(cluster_addr(&sh.L[rr], k)));
-          for (int k = 0; k < a.pre_splits; ++k) top = fmaxf(top, a.pre_l[k * all + row]);
-          auto add = [&](float L, const float* y) {
-            const float w = __expf(L - top);
+        if (top > -INFINITY)
+          for (int k = 0; k < a.pre_splits; ++k) {
+            const float w = __expf(a.pre_l[k * all + row] - top);
+            const float* y = a.pre_o + (k * all + row) * D + 2 * q4;
             sum += w;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = fmaf(w, y[i], x[i]);
-          };
-          if (top > -INFINITY) {
-            for (int k = 0; k < a.cluster; ++k) {
-              float y[4];
-              cluster_ld4(cluster_addr(&red[rr * C::kRedStride + c], k), y);
-              add(cluster_ld(cluster_addr(&sh.L[rr], k)), y);
-            }
-            for (int k = 0; k < a.pre_splits; ++k) {
-              const float4 y = *reinterpret_cast<const float4*>(a.pre_o + (k * all + row) * D + c);
-              const float z[4] = {y.x, y.y, y.z, y.w};
-              add(a.pre_l[k * all + row], z);
+            for (int n = 0; n < NT; ++n) {
+              const float2 z = *reinterpret_cast<const float2*>(y + 8 * n);
+              o[n][2 * i] = fmaf(w, z.x, o[n][2 * i]);
+              o[n][2 * i + 1] = fmaf(w, z.y, o[n][2 * i + 1]);
             }
           }
-          const float inv = sum == 0.f ? 0.f : 1.f / sum;
-          *reinterpret_cast<uint2*>(a.o + p.b * a.stride_b + h * a.stride_h +
-                                    static_cast<int64_t>(qt) * a.stride_n + c) =
-              make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
-          if (c == 0) a.lse[row] = sum == 0.f ? -INFINITY : top + logf(sum);
+        const float inv = sum == 0.f ? 0.f : a.pre_splits > 0 ? 1.f / sum : 1.f;
+        __nv_bfloat16* to =
+            a.o + p.b * a.stride_b + h * a.stride_h + static_cast<int64_t>(qt) * a.stride_n + 2 * q4;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          *reinterpret_cast<uint32_t*>(to + 8 * n) =
+              pack_bf16x2(o[n][2 * i] * inv, o[n][2 * i + 1] * inv);
+        if (q4 == 0)
+          a.lse[row] = sum == 0.f ? -INFINITY : a.pre_splits > 0 ? top + logf(sum) : L;
+      }
+    } else {
+      // ---- the slots' states merged: m, l per row, then O through shared memory
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        lrow[i] += __shfl_xor_sync(0xffffffffu, lrow[i], 1);
+        lrow[i] += __shfl_xor_sync(0xffffffffu, lrow[i], 2);
+        if (q4 == 0) {
+          sh.m[slot][rows[i]] = mrow[i];
+          sh.l[slot][rows[i]] = lrow[i];
         }
-        cluster_sync();   // the others have read this CTA's rows
-      } else {
-        for (int e = threadIdx.x; e < live * (D / 4); e += C::kThreads) {
-          const int rr = e / (D / 4), c = 4 * (e - rr * (D / 4)), r = 16 * m + rr;
-          const float4 x = *reinterpret_cast<const float4*>(&red[rr * C::kRedStride + c]);
-          if (whole) {
+      }
+      ok = __syncthreads_and(ok);
+      float scale[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float mx = -INFINITY, lt = 0.f;
+#pragma unroll
+        for (int w = 0; w < kSlots; ++w) mx = fmaxf(mx, sh.m[w][rows[i]]);
+#pragma unroll
+        for (int w = 0; w < kSlots; ++w) {
+          const float mw = sh.m[w][rows[i]];
+          if (mw != -INFINITY) lt += sh.l[w][rows[i]] * ex2_approx((mw - mx) * c2);
+        }
+        // this slot's weight, with the 1 / l folded in
+        scale[i] = mrow[i] == -INFINITY ? 0.f : ex2_approx((mrow[i] - mx) * c2) / lt;
+      }
+      const bool whole = p.whole();
+      const bool apart = a.pre_splits > 0;   // a prefix is merged afterwards
+      if constexpr (MODE == kSplit) {
+        if (p.t0 == 0 && !whole) note = paged_note<kPagedOverhead>(share, p);
+        if (a.by_segment && p.t0 == 0 && threadIdx.x == 0)
+          a.notes[p.b * a.heads + p.h] = whole ? MergeNote{p.b, p.h, 0, -1} : note;
+      }
+      const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (p.s < share.lo ? 0 : 1);
+      for (int m = 0; m < MT; ++m) {   // 16 rows at a time
+        for (int w = 0; w < kSlots; ++w) {   // in turn: the sum has a fixed order
+          if (slot == w && mt == m) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                float2* dst = reinterpret_cast<float2*>(&red[(g + 8 * i) * C::kRedStride + 8 * n + 2 * q4]);
+                float2 x = make_float2(o[n][2 * i] * scale[i], o[n][2 * i + 1] * scale[i]);
+                if (w > 0) {
+                  const float2 y = *dst;
+                  x.x += y.x;
+                  x.y += y.y;
+                }
+                *dst = x;
+              }
+          }
+          __syncthreads();
+        }
+        const int live = min(16, nrows - 16 * m);   // (none, perhaps)
+        auto logsumexp = [&](int r) {
+          float mx = -INFINITY, lt = 0.f;
+#pragma unroll
+          for (int w = 0; w < kSlots; ++w) mx = fmaxf(mx, sh.m[w][r]);
+#pragma unroll
+          for (int w = 0; w < kSlots; ++w) {
+            const float mw = sh.m[w][r];
+            if (mw != -INFINITY) lt += sh.l[w][r] * ex2_approx((mw - mx) * c2);
+          }
+          return lt == 0.f ? -INFINITY : fmaf(mx, a.scale, logf(lt));
+        };
+        if constexpr (CLUSTER) {
+          // the cluster's rows, and a prefix's pieces, merged: each CTA writes a
+          // part of the items
+          if (threadIdx.x < live) sh.L[threadIdx.x] = logsumexp(16 * m + threadIdx.x);
+          if (late) grid_dep_wait();
+          cluster_sync();
+          for (int e = rank * C::kThreads + threadIdx.x; e < live * (D / 4);
+               e += a.cluster * C::kThreads) {
+            const int rr = e / (D / 4), c = 4 * (e - rr * (D / 4)), r = 16 * m + rr;
             const int h = (row0 + r) / a.n_q, qt = row0 + r - h * a.n_q;
             const int64_t row = static_cast<int64_t>(p.b) * a.all_rows + row0 + r;
-            if (apart) {
-              const int64_t at = a.pre_splits * (static_cast<int64_t>(a.B) * a.all_rows) + row;
-              *reinterpret_cast<float4*>(a.pre_o + at * D + c) = x;
-              if (c == 0) a.pre_l[at] = logsumexp(r);
-              continue;
+            const int64_t all = static_cast<int64_t>(a.B) * a.all_rows;
+            float top = -INFINITY, sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int k = 0; k < a.cluster; ++k)
+              top = fmaxf(top, cluster_ld(cluster_addr(&sh.L[rr], k)));
+            for (int k = 0; k < a.pre_splits; ++k) top = fmaxf(top, a.pre_l[k * all + row]);
+            auto add = [&](float L, const float* y) {
+              const float w = __expf(L - top);
+              sum += w;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) x[i] = fmaf(w, y[i], x[i]);
+            };
+            if (top > -INFINITY) {
+              for (int k = 0; k < a.cluster; ++k) {
+                float y[4];
+                cluster_ld4(cluster_addr(&red[rr * C::kRedStride + c], k), y);
+                add(cluster_ld(cluster_addr(&sh.L[rr], k)), y);
+              }
+              for (int k = 0; k < a.pre_splits; ++k) {
+                const float4 y = *reinterpret_cast<const float4*>(a.pre_o + (k * all + row) * D + c);
+                const float z[4] = {y.x, y.y, y.z, y.w};
+                add(a.pre_l[k * all + row], z);
+              }
             }
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
             *reinterpret_cast<uint2*>(a.o + p.b * a.stride_b + h * a.stride_h +
                                       static_cast<int64_t>(qt) * a.stride_n + c) =
-                make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-            if (c == 0) a.lse[row] = logsumexp(r);
-          } else {
-            *reinterpret_cast<float4*>(a.part_o + (part * a.rows + r) * D + c) = x;
-            if (c == 0) a.part_l[part * a.rows + r] = logsumexp(r);
+                make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
+            if (c == 0) a.lse[row] = sum == 0.f ? -INFINITY : top + logf(sum);
           }
+          cluster_sync();   // the others have read this CTA's rows
+        } else {
+          for (int e = threadIdx.x; e < live * (D / 4); e += C::kThreads) {
+            const int rr = e / (D / 4), c = 4 * (e - rr * (D / 4)), r = 16 * m + rr;
+            const float4 x = *reinterpret_cast<const float4*>(&red[rr * C::kRedStride + c]);
+            if (whole) {
+              const int h = (row0 + r) / a.n_q, qt = row0 + r - h * a.n_q;
+              const int64_t row = static_cast<int64_t>(p.b) * a.all_rows + row0 + r;
+              if (apart) {
+                const int64_t at = a.pre_splits * (static_cast<int64_t>(a.B) * a.all_rows) + row;
+                *reinterpret_cast<float4*>(a.pre_o + at * D + c) = x;
+                if (c == 0) a.pre_l[at] = logsumexp(r);
+                continue;
+              }
+              *reinterpret_cast<uint2*>(a.o + p.b * a.stride_b + h * a.stride_h +
+                                        static_cast<int64_t>(qt) * a.stride_n + c) =
+                  make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+              if (c == 0) a.lse[row] = logsumexp(r);
+            } else {
+              *reinterpret_cast<float4*>(a.part_o + (part * a.rows + r) * D + c) = x;
+              if (c == 0) a.part_l[part * a.rows + r] = logsumexp(r);
+            }
+          }
+          __syncthreads();   // red (and after the last rows m, l) is free
         }
-        __syncthreads();   // red (and after the last rows m, l) is free
       }
     }
     if (!ok) break;
     p = next;
   }
-  if (!CLUSTER && !a.by_segment && threadIdx.x == 0) a.notes[blockIdx.x] = note;
-  if (!CLUSTER && late) grid_dep_wait();   // the merge waits for this kernel only
+  if (MODE == kSplit && !a.by_segment && threadIdx.x == 0) a.notes[blockIdx.x] = note;
+  if (late) grid_dep_wait();   // the merge, and whatever follows, waits for this kernel only
   if (!ok && mt == 0 && lane == 0) {   // let issued copies land before the CTA exits
     for (uint32_t t = issued > ST ? issued - ST : 0; t < issued; ++t)
       mbar_wait_drain(&sh.full[slot * ST + t % ST], (t / ST) & 1, a.timeout_ns);
@@ -616,7 +675,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_finish_kernel(const Paged
   if (live && threadIdx.x < kItems) write_row(a, note.b, hr, c, x, top, sum);
 }
 
-template <int D, int MT, bool CLUSTER>
+template <int D, int MT, PagedMode MODE>
 cudaError_t launch_mt(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, int ctas,
                       cudaStream_t s) {
   using C = PagedCfg<D, MT>;
@@ -626,34 +685,40 @@ cudaError_t launch_mt(const CUtensorMap& tk, const CUtensorMap& tv, const PagedA
   cudaError_t e = needs_setup(set_up, &dev, &todo);
   if (e != cudaSuccess) return e;
   if (todo) {
-    e = cudaFuncSetAttribute(paged_kernel<D, MT, CLUSTER>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    e = cudaFuncSetAttribute(paged_kernel<D, MT, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             C::kSmem);
     if (e != cudaSuccess) return e;
     mark_done(set_up, dev);
   }
-  if (CLUSTER)
-    return launch_clusters(paged_kernel<D, MT, CLUSTER>,
-                           dim3(static_cast<unsigned>(a.B * a.heads * a.cluster)), dim3(C::kThreads),
+  const unsigned segments = static_cast<unsigned>(a.B * a.heads);
+  if (MODE == kCluster)
+    return launch_clusters(paged_kernel<D, MT, MODE>, dim3(segments * a.cluster), dim3(C::kThreads),
                            C::kSmem, a.cluster, s, tk, tv, a);
-  return launch_pdl(paged_kernel<D, MT, CLUSTER>, dim3(ctas), dim3(C::kThreads), C::kSmem, s, tk, tv,
-                    a);
+  const unsigned grid = MODE == kSolo ? (segments + kSlots - 1) / kSlots : ctas;
+  return launch_pdl(paged_kernel<D, MT, MODE>, dim3(grid), dim3(C::kThreads), C::kSmem, s, tk, tv, a);
 }
 
-template <int D, bool CLUSTER>
+template <int D, PagedMode MODE>
 cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, int ctas,
                      cudaStream_t s) {
-  if (a.rows <= 16) return launch_mt<D, 1, CLUSTER>(tk, tv, a, ctas, s);
-  if (a.rows <= 32) return launch_mt<D, 2, CLUSTER>(tk, tv, a, ctas, s);
-  return launch_mt<D, 4, CLUSTER>(tk, tv, a, ctas, s);
+  if (a.rows <= 16) return launch_mt<D, 1, MODE>(tk, tv, a, ctas, s);
+  if (a.rows <= 32) return launch_mt<D, 2, MODE>(tk, tv, a, ctas, s);
+  return launch_mt<D, 4, MODE>(tk, tv, a, ctas, s);
+}
+
+template <int D>
+cudaError_t launch_mode(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, int ctas,
+                        cudaStream_t s) {
+  if (a.cluster == 1) return launch_d<D, kSolo>(tk, tv, a, ctas, s);
+  if (a.cluster > 1) return launch_d<D, kCluster>(tk, tv, a, ctas, s);
+  return launch_d<D, kSplit>(tk, tv, a, ctas, s);
 }
 
 }  // namespace
 
 cudaError_t launch_paged(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, int ctas,
                          cudaStream_t s) {
-  if (a.cluster > 0)
-    return a.d == 64 ? launch_d<64, true>(tk, tv, a, ctas, s) : launch_d<128, true>(tk, tv, a, ctas, s);
-  return a.d == 64 ? launch_d<64, false>(tk, tv, a, ctas, s) : launch_d<128, false>(tk, tv, a, ctas, s);
+  return a.d == 64 ? launch_mode<64>(tk, tv, a, ctas, s) : launch_mode<128>(tk, tv, a, ctas, s);
 }
 
 cudaError_t launch_paged_merge(const PagedArgs& a, int notes, cudaStream_t s) {

@@ -38,7 +38,9 @@ struct MergeNote {
 // Where the caches are short there is nothing to balance, and the merge's own
 // launch costs as much as the keys: then a segment falls to a cluster of CTAs,
 // each takes an equal part of its tiles, and they merge through their shared
-// memory (PagedArgs::cluster > 0; the note and the partials stay unused).
+// memory (PagedArgs::cluster > 0; the notes and the partials stay unused).  Of
+// many short ones each falls to one CTA, or (paged decode) to a part of one
+// (cluster == 1).
 struct PagedArgs {
   int B, H, heads;                // heads: segments per sequence, H_kv * blocks
   int blocks;                     // segments per key/value head (1 up to 64 query rows)
@@ -109,13 +111,16 @@ struct PrefixArgs {
 // share 6 or 9 units of 32 keys: one sequence of 517 keys 10.4 / 11.7 us; latent
 // 2 / 3 / 6 units of 64: 13.6 / 15.1 / 21.3 us with 700 tokens.  Clusters: at
 // most 24 / 48 key tiles a CTA (d = 128): 64 sequences of 200-800 keys 32.4 /
-// 34.5 us; at most 4 / 8 latent tiles: 3000 tokens 13.0 / 15.9 us.
+// 34.5 us; at most 4 / 8 latent tiles: 3000 tokens 13.0 / 15.9 us.  A segment
+// to itself for a slot up to 16 / 32 tiles: 64 sequences of 250-1000 keys 37.6 /
+// 41.0 us, of 125-500 keys 23.3 where 8 tiles give 25.8.
 constexpr int kPagedKeys = 32;        // keys per tile of the paged decode kernel
 constexpr int kPagedOverhead = 8;     // a segment's fixed cost in such tiles
 constexpr int kPagedMinUnits = 6;     // units a CTA takes at least
 constexpr int kLatentKeys = 64;       // keys per tile of the latent kernel
 constexpr int kLatentOverhead = 2;
 constexpr int kLatentMinUnits = 2;
+constexpr int kPagedSoloTiles = 16;      // ... of a slot that has a segment to itself
 constexpr int kPagedClusterTiles = 24;   // tiles of a cluster's CTA at most, at full caches
 constexpr int kLatentClusterTiles = 4;
 constexpr int kLatentRows = 64;       // query rows of one CTA
@@ -274,17 +279,18 @@ __device__ __forceinline__ PagedPiece paged_next(const PagedArgs& a, const Paged
   return paged_piece<KEYS, OVERHEAD>(a, sh, b, h, p.s + p.n + OVERHEAD);
 }
 
-// A cluster's CTA `rank`: its part of segment (b, h).
+// Part `rank` of `parts` of segment (b, h).
 template <int KEYS>
-__device__ __forceinline__ PagedPiece paged_part(const PagedArgs& a, int b, int h, int rank) {
+__device__ __forceinline__ PagedPiece paged_part(const PagedArgs& a, int b, int h, int rank,
+                                                 int parts) {
   PagedPiece p;
   p.b = b;
   p.h = h;
   p.len = paged_len(a, b);
   p.n = paged_tiles<KEYS>(a, b);
   p.s = 0;
-  p.t0 = static_cast<int>(static_cast<int64_t>(p.n) * rank / a.cluster);
-  p.t1 = static_cast<int>(static_cast<int64_t>(p.n) * (rank + 1) / a.cluster);
+  p.t0 = static_cast<int>(static_cast<int64_t>(p.n) * rank / parts);
+  p.t1 = static_cast<int>(static_cast<int64_t>(p.n) * (rank + 1) / parts);
   p.valid = true;
   return p;
 }

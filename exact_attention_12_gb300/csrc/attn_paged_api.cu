@@ -175,14 +175,15 @@ Layout layout(const attn_params* p, int32_t n_q, const attn_pages* g, bool laten
   }
   // short caches: a cluster per segment, of as many CTAs as the GPU holds at
   // once and as have a tile for each slot (latent: a tile), if that leaves each
-  // few tiles
+  // few tiles; a slot of a CTA per segment where more find no place
   const int64_t segments = segments_of(p, L);
   {
     int c = 8;
     while (c > 1 && (segments * c > room || c > (tiles + (latent ? 0 : 2)) / (latent ? 1 : 3))) c /= 2;
-    if (tiles <= static_cast<int64_t>(c) *
-                     (latent ? attn::kLatentClusterTiles : attn::kPagedClusterTiles))
-      L.cluster = c;
+    const int64_t each = latent   ? attn::kLatentClusterTiles
+                         : c == 1 ? attn::kPagedSoloTiles
+                                  : attn::kPagedClusterTiles;
+    if (tiles <= c * each) L.cluster = c;
   }
   L.by_segment = L.first > 0 || segments <= L.ctas;
   L.n_notes = L.by_segment ? static_cast<int>(segments) : L.ctas;

@@ -138,6 +138,16 @@ def test_many_short_and_one_long(ea):
     _run(ea, [5] * 130 + [4000] + [0] * 70, 4, 2, 1, 64, 16, seed=10)
 
 
+@pytest.mark.parametrize("H,n_q", [(4, 1), (12, 2), (20, 5), (40, 7)])
+@pytest.mark.parametrize("shared", [0, 48])
+def test_many_short_sequences(ea, H, n_q, shared):
+    # more segments than the GPU holds CTAs, few tiles each: one slot of a CTA per segment
+    rng = np.random.default_rng(H)
+    lens = [int(shared + x) for x in rng.integers(0, 200, 81)]
+    lens[3], lens[80] = shared, shared + 200
+    _run(ea, lens, H, 4, n_q, 64, 16, True, shared, seed=H)
+
+
 def test_large_scores(ea):
     # scores to +-100: the running maximum has to hold
     _run(ea, [500, 64], 4, 2, 2, 64, 32, scale=4.0, seed=11)

@@ -30,7 +30,7 @@ def test_paged(ea, seed):
     group = int(rng.choice([1, 2, 4, 5, 8]))
     n_q = int(rng.choice([1, 1, 2, 3, 7]))
     page = int(rng.choice([16, 32, 64, 128, 256]))
-    B = int(rng.choice([1, 2, 3, 9, 40]))
+    B = int(rng.choice([1, 2, 3, 9, 40, 160]))
     most = int(rng.choice([1, 40, 130, 700, 1500])) if B < 40 else int(rng.choice([3, 50, 200]))
     shared = page * int(rng.integers(0, 5)) if seed % 2 else 0
     lens = [x + shared for x in _lens(rng, B, most)]
