@@ -50,7 +50,7 @@ attn_status validate(const attn_params* p, int32_t n_q, const attn_pages* g, boo
     return fail(ATTN_ERR_INVALID_ARG, "scale must be positive and finite");
   if (p->dropout_p != 0.f || p->block_mask != nullptr)
     return fail(ATTN_ERR_UNSUPPORTED, "decode takes no dropout and no block mask");
-  if (p->key_lens == nullptr)
+  if (p->key_lens == nullptr && p->B > 0)
     return fail(ATTN_ERR_INVALID_ARG, "decode needs key_lens (cache lengths)");
   if (n_q < 1) return fail(ATTN_ERR_INVALID_ARG, "n_q must be >= 1");
   const int H_kv = latent ? 1 : (p->H_kv == 0 ? p->H : p->H_kv);
@@ -142,7 +142,7 @@ Layout layout(const attn_params* p, int32_t n_q, const attn_pages* g, bool laten
     L.heads = 1;
     L.head_rows = p->H * n_q;
     L.rows = static_cast<int>(groups * attn::kLatentRows);
-    most = sms / groups;
+    most = groups > 0 ? sms / groups : 1;
   } else {
     // more than 64 rows of a key/value head: in equal blocks, each of which
     // reads the keys

@@ -133,6 +133,17 @@ def test_pointers_and_workspace_are_checked(abi, latent):
     assert _status(abi, p, g, n_q, latent, nb=1 << 20, ptr=None) == abi.ATTN_OK
 
 
+@pytest.mark.parametrize("latent", [False, True])
+@pytest.mark.parametrize("none", [dict(H=0), dict(B=0, key_lens=None, table=None), dict(B=0, H=0)])
+def test_no_heads_or_no_sequences(abi, latent, none):
+    # nothing to do, whatever the pointers are; the sizes divide by nothing
+    p, g, n_q = _decode(abi, latent=latent, **none)
+    lib = abi.lib()
+    size = lib.attn_decode_latent_workspace_size if latent else lib.attn_decode_paged_workspace_size
+    assert size(ctypes.byref(p), n_q, ctypes.byref(g)) >= 256
+    assert _status(abi, p, g, n_q, latent, nb=1 << 20, ptr=None) == abi.ATTN_OK
+
+
 def _table(abi, **kw):
     t = abi.AttnPageTable(0x1000, 8, 0x1000, 0x1000, 4, 8, 16, 20)
     for k, v in kw.items():
