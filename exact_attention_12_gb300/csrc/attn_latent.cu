@@ -73,7 +73,7 @@ struct LatentCfg {
   // bf16 either way): its scores are complete when P is written
   static constexpr int kPOffset = (kBoxes - 1) * kBoxBytes;
   static constexpr int kSmem = (1 + kStages) * kTileBytes;
-  static constexpr int kCtl = 3072;                       // LatentCtl, in whole kilobytes
+  static constexpr int kCtl = 3 * 1024;                   // LatentCtl, in whole kilobytes
   static_assert(kSmem + kCtl <= 227 * 1024, "shared memory of a CTA");
   // warpgroups 0, 1: the eight warps of the softmax; warpgroup 2: copies, MMA
   // issue, two idle warps.  Registers re-split after the start: 256 * 216 +
@@ -296,8 +296,10 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
       // which groups of tile i have landed: all of them?
       auto landed = [&](int i) {
         const uint32_t u = T + i;
-        return __all_sync(0xffffffffu, lane >= C::kGroups ||
-                                           mbar_test(&ctl.full[u % ST][lane], (u / ST) & 1)) != 0;
+        const bool all = __all_sync(0xffffffffu, lane >= C::kGroups ||
+                                                     mbar_test(&ctl.full[u % ST][lane], (u / ST) & 1));
+        __syncwarp();   // what these lanes have seen the issuing lane may use
+        return all;
       };
       auto scores = [&](int i, bool all) {
         const uint32_t u = T + i, s = u % ST;
@@ -632,15 +634,15 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
       const int r = e / (DV / 4), c = 4 * (e - r * (DV / 4));
       float top = -INFINITY, sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
       for (int k = 0; k < a.cluster; ++k) top = fmaxf(top, cluster_ld(cluster_addr(&ctl.L[r], k)));
-      if (top > -INFINITY)
-        for (int k = 0; k < a.cluster; ++k) {
-          float y[4];
-          cluster_ld4(cluster_addr(o + r * DV + c, k), y);
-          const float w = __expf(cluster_ld(cluster_addr(&ctl.L[r], k)) - top);
-          sum += w;
+      top = merge_base(top);
+      for (int k = 0; k < a.cluster; ++k) {
+        float y[4];
+        cluster_ld4(cluster_addr(o + r * DV + c, k), y);
+        const float w = __expf(cluster_ld(cluster_addr(&ctl.L[r], k)) - top);
+        sum += w;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = fmaf(w, y[i], x[i]);
-        }
+        for (int i = 0; i < 4; ++i) x[i] = fmaf(w, y[i], x[i]);
+      }
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       const int64_t row = static_cast<int64_t>(cta) * a.all_rows + r0 + r;
       *reinterpret_cast<uint2*>(a.o + row * DV + c) =

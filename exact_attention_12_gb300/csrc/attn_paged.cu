@@ -368,26 +368,26 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
         const float L = l == 0.f ? -INFINITY : fmaf(mrow[i], a.scale, logf(l));
         float top = L;
         for (int k = 0; k < a.pre_splits; ++k) top = fmaxf(top, a.pre_l[k * all + row]);
+        top = merge_base(top);
         // (without a prefix the weight is 1)
-        float sum = top == -INFINITY ? 0.f : a.pre_splits > 0 ? __expf(L - top) : 1.f;
+        float sum = a.pre_splits > 0 ? __expf(L - top) : L == -INFINITY ? 0.f : 1.f;
         const float own = sum == 0.f ? 0.f : sum / l;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           o[n][2 * i] *= own;
           o[n][2 * i + 1] *= own;
         }
-        if (top > -INFINITY)
-          for (int k = 0; k < a.pre_splits; ++k) {
-            const float w = __expf(a.pre_l[k * all + row] - top);
-            const float* y = a.pre_o + (k * all + row) * D + 2 * q4;
-            sum += w;
+        for (int k = 0; k < a.pre_splits; ++k) {
+          const float w = __expf(a.pre_l[k * all + row] - top);
+          const float* y = a.pre_o + (k * all + row) * D + 2 * q4;
+          sum += w;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              const float2 z = *reinterpret_cast<const float2*>(y + 8 * n);
-              o[n][2 * i] = fmaf(w, z.x, o[n][2 * i]);
-              o[n][2 * i + 1] = fmaf(w, z.y, o[n][2 * i + 1]);
-            }
+          for (int n = 0; n < NT; ++n) {
+            const float2 z = *reinterpret_cast<const float2*>(y + 8 * n);
+            o[n][2 * i] = fmaf(w, z.x, o[n][2 * i]);
+            o[n][2 * i + 1] = fmaf(w, z.y, o[n][2 * i + 1]);
           }
+        }
         const float inv = sum == 0.f ? 0.f : a.pre_splits > 0 ? 1.f / sum : 1.f;
         __nv_bfloat16* to =
             a.o + p.b * a.stride_b + h * a.stride_h + static_cast<int64_t>(qt) * a.stride_n + 2 * q4;
@@ -404,6 +404,7 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
       for (int i = 0; i < 2; ++i) {
         lrow[i] += __shfl_xor_sync(0xffffffffu, lrow[i], 1);
         lrow[i] += __shfl_xor_sync(0xffffffffu, lrow[i], 2);
+        if (lrow[i] != lrow[i]) mrow[i] = 0.f;   // a row of NaN scores has seen keys
         if (q4 == 0) {
           sh.m[slot][rows[i]] = mrow[i];
           sh.l[slot][rows[i]] = lrow[i];
@@ -479,23 +480,22 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
             for (int k = 0; k < a.cluster; ++k)
               top = fmaxf(top, cluster_ld(cluster_addr(&sh.L[rr], k)));
             for (int k = 0; k < a.pre_splits; ++k) top = fmaxf(top, a.pre_l[k * all + row]);
+            top = merge_base(top);
             auto add = [&](float L, const float* y) {
               const float w = __expf(L - top);
               sum += w;
 #pragma unroll
               for (int i = 0; i < 4; ++i) x[i] = fmaf(w, y[i], x[i]);
             };
-            if (top > -INFINITY) {
-              for (int k = 0; k < a.cluster; ++k) {
-                float y[4];
-                cluster_ld4(cluster_addr(&red[rr * C::kRedStride + c], k), y);
-                add(cluster_ld(cluster_addr(&sh.L[rr], k)), y);
-              }
-              for (int k = 0; k < a.pre_splits; ++k) {
-                const float4 y = *reinterpret_cast<const float4*>(a.pre_o + (k * all + row) * D + c);
-                const float z[4] = {y.x, y.y, y.z, y.w};
-                add(a.pre_l[k * all + row], z);
-              }
+            for (int k = 0; k < a.cluster; ++k) {
+              float y[4];
+              cluster_ld4(cluster_addr(&red[rr * C::kRedStride + c], k), y);
+              add(cluster_ld(cluster_addr(&sh.L[rr], k)), y);
+            }
+            for (int k = 0; k < a.pre_splits; ++k) {
+              const float4 y = *reinterpret_cast<const float4*>(a.pre_o + (k * all + row) * D + c);
+              const float z[4] = {y.x, y.y, y.z, y.w};
+              add(a.pre_l[k * all + row], z);
             }
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             *reinterpret_cast<uint2*>(a.o + p.b * a.stride_b + h * a.stride_h +
@@ -548,7 +548,7 @@ struct Partial {
 constexpr int kMergeThreads = 256;
 
 // Four columns of a row's O merged from `n` partials, O = sum e^(L_i - L) O_i,
-// and the parts of L = log sum e^(L_i) = top + log(sum).  GROUPS threads share
+// and the parts of L = log sum e^(L_i) = top + log(sum) (-inf if sum = 0).  GROUPS threads share
 // an item (threads kMergeThreads / GROUPS apart), each takes every GROUPS-th
 // partial; the first has the result.  `live`: the item exists.  The whole CTA.
 template <int GROUPS, typename From>
@@ -570,18 +570,17 @@ __device__ __forceinline__ void merge_row(bool live, int n, const From& from, fl
 #pragma unroll
     for (int k = 0; k < GROUPS; ++k) top = fmaxf(top, tops[item + k * kItems]);
   }
-  if (top > -INFINITY) {
+  top = merge_base(top);
 #pragma unroll 4
-    for (int i = group; i < n; i += GROUPS) {
-      const Partial part = from(i);
-      const float w = __expf(*part.l - top);
-      const float4 y = *reinterpret_cast<const float4*>(part.o);
-      sum += w;
-      x.x = fmaf(w, y.x, x.x);
-      x.y = fmaf(w, y.y, x.y);
-      x.z = fmaf(w, y.z, x.z);
-      x.w = fmaf(w, y.w, x.w);
-    }
+  for (int i = group; i < n; i += GROUPS) {
+    const Partial part = from(i);
+    const float w = __expf(*part.l - top);
+    const float4 y = *reinterpret_cast<const float4*>(part.o);
+    sum += w;
+    x.x = fmaf(w, y.x, x.x);
+    x.y = fmaf(w, y.y, x.y);
+    x.z = fmaf(w, y.z, x.z);
+    x.w = fmaf(w, y.w, x.w);
   }
   if constexpr (GROUPS > 1) {
     sums[threadIdx.x] = sum;

@@ -134,6 +134,11 @@ enum PagedSite : int {
   kSitePageIndex = 80
 };
 
+// What the weights of a merge, e^(L_i - base), are taken against: the largest
+// L_i, or 0 where all are -inf (no keys: the weights and partials are 0) or NaN
+// (which fmaxf passes over, and the weights then carry).
+__device__ __forceinline__ float merge_base(float top) { return top == -INFINITY ? 0.f : top; }
+
 __device__ __forceinline__ int paged_len(const PagedArgs& a, int b) {
   return min(max(a.key_lens[b], 0), a.cap);
 }

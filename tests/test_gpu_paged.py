@@ -316,6 +316,49 @@ def test_bad_page_is_reported_and_reads_as_zeros(ea):
         ea.check()
 
 
+def _nan_rows(call, q, b, h, t):
+    """A NaN in one query row shows in all of that row's results and nowhere else."""
+    o, lse = call(q)
+    bad = q.clone()
+    bad[b, h, t, 3] = float("nan")
+    o2, lse2 = call(bad)
+    hit = torch.zeros(q.shape[:3], dtype=torch.bool, device="cuda")
+    hit[b, h, t] = True
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+    assert torch.isnan(o2[hit]).all() and torch.isnan(lse2[hit]).all()
+    assert torch.equal(o2[~hit], o[~hit]) and torch.equal(lse2[~hit], lse[~hit])
+
+
+# one CTA per segment and cut ones, clusters, many short sequences; with a prefix each
+@pytest.mark.parametrize("lens,room", [([200, 1500, 40], WIDE), ([200, 300, 40], 0),
+                                       ([40 + i for i in range(90)], 0)])
+@pytest.mark.parametrize("shared", [0, 32])
+@pytest.mark.parametrize("n_q", [1, 5])
+def test_a_nan_query_is_not_hidden(ea, lens, room, shared, n_q):
+    rng, g = np.random.default_rng(7), torch.Generator().manual_seed(7)
+    table, P = _table(rng, lens, 16, shared=shared, room=room)
+    k, v = (torch.randn(P, 4, 16, 64, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    q = torch.randn(len(lens), 16, n_q, 64, generator=g).to(torch.bfloat16).cuda()
+    t, n = torch.from_numpy(table).cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    for b in range(min(3, len(lens))):
+        _nan_rows(lambda x: ea.attention_decode_paged(x, k, v, t, n, shared_len=shared), q, b, 5,
+                  n_q - 1)
+    ea.check()
+
+
+@pytest.mark.parametrize("lens,room,H", [([200, 1500, 40], WIDE, 8), ([200, 1500, 40], WIDE, 128),
+                                         ([200, 250, 40], 0, 8), ([200, 250, 40], 0, 70)])
+def test_a_nan_latent_query_is_not_hidden(ea, lens, room, H):
+    rng, g = np.random.default_rng(8), torch.Generator().manual_seed(8)
+    table, P = _table(rng, lens, 16, room=room)
+    c = torch.randn(P, 16, 576, generator=g).to(torch.bfloat16).cuda()
+    q = torch.randn(len(lens), H, 2, 576, generator=g).to(torch.bfloat16).cuda()
+    t, n = torch.from_numpy(table).cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    for b in range(3):
+        _nan_rows(lambda x: ea.attention_decode_latent(x, c, t, n, scale=0.04), q, b, H - 3, 1)
+    ea.check()
+
+
 @pytest.mark.parametrize("room", [0, WIDE])
 def test_replayed_graph_follows_lengths_and_tables(ea, room):
     """Captured once, replayed with other lengths, pages and queries."""
