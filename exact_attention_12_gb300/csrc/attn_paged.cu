@@ -32,6 +32,8 @@
 // queries, 64 heads over 8, 2.2 GB in 334 us = 6.5 TB/s; one sequence of 517
 // keys 8.2 us, two reads of lengths and pages, a tile's copy and the merge one
 // after another.  DRAM traffic is the algorithmic bytes plus 1 %.
+#include <type_traits>
+
 #include "attn_paged.cuh"
 
 namespace attn {
@@ -546,55 +548,82 @@ struct Partial {
 };
 
 constexpr int kMergeThreads = 256;
+// pieces of a segment that sixteen threads share (one sequence of 100000 latent
+// vectors: 34.1 us a step, with four threads 41.4; two sequences of 30000 keys,
+// 64 rows: 26.2 against 29.5; 6 or 12 pieces are alike)
+constexpr int kMergeMany = 6;
 
 // Four columns of a row's O merged from `n` partials, O = sum e^(L_i - L) O_i,
-// and the parts of L = log sum e^(L_i) = top + log(sum) (-inf if sum = 0).  GROUPS threads share
-// an item (threads kMergeThreads / GROUPS apart), each takes every GROUPS-th
-// partial; the first has the result.  `live`: the item exists.  The whole CTA.
+// and the parts of L = log sum e^(L_i) = top + log(sum) (-inf if sum = 0).
+// GROUPS threads share an item (threads kMergeThreads / GROUPS apart), each
+// takes every GROUPS-th partial, two of them at once so that their L
+// and O are on the way together, with a running maximum; the first thread has
+// the result.  `live`: the item exists.  The whole CTA.
 template <int GROUPS, typename From>
 __device__ __forceinline__ void merge_row(bool live, int n, const From& from, float4& x, float& top,
                                           float& sum) {
-  constexpr int kItems = kMergeThreads / GROUPS;
-  __shared__ float tops[GROUPS > 1 ? kMergeThreads : 1], sums[GROUPS > 1 ? kMergeThreads : 1];
-  __shared__ float4 xs[GROUPS > 1 ? kMergeThreads : 1];
+  constexpr int kItems = kMergeThreads / GROUPS, kAtOnce = 2;
   const int group = threadIdx.x / kItems, item = threadIdx.x % kItems;
   if (!live) n = 0;
   x = make_float4(0.f, 0.f, 0.f, 0.f);
-  top = -INFINITY;
-  sum = 0.f;
-#pragma unroll 4
-  for (int i = group; i < n; i += GROUPS) top = fmaxf(top, *from(i).l);
-  if constexpr (GROUPS > 1) {
-    tops[threadIdx.x] = top;
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < GROUPS; ++k) top = fmaxf(top, tops[item + k * kItems]);
-  }
-  top = merge_base(top);
-#pragma unroll 4
-  for (int i = group; i < n; i += GROUPS) {
-    const Partial part = from(i);
-    const float w = __expf(*part.l - top);
-    const float4 y = *reinterpret_cast<const float4*>(part.o);
-    sum += w;
+  float most = -INFINITY;
+  top = sum = 0.f;
+  // what is there weighs e^(before - top), then w y comes on top
+  auto scale = [&](float before) {
+    top = merge_base(most);
+    const float w = __expf(before - top);
+    sum *= w;
+    x.x *= w;
+    x.y *= w;
+    x.z *= w;
+    x.w *= w;
+  };
+  auto add = [&](float w, float s, const float4& y) {
+    sum = fmaf(w, s, sum);
     x.x = fmaf(w, y.x, x.x);
     x.y = fmaf(w, y.y, x.y);
     x.z = fmaf(w, y.z, x.z);
     x.w = fmaf(w, y.w, x.w);
+  };
+  for (int i0 = group; i0 < n; i0 += GROUPS * kAtOnce) {
+    float l[kAtOnce];
+    float4 y[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const bool in = i0 + k * GROUPS < n;
+      l[k] = -INFINITY;
+      y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (in) {
+        const Partial part = from(i0 + k * GROUPS);
+        l[k] = *part.l;
+        y[k] = *reinterpret_cast<const float4*>(part.o);
+      }
+    }
+    const float before = most;
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) most = fmaxf(most, l[k]);
+    scale(before);
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) add(__expf(l[k] - top), 1.f, y[k]);
   }
   if constexpr (GROUPS > 1) {
-    sums[threadIdx.x] = sum;
-    xs[threadIdx.x] = x;
+    __shared__ float mosts[kMergeThreads], sums[kMergeThreads];
+    __shared__ float4 xs[kMergeThreads];
+    if (group > 0) {
+      mosts[threadIdx.x] = most;
+      sums[threadIdx.x] = sum;
+      xs[threadIdx.x] = x;
+    }
     __syncthreads();
     if (group == 0) {
+      const float before = most;
+#pragma unroll
+      for (int k = 1; k < GROUPS; ++k) most = fmaxf(most, mosts[item + k * kItems]);
+      scale(before);
 #pragma unroll
       for (int k = 1; k < GROUPS; ++k) {
-        const float4 y = xs[item + k * kItems];
-        sum += sums[item + k * kItems];
-        x.x += y.x;
-        x.y += y.y;
-        x.z += y.z;
-        x.w += y.w;
+        const int at = item + k * kItems;
+        add(__expf(mosts[at] - top), sums[at], xs[at]);
       }
     }
   }
@@ -720,31 +749,51 @@ cudaError_t launch_paged(const CUtensorMap& tk, const CUtensorMap& tv, const Pag
   return a.d == 64 ? launch_mode<64>(tk, tv, a, ctas, s) : launch_mode<128>(tk, tv, a, ctas, s);
 }
 
-cudaError_t launch_paged_merge(const PagedArgs& a, int notes, cudaStream_t s) {
-  // Four threads an item while the items are too few to fill the GPU: 16
-  // sequences of 4096 latent vectors, 16 heads (32 K items of 10 pieces) 26.2
-  // against 28.6 us a step, but with 64 heads (131 K items) 39.6 against 36.4.
-  const int64_t items = static_cast<int64_t>(notes) * min(a.rows, a.all_rows) * (a.d / 4);
-  const bool groups = items <= (1 << 16);
-  const int per = groups ? kMergeThreads / 4 : kMergeThreads;
-  const dim3 grid(static_cast<unsigned>(notes),
-                  static_cast<unsigned>((min(a.rows, a.all_rows) * (a.d / 4) + per - 1) / per));
-  auto kernel = a.d == 64    ? (groups ? paged_merge_kernel<64, 4> : paged_merge_kernel<64, 1>)
-                : a.d == 128 ? (groups ? paged_merge_kernel<128, 4> : paged_merge_kernel<128, 1>)
-                : a.d == 256 ? (groups ? paged_merge_kernel<256, 4> : paged_merge_kernel<256, 1>)
-                             : (groups ? paged_merge_kernel<512, 4> : paged_merge_kernel<512, 1>);
-  return launch_pdl(kernel, grid, dim3(kMergeThreads), 0, s, a);
+namespace {
+
+template <int GROUPS>
+using Groups = std::integral_constant<int, GROUPS>;
+
+// `go` with the number of threads that share an item, 16, 4 or 1: 16 where a
+// segment has many pieces (kMergeMany), which one thread would read one
+// after the other, and the items are few; 4 if `some`.
+template <typename Go>
+cudaError_t with_groups(int64_t items, int64_t pieces, bool some, const Go& go) {
+  if (pieces >= kMergeMany && items <= (1 << 14)) return go(Groups<16>());
+  return some ? go(Groups<4>()) : go(Groups<1>());
 }
 
-cudaError_t launch_paged_finish(const PagedArgs& a, cudaStream_t s) {
-  // (109 against 115 us a step with 9 pieces of the prefix and 131 K items)
-  const bool groups = a.pre_splits >= 3;
-  const int per = groups ? kMergeThreads / 4 : kMergeThreads;
-  const dim3 grid(static_cast<unsigned>(a.B * a.heads),
-                  static_cast<unsigned>((a.rows * (a.d / 4) + per - 1) / per));
-  auto kernel = a.d == 64 ? (groups ? paged_finish_kernel<64, 4> : paged_finish_kernel<64, 1>)
-                          : (groups ? paged_finish_kernel<128, 4> : paged_finish_kernel<128, 1>);
-  return launch_pdl(kernel, grid, dim3(kMergeThreads), 0, s, a);
+}  // namespace
+
+cudaError_t launch_paged_merge(const PagedArgs& a, int notes, int ctas, cudaStream_t s) {
+  // Four threads an item while the items are too few to fill the GPU: 16
+  // sequences of 4096 latent vectors, 16 heads (32 K items of 10 pieces) 25.1
+  // against 27.1 us a step, but with 64 heads (131 K items) 38.3 against 35.6.
+  const int rows = min(a.rows, a.all_rows);
+  const int64_t items = static_cast<int64_t>(notes) * rows * (a.d / 4);
+  return with_groups(items, a.by_segment ? ctas / notes : 1, items <= (1 << 16), [&](auto g) {
+    constexpr int kGroups = decltype(g)::value, kPer = kMergeThreads / kGroups;
+    const dim3 grid(static_cast<unsigned>(notes),
+                    static_cast<unsigned>((rows * (a.d / 4) + kPer - 1) / kPer));
+    auto kernel = a.d == 64    ? paged_merge_kernel<64, kGroups>
+                  : a.d == 128 ? paged_merge_kernel<128, kGroups>
+                  : a.d == 256 ? paged_merge_kernel<256, kGroups>
+                               : paged_merge_kernel<512, kGroups>;
+    return launch_pdl(kernel, grid, dim3(kMergeThreads), 0, s, a);
+  });
+}
+
+cudaError_t launch_paged_finish(const PagedArgs& a, int ctas, cudaStream_t s) {
+  // (92 against 93 us a step with 9 pieces of the prefix and 131 K items)
+  const int segments = a.B * a.heads;
+  const int64_t items = static_cast<int64_t>(segments) * a.rows * (a.d / 4);
+  return with_groups(items, a.pre_splits + ctas / segments, a.pre_splits >= 3, [&](auto g) {
+    constexpr int kGroups = decltype(g)::value, kPer = kMergeThreads / kGroups;
+    const dim3 grid(static_cast<unsigned>(segments),
+                    static_cast<unsigned>((a.rows * (a.d / 4) + kPer - 1) / kPer));
+    auto kernel = a.d == 64 ? paged_finish_kernel<64, kGroups> : paged_finish_kernel<128, kGroups>;
+    return launch_pdl(kernel, grid, dim3(kMergeThreads), 0, s, a);
+  });
 }
 
 }  // namespace attn

@@ -333,8 +333,8 @@ cudaError_t launch_paged(const CUtensorMap& tk, const CUtensorMap& tv, const Pag
 cudaError_t launch_prefix(const CUtensorMap& tk, const CUtensorMap& tv, const PrefixArgs& a,
                           cudaStream_t s);
 cudaError_t launch_latent(const CUtensorMap& tc, const PagedArgs& a, int ctas, cudaStream_t s);
-cudaError_t launch_paged_merge(const PagedArgs& a, int notes, cudaStream_t s);
-cudaError_t launch_paged_finish(const PagedArgs& a, cudaStream_t s);
+cudaError_t launch_paged_merge(const PagedArgs& a, int notes, int ctas, cudaStream_t s);
+cudaError_t launch_paged_finish(const PagedArgs& a, int ctas, cudaStream_t s);
 
 // Tensor map of a paged cache for the host code (an attn_status).
 int encode_pages(CUtensorMap* map, const void* ptr, int num_pages, int heads, int page_size, int d,

@@ -324,9 +324,9 @@ attn_status attn_decode_paged(const attn_params* p, int32_t n_q, const attn_page
   if ((st = launched(attn::launch_paged(tk, tv, a, L.ctas, s), "paged decode launch")) != ATTN_OK)
     return st;
   if (L.cluster > 0) return ATTN_OK;   // merged already
-  if (L.first > 0) return launched(attn::launch_paged_finish(a, s), "shared prefix merge launch");
+  if (L.first > 0) return launched(attn::launch_paged_finish(a, L.ctas, s), "shared prefix merge launch");
   if (L.ctas == 1) return ATTN_OK;   // one CTA cuts nothing
-  return launched(attn::launch_paged_merge(a, L.n_notes, s), "paged merge launch");
+  return launched(attn::launch_paged_merge(a, L.n_notes, L.ctas, s), "paged merge launch");
 }
 
 size_t attn_decode_latent_workspace_size(const attn_params* p, int32_t n_q,
@@ -361,7 +361,7 @@ attn_status attn_decode_latent(const attn_params* p, int32_t n_q, const attn_pag
   a.stride_n = p->d;
   a.stride_h = static_cast<int64_t>(n_q) * p->d;
   a.stride_b = static_cast<int64_t>(p->H) * n_q * p->d;
-  return launched(attn::launch_paged_merge(a, L.n_notes, s), "latent merge launch");
+  return launched(attn::launch_paged_merge(a, L.n_notes, L.ctas, s), "latent merge launch");
 }
 
 }  // extern "C"

@@ -134,6 +134,14 @@ def test_one_long_sequence_over_all_ctas(ea):
     _run(ea, [9001], 4, 1, 1, 128, 64, seed=9)
 
 
+@pytest.mark.parametrize("lens,H,H_kv,n_q,d,shared", [
+    ([20000], 2, 1, 1, 64, 0), ([6001, 5999], 64, 1, 1, 128, 0), ([9000, 40], 4, 1, 3, 64, 0),
+    ([5000, 4100], 4, 2, 2, 64, 1024), ([2100, 2048], 33, 1, 1, 128, 2048)])
+def test_few_sequences_in_many_pieces(ea, lens, H, H_kv, n_q, d, shared):
+    # sixteen threads share a merge's items, in rounds, a thread's pieces two at a time
+    _run(ea, lens, H, H_kv, n_q, d, 32, True, shared, seed=12, room=WIDE)
+
+
 def test_many_short_and_one_long(ea):
     _run(ea, [5] * 130 + [4000] + [0] * 70, 4, 2, 1, 64, 16, seed=10)
 
@@ -230,6 +238,11 @@ def test_latent_pages(ea, page, causal, room):
 
 def test_latent_long_and_ragged(ea):
     _run_latent(ea, [5000, 3, 700, 0, 0, 90], 16, 1, 512, 64, seed=2)
+
+
+@pytest.mark.parametrize("lens,H,d_v", [([20000], 5, 256), ([15000, 3], 16, 512), ([7000], 64, 256)])
+def test_latent_few_sequences_in_many_pieces(ea, lens, H, d_v):
+    _run_latent(ea, lens, H, 1, d_v, 64, seed=13, room=WIDE)
 
 
 @pytest.mark.parametrize("room", [0, WIDE])
