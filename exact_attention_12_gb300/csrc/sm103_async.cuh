@@ -54,6 +54,26 @@ __device__ __forceinline__ void cluster_ld4(uint32_t addr, float* x) {
                : "memory");
 }
 
+// How L2 treats what a copy brings in: as other data, or, for data that is read
+// once, the first to make place.
+__device__ __forceinline__ uint64_t l2_policy(bool once) {
+  uint64_t normal, first;
+  asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(normal));
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(first));
+  return once ? first : normal;
+}
+
+// tma_load_4d with such a policy.
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int c0, int c1, int c2, int c3, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2),
+      "r"(c3), "l"(policy)
+      : "memory");
+}
+
 // tma_load_4d into every CTA of the cluster that `mask` names, at the same
 // shared-memory address and counted on the same barrier of each.
 __device__ __forceinline__ void tma_load_4d_multicast(void* dst, const CUtensorMap* map,
