@@ -130,6 +130,18 @@ def test_empty_sequences(ea, room):
     assert torch.all(o == 0) and torch.all(torch.isneginf(lse))
 
 
+def test_no_sequences(ea):
+    i32 = dict(dtype=torch.int32, device="cuda")
+    k = torch.zeros(3, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
+    t, n = torch.zeros(0, 4, **i32), torch.zeros(0, **i32)
+    o, lse = ea.attention_decode_paged(k.new_zeros(0, 4, 1, 64), k, k, t, n)
+    assert o.shape == (0, 4, 1, 64) and lse.shape == (0, 4, 1)
+    o, lse = ea.attention_decode_latent(k.new_zeros(0, 4, 2, 320), k.new_zeros(3, 16, 320), t, n,
+                                        scale=0.1, d_v=256)
+    assert o.shape == (0, 4, 2, 256) and lse.shape == (0, 4, 2)
+    ea.check()
+
+
 def test_one_long_sequence_over_all_ctas(ea):
     _run(ea, [9001], 4, 1, 1, 128, 64, seed=9)
 
