@@ -43,11 +43,11 @@
 //
 // Measured (d_v = 512, whole steps replayed from a CUDA graph): up to 64 rows
 // the kernel streams at the copy rate once it runs (16 sequences, 16 heads:
-// 16384 more tokens each cost 44 us = 6.8 TB/s); what remains is 12 us of
-// set-up, first and last tiles and the merge (4096 tokens each: 27 us).  With
+// 16384 more tokens each cost 44 us = 6.8 TB/s); what remains is 14 us of
+// set-up, first and last tiles and the merge (4096 tokens each: 25 us).  With
 // 128 rows each tile is worked on by two CTAs, and shared memory bounds it: a
 // tile's operand reads, its copy and P take 2600 cycles of its bandwidth, its
-// MMAs 2000, and a tile takes 3000 (64 sequences of 4096-8192 tokens: 169 us,
+// MMAs 2000, and a tile takes 3000 (64 sequences of 4096-8192 tokens: 167 us,
 // where the tokens' bytes need 69 and the operations 58).
 #include "attn_paged.cuh"
 

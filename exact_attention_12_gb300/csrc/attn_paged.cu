@@ -28,8 +28,8 @@
 //
 // Measured (whole steps replayed from a CUDA graph, measured copy rate 6.8
 // TB/s): 16 sequences of 4096-8192 keys, 32 heads over 8, d = 128, 403 MB in
-// 70 us = 5.7 TB/s, of it 3.5 us the merge; 64 sequences of 0-16384 keys, 4
-// queries, 64 heads over 8, 2.2 GB in 334 us = 6.5 TB/s; one sequence of 517
+// 70 us = 5.8 TB/s, of it 2.7 us the merge; 64 sequences of 0-16384 keys, 4
+// queries, 64 heads over 8, 2.2 GB in 332 us = 6.5 TB/s; one sequence of 517
 // keys 8.2 us, two reads of lengths and pages, a tile's copy and the merge one
 // after another.  DRAM traffic is the algorithmic bytes plus 1 %.
 #include <type_traits>
