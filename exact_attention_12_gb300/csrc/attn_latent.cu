@@ -410,7 +410,15 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
                        src + c * 8, true);
       }
     };
+    auto q_ready = [&](const PagedPiece& w) {
+      if (!w.valid || w.t0 == w.t1) return;
+      copies_wait();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.qfull);
+    };
     load_q(p);
+    q_ready(p);
     for (PagedPiece nx = p; p.valid; p = nx) {
       nx = next_of(p);
       const int n = p.t1 - p.t0;
@@ -418,12 +426,6 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
       float mc[8], l[8];                        // softmax: this thread's columns
 #pragma unroll
       for (int j = 0; j < 8; ++j) mc[j] = l[j] = 0.f;
-      if (n > 0) {
-        copies_wait();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.qfull);
-      }
       const int open = a.causal ? p.len - a.n_q + 1 : p.len;   // every row is allowed keys below it
       for (int i = 0; i < n; ++i, ++T) {
         const int buf = T & 1;
@@ -559,6 +561,9 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
         inv[e] = s != 0.f ? 1.f / s : 0.f;
         L[e] = s != 0.f ? fmaf(mref[e], a.scale, logf(s)) : -INFINITY;
       }
+      // the next piece's scores can run under the write-out (its maxima go where
+      // the sums were: those are read)
+      q_ready(nx);
       const bool whole = !CLUSTER && p.whole();
       if constexpr (!CLUSTER) {
         if (p.t0 == 0 && !whole) note = paged_note<kLatentOverhead>(share, p);
