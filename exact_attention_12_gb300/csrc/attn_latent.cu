@@ -289,10 +289,8 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
     for (; ok && __shfl_sync(0xffffffffu, p.valid, 0);
          p = next_of(p)) {
       const int n = __shfl_sync(0xffffffffu, p.t1 - p.t0, 0);
-      const int left = __shfl_sync(0xffffffffu, p.len - p.t0 * KT, 0);
       if (n == 0) continue;
-      // S^T of the piece's tile i, group by group as they land; what lies past
-      // the sequence's end is zeroed (it would be a value row)
+      // S^T of the piece's tile i, group by group as they land
       // which groups of tile i have landed: all of them?
       auto landed = [&](int i) {
         const uint32_t u = T + i;
@@ -304,7 +302,6 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
       auto scores = [&](int i, bool all) {
         const uint32_t u = T + i, s = u % ST;
         uint8_t* tile = sC + s * C::kTileBytes;
-        const int from = left - i * KT;
         const uint64_t dc = smem_desc(smem_u32(tile), 16, 1024);
 #pragma unroll
         for (int y = 1; y <= C::kGroups; ++y) {
@@ -316,15 +313,6 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
             tc_fence_after();
           }
           const int box = x == 0 ? C::kBoxes - 1 : 2 * (x - 1), boxes = x == 0 ? 1 : 2;
-          if (from < KT) {
-            for (int e = lane; e < (KT - from) * boxes * 8; e += 32) {
-              const int j = from + e / (boxes * 8), c = box * 8 + e % (boxes * 8);
-              *reinterpret_cast<uint4*>(tile + (c >> 3) * C::kBoxBytes + j * 128 + ((c & 7) << 4)) =
-                  make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
           if (one) {
 #pragma unroll
             for (int kk = 4 * box; kk < 4 * (box + boxes); ++kk) {
@@ -463,6 +451,18 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
           }
         }
         named_barrier_sync(1, 256);
+        // (the tile's scores are complete) what lies past the sequence's end: zero,
+        // before it is used as value rows
+        const int from = p.len - (p.t0 + i) * KT;
+        if (from < KT) {
+          uint8_t* tile = sC + (T % ST) * C::kTileBytes;
+          for (int e = threadIdx.x; e < (KT - from) * (DV / 8); e += 256) {
+            const int j = from + e / (DV / 8), c = e % (DV / 8);
+            *reinterpret_cast<uint4*>(tile + (c >> 3) * C::kBoxBytes + j * 128 + ((c & 7) << 4)) =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+        }
         float alpha[2];
         bool grown[2];
 #pragma unroll
