@@ -56,7 +56,7 @@ using namespace sm103;
 
 namespace {
 
-constexpr int kAhead = 1;   // tiles between a tile's way to L2 and its copy
+constexpr int kLooks = 4096;   // at two barriers in turn, before the wait (which is limited) for one
 
 template <int DV>
 struct LatentCfg {
@@ -209,6 +209,10 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
     // L2: the two tiles in shared memory are too few to cover the latency of
     // HBM, and their copies go through a tile's memory 256 bytes of a token at
     // a time, where this reads it in one run.
+    // kAhead: tiles between a tile's way to L2 and its copy.  (Two for a pair: 156.2
+    // against 158.2 us; alone one: 2 x that many CTAs' tiles would leave too early,
+    // 32 sequences of 0-8192 tokens 38.7 against 40.4.)
+    constexpr int kAhead = PAIR ? 2 : 1;
     auto ahead = [&](int t) {
       int b = p.b, len = p.len;
       if (t >= p.t1) {
@@ -329,13 +333,16 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
       tc_fence_after();
       scores(0, landed(0));
       for (int i = 0; ok && i < n; ++i) {
-        // the next tile's scores first if it has landed; P of this tile
-        // does not wait for it
+        // the next tile's scores first if it lands before P is there
         const uint32_t u = T + i, s = u % ST;
         bool next = i + 1 < n;
-        if (next && landed(i + 1)) {
-          scores(i + 1, true);
-          next = false;
+        for (int looks = 0; next && looks < kLooks; ++looks) {
+          if (landed(i + 1)) {
+            scores(i + 1, true);
+            next = false;
+          } else if (__all_sync(0xffffffffu, mbar_test(&ctl.pfull[u & 1], (u >> 1) & 1))) {
+            break;
+          }
         }
         if (!ok || !(ok = __all_sync(0xffffffffu, mbar_wait(&ctl.pfull[u & 1], (u >> 1) & 1, wc,
                                                             kSiteLatentP))))
