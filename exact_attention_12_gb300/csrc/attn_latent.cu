@@ -56,6 +56,7 @@ using namespace sm103;
 
 namespace {
 
+constexpr int kAhead = 1;   // tiles between a tile's way to L2 and its copy (2: 38.7 -> 40.4 us)
 constexpr int kLooks = 4096;   // at two barriers in turn, before the wait (which is limited) for one
 
 template <int DV>
@@ -76,11 +77,16 @@ struct LatentCfg {
   static constexpr int kCtl = 3 * 1024;                   // LatentCtl, in whole kilobytes
   static_assert(kSmem + kCtl <= 227 * 1024, "shared memory of a CTA");
   // warpgroups 0, 1: the eight warps of the softmax; warpgroup 2: copies, MMA
-  // issue, two idle warps.  Registers re-split after the start: 256 * 216 +
-  // 128 * 72 <= 384 * 168
+  // issue, two idle warps.  Registers re-split after the start: 256 * 208 +
+  // 128 * 88, or for a pair 256 * 216 + 128 * 72, <= 384 * 168.  (The other way
+  // round 16 sequences of 16384 tokens 58.1 against 57.3 us, a pair's 150.5
+  // against 149.)
   static constexpr int kThreads = 384;
-  static constexpr uint32_t kRegsLaunch = 168, kRegsSoftmax = 216, kRegsOther = 72;
-  static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * kRegsLaunch,
+  static constexpr uint32_t kRegsLaunch = 168;
+  static constexpr uint32_t kRegsSoftmax = 208, kRegsOther = 88;
+  static constexpr uint32_t kPairRegsSoftmax = 216, kPairRegsOther = 72;
+  static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * kRegsLaunch &&
+                    256 * kPairRegsSoftmax + 128 * kPairRegsOther <= kThreads * kRegsLaunch,
                 "register re-split exceeds the launch allocation");
   // S^T of tile t at 64 (t mod 2), block i of O^T at 128 + 64 i
   static constexpr uint32_t kOCol = 128;
@@ -198,7 +204,7 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
   };
 
   if (warp >= 8) {
-    regs_decrease<C::kRegsOther>();
+    regs_decrease<PAIR ? C::kPairRegsOther : C::kRegsOther>();
   if (warp == 8) {
     // ------------------------------------------------------------ copies
     const int rows = min(KT, 1 << a.page_shift), parts = KT / rows;
@@ -209,10 +215,6 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
     // L2: the two tiles in shared memory are too few to cover the latency of
     // HBM, and their copies go through a tile's memory 256 bytes of a token at
     // a time, where this reads it in one run.
-    // kAhead: tiles between a tile's way to L2 and its copy.  (Two for a pair: 156.2
-    // against 158.2 us; alone one: 2 x that many CTAs' tiles would leave too early,
-    // 32 sequences of 0-8192 tokens 38.7 against 40.4.)
-    constexpr int kAhead = PAIR ? 2 : 1;
     auto ahead = [&](int t) {
       int b = p.b, len = p.len;
       if (t >= p.t1) {
@@ -380,7 +382,7 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
     __syncwarp();
   }
   } else {
-    regs_increase<C::kRegsSoftmax>();
+    regs_increase<PAIR ? C::kPairRegsSoftmax : C::kRegsSoftmax>();
     // ------------------------------------------- q, softmax, rescale, output
     // softmax: 16 keys and 32 of the columns a warp, in the MMA's fragment
     // layout: keys g, g + 8 and columns 8 b + 2 q, + 1 (b = 0 .. 3) a thread
