@@ -33,21 +33,21 @@
 //              grown by 2^8; write O
 //   warp 8     copies (a lane per page)
 //   warp 9     MMA issue: the scores of the next tile run under this tile's
-//              softmax
+//              softmax (it looks for whichever comes first, the tile or P)
 // A tile is copied, waited for and released in groups of columns, so that its
 // scores begin while the rest is on the way, and the next copies while its
 // last products run: two 72 KB tiles are few for 1.6 us of latency.
 // P is rounded to bf16 for the second product (relative 2^-8 per element);
 // m, l, O are fp32.  Rows past the end of a sequence are zeroed in shared
-// memory before they are used as values (0 * NaN is NaN).
+// memory, by the softmax warps, before they are used as values (0 * NaN is NaN).
 //
 // Measured (d_v = 512, whole steps replayed from a CUDA graph): up to 64 rows
 // the kernel streams at the copy rate once it runs (16 sequences, 16 heads:
-// 16384 more tokens each cost 44 us = 6.8 TB/s); what remains is 14 us of
-// set-up, first and last tiles and the merge (4096 tokens each: 25 us).  With
+// 16384 more tokens each cost 44 us = 6.8 TB/s); what remains is 12 us of
+// set-up, first and last tiles and the merge (4096 tokens each: 23 us).  With
 // 128 rows each tile is worked on by two CTAs, and shared memory bounds it: a
 // tile's operand reads, its copy and P take 2600 cycles of its bandwidth, its
-// MMAs 2000, and a tile takes 3000 (64 sequences of 4096-8192 tokens: 167 us,
+// MMAs 1900, and a tile takes 3100 (64 sequences of 4096-8192 tokens: 149 us,
 // where the tokens' bytes need 69 and the operations 58).
 #include "attn_paged.cuh"
 
