@@ -21,12 +21,9 @@
 // fill TMEM, and q alone would take 147 KB of shared memory.  So O^T takes
 // d_v / 128 * 64 TMEM columns, q 72 KB, and two 64-key tiles of 72 KB are in
 // flight, each used as both operands.  H * n_q rows are cut into groups of 64;
-// the CTAs of a sequence's groups run side by side on the same keys.  Where
-// the groups are even in number, two of them form a cluster, and each copies
-// half of a tile's value columns into both (multicast), which halves what L2
-// has to deliver; a column group's place is free again when both are done with
-// it (64 sequences of 4096-8192 tokens, 128 heads: 177 -> 169 us).  The keys
-// are divided over the CTAs as in the paged decode step.
+// the CTAs of a sequence's groups run side by side on the same keys, of which
+// each copies its own tiles (all but the first reading then comes from L2).
+// The keys are divided over the CTAs as in the paged decode step.
 //   warps 0-7  load q; softmax of 16 keys x 32 columns each, in the MMA's
 //              fragment layout; the sums stay in registers, a partial per
 //              thread, until the end; rescale O^T when some column's max has
@@ -47,7 +44,7 @@
 // set-up, first and last tiles and the merge (4096 tokens each: 23 us).  With
 // 128 rows each tile is worked on by two CTAs, and shared memory bounds it: a
 // tile's operand reads, its copy and P take 2600 cycles of its bandwidth, its
-// MMAs 1900, and a tile takes 3100 (64 sequences of 4096-8192 tokens: 149 us,
+// MMAs 1900, and a tile takes 3100 (64 sequences of 4096-8192 tokens: 152 us,
 // where the tokens' bytes need 69 and the operations 58).
 #include "attn_paged.cuh"
 
@@ -78,15 +75,12 @@ struct LatentCfg {
   static_assert(kSmem + kCtl <= 227 * 1024, "shared memory of a CTA");
   // warpgroups 0, 1: the eight warps of the softmax; warpgroup 2: copies, MMA
   // issue, two idle warps.  Registers re-split after the start: 256 * 208 +
-  // 128 * 88, or for a pair 256 * 216 + 128 * 72, <= 384 * 168.  (The other way
-  // round 16 sequences of 16384 tokens 58.1 against 57.3 us, a pair's 150.5
-  // against 149.)
+  // 128 * 88 <= 384 * 168 (216 and 72: 16 sequences of 16384 tokens 58.1 against
+  // 57.3 us).
   static constexpr int kThreads = 384;
   static constexpr uint32_t kRegsLaunch = 168;
   static constexpr uint32_t kRegsSoftmax = 208, kRegsOther = 88;
-  static constexpr uint32_t kPairRegsSoftmax = 216, kPairRegsOther = 72;
-  static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * kRegsLaunch &&
-                    256 * kPairRegsSoftmax + 128 * kPairRegsOther <= kThreads * kRegsLaunch,
+  static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * kRegsLaunch,
                 "register re-split exceeds the launch allocation");
   // S^T of tile t at 64 (t mod 2), block i of O^T at 128 + 64 i
   static constexpr uint32_t kOCol = 128;
@@ -119,18 +113,16 @@ __device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t* r) {
       : "r"(taddr));
 }
 
-// How a launch uses clusters.
-//   kAlone  none: the balanced split
-//   kPair   the balanced split, two row groups of the same tiles a cluster: each
-//           CTA copies half of a tile's value columns into both
+// How the keys are given out.
+//   kAlone  the balanced split
 //   kSeq    a sequence per cluster (a.cluster CTAs)
-enum LatentMode { kAlone, kPair, kSeq };
+enum LatentMode { kAlone, kSeq };
 
 template <int DV, LatentMode MODE>
 __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
     latent_kernel(const __grid_constant__ CUtensorMap tc, const PagedArgs a, int groups) {
   using C = LatentCfg<DV>;
-  constexpr bool CLUSTER = MODE == kSeq, PAIR = MODE == kPair;
+  constexpr bool CLUSTER = MODE == kSeq;
   constexpr int ST = C::kStages, KT = kLatentKeys;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ LatentCtl<ST> ctl;
@@ -150,7 +142,7 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
   const int unit = CLUSTER ? blockIdx.x / a.cluster : blockIdx.x;
   const int r0 = unit % groups * kLatentRows;   // first query row
   const int cta = unit / groups, ctas = gridDim.x / groups;
-  const int rank = MODE == kAlone ? 0 : static_cast<int>(cluster_rank());
+  const int rank = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
   const int live = min(kLatentRows, a.all_rows - r0);
 
   if (threadIdx.x == 0) {
@@ -158,8 +150,7 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
     for (int s = 0; s < ST; ++s)
       for (int x = 0; x < C::kGroups; ++x) {
         mbar_init(&ctl.full[s][x], 1);
-        // (a pair's value columns are free when both CTAs are done with them)
-        mbar_init(&ctl.empty[s][x], PAIR && x > 0 ? 2 : 1);
+        mbar_init(&ctl.empty[s][x], 1);
       }
     mbar_init(&ctl.sfull[0], 1);
     mbar_init(&ctl.sfull[1], 1);
@@ -184,7 +175,6 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
-  if constexpr (PAIR) cluster_sync();   // the other CTA's barriers are ready
   tc_fence_after();
   grid_dep_wait();
   grid_dep_launch();
@@ -204,7 +194,7 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
   };
 
   if (warp >= 8) {
-    regs_decrease<PAIR ? C::kPairRegsOther : C::kRegsOther>();
+    regs_decrease<C::kRegsOther>();
   if (warp == 8) {
     // ------------------------------------------------------------ copies
     const int rows = min(KT, 1 << a.page_shift), parts = KT / rows;
@@ -253,12 +243,7 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
           const int box = x == 0 ? C::kBoxes - 1 : 2 * (x - 1), boxes = x == 0 ? 1 : 2;
           if (lane == 0) mbar_arrive_expect_tx(&ctl.full[s][x], boxes * C::kBoxBytes);
           __syncwarp();
-          if (PAIR && x > 0) {
-            if (lane < parts)
-              tma_load_4d_multicast(
-                  sC + s * C::kTileBytes + (box + rank) * C::kBoxBytes + lane * rows * 128, &tc,
-                  &ctl.full[s][x], (box + rank) * 64, at & ((1 << a.page_shift) - 1), 0, page, 3);
-          } else if (lane < parts) {
+          if (lane < parts) {
             for (int k = box; k < box + boxes; ++k)
               tma_load_4d(sC + s * C::kTileBytes + k * C::kBoxBytes + lane * rows * 128, &tc,
                           &ctl.full[s][x], k * 64, at & ((1 << a.page_shift) - 1), 0, page);
@@ -283,8 +268,8 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
     // every 31 cycles (64 x 64 x 16) or 46 (128 x 64 x 16) instead of every 58.
     // Only as many of the 64 rows as live, in sixteens: 16 rows read 162 KB of
     // operands a tile instead of 245 (32 sequences of 0-8192 tokens 43.0 -> 41.9
-    // us).  A pair's rows are nearly all live, and a constant is faster there.
-    const int wide = PAIR ? kLatentRows : (live + 15) / 16 * 16;
+    // us).
+    const int wide = (live + 15) / 16 * 16;
     const uint32_t id_s = idesc_bf16(64, wide, false, false);
     const uint32_t id_o = idesc_bf16(128, wide, true, true);
     const bool one = elect_one_lane();
@@ -361,8 +346,7 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
               const uint64_t off = static_cast<uint64_t>((kk * 2048) >> 4);
               mma_ss(tmem + C::kOCol + 64 * blk, dv + off, dp + off, id_o, i > 0 || kk > 0 ? 1u : 0u);
             }
-            if constexpr (PAIR) mma_commit_multicast(&ctl.empty[s][1 + blk], 3);
-            else mma_commit(&ctl.empty[s][1 + blk]);
+            mma_commit(&ctl.empty[s][1 + blk]);
           }
         }
         if (one) {
@@ -382,7 +366,7 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
     __syncwarp();
   }
   } else {
-    regs_increase<PAIR ? C::kPairRegsSoftmax : C::kRegsSoftmax>();
+    regs_increase<C::kRegsSoftmax>();
     // ------------------------------------------- q, softmax, rescale, output
     // softmax: 16 keys and 32 of the columns a warp, in the MMA's fragment
     // layout: keys g, g + 8 and columns 8 b + 2 q, + 1 (b = 0 .. 3) a thread
@@ -666,10 +650,6 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
     cluster_sync();   // the others have read this CTA's rows
   }
 
-  if constexpr (PAIR) {   // neither CTA leaves while the other's copies or commits may come
-    __syncwarp();
-    cluster_sync();
-  }
   tc_fence_before();
   __syncthreads();
   if (warp == 9) {
@@ -701,9 +681,6 @@ cudaError_t launch_dv(const CUtensorMap& tc, const PagedArgs& a, int ctas, cudaS
     return launch_clusters(latent_kernel<DV, MODE>,
                            dim3(static_cast<unsigned>(a.B * groups * a.cluster)), dim3(C::kThreads),
                            C::kSmem, a.cluster, s, tc, a, groups);
-  if (MODE == kPair)
-    return launch_clusters(latent_kernel<DV, MODE>, dim3(ctas * groups), dim3(C::kThreads), C::kSmem,
-                           2, s, tc, a, groups);
   return launch_pdl(latent_kernel<DV, MODE>, dim3(ctas * groups), dim3(C::kThreads), C::kSmem, s,
                     tc, a, groups);
 }
@@ -714,8 +691,6 @@ cudaError_t launch_latent(const CUtensorMap& tc, const PagedArgs& a, int ctas, c
   const bool wide = a.d == 512;
   if (a.cluster > 0)
     return wide ? launch_dv<512, kSeq>(tc, a, ctas, s) : launch_dv<256, kSeq>(tc, a, ctas, s);
-  if (a.rows / kLatentRows % 2 == 0)
-    return wide ? launch_dv<512, kPair>(tc, a, ctas, s) : launch_dv<256, kPair>(tc, a, ctas, s);
   return wide ? launch_dv<512, kAlone>(tc, a, ctas, s) : launch_dv<256, kAlone>(tc, a, ctas, s);
 }
 
