@@ -25,6 +25,9 @@ ATTN_FP8_E4M3 = 2
 ATTN_STALL_NONE = 0
 ATTN_STALL_FWD_SOFTMAX = 1
 ATTN_STALL_BWD_COMPUTE = 2
+ATTN_STALL_PAGED_TILE = 3
+ATTN_STALL_PREFIX_SOFTMAX = 4
+ATTN_STALL_LATENT_SOFTMAX = 5
 
 # every function the header declares, with its ctypes signature
 EXPORTS = {

@@ -407,6 +407,13 @@ int attn::record_error(int status, const char* msg) {
   return static_cast<int>(fail(static_cast<attn_status>(status), "%s", msg));
 }
 
+bool attn::take_stall(int which, uint64_t* limit_ns) {
+  if (g_stall != which || which == kStallNone) return false;
+  *limit_ns = g_stall_limit_ns;
+  g_stall = kStallNone;
+  return true;
+}
+
 int attn::encode_pages(CUtensorMap* map, const void* ptr, int num_pages, int heads, int page_size,
                        int d, int64_t stride_p, int64_t stride_h, int64_t stride_n, int box_rows) {
   return static_cast<int>(make_map(map, ptr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, num_pages, heads,
@@ -763,8 +770,7 @@ attn_status attn_decode(const attn_params* p, int32_t n_q, const void* q, const 
 }
 
 attn_status attn_debug_stall(int32_t which, uint64_t limit_ns) {
-  if (which != ATTN_STALL_NONE && which != ATTN_STALL_FWD_SOFTMAX &&
-      which != ATTN_STALL_BWD_COMPUTE)
+  if (which < ATTN_STALL_NONE || which > ATTN_STALL_LATENT_SOFTMAX)
     return fail(ATTN_ERR_INVALID_ARG, "unknown stall %d", which);
   if (limit_ns < 1000000ull) limit_ns = 1000000ull;          // 1 ms
   if (limit_ns > kTimeoutNs) limit_ns = kTimeoutNs;          // 2 s

@@ -68,7 +68,14 @@ enum WaitSite : int {
 // One-shot stalls armed by attn_debug_stall (a test of the kernels' own
 // time-out path): the named role withholds one barrier arrive in its first
 // tile, so the wait on that barrier runs out.
-enum StallSite : int { kStallNone = 0, kStallFwdSoftmax = 1, kStallBwdCompute = 2 };
+enum StallSite : int {
+  kStallNone = 0,
+  kStallFwdSoftmax = 1,
+  kStallBwdCompute = 2,
+  kStallPagedTile = 3,
+  kStallPrefixSoftmax = 4,
+  kStallLatentSoftmax = 5
+};
 
 // Device status code for a kernel that found its shared memory misaligned
 // and returned without doing anything (equals ATTN_ERR_CUDA in attn.h).

@@ -520,7 +520,9 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.pfull[buf]);
+        // (an armed test stall: warp 0 withholds its first arrive, so the MMA
+        // warp's wait runs out)
+        if (lane == 0 && !(a.stall != 0 && warp == 0 && T == 0)) mbar_arrive(&ctl.pfull[buf]);
       }
 
       // ---- O = O^T / l and L of the piece; every score MMA of the piece is

@@ -184,7 +184,9 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
                                              kSitePagedFree));
       if (!ok) return;
     }
-    if (lane == 0) {
+    // (an armed test stall: slot 0's first tile is not copied, so the wait for it
+    // runs out)
+    if (lane == 0 && !(a.stall != 0 && slot == 0 && issued == 0)) {
       uint64_t* bar = &sh.full[slot * ST + st];
       const int row = (a.first + (p.t0 + first_tile + kStep * u) * KT) & ((1 << a.page_shift) - 1);
       const int head = p.h / a.blocks;
@@ -662,7 +664,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
   grid_dep_launch();
   const int4 raw = *reinterpret_cast<const int4*>(a.notes + blockIdx.x);
   const MergeNote note{raw.x, raw.y, raw.z, raw.w};
-  if (note.b < 0 || note.more < 0) return;   // (uniform over the CTA)
+  if (note.more < 0 || !note_holds(a, note)) return;   // (uniform over the CTA)
   const int e = blockIdx.y * kItems + threadIdx.x % kItems;
   const int r = e / (D / 4), c = 4 * (e % (D / 4)), hr = segment_row(a, note.h) + r;
   const bool live = r < segment_rows(a, note.h);
@@ -686,6 +688,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_finish_kernel(const Paged
   grid_dep_launch();
   const int4 raw = *reinterpret_cast<const int4*>(a.notes + blockIdx.x);
   const MergeNote note{raw.x, raw.y, raw.z, raw.w};
+  if (!note_holds(a, note)) return;
   const int e = blockIdx.y * kItems + threadIdx.x % kItems;
   const int r = e / (D / 4), c = 4 * (e % (D / 4)), hr = segment_row(a, note.h) + r;
   const bool live = r < segment_rows(a, note.h);

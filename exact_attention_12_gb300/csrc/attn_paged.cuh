@@ -72,9 +72,21 @@ struct PagedArgs {
   float* pre_o;                   // workspace [pre_splits + 1][B*H*n_q][d]
   float* pre_l;                   // workspace [pre_splits + 1][B*H*n_q]
   int pre_splits;
+  int ctas;                       // G, the CTAs with partial slots
+  int stall;                      // kStallPagedTile, kStallLatentSoftmax: see attn_debug_stall
   int* status;
   uint64_t timeout_ns;
 };
+
+// Whether the merges can follow a note.  A CTA whose wait has run out writes no
+// more notes, and one whose shared memory is misaligned none at all; what the
+// workspace holds in their place may be another call's.
+__device__ __forceinline__ bool note_holds(const PagedArgs& a, const MergeNote& n) {
+  return static_cast<unsigned>(n.b) < static_cast<unsigned>(a.B) &&
+         static_cast<unsigned>(n.h) < static_cast<unsigned>(a.heads) &&
+         static_cast<unsigned>(n.slot) < 2u * static_cast<unsigned>(a.ctas) && n.more >= -1 &&
+         n.more < a.ctas - (n.slot >> 1);
+}
 
 // Where segment h of a sequence begins among the sequence's rows (head * n_q +
 // query), and how many it has.
@@ -101,6 +113,7 @@ struct PrefixArgs {
   int64_t stride_b, stride_h, stride_n;
   float* pre_o;
   float* pre_l;
+  int stall;                      // kStallPrefixSoftmax: see attn_debug_stall
   int* status;
   uint64_t timeout_ns;
 };
@@ -335,6 +348,9 @@ cudaError_t launch_prefix(const CUtensorMap& tk, const CUtensorMap& tv, const Pr
 cudaError_t launch_latent(const CUtensorMap& tc, const PagedArgs& a, int ctas, cudaStream_t s);
 cudaError_t launch_paged_merge(const PagedArgs& a, int notes, int ctas, cudaStream_t s);
 cudaError_t launch_paged_finish(const PagedArgs& a, int ctas, cudaStream_t s);
+
+// Whether attn_debug_stall armed `which` for this launch; then its wait limit.
+bool take_stall(int which, uint64_t* limit_ns);
 
 // Tensor map of a paged cache for the host code (an attn_status).
 int encode_pages(CUtensorMap* map, const void* ptr, int num_pages, int heads, int page_size, int d,

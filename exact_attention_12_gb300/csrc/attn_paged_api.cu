@@ -241,6 +241,7 @@ PagedArgs args_of(const attn_params* p, int32_t n_q, const attn_pages* g, const 
   a.pre_splits = L.splits;
   a.pre_o = reinterpret_cast<float*>(w + L.pre_o);
   a.pre_l = reinterpret_cast<float*>(w + L.pre_l);
+  a.ctas = L.ctas;
   a.status = reinterpret_cast<int*>(w);
   a.timeout_ns = kTimeoutNs;
   return a;
@@ -278,7 +279,7 @@ attn_status attn_decode_paged(const attn_params* p, int32_t n_q, const attn_page
   if (empty(p)) return ATTN_OK;
   if ((st = check_ptrs({q, k, v, o, lse})) != ATTN_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const PagedArgs a = args_of(p, n_q, pages, L, q, o, lse, ws);
+  PagedArgs a = args_of(p, n_q, pages, L, q, o, lse, ws);
   const auto map = [&](CUtensorMap* m, const void* ptr, int keys) {
     return static_cast<attn_status>(attn::encode_pages(
         m, ptr, at_least_1(pages->num_pages), kv_heads(p), pages->page_size, p->d, p->kv_stride_b,
@@ -315,12 +316,14 @@ attn_status attn_decode_paged(const attn_params* p, int32_t n_q, const attn_page
     f.pre_l = a.pre_l;
     f.status = a.status;
     f.timeout_ns = a.timeout_ns;
+    f.stall = attn::take_stall(attn::kStallPrefixSoftmax, &f.timeout_ns);
     if ((st = launched(attn::launch_prefix(tk, tv, f, s), "shared prefix launch")) != ATTN_OK)
       return st;
   }
   if ((st = map(&tk, k, attn::kPagedKeys)) != ATTN_OK ||
       (st = map(&tv, v, attn::kPagedKeys)) != ATTN_OK)
     return st;
+  a.stall = attn::take_stall(attn::kStallPagedTile, &a.timeout_ns);
   if ((st = launched(attn::launch_paged(tk, tv, a, L.ctas, s), "paged decode launch")) != ATTN_OK)
     return st;
   if (L.cluster > 0) return ATTN_OK;   // merged already
@@ -354,6 +357,7 @@ attn_status attn_decode_latent(const attn_params* p, int32_t n_q, const attn_pag
       &tc, c, at_least_1(pages->num_pages), 1, pages->page_size, p->d + attn::kLatentRope,
       p->kv_stride_b, p->kv_stride_b, p->kv_stride_n, box_rows(pages, attn::kLatentKeys)));
   if (st != ATTN_OK) return st;
+  a.stall = attn::take_stall(attn::kStallLatentSoftmax, &a.timeout_ns);
   if ((st = launched(attn::launch_latent(tc, a, L.ctas, s), "latent decode launch")) != ATTN_OK)
     return st;
   if (L.ctas == 1 || L.cluster > 0) return ATTN_OK;

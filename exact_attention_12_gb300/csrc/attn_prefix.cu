@@ -394,7 +394,9 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl.pfull[x]);
+      // (an armed test stall: warp 0 withholds its first arrive, so the MMA warp's
+      // wait runs out)
+      if (lane == 0 && !(a.stall != 0 && warp == 0 && t == 0)) mbar_arrive(&ctl.pfull[x]);
     }
     if (ok && mine > 0) {
       ok = __all_sync(0xffffffffu, mbar_wait(&ctl.done, 0, wc, kSitePrefixDone));

@@ -382,8 +382,14 @@ attn_status attn_selftest_timeout(void* ws, uint64_t limit_ns, void* stream);
  *   ATTN_STALL_BWD_COMPUTE  the backward main kernel (attn_bwd, attn_bwd_main,
  *                           attn_bwd_noalloc): in every CTA, compute warp 0
  *                           withholds its "P ready" arrive for its first
- *                           query tile.
- * The MMA warp's wait on that barrier then runs out; every wait of that launch
+ *                           query tile;
+ *   ATTN_STALL_PAGED_TILE   the paged decode kernel (attn_decode_paged): in
+ *                           every CTA, the first key tile is not copied;
+ *   ATTN_STALL_PREFIX_SOFTMAX  the shared prefix's kernel (attn_decode_paged
+ *                           with shared_len > 0 and two sequences or more), as
+ *                           the forward's;
+ *   ATTN_STALL_LATENT_SOFTMAX  attn_decode_latent, as the forward's.
+ * The wait on that barrier then runs out; every wait of that launch
  * gives up after `limit_ns` (clamped to [1 ms, 2 s]).  The kernel drains its
  * copies and MMAs, frees its tensor memory and returns, and the status words
  * of the call's workspace hold ATTN_ERR_TIMEOUT and the wait site, which
@@ -393,7 +399,10 @@ attn_status attn_selftest_timeout(void* ws, uint64_t limit_ns, void* stream);
 typedef enum {
   ATTN_STALL_NONE = 0,
   ATTN_STALL_FWD_SOFTMAX = 1,
-  ATTN_STALL_BWD_COMPUTE = 2
+  ATTN_STALL_BWD_COMPUTE = 2,
+  ATTN_STALL_PAGED_TILE = 3,
+  ATTN_STALL_PREFIX_SOFTMAX = 4,
+  ATTN_STALL_LATENT_SOFTMAX = 5
 } attn_stall;
 attn_status attn_debug_stall(int32_t which, uint64_t limit_ns);
 

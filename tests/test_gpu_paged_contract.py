@@ -1,0 +1,81 @@
+"""What the paged-cache calls promise beyond ordinary results: waits that run
+out, wrong state, caches and batches of nothing."""
+
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged as oracle
+from tests.helpers import np64
+from tests.test_gpu_paged import WIDE, _hold, _poison, _run, _table, ea  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------- waits that run out --
+
+def _used_workspace():
+    """A workspace whose header is zero and whose rest holds another call's data."""
+    g = torch.Generator().manual_seed(1)
+    ws = torch.randint(-2 ** 31, 2 ** 31, (1 << 24,), generator=g, dtype=torch.int64).to(torch.int32)
+    ws[:64] = 0
+    return ws.cuda()
+
+
+def _stalled(stall, sites, call, want):
+    """The call with one of its kernels stalled, then twice as it is."""
+    from exact_attention_12_gb300 import _abi
+    lib, ws = _abi.lib(), _used_workspace()
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert lib.attn_debug_stall(stall, 20_000_000) == _abi.ATTN_OK
+    call(ws)
+    assert lib.attn_check(ws.data_ptr(), stream) == _abi.ATTN_ERR_TIMEOUT
+    msg = lib.attn_last_error().decode()
+    assert int(msg.rsplit("wait site", 1)[1]) in sites, msg
+    assert lib.attn_check(ws.data_ptr(), stream) == _abi.ATTN_OK   # read and cleared
+    for _ in range(2):
+        o, lse = call(ws)
+        assert lib.attn_check(ws.data_ptr(), stream) == _abi.ATTN_OK
+        _hold(o, lse, want)
+
+
+# The balanced split with a merge per segment and per CTA, one CTA's 64 rows, a
+# cluster per segment, a slot per segment; with a prefix, stalled in either
+# kernel: its own merge, and the decode kernel's
+@pytest.mark.parametrize("kernel,lens,H,H_kv,shared,room", [
+    ("paged", [9000, 40, 0, 700], 4, 1, 0, WIDE), ("paged", [300, 0, 41] * 30, 8, 4, 0, WIDE),
+    ("paged", [700, 900], 64, 1, 0, WIDE), ("paged", [300, 1, 33], 4, 2, 0, 0),
+    ("paged", [40, 0, 77] * 30, 8, 4, 0, 0)] + [
+    (kernel, *case) for kernel in ("paged", "prefix") for case in (
+        ([5000, 4100, 1100], 4, 2, 1024, WIDE), ([1100, 1024, 1050], 4, 2, 1024, 0),
+        ([300] * 90, 8, 4, 256, 0))])
+def test_a_stalled_paged_step_ends_and_reports(ea, kernel, lens, H, H_kv, shared, room):
+    from exact_attention_12_gb300 import _abi
+    rng, g = np.random.default_rng(3), torch.Generator().manual_seed(3)
+    table, P = _table(rng, lens, 16, shared=shared, room=room)
+    k, v = (_poison(torch.randn(P, H_kv, 16, 64, generator=g).to(torch.bfloat16), table, lens, 16)
+            for _ in range(2))
+    q = torch.randn(len(lens), H, 1, 64, generator=g).to(torch.bfloat16)
+    args = [x.cuda() for x in (q, k, v, torch.from_numpy(table),
+                               torch.tensor(lens, dtype=torch.int32))]
+    stall, sites = {"paged": (_abi.ATTN_STALL_PAGED_TILE, (60, 61)),
+                    "prefix": (_abi.ATTN_STALL_PREFIX_SOFTMAX, range(62, 70))}[kernel]
+    _stalled(stall, sites,
+             lambda ws: ea.attention_decode_paged(*args, shared_len=shared, ws=ws),
+             oracle.paged_decode(np64(q), np64(k), np64(v), table, lens, 0.125))
+
+
+@pytest.mark.parametrize("lens,H,room", [([5000, 40, 0, 700], 16, WIDE), ([5000, 700], 128, WIDE),
+                                         ([130, 0, 65] * 60, 8, WIDE), ([200, 1, 64], 40, 0)])
+def test_a_stalled_latent_step_ends_and_reports(ea, lens, H, room):
+    from exact_attention_12_gb300 import _abi
+    rng, g = np.random.default_rng(4), torch.Generator().manual_seed(4)
+    table, P = _table(rng, lens, 32, room=room)
+    c = _poison(torch.randn(P, 32, 320, generator=g).to(torch.bfloat16), table, lens, 32)
+    q = torch.randn(len(lens), H, 1, 320, generator=g).to(torch.bfloat16)
+    args = [x.cuda() for x in (q, c, torch.from_numpy(table), torch.tensor(lens, dtype=torch.int32))]
+    _stalled(_abi.ATTN_STALL_LATENT_SOFTMAX, range(70, 77),
+             lambda ws: ea.attention_decode_latent(*args, scale=0.05, d_v=256, ws=ws),
+             oracle.latent_decode(np64(q), np64(c), table, lens, 0.05, 256))

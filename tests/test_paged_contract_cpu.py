@@ -20,3 +20,25 @@ def test_no_copy_or_commit_reaches_another_cta():
     # any device pointer: a TMA copy goes to the CTA that issues it only
     for path in glob.glob(os.path.join(CSRC, "*.cu*")):
         assert "multicast" not in _code(path), path
+
+
+def test_every_note_is_checked_before_it_is_followed():
+    # a wait that has run out leaves notes unwritten: whatever the workspace holds in
+    # their place must not be used as an index
+    text = _code(os.path.join(CSRC, "attn_paged.cu"))
+    kernels = [k for k in re.split(r"__global__", text) if "const MergeNote note{raw" in k]
+    assert len(kernels) == 2
+    for k in kernels:
+        body = k[k.index("const MergeNote note{raw"):]
+        check = re.search(r"if \([^\n]*!note_holds\(a, note\)\) return;", body)
+        assert check and not re.search(r"note\.(b|h|slot)", body[:check.start()])
+
+
+def test_the_paged_kernels_can_be_stalled():
+    from exact_attention_12_gb300 import _abi
+    lib = _abi.lib()
+    for which in (_abi.ATTN_STALL_PAGED_TILE, _abi.ATTN_STALL_PREFIX_SOFTMAX,
+                  _abi.ATTN_STALL_LATENT_SOFTMAX, _abi.ATTN_STALL_NONE):
+        assert lib.attn_debug_stall(which, 1) == _abi.ATTN_OK
+    for which in (-1, 6):
+        assert lib.attn_debug_stall(which, 1) == _abi.ATTN_ERR_INVALID_ARG
