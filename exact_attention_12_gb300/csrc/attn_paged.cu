@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
           }
           __syncthreads();
         }
-        const int live = min(16, nrows - 16 * m);   // (none, perhaps)
+        const int live = min(16, nrows - 16 * m);   // (negative where a tile has no rows)
         auto logsumexp = [&](int r) {
           float mx = -INFINITY, lt = 0.f;
 #pragma unroll
@@ -476,7 +476,8 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::kThreads, PagedCfg<D, MT>::kC
         if constexpr (CLUSTER) {
           // the cluster's rows, and a prefix's pieces, merged: each CTA writes a
           // part of the items
-          if (threadIdx.x < live) sh.L[threadIdx.x] = logsumexp(16 * m + threadIdx.x);
+          if (static_cast<int>(threadIdx.x) < live)
+            sh.L[threadIdx.x] = logsumexp(16 * m + threadIdx.x);
           if (late) grid_dep_wait();
           cluster_sync();
           for (int e = rank * C::kThreads + threadIdx.x; e < live * (D / 4);

@@ -79,3 +79,16 @@ def test_a_stalled_latent_step_ends_and_reports(ea, lens, H, room):
     _stalled(_abi.ATTN_STALL_LATENT_SOFTMAX, range(70, 77),
              lambda ws: ea.attention_decode_latent(*args, scale=0.05, d_v=256, ws=ws),
              oracle.latent_decode(np64(q), np64(c), table, lens, 0.05, 256))
+
+
+# ------------------------------------------------------------ rows of a CTA --
+
+# 33 to 63 rows of a key/value head take four row tiles, the last of which may
+# have none; 65 are a block of 33 and one of 32
+@pytest.mark.parametrize("H,n_q", [(33, 1), (40, 1), (47, 1), (48, 1), (49, 1), (65, 1), (5, 7),
+                                   (97, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("shared", [0, 64])
+@pytest.mark.parametrize("room", [0, WIDE])
+def test_row_tiles_without_rows(ea, H, n_q, d, shared, room):
+    _run(ea, [shared + n for n in (300, 1, 170)], H, 1, n_q, d, 32, True, shared, seed=H, room=room)

@@ -42,3 +42,11 @@ def test_the_paged_kernels_can_be_stalled():
         assert lib.attn_debug_stall(which, 1) == _abi.ATTN_OK
     for which in (-1, 6):
         assert lib.attn_debug_stall(which, 1) == _abi.ATTN_ERR_INVALID_ARG
+
+
+def test_thread_indices_are_compared_as_what_they_are():
+    # threadIdx.x is unsigned: against a signed count that may be negative the comparison
+    # holds for every thread.  Constants (kItems, 32) are never negative.
+    for path in glob.glob(os.path.join(CSRC, "*.cu*")):
+        for other in re.findall(r"threadIdx\.x\s*(?:<|>=|<=|>)\s*([\w:]+)", _code(path)):
+            assert re.fullmatch(r"(C::)?k[A-Z]\w*|\d+", other), (path, other)
