@@ -102,7 +102,8 @@ __device__ __forceinline__ int segment_rows(const PagedArgs& a, int h) {
 struct PrefixArgs {
   int B, H, H_kv, group, n_q, causal, d;
   const int32_t* key_lens;
-  const int32_t* table;           // row 0 names the prefix
+  const int32_t* table;           // [B][table_stride]; the longest sequence's row names the prefix
+  int64_t table_stride;
   int cap;                        // keys a row of the table can name
   int page_shift, num_pages;
   int shared_len;

@@ -299,6 +299,7 @@ attn_status attn_decode_paged(const attn_params* p, int32_t n_q, const attn_page
     f.d = p->d;
     f.key_lens = p->key_lens;
     f.table = pages->table;
+    f.table_stride = pages->table_stride;
     f.cap = a.cap;
     f.page_shift = a.page_shift;
     f.num_pages = pages->num_pages;

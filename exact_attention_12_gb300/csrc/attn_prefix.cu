@@ -121,12 +121,17 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
     regs_decrease<C::kRegsOther>();
     if (warp == 8) {
       // ---------------------------------------------------------- copies
-      // keys at or past `end` belong to no sequence
-      int end = 0;
-      for (int b = lane; b < a.B; b += 32) end = max(end, a.key_lens[b]);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) end = max(end, __shfl_xor_sync(0xffffffffu, end, o));
-      end = min(end, a.shared_len);
+      // keys at or past `end` belong to no sequence; those before it are named by
+      // the row of the longest sequence (the first of equals), which holds them all
+      int end = 0, from = 0;
+      for (int b = lane; b < a.B; b += 32) {
+        const int len = a.key_lens[b];
+        if (len > end) end = len, from = b;
+      }
+      const int most = __reduce_max_sync(0xffffffffu, end);
+      from = __reduce_min_sync(0xffffffffu, end == most ? from : a.B - 1);
+      end = min(most, a.shared_len);
+      const int32_t* table = a.table + from * a.table_stride;
       const int rows = min(kTile, 1 << a.page_shift);   // keys per copy
       const int parts = kTile / rows;
       bool ok = true;
@@ -137,7 +142,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         const int key = k0 + lane * rows;
         const bool mine = lane < parts && key < end;   // this lane's page of the tile
         int page = 0;
-        if (mine) page = checked_page(a.table[key >> a.page_shift], a.num_pages, a.status);
+        if (mine) page = checked_page(table[key >> a.page_shift], a.num_pages, a.status);
         // (the keys are free once both tiles' scores are complete, a tile's
         // products before the values)
         if (t >= ST && !(ok = __all_sync(0xffffffffu, mbar_wait(&ctl.kempty[s], ((t / ST) - 1) & 1, wc,

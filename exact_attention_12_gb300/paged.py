@@ -117,8 +117,8 @@ def attention_decode_paged(q, k_pages, v_pages, page_table, cache_lens, *, scale
     16 on; page_table: int32 [B, max_pages]: key j of sequence b is row
     j % page_size of page page_table[b, j // page_size]; cache_lens: int32 [B].
     shared_len: a multiple of page_size; the first shared_len keys of all
-    sequences lie in the same pages (row 0's are read) and are attended once
-    for the whole batch.  Returns (o, lse) with o like q and lse fp32
+    sequences (of a shorter one, all it has) lie in the same pages and are
+    attended once for the whole batch.  Returns (o, lse) with o like q and lse fp32
     [B, H, n_q].  A page index outside the cache is reported by check().
     """
     shape, pages, index = q.shape, k_pages.shape, q.get_device()

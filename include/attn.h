@@ -267,9 +267,9 @@ typedef struct attn_pages {
  * limited to 64 here; the cache is read once per 64 of these rows.  Rows of a
  * page past the end of its sequence are not used, whatever they hold.
  *
- * shared_len > 0: the first shared_len / page_size entries of every table row
- * name the same pages (a fork of one prompt, a common system prompt), of
- * which row 0 is read.  Their keys are attended once for all sequences, the
+ * shared_len > 0: the first shared_len / page_size entries of the table rows,
+ * as far as each sequence reaches, name the same pages (a fork of one prompt, a
+ * common system prompt); those of the longest sequence are read.  Their keys are attended once for all sequences, the
  * rest per sequence, and the two are merged by the logsumexp rule; the result
  * is that of shared_len = 0 up to rounding.  shared_len must be a multiple
  * of page_size and at most p->N.  A cache_lens[b] below shared_len is allowed:

@@ -92,3 +92,27 @@ def test_a_stalled_latent_step_ends_and_reports(ea, lens, H, room):
 @pytest.mark.parametrize("room", [0, WIDE])
 def test_row_tiles_without_rows(ea, H, n_q, d, shared, room):
     _run(ea, [shared + n for n in (300, 1, 170)], H, 1, n_q, d, 32, True, shared, seed=H, room=room)
+
+
+# --------------------------------------------------------------- the prefix --
+
+@pytest.mark.parametrize("lens", [[0, 300, 257], [100, 300, 90, 513], [0, 0, 90, 30], [64, 256, 256],
+                                  [0] * 40 + [270] + [0] * 40 + [400]])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("room", [0, WIDE])
+def test_a_prefix_is_read_where_a_sequence_holds_it(ea, lens, causal, room):
+    """The first rows of a batch may be empty (padding, ended sequences) or end
+    inside the prefix: their unused entries name nothing."""
+    shared, page = 256, 32
+    rng, g = np.random.default_rng(2), torch.Generator().manual_seed(2)
+    table, P = _table(rng, lens, page, shared=shared, room=room)
+    for b, n in enumerate(lens):
+        table[b, -(-n // page):] = -1
+    k, v = (_poison(torch.randn(P, 2, page, 64, generator=g).to(torch.bfloat16), table, lens, page)
+            for _ in range(2))
+    q = torch.randn(len(lens), 4, 2, 64, generator=g).to(torch.bfloat16)
+    o, lse = ea.attention_decode_paged(q.cuda(), k.cuda(), v.cuda(), torch.from_numpy(table).cuda(),
+                                       torch.tensor(lens, dtype=torch.int32).cuda(), causal=causal,
+                                       shared_len=shared)
+    ea.check()
+    _hold(o, lse, oracle.paged_decode(np64(q), np64(k), np64(v), table, lens, 0.125, causal))
