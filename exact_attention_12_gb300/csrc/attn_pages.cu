@@ -429,8 +429,10 @@ __global__ void __launch_bounds__(kCopyThreads)
       int32_t* row = t.table + s * t.stride;
       for (int j = threadIdx.x; j < n; j += kCopyThreads) {
         const int pg = row[j];
-        if (in_range(pg, t.num_pages)) row[j] = moved[pg];
-        else report(t.status, kStatusPage);
+        const bool there = in_range(pg, t.num_pages);
+        const int to = there ? moved[pg] : -1;   // -1: a free page, which is nobody's now
+        if (there) row[j] = to;
+        if (to < 0) report(t.status, kStatusPage);
       }
     } else {
       const int64_t c = w - heads, i = c / pools.pieces;

@@ -361,7 +361,8 @@ attn_status attn_pages_free(const attn_page_table* t, const int32_t* seqs, int32
 /* Moves the pages in use to the places [0, pages in use): those behind, in
  * ascending order, to the free ones before, in ascending order, in every
  * pool; tables and counts follow.  moved[p] (device [num_pages], output) is
- * where page p now is, -1 for a page that was free. */
+ * where page p now is, -1 for a page that was free (an entry that names one
+ * becomes -1 and is recorded, one outside the cache stays as it is). */
 attn_status attn_pages_compact(const attn_page_table* t, const attn_pool* pools, int32_t n_pools,
                                int32_t* moved, void* ws, size_t ws_bytes, void* stream);
 

@@ -10,6 +10,7 @@ import torch
 from oracle import paged as oracle
 from tests.helpers import np64
 from tests.test_gpu_paged import WIDE, _hold, _poison, _run, _table, ea  # noqa: F401
+from tests.test_gpu_pages import Cache, _i
 
 pytestmark = pytest.mark.gpu
 
@@ -116,3 +117,28 @@ def test_a_prefix_is_read_where_a_sequence_holds_it(ea, lens, causal, room):
                                        shared_len=shared)
     ea.check()
     _hold(o, lse, oracle.paged_decode(np64(q), np64(k), np64(v), table, lens, 0.125, causal))
+
+
+# --------------------------------------------------------------- wrong state --
+
+def _reported(ea):
+    from exact_attention_12_gb300 import _abi
+    with pytest.raises(_abi.AttnError) as e:
+        ea.check()
+    assert e.value.status == _abi.ATTN_ERR_PAGE
+
+
+def test_compact_reports_entries_that_name_no_page_in_use(ea):
+    for wrong in ("free", 20, -1):
+        c = Cache(np.random.default_rng(4), 6, 4, 20, 16, [20, 60, 5, 33])
+        if wrong == "free":
+            wrong = c.twin.refs.index(0)
+        was = c.twin.table[1][2]
+        c.table[1, 2] = wrong
+        moved = ea.pages_compact(c.pools, *c.state, page_size=16)
+        assert moved.cpu().tolist() == c.twin.compact(c.plain)
+        _reported(ea)
+        # the page that the entry had named moved with the others; the entry is as documented
+        assert c.twin.table[1][2] == moved[was].item()
+        c.twin.table[1][2] = wrong if not 0 <= wrong < 20 else -1
+        c.same()
