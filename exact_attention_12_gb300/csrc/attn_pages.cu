@@ -11,14 +11,15 @@
 // launches, so an operation takes one kernel, or two where copies follow from
 // a decision: a one-CTA plan kernel (which pages are taken, which move: ranks
 // by ballots and a scan, so the choice is the lowest free page first and does
-// not depend on timing), then a copy kernel over the whole GPU.  Copies are
+// not depend on timing), then a copy kernel over the whole GPU.  (A fork has a
+// third before them, which looks at every page of the parents.)  Copies are
 // cut into pieces of 16 KB, one per CTA turn, four 16-byte loads in flight a
 // thread.
 //
 // Measured: closing the gaps of 8194 pages of 64 keys (8 heads, d = 128, keys
 // and values; 0.93 GB read and written) 143 us = 6.5 TB/s, the plan before it
-// 8 us; 512 forks of 64 sequences, each with its last page copied, 35 us; four
-// forks of a short prompt 6 us, which is the two launches.
+// 8 us; 512 forks of 64 sequences, each with its last page copied, 36 us; four
+// forks of a short prompt 7 us, which is the three launches.
 #include <climits>
 #include <cstdio>
 
@@ -217,12 +218,40 @@ __global__ void __launch_bounds__(kPlanThreads)
 
 // --------------------------------------------------------------------- fork --
 
+// Whether fork i can be made, as far as it does not depend on the others: its
+// rows exist, the child is empty, and every page that the parent holds is in
+// use (one that is free could be handed out as new in this very call).
+// plen[i]: the parent's length, -1 if not.  A CTA per fork: the plan's one CTA
+// would read all the parents' rows one after another.
+__global__ void __launch_bounds__(128)
+    fork_check_kernel(Table t, const int32_t* parents, const int32_t* children, int32_t* plen) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int i = blockIdx.x, c = children[i], p = parents[i];
+  bool ok = in_range(c, t.rows) && in_range(p, t.rows);
+  const int len = ok ? t.lens[p] : -1;
+  if (ok)
+    ok = t.lens[c] == 0 && len >= 0 && len <= static_cast<int64_t>(t.max_pages) * t.page_size;
+  if (ok) {
+    const int held = held_pages(t, len);
+    for (int j = threadIdx.x; j < held; j += 128) {
+      const int pg = t.table[p * t.stride + j];
+      ok = ok && in_range(pg, t.num_pages) && t.refs[pg] > 0;
+    }
+  }
+  ok = __syncthreads_and(ok);
+  if (threadIdx.x == 0) {
+    plen[i] = ok ? len : -1;
+    if (!ok) report(t.status, kStatusPage);
+  }
+}
+
 // Fork i: children[i] becomes a copy of parents[i].  Its full pages are
 // shared, a part-filled last page gets a page of its own: new_pages[i] (-1:
 // none is needed, -2: the fork is refused or no page is free).
 __global__ void __launch_bounds__(kPlanThreads)
-    fork_plan_kernel(Table t, const int32_t* parents, const int32_t* children, int n,
-                     int32_t* new_pages, int32_t* plen, int32_t* claim, int32_t* list) {
+    fork_plan_kernel(Table t, const int32_t* children, int n, int32_t* new_pages,
+                     int32_t* plen, int32_t* claim, int32_t* list) {
   grid_dep_wait();
   grid_dep_launch();
   __shared__ int scratch[33];
@@ -232,19 +261,12 @@ __global__ void __launch_bounds__(kPlanThreads)
     const int i = i0 + threadIdx.x;
     int part = 0, len = -1;
     if (i < n) {
-      const int c = children[i], p = parents[i];
-      if (in_range(c, t.rows) && in_range(p, t.rows) && claim[c] == i && t.lens[c] == 0 &&
-          t.lens[p] >= 0 &&
-          t.lens[p] <= static_cast<int64_t>(t.max_pages) * t.page_size) {
-        len = t.lens[p];
-        part = len % t.page_size != 0;
-        if (part && !in_range(t.table[p * t.stride + len / t.page_size], t.num_pages)) {
-          part = 0;
-          len = -1;
-        }
+      len = plen[i];
+      if (len >= 0 && claim[children[i]] != i) {   // an earlier fork has the child
+        len = plen[i] = -1;
+        report(t.status, kStatusPage);
       }
-      if (len < 0) report(t.status, kStatusPage);
-      plen[i] = len;
+      part = len > 0 && len % t.page_size != 0;
     }
     int total;
     const int at = need + block_rank(part, scratch, &total);
@@ -314,8 +336,7 @@ __global__ void __launch_bounds__(kCopyThreads)
       for (int j = threadIdx.x; j < full; j += kCopyThreads) {
         const int pg = from[j];
         to[j] = pg;
-        if (in_range(pg, t.num_pages)) atomicAdd(&t.refs[pg], 1);
-        else report(t.status, kStatusPage);
+        atomicAdd(&t.refs[pg], 1);
       }
       if (threadIdx.x == 0) {
         if (new_pages[i] >= 0) {
@@ -610,9 +631,12 @@ attn_status attn_pages_fork(const attn_page_table* t, const attn_pool* pools, in
   const Table d = dev_table(t, ws);
   const size_t rows = static_cast<size_t>(t->rows);
   int32_t* plen = ints(ws, rows);
-  cudaError_t e = launch_pdl(fork_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, d, parents, children,
-                             static_cast<int>(n), new_pages, plen, ints(ws, 0),
-                             ints(ws, rows + 2 * static_cast<size_t>(n)));
+  cudaError_t e = launch_pdl(fork_check_kernel, dim3(static_cast<unsigned>(n)), dim3(128), 0, s, d,
+                             parents, children, plen);
+  if (e == cudaSuccess)
+    e = launch_pdl(fork_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, d, children,
+                   static_cast<int>(n), new_pages, plen, ints(ws, 0),
+                   ints(ws, rows + 2 * static_cast<size_t>(n)));
   for (int i0 = 0; e == cudaSuccess && (i0 < n_pools || i0 == 0); i0 += kPoolsPerLaunch) {
     const Pools g = group(pools, n_pools, i0);
     e = launch_pdl(fork_apply_kernel, dim3(copy_grid(n * (g.pieces + (i0 == 0 ? 1 : 0)))),

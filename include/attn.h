@@ -347,7 +347,8 @@ attn_status attn_pages_extend(const attn_page_table* t, const int32_t* seqs,
  * parents[i]: full pages are shared (their counts grow), a part-filled last
  * page is copied, in every pool, to the lowest free page.  new_pages[i]
  * (device, output) is that page, -1 if none was needed, -2 if the fork was
- * not made.  Of a child that is named twice the first entry counts; all
+ * not made, because of its rows, of a page of the parent that is free or
+ * outside the cache, or for want of a free page.  Of a child that is named twice the first entry counts; all
  * entries see the state before the call. */
 attn_status attn_pages_fork(const attn_page_table* t, const attn_pool* pools, int32_t n_pools,
                             const int32_t* parents, const int32_t* children, int32_t n,

@@ -87,7 +87,7 @@ class PageTable:
 
     def fork(self, parents, children, pools=()):
         free, seen, new = self.free_pages(), set(), []
-        lens = list(self.lens)
+        lens, refs = list(self.lens), list(self.refs)
         for p, c in zip(parents, children):
             rows = range(len(self.table))
             if c not in rows or c in seen:
@@ -98,6 +98,11 @@ class PageTable:
                 new.append(-2)
                 continue
             full, rest = divmod(lens[p], self.size)
+            held = self.table[p][:self.held(lens[p])]
+            if (lens[p] < 0 or lens[p] > len(self.table[p]) * self.size
+                    or not all(0 <= g < len(refs) and refs[g] > 0 for g in held)):
+                new.append(-2)
+                continue
             if rest and not free:
                 new.append(-2)
                 continue

@@ -142,3 +142,30 @@ def test_compact_reports_entries_that_name_no_page_in_use(ea):
         assert c.twin.table[1][2] == moved[was].item()
         c.twin.table[1][2] = wrong if not 0 <= wrong < 20 else -1
         c.same()
+
+
+@pytest.mark.parametrize("at", [0, 2, 3])   # a full page, the last full one, the part-filled one
+@pytest.mark.parametrize("wrong", ["free", "the lowest free", 30, -1, 1 << 30])
+def test_forks_of_a_parent_with_a_wrong_page_are_not_made(ea, at, wrong):
+    """Such a page has no count to raise, and one that is free may be handed out as new
+    in the same call."""
+    c = Cache(np.random.default_rng(5), 9, 5, 30, 16, [20, 60, 5, 33])
+    unused = [p for p, r in enumerate(c.twin.refs) if r == 0]
+    name = {"free": unused[3], "the lowest free": unused[0]}.get(wrong, wrong)
+    c.table[1, at], c.twin.table[1][at] = name, name
+    par, kid = [0, 1, 3, 1, 2], [4, 5, 6, 7, 8]
+    new = ea.pages_fork(c.pools, *c.state, _i(par), _i(kid), page_size=16)
+    want = c.twin.fork(par, kid, c.plain)
+    assert want[1] == want[3] == -2 and new.cpu().tolist() == want
+    _reported(ea)
+    c.same()
+
+
+def test_forks_of_a_parent_with_a_wrong_length_are_not_made(ea):
+    for n in (-1, -16, 81, 1 << 30):
+        c = Cache(np.random.default_rng(6), 6, 5, 30, 16, [20, 60])
+        c.lens[1], c.twin.lens[1] = n, n
+        new = ea.pages_fork(c.pools, *c.state, _i([0, 1]), _i([4, 5]), page_size=16)
+        assert new.cpu().tolist() == c.twin.fork([0, 1], [4, 5], c.plain) and new[1] == -2
+        _reported(ea)
+        c.same()
