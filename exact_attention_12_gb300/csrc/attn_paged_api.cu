@@ -254,7 +254,8 @@ attn_status launched(cudaError_t e, const char* what) {
   return fail(ATTN_ERR_CUDA, msg);
 }
 
-// A tensor map of a cache without pages is never read; it needs some extent.
+// The tensor map of a cache without pages is read past its end only (a table may
+// name pages all the same); it needs some extent.
 int at_least_1(int n) { return n < 1 ? 1 : n; }
 
 int box_rows(const attn_pages* g, int keys) { return g->page_size < keys ? g->page_size : keys; }
@@ -277,6 +278,7 @@ attn_status attn_decode_paged(const attn_params* p, int32_t n_q, const attn_page
   const Layout L = layout(p, n_q, pages, false);
   if ((st = check_ws(ws, ws_bytes, L.total)) != ATTN_OK) return st;
   if (empty(p)) return ATTN_OK;
+  if (pages->num_pages == 0) k = v = q;   // no cache to point at, and none is read
   if ((st = check_ptrs({q, k, v, o, lse})) != ATTN_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   PagedArgs a = args_of(p, n_q, pages, L, q, o, lse, ws);
@@ -347,6 +349,7 @@ attn_status attn_decode_latent(const attn_params* p, int32_t n_q, const attn_pag
   const Layout L = layout(p, n_q, pages, true);
   if ((st = check_ws(ws, ws_bytes, L.total)) != ATTN_OK) return st;
   if (empty(p)) return ATTN_OK;
+  if (pages->num_pages == 0) c = q;   // no cache to point at, and none is read
   if ((st = check_ptrs({q, c, o, lse})) != ATTN_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   PagedArgs a = args_of(p, n_q, pages, L, q, o, lse, ws);

@@ -501,12 +501,12 @@ int check_table(const attn_page_table* t) {
   return ATTN_OK;
 }
 
-int check_pools(const attn_pool* pools, int n_pools) {
+int check_pools(const attn_pool* pools, int n_pools, int num_pages) {
   if (n_pools < 0 || (n_pools > 0 && pools == nullptr))
     return bad(ATTN_ERR_INVALID_ARG, "pools: bad count or NULL");
   for (int i = 0; i < n_pools; ++i) {
     const attn_pool& p = pools[i];
-    if (p.base == nullptr || (reinterpret_cast<uintptr_t>(p.base) & 15u) != 0)
+    if ((p.base == nullptr && num_pages > 0) || (reinterpret_cast<uintptr_t>(p.base) & 15u) != 0)
       return bad(ATTN_ERR_INVALID_ARG, "pools: base must be 16-byte aligned");
     if (p.page_bytes <= 0 || p.page_bytes % 16 != 0 || p.page_stride % 16 != 0 ||
         p.page_stride < p.page_bytes)
@@ -585,7 +585,8 @@ attn_status attn_pages_copy(const attn_pool* pools, int32_t n_pools, int32_t num
                             const int32_t* src, const int32_t* dst, int32_t n, void* ws,
                             size_t ws_bytes, void* stream) {
   int st;
-  if ((st = check_pools(pools, n_pools)) != ATTN_OK || (st = check_list(n, src, dst)) != ATTN_OK ||
+  if ((st = check_pools(pools, n_pools, num_pages)) != ATTN_OK ||
+      (st = check_list(n, src, dst)) != ATTN_OK ||
       (st = check_ws_bytes(ws, ws_bytes, kHeader)) != ATTN_OK)
     return static_cast<attn_status>(st);
   if (num_pages < 0) return static_cast<attn_status>(bad(ATTN_ERR_INVALID_ARG, "negative num_pages"));
@@ -621,7 +622,8 @@ attn_status attn_pages_fork(const attn_page_table* t, const attn_pool* pools, in
                             const int32_t* parents, const int32_t* children, int32_t n,
                             int32_t* new_pages, void* ws, size_t ws_bytes, void* stream) {
   int st;
-  if ((st = check_table(t)) != ATTN_OK || (st = check_pools(pools, n_pools)) != ATTN_OK ||
+  if ((st = check_table(t)) != ATTN_OK ||
+      (st = check_pools(pools, n_pools, t->num_pages)) != ATTN_OK ||
       (st = check_list(n, parents, children)) != ATTN_OK ||
       (st = check_list(n, new_pages, new_pages)) != ATTN_OK ||
       (st = check_ws_bytes(ws, ws_bytes, attn_pages_workspace_size(t, n))) != ATTN_OK)
@@ -663,11 +665,12 @@ attn_status attn_pages_free(const attn_page_table* t, const int32_t* seqs, int32
 attn_status attn_pages_compact(const attn_page_table* t, const attn_pool* pools, int32_t n_pools,
                                int32_t* moved, void* ws, size_t ws_bytes, void* stream) {
   int st;
-  if ((st = check_table(t)) != ATTN_OK || (st = check_pools(pools, n_pools)) != ATTN_OK ||
+  if ((st = check_table(t)) != ATTN_OK ||
+      (st = check_pools(pools, n_pools, t->num_pages)) != ATTN_OK ||
       (st = check_ws_bytes(ws, ws_bytes, attn_pages_workspace_size(t, 0))) != ATTN_OK)
     return static_cast<attn_status>(st);
-  if (t->num_pages == 0) return ATTN_OK;
-  if (moved == nullptr) return static_cast<attn_status>(bad(ATTN_ERR_INVALID_ARG, "moved is NULL"));
+  if (moved == nullptr && t->num_pages > 0)
+    return static_cast<attn_status>(bad(ATTN_ERR_INVALID_ARG, "moved is NULL"));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const Table d = dev_table(t, ws);
   const size_t P = static_cast<size_t>(t->num_pages);

@@ -265,7 +265,8 @@ typedef struct attn_pages {
  *   p->N    must be max_pages * page_size
  * and the same query rows, masks and outputs.  (H / H_kv) * n_q is not
  * limited to 64 here; the cache is read once per 64 of these rows.  Rows of a
- * page past the end of its sequence are not used, whatever they hold.
+ * page past the end of its sequence are not used, whatever they hold.  A cache
+ * of no pages is one too: k and v may be NULL then.
  *
  * shared_len > 0: the first shared_len / page_size entries of the table rows,
  * as far as each sequence reaches, name the same pages (a fork of one prompt, a
@@ -317,8 +318,8 @@ typedef struct attn_page_table {
 } attn_page_table;
 
 /* One buffer of pages (keys or values of one layer, latent vectors, ...): a
- * page's page_bytes are contiguous.  base 16-byte aligned, both sizes
- * multiples of 16. */
+ * page's page_bytes are contiguous.  base 16-byte aligned (NULL where the cache
+ * has no pages), both sizes multiples of 16. */
 typedef struct attn_pool {
   void* base;
   int64_t page_stride, page_bytes;

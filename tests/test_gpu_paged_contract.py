@@ -169,3 +169,47 @@ def test_forks_of_a_parent_with_a_wrong_length_are_not_made(ea):
         assert new.cpu().tolist() == c.twin.fork([0, 1], [4, 5], c.plain) and new[1] == -2
         _reported(ea)
         c.same()
+
+
+# ------------------------------------------------------------------ nothing --
+
+def test_caches_without_pages(ea):
+    """As a serving program has them before it has decided how many pages there are."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    k, c = (torch.zeros(0, *s, dtype=torch.bfloat16, device="cuda") for s in ((2, 16, 64), (16, 320)))
+    q, qc = (torch.ones(3, 4, 2, d, dtype=torch.bfloat16, device="cuda") for d in (64, 320))
+    for width, len_ in ((0, 0), (4, 0), (2000, 0), (4, 40), (2000, 40)):
+        t, n = torch.zeros(3, width, **i32), torch.full((3,), len_, **i32)
+        for shared in (0, 32):
+            if shared > width * 16:
+                continue
+            o, lse = ea.attention_decode_paged(q, k, k, t, n, shared_len=shared)
+            assert torch.all(o == 0)   # keys that are named read as zeros
+            _empty_or_named(ea, lse, len_)
+        o, lse = ea.attention_decode_latent(qc, c, t, n, scale=0.1, d_v=256)
+        assert torch.all(o == 0)
+        _empty_or_named(ea, lse, len_)
+    t, n, refs = torch.full((3, 4), -1, **i32), torch.zeros(3, **i32), torch.zeros(0, **i32)
+    none = torch.zeros(0, **i32)
+    pools = (k, c)
+    assert ea.pages_compact(pools, t, n, refs, page_size=16).numel() == 0
+    assert ea.pages_fork(pools, t, n, refs, none, none, page_size=16).numel() == 0
+    assert ea.pages_fork(pools, t, n, refs, _i([0]), _i([2]), page_size=16).tolist() == [-1]
+    ea.pages_copy(pools, none, none)
+    ea.pages_free(t, n, refs, _i([0, 1]), page_size=16)
+    ea.pages_extend(t, n, refs, _i([0]), _i([0]), page_size=16)
+    ea.check()
+    assert torch.all(t == -1) and torch.all(n == 0)
+    n[1] = 20
+    ea.pages_compact(pools, t, n, refs, page_size=16)
+    _reported(ea)
+
+
+def _empty_or_named(ea, lse, len_):
+    if len_ == 0:
+        assert torch.all(torch.isneginf(lse))
+        ea.check()
+    else:
+        want = torch.tensor([[len_ - 1, len_]], dtype=torch.float64).log()   # scores of 0, causal
+        assert (lse.cpu() - want).abs().max() <= 1e-5
+        _reported(ea)
