@@ -87,8 +87,8 @@ def _table(table, cache_lens, B, index, page_size):
 
 
 def _strides(t):
-    """Strides of a tensor; an axis of one element, over which nothing strides,
-    has the value it has in a contiguous tensor."""
+    """Strides of a tensor; an axis of one element or none, over which nothing
+    strides, has the value it has in a contiguous tensor."""
     shape = t.shape
     if not t.is_contiguous():
         s = list(t.stride())
@@ -97,7 +97,7 @@ def _strides(t):
     else:
         s = [1] * len(shape)
         for i in range(len(shape) - 2, -1, -1):
-            s[i] = s[i + 1] * shape[i + 1]
+            s[i] = s[i + 1] * (shape[i + 1] or 1)
         return s
     inner = shape[-1]
     for i in range(len(shape) - 2, -1, -1):
@@ -130,17 +130,17 @@ def attention_decode_paged(q, k_pages, v_pages, page_table, cache_lens, *, scale
                          "[num_pages, H_kv, page_size, d]")
     B, H, n_q, d = shape
     num_pages, H_kv, page_size, _ = pages
-    if H_kv < 1 or H % H_kv:
+    if H_kv < (1 if H else 0) or (H_kv and H % H_kv):
         raise ValueError("H_kv must divide q's H")
     if k_pages.is_contiguous() and v_pages.is_contiguous():
-        ks = (H_kv * page_size * d, page_size * d, d)
+        ks = ((H_kv or 1) * page_size * d, page_size * d, d)
     else:
         ks = _strides(k_pages)
         if ks != _strides(v_pages):
             raise ValueError("k_pages and v_pages must share strides")
     device = q.device
     dense = q.is_contiguous()
-    qs = (H * n_q * d, n_q * d, d) if dense else _strides(q)[:3]
+    qs = ((H or 1) * n_q * d, n_q * d, d) if dense else _strides(q)[:3]
     if out is None:
         out = _empty_like(q) if dense else torch.empty_strided(shape, q.stride(), dtype=_bf16,
                                                                device=device)

@@ -213,3 +213,20 @@ def _empty_or_named(ea, lse, len_):
         want = torch.tensor([[len_ - 1, len_]], dtype=torch.float64).log()   # scores of 0, causal
         assert (lse.cpu() - want).abs().max() <= 1e-5
         _reported(ea)
+
+
+@pytest.mark.parametrize("H_kv", [0, 2])
+def test_no_heads(ea, H_kv):
+    i32 = dict(dtype=torch.int32, device="cuda")
+    t, n = torch.zeros(3, 4, **i32), torch.full((3,), 20, **i32)
+    k = torch.zeros(5, H_kv, 16, 64, dtype=torch.bfloat16, device="cuda")
+    for n_q in (1, 2):
+        o, lse = ea.attention_decode_paged(k.new_zeros(3, 0, n_q, 64), k, k, t, n)
+        assert o.shape == (3, 0, n_q, 64) and lse.shape == (3, 0, n_q)
+        o, lse = ea.attention_decode_latent(k.new_zeros(3, 0, n_q, 320), k.new_zeros(5, 16, 320), t,
+                                            n, scale=0.1, d_v=256)
+        assert o.shape == (3, 0, n_q, 256) and lse.shape == (3, 0, n_q)
+    if H_kv == 0:   # heads that no key/value head serves
+        with pytest.raises(ValueError):
+            ea.attention_decode_paged(k.new_zeros(3, 4, 1, 64), k, k, t, n)
+    ea.check()

@@ -5,6 +5,9 @@ import glob
 import os
 import re
 
+import pytest
+import torch
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "exact_attention_12_gb300", "csrc")
 
@@ -50,3 +53,23 @@ def test_thread_indices_are_compared_as_what_they_are():
     for path in glob.glob(os.path.join(CSRC, "*.cu*")):
         for other in re.findall(r"threadIdx\.x\s*(?:<|>=|<=|>)\s*([\w:]+)", _code(path)):
             assert re.fullmatch(r"(C::)?k[A-Z]\w*|\d+", other), (path, other)
+
+
+@pytest.mark.parametrize("H_kv", [0, 2])
+@pytest.mark.parametrize("n_q", [1, 3])
+def test_no_heads_reach_the_library_with_strides_it_takes(monkeypatch, H_kv, n_q):
+    from exact_attention_12_gb300 import _abi, paged
+    seen = []
+
+    def call(fn, size_fn, size_args, args, device, ws, what):
+        p, q, g = size_args
+        seen.append(size_fn(p, q, g))
+
+    monkeypatch.setattr(paged, "_call", call)
+    bf = torch.bfloat16
+    t, n = torch.zeros(3, 4, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    k = torch.zeros(5, H_kv, 16, 64, dtype=bf)
+    paged.attention_decode_paged(torch.zeros(3, 0, n_q, 64, dtype=bf), k, k, t, n)
+    paged.attention_decode_latent(torch.zeros(3, 0, n_q, 320, dtype=bf),
+                                  torch.zeros(5, 16, 320, dtype=bf), t, n, scale=0.1, d_v=256)
+    assert min(seen) >= 256, _abi.lib().attn_last_error()
