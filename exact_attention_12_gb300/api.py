@@ -22,6 +22,14 @@ _workspaces = {}
 _retired = {}
 
 
+def _device(device):
+    """`device` as a torch.device; "cuda" is the current one, with its number."""
+    dev = device if isinstance(device, torch.device) else torch.device(device)
+    if dev.type == "cuda" and dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    return dev
+
+
 def workspace(device, nbytes):
     """A zero-initialised device workspace of at least `nbytes`, cached per device.
 
@@ -30,9 +38,9 @@ def workspace(device, nbytes):
     pass separate workspaces.  When a call needs more, the cache grows to at
     least twice its size; the buffer it replaces stays allocated for the life
     of the process, because a CUDA graph captured earlier still holds its
-    address.
+    address; check() looks at it as well.
     """
-    dev = device if isinstance(device, torch.device) else torch.device(device)
+    dev = _device(device)
     key = (dev.type, dev.index)
     t = _workspaces.get(key)
     if t is None or t.numel() < nbytes:
@@ -224,8 +232,16 @@ def attention_decode(q, k, v, cache_lens, *, scale=None, causal=True, out=None, 
 
 
 def check(ws=None, device=None):
-    """Synchronise the current stream and raise if a kernel recorded a time-out."""
-    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    w = workspace(dev, 256) if ws is None else ws
-    st = lib().attn_check(w.data_ptr(), _stream(dev))
+    """Synchronise the device's current stream and raise if a kernel recorded an
+    error: a wait that timed out, a page index or list entry out of range, a
+    cache without a free page.  `ws`: the workspace of the calls to check;
+    None is the device's shared one, with those it has grown out of (calls and
+    graphs from before record theirs there)."""
+    dev = _device("cuda" if device is None else device)
+    spaces = [ws]
+    if ws is None:
+        spaces = [*_retired.get((dev.type, dev.index), ()), workspace(dev, 256)]
+    st = _abi.ATTN_OK
+    for w in spaces:
+        st = lib().attn_check(w.data_ptr(), _stream(dev)) or st   # each is read and cleared
     check_status(st, "attn_check")

@@ -230,3 +230,36 @@ def test_no_heads(ea, H_kv):
         with pytest.raises(ValueError):
             ea.attention_decode_paged(k.new_zeros(3, 4, 1, 64), k, k, t, n)
     ea.check()
+
+
+# ------------------------------------------------------------------- status --
+
+def test_check_sees_what_was_recorded_before_the_workspace_grew(ea):
+    from exact_attention_12_gb300 import _abi
+    k = torch.zeros(4, 1, 16, 64, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(1, 2, 1, 64, dtype=torch.bfloat16, device="cuda")
+    t, n = _i([0, 9]).view(1, 2), _i([32])
+    dev = q.device
+
+    def grow():
+        before = ea.workspace(dev, 256)
+        assert ea.workspace(dev, before.numel() + 1).data_ptr() != before.data_ptr()
+
+    def page():
+        _reported(ea)
+        ea.check()   # read and cleared
+
+    ea.attention_decode_paged(q, k, k, t, n)
+    grow()
+    page()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ea.attention_decode_paged(q, k, k, t, n)
+    grow()
+    graph.replay()
+    page()
+    ea.attention_decode_paged(q, k, k, t, n)
+    with pytest.raises(_abi.AttnError):
+        ea.check(device="cuda")
+    assert ea.workspace("cuda", 256).data_ptr() == ea.workspace(dev, 256).data_ptr()
+    ea.check()

@@ -73,3 +73,32 @@ def test_no_heads_reach_the_library_with_strides_it_takes(monkeypatch, H_kv, n_q
     paged.attention_decode_latent(torch.zeros(3, 0, n_q, 320, dtype=bf),
                                   torch.zeros(5, 16, 320, dtype=bf), t, n, scale=0.1, d_v=256)
     assert min(seen) >= 256, _abi.lib().attn_last_error()
+
+
+def test_check_reads_every_workspace_of_the_device(monkeypatch):
+    from exact_attention_12_gb300 import _abi, api
+
+    class Lib:
+        def attn_check(self, ptr, stream):
+            seen.append(ptr)
+            return bad.pop(ptr, _abi.ATTN_OK)   # read and cleared
+
+        def attn_last_error(self):
+            return b""
+
+    monkeypatch.setattr(api, "lib", Lib)
+    monkeypatch.setattr(_abi, "lib", Lib)
+    monkeypatch.setattr(api, "_stream", lambda dev: None)
+    monkeypatch.setattr(api, "_workspaces", {})
+    monkeypatch.setattr(api, "_retired", {})
+    spaces = [api.workspace("cpu", 256 << i) for i in range(3)]
+    for w in spaces:
+        seen, bad = [], {w.data_ptr(): _abi.ATTN_ERR_PAGE}
+        with pytest.raises(_abi.AttnError) as e:
+            api.check(device="cpu")
+        assert e.value.status == _abi.ATTN_ERR_PAGE
+        assert sorted(seen) == sorted(x.data_ptr() for x in spaces)
+        api.check(device="cpu")
+    seen = []
+    api.check(ws=spaces[1], device="cpu")   # the caller's own: that one alone
+    assert seen == [spaces[1].data_ptr()]
