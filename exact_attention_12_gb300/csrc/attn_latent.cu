@@ -53,7 +53,6 @@ using namespace sm103;
 
 namespace {
 
-constexpr int kAhead = 1;   // tiles between a tile's way to L2 and its copy (2: 38.7 -> 40.4 us)
 constexpr int kLooks = 4096;   // at two barriers in turn, before the wait (which is limited) for one
 
 template <int DV>
@@ -204,7 +203,7 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
     // Tile t of piece p, or past its end of the piece behind it, on its way to
     // L2: the two tiles in shared memory are too few to cover the latency of
     // HBM, and their copies go through a tile's memory 256 bytes of a token at
-    // a time, where this reads it in one run.
+    // a time, where this reads it in one run.  (Two tiles ahead: 38.7 -> 40.4 us.)
     auto ahead = [&](int t) {
       int b = p.b, len = p.len;
       if (t >= p.t1) {
@@ -251,8 +250,7 @@ __global__ void __launch_bounds__(LatentCfg<DV>::kThreads, 1)
         }
         if (!ok) break;
         // (a CTA's first tiles themselves go out before any of this)
-        if (fetch && T + 1 >= ST)
-          for (int k = T + 1 == ST ? 1 : kAhead; k <= kAhead; ++k) ahead(t + k);
+        if (fetch && T + 1 >= ST) ahead(t + 1);
       }
     }
     if (!ok && lane == 0)   // let issued copies land before the CTA exits

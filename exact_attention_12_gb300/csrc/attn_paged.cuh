@@ -173,12 +173,6 @@ __device__ __forceinline__ int checked_page(int page, int num_pages, int* status
   return max(num_pages, 1);   // (the tensor map of an empty cache has one page)
 }
 
-// CTAs that share T units when `launched` are there.
-__device__ __forceinline__ int paged_ctas(int64_t total, int launched) {
-  const int64_t most = total / kPagedMinUnits;
-  return most >= launched ? launched : max(1, static_cast<int>(most));
-}
-
 // A CTA's run [lo, hi) of the units, and where it starts.  (All units together
 // are less than 2^31: the host sees to that.)
 struct PagedShare {
