@@ -120,9 +120,11 @@ struct PrefixArgs {
 };
 
 // The constants below were swept on whole steps.  Overhead (units a segment
-// costs beside its tiles): ragged batches of long caches 342 / 332 / 326 us at
-// 4 / 8 / 12, a batch of short ones under a prefix 110 us at 8 and 12; least
-// share 6 or 9 units of 32 keys: one sequence of 517 keys 10.4 / 11.7 us; latent
+// costs beside its tiles) 8 / 12, neither best throughout: 48 sequences of
+// 250-1000 keys 30.8 / 31.5 us, 4 of 10000-20000 45.4 / 45.6, 16 of 4096-8192
+// 70.9 / 70.6, 64 of 0-16384 with 32 rows 330 / 320, 2 of 30000 with 64 rows
+// 27.2 / 24.3, a batch of short ones under a prefix 86.8 / 86.1.  8 is what the
+// other constants were swept with.  Least share 6 or 9 units of 32 keys: one sequence of 517 keys 10.4 / 11.7 us; latent
 // 2 / 3 / 6 units of 64: 13.6 / 15.1 / 21.3 us with 700 tokens.  Clusters: at
 // most 24 / 48 key tiles a CTA (d = 128): 64 sequences of 200-800 keys 32.4 /
 // 34.5 us; at most 4 / 8 latent tiles: 3000 tokens 13.0 / 15.9 us.  A segment
