@@ -111,6 +111,9 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // In this order: the decode kernel behind this one does not wait for it before
+  // it reads and writes (attn_paged.cu), it relies on every CTA here having
+  // waited for what comes before.
   grid_dep_wait();
   grid_dep_launch();
   const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.tmem_base, 0);

@@ -61,8 +61,12 @@
  * value, so the calls can be captured into a CUDA graph and replayed.  Make
  * one uncaptured call of each kind first: it sets the kernels' attributes.
  * The forward and backward kernels and those on paged caches are launched
- * with programmatic stream serialisation; each waits for the preceding work in the stream to complete
- * before it reads or writes global memory.
+ * with programmatic stream serialisation; each waits for the preceding work in
+ * the stream to complete before it reads or writes global memory.  One does not
+ * wait for the kernel directly before it: with a shared prefix the paged decode
+ * kernel starts on its own keys as soon as every CTA of the prefix kernel has
+ * passed that wait, so everything before the call is complete, and waits for the
+ * prefix kernel before it merges and before it ends.
  *
  * Thread safety: calls on different workspaces may run concurrently; two
  * calls in flight on the same workspace race.
@@ -263,10 +267,20 @@ typedef struct attn_pages {
  *   k, v    [num_pages, H_kv, page_size, d] bf16, where kv_stride_b is the
  *           stride between pages (all three key/value strides are required)
  *   p->N    must be max_pages * page_size
- * and the same query rows, masks and outputs.  (H / H_kv) * n_q is not
- * limited to 64 here; the cache is read once per 64 of these rows.  Rows of a
- * page past the end of its sequence are not used, whatever they hold.  A cache
- * of no pages is one too: k and v may be NULL then.
+ * and the same query rows, masks and outputs.  rows = (H / H_kv) * n_q is not
+ * limited to 64 here; the cache is read once per 64 of these rows.  Limits
+ * (ATTN_ERR_UNSUPPORTED beyond): H * n_q <= 32768, B * H * n_q <= 2^30, p->N <=
+ * 2^30, and B * H_kv * ceil(rows / 64) * (p->N / 32 + 9) < 2^31.
+ * Rows of a page past the end of its sequence are not used, whatever they
+ * hold.  A key that a query row may not attend (causal, n_q > 1) may hold
+ * anything too, but its value must be finite unless no row of its sequence
+ * attends it: a probability of 0 times infinity or NaN is NaN.  A cache of no
+ * pages is one too: k and v may be NULL then.
+ *
+ * How the work is given out goes by max_pages, not by the lengths, which are on
+ * the device: where all sequences are short, a table that is no wider than the
+ * longest needs is faster (64 sequences of 50 to 200 keys: 13 us, with room for
+ * 20000 keys 19 us).
  *
  * shared_len > 0: the first shared_len / page_size entries of the table rows,
  * as far as each sequence reaches, name the same pages (a fork of one prompt, a
@@ -294,8 +308,10 @@ attn_status attn_decode_paged(const attn_params* p, int32_t n_q, const attn_page
  *   c       [num_pages, page_size, d + 64] bf16; kv_stride_b between pages,
  *           kv_stride_n between tokens (kv_stride_h is ignored)
  *   o       [B, H, n_q, d] bf16, contiguous;  lse fp32 [B, H, n_q]
- * key_lens, causal and the query positions are those of attn_decode; H * n_q
- * is not limited.  pages->shared_len must be 0. */
+ * key_lens, causal and the query positions are those of attn_decode, what is
+ * said of max_pages and of values that some rows may not attend holds here too.
+ * Limits (ATTN_ERR_UNSUPPORTED beyond): H * n_q <= 32768, B * H * n_q <= 2^30,
+ * p->N <= 2^30, B * (p->N / 64 + 9) < 2^31.  pages->shared_len must be 0. */
 size_t attn_decode_latent_workspace_size(const attn_params* p, int32_t n_q,
                                          const attn_pages* pages);
 attn_status attn_decode_latent(const attn_params* p, int32_t n_q, const attn_pages* pages,

@@ -1,6 +1,7 @@
 """What the paged-cache calls promise beyond their results, as far as it shows
 without a GPU: the sources, the argument checks, the binding."""
 
+import ctypes
 import glob
 import os
 import re
@@ -102,3 +103,57 @@ def test_check_reads_every_workspace_of_the_device(monkeypatch):
     seen = []
     api.check(ws=spaces[1], device="cpu")   # the caller's own: that one alone
     assert seen == [spaces[1].data_ptr()]
+
+
+def _step(latent, **kw):
+    """The workspace size of a decode step with these sizes; 0: refused."""
+    from exact_attention_12_gb300 import _abi
+    d = 256 if latent else 64
+    cols = d + 64 if latent else d
+    p, g = _abi.AttnParams(), _abi.AttnPages()
+    p.B, p.H, p.H_kv, p.d, p.scale = 1, 4, 1, d, 1.0
+    p.stride_b, p.stride_h, p.stride_n = 1 << 30, 1 << 20, cols
+    p.kv_stride_b, p.kv_stride_h, p.kv_stride_n = 1 << 30, 1 << 20, cols
+    p.key_lens = g.table = 0x1000
+    g.max_pages, g.page_size, g.num_pages = 1, 16, 1
+    n_q = kw.pop("n_q", 1)
+    for k, v in kw.items():
+        setattr(g if hasattr(g, k) else p, k, v)
+    g.table_stride, p.N = g.max_pages, g.max_pages * g.page_size
+    f = _abi.lib().attn_decode_latent_workspace_size if latent \
+        else _abi.lib().attn_decode_paged_workspace_size
+    size = f(ctypes.byref(p), n_q, ctypes.byref(g))
+    assert size or b"2^3" in _abi.lib().attn_last_error()
+    return size
+
+
+@pytest.mark.parametrize("latent", [False, True])
+@pytest.mark.parametrize("most,more", [
+    (dict(H=32768), dict(H=32769)), (dict(H=8, n_q=4096), dict(H=8, n_q=4097)),
+    (dict(H=1 << 10, B=1 << 20), dict(H=1 << 10, B=(1 << 20) + 1)),
+    (dict(max_pages=1 << 15, page_size=32768), dict(max_pages=(1 << 15) + 1, page_size=32768))])
+def test_the_documented_limits(latent, most, more):
+    assert _step(latent, **most) > 0 and _step(latent, **more) == 0
+
+
+def test_the_documented_limit_of_all_work_together():
+    # B * H_kv * ceil(rows / 64) * (N / 32 + 9) < 2^31, latent B * (N / 64 + 9)
+    units = (1 << 15) // 32 + 9
+    b = ((1 << 31) - 1) // (2 * units)
+    wide = dict(H=65, H_kv=1, max_pages=1 << 11)
+    assert b * 65 <= 1 << 30
+    assert _step(False, B=b, **wide) > 0 and _step(False, B=b + 1, **wide) == 0
+    units = (1 << 22) // 64 + 9
+    b = ((1 << 31) - 1) // units
+    wide = dict(max_pages=1 << 18)
+    assert _step(True, B=b, **wide) > 0 and _step(True, B=b + 1, **wide) == 0
+
+
+def test_kernels_wait_before_they_let_the_next_one_start():
+    # a kernel behind a shared prefix's relies on it: all work before the prefix kernel is
+    # complete once that has let it start
+    for path in glob.glob(os.path.join(CSRC, "*.cu")):
+        for kernel in re.split(r"__global__", _code(path))[1:]:
+            launch = kernel.find("grid_dep_launch();")
+            if launch >= 0:
+                assert 0 <= kernel.find("grid_dep_wait();") < launch, path
