@@ -118,7 +118,8 @@ def attention_decode_paged(q, k_pages, v_pages, page_table, cache_lens, *, scale
     j % page_size of page page_table[b, j // page_size]; cache_lens: int32 [B].
     shared_len: a multiple of page_size; the first shared_len keys of all
     sequences (of a shorter one, all it has) lie in the same pages and are
-    attended once for the whole batch.  A table no wider than the longest
+    attended once for the whole batch, which pays from about B * H_kv = 32 on.
+    A table no wider than the longest
     sequence needs (page_table[:, :most]) is faster where all are short.
     Returns (o, lse) with o like q and lse fp32 [B, H, n_q].  A page index
     outside the cache is reported by check().
