@@ -119,10 +119,10 @@ def attention_decode_paged(q, k_pages, v_pages, page_table, cache_lens, *, scale
     shared_len: a multiple of page_size; the first shared_len keys of all
     sequences (of a shorter one, all it has) lie in the same pages and are
     attended once for the whole batch, which pays from about B * H_kv = 32 on.
-    A table no wider than the longest
-    sequence needs (page_table[:, :most]) is faster where all are short.
-    Returns (o, lse) with o like q and lse fp32 [B, H, n_q].  A page index
-    outside the cache is reported by check().
+    A table no wider than the longest sequence needs (page_table[:, :most]) is
+    faster where all are short.  Returns (o, lse) with o like
+    q and lse fp32 [B, H, n_q].  A page index outside the cache is reported by
+    check().
     """
     shape, pages, index = q.shape, k_pages.shape, q.get_device()
     if not (q.dtype is k_pages.dtype is v_pages.dtype is _bf16) \
