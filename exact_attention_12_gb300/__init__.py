@@ -15,6 +15,8 @@ from .api import (  # noqa: F401
     workspace,
     workspace_size,
 )
+from .eviction import attention_key_weights, pages_evict  # noqa: F401
+from .fp4 import attention_decode_fp4, pages_load_fp4, pages_store_fp4  # noqa: F401
 from .paged import (  # noqa: F401
     attention_decode_latent,
     attention_decode_paged,

@@ -65,6 +65,26 @@ EXPORTS = {
     "attn_pages_compact": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
                                           ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
                                           ctypes.c_void_p]),
+    "attn_pages_store_fp4": (ctypes.c_int, [ctypes.c_void_p] * 8 + [ctypes.c_size_t,
+                                                                    ctypes.c_void_p]),
+    "attn_pages_load_fp4": (ctypes.c_int, [ctypes.c_void_p] * 8 + [ctypes.c_size_t,
+                                                                   ctypes.c_void_p]),
+    "attn_decode_fp4_workspace_size": (ctypes.c_size_t, [ctypes.c_void_p, ctypes.c_int32,
+                                                         ctypes.c_void_p]),
+    "attn_decode_fp4": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32] + [ctypes.c_void_p] * 7
+                        + [ctypes.c_size_t, ctypes.c_void_p]),
+    "attn_key_weights": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32] + [ctypes.c_void_p] * 6
+                         + [ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p,
+                            ctypes.c_size_t, ctypes.c_void_p]),
+    "attn_pages_evict_workspace_size": (ctypes.c_size_t, [ctypes.c_void_p, ctypes.c_int32,
+                                                          ctypes.c_int32, ctypes.c_void_p,
+                                                          ctypes.c_int32]),
+    "attn_pages_evict": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                                        ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64,
+                                        ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p,
+                                        ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
+                                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                                        ctypes.c_void_p]),
     "attn_selftest_timeout": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p]),
     "attn_debug_stall": (ctypes.c_int, [ctypes.c_int32, ctypes.c_uint64]),
     "attn_check": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
@@ -118,6 +138,27 @@ class AttnPool(ctypes.Structure):
 
     _fields_ = [("base", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
                 ("page_bytes", ctypes.c_int64)]
+
+
+class AttnFp4(ctypes.Structure):
+    """Mirror of `attn_fp4`."""
+
+    _fields_ = [
+        ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+        ("code_page", ctypes.c_int64), ("code_head", ctypes.c_int64),
+        ("scale_page", ctypes.c_int64), ("scale_head", ctypes.c_int64),
+        ("descale", ctypes.c_float), ("reserved", ctypes.c_int32),
+    ]
+
+
+class AttnRows(ctypes.Structure):
+    """Mirror of `attn_rows`."""
+
+    _fields_ = [
+        ("base", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64),
+        ("row_bytes", ctypes.c_int32), ("reserved", ctypes.c_int32),
+    ]
 
 
 class AttnError(RuntimeError):

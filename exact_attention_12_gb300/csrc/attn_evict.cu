@@ -1,0 +1,642 @@
+// Eviction from a paged cache by gathered attention weight.
+//
+// What it computes (include/attn.h): of a sequence of `old` keys that shrinks to
+// `len`, each head keeps its last r = min(recent, len) keys and the len - r of the
+// others that have the largest weights, in their order, at the front.
+//
+// Three kernels:
+//   1. select, a cluster of CTAs per (sequence, head): the weights as 32-bit keys
+//      in the order of the numbers; the (len - r)-th largest by three rounds of
+//      counting digits (11, 11, 10 bits), every CTA its own part, the counts
+//      added up through the cluster's shared memory; then where each kept key
+//      goes, by ballots and running counts.
+//   2. move, in place.  Key j comes from slots[j] >= j, and slots ascends, so the
+//      keys are moved in chunks of T: a CTA reads a chunk's rows of all pools
+//      into shared memory, says so, waits until the chunks in front of it whose
+//      rows lie where it writes have been read too, and writes.  Chunks are given
+//      out by a ticket, front to back, so what a CTA waits for is always being
+//      worked on, whichever CTAs are resident; a row is read and written once,
+//      and what stays where it is is not touched.
+//   3. finish: pages that are left over go back, lengths and tables follow.
+//
+// Bound: HBM, the moved rows twice and the weights once; on a short cache the
+// three launches.
+#include <climits>
+#include <cstdio>
+
+#include "attn.h"
+#include "attn_kernels.cuh"
+#include "attn_paged.cuh"
+
+namespace attn {
+using namespace sm103;
+
+namespace {
+
+constexpr int kSelectThreads = 1024;
+constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kMaxCluster = 8;
+constexpr int kMoveThreads = 256;
+constexpr int kMoveBytes = 32768;         // of a chunk, all pools
+constexpr int kMaxChunk = 1024;           // keys of a chunk
+constexpr int kMaxPools = 16;
+constexpr int kFinishThreads = 128;
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+
+struct RowPool {
+  char* base;
+  int64_t page, head, row;   // bytes between pages, heads, rows
+  int bytes;                 // of a row
+  int unit;                  // bytes of one copy: 16, 8 or 4
+  int at;                    // where its rows begin in a chunk's buffer
+};
+
+struct EvictArgs {
+  int32_t* table;
+  int64_t table_stride;
+  int32_t* lens;
+  int32_t* refs;
+  int rows, max_pages, page_shift, num_pages;
+  int heads, n, recent, width;
+  float* weights;
+  int64_t weight_row, weight_head;
+  const int32_t* seqs;
+  const int32_t* new_lens;
+  int32_t* slots;            // [n][heads][width]
+  // workspace
+  int32_t* old_len;          // [n]: -1 where nothing is done
+  int32_t* new_len;          // [n]
+  int32_t* ticket;
+  int32_t* read;             // [n][heads][chunks]: the chunk's rows have been read
+  int32_t* bound;            // [n][heads][chunks + 1]: kept keys before slot c T
+  int chunk, chunks;         // T; chunks of a row of the table
+  int cluster;               // CTAs per (sequence, head) of the first kernel
+  int n_pools;
+  RowPool pools[kMaxPools];
+  int buffer;                // bytes of a chunk, all pools
+  int* status;
+};
+
+__device__ void report(int* status, int code) {
+  if (atomicCAS(status, 0, code) == 0) atomicExch(status + 1, kSitePageIndex);
+}
+
+__device__ __forceinline__ bool in_range(int i, int n) {
+  return static_cast<unsigned>(i) < static_cast<unsigned>(n);
+}
+
+// A weight as an unsigned number of the same order; a NaN above all.
+__device__ __forceinline__ uint32_t order_key(float w) {
+  if (w != w) return 0xffffffffu;
+  const uint32_t b = __float_as_uint(w + 0.f);   // (-0 is 0)
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// Entry i of the list: whether its sequence can be shrunk, from `old` to `len`
+// keys (old <= len: nothing to do).  The whole CTA.
+__device__ bool check_entry(const EvictArgs& a, int i, int* old_out, int* len_out) {
+  const int s = a.seqs[i], len = a.new_lens[i];
+  bool ok = in_range(s, a.rows) && len >= 0;
+  const int old = ok ? a.lens[s] : 0;
+  const int64_t cap = static_cast<int64_t>(a.max_pages) << a.page_shift;
+  ok = ok && old >= 0 && old <= cap;
+  if (ok) {
+    for (int j = threadIdx.x; j < i; j += kSelectThreads) ok = ok && a.seqs[j] != s;
+    const int size = 1 << a.page_shift;
+    const int held = (old + size - 1) >> a.page_shift;
+    const int stay = len < old ? (len + size - 1) >> a.page_shift : 0;   // pages that are written
+    const int32_t* row = a.table + s * a.table_stride;
+    for (int j = threadIdx.x; j < held; j += kSelectThreads) {
+      const int pg = row[j];
+      ok = ok && in_range(pg, a.num_pages);
+      if (ok) {
+        const int refs = a.refs[pg];
+        ok = j < stay ? refs == 1 : refs > 0;
+      }
+    }
+  }
+  *old_out = old;
+  *len_out = min(len, old);
+  return __syncthreads_and(ok);
+}
+
+struct SelectShared {
+  uint32_t bins[3][kBins];
+  uint32_t warp_sum[kSelectWarps + 1];
+  uint32_t digit, left;              // the round's digit; how many are still to choose in it
+  uint32_t above[kSelectWarps], equal[kSelectWarps];
+  uint32_t cta_above, cta_equal;     // of this CTA's part, for the others
+};
+
+__device__ __forceinline__ uint32_t cluster_ld_u32(uint32_t addr) {
+  uint32_t x;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(addr) : "memory");
+  return x;
+}
+
+// CACHED: the CTA's part of the weights stays in shared memory.
+template <bool CACHED>
+__global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs a) {
+  extern __shared__ __align__(16) uint32_t cache[];
+  __shared__ SelectShared sh;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int C = a.cluster, rank = C > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int item = blockIdx.x / C, i = item / a.heads, h = item - i * a.heads;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int old, len;
+  const bool ok = check_entry(a, i, &old, &len);
+  const bool first = h == 0 && rank == 0 && threadIdx.x == 0;
+  if (first && !ok) report(a.status, kStatusPage);
+  if (first) {
+    a.old_len[i] = ok && len < old ? old : -1;
+    a.new_len[i] = len;
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
+  int32_t* slots = a.slots + static_cast<int64_t>(item) * a.width;
+  const int all = C * kSelectThreads, me = rank * kSelectThreads + static_cast<int>(threadIdx.x);
+  if (!ok || len == old) {   // (the same in all CTAs of the cluster)
+    for (int j = me; j < a.width; j += all) slots[j] = ok ? (j < old ? j : -1) : -2;
+    return;
+  }
+  const int chunks = (len + a.chunk - 1) / a.chunk;
+  int32_t* read = a.read + static_cast<int64_t>(item) * a.chunks;
+  int32_t* bound = a.bound + static_cast<int64_t>(item) * (a.chunks + 1);
+  for (int c = me; c < chunks; c += all) read[c] = 0;
+  const int r = min(a.recent, len), m = old - r;   // slots from m on stay
+  uint32_t left = static_cast<uint32_t>(len - r);  // to be chosen of the m
+  const float* w = a.weights + a.seqs[i] * a.weight_row + h * a.weight_head;
+  // this CTA's part of the slots: a multiple of 32 per warp
+  const int per_warp = (old + C * kSelectThreads - 1) / (C * kSelectThreads) * 32;
+  const int lo = rank * per_warp * kSelectWarps;
+  const int part = max(0, min(per_warp * kSelectWarps, old - lo));
+  auto key_at = [&](int j) { return CACHED ? cache[j] : order_key(w[lo + j]); };
+  for (int k = threadIdx.x; k < 3 * kBins; k += kSelectThreads) (&sh.bins[0][0])[k] = 0;
+  if constexpr (CACHED)
+    for (int j = threadIdx.x; j < part; j += kSelectThreads) cache[j] = order_key(w[lo + j]);
+  __syncthreads();
+
+  // the left-th largest key of slots [0, m): digit by digit from the top
+  const int mine = max(0, min(part, m - lo));
+  uint32_t prefix = 0;
+  if (left > 0) {
+#pragma unroll
+    for (int round = 0; round < 3; ++round) {
+      const int shift = round == 0 ? 21 : round == 1 ? 10 : 0;
+      const int bits = round == 2 ? 10 : 11, known = round == 0 ? 32 : shift + bits;
+      for (int j = threadIdx.x; j < mine; j += kSelectThreads) {
+        const uint32_t k = key_at(j);
+        if (known == 32 || (k >> known) == (prefix >> known))
+          atomicAdd(&sh.bins[round][(k >> shift) & ((1u << bits) - 1u)], 1u);
+      }
+      if (C > 1) cluster_sync();
+      else __syncthreads();
+      // thread x has the bins 2047 - 2 x and 2046 - 2 x, from the top
+      uint32_t n2[2] = {0, 0};
+      const int top = kBins - 1 - 2 * static_cast<int>(threadIdx.x);
+      for (int q = 0; q < C; ++q) {
+        if (C > 1) {
+          n2[0] += cluster_ld_u32(cluster_addr(&sh.bins[round][top], q));
+          n2[1] += cluster_ld_u32(cluster_addr(&sh.bins[round][top - 1], q));
+        } else {
+          n2[0] += sh.bins[round][top];
+          n2[1] += sh.bins[round][top - 1];
+        }
+      }
+      uint32_t inc = n2[0] + n2[1];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      if (lane == 31) sh.warp_sum[warp] = inc;
+      __syncthreads();
+      uint32_t before = 0;
+      for (int q = 0; q < warp; ++q) before += sh.warp_sum[q];
+      const uint32_t end = before + inc, start = end - n2[0] - n2[1];
+      if (start < left && left <= end) {   // one thread
+        const bool second = left > start + n2[0];
+        sh.digit = static_cast<uint32_t>(second ? top - 1 : top);
+        sh.left = left - start - (second ? n2[0] : 0u);
+      }
+      __syncthreads();
+      prefix |= sh.digit << shift;
+      left = sh.left;
+    }
+  }
+  // kept: slots from m on, keys above `prefix`, and the first `left` that equal it
+  const bool any = len > r;
+  uint32_t above = 0, equal = 0;
+  const int begin = warp * per_warp, stop = min(begin + per_warp, part);
+  for (int j0 = begin; j0 < stop; j0 += 32) {
+    const int j = j0 + lane;
+    bool up = false, same = false;
+    if (j < stop) {
+      if (lo + j >= m) {
+        up = true;
+      } else if (any) {
+        const uint32_t k = key_at(j);
+        up = k > prefix;
+        same = k == prefix;
+      }
+    }
+    above += __popc(__ballot_sync(0xffffffffu, up));
+    equal += __popc(__ballot_sync(0xffffffffu, same));
+  }
+  if (lane == 0) {
+    sh.above[warp] = above;
+    sh.equal[warp] = equal;
+  }
+  __syncthreads();
+  above = equal = 0;   // of the warps before
+  for (int q = 0; q < warp; ++q) {
+    above += sh.above[q];
+    equal += sh.equal[q];
+  }
+  if (C > 1) {
+    if (threadIdx.x == kSelectThreads - 1) {
+      sh.cta_above = above + sh.above[kSelectWarps - 1];
+      sh.cta_equal = equal + sh.equal[kSelectWarps - 1];
+    }
+    cluster_sync();
+    for (int q = 0; q < rank; ++q) {
+      above += cluster_ld_u32(cluster_addr(&sh.cta_above, q));
+      equal += cluster_ld_u32(cluster_addr(&sh.cta_equal, q));
+    }
+  }
+  for (int j0 = begin; j0 < stop; j0 += 32) {
+    const int j = j0 + lane;
+    bool up = false, same = false;
+    if (j < stop) {
+      if (lo + j >= m) {
+        up = true;
+      } else if (any) {
+        const uint32_t k = key_at(j);
+        up = k > prefix;
+        same = k == prefix;
+      }
+    }
+    const uint32_t ups = __ballot_sync(0xffffffffu, up), sames = __ballot_sync(0xffffffffu, same);
+    const uint32_t low = (1u << lane) - 1u;
+    const uint32_t e = equal + __popc(sames & low);
+    const int to = static_cast<int>(above + __popc(ups & low) + min(e, left));
+    if (j < stop) {
+      const int slot = lo + j;
+      if (up || (same && e < left)) slots[to] = slot;
+      if (slot % a.chunk == 0 && slot / a.chunk <= chunks) bound[slot / a.chunk] = to;
+    }
+    above += __popc(ups);
+    equal += __popc(sames);
+  }
+  for (int c = (old + a.chunk - 1) / a.chunk + me; c <= chunks; c += all) bound[c] = len;
+  for (int j = len + me; j < a.width; j += all) slots[j] = -1;
+  if (C > 1) cluster_sync();   // the others have read this CTA's counts
+}
+
+__device__ __forceinline__ void copy_async(uint8_t* dst, const char* src, int unit) {
+  const uint32_t d = smem_u32(dst);
+  const uint64_t s = reinterpret_cast<uint64_t>(src);
+  if (unit == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(s) : "memory");
+  else if (unit == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(s) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(s) : "memory");
+}
+
+struct MoveShared {
+  int page[2][kMaxChunk];    // of a key's old and new place
+  int row[kMaxChunk];        // in the old page
+  float weight[kMaxChunk];
+  int ticket, give_up;
+};
+
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constant__ EvictArgs a) {
+  extern __shared__ __align__(16) uint8_t buffer[];
+  __shared__ MoveShared sh;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int T = a.chunk;
+  int most = 0;
+  for (int i = threadIdx.x; i < a.n; i += kMoveThreads)
+    if (a.old_len[i] >= 0) most = max(most, (a.new_len[i] + T - 1) / T);
+  if (threadIdx.x == 0) sh.ticket = sh.give_up = 0;
+  __syncthreads();
+  atomicMax(&sh.ticket, most);
+  __syncthreads();
+  most = sh.ticket;
+  const int items = a.n * a.heads;
+  for (;;) {
+    __syncthreads();   // the chunk before is done with, sh.ticket has been read
+    if (threadIdx.x == 0) sh.ticket = atomicAdd(a.ticket, 1);
+    __syncthreads();
+    const int ticket = sh.ticket;
+    const int c = ticket / items;
+    if (c >= most) break;
+    const int item = ticket - c * items, i = item / a.heads, h = item - i * a.heads;
+    if (a.old_len[i] < 0) continue;
+    const int len = a.new_len[i], first = c * T, count = min(T, len - first);
+    if (count <= 0) continue;
+    const int32_t* slots = a.slots + static_cast<int64_t>(item) * a.width;
+    if (slots[first + count - 1] == first + count - 1) continue;   // all of it stays
+    const int seq = a.seqs[i];
+    const int32_t* table = a.table + seq * a.table_stride;
+    float* w = a.weights + seq * a.weight_row + h * a.weight_head;
+    for (int j = threadIdx.x; j < count; j += kMoveThreads) {
+      const int from = slots[first + j], to = first + j;
+      sh.page[0][j] = table[from >> a.page_shift];
+      sh.page[1][j] = table[to >> a.page_shift];
+      sh.row[j] = from & ((1 << a.page_shift) - 1);
+      sh.weight[j] = w[from];
+    }
+    __syncthreads();
+    for (int k = 0; k < a.n_pools; ++k) {
+      const RowPool& pool = a.pools[k];
+      const int per = pool.bytes / pool.unit;
+      const char* base = pool.base + h * pool.head;
+      for (int e = threadIdx.x; e < count * per; e += kMoveThreads) {
+        const int j = e / per, at = (e - j * per) * pool.unit;
+        copy_async(buffer + pool.at + j * pool.bytes + at,
+                   base + sh.page[0][j] * pool.page + sh.row[j] * pool.row + at, pool.unit);
+      }
+    }
+    copies_wait();
+    __syncthreads();
+    const int32_t* read = a.read + static_cast<int64_t>(item) * a.chunks;
+    if (threadIdx.x == 0) {
+      __threadfence();
+      atomicExch(const_cast<int32_t*>(read) + c, 1);
+    }
+    // chunks in front of this one that have rows where it writes
+    const int32_t* bound = a.bound + static_cast<int64_t>(item) * (a.chunks + 1);
+    const int from = bound[c] / T, until = min((bound[c + 1] + T - 1) / T, c);
+    for (int q = from + static_cast<int>(threadIdx.x); q < until; q += kMoveThreads) {
+      if (slots[q * T + T - 1] < first) continue;
+      const volatile int32_t* flag = read + q;
+      const uint64_t t0 = globaltimer_ns();
+      for (uint32_t it = 1; *flag == 0; ++it)
+        if ((it & 63u) == 0 && globaltimer_ns() - t0 > kTimeoutNs) {
+          report(a.status, kStatusTimeout);
+          sh.give_up = 1;
+          break;
+        }
+      __threadfence();
+    }
+    __syncthreads();
+    if (sh.give_up) break;
+    for (int k = 0; k < a.n_pools; ++k) {
+      const RowPool& pool = a.pools[k];
+      const int per = pool.bytes / pool.unit;
+      char* base = pool.base + h * pool.head;
+      for (int e = threadIdx.x; e < count * per; e += kMoveThreads) {
+        const int j = e / per, at = (e - j * per) * pool.unit;
+        char* to = base + sh.page[1][j] * pool.page +
+                   ((first + j) & ((1 << a.page_shift) - 1)) * pool.row + at;
+        const uint8_t* from_at = buffer + pool.at + j * pool.bytes + at;
+        if (pool.unit == 16) *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from_at);
+        else if (pool.unit == 8) *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(from_at);
+        else *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(from_at);
+      }
+    }
+    for (int j = threadIdx.x; j < count; j += kMoveThreads) w[first + j] = sh.weight[j];
+  }
+}
+
+// CTA (head, entry): the weights behind the new length; head 0 also the pages.
+__global__ void __launch_bounds__(kFinishThreads) finish_kernel(const EvictArgs a) {
+  grid_dep_wait();
+  grid_dep_launch();
+  for (int i = blockIdx.y; i < a.n; i += gridDim.y) {
+    const int old = a.old_len[i], len = a.new_len[i], h = blockIdx.x;
+    if (old < 0) continue;
+    const int seq = a.seqs[i];
+    float* w = a.weights + seq * a.weight_row + h * a.weight_head;
+    for (int j = len + static_cast<int>(threadIdx.x); j < old; j += kFinishThreads) w[j] = 0.f;
+    if (h > 0) continue;
+    const int size = 1 << a.page_shift;
+    int32_t* row = a.table + seq * a.table_stride;
+    const int held = (old + size - 1) >> a.page_shift;
+    for (int j = ((len + size - 1) >> a.page_shift) + static_cast<int>(threadIdx.x); j < held;
+         j += kFinishThreads) {
+      atomicSub(&a.refs[row[j]], 1);   // (checked by the first kernel)
+      row[j] = -1;
+    }
+    if (threadIdx.x == 0) a.lens[seq] = len;
+  }
+}
+
+// --------------------------------------------------------------------- host --
+
+constexpr size_t kHeader = 256;
+
+int bad(int status, const char* msg) { return record_error(status, msg); }
+
+int multiprocessors() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+    sms = 148;
+  return sms;
+}
+
+int check_evict(const attn_page_table* t, int32_t heads, int32_t n, const attn_rows* pools,
+                int32_t n_pools) {
+  if (t == nullptr) return bad(ATTN_ERR_INVALID_ARG, "page table is NULL");
+  if (t->rows < 0 || t->max_pages < 0 || t->num_pages < 0 || heads < 0 || n < 0)
+    return bad(ATTN_ERR_INVALID_ARG, "page table or list: negative size");
+  if (t->page_size < 16 || t->page_size > 32768 || (t->page_size & (t->page_size - 1)) != 0)
+    return bad(ATTN_ERR_INVALID_ARG, "page_size must be a power of two, 16 to 32768");
+  if (static_cast<int64_t>(t->max_pages) * t->page_size > (int64_t{1} << 30))
+    return bad(ATTN_ERR_UNSUPPORTED, "page table: more than 2^30 keys per row");
+  if (t->table_stride < t->max_pages)
+    return bad(ATTN_ERR_INVALID_ARG, "page table: table_stride < max_pages");
+  if ((t->rows > 0 && t->max_pages > 0 && t->table == nullptr) ||
+      (t->rows > 0 && t->lens == nullptr) || (t->num_pages > 0 && t->refs == nullptr))
+    return bad(ATTN_ERR_INVALID_ARG, "page table: NULL pointer");
+  // (a ticket counts chunks of at least one key over all heads and entries)
+  if (static_cast<int64_t>(heads) * n >= (1 << 20))
+    return bad(ATTN_ERR_UNSUPPORTED, "heads * n must stay below 2^20");
+  if (n_pools < 0 || (n_pools > 0 && pools == nullptr))
+    return bad(ATTN_ERR_INVALID_ARG, "pools: bad count or NULL");
+  if (n_pools > kMaxPools) return bad(ATTN_ERR_UNSUPPORTED, "more than 16 pools");
+  int64_t total = 0;
+  for (int i = 0; i < n_pools; ++i) {
+    const attn_rows& p = pools[i];
+    if (p.reserved != 0) return bad(ATTN_ERR_INVALID_ARG, "pools: reserved field must be 0");
+    if ((p.base == nullptr && t->num_pages > 0) || (reinterpret_cast<uintptr_t>(p.base) & 3u) != 0 ||
+        p.row_bytes <= 0 || p.row_bytes % 4 != 0 || p.page_stride % 4 != 0 ||
+        p.head_stride % 4 != 0 || p.row_stride % 4 != 0 || p.page_stride < 0 ||
+        p.head_stride < 0 || p.row_stride < p.row_bytes)
+      return bad(ATTN_ERR_INVALID_ARG,
+                 "pools: base, row_bytes and strides must be multiples of 4, rows apart");
+    total += p.row_bytes;
+  }
+  if (total > kMoveBytes) return bad(ATTN_ERR_UNSUPPORTED, "pools: more than 32768 bytes a row");
+  return ATTN_OK;
+}
+
+struct EvictLayout {
+  int chunk, chunks, buffer;
+  size_t old_len, new_len, ticket, read, bound, total;
+};
+
+EvictLayout evict_layout(const attn_page_table* t, int heads, int n, const attn_rows* pools,
+                         int n_pools) {
+  EvictLayout L{};
+  int64_t bytes = 0, units = 0;
+  for (int i = 0; i < n_pools; ++i) bytes += pools[i].row_bytes;
+  L.chunk = kMaxChunk;
+  while (L.chunk > 1 && L.chunk * bytes > kMoveBytes) L.chunk /= 2;
+  const int64_t cap = static_cast<int64_t>(t->max_pages) * t->page_size;
+  // fewer keys a chunk where that leaves SMs without one
+  units = static_cast<int64_t>(heads) * n;
+  while (L.chunk > 16 && units * ((cap + L.chunk - 1) / L.chunk) < 2 * multiprocessors()) L.chunk /= 2;
+  L.chunks = static_cast<int>((cap + L.chunk - 1) / L.chunk);
+  L.buffer = static_cast<int>(L.chunk * bytes) + 16 * n_pools;
+  size_t at = kHeader;
+  L.ticket = at;
+  L.old_len = at += 4;
+  L.new_len = at += 4 * static_cast<size_t>(n);
+  L.read = at += 4 * static_cast<size_t>(n);
+  L.bound = at += 4 * static_cast<size_t>(units) * L.chunks;
+  L.total = at + 4 * static_cast<size_t>(units) * (static_cast<size_t>(L.chunks) + 1);
+  return L;
+}
+
+// CTAs per (sequence, head) of the first kernel: as many as leave each some
+// thousands of weights, while the GPU has room for them.
+int select_cluster(int64_t cap, int64_t items) {
+  int c = 1;
+  while (c < kMaxCluster && cap > 4096ll * c && items * c * 2 <= 2 * multiprocessors()) c *= 2;
+  return c;
+}
+
+template <bool CACHED>
+cudaError_t launch_select(const EvictArgs& a, size_t bytes, cudaStream_t s) {
+  static std::atomic<uint64_t> set_up{0};
+  int dev = 0;
+  bool todo = false;
+  cudaError_t e = needs_setup(set_up, &dev, &todo);
+  if (e != cudaSuccess) return e;
+  if (todo) {
+    e = cudaFuncSetAttribute(select_kernel<CACHED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             192 * 1024);
+    if (e != cudaSuccess) return e;
+    mark_done(set_up, dev);
+  }
+  const dim3 grid(static_cast<unsigned>(a.n * a.heads * a.cluster));
+  return launch_clusters(select_kernel<CACHED>, grid, dim3(kSelectThreads), bytes, a.cluster, s, a);
+}
+
+cudaError_t launch_move(const EvictArgs& a, cudaStream_t s) {
+  static std::atomic<uint64_t> set_up{0};
+  int dev = 0;
+  bool todo = false;
+  cudaError_t e = needs_setup(set_up, &dev, &todo);
+  if (e != cudaSuccess) return e;
+  if (todo) {
+    e = cudaFuncSetAttribute(move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kMoveBytes + 16 * kMaxPools);
+    if (e != cudaSuccess) return e;
+    mark_done(set_up, dev);
+  }
+  const int64_t work = static_cast<int64_t>(a.n) * a.heads * a.chunks, room = 4ll * multiprocessors();
+  return launch_pdl(move_kernel, dim3(static_cast<unsigned>(work < room ? work : room)),
+                    dim3(kMoveThreads), a.buffer, s, a);
+}
+
+}  // namespace
+}  // namespace attn
+
+using namespace attn;
+
+extern "C" {
+
+size_t attn_pages_evict_workspace_size(const attn_page_table* t, int32_t heads, int32_t n,
+                                       const attn_rows* pools, int32_t n_pools) {
+  if (check_evict(t, heads, n, pools, n_pools) != ATTN_OK) return 0;
+  return evict_layout(t, heads, n, pools, n_pools).total;
+}
+
+attn_status attn_pages_evict(const attn_page_table* t, const attn_rows* pools, int32_t n_pools,
+                             int32_t heads, float* weights, int64_t weight_stride_row,
+                             int64_t weight_stride_head, int32_t width, const int32_t* seqs,
+                             const int32_t* new_lens, int32_t n, int32_t recent, int32_t* slots,
+                             void* ws, size_t ws_bytes, void* stream) {
+  const int st = check_evict(t, heads, n, pools, n_pools);
+  if (st != ATTN_OK) return static_cast<attn_status>(st);
+  if (recent < 0) return static_cast<attn_status>(bad(ATTN_ERR_INVALID_ARG, "recent is negative"));
+  const int64_t cap = static_cast<int64_t>(t->max_pages) * t->page_size;
+  if (width < cap || weight_stride_row < 0 || weight_stride_head < 0)
+    return static_cast<attn_status>(
+        bad(ATTN_ERR_INVALID_ARG, "weights: width below max_pages * page_size, or negative stride"));
+  const EvictLayout L = evict_layout(t, heads, n, pools, n_pools);
+  if (static_cast<int64_t>(n) * heads * L.chunks >= (int64_t{1} << 30))
+    return static_cast<attn_status>(bad(ATTN_ERR_UNSUPPORTED, "more than 2^30 chunks to move"));
+  if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+    return static_cast<attn_status>(
+        bad(ATTN_ERR_WORKSPACE, "workspace is NULL or not 256-byte aligned"));
+  if (ws_bytes < L.total)
+    return static_cast<attn_status>(bad(ATTN_ERR_WORKSPACE, "workspace too small"));
+  if (n == 0 || heads == 0) return ATTN_OK;
+  if (seqs == nullptr || new_lens == nullptr ||
+      (cap > 0 && (weights == nullptr || slots == nullptr)))
+    return static_cast<attn_status>(bad(ATTN_ERR_INVALID_ARG, "list, weights or slots is NULL"));
+  char* w = static_cast<char*>(ws);
+  auto ints = [&](size_t at) { return reinterpret_cast<int32_t*>(w + at); };
+  EvictArgs a{};
+  a.table = t->table;
+  a.table_stride = t->table_stride;
+  a.lens = t->lens;
+  a.refs = t->refs;
+  a.rows = t->rows;
+  a.max_pages = t->max_pages;
+  while ((1 << a.page_shift) < t->page_size) ++a.page_shift;
+  a.num_pages = t->num_pages;
+  a.heads = heads;
+  a.n = n;
+  a.recent = recent;
+  a.width = width;
+  a.weights = weights;
+  a.weight_row = weight_stride_row;
+  a.weight_head = weight_stride_head;
+  a.seqs = seqs;
+  a.new_lens = new_lens;
+  a.slots = slots;
+  a.old_len = ints(L.old_len);
+  a.new_len = ints(L.new_len);
+  a.ticket = ints(L.ticket);
+  a.read = ints(L.read);
+  a.bound = ints(L.bound);
+  a.chunk = L.chunk;
+  a.chunks = L.chunks;
+  a.buffer = L.buffer;
+  a.cluster = select_cluster(cap, static_cast<int64_t>(n) * heads);
+  a.n_pools = n_pools;
+  int at = 0;
+  for (int i = 0; i < n_pools; ++i) {
+    const attn_rows& p = pools[i];
+    const int64_t all = static_cast<int64_t>(reinterpret_cast<uintptr_t>(p.base)) | p.row_bytes |
+                        p.page_stride | p.head_stride | p.row_stride;
+    a.pools[i] = RowPool{static_cast<char*>(p.base), p.page_stride,
+                         p.head_stride,              p.row_stride,
+                         p.row_bytes,                all % 16 == 0 ? 16 : all % 8 == 0 ? 8 : 4,
+                         at};
+    at = (at + L.chunk * p.row_bytes + 15) / 16 * 16;
+  }
+  a.status = reinterpret_cast<int*>(ws);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // a CTA's part of the weights, if it fits
+  const int64_t part = (cap + a.cluster * kSelectThreads - 1) / (a.cluster * kSelectThreads) *
+                       kSelectThreads * 4;
+  cudaError_t e = part <= 160 * 1024 ? launch_select<true>(a, static_cast<size_t>(part), s)
+                                     : launch_select<false>(a, 0, s);
+  if (e == cudaSuccess && cap > 0) e = launch_move(a, s);
+  if (e == cudaSuccess)
+    e = launch_pdl(finish_kernel, dim3(static_cast<unsigned>(heads), static_cast<unsigned>(n < 65535 ? n : 65535)),
+                   dim3(kFinishThreads), 0, s, a);
+  if (e == cudaSuccess) return ATTN_OK;
+  char msg[256];
+  snprintf(msg, sizeof(msg), "page evict launch: %s", cudaGetErrorString(e));
+  return static_cast<attn_status>(bad(ATTN_ERR_CUDA, msg));
+}
+
+}  // extern "C"

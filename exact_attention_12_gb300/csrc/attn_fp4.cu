@@ -1,0 +1,518 @@
+// Decode step against a paged key/value cache held in 4 bits.
+//
+// What it computes: the decode step of attn_paged.cu (query row t of sequence b
+// at position len_b - n_q + t attends the cached keys j < len_b, j <= its
+// position when causal; O = softmax(c q K^T) V, L = logsumexp) on keys and values
+// K = descale_k s c, V = descale_v s c (attn_fp4.cuh).
+//
+// Bound: HBM, 9 d / 8 bytes a key (144 at d = 128, where bf16 has 512); but 2 d
+// values a key have to be unpacked meanwhile, 42 a clock and SM at the copy
+// rate, so the path from the packed bytes to the matrix unit decides:
+//   * the products are 16 x 8 x 16 warp MMAs in fp16 with the keys (and the
+//     columns of V) as the 16, and the query rows as the 8: S^T = K Q^T and
+//     O^T = V^T P^T.  Up to 8 rows no lane works on padding, and what is unpacked
+//     is the MMA's A operand as it stands: lane (g, t) = (lane / 4, lane % 4) takes
+//     the quarter row t of keys g and g + 8 (of 16 bytes at d = 128, whose scales
+//     are its own), since the sum over d may go in any order;
+//   * two values a conversion (cvt.f16x2.e2m1x2; measured 50 a clock and SM,
+//     shifts and masks 30), one multiplication by the scale, both exact;
+//   * V^T wants two keys in a register: the codes of two keys are interleaved
+//     before they are converted, two operations per four pairs;
+//   * P^T comes from S^T by movmatrix, without shared memory.
+// Q enters as fp16, scaled by a power of two per row so that its largest element
+// is in [2^14, 2^15): exact for elements down to 2^-31 of that one.  P is
+// rounded to fp16 (a relative 2^-11, of p below 2^-14 an absolute 2^-25), the row
+// sums are of the unrounded fp32 values, S, m, l, O are fp32.
+//
+// The keys of all sequences are divided evenly over the CTAs (attn_paged.cuh).
+// A slot (MT warps, 16 rows each; one warp up to 16 rows) streams its own 32-key
+// tiles by 16-byte asynchronous copies through its own ring; what is no page
+// is filled with zeros.  Value rows past the end of a sequence may hold
+// anything: their scores are replaced, their values' scales are taken as zero.
+#include <type_traits>
+
+#include "attn_fp4.cuh"
+
+namespace attn {
+using namespace sm103;
+
+namespace {
+
+template <int D, int NT, int MT>
+struct Fp4Cfg {
+  static constexpr int kWarps = NT == 1 ? 8 : 6;
+  static constexpr int kW = MT == 4 ? 8 : kWarps;
+  static constexpr int kSlots = kW / MT;
+  static constexpr int kThreads = 32 * kW;
+  static constexpr int kRows = 8 * NT * MT;                  // of a CTA
+  static constexpr int kCodeBytes = kFp4Keys * D / 2;        // of a tile's keys (or values)
+  static constexpr int kScaleBytes = kFp4Keys * D / kFp4Block;
+  static constexpr int kTileBytes = 2 * (kCodeBytes + kScaleBytes);
+  static constexpr int kCtasPerSm = MT == 4 ? 1 : 2;
+  // O of all slots goes through shared memory, 16 columns of eight at a time
+  static constexpr int kRedStride = D + 4;
+  static constexpr int kRedBytes = kRows * kRedStride * 4;   // of a slot
+  static constexpr int kStages = MT == 4 ? 1024 / D : (D == 128 ? 3 : 6) - (NT == 1 ? 1 : 0);
+  static constexpr int kRingBytes = kSlots * kStages * kTileBytes;
+  static constexpr int kSmem = kRingBytes + 2 * kRedBytes;
+  static_assert(kCtasPerSm * (kSmem + 1024 + 2560) <= 228 * 1024, "shared memory of an SM");
+};
+
+template <int D, int NT, int MT>
+struct Fp4Shared {
+  float m[Fp4Cfg<D, NT, MT>::kSlots][Fp4Cfg<D, NT, MT>::kRows];   // largest score, log2 units
+  float l[Fp4Cfg<D, NT, MT>::kSlots][Fp4Cfg<D, NT, MT>::kRows];
+};
+
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void copies_wait_but() {   // all groups but the last N have landed
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {   // an 8 x 8 matrix of 16 bits
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// Eight bytes of shared memory (four at d = 64).
+template <int D>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
+  if constexpr (D == 128) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    w[0] = x.x;
+    w[1] = x.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
+
+template <int D, int NT, int MT>
+__global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>::kCtasPerSm)
+    fp4_decode_kernel(const PagedArgs a, const Fp4Args f) {
+  using C = Fp4Cfg<D, NT, MT>;
+  constexpr int ST = C::kStages, KT = kFp4Keys, kSlots = C::kSlots;
+  constexpr int kSteps = D / 16;            // MMA steps along d, and 16-column groups of V
+  constexpr int kKeyWords = D / 32;         // 32-bit words of a lane's quarter key row
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Fp4Shared<D, NT, MT> sh;
+  float* red = reinterpret_cast<float*>(smem + C::kRingBytes);   // [2][kRows][kRedStride]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int slot = warp / MT, mt = warp % MT;
+  const int g = lane >> 2, t = lane & 3;
+  uint8_t* ring = smem + slot * ST * C::kTileBytes;
+  grid_dep_wait();
+  grid_dep_launch();
+  const PagedShare share =
+      paged_share<KT, kFp4Overhead, kFp4MinUnits>(a, blockIdx.x, gridDim.x);
+  MergeNote note{-1, 0, 0, 0};
+  const bool small_pages = a.page_shift < 5;   // 16 keys: a tile lies in two
+
+  // ---- the copies: tile u of this slot is tile t0 + slot + kSlots u of the
+  // piece; lane l holds the pages of tile 32 * (batch) + l
+  int page_of[2] = {0, 0};
+  auto slot_tiles = [&](const PagedPiece& p) {
+    const int n = p.t1 - p.t0 - slot;
+    return n > 0 ? (n + kSlots - 1) / kSlots : 0;
+  };
+  auto load_pages = [&](const PagedPiece& p, int u0, int nu) {
+    const int u = u0 + lane;
+    if (u < nu) {
+      const int key = (p.t0 + slot + kSlots * u) * KT;
+      const int32_t* row = a.table + p.b * a.table_stride;
+      page_of[0] = checked_page(row[key >> a.page_shift], a.num_pages, a.status);
+      page_of[1] = !small_pages || key + 16 >= p.len
+                       ? page_of[0]
+                       : checked_page(row[(key >> a.page_shift) + 1], a.num_pages, a.status);
+    }
+  };
+  auto issue = [&](const PagedPiece& p, int u) {
+    const int pg0 = __shfl_sync(0xffffffffu, page_of[0], u & 31);
+    const int pg1 = __shfl_sync(0xffffffffu, page_of[1], u & 31);
+    uint8_t* to = ring + u % ST * C::kTileBytes;
+    const int row = small_pages ? 0 : (p.t0 + slot + kSlots * u) * KT & ((1 << a.page_shift) - 1);
+    const int64_t head = p.h / a.blocks;
+    const int me = mt * 32 + lane;
+    // `bytes` of the tile's rows, half of them in each of two small pages
+    auto copy = [&](uint8_t* dst, const uint8_t* src, int64_t page_step, int64_t head_step,
+                    int row_bytes, int bytes) {
+      const uint8_t* base = src + head * head_step + row * row_bytes;
+#pragma unroll
+      for (int c = me * 16; c < bytes; c += MT * 512) {
+        const bool second = small_pages && c >= bytes / 2;
+        const int page = second ? pg1 : pg0;
+        const bool there = page < a.num_pages;
+        copy16_async(dst + c,
+                     there ? base + page * page_step + (second ? c - bytes / 2 : c) : src, there);
+      }
+    };
+    copy(to, f.k.codes, f.k.code_page, f.k.code_head, D / 2, C::kCodeBytes);
+    copy(to + C::kCodeBytes, f.v.codes, f.v.code_page, f.v.code_head, D / 2, C::kCodeBytes);
+    copy(to + 2 * C::kCodeBytes, f.k.scales, f.k.scale_page, f.k.scale_head, D / kFp4Block,
+         C::kScaleBytes);
+    copy(to + 2 * C::kCodeBytes + C::kScaleBytes, f.v.scales, f.v.scale_page, f.v.scale_head,
+         D / kFp4Block, C::kScaleBytes);
+  };
+  // every warp of the slot: its copies of the tile have landed, and it is done
+  // with the tile before
+  auto slot_sync = [&] {
+    if constexpr (MT == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(slot + 1), "n"(32 * MT) : "memory");
+  };
+
+  PagedPiece p = paged_piece<KT, kFp4Overhead>(a, share, share.b, 0, share.s);
+  while (p.valid) {   // (the same pieces in every warp)
+    const int nu = slot_tiles(p);
+    slot_sync();      // the ring is free
+    if (nu > 0) load_pages(p, 0, nu);
+    for (int u = 0; u < ST - 1; ++u) {
+      if (u < nu) issue(p, u);
+      copies_commit();
+    }
+    // Q^T fragments: row r = 8 n + g, columns of quarter t, as fp16 times 2^e
+    const int row0 = segment_row(a, p.h), nrows = segment_rows(a, p.h);
+    uint32_t qb[NT][kSteps][2];
+    float c2[NT][2];                // what turns a score into log2 units, rows 2t, 2t + 1
+    int lim[NT][2];                 // keys below lim are allowed
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int r = (mt * NT + n) * 8 + g;
+      const bool live = r < nrows;
+      const int h = (row0 + r) / a.n_q, qt = row0 + r - h * a.n_q;
+      const uint4* qr = reinterpret_cast<const uint4*>(
+          a.q + p.b * a.stride_b + h * a.stride_h + static_cast<int64_t>(qt) * a.stride_n +
+          t * (D / 4));
+      uint32_t w[D / 8];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const uint4 x = live ? qr[i] : make_uint4(0u, 0u, 0u, 0u);
+        w[4 * i] = x.x;
+        w[4 * i + 1] = x.y;
+        w[4 * i + 2] = x.z;
+        w[4 * i + 3] = x.w;
+      }
+      int e;
+      half_rows<D / 8>(w, &e);
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        qb[n][i][0] = w[2 * i];
+        qb[n][i][1] = w[2 * i + 1];
+      }
+      const float c = score_factor(a.scale_log2 * f.k_descale, e);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        c2[n][i] = __shfl_sync(0xffffffffu, c, 4 * (2 * t + i));
+        const int rr = (mt * NT + n) * 8 + 2 * t + i;
+        const int at = (row0 + rr) % a.n_q;
+        lim[n][i] = rr >= nrows ? 0 : (a.causal ? min(p.len, p.len - a.n_q + at + 1) : p.len);
+      }
+    }
+    const int open = a.causal ? p.len - a.n_q + 1 : p.len;   // every row is allowed keys below it
+    float m[NT][2], l[NT][2];
+    float o[kSteps][NT][4];         // columns (D / 8) g + 2 i, + 1; rows 2t, 2t + 1
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        m[n][i] = -INFINITY;
+        l[n][i] = 0.f;
+      }
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
+
+    for (int u = 0; u < nu; ++u) {
+      copies_wait_but<ST - 2>();
+      slot_sync();
+      if (u + ST - 1 < nu) {   // into the stage that the tile before this one has left
+        if (((u + ST - 1) & 31) == 0) load_pages(p, u + ST - 1, nu);
+        issue(p, u + ST - 1);
+      }
+      copies_commit();
+      const uint8_t* kc = ring + u % ST * C::kTileBytes;
+      const uint8_t* vc = kc + C::kCodeBytes;
+      const uint8_t* ks = kc + 2 * C::kCodeBytes;
+      const uint8_t* vs = ks + C::kScaleBytes;
+      const int k0 = (p.t0 + slot + kSlots * u) * KT;
+
+      // S^T: row m of 16 keys is key m / 2 % 4 + 4 (m % 2) + 8 (m / 8), so that V's
+      // pairs below are keys t, t + 4 and t + 8, t + 12
+      float sc[2][NT][4];
+      const int kg = (g >> 1) + 4 * (g & 1);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          sc[half][n][0] = sc[half][n][1] = sc[half][n][2] = sc[half][n][3] = 0.f;
+        uint32_t w[2][kKeyWords], unit[2][D / 64];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int key = 16 * half + kg + 8 * i;
+          if constexpr (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(kc + key * 64 + 16 * t);
+            w[i][0] = x.x;
+            w[i][1] = x.y;
+            w[i][2] = x.z;
+            w[i][3] = x.w;
+            const uint32_t s = e4m3_to_half(
+                *reinterpret_cast<const uint16_t*>(ks + key * 8 + 2 * t));
+            unit[i][0] = __byte_perm(s, 0, 0x1010);
+            unit[i][1] = __byte_perm(s, 0, 0x3232);
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(kc + key * 32 + 8 * t);
+            w[i][0] = x.x;
+            w[i][1] = x.y;
+            unit[i][0] = e4m3_to_half(ks[key * 4 + t] * 0x0101u);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kKeyWords; ++j) {
+          uint32_t x[2][4];
+          e2m1_to_half(w[0][j], x[0]);
+          e2m1_to_half(w[1][j], x[1]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {   // two steps of 16 columns a word
+            const uint32_t ka[4] = {mul_half2(x[0][2 * i], unit[0][j / 2]),
+                                    mul_half2(x[1][2 * i], unit[1][j / 2]),
+                                    mul_half2(x[0][2 * i + 1], unit[0][j / 2]),
+                                    mul_half2(x[1][2 * i + 1], unit[1][j / 2])};
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              mma16816_half(sc[half][n], ka, qb[n][2 * j + i][0], qb[n][2 * j + i][1]);
+          }
+        }
+      }
+      if (k0 + KT > open) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (k0 + 16 * half + kg + 8 * (e >> 1) >= lim[n][e & 1]) sc[half][n][e] = -INFINITY;
+      }
+      // the running maximum (of a row: over the lanes of equal t)
+      float alpha[NT][2], base[NT][2];
+      bool moved = false;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float top = fmaxf(fmaxf(sc[0][n][i], sc[0][n][2 + i]), fmaxf(sc[1][n][i], sc[1][n][2 + i]));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          const float mn = fmaxf(m[n][i], top * c2[n][i]);
+          base[n][i] = mn == -INFINITY ? 0.f : mn;   // -inf: no allowed key seen yet
+          alpha[n][i] = m[n][i] == -INFINITY ? 0.f : ex2_approx(m[n][i] - base[n][i]);
+          m[n][i] = mn;
+          moved = moved || alpha[n][i] != 1.f;
+        }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            l[n][i] *= alpha[n][i];
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+              o[k][n][i] *= alpha[n][i];
+              o[k][n][2 + i] *= alpha[n][i];
+            }
+          }
+      }
+      // P^T = 2^(S c - m c) as fp16 B fragments; row sums from the same fp32 values
+      uint32_t pb[2][NT][2];
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float p0 = ex2_approx(fmaf(sc[half][n][2 * i], c2[n][0], -base[n][0]));
+            const float p1 = ex2_approx(fmaf(sc[half][n][2 * i + 1], c2[n][1], -base[n][1]));
+            l[n][0] += p0;
+            l[n][1] += p1;
+            pb[half][n][i] = transpose8(pack_half2(p0, p1));
+          }
+      // O^T += V^T P^T: lane g has columns (D / 8) g ...; MMA row g is column 2 i, row
+      // g + 8 column 2 i + 1 of them
+      const bool last = k0 + KT > p.len;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t w[4][D / 64], s[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int key = 16 * half + t + 4 * j;
+          load_words<D>(vc + key * (D / 2) + (D / 16) * g, w[j]);
+          s[j] = vs[key * (D / kFp4Block) + (D == 128 ? g : g >> 1)];
+          if (last && k0 + key >= p.len) s[j] = 0;
+        }
+        const uint32_t unit[2] = {e4m3_to_half(s[0] | s[1] << 8), e4m3_to_half(s[2] | s[3] << 8)};
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {
+          uint32_t x[2][2][4];   // [pair of keys][column 2 i or 2 i + 1][i]
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t w0 = w[2 * k][j], w1 = w[2 * k + 1][j];
+            e2m1_to_half((w0 & 0x0f0f0f0fu) | ((w1 << 4) & 0xf0f0f0f0u), x[k][0]);
+            e2m1_to_half(((w0 >> 4) & 0x0f0f0f0fu) | (w1 & 0xf0f0f0f0u), x[k][1]);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t va[4] = {mul_half2(x[0][0][i], unit[0]), mul_half2(x[0][1][i], unit[0]),
+                                    mul_half2(x[1][0][i], unit[1]), mul_half2(x[1][1][i], unit[1])};
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              mma16816_half(o[4 * j + i][n], va, pb[half][n][0], pb[half][n][1]);
+          }
+        }
+      }
+    }
+    copies_wait_but<0>();
+
+    // ---- the slots' states merged: m, l per row, then O through shared memory
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], 4);
+        l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], 8);
+        l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], 16);
+        if (l[n][i] != l[n][i]) m[n][i] = 0.f;   // a row of NaN scores has seen keys
+        if (g == 0) {
+          sh.m[slot][(mt * NT + n) * 8 + 2 * t + i] = m[n][i];
+          sh.l[slot][(mt * NT + n) * 8 + 2 * t + i] = l[n][i];
+        }
+      }
+    __syncthreads();
+    auto total = [&](int r, float* top) {
+      float mx = -INFINITY, lt = 0.f;
+#pragma unroll
+      for (int w = 0; w < kSlots; ++w) mx = fmaxf(mx, sh.m[w][r]);
+#pragma unroll
+      for (int w = 0; w < kSlots; ++w) {
+        const float mw = sh.m[w][r];
+        if (mw != -INFINITY) lt += sh.l[w][r] * ex2_approx(mw - mx);
+      }
+      *top = mx;
+      return lt;
+    };
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float mx;
+        const float lt = total((mt * NT + n) * 8 + 2 * t + i, &mx);
+        // this slot's weight, with descale / l folded in
+        const float w = m[n][i] == -INFINITY ? 0.f : ex2_approx(m[n][i] - mx) * (f.v_descale / lt);
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+          o[k][n][i] *= w;
+          o[k][n][2 + i] *= w;
+        }
+      }
+    const bool whole = p.whole();
+    if (p.t0 == 0 && !whole) note = paged_note<kFp4Overhead>(share, p);
+    if (a.by_segment && p.t0 == 0 && threadIdx.x == 0)
+      a.notes[p.b * a.heads + p.h] = whole ? MergeNote{p.b, p.h, 0, -1} : note;
+    const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (p.s < share.lo ? 0 : 1);
+    // slots 0, 1 write, 2, 3 add, ...: the sum has a fixed order.  Column (D / 8) g +
+    // 2 i + b of a row lies at 16 i + 2 g + b
+    for (int w = 0; w < kSlots; w += 2) {
+      if (slot == w || slot == w + 1) {
+        float* to = red + (slot - w) * C::kRows * C::kRedStride;
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float2* at = reinterpret_cast<float2*>(
+                  to + ((mt * NT + n) * 8 + 2 * t + i) * C::kRedStride + 16 * k + 2 * g);
+              float2 x = make_float2(o[k][n][i], o[k][n][2 + i]);
+              if (w > 0) {
+                const float2 y = *at;
+                x.x += y.x;
+                x.y += y.y;
+              }
+              *at = x;
+            }
+      }
+      __syncthreads();
+    }
+    for (int e = threadIdx.x; e < nrows * (D / 4); e += C::kThreads) {
+      const int r = e / (D / 4), c = 4 * (e - r * (D / 4));
+      const int gg = c / (D / 8), k = c % (D / 8) / 2;
+      float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < (kSlots > 1 ? 2 : 1); ++w) {
+        const float* from = red + (w * C::kRows + r) * C::kRedStride + 2 * gg;
+        const float2 y = *reinterpret_cast<const float2*>(from + 16 * k);
+        const float2 z = *reinterpret_cast<const float2*>(from + 16 * k + 16);
+        x[0] += y.x;
+        x[1] += y.y;
+        x[2] += z.x;
+        x[3] += z.y;
+      }
+      float mx, L = 0.f;
+      if (c == 0) {
+        const float lt = total(r, &mx);
+        L = lt == 0.f ? -INFINITY : fmaf(mx, 0.69314718f, logf(lt));
+      }
+      if (whole) {
+        const int h = (row0 + r) / a.n_q, qt = row0 + r - h * a.n_q;
+        *reinterpret_cast<uint2*>(a.o + p.b * a.stride_b + h * a.stride_h +
+                                  static_cast<int64_t>(qt) * a.stride_n + c) =
+            make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+        if (c == 0) a.lse[static_cast<int64_t>(p.b) * a.all_rows + row0 + r] = L;
+      } else {
+        *reinterpret_cast<float4*>(a.part_o + (part * a.rows + r) * D + c) =
+            make_float4(x[0], x[1], x[2], x[3]);
+        if (c == 0) a.part_l[part * a.rows + r] = L;
+      }
+    }
+    __syncthreads();   // red, m and l are free
+    p = paged_next<KT, kFp4Overhead>(a, share, p);
+  }
+  if (!a.by_segment && threadIdx.x == 0) a.notes[blockIdx.x] = note;
+}
+
+template <int D, int NT, int MT>
+cudaError_t launch_rows(const PagedArgs& a, const Fp4Args& f, int ctas, cudaStream_t s) {
+  using C = Fp4Cfg<D, NT, MT>;
+  static std::atomic<uint64_t> set_up{0};
+  int dev = 0;
+  bool todo = false;
+  cudaError_t e = needs_setup(set_up, &dev, &todo);
+  if (e != cudaSuccess) return e;
+  if (todo) {
+    e = cudaFuncSetAttribute(fp4_decode_kernel<D, NT, MT>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    mark_done(set_up, dev);
+  }
+  return launch_pdl(fp4_decode_kernel<D, NT, MT>, dim3(ctas), dim3(C::kThreads), C::kSmem, s, a, f);
+}
+
+template <int D>
+cudaError_t launch_width(const PagedArgs& a, const Fp4Args& f, int ctas, cudaStream_t s) {
+  if (a.rows <= 8) return launch_rows<D, 1, 1>(a, f, ctas, s);
+  if (a.rows <= 16) return launch_rows<D, 2, 1>(a, f, ctas, s);
+  if (a.rows <= 32) return launch_rows<D, 2, 2>(a, f, ctas, s);
+  return launch_rows<D, 2, 4>(a, f, ctas, s);
+}
+
+}  // namespace
+
+cudaError_t launch_fp4_decode(const PagedArgs& a, const Fp4Args& f, int ctas, cudaStream_t s) {
+  return a.d == 64 ? launch_width<64>(a, f, ctas, s) : launch_width<128>(a, f, ctas, s);
+}
+
+}  // namespace attn

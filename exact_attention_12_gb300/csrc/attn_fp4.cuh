@@ -1,0 +1,150 @@
+// Caches in 4 bits: the format, its conversions, and the argument blocks of the
+// kernels that store, load and read them (attn_fp4.cu, attn_fp4_store.cu,
+// attn_weights.cu).
+//
+// A value is x = descale * s * c: c one of 0, 0.5, 1, 1.5, 2, 3, 4, 6 with a sign
+// (E2M1: two exponent bits, one of mantissa), s an E4M3 number that 16
+// consecutive columns share, descale one fp32 factor of the tensor.  s * c has
+// 4 + 2 significant bits and lies between 2^-10 and 2688: it is exact in fp16
+// (and bf16), so the products of attention take the cache's values as they
+// are, and descale is folded into the score scale and into O.
+#pragma once
+#include <cuda_fp16.h>
+
+#include "attn_paged.cuh"
+
+namespace attn {
+
+constexpr int kFp4Block = 16;   // columns that share a scale
+
+// One tensor of the cache: a head's rows of a page follow one another.
+struct Fp4Cache {
+  uint8_t* codes;                  // [num_pages][H_kv][page_size][d / 2]
+  uint8_t* scales;                 // [num_pages][H_kv][page_size][d / 16]
+  int64_t code_page, code_head;    // bytes between pages, between heads
+  int64_t scale_page, scale_head;
+};
+
+struct Fp4Args {
+  Fp4Cache k, v;
+  float k_descale, v_descale;
+};
+
+// Storing the newest tokens of each sequence, and loading them back.
+struct Fp4CopyArgs {
+  int B, H, n, d;
+  const int32_t* lens;             // [B] cache lengths
+  const int32_t* counts;           // [B] tokens of each sequence among the n; null: n
+  const int32_t* table;
+  int64_t table_stride;
+  int cap, page_shift, num_pages;
+  __nv_bfloat16 *k, *v;            // [B][H][n][d]
+  int64_t stride_b, stride_h, stride_n;
+  Fp4Args cache;
+  int* status;
+};
+
+// The attention weight of each key (attn_weights.cu).
+struct WeightArgs {
+  const __nv_bfloat16* k;          // null: the cache in 4 bits
+  int64_t stride_page, stride_head, stride_row;
+  Fp4Cache cache;
+  float k_descale;
+  const float* lse;                // [B][H][n_q]
+  float* weights;
+  int64_t stride_b, stride_h;      // of the weights
+  int add;
+  int pass_rows;                   // query rows of a pass, set by the launcher
+};
+cudaError_t launch_key_weights(const PagedArgs& a, WeightArgs f, int ctas, cudaStream_t s);
+
+constexpr int kWeightKeys = 32;
+constexpr int kWeightOverhead = 8;
+constexpr int kWeightMinUnits = 16;
+
+constexpr float kLog2Of = 1.4426950408889634f;   // log2(e)
+
+cudaError_t launch_fp4_store(const Fp4CopyArgs& a, cudaStream_t s);
+cudaError_t launch_fp4_load(const Fp4CopyArgs& a, cudaStream_t s);
+cudaError_t launch_fp4_decode(const PagedArgs& a, const Fp4Args& f, int ctas, cudaStream_t s);
+
+// Decode: key tiles of 32, the split's constants in such tiles.
+constexpr int kFp4Keys = 32;
+constexpr int kFp4Overhead = 8;
+constexpr int kFp4MinUnits = 6;
+
+// ------------------------------------------------------------- conversions --
+
+// Four bytes of codes: r[i] the two values of byte i (the low four bits first) as
+// fp16.
+__device__ __forceinline__ void e2m1_to_half(uint32_t w, uint32_t* r) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w));
+}
+
+// Two E4M3 numbers (the low byte first) as fp16.
+__device__ __forceinline__ uint32_t e4m3_to_half(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %1;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t}"
+      : "=r"(r)
+      : "r"(w));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// c += a b, 16 x 8 x 16, fp16 inputs, fp32 accumulators
+__device__ __forceinline__ void mma16816_half(float* c, const uint32_t* a, uint32_t b0,
+                                              uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// A row of Q, W words of bf16 pairs in each of the four lanes of equal lane / 4,
+// as fp16 pairs times 2^e, with the row's largest element in [2^14, 2^15)
+// (an infinite row: as it is).
+template <int W>
+__device__ __forceinline__ void half_rows(uint32_t* w, int* e) {
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < W; ++i)
+    top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[i] << 16)),
+                           fabsf(__uint_as_float(w[i] & 0xffff0000u))));
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  const int ef = static_cast<int>(__float_as_uint(top) >> 23);
+  *e = ef == 255 ? 0 : min(141 - ef, 127);
+  const float up = ldexpf(1.f, *e);
+#pragma unroll
+  for (int i = 0; i < W; ++i)
+    w[i] = pack_half2(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);
+}
+
+// What turns a product with such a row into log2 units: `factor` 2^-e, never 0 or
+// infinite (a masked score stays -inf, a score of 0 stays 0).
+__device__ __forceinline__ float score_factor(float factor, int e) {
+  return fminf(fmaxf(ldexpf(factor, -e), 1.2e-38f), 3.0e38f);
+}
+
+}  // namespace attn

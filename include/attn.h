@@ -321,6 +321,79 @@ attn_status attn_decode_latent(const attn_params* p, int32_t n_q, const attn_pag
                                const void* q, const void* c, void* o, float* lse, void* ws,
                                size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Paged caches in 4 bits.  Every 16 columns of a key (or value) share a scale:
+ *   x = descale * s * c,
+ * c in {0, 0.5, 1, 1.5, 2, 3, 4, 6} with a sign (E2M1; a byte holds two, the
+ * column of even index in its low four bits), s an E4M3 number (the OCP 8-bit
+ * format, as in attn_fwd), descale one factor of the tensor.  9 d / 16 bytes a
+ * key where bf16 has 2 d.  Codes and scales are two buffers of pages: codes
+ * [num_pages][H_kv][page_size][d / 2], scales [num_pages][H_kv][page_size][d / 16];
+ * a head's rows of a page follow one another without gaps, pages and heads may
+ * be apart.  attn_pages_copy, _fork, _compact and _evict take them as pools.
+ * (The pages about attention have no counterpart.) */
+typedef struct attn_fp4 {
+  void* codes;               /* 16-byte aligned, as is scales */
+  void* scales;
+  int64_t code_page, code_head;    /* bytes between pages and between heads, */
+  int64_t scale_page, scale_head;  /* multiples of 16 */
+  float descale;             /* 2^-100 to 2^100 */
+  int32_t reserved;          /* must be 0 */
+} attn_fp4;
+
+/* Stores new keys and values: token t of sequence b, t < counts[b], becomes the
+ * cached key (and value) at position key_lens[b] - counts[b] + t, that is, the
+ * cache has grown already (attn_pages_extend) and these are its newest tokens.
+ *   p->B, p->H_kv, p->d (64 or 128);  p->N = n, the tokens k and v have room for;
+ *   p->key_lens  the cache lengths, clamped to [0, max_pages * page_size]
+ *   counts       device [B], clamped to [0, n]; NULL: n for every sequence
+ *   k, v         [B, H_kv, n, d] bf16 with the kv strides
+ * s is the E4M3 number nearest to max |x| / (6 descale) of its columns (at most
+ * 448), c the nearest to x / (s descale) (at most 6), ties to the even code.  A
+ * NaN makes its 16 columns NaN; infinities become the largest value.
+ * Tokens whose position is negative are left out; an entry of the table outside
+ * the cache is recorded (ATTN_ERR_PAGE) and its tokens are left out.  Fields of
+ * p that are not named are ignored; H_kv * n < 2^31 / 8.  ws: 256 bytes. */
+attn_status attn_pages_store_fp4(const attn_params* p, const attn_pages* pages,
+                                 const int32_t* counts, const void* k, const void* v,
+                                 const attn_fp4* k_cache, const attn_fp4* v_cache, void* ws,
+                                 size_t ws_bytes, void* stream);
+
+/* The way back: k and v [B, H_kv, n, d] receive, as bf16, what the cache holds of
+ * the tokens that attn_pages_store_fp4 would store; zeros where there is none. */
+attn_status attn_pages_load_fp4(const attn_params* p, const attn_pages* pages,
+                                const int32_t* counts, const attn_fp4* k_cache,
+                                const attn_fp4* v_cache, void* k, void* v, void* ws,
+                                size_t ws_bytes, void* stream);
+
+/* attn_decode_paged on such a cache (the kv strides of p are ignored, shared_len
+ * must be 0): what it says of rows, masks, lengths and of values that are not
+ * attended holds here.  Q and P enter the products in fp16, Q scaled by a power
+ * of two per row; keys and values as they are.  S, L and O in fp32, O rounded
+ * to bf16. */
+size_t attn_decode_fp4_workspace_size(const attn_params* p, int32_t n_q, const attn_pages* pages);
+attn_status attn_decode_fp4(const attn_params* p, int32_t n_q, const attn_pages* pages,
+                            const void* q, const attn_fp4* k, const attn_fp4* v, void* o,
+                            float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* The attention weight that query rows give each cached key:
+ *   W[b, h, j] = sum over the query heads of key/value head h and the n_q rows of
+ *                exp(scale q k_j - lse)   over the rows that attend key j,
+ * added to weights[b, h, j] (add != 0) or written there, for j < key_lens[b];
+ * further entries stay as they are.  Rows, masks and positions as in
+ * attn_decode_paged, whose lse [B, H, n_q] this takes; a row with lse = -inf gives
+ * nothing.  Summed in fp32 in an order that does not depend on timing.
+ *   k         [num_pages, H_kv, page_size, d] bf16 with the kv strides, or NULL and
+ *   k_cache   a cache in 4 bits (then NULL otherwise)
+ *   weights   fp32, weight_stride_b and weight_stride_h entries between sequences
+ *             and heads, max_pages * page_size entries of a head at least
+ * ws: 256 bytes. */
+attn_status attn_key_weights(const attn_params* p, int32_t n_q, const attn_pages* pages,
+                             const void* q, const void* k, const attn_fp4* k_cache,
+                             const float* lse, float* weights, int64_t weight_stride_b,
+                             int64_t weight_stride_h, int32_t add, void* ws, size_t ws_bytes,
+                             void* stream);
+
 /* Upkeep of a paged cache, on the device: no call synchronises or reads
  * anything back.  The state is a table of pages, a length per sequence (row)
  * and a reference count per page; a page with count 0 is free.  A row holds
@@ -386,6 +459,41 @@ attn_status attn_pages_free(const attn_page_table* t, const int32_t* seqs, int32
  * becomes -1 and is recorded, one outside the cache stays as it is). */
 attn_status attn_pages_compact(const attn_page_table* t, const attn_pool* pools, int32_t n_pools,
                                int32_t* moved, void* ws, size_t ws_bytes, void* stream);
+
+/* A buffer of pages by its rows: row r of head h in page g is row_bytes bytes at
+ * base + g * page_stride + h * head_stride + r * row_stride (bytes).  Everything a
+ * multiple of 4; rows apart. */
+typedef struct attn_rows {
+  void* base;
+  int64_t page_stride, head_stride, row_stride;
+  int32_t row_bytes, reserved;     /* reserved must be 0 */
+} attn_rows;
+
+/* Eviction by gathered attention weight: sequence seqs[i] shrinks to new_lens[i]
+ * keys, every head by its own weights.  A head keeps its last
+ * min(recent, new_lens[i]) keys and, of those before them, the ones with the
+ * largest weights (of equal ones those in front; NaN counts as the largest); they keep
+ * their order and move to the front, in every pool.  The weights move along, those
+ * behind the new length become 0.  Pages that are no longer needed are given
+ * back as in attn_pages_free.  A sequence that is not longer than new_lens[i] stays
+ * as it is.
+ *   weights    fp32 [rows][heads][width], weight_stride_row and weight_stride_head
+ *              entries apart, width >= max_pages * page_size
+ *   slots      device int32 [n][heads][width], output: slots[i][h][j] is where the
+ *              key that is now in place j was before; -1 from the new length on,
+ *              -2 throughout where a sequence was refused
+ * Refused and recorded (ATTN_ERR_PAGE): a sequence outside the table, or named
+ * before in the list; a negative new length; a length or page outside the cache, a
+ * page that is free; a page that would be written to but is shared with another
+ * sequence (of a fork; pages_copy to pages of its own first).  Pages behind the new
+ * length may be shared.  All pools together at most 32768 bytes a row, 16 pools. */
+size_t attn_pages_evict_workspace_size(const attn_page_table* t, int32_t heads, int32_t n,
+                                       const attn_rows* pools, int32_t n_pools);
+attn_status attn_pages_evict(const attn_page_table* t, const attn_rows* pools, int32_t n_pools,
+                             int32_t heads, float* weights, int64_t weight_stride_row,
+                             int64_t weight_stride_head, int32_t width, const int32_t* seqs,
+                             const int32_t* new_lens, int32_t n, int32_t recent, int32_t* slots,
+                             void* ws, size_t ws_bytes, void* stream);
 
 /* Diagnostic: runs the kernels' time-out path on purpose.  Enqueues one warp
  * that waits on a barrier nothing arrives at, giving up after `limit_ns`
