@@ -38,23 +38,26 @@ using namespace sm103;
 
 namespace {
 
+constexpr float kLazy = 8.f;
+
+// NT: blocks of 8 query rows per warp; MT: warps that share a tile.
 template <int D, int NT, int MT>
 struct Fp4Cfg {
-  static constexpr int kWarps = NT == 1 ? 8 : 6;
-  static constexpr int kW = MT == 4 ? 8 : kWarps;
-  static constexpr int kSlots = kW / MT;
-  static constexpr int kThreads = 32 * kW;
+  static constexpr int kWarps = NT == 2 ? 6 : 8;
+  static constexpr int kSlots = kWarps / MT;
+  static constexpr int kThreads = 32 * kWarps;
   static constexpr int kRows = 8 * NT * MT;                  // of a CTA
+  static constexpr bool kSharedQ = NT == 4;                  // Q's fragments in shared memory
   static constexpr int kCodeBytes = kFp4Keys * D / 2;        // of a tile's keys (or values)
   static constexpr int kScaleBytes = kFp4Keys * D / kFp4Block;
   static constexpr int kTileBytes = 2 * (kCodeBytes + kScaleBytes);
-  static constexpr int kCtasPerSm = MT == 4 ? 1 : 2;
-  // O of all slots goes through shared memory, 16 columns of eight at a time
-  static constexpr int kRedStride = D + 4;
+  static constexpr int kCtasPerSm = NT == 4 ? 1 : 2;
+  static constexpr int kRedStride = D + 4;                   // floats; the pad spreads the rows
   static constexpr int kRedBytes = kRows * kRedStride * 4;   // of a slot
-  static constexpr int kStages = MT == 4 ? 1024 / D : (D == 128 ? 3 : 6) - (NT == 1 ? 1 : 0);
+  static constexpr int kStages = NT == 4 ? (D == 128 ? 3 : 4) * MT : NT == 2 || D == 64 ? 3 : 2;
   static constexpr int kRingBytes = kSlots * kStages * kTileBytes;
-  static constexpr int kSmem = kRingBytes + 2 * kRedBytes;
+  static constexpr int kQBytes = kSharedQ ? kRows * D * 2 : 0;
+  static constexpr int kSmem = kRingBytes + 2 * kRedBytes + kQBytes;
   static_assert(kCtasPerSm * (kSmem + 1024 + 2560) <= 228 * 1024, "shared memory of an SM");
 };
 
@@ -62,7 +65,15 @@ template <int D, int NT, int MT>
 struct Fp4Shared {
   float m[Fp4Cfg<D, NT, MT>::kSlots][Fp4Cfg<D, NT, MT>::kRows];   // largest score, log2 units
   float l[Fp4Cfg<D, NT, MT>::kSlots][Fp4Cfg<D, NT, MT>::kRows];
+  float c2[Fp4Cfg<D, NT, MT>::kRows];   // (kSharedQ)
 };
+
+// 16 bytes to shared memory, asynchronously; zeros where nothing is `there`.
+__device__ __forceinline__ void copy16_sized(uint32_t dst, const uint8_t* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(there ? 16 : 0)
+               : "memory");
+}
 
 __device__ __forceinline__ void copies_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -101,6 +112,7 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Fp4Shared<D, NT, MT> sh;
   float* red = reinterpret_cast<float*>(smem + C::kRingBytes);   // [2][kRows][kRedStride]
+  uint2* sq = reinterpret_cast<uint2*>(smem + C::kRingBytes + 2 * C::kRedBytes);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int slot = warp / MT, mt = warp % MT;
@@ -131,32 +143,57 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
                        : checked_page(row[(key >> a.page_shift) + 1], a.num_pages, a.status);
     }
   };
-  auto issue = [&](const PagedPiece& p, int u) {
+  // A lane's sources: 16-byte pieces of the tile's key and value codes, and (the
+  // slot's first warp) one of its scales, of keys or values.
+  constexpr int kCopies = C::kCodeBytes / (MT * 512);    // of codes, per tensor
+  constexpr int kScalePieces = C::kScaleBytes / 16;      // per tensor
+  const int me = mt * 32 + lane;
+  const bool of_values = lane >= kScalePieces;
+  const int scale_piece = lane & (kScalePieces - 1);
+  const bool scales = mt == 0 && lane < 2 * kScalePieces;
+  const uint32_t to_codes = smem_u32(ring) + me * 16;
+  const uint32_t to_scales = smem_u32(ring) + 2 * C::kCodeBytes + lane * 16;
+  const int64_t scale_page = of_values ? f.v.scale_page : f.k.scale_page;
+  const uint8_t *from_k = nullptr, *from_v = nullptr, *from_s = nullptr;
+  auto sources = [&](const PagedPiece& p) {
+    const int64_t head = p.h / a.blocks;
+    from_k = f.k.codes + head * f.k.code_head + me * 16;
+    from_v = f.v.codes + head * f.v.code_head + me * 16;
+    from_s = (of_values ? f.v.scales + head * f.v.scale_head : f.k.scales + head * f.k.scale_head) +
+             scale_piece * 16;
+  };
+  auto issue = [&](const PagedPiece& p, int u, int stage) {
     const int pg0 = __shfl_sync(0xffffffffu, page_of[0], u & 31);
     const int pg1 = __shfl_sync(0xffffffffu, page_of[1], u & 31);
-    uint8_t* to = ring + u % ST * C::kTileBytes;
-    const int row = small_pages ? 0 : (p.t0 + slot + kSlots * u) * KT & ((1 << a.page_shift) - 1);
-    const int64_t head = p.h / a.blocks;
-    const int me = mt * 32 + lane;
-    // `bytes` of the tile's rows, half of them in each of two small pages
-    auto copy = [&](uint8_t* dst, const uint8_t* src, int64_t page_step, int64_t head_step,
-                    int row_bytes, int bytes) {
-      const uint8_t* base = src + head * head_step + row * row_bytes;
+    const bool in0 = pg0 < a.num_pages, in1 = pg1 < a.num_pages;
+    const int row = (p.t0 + slot + kSlots * u) * KT & ((1 << a.page_shift) - 1);
+    // the two halves of a tile lie apart where pages have 16 keys
+    const uint8_t *k0 = from_k + (in0 ? pg0 * f.k.code_page : 0) + row * (D / 2), *k1 = k0;
+    const uint8_t *v0 = from_v + (in0 ? pg0 * f.v.code_page : 0) + row * (D / 2), *v1 = v0;
+    const bool upper = scale_piece >= kScalePieces / 2;
+    const uint8_t* s0 =
+        from_s + (in0 ? pg0 * scale_page : 0) + row * (D / kFp4Block);
+    bool s_in = in0;
+    if (small_pages) {
+      k0 = from_k + (in0 ? pg0 * f.k.code_page : 0);
+      v0 = from_v + (in0 ? pg0 * f.v.code_page : 0);
+      k1 = from_k + (in1 ? pg1 * f.k.code_page : 0) - C::kCodeBytes / 2;
+      v1 = from_v + (in1 ? pg1 * f.v.code_page : 0) - C::kCodeBytes / 2;
+      s_in = upper ? in1 : in0;
+      s0 = from_s + (s_in ? (upper ? pg1 : pg0) * scale_page : 0) -
+           (upper ? C::kScaleBytes / 2 : 0);
+    }
+    const uint32_t at = stage * C::kTileBytes;
 #pragma unroll
-      for (int c = me * 16; c < bytes; c += MT * 512) {
-        const bool second = small_pages && c >= bytes / 2;
-        const int page = second ? pg1 : pg0;
-        const bool there = page < a.num_pages;
-        copy16_async(dst + c,
-                     there ? base + page * page_step + (second ? c - bytes / 2 : c) : src, there);
-      }
-    };
-    copy(to, f.k.codes, f.k.code_page, f.k.code_head, D / 2, C::kCodeBytes);
-    copy(to + C::kCodeBytes, f.v.codes, f.v.code_page, f.v.code_head, D / 2, C::kCodeBytes);
-    copy(to + 2 * C::kCodeBytes, f.k.scales, f.k.scale_page, f.k.scale_head, D / kFp4Block,
-         C::kScaleBytes);
-    copy(to + 2 * C::kCodeBytes + C::kScaleBytes, f.v.scales, f.v.scale_page, f.v.scale_head,
-         D / kFp4Block, C::kScaleBytes);
+    for (int i = 0; i < kCopies; ++i) {
+      constexpr int kHalf = C::kCodeBytes / 2;
+      const bool second = MT * 512 <= kHalf ? i * MT * 512 >= kHalf : mt * 512 >= kHalf;
+      const bool in = second ? in1 : in0;
+      copy16_sized(to_codes + at + i * MT * 512, (second ? k1 : k0) + i * MT * 512, in);
+      copy16_sized(to_codes + at + C::kCodeBytes + i * MT * 512, (second ? v1 : v0) + i * MT * 512,
+                   in);
+    }
+    if (scales) copy16_sized(to_scales + at, s0, s_in);
   };
   // every warp of the slot: its copies of the tile have landed, and it is done
   // with the tile before
@@ -170,24 +207,20 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
     const int nu = slot_tiles(p);
     slot_sync();      // the ring is free
     if (nu > 0) load_pages(p, 0, nu);
+    sources(p);
     for (int u = 0; u < ST - 1; ++u) {
-      if (u < nu) issue(p, u);
+      if (u < nu) issue(p, u, u);
       copies_commit();
     }
     // Q^T fragments: row r = 8 n + g, columns of quarter t, as fp16 times 2^e
     const int row0 = segment_row(a, p.h), nrows = segment_rows(a, p.h);
-    uint32_t qb[NT][kSteps][2];
-    float c2[NT][2];                // what turns a score into log2 units, rows 2t, 2t + 1
-    int lim[NT][2];                 // keys below lim are allowed
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int r = (mt * NT + n) * 8 + g;
+    auto load_q = [&](int block, uint32_t* w) {   // a block of 8 rows; the factor of row g
+      const int r = block * 8 + g;
       const bool live = r < nrows;
       const int h = (row0 + r) / a.n_q, qt = row0 + r - h * a.n_q;
       const uint4* qr = reinterpret_cast<const uint4*>(
           a.q + p.b * a.stride_b + h * a.stride_h + static_cast<int64_t>(qt) * a.stride_n +
           t * (D / 4));
-      uint32_t w[D / 8];
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         const uint4 x = live ? qr[i] : make_uint4(0u, 0u, 0u, 0u);
@@ -198,20 +231,42 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
       }
       int e;
       half_rows<D / 8>(w, &e);
+      return score_factor(a.scale_log2 * f.k_descale, e);
+    };
+    uint32_t qb[C::kSharedQ ? 1 : NT][kSteps][2];
+    float c2[NT][2];                // what turns a score into log2 units, rows 2t, 2t + 1
+    if constexpr (C::kSharedQ) {
+      for (int n = warp; n < NT * MT; n += C::kWarps) {
+        uint32_t w[D / 8];
+        const float c = load_q(n, w);
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        qb[n][i][0] = w[2 * i];
-        qb[n][i][1] = w[2 * i + 1];
+        for (int i = 0; i < kSteps; ++i)
+          sq[(n * kSteps + i) * 32 + lane] = make_uint2(w[2 * i], w[2 * i + 1]);
+        if (t == 0) sh.c2[n * 8 + g] = c;
       }
-      const float c = score_factor(a.scale_log2 * f.k_descale, e);
+      __syncthreads();
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        c2[n][i] = __shfl_sync(0xffffffffu, c, 4 * (2 * t + i));
-        const int rr = (mt * NT + n) * 8 + 2 * t + i;
-        const int at = (row0 + rr) % a.n_q;
-        lim[n][i] = rr >= nrows ? 0 : (a.causal ? min(p.len, p.len - a.n_q + at + 1) : p.len);
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) c2[n][i] = sh.c2[(mt * NT + n) * 8 + 2 * t + i];
+    } else {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        uint32_t w[D / 8];
+        const float c = load_q(mt * NT + n, w);
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          qb[n][i][0] = w[2 * i];
+          qb[n][i][1] = w[2 * i + 1];
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) c2[n][i] = __shfl_sync(0xffffffffu, c, 4 * (2 * t + i));
       }
     }
+    auto limit = [&](int n, int i) {   // keys below it are allowed, row 2t + i of block n
+      const int r = (mt * NT + n) * 8 + 2 * t + i, qt = (row0 + r) % a.n_q;
+      return r >= nrows ? 0 : (a.causal ? min(p.len, p.len - a.n_q + qt + 1) : p.len);
+    };
     const int open = a.causal ? p.len - a.n_q + 1 : p.len;   // every row is allowed keys below it
     float m[NT][2], l[NT][2];
     float o[kSteps][NT][4];         // columns (D / 8) g + 2 i, + 1; rows 2t, 2t + 1
@@ -227,106 +282,131 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
 #pragma unroll
       for (int n = 0; n < NT; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
 
+    int stage = 0, ahead = ST - 1;   // of tile u; of tile u + ST - 1
     for (int u = 0; u < nu; ++u) {
       copies_wait_but<ST - 2>();
       slot_sync();
       if (u + ST - 1 < nu) {   // into the stage that the tile before this one has left
         if (((u + ST - 1) & 31) == 0) load_pages(p, u + ST - 1, nu);
-        issue(p, u + ST - 1);
+        issue(p, u + ST - 1, ahead);
       }
       copies_commit();
-      const uint8_t* kc = ring + u % ST * C::kTileBytes;
+      const uint8_t* kc = ring + stage * C::kTileBytes;
       const uint8_t* vc = kc + C::kCodeBytes;
       const uint8_t* ks = kc + 2 * C::kCodeBytes;
       const uint8_t* vs = ks + C::kScaleBytes;
+      stage = stage + 1 == ST ? 0 : stage + 1;
+      ahead = ahead + 1 == ST ? 0 : ahead + 1;
       const int k0 = (p.t0 + slot + kSlots * u) * KT;
 
       // S^T: row m of 16 keys is key m / 2 % 4 + 4 (m % 2) + 8 (m / 8), so that V's
       // pairs below are keys t, t + 4 and t + 8, t + 12
       float sc[2][NT][4];
       const int kg = (g >> 1) + 4 * (g & 1);
+      uint32_t w[2][2][kKeyWords], unit[2][2][D / 64];
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
           sc[half][n][0] = sc[half][n][1] = sc[half][n][2] = sc[half][n][3] = 0.f;
-        uint32_t w[2][kKeyWords], unit[2][D / 64];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int key = 16 * half + kg + 8 * i;
           if constexpr (D == 128) {
             const uint4 x = *reinterpret_cast<const uint4*>(kc + key * 64 + 16 * t);
-            w[i][0] = x.x;
-            w[i][1] = x.y;
-            w[i][2] = x.z;
-            w[i][3] = x.w;
+            w[half][i][0] = x.x;
+            w[half][i][1] = x.y;
+            w[half][i][2] = x.z;
+            w[half][i][3] = x.w;
             const uint32_t s = e4m3_to_half(
                 *reinterpret_cast<const uint16_t*>(ks + key * 8 + 2 * t));
-            unit[i][0] = __byte_perm(s, 0, 0x1010);
-            unit[i][1] = __byte_perm(s, 0, 0x3232);
+            unit[half][i][0] = __byte_perm(s, 0, 0x1010);
+            unit[half][i][1] = __byte_perm(s, 0, 0x3232);
           } else {
             const uint2 x = *reinterpret_cast<const uint2*>(kc + key * 32 + 8 * t);
-            w[i][0] = x.x;
-            w[i][1] = x.y;
-            unit[i][0] = e4m3_to_half(ks[key * 4 + t] * 0x0101u);
+            w[half][i][0] = x.x;
+            w[half][i][1] = x.y;
+            unit[half][i][0] = e4m3_to_half(ks[key * 4 + t] * 0x0101u);
           }
         }
+      }
 #pragma unroll
-        for (int j = 0; j < kKeyWords; ++j) {
-          uint32_t x[2][4];
-          e2m1_to_half(w[0][j], x[0]);
-          e2m1_to_half(w[1][j], x[1]);
+      for (int j = 0; j < kKeyWords; ++j) {
+        uint32_t x[2][2][4];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {   // two steps of 16 columns a word
-            const uint32_t ka[4] = {mul_half2(x[0][2 * i], unit[0][j / 2]),
-                                    mul_half2(x[1][2 * i], unit[1][j / 2]),
-                                    mul_half2(x[0][2 * i + 1], unit[0][j / 2]),
-                                    mul_half2(x[1][2 * i + 1], unit[1][j / 2])};
+        for (int half = 0; half < 2; ++half) {
+          e2m1_to_half(w[half][0][j], x[half][0]);
+          e2m1_to_half(w[half][1][j], x[half][1]);
+        }
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-              mma16816_half(sc[half][n], ka, qb[n][2 * j + i][0], qb[n][2 * j + i][1]);
+        for (int i = 0; i < 2; ++i) {   // two steps of 16 columns a word
+          uint32_t ka[2][4];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            ka[half][0] = mul_half2(x[half][0][2 * i], unit[half][0][j / 2]);
+            ka[half][1] = mul_half2(x[half][1][2 * i], unit[half][1][j / 2]);
+            ka[half][2] = mul_half2(x[half][0][2 * i + 1], unit[half][0][j / 2]);
+            ka[half][3] = mul_half2(x[half][1][2 * i + 1], unit[half][1][j / 2]);
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            uint2 q;
+            if constexpr (C::kSharedQ) q = sq[((mt * NT + n) * kSteps + 2 * j + i) * 32 + lane];
+            else q = make_uint2(qb[n][2 * j + i][0], qb[n][2 * j + i][1]);
+            mma16816_half(sc[0][n], ka[0], q.x, q.y);
+            mma16816_half(sc[1][n], ka[1], q.x, q.y);
           }
         }
       }
       if (k0 + KT > open) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+          for (int i = 0; i < 2; ++i) {
+            const int end = limit(n, i) - k0 - kg;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (k0 + 16 * half + kg + 8 * (e >> 1) >= lim[n][e & 1]) sc[half][n][e] = -INFINITY;
+            for (int half = 0; half < 2; ++half) {
+              if (16 * half >= end) sc[half][n][i] = -INFINITY;
+              if (16 * half + 8 >= end) sc[half][n][2 + i] = -INFINITY;
+            }
+          }
       }
-      // the running maximum (of a row: over the lanes of equal t)
-      float alpha[NT][2], base[NT][2];
-      bool moved = false;
+      // The maximum that the scores are taken against follows only where a score
+      // is 2^kLazy above it (P then stays below 2^kLazy, far inside fp16's range).
+      bool over = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float top = fmaxf(fmaxf(sc[0][n][i], sc[0][n][2 + i]), fmaxf(sc[1][n][i], sc[1][n][2 + i]));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-          const float mn = fmaxf(m[n][i], top * c2[n][i]);
-          base[n][i] = mn == -INFINITY ? 0.f : mn;   // -inf: no allowed key seen yet
-          alpha[n][i] = m[n][i] == -INFINITY ? 0.f : ex2_approx(m[n][i] - base[n][i]);
-          m[n][i] = mn;
-          moved = moved || alpha[n][i] != 1.f;
+          const float top = fmaxf(fmaxf(sc[0][n][i], sc[0][n][2 + i]), fmaxf(sc[1][n][i], sc[1][n][2 + i]));
+          over = over || fmaf(top, c2[n][i], -kLazy) > m[n][i];
         }
-      if (__any_sync(0xffffffffu, moved)) {
+      if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            l[n][i] *= alpha[n][i];
+            float top = fmaxf(fmaxf(sc[0][n][i], sc[0][n][2 + i]), fmaxf(sc[1][n][i], sc[1][n][2 + i]));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            const float mn = fmaxf(m[n][i], top * c2[n][i]);
+            const float alpha = m[n][i] == -INFINITY ? 0.f : ex2_approx(m[n][i] - mn);
+            m[n][i] = mn;
+            l[n][i] *= alpha;
 #pragma unroll
             for (int k = 0; k < kSteps; ++k) {
-              o[k][n][i] *= alpha[n][i];
-              o[k][n][2 + i] *= alpha[n][i];
+              o[k][n][i] *= alpha;
+              o[k][n][2 + i] *= alpha;
             }
           }
       }
+      float base[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          base[n][i] = m[n][i] == -INFINITY ? 0.f : m[n][i];   // -inf: no allowed key seen yet
       // P^T = 2^(S c - m c) as fp16 B fragments; row sums from the same fp32 values
       uint32_t pb[2][NT][2];
 #pragma unroll
@@ -505,8 +585,8 @@ template <int D>
 cudaError_t launch_width(const PagedArgs& a, const Fp4Args& f, int ctas, cudaStream_t s) {
   if (a.rows <= 8) return launch_rows<D, 1, 1>(a, f, ctas, s);
   if (a.rows <= 16) return launch_rows<D, 2, 1>(a, f, ctas, s);
-  if (a.rows <= 32) return launch_rows<D, 2, 2>(a, f, ctas, s);
-  return launch_rows<D, 2, 4>(a, f, ctas, s);
+  if (a.rows <= 32) return launch_rows<D, 4, 1>(a, f, ctas, s);
+  return launch_rows<D, 4, 2>(a, f, ctas, s);
 }
 
 }  // namespace

@@ -38,18 +38,21 @@ def attention_key_weights(q, k_pages, page_table, cache_lens, lse, weights, *, k
     if q.dtype is not _bf16 or len(shape) != 4:
         raise TypeError("q must be bf16 [B, H, n_q, d]")
     B, H, n_q, d = shape
+    dense = q.is_contiguous()
+    qs = ((H or 1) * n_q * d, n_q * d, d) if dense else _strides(q)[:3]
     cache = keys = 0
     ks = (0, 0, 0)
     if k_scales is not None:
         cache, pages = _cache(k_pages, k_scales, k_descale, index, "keys")
     else:
-        pages = tuple(k_pages.shape)
+        pages = k_pages.shape
         if k_pages.dtype is not _bf16 or k_pages.get_device() != index:
             raise TypeError("k_pages must be bf16 on q's device, or codes with k_scales")
         if len(pages) != 4:
             raise ValueError("k_pages must be [num_pages, H_kv, page_size, d]")
         keys = k_pages.data_ptr()
-        ks = [x or d for x in _strides(k_pages)[:3]]
+        ks = ((pages[1] or 1) * pages[2] * d, pages[2] * d, d) if k_pages.is_contiguous() \
+            else _strides(k_pages)[:3]
     num_pages, H_kv, page_size, cols = pages
     if cols != d or H_kv < (1 if H else 0) or (H_kv and H % H_kv):
         raise ValueError("the keys must have q's d and an H_kv that divides its H")
@@ -58,7 +61,6 @@ def attention_key_weights(q, k_pages, page_table, cache_lens, lse, weights, *, k
         raise ValueError("lse must be a contiguous fp32 [B, H, n_q] on q's device")
     table, row, width, lens = _table(page_table, cache_lens, B, index, page_size)
     w = _weights(weights, B, H_kv, width * page_size, index)
-    qs = [x or d for x in _strides(q)[:3]]
     p = _PARAMS(B, H, width * page_size, d, 0, d ** -0.5 if scale is None else scale,
                 1 if causal else 0, 0.0, 0, 0, lens, 0, 0, *qs, H_kv, 0, *ks, 0.0, 0.0, 0.0, 0)
     g = _PAGES(table, row, width, page_size, num_pages, 0)
@@ -88,22 +90,28 @@ def pages_evict(pools, page_table, cache_lens, refs, weights, seqs, new_lens, *,
         raise ValueError("weights must be [rows, H_kv, keys]")
     heads = weights.shape[1]
     w = _weights(weights, page_table.shape[0], heads, page_table.shape[1] * page_size, index)
-    rows = b""
+    lead, rows = (P, heads, page_size), b""
     for x in pools:
-        if x.get_device() != index or x.dim() < 4 or tuple(x.shape[:3]) != (P, heads, page_size):
+        shape, n = x.shape, x.element_size()   # n: bytes of a row
+        if x.get_device() != index or len(shape) < 4 or shape[:3] != lead:
             raise ValueError("pools must be [num_pages, H_kv, page_size, ...] on the table's device")
-        s, item = _strides(x), x.element_size()
-        n = 1
-        for size, step in zip(reversed(x.shape[3:]), reversed(s[3:])):
-            if size != 1 and step != n:
-                raise ValueError("a pool's row must be one contiguous block of memory")
-            n *= size
-        rows += _ROWS(x.data_ptr(), s[0] * item, s[1] * item, s[2] * item, n * item, 0)
+        if x.is_contiguous():
+            for size in shape[3:]:
+                n *= size
+            steps = heads * page_size * n, page_size * n, n
+        else:
+            s, item = _strides(x), n
+            for size, step in zip(reversed(shape[3:]), reversed(s[3:])):
+                if size != 1 and step * item != n:
+                    raise ValueError("a pool's row must be one contiguous block of memory")
+                n *= size
+            steps = s[0] * item, s[1] * item, s[2] * item
+        rows += _ROWS(x.data_ptr(), *steps, n, 0)
     a, n = _list(seqs, refs.device, "seqs")
     b, m = _list(new_lens, refs.device, "new_lens")
     if n != m:
         raise ValueError("seqs and new_lens must have the same length")
-    slots = torch.empty((n, heads, weights.shape[2]), dtype=torch.int32, device=refs.device)
+    slots = refs.new_empty((n, heads, weights.shape[2]))
     c = lib()
     _call(c.attn_pages_evict, c.attn_pages_evict_workspace_size, (t, heads, n, rows, len(pools)),
           (t, rows, len(pools), heads, *w, weights.shape[2], a, b, n, recent, slots.data_ptr()),

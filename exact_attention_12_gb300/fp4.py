@@ -14,29 +14,33 @@ import torch
 
 from .api import _FP8
 from ._abi import lib
-from .paged import _PAGES, _PARAMS, _bf16, _call, _empty_like, _lse, _strides, _table
+from .paged import _PAGES, _PARAMS, _bf16, _call, _empty_like, _i32, _lse, _strides, _table
 
 _FP4 = struct.Struct("@PP4qfi").pack   # attn_fp4 as bytes
 _u8 = torch.uint8
 
 
 def _cache(codes, scales, descale, index, what):
-    """attn_fp4 of a cache tensor, and its [num_pages, H_kv, page_size, d]."""
+    """attn_fp4 of a cache tensor, and its (num_pages, H_kv, page_size, d)."""
     if codes.dtype is not _u8 or scales.dtype is not _FP8 \
             or not index == codes.get_device() == scales.get_device():
         raise TypeError(f"{what}: codes must be uint8 and scales float8_e4m3fn, on one device")
-    shape, half = scales.shape, codes.shape
+    half, shape = codes.shape, scales.shape
     if len(half) != 4 or len(shape) != 4 or half[:3] != shape[:3] or half[3] != 8 * shape[3]:
         raise ValueError(f"{what}: codes must be [num_pages, H_kv, page_size, d / 2], scales "
                          "[num_pages, H_kv, page_size, d / 16]")
     P, H, size, n = shape
-    cs, ss = _strides(codes), _strides(scales)
-    if (cs[2], ss[2]) != (8 * n, n) and size > 1:
-        raise ValueError(f"{what}: a head's rows of a page must follow one another")
-    d = 16 * n
-    # (a cache without heads or pages has no strides to speak of)
-    return _FP4(codes.data_ptr(), scales.data_ptr(), cs[0] or 16, cs[1] or 16, ss[0] or 16,
-                ss[1] or 16, descale, 0), (P, H, size, d)
+    if codes.is_contiguous() and scales.is_contiguous():
+        # (a cache without heads has no strides to speak of)
+        head = size * n
+        page = (H or 1) * head
+        steps = 8 * page, 8 * head, page, head
+    else:
+        cs, ss = _strides(codes), _strides(scales)
+        if (cs[2], ss[2]) != (8 * n, n) and size > 1:
+            raise ValueError(f"{what}: a head's rows of a page must follow one another")
+        steps = cs[0], cs[1], ss[0], ss[1]
+    return _FP4(codes.data_ptr(), scales.data_ptr(), *steps, descale, 0), (P, H, size, 16 * n)
 
 
 def _both(k_codes, k_scales, v_codes, v_scales, k_descale, v_descale, index):
@@ -88,25 +92,15 @@ def attention_decode_fp4(q, k_codes, k_scales, v_codes, v_scales, page_table, ca
     return out, lse
 
 
-def _copy_args(k, v, cache, page_table, cache_lens, counts):
+def _copy_args(B, n, strides, cache, page_table, cache_lens, counts, index):
     """attn_params, attn_pages and the counts' pointer of a store or load."""
     num_pages, H_kv, page_size, d = cache
-    if len(k.shape) != 4 or k.shape != v.shape or k.shape[1] != H_kv or k.shape[3] != d:
-        raise ValueError("k and v must be [B, H_kv, n, d] with the cache's H_kv and d")
-    B, _, n, _ = k.shape
-    index = k.get_device()
-    if not (k.dtype is v.dtype is _bf16) or v.get_device() != index:
-        raise TypeError("k and v must be bf16 on one device")
-    ks = _strides(k)
-    if ks != _strides(v):
-        raise ValueError("k and v must share strides")
-    if counts is not None and (counts.dtype is not torch.int32 or counts.get_device() != index
+    if counts is not None and (counts.dtype is not _i32 or counts.get_device() != index
                                or counts.shape != (B,) or not counts.is_contiguous()):
         raise ValueError("counts must be a contiguous int32 [B] on the tensors' device")
     table, row, width, lens = _table(page_table, cache_lens, B, index, page_size)
-    # (strides of a tensor without heads or tokens: some that hold)
-    p = _PARAMS(B, H_kv, n, d, 0, 1.0, 0, 0.0, 0, 0, lens, 0, 0, d, d, d, H_kv, 0, ks[0] or d,
-                ks[1] or d, ks[2], 0.0, 0.0, 0.0, 0)
+    p = _PARAMS(B, H_kv, n, d, 0, 1.0, 0, 0.0, 0, 0, lens, 0, 0, d, d, d, H_kv, 0, *strides,
+                0.0, 0.0, 0.0, 0)
     return p, _PAGES(table, row, width, page_size, num_pages, 0), \
         0 if counts is None else counts.data_ptr()
 
@@ -122,9 +116,21 @@ def pages_store_fp4(k, v, k_codes, k_scales, v_codes, v_scales, page_table, cach
     2688 (6 * 448, the format's largest); a block of 16 columns keeps its relative
     precision down to 2^-14 of that.
     """
-    kc, vc, cache = _both(k_codes, k_scales, v_codes, v_scales, k_descale, v_descale,
-                          k.get_device())
-    p, g, m = _copy_args(k, v, cache, page_table, cache_lens, counts)
+    shape, index = k.shape, k.get_device()
+    kc, vc, cache = _both(k_codes, k_scales, v_codes, v_scales, k_descale, v_descale, index)
+    if not (k.dtype is v.dtype is _bf16) or v.get_device() != index:
+        raise TypeError("k and v must be bf16 on one device")
+    _, H_kv, _, d = cache
+    if len(shape) != 4 or shape != v.shape or shape[1] != H_kv or shape[3] != d:
+        raise ValueError("k and v must be [B, H_kv, n, d] with the cache's H_kv and d")
+    B, _, n, _ = shape
+    if k.is_contiguous() and v.is_contiguous():
+        strides = (H_kv or 1) * (n or 1) * d, (n or 1) * d, d
+    else:
+        strides = _strides(k)[:3]
+        if strides != _strides(v)[:3]:
+            raise ValueError("k and v must share strides")
+    p, g, m = _copy_args(B, n, strides, cache, page_table, cache_lens, counts, index)
     _call(lib().attn_pages_store_fp4, None, (), (p, g, m, k.data_ptr(), v.data_ptr(), kc, vc),
           k.device, ws, "attn_pages_store_fp4")
 
@@ -134,12 +140,14 @@ def pages_load_fp4(k_codes, k_scales, v_codes, v_scales, page_table, cache_lens,
     """The newest tokens of each sequence out of a cache of 4 bits: (k, v), bf16
     [B, H_kv, n, d], token t < counts[b] (None: n) that of position cache_lens[b] -
     counts[b] + t, zeros elsewhere.  With counts = cache_lens: whole sequences."""
-    device = k_codes.device
-    kc, vc, cache = _both(k_codes, k_scales, v_codes, v_scales, k_descale, v_descale,
-                          k_codes.get_device())
-    k, v = (torch.empty((page_table.shape[0], cache[1], n, cache[3]), dtype=_bf16, device=device)
-            for _ in range(2))
-    p, g, m = _copy_args(k, v, cache, page_table, cache_lens, counts)
+    index = k_codes.get_device()
+    kc, vc, cache = _both(k_codes, k_scales, v_codes, v_scales, k_descale, v_descale, index)
+    _, H_kv, _, d = cache
+    B = page_table.shape[0]
+    k = k_codes.new_empty((B, H_kv, n, d), dtype=_bf16)
+    v = _empty_like(k)
+    p, g, m = _copy_args(B, n, ((H_kv or 1) * (n or 1) * d, (n or 1) * d, d), cache, page_table,
+                         cache_lens, counts, index)
     _call(lib().attn_pages_load_fp4, None, (), (p, g, m, kc, vc, k.data_ptr(), v.data_ptr()),
-          device, ws, "attn_pages_load_fp4")
+          k_codes.device, ws, "attn_pages_load_fp4")
     return k, v
