@@ -39,11 +39,12 @@ using namespace sm103;
 namespace {
 
 constexpr float kLazy = 8.f;
+constexpr float kNone = -3e38f;   // a row's maximum before its first key
 
 // NT: blocks of 8 query rows per warp; MT: warps that share a tile.
 template <int D, int NT, int MT>
 struct Fp4Cfg {
-  static constexpr int kWarps = NT == 2 ? 6 : 8;
+  static constexpr int kWarps = 4 * MT;
   static constexpr int kSlots = kWarps / MT;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kRows = 8 * NT * MT;                  // of a CTA
@@ -51,10 +52,10 @@ struct Fp4Cfg {
   static constexpr int kCodeBytes = kFp4Keys * D / 2;        // of a tile's keys (or values)
   static constexpr int kScaleBytes = kFp4Keys * D / kFp4Block;
   static constexpr int kTileBytes = 2 * (kCodeBytes + kScaleBytes);
-  static constexpr int kCtasPerSm = NT == 4 ? 1 : 2;
+  static constexpr int kCtasPerSm = fp4_ctas_per_sm(8 * NT * MT);
   static constexpr int kRedStride = D + 4;                   // floats; the pad spreads the rows
   static constexpr int kRedBytes = kRows * kRedStride * 4;   // of a slot
-  static constexpr int kStages = NT == 4 ? (D == 128 ? 3 : 4) * MT : NT == 2 || D == 64 ? 3 : 2;
+  static constexpr int kStages = NT == 1 && D == 128 ? 2 : MT == 2 || D == 64 ? 4 : 3;
   static constexpr int kRingBytes = kSlots * kStages * kTileBytes;
   static constexpr int kQBytes = kSharedQ ? kRows * D * 2 : 0;
   static constexpr int kSmem = kRingBytes + 2 * kRedBytes + kQBytes;
@@ -90,16 +91,33 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {   // an 8 x 8 matri
   return r;
 }
 
-// Eight bytes of shared memory (four at d = 64).
-template <int D>
-__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
-  if constexpr (D == 128) {
-    const uint2 x = *reinterpret_cast<const uint2*>(p);
-    w[0] = x.x;
-    w[1] = x.y;
-  } else {
-    w[0] = *reinterpret_cast<const uint32_t*>(p);
-  }
+// N words of shared memory.
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t addr, uint32_t* w) {
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+  else
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+}
+
+__device__ __forceinline__ uint32_t load_byte(uint32_t addr) {
+  uint32_t r;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(addr));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t load_pair(uint32_t addr) {   // two bytes
+  uint32_t r;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=r"(r) : "r"(addr));
+  return r;
+}
+
+// base + page * step, the step in 32 bits (the host sees to that).
+__device__ __forceinline__ const uint8_t* page_at(const uint8_t* base, int page, int64_t step) {
+  return base + static_cast<uint64_t>(static_cast<uint32_t>(page)) * static_cast<uint32_t>(step);
 }
 
 template <int D, int NT, int MT>
@@ -155,6 +173,13 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
   const uint32_t to_scales = smem_u32(ring) + 2 * C::kCodeBytes + lane * 16;
   const int64_t scale_page = of_values ? f.v.scale_page : f.k.scale_page;
   const uint8_t *from_k = nullptr, *from_v = nullptr, *from_s = nullptr;
+  // and where it reads: see the products
+  const int kg = (g >> 1) + 4 * (g & 1);
+  const uint32_t at_k = smem_u32(ring) + kg * (D / 2) + t * (D / 8);
+  const uint32_t at_v = smem_u32(ring) + C::kCodeBytes + t * (D / 2) + g * (D / 16);
+  const uint32_t at_ks = smem_u32(ring) + 2 * C::kCodeBytes + kg * (D / kFp4Block) + t * (D / 64);
+  const uint32_t at_vs = smem_u32(ring) + 2 * C::kCodeBytes + C::kScaleBytes +
+                         t * (D / kFp4Block) + (D == 128 ? g : g >> 1);
   auto sources = [&](const PagedPiece& p) {
     const int64_t head = p.h / a.blocks;
     from_k = f.k.codes + head * f.k.code_head + me * 16;
@@ -162,38 +187,39 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
     from_s = (of_values ? f.v.scales + head * f.v.scale_head : f.k.scales + head * f.k.scale_head) +
              scale_piece * 16;
   };
-  auto issue = [&](const PagedPiece& p, int u, int stage) {
-    const int pg0 = __shfl_sync(0xffffffffu, page_of[0], u & 31);
-    const int pg1 = __shfl_sync(0xffffffffu, page_of[1], u & 31);
-    const bool in0 = pg0 < a.num_pages, in1 = pg1 < a.num_pages;
-    const int row = (p.t0 + slot + kSlots * u) * KT & ((1 << a.page_shift) - 1);
-    // the two halves of a tile lie apart where pages have 16 keys
-    const uint8_t *k0 = from_k + (in0 ? pg0 * f.k.code_page : 0) + row * (D / 2), *k1 = k0;
-    const uint8_t *v0 = from_v + (in0 ? pg0 * f.v.code_page : 0) + row * (D / 2), *v1 = v0;
-    const bool upper = scale_piece >= kScalePieces / 2;
-    const uint8_t* s0 =
-        from_s + (in0 ? pg0 * scale_page : 0) + row * (D / kFp4Block);
-    bool s_in = in0;
-    if (small_pages) {
-      k0 = from_k + (in0 ? pg0 * f.k.code_page : 0);
-      v0 = from_v + (in0 ? pg0 * f.v.code_page : 0);
-      k1 = from_k + (in1 ? pg1 * f.k.code_page : 0) - C::kCodeBytes / 2;
-      v1 = from_v + (in1 ? pg1 * f.v.code_page : 0) - C::kCodeBytes / 2;
+  auto issue = [&](const PagedPiece& p, int u, uint32_t stage) {   // stage: its offset
+    int pg0 = __shfl_sync(0xffffffffu, page_of[0], u & 31);
+    const bool in0 = pg0 < a.num_pages;
+    pg0 = in0 ? pg0 : 0;
+    const uint8_t *k0, *v0, *s0, *k1, *v1;
+    bool in1 = in0, s_in = in0;
+    if (!small_pages) {
+      const uint32_t row = (p.t0 + slot + kSlots * u) * KT & ((1 << a.page_shift) - 1);
+      k0 = k1 = page_at(from_k, pg0, f.k.code_page) + row * (D / 2);
+      v0 = v1 = page_at(from_v, pg0, f.v.code_page) + row * (D / 2);
+      s0 = page_at(from_s, pg0, scale_page) + row * (D / kFp4Block);
+    } else {   // the two halves of a tile lie apart
+      int pg1 = __shfl_sync(0xffffffffu, page_of[1], u & 31);
+      in1 = pg1 < a.num_pages;
+      pg1 = in1 ? pg1 : 0;
+      k0 = page_at(from_k, pg0, f.k.code_page);
+      v0 = page_at(from_v, pg0, f.v.code_page);
+      k1 = page_at(from_k, pg1, f.k.code_page) - C::kCodeBytes / 2;
+      v1 = page_at(from_v, pg1, f.v.code_page) - C::kCodeBytes / 2;
+      const bool upper = scale_piece >= kScalePieces / 2;
       s_in = upper ? in1 : in0;
-      s0 = from_s + (s_in ? (upper ? pg1 : pg0) * scale_page : 0) -
-           (upper ? C::kScaleBytes / 2 : 0);
+      s0 = page_at(from_s, upper ? pg1 : pg0, scale_page) - (upper ? C::kScaleBytes / 2 : 0);
     }
-    const uint32_t at = stage * C::kTileBytes;
 #pragma unroll
     for (int i = 0; i < kCopies; ++i) {
       constexpr int kHalf = C::kCodeBytes / 2;
       const bool second = MT * 512 <= kHalf ? i * MT * 512 >= kHalf : mt * 512 >= kHalf;
       const bool in = second ? in1 : in0;
-      copy16_sized(to_codes + at + i * MT * 512, (second ? k1 : k0) + i * MT * 512, in);
-      copy16_sized(to_codes + at + C::kCodeBytes + i * MT * 512, (second ? v1 : v0) + i * MT * 512,
-                   in);
+      copy16_sized(to_codes + stage + i * MT * 512, (second ? k1 : k0) + i * MT * 512, in);
+      copy16_sized(to_codes + stage + C::kCodeBytes + i * MT * 512,
+                   (second ? v1 : v0) + i * MT * 512, in);
     }
-    if (scales) copy16_sized(to_scales + at, s0, s_in);
+    if (scales) copy16_sized(to_scales + stage, s0, s_in);
   };
   // every warp of the slot: its copies of the tile have landed, and it is done
   // with the tile before
@@ -209,7 +235,7 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
     if (nu > 0) load_pages(p, 0, nu);
     sources(p);
     for (int u = 0; u < ST - 1; ++u) {
-      if (u < nu) issue(p, u, u);
+      if (u < nu) issue(p, u, u * C::kTileBytes);
       copies_commit();
     }
     // Q^T fragments: row r = 8 n + g, columns of quarter t, as fp16 times 2^e
@@ -274,7 +300,7 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        m[n][i] = -INFINITY;
+        m[n][i] = kNone;
         l[n][i] = 0.f;
       }
 #pragma unroll
@@ -282,7 +308,7 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
 #pragma unroll
       for (int n = 0; n < NT; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
 
-    int stage = 0, ahead = ST - 1;   // of tile u; of tile u + ST - 1
+    uint32_t stage = 0, ahead = (ST - 1) * C::kTileBytes;   // of tile u; of tile u + ST - 1
     for (int u = 0; u < nu; ++u) {
       copies_wait_but<ST - 2>();
       slot_sync();
@@ -291,18 +317,20 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
         issue(p, u + ST - 1, ahead);
       }
       copies_commit();
-      const uint8_t* kc = ring + stage * C::kTileBytes;
-      const uint8_t* vc = kc + C::kCodeBytes;
-      const uint8_t* ks = kc + 2 * C::kCodeBytes;
-      const uint8_t* vs = ks + C::kScaleBytes;
-      stage = stage + 1 == ST ? 0 : stage + 1;
-      ahead = ahead + 1 == ST ? 0 : ahead + 1;
+      const uint32_t kc = at_k + stage, vc = at_v + stage, ks = at_ks + stage, vs = at_vs + stage;
       const int k0 = (p.t0 + slot + kSlots * u) * KT;
+      if (k0 + KT > p.len) {   // value rows past the end: their scales are zero
+        const int from = (p.len - k0) * (D / kFp4Block) + lane;
+        uint8_t* to = ring + stage + 2 * C::kCodeBytes + C::kScaleBytes;
+        for (int i = from; i < C::kScaleBytes; i += 32) to[i] = 0;
+        __syncwarp();
+      }
+      stage = stage == (ST - 1) * C::kTileBytes ? 0 : stage + C::kTileBytes;
+      ahead = ahead == (ST - 1) * C::kTileBytes ? 0 : ahead + C::kTileBytes;
 
       // S^T: row m of 16 keys is key m / 2 % 4 + 4 (m % 2) + 8 (m / 8), so that V's
       // pairs below are keys t, t + 4 and t + 8, t + 12
       float sc[2][NT][4];
-      const int kg = (g >> 1) + 4 * (g & 1);
       uint32_t w[2][2][kKeyWords], unit[2][2][D / 64];
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -311,22 +339,15 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
           sc[half][n][0] = sc[half][n][1] = sc[half][n][2] = sc[half][n][3] = 0.f;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int key = 16 * half + kg + 8 * i;
+          constexpr int kRow = D / 2, kScaleRow = D / kFp4Block;
+          load_words<kKeyWords>(kc + (16 * half + 8 * i) * kRow, w[half][i]);
           if constexpr (D == 128) {
-            const uint4 x = *reinterpret_cast<const uint4*>(kc + key * 64 + 16 * t);
-            w[half][i][0] = x.x;
-            w[half][i][1] = x.y;
-            w[half][i][2] = x.z;
-            w[half][i][3] = x.w;
-            const uint32_t s = e4m3_to_half(
-                *reinterpret_cast<const uint16_t*>(ks + key * 8 + 2 * t));
+            const uint32_t s = e4m3_to_half(load_pair(ks + (16 * half + 8 * i) * kScaleRow));
             unit[half][i][0] = __byte_perm(s, 0, 0x1010);
             unit[half][i][1] = __byte_perm(s, 0, 0x3232);
           } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(kc + key * 32 + 8 * t);
-            w[half][i][0] = x.x;
-            w[half][i][1] = x.y;
-            unit[half][i][0] = e4m3_to_half(ks[key * 4 + t] * 0x0101u);
+            unit[half][i][0] =
+                e4m3_to_half(load_byte(ks + (16 * half + 8 * i) * kScaleRow) * 0x0101u);
           }
         }
       }
@@ -391,7 +412,7 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
             const float mn = fmaxf(m[n][i], top * c2[n][i]);
-            const float alpha = m[n][i] == -INFINITY ? 0.f : ex2_approx(m[n][i] - mn);
+            const float alpha = ex2_approx(m[n][i] - mn);
             m[n][i] = mn;
             l[n][i] *= alpha;
 #pragma unroll
@@ -401,12 +422,6 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
             }
           }
       }
-      float base[NT][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          base[n][i] = m[n][i] == -INFINITY ? 0.f : m[n][i];   // -inf: no allowed key seen yet
       // P^T = 2^(S c - m c) as fp16 B fragments; row sums from the same fp32 values
       uint32_t pb[2][NT][2];
 #pragma unroll
@@ -415,26 +430,24 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float p0 = ex2_approx(fmaf(sc[half][n][2 * i], c2[n][0], -base[n][0]));
-            const float p1 = ex2_approx(fmaf(sc[half][n][2 * i + 1], c2[n][1], -base[n][1]));
+            const float p0 = ex2_approx(fmaf(sc[half][n][2 * i], c2[n][0], -m[n][0]));
+            const float p1 = ex2_approx(fmaf(sc[half][n][2 * i + 1], c2[n][1], -m[n][1]));
             l[n][0] += p0;
             l[n][1] += p1;
             pb[half][n][i] = transpose8(pack_half2(p0, p1));
           }
       // O^T += V^T P^T: lane g has columns (D / 8) g ...; MMA row g is column 2 i, row
       // g + 8 column 2 i + 1 of them
-      const bool last = k0 + KT > p.len;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         uint32_t w[4][D / 64], s[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int key = 16 * half + t + 4 * j;
-          load_words<D>(vc + key * (D / 2) + (D / 16) * g, w[j]);
-          s[j] = vs[key * (D / kFp4Block) + (D == 128 ? g : g >> 1)];
-          if (last && k0 + key >= p.len) s[j] = 0;
+          load_words<D / 64>(vc + (16 * half + 4 * j) * (D / 2), w[j]);
+          s[j] = load_byte(vs + (16 * half + 4 * j) * (D / kFp4Block));
         }
-        const uint32_t unit[2] = {e4m3_to_half(s[0] | s[1] << 8), e4m3_to_half(s[2] | s[3] << 8)};
+        const uint32_t unit[2] = {e4m3_to_half(__byte_perm(s[0], s[1], 0x0040)),
+                                  e4m3_to_half(__byte_perm(s[2], s[3], 0x0040))};
 #pragma unroll
         for (int j = 0; j < D / 64; ++j) {
           uint32_t x[2][2][4];   // [pair of keys][column 2 i or 2 i + 1][i]
@@ -465,7 +478,9 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
         l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], 4);
         l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], 8);
         l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], 16);
-        if (l[n][i] != l[n][i]) m[n][i] = 0.f;   // a row of NaN scores has seen keys
+        // no keys; a row of NaN scores has seen some
+        if (l[n][i] == 0.f) m[n][i] = -INFINITY;
+        else if (l[n][i] != l[n][i]) m[n][i] = 0.f;
         if (g == 0) {
           sh.m[slot][(mt * NT + n) * 8 + 2 * t + i] = m[n][i];
           sh.l[slot][(mt * NT + n) * 8 + 2 * t + i] = l[n][i];

@@ -73,6 +73,12 @@ constexpr int kFp4Keys = 32;
 constexpr int kFp4Overhead = 8;
 constexpr int kFp4MinUnits = 6;
 
+// CTAs of the decode kernel per SM at `rows` query rows of a segment: 16 warps of
+// up to 8 rows, 12 of 16, 8 of 32.
+constexpr int fp4_ctas_per_sm(int rows) {
+  return rows <= 8 ? 4 : rows <= 16 ? 3 : rows <= 32 ? 2 : 1;
+}
+
 // ------------------------------------------------------------- conversions --
 
 // Four bytes of codes: r[i] the two values of byte i (the low four bits first) as

@@ -79,6 +79,8 @@ attn_status check_cache(const attn_fp4* c, int num_pages) {
   for (int64_t s : steps)
     if (s <= 0 || s % 16 != 0)
       return fail(ATTN_ERR_INVALID_ARG, "cache: strides must be positive multiples of 16 bytes");
+  if (c->code_page >> 32 != 0 || c->scale_page >> 32 != 0)
+    return fail(ATTN_ERR_UNSUPPORTED, "cache: pages must be less than 2^32 bytes apart");
   return ATTN_OK;
 }
 
@@ -165,7 +167,7 @@ Layout decode_layout(const attn_params* p, int32_t n_q, const attn_pages* g) {
   L.blocks = (L.head_rows + attn::kDecMaxRows - 1) / attn::kDecMaxRows;
   L.rows = L.blocks > 0 ? (L.head_rows + L.blocks - 1) / L.blocks : 0;
   L.heads = H_kv * L.blocks;
-  const int64_t most = L.rows > 16 ? sms : 2 * sms;
+  const int64_t most = attn::fp4_ctas_per_sm(L.rows) * sms;
   const int64_t tiles = (static_cast<int64_t>(p->N) + attn::kFp4Keys - 1) / attn::kFp4Keys;
   const int64_t segments = static_cast<int64_t>(p->B) * L.heads;
   const int64_t want = segments * (tiles + attn::kFp4Overhead) / attn::kFp4MinUnits;

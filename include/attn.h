@@ -335,8 +335,8 @@ attn_status attn_decode_latent(const attn_params* p, int32_t n_q, const attn_pag
 typedef struct attn_fp4 {
   void* codes;               /* 16-byte aligned, as is scales */
   void* scales;
-  int64_t code_page, code_head;    /* bytes between pages and between heads, */
-  int64_t scale_page, scale_head;  /* multiples of 16 */
+  int64_t code_page, code_head;    /* bytes between pages (below 2^32) and between */
+  int64_t scale_page, scale_head;  /* heads, multiples of 16 */
   float descale;             /* 2^-100 to 2^100 */
   int32_t reserved;          /* must be 0 */
 } attn_fp4;
