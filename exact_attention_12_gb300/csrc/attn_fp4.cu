@@ -52,6 +52,7 @@ struct Fp4Cfg {
   static constexpr int kCodeBytes = kFp4Keys * D / 2;        // of a tile's keys (or values)
   static constexpr int kScaleBytes = kFp4Keys * D / kFp4Block;
   static constexpr int kTileBytes = 2 * (kCodeBytes + kScaleBytes);
+  static constexpr int kOverhead = fp4_overhead(kRows);
   static constexpr int kCtasPerSm = fp4_ctas_per_sm(8 * NT * MT);
   static constexpr int kRedStride = D + 4;                   // floats; the pad spreads the rows
   static constexpr int kRedBytes = kRows * kRedStride * 4;   // of a slot
@@ -91,28 +92,23 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {   // an 8 x 8 matri
   return r;
 }
 
-// N words of shared memory.
+// N words of shared memory.  (Plain loads, so that the compiler may move them
+// between the products, but not across the waits for the copies.)
 template <int N>
-__device__ __forceinline__ void load_words(uint32_t addr, uint32_t* w) {
-  if constexpr (N == 4)
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
-  else if constexpr (N == 2)
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
-  else
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
-}
-
-__device__ __forceinline__ uint32_t load_byte(uint32_t addr) {
-  uint32_t r;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(addr));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t load_pair(uint32_t addr) {   // two bytes
-  uint32_t r;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=r"(r) : "r"(addr));
-  return r;
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
+  if constexpr (N == 4) {
+    const uint4 x = *reinterpret_cast<const uint4*>(p);
+    w[0] = x.x;
+    w[1] = x.y;
+    w[2] = x.z;
+    w[3] = x.w;
+  } else if constexpr (N == 2) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    w[0] = x.x;
+    w[1] = x.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
 }
 
 // base + page * step, the step in 32 bits (the host sees to that).
@@ -139,7 +135,7 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
   grid_dep_wait();
   grid_dep_launch();
   const PagedShare share =
-      paged_share<KT, kFp4Overhead, kFp4MinUnits>(a, blockIdx.x, gridDim.x);
+      paged_share<KT, C::kOverhead, kFp4MinUnits>(a, blockIdx.x, gridDim.x);
   MergeNote note{-1, 0, 0, 0};
   const bool small_pages = a.page_shift < 5;   // 16 keys: a tile lies in two
 
@@ -175,10 +171,10 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
   const uint8_t *from_k = nullptr, *from_v = nullptr, *from_s = nullptr;
   // and where it reads: see the products
   const int kg = (g >> 1) + 4 * (g & 1);
-  const uint32_t at_k = smem_u32(ring) + kg * (D / 2) + t * (D / 8);
-  const uint32_t at_v = smem_u32(ring) + C::kCodeBytes + t * (D / 2) + g * (D / 16);
-  const uint32_t at_ks = smem_u32(ring) + 2 * C::kCodeBytes + kg * (D / kFp4Block) + t * (D / 64);
-  const uint32_t at_vs = smem_u32(ring) + 2 * C::kCodeBytes + C::kScaleBytes +
+  const uint8_t* at_k = ring + kg * (D / 2) + t * (D / 8);
+  const uint8_t* at_v = ring + C::kCodeBytes + t * (D / 2) + g * (D / 16);
+  const uint8_t* at_ks = ring + 2 * C::kCodeBytes + kg * (D / kFp4Block) + t * (D / 64);
+  const uint8_t* at_vs = ring + 2 * C::kCodeBytes + C::kScaleBytes +
                          t * (D / kFp4Block) + (D == 128 ? g : g >> 1);
   auto sources = [&](const PagedPiece& p) {
     const int64_t head = p.h / a.blocks;
@@ -228,20 +224,15 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
     else asm volatile("bar.sync %0, %1;" ::"r"(slot + 1), "n"(32 * MT) : "memory");
   };
 
-  PagedPiece p = paged_piece<KT, kFp4Overhead>(a, share, share.b, 0, share.s);
-  while (p.valid) {   // (the same pieces in every warp)
-    const int nu = slot_tiles(p);
-    slot_sync();      // the ring is free
-    if (nu > 0) load_pages(p, 0, nu);
-    sources(p);
-    for (int u = 0; u < ST - 1; ++u) {
-      if (u < nu) issue(p, u, u * C::kTileBytes);
-      copies_commit();
-    }
-    // Q^T fragments: row r = 8 n + g, columns of quarter t, as fp16 times 2^e
+  // What a piece begins with, on its way early: its rows of Q (raw), its pages,
+  // its first tiles.
+  constexpr int kQBlocks = C::kSharedQ ? 1 : NT;   // of 8 rows that this warp loads
+  uint32_t qw[kQBlocks][D / 8];
+  auto fetch_q = [&](const PagedPiece& p) {
     const int row0 = segment_row(a, p.h), nrows = segment_rows(a, p.h);
-    auto load_q = [&](int block, uint32_t* w) {   // a block of 8 rows; the factor of row g
-      const int r = block * 8 + g;
+#pragma unroll
+    for (int n = 0; n < kQBlocks; ++n) {
+      const int r = (C::kSharedQ ? warp : mt * NT + n) * 8 + g;
       const bool live = r < nrows;
       const int h = (row0 + r) / a.n_q, qt = row0 + r - h * a.n_q;
       const uint4* qr = reinterpret_cast<const uint4*>(
@@ -250,26 +241,52 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         const uint4 x = live ? qr[i] : make_uint4(0u, 0u, 0u, 0u);
-        w[4 * i] = x.x;
-        w[4 * i + 1] = x.y;
-        w[4 * i + 2] = x.z;
-        w[4 * i + 3] = x.w;
+        qw[n][4 * i] = x.x;
+        qw[n][4 * i + 1] = x.y;
+        qw[n][4 * i + 2] = x.z;
+        qw[n][4 * i + 3] = x.w;
       }
-      int e;
-      half_rows<D / 8>(w, &e);
-      return score_factor(a.scale_log2 * f.k_descale, e);
-    };
-    uint32_t qb[C::kSharedQ ? 1 : NT][kSteps][2];
+    }
+  };
+  auto fetch = [&](const PagedPiece& p) {
+    const int nu = slot_tiles(p);
+    if constexpr (!C::kSharedQ) fetch_q(p);
+    if (nu > 0) load_pages(p, 0, nu);
+    sources(p);
+    for (int u = 0; u < ST - 1; ++u) {
+      if (u < nu) issue(p, u, u * C::kTileBytes);
+      copies_commit();
+    }
+  };
+
+  PagedPiece p = paged_piece<KT, C::kOverhead>(a, share, share.b, 0, share.s);
+  if (p.valid) fetch(p);
+  while (p.valid) {   // (the same pieces in every warp)
+    const int nu = slot_tiles(p);
+    // Q^T fragments: row r = 8 n + g, columns of quarter t, as fp16 times 2^e
+    const int row0 = segment_row(a, p.h), nrows = segment_rows(a, p.h);
     float c2[NT][2];                // what turns a score into log2 units, rows 2t, 2t + 1
-    if constexpr (C::kSharedQ) {
-      for (int n = warp; n < NT * MT; n += C::kWarps) {
-        uint32_t w[D / 8];
-        const float c = load_q(n, w);
+    float factor[kQBlocks];
+    if constexpr (C::kSharedQ) fetch_q(p);   // (late: the registers are O's until then)
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i)
-          sq[(n * kSteps + i) * 32 + lane] = make_uint2(w[2 * i], w[2 * i + 1]);
-        if (t == 0) sh.c2[n * 8 + g] = c;
+    for (int n = 0; n < kQBlocks; ++n) {
+      int e;
+      half_rows<D / 8>(qw[n], &e);
+      factor[n] = score_factor(a.scale_log2 * f.k_descale, e);
+    }
+    uint32_t qb[kQBlocks][kSteps][2];
+#pragma unroll
+    for (int n = 0; n < kQBlocks; ++n)
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        qb[n][i][0] = qw[n][2 * i];
+        qb[n][i][1] = qw[n][2 * i + 1];
       }
+    if constexpr (C::kSharedQ) {
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+        sq[(warp * kSteps + i) * 32 + lane] = make_uint2(qb[0][i][0], qb[0][i][1]);
+      if (t == 0) sh.c2[warp * 8 + g] = factor[0];
       __syncthreads();
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -277,17 +294,10 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
         for (int i = 0; i < 2; ++i) c2[n][i] = sh.c2[(mt * NT + n) * 8 + 2 * t + i];
     } else {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        uint32_t w[D / 8];
-        const float c = load_q(mt * NT + n, w);
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-          qb[n][i][0] = w[2 * i];
-          qb[n][i][1] = w[2 * i + 1];
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) c2[n][i] = __shfl_sync(0xffffffffu, c, 4 * (2 * t + i));
-      }
+        for (int i = 0; i < 2; ++i)
+          c2[n][i] = __shfl_sync(0xffffffffu, factor[n], 4 * (2 * t + i));
     }
     auto limit = [&](int n, int i) {   // keys below it are allowed, row 2t + i of block n
       const int r = (mt * NT + n) * 8 + 2 * t + i, qt = (row0 + r) % a.n_q;
@@ -317,7 +327,7 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
         issue(p, u + ST - 1, ahead);
       }
       copies_commit();
-      const uint32_t kc = at_k + stage, vc = at_v + stage, ks = at_ks + stage, vs = at_vs + stage;
+      const uint8_t *kc = at_k + stage, *vc = at_v + stage, *ks = at_ks + stage, *vs = at_vs + stage;
       const int k0 = (p.t0 + slot + kSlots * u) * KT;
       if (k0 + KT > p.len) {   // value rows past the end: their scales are zero
         const int from = (p.len - k0) * (D / kFp4Block) + lane;
@@ -342,12 +352,13 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
           constexpr int kRow = D / 2, kScaleRow = D / kFp4Block;
           load_words<kKeyWords>(kc + (16 * half + 8 * i) * kRow, w[half][i]);
           if constexpr (D == 128) {
-            const uint32_t s = e4m3_to_half(load_pair(ks + (16 * half + 8 * i) * kScaleRow));
+            const uint32_t s = e4m3_to_half(*reinterpret_cast<const uint16_t*>(
+                ks + (16 * half + 8 * i) * kScaleRow));
             unit[half][i][0] = __byte_perm(s, 0, 0x1010);
             unit[half][i][1] = __byte_perm(s, 0, 0x3232);
           } else {
             unit[half][i][0] =
-                e4m3_to_half(load_byte(ks + (16 * half + 8 * i) * kScaleRow) * 0x0101u);
+                e4m3_to_half(ks[(16 * half + 8 * i) * kScaleRow] * 0x0101u);
           }
         }
       }
@@ -444,7 +455,7 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           load_words<D / 64>(vc + (16 * half + 4 * j) * (D / 2), w[j]);
-          s[j] = load_byte(vs + (16 * half + 4 * j) * (D / kFp4Block));
+          s[j] = vs[(16 * half + 4 * j) * (D / kFp4Block)];
         }
         const uint32_t unit[2] = {e4m3_to_half(__byte_perm(s[0], s[1], 0x0040)),
                                   e4m3_to_half(__byte_perm(s[2], s[3], 0x0040))};
@@ -469,6 +480,9 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
       }
     }
     copies_wait_but<0>();
+    const PagedPiece next = paged_next<KT, C::kOverhead>(a, share, p);
+    slot_sync();   // the ring is free
+    if (next.valid) fetch(next);
 
     // ---- the slots' states merged: m, l per row, then O through shared memory
 #pragma unroll
@@ -514,7 +528,7 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
         }
       }
     const bool whole = p.whole();
-    if (p.t0 == 0 && !whole) note = paged_note<kFp4Overhead>(share, p);
+    if (p.t0 == 0 && !whole) note = paged_note<C::kOverhead>(share, p);
     if (a.by_segment && p.t0 == 0 && threadIdx.x == 0)
       a.notes[p.b * a.heads + p.h] = whole ? MergeNote{p.b, p.h, 0, -1} : note;
     const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (p.s < share.lo ? 0 : 1);
@@ -574,7 +588,7 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
       }
     }
     __syncthreads();   // red, m and l are free
-    p = paged_next<KT, kFp4Overhead>(a, share, p);
+    p = next;
   }
   if (!a.by_segment && threadIdx.x == 0) a.notes[blockIdx.x] = note;
 }

@@ -70,7 +70,7 @@ cudaError_t launch_fp4_decode(const PagedArgs& a, const Fp4Args& f, int ctas, cu
 
 // Decode: key tiles of 32, the split's constants in such tiles.
 constexpr int kFp4Keys = 32;
-constexpr int kFp4Overhead = 8;
+constexpr int fp4_overhead(int rows) { return rows <= 16 ? 8 : 20; }
 constexpr int kFp4MinUnits = 6;
 
 // CTAs of the decode kernel per SM at `rows` query rows of a segment: 16 warps of
@@ -120,7 +120,7 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 // c += a b, 16 x 8 x 16, fp16 inputs, fp32 accumulators
 __device__ __forceinline__ void mma16816_half(float* c, const uint32_t* a, uint32_t b0,
                                               uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])

@@ -170,7 +170,7 @@ Layout decode_layout(const attn_params* p, int32_t n_q, const attn_pages* g) {
   const int64_t most = attn::fp4_ctas_per_sm(L.rows) * sms;
   const int64_t tiles = (static_cast<int64_t>(p->N) + attn::kFp4Keys - 1) / attn::kFp4Keys;
   const int64_t segments = static_cast<int64_t>(p->B) * L.heads;
-  const int64_t want = segments * (tiles + attn::kFp4Overhead) / attn::kFp4MinUnits;
+  const int64_t want = segments * (tiles + attn::fp4_overhead(L.rows)) / attn::kFp4MinUnits;
   L.ctas = static_cast<int>(most < want ? most : want);
   if (L.ctas < 1) L.ctas = 1;
   L.by_segment = segments <= L.ctas;
@@ -272,7 +272,8 @@ attn_status attn_pages_load_fp4(const attn_params* p, const attn_pages* pages,
 }
 
 size_t attn_decode_fp4_workspace_size(const attn_params* p, int32_t n_q, const attn_pages* pages) {
-  if (check_step(p, n_q, pages, attn::kFp4Keys, attn::kFp4Overhead, attn::kDecMaxRows) != ATTN_OK)
+  if (check_step(p, n_q, pages, attn::kFp4Keys, attn::fp4_overhead(attn::kDecMaxRows),
+                 attn::kDecMaxRows) != ATTN_OK)
     return 0;
   return decode_layout(p, n_q, pages).total;
 }
@@ -281,7 +282,8 @@ attn_status attn_decode_fp4(const attn_params* p, int32_t n_q, const attn_pages*
                             const void* q, const attn_fp4* k, const attn_fp4* v, void* o,
                             float* lse, void* ws, size_t ws_bytes, void* stream) {
   attn_status st =
-      check_step(p, n_q, pages, attn::kFp4Keys, attn::kFp4Overhead, attn::kDecMaxRows);
+      check_step(p, n_q, pages, attn::kFp4Keys, attn::fp4_overhead(attn::kDecMaxRows),
+                 attn::kDecMaxRows);
   if (st != ATTN_OK || (st = check_cache(k, pages->num_pages)) != ATTN_OK ||
       (st = check_cache(v, pages->num_pages)) != ATTN_OK)
     return st;
