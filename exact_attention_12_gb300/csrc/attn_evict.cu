@@ -33,13 +33,13 @@ using namespace sm103;
 
 namespace {
 
-constexpr int kSelectThreads = 1024;
+constexpr int kSelectThreads = 512;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 constexpr int kMoveThreads = 256;
 constexpr int kMoveBytes = 32768;         // of a chunk, all pools
-constexpr int kMaxChunk = 1024;           // keys of a chunk
+constexpr int kMaxChunk = 512;            // keys of a chunk
 constexpr int kMaxPools = 16;
 constexpr int kFinishThreads = 128;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
@@ -49,6 +49,7 @@ struct RowPool {
   int64_t page, head, row;   // bytes between pages, heads, rows
   int bytes;                 // of a row
   int unit;                  // bytes of one copy: 16, 8 or 4
+  int shift;                 // log2 of the copies of a row, -1: no power of two
   int at;                    // where its rows begin in a chunk's buffer
 };
 
@@ -70,7 +71,8 @@ struct EvictArgs {
   int32_t* ticket;
   int32_t* read;             // [n][heads][chunks]: the chunk's rows have been read
   int32_t* bound;            // [n][heads][chunks + 1]: kept keys before slot c T
-  int chunk, chunks;         // T; chunks of a row of the table
+  int chunk, chunk_shift;    // T, a power of two
+  int chunks;                // of a row of the table
   int cluster;               // CTAs per (sequence, head) of the first kernel
   int n_pools;
   RowPool pools[kMaxPools];
@@ -122,12 +124,21 @@ __device__ bool check_entry(const EvictArgs& a, int i, int* old_out, int* len_ou
 }
 
 struct SelectShared {
-  uint32_t bins[3][kBins];
+  alignas(16) uint32_t bins[3][kBins];
   uint32_t warp_sum[kSelectWarps + 1];
   uint32_t digit, left;              // the round's digit; how many are still to choose in it
   uint32_t above[kSelectWarps], equal[kSelectWarps];
   uint32_t cta_above, cta_equal;     // of this CTA's part, for the others
 };
+
+__device__ __forceinline__ uint4 cluster_ld_u4(uint32_t addr) {
+  uint4 x;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+               : "r"(addr)
+               : "memory");
+  return x;
+}
 
 __device__ __forceinline__ uint32_t cluster_ld_u32(uint32_t addr) {
   uint32_t x;
@@ -137,7 +148,7 @@ __device__ __forceinline__ uint32_t cluster_ld_u32(uint32_t addr) {
 
 // CACHED: the CTA's part of the weights stays in shared memory.
 template <bool CACHED>
-__global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const EvictArgs a) {
   extern __shared__ __align__(16) uint32_t cache[];
   __shared__ SelectShared sh;
   grid_dep_wait();
@@ -192,19 +203,26 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs 
       }
       if (C > 1) cluster_sync();
       else __syncthreads();
-      // thread x has the bins 2047 - 2 x and 2046 - 2 x, from the top
-      uint32_t n2[2] = {0, 0};
-      const int top = kBins - 1 - 2 * static_cast<int>(threadIdx.x);
-      for (int q = 0; q < C; ++q) {
-        if (C > 1) {
-          n2[0] += cluster_ld_u32(cluster_addr(&sh.bins[round][top], q));
-          n2[1] += cluster_ld_u32(cluster_addr(&sh.bins[round][top - 1], q));
-        } else {
-          n2[0] += sh.bins[round][top];
-          n2[1] += sh.bins[round][top - 1];
-        }
+      // thread x has the bins 2047 - 4 x, ..., 2044 - 4 x, from the top
+      const int low = kBins - 4 - 4 * static_cast<int>(threadIdx.x);
+      uint32_t n4[4] = {0, 0, 0, 0};
+      uint4 got[kMaxCluster];
+#pragma unroll
+      for (int q = 0; q < kMaxCluster; ++q) {   // (all on their way before the first is used)
+        got[q] = make_uint4(0, 0, 0, 0);
+        if (q < C)
+          got[q] = C > 1 ? cluster_ld_u4(cluster_addr(&sh.bins[round][low], q))
+                         : *reinterpret_cast<const uint4*>(&sh.bins[round][low]);
       }
-      uint32_t inc = n2[0] + n2[1];
+#pragma unroll
+      for (int q = 0; q < kMaxCluster; ++q) {
+        n4[0] += got[q].w;
+        n4[1] += got[q].z;
+        n4[2] += got[q].y;
+        n4[3] += got[q].x;
+      }
+      const uint32_t own = n4[0] + n4[1] + n4[2] + n4[3];
+      uint32_t inc = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
@@ -213,12 +231,15 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs 
       if (lane == 31) sh.warp_sum[warp] = inc;
       __syncthreads();
       uint32_t before = 0;
-      for (int q = 0; q < warp; ++q) before += sh.warp_sum[q];
-      const uint32_t end = before + inc, start = end - n2[0] - n2[1];
+#pragma unroll
+      for (int q = 0; q < kSelectWarps; ++q) before += q < warp ? sh.warp_sum[q] : 0u;
+      const uint32_t end = before + inc;
+      uint32_t start = end - own;
       if (start < left && left <= end) {   // one thread
-        const bool second = left > start + n2[0];
-        sh.digit = static_cast<uint32_t>(second ? top - 1 : top);
-        sh.left = left - start - (second ? n2[0] : 0u);
+        int q = 0;
+        while (q < 3 && left > start + n4[q]) start += n4[q++];
+        sh.digit = static_cast<uint32_t>(low + 3 - q);
+        sh.left = left - start;
       }
       __syncthreads();
       prefix |= sh.digit << shift;
@@ -284,7 +305,8 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs 
     if (j < stop) {
       const int slot = lo + j;
       if (up || (same && e < left)) slots[to] = slot;
-      if (slot % a.chunk == 0 && slot / a.chunk <= chunks) bound[slot / a.chunk] = to;
+      if ((slot & (a.chunk - 1)) == 0 && slot >> a.chunk_shift <= chunks)
+        bound[slot >> a.chunk_shift] = to;
     }
     above += __popc(ups);
     equal += __popc(sames);
@@ -302,14 +324,18 @@ __device__ __forceinline__ void copy_async(uint8_t* dst, const char* src, int un
   else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(s) : "memory");
 }
 
-struct MoveShared {
+// A chunk that has been looked up: where its keys come from and go to.
+struct ChunkKeys {
   int page[2][kMaxChunk];    // of a key's old and new place
   int row[kMaxChunk];        // in the old page
   float weight[kMaxChunk];
+};
+struct MoveShared {
+  ChunkKeys keys[2];
   int ticket, give_up;
 };
 
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const __grid_constant__ EvictArgs a) {
   extern __shared__ __align__(16) uint8_t buffer[];
   __shared__ MoveShared sh;
   grid_dep_wait();
@@ -317,86 +343,124 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
   const int T = a.chunk;
   int most = 0;
   for (int i = threadIdx.x; i < a.n; i += kMoveThreads)
-    if (a.old_len[i] >= 0) most = max(most, (a.new_len[i] + T - 1) / T);
+    if (a.old_len[i] >= 0) most = max(most, (a.new_len[i] + T - 1) >> a.chunk_shift);
   if (threadIdx.x == 0) sh.ticket = sh.give_up = 0;
   __syncthreads();
   atomicMax(&sh.ticket, most);
   __syncthreads();
   most = sh.ticket;
   const int items = a.n * a.heads;
-  for (;;) {
-    __syncthreads();   // the chunk before is done with, sh.ticket has been read
-    if (threadIdx.x == 0) sh.ticket = atomicAdd(a.ticket, 1);
-    __syncthreads();
-    const int ticket = sh.ticket;
-    const int c = ticket / items;
-    if (c >= most) break;
-    const int item = ticket - c * items, i = item / a.heads, h = item - i * a.heads;
-    if (a.old_len[i] < 0) continue;
-    const int len = a.new_len[i], first = c * T, count = min(T, len - first);
-    if (count <= 0) continue;
-    const int32_t* slots = a.slots + static_cast<int64_t>(item) * a.width;
-    if (slots[first + count - 1] == first + count - 1) continue;   // all of it stays
-    const int seq = a.seqs[i];
+  const int last = most * items;
+
+  struct Chunk {
+    int item, c, h, first, count;   // count 0: nothing to move
+    int from, until;                // chunks to wait for
+    float* w;
+  };
+  // Looks chunk `ticket` up, into keys[buf].  One that stays where it is counts as
+  // read.
+  auto look_up = [&](int ticket, int buf) {
+    Chunk k{};
+    if (ticket >= last) return k;
+    k.c = ticket / items;
+    k.item = ticket - k.c * items;
+    const int i = k.item / a.heads;
+    k.h = k.item - i * a.heads;
+    const int len = a.old_len[i] < 0 ? 0 : a.new_len[i];
+    k.first = k.c * T;
+    const int count = min(T, len - k.first);
+    if (count <= 0) return k;
+    const int32_t* slots = a.slots + static_cast<int64_t>(k.item) * a.width + k.first;
+    const int32_t* bound = a.bound + static_cast<int64_t>(k.item) * (a.chunks + 1) + k.c;
+    const int seq = a.seqs[i], end = slots[count - 1], b0 = bound[0], b1 = bound[1];
+    if (end == k.first + count - 1) {
+      if (threadIdx.x == 0) a.read[static_cast<int64_t>(k.item) * a.chunks + k.c] = 1;
+      return k;
+    }
+    k.count = count;
+    k.from = b0 >> a.chunk_shift;
+    k.until = min((b1 + T - 1) >> a.chunk_shift, k.c);
     const int32_t* table = a.table + seq * a.table_stride;
-    float* w = a.weights + seq * a.weight_row + h * a.weight_head;
+    k.w = a.weights + seq * a.weight_row + k.h * a.weight_head;
+    ChunkKeys& to = sh.keys[buf];
     for (int j = threadIdx.x; j < count; j += kMoveThreads) {
-      const int from = slots[first + j], to = first + j;
-      sh.page[0][j] = table[from >> a.page_shift];
-      sh.page[1][j] = table[to >> a.page_shift];
-      sh.row[j] = from & ((1 << a.page_shift) - 1);
-      sh.weight[j] = w[from];
+      const int from = slots[j];
+      to.page[0][j] = table[from >> a.page_shift];
+      to.page[1][j] = table[(k.first + j) >> a.page_shift];
+      to.row[j] = from & ((1 << a.page_shift) - 1);
+      to.weight[j] = k.w[from];
     }
-    __syncthreads();
-    for (int k = 0; k < a.n_pools; ++k) {
-      const RowPool& pool = a.pools[k];
-      const int per = pool.bytes / pool.unit;
-      const char* base = pool.base + h * pool.head;
-      for (int e = threadIdx.x; e < count * per; e += kMoveThreads) {
-        const int j = e / per, at = (e - j * per) * pool.unit;
-        copy_async(buffer + pool.at + j * pool.bytes + at,
-                   base + sh.page[0][j] * pool.page + sh.row[j] * pool.row + at, pool.unit);
-      }
-    }
-    copies_wait();
-    __syncthreads();
-    const int32_t* read = a.read + static_cast<int64_t>(item) * a.chunks;
-    if (threadIdx.x == 0) {
-      __threadfence();
-      atomicExch(const_cast<int32_t*>(read) + c, 1);
-    }
-    // chunks in front of this one that have rows where it writes
-    const int32_t* bound = a.bound + static_cast<int64_t>(item) * (a.chunks + 1);
-    const int from = bound[c] / T, until = min((bound[c + 1] + T - 1) / T, c);
-    for (int q = from + static_cast<int>(threadIdx.x); q < until; q += kMoveThreads) {
-      if (slots[q * T + T - 1] < first) continue;
-      const volatile int32_t* flag = read + q;
-      const uint64_t t0 = globaltimer_ns();
-      for (uint32_t it = 1; *flag == 0; ++it)
-        if ((it & 63u) == 0 && globaltimer_ns() - t0 > kTimeoutNs) {
-          report(a.status, kStatusTimeout);
-          sh.give_up = 1;
-          break;
+    return k;
+  };
+  auto row_of = [](const RowPool& pool, int e, int per) {
+    return pool.shift >= 0 ? e >> pool.shift : e / per;
+  };
+
+  // One chunk's rows are on their way while the next one is looked up.
+  __syncthreads();
+  if (threadIdx.x == 0) sh.ticket = atomicAdd(a.ticket, 1);
+  __syncthreads();
+  int ticket = sh.ticket;
+  Chunk now = look_up(ticket, 0);
+  for (int buf = 0; ticket < last; buf ^= 1) {
+    __syncthreads();   // its keys are there; the buffer is free; sh.ticket has been read
+    int next_ticket = 0;
+    if (threadIdx.x == 0) next_ticket = atomicAdd(a.ticket, 1);
+    const ChunkKeys& keys = sh.keys[buf];
+    if (now.count > 0)
+      for (int k = 0; k < a.n_pools; ++k) {
+        const RowPool& pool = a.pools[k];
+        const int per = pool.bytes / pool.unit;
+        const char* base = pool.base + now.h * pool.head;
+        for (int e = threadIdx.x; e < now.count * per; e += kMoveThreads) {
+          const int j = row_of(pool, e, per), at = (e - j * per) * pool.unit;
+          copy_async(buffer + pool.at + j * pool.bytes + at,
+                     base + keys.page[0][j] * pool.page + keys.row[j] * pool.row + at, pool.unit);
         }
-      __threadfence();
-    }
-    __syncthreads();
-    if (sh.give_up) break;
-    for (int k = 0; k < a.n_pools; ++k) {
-      const RowPool& pool = a.pools[k];
-      const int per = pool.bytes / pool.unit;
-      char* base = pool.base + h * pool.head;
-      for (int e = threadIdx.x; e < count * per; e += kMoveThreads) {
-        const int j = e / per, at = (e - j * per) * pool.unit;
-        char* to = base + sh.page[1][j] * pool.page +
-                   ((first + j) & ((1 << a.page_shift) - 1)) * pool.row + at;
-        const uint8_t* from_at = buffer + pool.at + j * pool.bytes + at;
-        if (pool.unit == 16) *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from_at);
-        else if (pool.unit == 8) *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(from_at);
-        else *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(from_at);
       }
+    if (threadIdx.x == 0) sh.ticket = next_ticket;
+    __syncthreads();
+    ticket = sh.ticket;
+    const Chunk next = look_up(ticket, buf ^ 1);
+    if (now.count > 0) {
+      copies_wait();
+      __syncthreads();
+      int32_t* read = a.read + static_cast<int64_t>(now.item) * a.chunks;
+      if (threadIdx.x == 0) {
+        __threadfence();
+        atomicExch(read + now.c, 1);
+      }
+      // chunks in front of this one that have rows where it writes
+      for (int q = now.from + static_cast<int>(threadIdx.x); q < now.until; q += kMoveThreads) {
+        const volatile int32_t* flag = read + q;
+        const uint64_t t0 = globaltimer_ns();
+        for (uint32_t it = 1; *flag == 0; ++it)
+          if ((it & 63u) == 0 && globaltimer_ns() - t0 > kTimeoutNs) {
+            report(a.status, kStatusTimeout);
+            sh.give_up = 1;
+            break;
+          }
+        __threadfence();
+      }
+      __syncthreads();
+      if (sh.give_up) break;
+      for (int k = 0; k < a.n_pools; ++k) {
+        const RowPool& pool = a.pools[k];
+        const int per = pool.bytes / pool.unit;
+        char* base = pool.base + now.h * pool.head;
+        for (int e = threadIdx.x; e < now.count * per; e += kMoveThreads) {
+          const int j = row_of(pool, e, per), at = (e - j * per) * pool.unit;
+          char* to = base + keys.page[1][j] * pool.page +
+                     ((now.first + j) & ((1 << a.page_shift) - 1)) * pool.row + at;
+          const uint8_t* from = buffer + pool.at + j * pool.bytes + at;
+          if (pool.unit == 16) *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
+          else if (pool.unit == 8) *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(from);
+          else *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(from);
+        }
+      }
+      for (int j = threadIdx.x; j < now.count; j += kMoveThreads) now.w[now.first + j] = keys.weight[j];
     }
-    for (int j = threadIdx.x; j < count; j += kMoveThreads) w[first + j] = sh.weight[j];
+    now = next;
   }
 }
 
@@ -607,6 +671,7 @@ attn_status attn_pages_evict(const attn_page_table* t, const attn_rows* pools, i
   a.read = ints(L.read);
   a.bound = ints(L.bound);
   a.chunk = L.chunk;
+  while ((1 << a.chunk_shift) < L.chunk) ++a.chunk_shift;
   a.chunks = L.chunks;
   a.buffer = L.buffer;
   a.cluster = select_cluster(cap, static_cast<int64_t>(n) * heads);
@@ -619,7 +684,10 @@ attn_status attn_pages_evict(const attn_page_table* t, const attn_rows* pools, i
     a.pools[i] = RowPool{static_cast<char*>(p.base), p.page_stride,
                          p.head_stride,              p.row_stride,
                          p.row_bytes,                all % 16 == 0 ? 16 : all % 8 == 0 ? 8 : 4,
-                         at};
+                         -1,                 at};
+    const int per = p.row_bytes / a.pools[i].unit;
+    for (int x = 0; x < 16; ++x)
+      if (per == 1 << x) a.pools[i].shift = x;
     at = (at + L.chunk * p.row_bytes + 15) / 16 * 16;
   }
   a.status = reinterpret_cast<int*>(ws);

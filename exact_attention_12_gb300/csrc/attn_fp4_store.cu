@@ -32,15 +32,30 @@ __device__ __forceinline__ float e4m3_value(uint32_t code) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(e4m3_to_half(code) & 0xffffu)));
 }
 
-__device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi) {
+// Eight values as codes, the first in the low four bits; nearest, at most 6.
+__device__ __forceinline__ uint32_t e2m1_of(const uint64_t* x) {   // four packed pairs
   uint32_t r;
-  asm("{\n\t.reg .b8 x;\n\t.reg .b16 y;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 x, %1, %2;\n\t"
-      "mov.b16 y, {x, 0};\n\t"
-      "cvt.u32.u16 %0, y;\n\t}"
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t.reg .f32 l, h;\n\t"
+      "mov.b64 {l, h}, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 a, h, l;\n\t"
+      "mov.b64 {l, h}, %2;\n\tcvt.rn.satfinite.e2m1x2.f32 b, h, l;\n\t"
+      "mov.b64 {l, h}, %3;\n\tcvt.rn.satfinite.e2m1x2.f32 c, h, l;\n\t"
+      "mov.b64 {l, h}, %4;\n\tcvt.rn.satfinite.e2m1x2.f32 d, h, l;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
       : "=r"(r)
-      : "f"(hi), "f"(lo));
-  return r & 0xffu;
+      : "l"(x[0]), "l"(x[1]), "l"(x[2]), "l"(x[3]));
+  return r;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ float reciprocal(float x) {   // off by an ulp or so
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 __device__ __forceinline__ float e2m1_value(uint32_t magnitude) {   // of the low three bits
@@ -66,39 +81,88 @@ __device__ __forceinline__ uint32_t block_scale(float top, float descale, float 
   return nearer(low, high, top, 6.f, descale, [](uint32_t c) { return e4m3_value(c); });
 }
 
-// One thread's block: which one, or none.
+// The blocks of a sequence's tokens: block i of `items` is columns 16 (i mod d / 16)
+// of token i / (d / 16) (head * n + t).
 struct Place {
-  int b, h, t, blk;
-  int page, row;       // where the token lies; page < 0: nowhere
-  bool valid, live;    // there is such a block; the sequence has such a token
+  int h, t, blk;
+  int page, row;     // where the token lies; page < 0: nowhere
+  bool valid, live;  // there is such a block; the sequence has such a token
 };
 
 template <int D>
-__device__ __forceinline__ Place place(const Fp4CopyArgs& a, int b, bool report) {
+__device__ __forceinline__ Place place(const Fp4CopyArgs& a, int b, int64_t i, int len, int count) {
   constexpr int kBlocks = D / kFp4Block;
   Place p{};
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kFp4Threads + threadIdx.x;
   p.valid = i < static_cast<int64_t>(a.H) * a.n * kBlocks;
+  p.page = -1;
   if (!p.valid) return p;
-  p.b = b;
   p.blk = static_cast<int>(i % kBlocks);
   const uint32_t r = static_cast<uint32_t>(i / kBlocks);
   p.h = static_cast<int>(r / static_cast<uint32_t>(a.n));
   p.t = static_cast<int>(r - static_cast<uint32_t>(p.h) * a.n);
-  const int len = min(max(a.lens[b], 0), a.cap);
-  const int count = a.counts == nullptr ? a.n : min(max(a.counts[b], 0), a.n);
   const int pos = len - count + p.t;
   p.live = p.t < count && pos >= 0;
-  p.page = -1;
   if (!p.live) return p;
   const int page = a.table[b * a.table_stride + (pos >> a.page_shift)];
   if (static_cast<unsigned>(page) < static_cast<unsigned>(a.num_pages)) p.page = page;
-  else if (report) checked_page(page, a.num_pages, a.status);
+  else checked_page(page, a.num_pages, a.status);   // (records it)
   p.row = pos & ((1 << a.page_shift) - 1);
   return p;
 }
 
-template <int D>
+__device__ __forceinline__ int cache_len(const Fp4CopyArgs& a, int b) {
+  return min(max(a.lens[b], 0), a.cap);
+}
+
+__device__ __forceinline__ int token_count(const Fp4CopyArgs& a, int b) {
+  return a.counts == nullptr ? a.n : min(max(a.counts[b], 0), a.n);
+}
+
+// A block's codes and the code of its scale.
+__device__ __forceinline__ uint2 quantised(const uint32_t* w, float descale, float inv6,
+                                           uint32_t* scale) {
+  uint64_t x[8];
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xffff0000u);
+    top = max_nan(top, max_nan(fabsf(lo), fabsf(hi)));
+    x[i] = f2_pack(lo, hi);
+  }
+  *scale = 0x7fu;   // NaN
+  if (top != top) return make_uint2(0u, 0u);
+  *scale = block_scale(top, descale, inv6);
+  if (*scale == 0) return make_uint2(0u, 0u);
+  const float unit = e4m3_value(*scale), inv = reciprocal(unit * descale);
+  const uint64_t inv2 = f2_pack(inv, inv), below = f2_pack(kBelow, kBelow),
+                 above = f2_pack(kAbove, kAbove);
+  uint64_t low[8], high[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint64_t t = f2_mul(x[i], inv2);
+    low[i] = f2_mul(t, below);
+    high[i] = f2_mul(t, above);
+  }
+  uint32_t codes[2] = {e2m1_of(low), e2m1_of(low + 4)};
+  const uint32_t other[2] = {e2m1_of(high), e2m1_of(high + 4)};
+  if (codes[0] != other[0] || codes[1] != other[1]) {   // a value next to a border
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int s = 4 * (i & 7);
+      const uint32_t l = (codes[i >> 3] >> s) & 15u, g = (other[i >> 3] >> s) & 15u;
+      if (l == g) continue;
+      float lo, hi;
+      f2_unpack(x[i >> 1], lo, hi);
+      const uint32_t m = nearer(l & 7u, g & 7u, fabsf(i & 1 ? hi : lo), unit, descale,
+                                [](uint32_t c) { return e2m1_value(c); });
+      codes[i >> 3] = (codes[i >> 3] & ~(15u << s)) | ((l & 8u) | m) << s;
+    }
+  }
+  return make_uint2(codes[0], codes[1]);
+}
+
+// N: blocks of a thread.
+template <int D, int N>
 __global__ void __launch_bounds__(kFp4Threads) fp4_store_kernel(const Fp4CopyArgs a) {
   grid_dep_wait();
   grid_dep_launch();
@@ -107,57 +171,37 @@ __global__ void __launch_bounds__(kFp4Threads) fp4_store_kernel(const Fp4CopyArg
   const float descale = values ? a.cache.v_descale : a.cache.k_descale;
   const float inv6 = 1.f / (6.f * descale);
   for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
-    const Place p = place<D>(a, b, true);
-    if (!p.valid || !p.live || p.page < 0) continue;
-    const uint4* src = reinterpret_cast<const uint4*>(
-        (values ? a.v : a.k) + p.b * a.stride_b + p.h * a.stride_h + p.t * a.stride_n +
-        kFp4Block * p.blk);
-    const uint4 w0 = __ldcs(src), w1 = __ldcs(src + 1);
-    const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-    float x[16], top = 0.f;
-    bool nan = false;
+    const int len = cache_len(a, b), count = token_count(a, b);
+    Place p[N];
+    uint4 w[N][2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      nan = nan || x[2 * i] != x[2 * i] || x[2 * i + 1] != x[2 * i + 1];
-      top = fmaxf(top, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
-    }
-    uint32_t scale = 0x7fu;   // NaN
-    uint64_t codes = 0;
-    if (!nan) {
-      scale = block_scale(top, descale, inv6);
-      if (scale != 0) {
-        const float unit = e4m3_value(scale), inv = 1.f / (unit * descale);
-        uint64_t low = 0, high = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float t0 = x[2 * i] * inv, t1 = x[2 * i + 1] * inv;
-          low |= static_cast<uint64_t>(e2m1_pair(t0 * kBelow, t1 * kBelow)) << (8 * i);
-          high |= static_cast<uint64_t>(e2m1_pair(t0 * kAbove, t1 * kAbove)) << (8 * i);
-        }
-        if (low != high) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint32_t l = (low >> (4 * i)) & 15u, g = (high >> (4 * i)) & 15u;
-            if (l == g) continue;
-            const uint64_t at = static_cast<uint64_t>(15) << (4 * i);
-            const uint32_t m = nearer(l & 7u, g & 7u, fabsf(x[i]), unit, descale,
-                                      [](uint32_t c) { return e2m1_value(c); });
-            low = (low & ~at) | static_cast<uint64_t>((l & 8u) | m) << (4 * i);
-          }
-        }
-        codes = low;
+    for (int k = 0; k < N; ++k) {
+      p[k] = place<D>(a, b, (static_cast<int64_t>(blockIdx.x) * N + k) * kFp4Threads + threadIdx.x,
+                      len, count);
+      if (p[k].live) {
+        const uint4* src = reinterpret_cast<const uint4*>(
+            (values ? a.v : a.k) + b * a.stride_b + p[k].h * a.stride_h + p[k].t * a.stride_n +
+            kFp4Block * p[k].blk);
+        w[k][0] = __ldcs(src);
+        w[k][1] = __ldcs(src + 1);
       }
     }
-    *reinterpret_cast<uint64_t*>(c.codes + p.page * c.code_page + p.h * c.code_head +
-                                 p.row * (D / 2) + 8 * p.blk) = codes;
-    c.scales[p.page * c.scale_page + p.h * c.scale_head + p.row * (D / kFp4Block) + p.blk] =
-        static_cast<uint8_t>(scale);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      if (p[k].page < 0) continue;
+      const uint32_t x[8] = {w[k][0].x, w[k][0].y, w[k][0].z, w[k][0].w,
+                             w[k][1].x, w[k][1].y, w[k][1].z, w[k][1].w};
+      uint32_t scale;
+      const uint2 codes = quantised(x, descale, inv6, &scale);
+      *reinterpret_cast<uint2*>(c.codes + p[k].page * c.code_page + p[k].h * c.code_head +
+                                p[k].row * (D / 2) + 8 * p[k].blk) = codes;
+      c.scales[p[k].page * c.scale_page + p[k].h * c.scale_head + p[k].row * (D / kFp4Block) +
+               p[k].blk] = static_cast<uint8_t>(scale);
+    }
   }
 }
 
-template <int D>
+template <int D, int N>
 __global__ void __launch_bounds__(kFp4Threads) fp4_load_kernel(const Fp4CopyArgs a) {
   grid_dep_wait();
   grid_dep_launch();
@@ -165,48 +209,77 @@ __global__ void __launch_bounds__(kFp4Threads) fp4_load_kernel(const Fp4CopyArgs
   const Fp4Cache& c = values ? a.cache.v : a.cache.k;
   const float descale = values ? a.cache.v_descale : a.cache.k_descale;
   for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
-    const Place p = place<D>(a, b, true);
-    if (!p.valid) continue;
-    uint32_t out[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (p.page >= 0) {
-      const uint2 codes = __ldcs(reinterpret_cast<const uint2*>(
-          c.codes + p.page * c.code_page + p.h * c.code_head + p.row * (D / 2) + 8 * p.blk));
-      const float unit =
-          e4m3_value(c.scales[p.page * c.scale_page + p.h * c.scale_head +
-                              p.row * (D / kFp4Block) + p.blk]);
-      uint32_t h[8];
-      e2m1_to_half(codes.x, h);
-      e2m1_to_half(codes.y, h + 4);
+    const int len = cache_len(a, b), count = token_count(a, b);
+    Place p[N];
+    uint2 codes[N];
+    uint32_t scale[N];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {   // s * c is exact, so this rounds in fp32 and to bf16
-        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-        out[i] = pack_bf16x2(x.x * unit * descale, x.y * unit * descale);
+    for (int k = 0; k < N; ++k) {
+      p[k] = place<D>(a, b, (static_cast<int64_t>(blockIdx.x) * N + k) * kFp4Threads + threadIdx.x,
+                      len, count);
+      codes[k] = make_uint2(0u, 0u);
+      scale[k] = 0;
+      if (p[k].page >= 0) {
+        codes[k] = __ldcs(reinterpret_cast<const uint2*>(
+            c.codes + p[k].page * c.code_page + p[k].h * c.code_head + p[k].row * (D / 2) +
+            8 * p[k].blk));
+        scale[k] = c.scales[p[k].page * c.scale_page + p[k].h * c.scale_head +
+                            p[k].row * (D / kFp4Block) + p[k].blk];
       }
     }
-    uint4* dst = reinterpret_cast<uint4*>((values ? a.v : a.k) + p.b * a.stride_b +
-                                          p.h * a.stride_h + p.t * a.stride_n +
-                                          kFp4Block * p.blk);
-    __stcs(dst, make_uint4(out[0], out[1], out[2], out[3]));
-    __stcs(dst + 1, make_uint4(out[4], out[5], out[6], out[7]));
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      if (!p[k].valid) continue;
+      // (two roundings of 2^-24 before the one to bf16)
+      const float unit = e4m3_value(scale[k]) * descale;
+      const uint64_t unit2 = f2_pack(unit, unit);
+      uint32_t h[8], out[8];
+      e2m1_to_half(codes[k].x, h);
+      e2m1_to_half(codes[k].y, h + 4);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+        float lo, hi;
+        f2_unpack(f2_mul(f2_pack(x.x, x.y), unit2), lo, hi);
+        out[i] = pack_bf16x2(lo, hi);
+      }
+      uint4* dst = reinterpret_cast<uint4*>((values ? a.v : a.k) + b * a.stride_b +
+                                            p[k].h * a.stride_h + p[k].t * a.stride_n +
+                                            kFp4Block * p[k].blk);
+      __stcs(dst, make_uint4(out[0], out[1], out[2], out[3]));
+      __stcs(dst + 1, make_uint4(out[4], out[5], out[6], out[7]));
+    }
   }
 }
 
+// Four blocks a thread where that leaves enough CTAs: their loads are on the way
+// together.
+constexpr int kFp4Many = 4;
+
+int64_t items_of(const Fp4CopyArgs& a) {
+  return static_cast<int64_t>(a.H) * a.n * (a.d / kFp4Block);
+}
+
+bool many(const Fp4CopyArgs& a) { return items_of(a) * a.B >= kFp4Many * kFp4Threads * 512ll; }
+
 dim3 copy_grid(const Fp4CopyArgs& a) {
-  const int64_t items = static_cast<int64_t>(a.H) * a.n * (a.d / kFp4Block);
-  return dim3(static_cast<unsigned>((items + kFp4Threads - 1) / kFp4Threads),
+  const int64_t per = (many(a) ? kFp4Many : 1) * kFp4Threads;
+  return dim3(static_cast<unsigned>((items_of(a) + per - 1) / per),
               static_cast<unsigned>(a.B < 65535 ? a.B : 65535), 2);
 }
 
 }  // namespace
 
 cudaError_t launch_fp4_store(const Fp4CopyArgs& a, cudaStream_t s) {
-  return launch_pdl(a.d == 64 ? fp4_store_kernel<64> : fp4_store_kernel<128>, copy_grid(a),
-                    dim3(kFp4Threads), 0, s, a);
+  auto kernel = many(a) ? (a.d == 64 ? fp4_store_kernel<64, kFp4Many> : fp4_store_kernel<128, kFp4Many>)
+                        : (a.d == 64 ? fp4_store_kernel<64, 1> : fp4_store_kernel<128, 1>);
+  return launch_pdl(kernel, copy_grid(a), dim3(kFp4Threads), 0, s, a);
 }
 
 cudaError_t launch_fp4_load(const Fp4CopyArgs& a, cudaStream_t s) {
-  return launch_pdl(a.d == 64 ? fp4_load_kernel<64> : fp4_load_kernel<128>, copy_grid(a),
-                    dim3(kFp4Threads), 0, s, a);
+  auto kernel = many(a) ? (a.d == 64 ? fp4_load_kernel<64, kFp4Many> : fp4_load_kernel<128, kFp4Many>)
+                        : (a.d == 64 ? fp4_load_kernel<64, 1> : fp4_load_kernel<128, 1>);
+  return launch_pdl(kernel, copy_grid(a), dim3(kFp4Threads), 0, s, a);
 }
 
 }  // namespace attn
