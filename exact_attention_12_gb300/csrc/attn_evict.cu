@@ -38,7 +38,7 @@ constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 constexpr int kMoveThreads = 256;
-constexpr int kMoveBytes = 32768;         // of a chunk, all pools
+constexpr int kMoveBytes = 40960;         // of a chunk, all pools
 constexpr int kMaxChunk = 512;            // keys of a chunk
 constexpr int kMaxPools = 16;
 constexpr int kFinishThreads = 128;
@@ -426,10 +426,9 @@ __global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const __grid_cons
       copies_wait();
       __syncthreads();
       int32_t* read = a.read + static_cast<int64_t>(now.item) * a.chunks;
-      if (threadIdx.x == 0) {
-        __threadfence();
-        atomicExch(read + now.c, 1);
-      }
+      // (The rows have arrived, so the flag needs no fence before it; and whoever
+      // sees it set writes only after that.)
+      if (threadIdx.x == 0) atomicExch(read + now.c, 1);
       // chunks in front of this one that have rows where it writes
       for (int q = now.from + static_cast<int>(threadIdx.x); q < now.until; q += kMoveThreads) {
         const volatile int32_t* flag = read + q;
@@ -440,7 +439,6 @@ __global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const __grid_cons
             sh.give_up = 1;
             break;
           }
-        __threadfence();
       }
       __syncthreads();
       if (sh.give_up) break;
@@ -533,7 +531,7 @@ int check_evict(const attn_page_table* t, int32_t heads, int32_t n, const attn_r
                  "pools: base, row_bytes and strides must be multiples of 4, rows apart");
     total += p.row_bytes;
   }
-  if (total > kMoveBytes) return bad(ATTN_ERR_UNSUPPORTED, "pools: more than 32768 bytes a row");
+  if (total > 32768) return bad(ATTN_ERR_UNSUPPORTED, "pools: more than 32768 bytes a row");
   return ATTN_OK;
 }
 

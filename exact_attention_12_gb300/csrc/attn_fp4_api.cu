@@ -222,8 +222,7 @@ attn_status copy(const attn_params* p, const attn_pages* g, const int32_t* count
   if (st != ATTN_OK || (st = check_cache(kc, g->num_pages)) != ATTN_OK ||
       (st = check_cache(vc, g->num_pages)) != ATTN_OK)
     return st;
-  if (static_cast<int64_t>(p->H_kv) * p->N >= (int64_t{1} << 28))
-    return fail(ATTN_ERR_UNSUPPORTED, "H_kv * n must stay below 2^28");
+  if (p->N > (1 << 30)) return fail(ATTN_ERR_UNSUPPORTED, "more than 2^30 tokens");
   if (!good_strides({p->kv_stride_b, p->kv_stride_h, p->kv_stride_n}, p->d))
     return fail(ATTN_ERR_INVALID_ARG, "kv strides must be positive multiples of 8, the last >= d");
   if ((st = check_ws(ws, ws_bytes, kHeaderBytes)) != ATTN_OK) return st;

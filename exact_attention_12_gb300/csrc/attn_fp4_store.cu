@@ -9,9 +9,9 @@
 // above, and where the two differ (a few in 2^19) the sign of x - border * descale
 // decides, which one fused multiply-add gives exactly.
 //
-// Bound: HBM, 2.56 bytes an element.  A thread takes one block of 16 columns,
-// 32 bytes in, 9 out; the rows of a page follow one another, so both sides
-// are contiguous over a warp.
+// Bound: HBM, 2.56 bytes an element.  A thread takes 8 columns, 16 bytes in and 4
+// out, so that each access of a warp is one run of bytes; two lanes share a
+// scale.
 #include "attn_fp4.cuh"
 
 namespace attn {
@@ -81,35 +81,6 @@ __device__ __forceinline__ uint32_t block_scale(float top, float descale, float 
   return nearer(low, high, top, 6.f, descale, [](uint32_t c) { return e4m3_value(c); });
 }
 
-// The blocks of a sequence's tokens: block i of `items` is columns 16 (i mod d / 16)
-// of token i / (d / 16) (head * n + t).
-struct Place {
-  int h, t, blk;
-  int page, row;     // where the token lies; page < 0: nowhere
-  bool valid, live;  // there is such a block; the sequence has such a token
-};
-
-template <int D>
-__device__ __forceinline__ Place place(const Fp4CopyArgs& a, int b, int64_t i, int len, int count) {
-  constexpr int kBlocks = D / kFp4Block;
-  Place p{};
-  p.valid = i < static_cast<int64_t>(a.H) * a.n * kBlocks;
-  p.page = -1;
-  if (!p.valid) return p;
-  p.blk = static_cast<int>(i % kBlocks);
-  const uint32_t r = static_cast<uint32_t>(i / kBlocks);
-  p.h = static_cast<int>(r / static_cast<uint32_t>(a.n));
-  p.t = static_cast<int>(r - static_cast<uint32_t>(p.h) * a.n);
-  const int pos = len - count + p.t;
-  p.live = p.t < count && pos >= 0;
-  if (!p.live) return p;
-  const int page = a.table[b * a.table_stride + (pos >> a.page_shift)];
-  if (static_cast<unsigned>(page) < static_cast<unsigned>(a.num_pages)) p.page = page;
-  else checked_page(page, a.num_pages, a.status);   // (records it)
-  p.row = pos & ((1 << a.page_shift) - 1);
-  return p;
-}
-
 __device__ __forceinline__ int cache_len(const Fp4CopyArgs& a, int b) {
   return min(max(a.lens[b], 0), a.cap);
 }
@@ -118,168 +89,197 @@ __device__ __forceinline__ int token_count(const Fp4CopyArgs& a, int b) {
   return a.counts == nullptr ? a.n : min(max(a.counts[b], 0), a.n);
 }
 
-// A block's codes and the code of its scale.
-__device__ __forceinline__ uint2 quantised(const uint32_t* w, float descale, float inv6,
-                                           uint32_t* scale) {
-  uint64_t x[8];
+// A CTA takes 2^tile_shift tokens of a sequence, one thread 8 columns of one token,
+// of every (kRows >> tile_shift)-th head; kRows rows at once.
+template <int D>
+struct Lanes {
+  static constexpr int kParts = D / 8, kRows = kFp4Threads / kParts;
+  int t, h, step, part;   // token, first head, heads between, which 8 columns
+  __device__ explicit Lanes(int tile_shift) {
+    const int row = threadIdx.x / kParts;
+    part = threadIdx.x % kParts;
+    t = (blockIdx.x << tile_shift) + (row & ((1 << tile_shift) - 1));
+    h = row >> tile_shift;
+    step = kRows >> tile_shift;
+  }
+};
+
+// The page of a token's position, -1 where the table names none.
+__device__ __forceinline__ int token_page(const Fp4CopyArgs& a, int b, int pos) {
+  const int page = a.table[b * a.table_stride + (pos >> a.page_shift)];
+  if (static_cast<unsigned>(page) < static_cast<unsigned>(a.num_pages)) return page;
+  checked_page(page, a.num_pages, a.status);   // (records it)
+  return -1;
+}
+
+// The codes of 8 columns and the code of the scale that they share with the
+// neighbouring lane's (which is here too).
+__device__ __forceinline__ uint32_t quantised(const uint4& w, float descale, float inv6,
+                                              uint32_t* scale) {
+  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+  uint64_t x[4];
   float top = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xffff0000u);
+  for (int i = 0; i < 4; ++i) {
+    const float lo = __uint_as_float(v[i] << 16), hi = __uint_as_float(v[i] & 0xffff0000u);
     top = max_nan(top, max_nan(fabsf(lo), fabsf(hi)));
     x[i] = f2_pack(lo, hi);
   }
+  top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
   *scale = 0x7fu;   // NaN
-  if (top != top) return make_uint2(0u, 0u);
+  if (top != top) return 0u;
   *scale = block_scale(top, descale, inv6);
-  if (*scale == 0) return make_uint2(0u, 0u);
+  if (*scale == 0) return 0u;
   const float unit = e4m3_value(*scale), inv = reciprocal(unit * descale);
   const uint64_t inv2 = f2_pack(inv, inv), below = f2_pack(kBelow, kBelow),
                  above = f2_pack(kAbove, kAbove);
-  uint64_t low[8], high[8];
+  uint64_t low[4], high[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     const uint64_t t = f2_mul(x[i], inv2);
     low[i] = f2_mul(t, below);
     high[i] = f2_mul(t, above);
   }
-  uint32_t codes[2] = {e2m1_of(low), e2m1_of(low + 4)};
-  const uint32_t other[2] = {e2m1_of(high), e2m1_of(high + 4)};
-  if (codes[0] != other[0] || codes[1] != other[1]) {   // a value next to a border
+  uint32_t codes = e2m1_of(low);
+  const uint32_t other = e2m1_of(high);
+  if (codes != other) {   // a value next to a border
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int s = 4 * (i & 7);
-      const uint32_t l = (codes[i >> 3] >> s) & 15u, g = (other[i >> 3] >> s) & 15u;
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t l = (codes >> (4 * i)) & 15u, g = (other >> (4 * i)) & 15u;
       if (l == g) continue;
       float lo, hi;
       f2_unpack(x[i >> 1], lo, hi);
       const uint32_t m = nearer(l & 7u, g & 7u, fabsf(i & 1 ? hi : lo), unit, descale,
                                 [](uint32_t c) { return e2m1_value(c); });
-      codes[i >> 3] = (codes[i >> 3] & ~(15u << s)) | ((l & 8u) | m) << s;
+      codes = (codes & ~(15u << (4 * i))) | ((l & 8u) | m) << (4 * i);
     }
   }
-  return make_uint2(codes[0], codes[1]);
+  return codes;
 }
 
-// N: blocks of a thread.
-template <int D, int N>
-__global__ void __launch_bounds__(kFp4Threads) fp4_store_kernel(const Fp4CopyArgs a) {
+constexpr int kAtOnce = 4;   // heads whose loads are on the way together
+
+template <int D>
+__global__ void __launch_bounds__(kFp4Threads) fp4_store_kernel(const Fp4CopyArgs a, int tile_shift) {
   grid_dep_wait();
   grid_dep_launch();
   const bool values = blockIdx.z != 0;
   const Fp4Cache& c = values ? a.cache.v : a.cache.k;
   const float descale = values ? a.cache.v_descale : a.cache.k_descale;
   const float inv6 = 1.f / (6.f * descale);
+  const Lanes<D> me(tile_shift);
   for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
-    const int len = cache_len(a, b), count = token_count(a, b);
-    Place p[N];
-    uint4 w[N][2];
+    const int count = token_count(a, b), pos = cache_len(a, b) - count + me.t;
+    if (static_cast<int>(blockIdx.x) << tile_shift >= count) continue;
+    const bool live = me.t < count && pos >= 0;
+    const __nv_bfloat16* src =
+        (values ? a.v : a.k) + b * a.stride_b + me.t * a.stride_n + 8 * me.part;
+    const int row = pos & ((1 << a.page_shift) - 1);
+    int page = -1;
+    for (int base = 0; base < a.H; base += kAtOnce * me.step) {   // (all lanes: two share a scale)
+      uint4 w[kAtOnce];
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-      p[k] = place<D>(a, b, (static_cast<int64_t>(blockIdx.x) * N + k) * kFp4Threads + threadIdx.x,
-                      len, count);
-      if (p[k].live) {
-        const uint4* src = reinterpret_cast<const uint4*>(
-            (values ? a.v : a.k) + b * a.stride_b + p[k].h * a.stride_h + p[k].t * a.stride_n +
-            kFp4Block * p[k].blk);
-        w[k][0] = __ldcs(src);
-        w[k][1] = __ldcs(src + 1);
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int h = base + me.h + k * me.step;
+        w[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (live && h < a.H) w[k] = __ldcs(reinterpret_cast<const uint4*>(src + h * a.stride_h));
       }
-    }
+      if (live && base == 0) page = token_page(a, b, pos);
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-      if (p[k].page < 0) continue;
-      const uint32_t x[8] = {w[k][0].x, w[k][0].y, w[k][0].z, w[k][0].w,
-                             w[k][1].x, w[k][1].y, w[k][1].z, w[k][1].w};
-      uint32_t scale;
-      const uint2 codes = quantised(x, descale, inv6, &scale);
-      *reinterpret_cast<uint2*>(c.codes + p[k].page * c.code_page + p[k].h * c.code_head +
-                                p[k].row * (D / 2) + 8 * p[k].blk) = codes;
-      c.scales[p[k].page * c.scale_page + p[k].h * c.scale_head + p[k].row * (D / kFp4Block) +
-               p[k].blk] = static_cast<uint8_t>(scale);
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int h = base + me.h + k * me.step;
+        uint32_t scale;
+        const uint32_t codes = quantised(w[k], descale, inv6, &scale);
+        if (page < 0 || h >= a.H) continue;
+        *reinterpret_cast<uint32_t*>(c.codes + page * c.code_page + h * c.code_head +
+                                     row * (D / 2) + 4 * me.part) = codes;
+        if ((me.part & 1) == 0)
+          c.scales[page * c.scale_page + h * c.scale_head + row * (D / kFp4Block) + me.part / 2] =
+              static_cast<uint8_t>(scale);
+      }
     }
   }
 }
 
-template <int D, int N>
-__global__ void __launch_bounds__(kFp4Threads) fp4_load_kernel(const Fp4CopyArgs a) {
+template <int D>
+__global__ void __launch_bounds__(kFp4Threads) fp4_load_kernel(const Fp4CopyArgs a, int tile_shift) {
   grid_dep_wait();
   grid_dep_launch();
   const bool values = blockIdx.z != 0;
   const Fp4Cache& c = values ? a.cache.v : a.cache.k;
   const float descale = values ? a.cache.v_descale : a.cache.k_descale;
+  const Lanes<D> me(tile_shift);
   for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
-    const int len = cache_len(a, b), count = token_count(a, b);
-    Place p[N];
-    uint2 codes[N];
-    uint32_t scale[N];
+    const int count = token_count(a, b), pos = cache_len(a, b) - count + me.t;
+    if (me.t >= a.n) continue;
+    __nv_bfloat16* dst =
+        (values ? a.v : a.k) + b * a.stride_b + me.t * a.stride_n + 8 * me.part;
+    const int page = me.t < count && pos >= 0 ? token_page(a, b, pos) : -1;
+    const int row = pos & ((1 << a.page_shift) - 1);
+    for (int h0 = me.h; h0 < a.H; h0 += kAtOnce * me.step) {
+      uint32_t codes[kAtOnce], scale[kAtOnce];
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-      p[k] = place<D>(a, b, (static_cast<int64_t>(blockIdx.x) * N + k) * kFp4Threads + threadIdx.x,
-                      len, count);
-      codes[k] = make_uint2(0u, 0u);
-      scale[k] = 0;
-      if (p[k].page >= 0) {
-        codes[k] = __ldcs(reinterpret_cast<const uint2*>(
-            c.codes + p[k].page * c.code_page + p[k].h * c.code_head + p[k].row * (D / 2) +
-            8 * p[k].blk));
-        scale[k] = c.scales[p[k].page * c.scale_page + p[k].h * c.scale_head +
-                            p[k].row * (D / kFp4Block) + p[k].blk];
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int h = h0 + k * me.step;
+        codes[k] = scale[k] = 0;
+        if (page >= 0 && h < a.H) {
+          codes[k] = __ldcs(reinterpret_cast<const uint32_t*>(
+              c.codes + page * c.code_page + h * c.code_head + row * (D / 2) + 4 * me.part));
+          scale[k] = c.scales[page * c.scale_page + h * c.scale_head + row * (D / kFp4Block) +
+                              me.part / 2];
+        }
       }
-    }
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-      if (!p[k].valid) continue;
-      // (two roundings of 2^-24 before the one to bf16)
-      const float unit = e4m3_value(scale[k]) * descale;
-      const uint64_t unit2 = f2_pack(unit, unit);
-      uint32_t h[8], out[8];
-      e2m1_to_half(codes[k].x, h);
-      e2m1_to_half(codes[k].y, h + 4);
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int h = h0 + k * me.step;
+        if (h >= a.H) break;
+        // (two roundings of 2^-24 before the one to bf16)
+        const float unit = e4m3_value(scale[k]) * descale;
+        const uint64_t unit2 = f2_pack(unit, unit);
+        uint32_t x[4], out[4];
+        e2m1_to_half(codes[k], x);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-        float lo, hi;
-        f2_unpack(f2_mul(f2_pack(x.x, x.y), unit2), lo, hi);
-        out[i] = pack_bf16x2(lo, hi);
+        for (int i = 0; i < 4; ++i) {
+          const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x[i]));
+          float lo, hi;
+          f2_unpack(f2_mul(f2_pack(y.x, y.y), unit2), lo, hi);
+          out[i] = pack_bf16x2(lo, hi);
+        }
+        __stcs(reinterpret_cast<uint4*>(dst + h * a.stride_h),
+               make_uint4(out[0], out[1], out[2], out[3]));
       }
-      uint4* dst = reinterpret_cast<uint4*>((values ? a.v : a.k) + b * a.stride_b +
-                                            p[k].h * a.stride_h + p[k].t * a.stride_n +
-                                            kFp4Block * p[k].blk);
-      __stcs(dst, make_uint4(out[0], out[1], out[2], out[3]));
-      __stcs(dst + 1, make_uint4(out[4], out[5], out[6], out[7]));
     }
   }
 }
 
-// Four blocks a thread where that leaves enough CTAs: their loads are on the way
-// together.
-constexpr int kFp4Many = 4;
-
-int64_t items_of(const Fp4CopyArgs& a) {
-  return static_cast<int64_t>(a.H) * a.n * (a.d / kFp4Block);
+// Tokens of a CTA: as many as it has rows, fewer where there are fewer (its other
+// rows then take other heads).
+template <int D>
+int tile_of(const Fp4CopyArgs& a) {
+  int s = 0;
+  while ((1 << s) < a.n && (2 << s) <= Lanes<D>::kRows) ++s;
+  return s;
 }
 
-bool many(const Fp4CopyArgs& a) { return items_of(a) * a.B >= kFp4Many * kFp4Threads * 512ll; }
-
-dim3 copy_grid(const Fp4CopyArgs& a) {
-  const int64_t per = (many(a) ? kFp4Many : 1) * kFp4Threads;
-  return dim3(static_cast<unsigned>((items_of(a) + per - 1) / per),
-              static_cast<unsigned>(a.B < 65535 ? a.B : 65535), 2);
+template <int D>
+cudaError_t launch_copy(void (*kernel)(const Fp4CopyArgs, int), const Fp4CopyArgs& a,
+                        cudaStream_t s) {
+  const int shift = tile_of<D>(a);
+  const dim3 grid(static_cast<unsigned>((a.n + (1 << shift) - 1) >> shift),
+                  static_cast<unsigned>(a.B < 65535 ? a.B : 65535), 2);
+  return launch_pdl(kernel, grid, dim3(kFp4Threads), 0, s, a, shift);
 }
 
 }  // namespace
 
 cudaError_t launch_fp4_store(const Fp4CopyArgs& a, cudaStream_t s) {
-  auto kernel = many(a) ? (a.d == 64 ? fp4_store_kernel<64, kFp4Many> : fp4_store_kernel<128, kFp4Many>)
-                        : (a.d == 64 ? fp4_store_kernel<64, 1> : fp4_store_kernel<128, 1>);
-  return launch_pdl(kernel, copy_grid(a), dim3(kFp4Threads), 0, s, a);
+  return a.d == 64 ? launch_copy<64>(fp4_store_kernel<64>, a, s)
+                   : launch_copy<128>(fp4_store_kernel<128>, a, s);
 }
 
 cudaError_t launch_fp4_load(const Fp4CopyArgs& a, cudaStream_t s) {
-  auto kernel = many(a) ? (a.d == 64 ? fp4_load_kernel<64, kFp4Many> : fp4_load_kernel<128, kFp4Many>)
-                        : (a.d == 64 ? fp4_load_kernel<64, 1> : fp4_load_kernel<128, 1>);
-  return launch_pdl(kernel, copy_grid(a), dim3(kFp4Threads), 0, s, a);
+  return a.d == 64 ? launch_copy<64>(fp4_load_kernel<64>, a, s)
+                   : launch_copy<128>(fp4_load_kernel<128>, a, s);
 }
 
 }  // namespace attn

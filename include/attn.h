@@ -353,7 +353,7 @@ typedef struct attn_fp4 {
  * NaN makes its 16 columns NaN; infinities become the largest value.
  * Tokens whose position is negative are left out; an entry of the table outside
  * the cache is recorded (ATTN_ERR_PAGE) and its tokens are left out.  Fields of
- * p that are not named are ignored; H_kv * n < 2^31 / 8.  ws: 256 bytes. */
+ * p that are not named are ignored; n <= 2^30.  ws: 256 bytes. */
 attn_status attn_pages_store_fp4(const attn_params* p, const attn_pages* pages,
                                  const int32_t* counts, const void* k, const void* v,
                                  const attn_fp4* k_cache, const attn_fp4* v_cache, void* ws,
