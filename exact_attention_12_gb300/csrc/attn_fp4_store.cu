@@ -52,6 +52,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either 
   return r;
 }
 
+__device__ __forceinline__ uint32_t max_nan2(uint32_t a, uint32_t b) {   // of bf16 pairs
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 __device__ __forceinline__ float reciprocal(float x) {   // off by an ulp or so
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -117,15 +123,11 @@ __device__ __forceinline__ int token_page(const Fp4CopyArgs& a, int b, int pos) 
 __device__ __forceinline__ uint32_t quantised(const uint4& w, float descale, float inv6,
                                               uint32_t* scale) {
   const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-  uint64_t x[4];
-  float top = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float lo = __uint_as_float(v[i] << 16), hi = __uint_as_float(v[i] & 0xffff0000u);
-    top = max_nan(top, max_nan(fabsf(lo), fabsf(hi)));
-    x[i] = f2_pack(lo, hi);
-  }
-  top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  // |x| of two columns at once, NaN above all
+  uint32_t two = max_nan2(max_nan2(v[0] & 0x7fff7fffu, v[1] & 0x7fff7fffu),
+                          max_nan2(v[2] & 0x7fff7fffu, v[3] & 0x7fff7fffu));
+  two = max_nan2(two, __shfl_xor_sync(0xffffffffu, two, 1));
+  const float top = max_nan(__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u));
   *scale = 0x7fu;   // NaN
   if (top != top) return 0u;
   *scale = block_scale(top, descale, inv6);
@@ -136,23 +138,21 @@ __device__ __forceinline__ uint32_t quantised(const uint4& w, float descale, flo
   uint64_t low[4], high[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint64_t t = f2_mul(x[i], inv2);
+    const uint64_t t =
+        f2_mul(f2_pack(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xffff0000u)), inv2);
     low[i] = f2_mul(t, below);
     high[i] = f2_mul(t, above);
   }
   uint32_t codes = e2m1_of(low);
-  const uint32_t other = e2m1_of(high);
-  if (codes != other) {   // a value next to a border
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t l = (codes >> (4 * i)) & 15u, g = (other >> (4 * i)) & 15u;
-      if (l == g) continue;
-      float lo, hi;
-      f2_unpack(x[i >> 1], lo, hi);
-      const uint32_t m = nearer(l & 7u, g & 7u, fabsf(i & 1 ? hi : lo), unit, descale,
-                                [](uint32_t c) { return e2m1_value(c); });
-      codes = (codes & ~(15u << (4 * i))) | ((l & 8u) | m) << (4 * i);
-    }
+  for (uint32_t differ = codes ^ e2m1_of(high); differ != 0;) {   // values next to a border
+    const int i = (__ffs(differ) - 1) >> 2, s = 4 * i;
+    const uint32_t l = (codes >> s) & 15u, g = l ^ ((differ >> s) & 15u);
+    const uint32_t word = i & 4 ? (i & 2 ? v[3] : v[2]) : (i & 2 ? v[1] : v[0]);
+    const float x = __uint_as_float((i & 1 ? word : word << 16) & 0x7fff0000u);
+    const uint32_t m =
+        nearer(l & 7u, g & 7u, x, unit, descale, [](uint32_t c) { return e2m1_value(c); });
+    codes = (codes & ~(15u << s)) | ((l & 8u) | m) << s;
+    differ &= ~(15u << s);
   }
   return codes;
 }
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kFp4Threads) fp4_store_kernel(const Fp4CopyArg
     const __nv_bfloat16* src =
         (values ? a.v : a.k) + b * a.stride_b + me.t * a.stride_n + 8 * me.part;
     const int row = pos & ((1 << a.page_shift) - 1);
-    int page = -1;
+    uint8_t *codes_to = nullptr, *scales_to = nullptr;
     for (int base = 0; base < a.H; base += kAtOnce * me.step) {   // (all lanes: two share a scale)
       uint4 w[kAtOnce];
 #pragma unroll
@@ -184,18 +184,21 @@ __global__ void __launch_bounds__(kFp4Threads) fp4_store_kernel(const Fp4CopyArg
         w[k] = make_uint4(0u, 0u, 0u, 0u);
         if (live && h < a.H) w[k] = __ldcs(reinterpret_cast<const uint4*>(src + h * a.stride_h));
       }
-      if (live && base == 0) page = token_page(a, b, pos);
+      if (live && base == 0) {
+        const int page = token_page(a, b, pos);
+        if (page >= 0) {
+          codes_to = c.codes + page * c.code_page + row * (D / 2) + 4 * me.part;
+          scales_to = c.scales + page * c.scale_page + row * (D / kFp4Block) + me.part / 2;
+        }
+      }
 #pragma unroll
       for (int k = 0; k < kAtOnce; ++k) {
         const int h = base + me.h + k * me.step;
         uint32_t scale;
         const uint32_t codes = quantised(w[k], descale, inv6, &scale);
-        if (page < 0 || h >= a.H) continue;
-        *reinterpret_cast<uint32_t*>(c.codes + page * c.code_page + h * c.code_head +
-                                     row * (D / 2) + 4 * me.part) = codes;
-        if ((me.part & 1) == 0)
-          c.scales[page * c.scale_page + h * c.scale_head + row * (D / kFp4Block) + me.part / 2] =
-              static_cast<uint8_t>(scale);
+        if (codes_to == nullptr || h >= a.H) continue;
+        *reinterpret_cast<uint32_t*>(codes_to + h * c.code_head) = codes;
+        if ((me.part & 1) == 0) scales_to[h * c.scale_head] = static_cast<uint8_t>(scale);
       }
     }
   }
@@ -216,6 +219,9 @@ __global__ void __launch_bounds__(kFp4Threads) fp4_load_kernel(const Fp4CopyArgs
         (values ? a.v : a.k) + b * a.stride_b + me.t * a.stride_n + 8 * me.part;
     const int page = me.t < count && pos >= 0 ? token_page(a, b, pos) : -1;
     const int row = pos & ((1 << a.page_shift) - 1);
+    const uint8_t* codes_at = c.codes + max(page, 0) * c.code_page + row * (D / 2) + 4 * me.part;
+    const uint8_t* scales_at =
+        c.scales + max(page, 0) * c.scale_page + row * (D / kFp4Block) + me.part / 2;
     for (int h0 = me.h; h0 < a.H; h0 += kAtOnce * me.step) {
       uint32_t codes[kAtOnce], scale[kAtOnce];
 #pragma unroll
@@ -223,10 +229,8 @@ __global__ void __launch_bounds__(kFp4Threads) fp4_load_kernel(const Fp4CopyArgs
         const int h = h0 + k * me.step;
         codes[k] = scale[k] = 0;
         if (page >= 0 && h < a.H) {
-          codes[k] = __ldcs(reinterpret_cast<const uint32_t*>(
-              c.codes + page * c.code_page + h * c.code_head + row * (D / 2) + 4 * me.part));
-          scale[k] = c.scales[page * c.scale_page + h * c.scale_head + row * (D / kFp4Block) +
-                              me.part / 2];
+          codes[k] = __ldcs(reinterpret_cast<const uint32_t*>(codes_at + h * c.code_head));
+          scale[k] = scales_at[h * c.scale_head];
         }
       }
 #pragma unroll
