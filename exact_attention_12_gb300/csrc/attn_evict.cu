@@ -73,6 +73,7 @@ struct EvictArgs {
   int32_t* bound;            // [n][heads][chunks + 1]: kept keys before slot c T
   int chunk, chunk_shift;    // T, a power of two
   int chunks;                // of a row of the table
+  int finish_parts;          // CTAs of the last kernel per head and entry
   int cluster;               // CTAs per (sequence, head) of the first kernel
   int n_pools;
   RowPool pools[kMaxPools];
@@ -95,50 +96,46 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// Entry i of the list: whether its sequence can be shrunk, from `old` to `len`
-// keys (old <= len: nothing to do).  The whole CTA.
-__device__ bool check_entry(const EvictArgs& a, int i, int* old_out, int* len_out) {
-  const int s = a.seqs[i], len = a.new_lens[i];
-  bool ok = in_range(s, a.rows) && len >= 0;
-  const int old = ok ? a.lens[s] : 0;
-  const int64_t cap = static_cast<int64_t>(a.max_pages) << a.page_shift;
-  ok = ok && old >= 0 && old <= cap;
-  if (ok) {
-    for (int j = threadIdx.x; j < i; j += kSelectThreads) ok = ok && a.seqs[j] != s;
-    const int size = 1 << a.page_shift;
-    const int held = (old + size - 1) >> a.page_shift;
-    const int stay = len < old ? (len + size - 1) >> a.page_shift : 0;   // pages that are written
-    const int32_t* row = a.table + s * a.table_stride;
-    for (int j = threadIdx.x; j < held; j += kSelectThreads) {
-      const int pg = row[j];
-      ok = ok && in_range(pg, a.num_pages);
-      if (ok) {
-        const int refs = a.refs[pg];
-        ok = j < stay ? refs == 1 : refs > 0;
-      }
+// Entry i of the list: its sequence's length, and the new one; whether they hold
+// together.  (Every thread by itself.)
+__device__ __forceinline__ bool entry_lengths(const EvictArgs& a, int i, int* old, int* len) {
+  const int s = a.seqs[i], want = a.new_lens[i];
+  bool ok = in_range(s, a.rows) && want >= 0;
+  *old = ok ? a.lens[s] : 0;
+  ok = ok && *old >= 0 && *old <= static_cast<int64_t>(a.max_pages) << a.page_shift;
+  if (!ok) *old = 0;
+  *len = min(want, *old);
+  return ok;
+}
+
+// Whether the sequence is named for the first time, and its pages are what they
+// should be.  The whole CTA.
+__device__ bool check_pages(const EvictArgs& a, int i, int old, int len) {
+  const int s = a.seqs[i];
+  bool ok = true;
+  for (int j = threadIdx.x; j < i; j += kSelectThreads) ok = ok && a.seqs[j] != s;
+  const int size = 1 << a.page_shift;
+  const int held = (old + size - 1) >> a.page_shift;
+  const int stay = len < old ? (len + size - 1) >> a.page_shift : 0;   // pages that are written
+  const int32_t* row = a.table + s * a.table_stride;
+  for (int j = threadIdx.x; j < held; j += kSelectThreads) {
+    const int pg = row[j];
+    ok = ok && in_range(pg, a.num_pages);
+    if (ok) {
+      const int refs = a.refs[pg];
+      ok = j < stay ? refs == 1 : refs > 0;
     }
   }
-  *old_out = old;
-  *len_out = min(len, old);
   return __syncthreads_and(ok);
 }
 
 struct SelectShared {
   alignas(16) uint32_t bins[3][kBins];
-  uint32_t warp_sum[kSelectWarps + 1];
+  uint32_t sums[3][kBins / 32];
   uint32_t digit, left;              // the round's digit; how many are still to choose in it
   uint32_t above[kSelectWarps], equal[kSelectWarps];
   uint32_t cta_above, cta_equal;     // of this CTA's part, for the others
 };
-
-__device__ __forceinline__ uint4 cluster_ld_u4(uint32_t addr) {
-  uint4 x;
-  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-               : "r"(addr)
-               : "memory");
-  return x;
-}
 
 __device__ __forceinline__ uint32_t cluster_ld_u32(uint32_t addr) {
   uint32_t x;
@@ -157,7 +154,19 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const EvictAr
   const int item = blockIdx.x / C, i = item / a.heads, h = item - i * a.heads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int old, len;
-  const bool ok = check_entry(a, i, &old, &len);
+  bool ok = entry_lengths(a, i, &old, &len);
+  // this CTA's part of the slots: a multiple of 32 per warp
+  const int per_warp = (old + C * kSelectThreads - 1) / (C * kSelectThreads) * 32;
+  const int lo = rank * per_warp * kSelectWarps;
+  const int part = max(0, min(per_warp * kSelectWarps, old - lo));
+  const float* w = ok ? a.weights + a.seqs[i] * a.weight_row + h * a.weight_head : nullptr;
+  auto key_at = [&](int j) { return CACHED ? cache[j] : order_key(w[lo + j]); };
+  for (int k = threadIdx.x; k < 3 * kBins; k += kSelectThreads) (&sh.bins[0][0])[k] = 0;
+  if constexpr (CACHED)
+    if (len < old)
+#pragma unroll 4
+      for (int j = threadIdx.x; j < part; j += kSelectThreads) cache[j] = order_key(w[lo + j]);
+  ok = ok && check_pages(a, i, old, len);   // (and the CTA's keys are there)
   const bool first = h == 0 && rank == 0 && threadIdx.x == 0;
   if (first && !ok) report(a.status, kStatusPage);
   if (first) {
@@ -177,16 +186,6 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const EvictAr
   for (int c = me; c < chunks; c += all) read[c] = 0;
   const int r = min(a.recent, len), m = old - r;   // slots from m on stay
   uint32_t left = static_cast<uint32_t>(len - r);  // to be chosen of the m
-  const float* w = a.weights + a.seqs[i] * a.weight_row + h * a.weight_head;
-  // this CTA's part of the slots: a multiple of 32 per warp
-  const int per_warp = (old + C * kSelectThreads - 1) / (C * kSelectThreads) * 32;
-  const int lo = rank * per_warp * kSelectWarps;
-  const int part = max(0, min(per_warp * kSelectWarps, old - lo));
-  auto key_at = [&](int j) { return CACHED ? cache[j] : order_key(w[lo + j]); };
-  for (int k = threadIdx.x; k < 3 * kBins; k += kSelectThreads) (&sh.bins[0][0])[k] = 0;
-  if constexpr (CACHED)
-    for (int j = threadIdx.x; j < part; j += kSelectThreads) cache[j] = order_key(w[lo + j]);
-  __syncthreads();
 
   // the left-th largest key of slots [0, m): digit by digit from the top
   const int mine = max(0, min(part, m - lo));
@@ -201,45 +200,52 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const EvictAr
         if (known == 32 || (k >> known) == (prefix >> known))
           atomicAdd(&sh.bins[round][(k >> shift) & ((1u << bits) - 1u)], 1u);
       }
+      __syncthreads();
+      {   // sums of 32 bins, which are all that most of the search needs
+        const uint4 x = *reinterpret_cast<const uint4*>(&sh.bins[round][4 * threadIdx.x]);
+        uint32_t sum = x.x + x.y + x.z + x.w;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if ((lane & 7) == 0) sh.sums[round][threadIdx.x >> 3] = sum;
+      }
       if (C > 1) cluster_sync();
       else __syncthreads();
-      // thread x has the bins 2047 - 4 x, ..., 2044 - 4 x, from the top
-      const int low = kBins - 4 - 4 * static_cast<int>(threadIdx.x);
-      uint32_t n4[4] = {0, 0, 0, 0};
-      uint4 got[kMaxCluster];
+      if (warp == 0) {
+        // over the cluster: lane l has the sums 63 - 2 l and 62 - 2 l, then bin 31 - l of
+        // the run that holds the digit
+        auto over_cluster = [&](const uint32_t* at) {
+          uint32_t got[kMaxCluster], n = 0;
 #pragma unroll
-      for (int q = 0; q < kMaxCluster; ++q) {   // (all on their way before the first is used)
-        got[q] = make_uint4(0, 0, 0, 0);
-        if (q < C)
-          got[q] = C > 1 ? cluster_ld_u4(cluster_addr(&sh.bins[round][low], q))
-                         : *reinterpret_cast<const uint4*>(&sh.bins[round][low]);
-      }
+          for (int q = 0; q < kMaxCluster; ++q)   // (all on their way before the first is used)
+            got[q] = q >= C ? 0u : C > 1 ? cluster_ld_u32(cluster_addr(at, q)) : *at;
 #pragma unroll
-      for (int q = 0; q < kMaxCluster; ++q) {
-        n4[0] += got[q].w;
-        n4[1] += got[q].z;
-        n4[2] += got[q].y;
-        n4[3] += got[q].x;
-      }
-      const uint32_t own = n4[0] + n4[1] + n4[2] + n4[3];
-      uint32_t inc = own;
+          for (int q = 0; q < kMaxCluster; ++q) n += got[q];
+          return n;
+        };
+        auto inclusive = [&](uint32_t x) {
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-      }
-      if (lane == 31) sh.warp_sum[warp] = inc;
-      __syncthreads();
-      uint32_t before = 0;
-#pragma unroll
-      for (int q = 0; q < kSelectWarps; ++q) before += q < warp ? sh.warp_sum[q] : 0u;
-      const uint32_t end = before + inc;
-      uint32_t start = end - own;
-      if (start < left && left <= end) {   // one thread
-        int q = 0;
-        while (q < 3 && left > start + n4[q]) start += n4[q++];
-        sh.digit = static_cast<uint32_t>(low + 3 - q);
-        sh.left = left - start;
+          for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+          }
+          return x;
+        };
+        const uint32_t s0 = over_cluster(&sh.sums[round][63 - 2 * lane]);
+        const uint32_t s1 = over_cluster(&sh.sums[round][62 - 2 * lane]);
+        uint32_t end = inclusive(s0 + s1);
+        bool here = end - s0 - s1 < left && left <= end;
+        int from = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+        const bool second = left > end - s1;
+        const int run = __shfl_sync(0xffffffffu, second ? 62 - 2 * lane : 63 - 2 * lane, from);
+        const uint32_t rest = __shfl_sync(
+            0xffffffffu, left - (end - s0 - s1) - (second ? s0 : 0u), from);
+        const uint32_t n = over_cluster(&sh.bins[round][32 * run + 31 - lane]);
+        end = inclusive(n);
+        here = end - n < rest && rest <= end;
+        if (here) {   // one lane
+          sh.digit = static_cast<uint32_t>(32 * run + 31 - lane);
+          sh.left = rest - (end - n);
+        }
       }
       __syncthreads();
       prefix |= sh.digit << shift;
@@ -330,8 +336,10 @@ struct ChunkKeys {
   int row[kMaxChunk];        // in the old page
   float weight[kMaxChunk];
 };
+constexpr int kMoveEntries = 256;   // of the list that are kept at hand
 struct MoveShared {
   ChunkKeys keys[2];
+  int2 entries[kMoveEntries];       // new length (0: nothing to do), sequence
   int ticket, give_up;
 };
 
@@ -341,9 +349,13 @@ __global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const __grid_cons
   grid_dep_wait();
   grid_dep_launch();
   const int T = a.chunk;
+  auto entry_of = [&](int i) { return make_int2(a.old_len[i] < 0 ? 0 : a.new_len[i], a.seqs[i]); };
   int most = 0;
-  for (int i = threadIdx.x; i < a.n; i += kMoveThreads)
-    if (a.old_len[i] >= 0) most = max(most, (a.new_len[i] + T - 1) >> a.chunk_shift);
+  for (int i = threadIdx.x; i < a.n; i += kMoveThreads) {
+    const int2 entry = entry_of(i);
+    if (i < kMoveEntries) sh.entries[i] = entry;
+    most = max(most, (entry.x + T - 1) >> a.chunk_shift);
+  }
   if (threadIdx.x == 0) sh.ticket = sh.give_up = 0;
   __syncthreads();
   atomicMax(&sh.ticket, most);
@@ -366,22 +378,15 @@ __global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const __grid_cons
     k.item = ticket - k.c * items;
     const int i = k.item / a.heads;
     k.h = k.item - i * a.heads;
-    const int len = a.old_len[i] < 0 ? 0 : a.new_len[i];
+    const int2 entry = i < kMoveEntries ? sh.entries[i] : entry_of(i);
     k.first = k.c * T;
-    const int count = min(T, len - k.first);
+    const int count = min(T, entry.x - k.first);
     if (count <= 0) return k;
     const int32_t* slots = a.slots + static_cast<int64_t>(k.item) * a.width + k.first;
     const int32_t* bound = a.bound + static_cast<int64_t>(k.item) * (a.chunks + 1) + k.c;
-    const int seq = a.seqs[i], end = slots[count - 1], b0 = bound[0], b1 = bound[1];
-    if (end == k.first + count - 1) {
-      if (threadIdx.x == 0) a.read[static_cast<int64_t>(k.item) * a.chunks + k.c] = 1;
-      return k;
-    }
-    k.count = count;
-    k.from = b0 >> a.chunk_shift;
-    k.until = min((b1 + T - 1) >> a.chunk_shift, k.c);
-    const int32_t* table = a.table + seq * a.table_stride;
-    k.w = a.weights + seq * a.weight_row + k.h * a.weight_head;
+    const int b0 = bound[0], b1 = bound[1];
+    const int32_t* table = a.table + entry.y * a.table_stride;
+    k.w = a.weights + entry.y * a.weight_row + k.h * a.weight_head;
     ChunkKeys& to = sh.keys[buf];
     for (int j = threadIdx.x; j < count; j += kMoveThreads) {
       const int from = slots[j];
@@ -390,6 +395,13 @@ __global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const __grid_cons
       to.row[j] = from & ((1 << a.page_shift) - 1);
       to.weight[j] = k.w[from];
     }
+    if (b1 == k.first + T) {   // every key so far is kept: it stays
+      if (threadIdx.x == 0) a.read[static_cast<int64_t>(k.item) * a.chunks + k.c] = 1;
+      return k;
+    }
+    k.count = count;
+    k.from = b0 >> a.chunk_shift;
+    k.until = min((b1 + T - 1) >> a.chunk_shift, k.c);
     return k;
   };
   auto row_of = [](const RowPool& pool, int e, int per) {
@@ -462,17 +474,21 @@ __global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const __grid_cons
   }
 }
 
-// CTA (head, entry): the weights behind the new length; head 0 also the pages.
+// CTA (head and part, entry): the weights behind the new length; the first also the
+// pages.
 __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const EvictArgs a) {
   grid_dep_wait();
   grid_dep_launch();
   for (int i = blockIdx.y; i < a.n; i += gridDim.y) {
-    const int old = a.old_len[i], len = a.new_len[i], h = blockIdx.x;
+    const int old = a.old_len[i], len = a.new_len[i], h = blockIdx.x / a.finish_parts;
     if (old < 0) continue;
     const int seq = a.seqs[i];
     float* w = a.weights + seq * a.weight_row + h * a.weight_head;
-    for (int j = len + static_cast<int>(threadIdx.x); j < old; j += kFinishThreads) w[j] = 0.f;
-    if (h > 0) continue;
+    const int part = blockIdx.x - h * a.finish_parts;
+    for (int j = len + part * kFinishThreads + static_cast<int>(threadIdx.x); j < old;
+         j += a.finish_parts * kFinishThreads)
+      w[j] = 0.f;
+    if (blockIdx.x > 0) continue;
     const int size = 1 << a.page_shift;
     int32_t* row = a.table + seq * a.table_stride;
     const int held = (old + size - 1) >> a.page_shift;
@@ -696,8 +712,14 @@ attn_status attn_pages_evict(const attn_page_table* t, const attn_rows* pools, i
   cudaError_t e = part <= 160 * 1024 ? launch_select<true>(a, static_cast<size_t>(part), s)
                                      : launch_select<false>(a, 0, s);
   if (e == cudaSuccess && cap > 0) e = launch_move(a, s);
+  a.finish_parts = 1;   // a few thousand weights each, while the GPU has room
+  while (a.finish_parts < 64 && cap > 4096ll * a.finish_parts &&
+         static_cast<int64_t>(n) * heads * a.finish_parts < 8ll * multiprocessors())
+    a.finish_parts *= 2;
   if (e == cudaSuccess)
-    e = launch_pdl(finish_kernel, dim3(static_cast<unsigned>(heads), static_cast<unsigned>(n < 65535 ? n : 65535)),
+    e = launch_pdl(finish_kernel,
+                   dim3(static_cast<unsigned>(heads * a.finish_parts),
+                        static_cast<unsigned>(n < 65535 ? n : 65535)),
                    dim3(kFinishThreads), 0, s, a);
   if (e == cudaSuccess) return ATTN_OK;
   char msg[256];
