@@ -10,14 +10,13 @@
 // Bound: HBM for the few rows of a decode step, 2 d + 8 bytes a key (9 d / 16 + 8
 // in 4 bits); for the hundred rows of an observation window the exponentials,
 // 16 a clock and SM, and the products as much.
-//   * S^T = K Q^T by 16 x 8 x 16 warp MMAs, 16 keys by 8 rows: K's fragments come
-//     straight from global memory into registers (the sum over d may go in
-//     any order, so lane (g, t) takes 16-byte pieces of keys g and g + 8), the next
-//     group's while this one is worked on, and stay there for all rows;
+//   * 16 x 8 x 16 warp MMAs whose fragments of K come straight from global memory
+//     into registers (the sum over d may go in any order, so lane (g, t) takes
+//     16-byte pieces of its keys) and stay there for all rows;
 //   * Q's fragments lie in shared memory in the order in which a warp reads them,
 //     up to 256 rows at a time;
-//   * the sum over a key's rows is each lane's own until the last row, then
-//     two shuffles.
+//   * the sum over a key's rows is each lane's own until the last row, then a few
+//     shuffles.
 // Keys in 4 bits are unpacked as in attn_fp4.cu (exactly, to fp16).
 #include "attn_fp4.cuh"
 
@@ -38,29 +37,135 @@ struct RowInfo {
 
 __device__ __forceinline__ void mma16816_bf16(float* c, const uint32_t* a, uint32_t b0,
                                               uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// What a lane holds of 16 keys: its pieces of keys g and g + 8.
+// What lane (g, t) holds of a key: a quarter of its row.
 template <int D, bool PACKED>
-struct KeyPieces {
-  static constexpr int kWords = PACKED ? D / 32 : D / 8;
-  uint32_t w[2][kWords];
-  uint32_t scale[PACKED ? 2 : 1];
+struct KeyPart {
+  uint32_t w[PACKED ? D / 32 : D / 8];
+  uint32_t scale;
 };
 
+// Zeros where there is no page.
 template <int D, bool PACKED>
+__device__ __forceinline__ void load_part(const PagedArgs& a, const WeightArgs& f, int64_t page,
+                                          int head, int row, int t, KeyPart<D, PACKED>& x) {
+  const bool there = page < a.num_pages;
+  if constexpr (PACKED) {
+    const uint8_t* from = f.cache.codes + page * f.cache.code_page + head * f.cache.code_head +
+                          row * (D / 2) + t * (D / 8);
+    const uint8_t* unit = f.cache.scales + page * f.cache.scale_page + head * f.cache.scale_head +
+                          row * (D / kFp4Block) + t * (D / 64);
+    if constexpr (D == 128) {
+      const uint4 y =
+          there ? __ldcs(reinterpret_cast<const uint4*>(from)) : make_uint4(0u, 0u, 0u, 0u);
+      x.w[0] = y.x;
+      x.w[1] = y.y;
+      x.w[2] = y.z;
+      x.w[3] = y.w;
+      x.scale = there ? *reinterpret_cast<const uint16_t*>(unit) : 0u;
+    } else {
+      const uint2 y = there ? __ldcs(reinterpret_cast<const uint2*>(from)) : make_uint2(0u, 0u);
+      x.w[0] = y.x;
+      x.w[1] = y.y;
+      x.scale = there ? *unit * 0x0101u : 0u;
+    }
+  } else {
+    // piece k: 16 bytes, 8 columns, the four lanes' side by side
+    const __nv_bfloat16* from =
+        f.k + page * f.stride_page + head * f.stride_head + row * f.stride_row + 8 * t;
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) {
+      const uint4 y = there ? __ldcs(reinterpret_cast<const uint4*>(from + 32 * k))
+                            : make_uint4(0u, 0u, 0u, 0u);
+      x.w[4 * k] = y.x;
+      x.w[4 * k + 1] = y.y;
+      x.w[4 * k + 2] = y.z;
+      x.w[4 * k + 3] = y.w;
+    }
+  }
+}
+
+// The part as MMA operands: step s takes its columns 4 s ... 4 s + 3, two registers.
+template <int D, bool PACKED>
+__device__ __forceinline__ void operands(const KeyPart<D, PACKED>& x, uint32_t (*b)[2]) {
+  if constexpr (PACKED) {
+    const uint32_t s = e4m3_to_half(x.scale);
+    const uint32_t unit[2] = {__byte_perm(s, 0, 0x1010), __byte_perm(s, 0, 0x3232)};
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+      uint32_t y[4];
+      e2m1_to_half(x.w[j], y);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) b[2 * j + k / 2][k & 1] = mul_half2(y[k], unit[j / 2]);
+    }
+  } else {
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+      b[s][0] = x.w[2 * s];
+      b[s][1] = x.w[2 * s + 1];
+    }
+  }
+}
+
+// The quarter of a row of Q that goes with it, and what turns a score into log2
+// units.
+template <int D, bool PACKED>
+__device__ __forceinline__ float load_query(const PagedArgs& a, const WeightArgs& f, int b, int at,
+                                            bool live, int t, uint32_t* w) {
+  const int h = at / a.n_q, qt = at - h * a.n_q;
+  const __nv_bfloat16* qr =
+      a.q + b * a.stride_b + h * a.stride_h + static_cast<int64_t>(qt) * a.stride_n;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    const uint4 y = live ? *reinterpret_cast<const uint4*>(
+                               qr + (PACKED ? t * (D / 4) + 8 * i : 32 * i + 8 * t))
+                         : make_uint4(0u, 0u, 0u, 0u);
+    w[4 * i] = y.x;
+    w[4 * i + 1] = y.y;
+    w[4 * i + 2] = y.z;
+    w[4 * i + 3] = y.w;
+  }
+  if constexpr (PACKED) {
+    int e = 0;
+    half_rows<D / 8>(w, &e);
+    return score_factor(a.scale_log2 * f.k_descale, e);
+  }
+  return a.scale_log2;
+}
+
+__device__ __forceinline__ RowInfo row_info(const PagedArgs& a, const WeightArgs& f, int b, int len,
+                                            int at, bool live, float c2) {
+  const float L = live ? f.lse[static_cast<int64_t>(b) * a.all_rows + at] : -INFINITY;
+  RowInfo info;
+  info.c2 = c2;
+  info.l2 = L == -INFINITY ? INFINITY : L * kLog2Of;
+  info.lim = L == -INFINITY ? 0 : (a.causal ? min(len, len - a.n_q + at % a.n_q + 1) : len);
+  info.pad = 0;
+  return info;
+}
+
+// MANY: enough rows that the products take longer than the keys' way here.
+//   few rows    16 keys by 8 rows an MMA, no lane idle up to 8 rows; the next
+//               keys are on their way meanwhile
+//   many rows   16 rows by 8 keys: the keys' fragments are then the registers as
+//               they were loaded (as the other operand every use put them together
+//               anew: 161 instructions for 32 keys by 8 rows, now 95); 32 keys at
+//               a time share what is read of Q
+template <int D, bool PACKED, bool MANY>
 __global__ void __launch_bounds__(kWeightThreads, 2)
     key_weights_kernel(const PagedArgs a, const WeightArgs f) {
-  constexpr int kSteps = D / 16;
-  constexpr int G = PACKED ? 2 : 1;   // groups of 16 keys that are loaded together
+  constexpr int kSteps = D / 16, kWords = D / 8;
+  constexpr int kBlock = MANY ? 16 : 8;            // query rows of an MMA
+  constexpr int kParts = MANY || PACKED ? 4 : 2;   // keys of a lane at a time, 8 apart
   extern __shared__ __align__(16) uint8_t smem[];
-  RowInfo* rows = reinterpret_cast<RowInfo*>(smem);                        // [f.pass_rows]
-  uint2* qf = reinterpret_cast<uint2*>(smem + f.pass_rows * sizeof(RowInfo));   // [rows/8][kSteps][32]
+  RowInfo* rows = reinterpret_cast<RowInfo*>(smem);       // [f.pass_rows]
+  uint8_t* frag = smem + f.pass_rows * sizeof(RowInfo);   // Q: [rows / kBlock][kSteps][32]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   grid_dep_wait();
@@ -81,193 +186,170 @@ __global__ void __launch_bounds__(kWeightThreads, 2)
                        : checked_page(row[(key >> a.page_shift) + 1], a.num_pages, a.status);
     }
   };
-  // 16 keys (group v of the warp's: half v % 2 of tile v / 2); zeros where no page is
-  auto load = [&](const PagedPiece& p, int v, KeyPieces<D, PACKED>& x) {
-    const int u = v >> 1, half = v & 1;
+  // the warp's keys from 8 v on (part v % 4 of its tile v / 4)
+  auto load = [&](const PagedPiece& p, int v, KeyPart<D, PACKED>* x) {
+    const int u = v >> 2;
     const int pg0 = __shfl_sync(0xffffffffu, page_of[0], u & 31);
     const int pg1 = __shfl_sync(0xffffffffu, page_of[1], u & 31);
-    const int64_t page = small_pages && half ? pg1 : pg0;
-    const bool there = page < a.num_pages;
-    const int row = ((p.t0 + warp + kWeightWarps * u) * kWeightKeys + 16 * half) &
-                    ((1 << a.page_shift) - 1);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = row + g + 8 * i;
-      if constexpr (PACKED) {
-        const uint8_t* from = f.cache.codes + page * f.cache.code_page +
-                              p.h * f.cache.code_head + r * (D / 2) + t * (D / 8);
-        const uint8_t* unit = f.cache.scales + page * f.cache.scale_page +
-                              p.h * f.cache.scale_head + r * (D / kFp4Block) + t * (D / 64);
-        if constexpr (D == 128) {
-          const uint4 y = there ? __ldcs(reinterpret_cast<const uint4*>(from))
-                                : make_uint4(0u, 0u, 0u, 0u);
-          x.w[i][0] = y.x;
-          x.w[i][1] = y.y;
-          x.w[i][2] = y.z;
-          x.w[i][3] = y.w;
-          x.scale[i] = there ? *reinterpret_cast<const uint16_t*>(unit) : 0u;
-        } else {
-          const uint2 y = there ? __ldcs(reinterpret_cast<const uint2*>(from)) : make_uint2(0u, 0u);
-          x.w[i][0] = y.x;
-          x.w[i][1] = y.y;
-          x.scale[i] = there ? *unit * 0x0101u : 0u;
-        }
-      } else {
-        // piece k of a row: 16 bytes, 8 columns, the four lanes' side by side
-        const __nv_bfloat16* from = f.k + page * f.stride_page + p.h * f.stride_head +
-                                    r * f.stride_row + 8 * t;
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
-          const uint4 y = there ? __ldcs(reinterpret_cast<const uint4*>(from + 32 * k))
-                                : make_uint4(0u, 0u, 0u, 0u);
-          x.w[i][4 * k] = y.x;
-          x.w[i][4 * k + 1] = y.y;
-          x.w[i][4 * k + 2] = y.z;
-          x.w[i][4 * k + 3] = y.w;
-        }
-      }
-    }
-  };
-  // A fragments: step s takes columns 4 s ... 4 s + 3 of a lane's pieces
-  auto fragments = [&](const KeyPieces<D, PACKED>& x, uint32_t (*ka)[4]) {
-    if constexpr (PACKED) {
-      uint32_t unit[2][2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t s = e4m3_to_half(x.scale[i]);
-        unit[i][0] = __byte_perm(s, 0, 0x1010);
-        unit[i][1] = __byte_perm(s, 0, 0x3232);
-      }
-#pragma unroll
-      for (int j = 0; j < KeyPieces<D, PACKED>::kWords; ++j)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t y[4];
-          e2m1_to_half(x.w[i][j], y);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            ka[2 * j + k / 2][i + 2 * (k & 1)] = mul_half2(y[k], unit[i][j / 2]);
-        }
-    } else {
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        ka[s][0] = x.w[0][2 * s];
-        ka[s][1] = x.w[1][2 * s];
-        ka[s][2] = x.w[0][2 * s + 1];
-        ka[s][3] = x.w[1][2 * s + 1];
-      }
+    for (int i = 0; i < kParts; ++i) {
+      const int part = (v & 3) + i;
+      const int row = ((p.t0 + warp + kWeightWarps * u) * kWeightKeys + 8 * part) &
+                      ((1 << a.page_shift) - 1);
+      load_part<D, PACKED>(a, f, small_pages && part >= 2 ? pg1 : pg0, p.h, row + g, t, x[i]);
     }
   };
 
   for (PagedPiece p = paged_piece<kWeightKeys, kWeightOverhead>(a, share, share.b, 0, share.s);
        p.valid; p = paged_next<kWeightKeys, kWeightOverhead>(a, share, p)) {
     const int tiles = p.t1 - p.t0 - warp;
-    const int nu = tiles > 0 ? (tiles + kWeightWarps - 1) / kWeightWarps : 0;
+    const int nv = tiles > 0 ? (tiles + kWeightWarps - 1) / kWeightWarps * 4 : 0;
     for (int r0 = 0; r0 < a.head_rows; r0 += f.pass_rows) {   // (one pass but for very many rows)
-      const int nrows = min(a.head_rows - r0, f.pass_rows), blocks = (nrows + 7) / 8;
+      const int nrows = min(a.head_rows - r0, f.pass_rows), blocks = (nrows + kBlock - 1) / kBlock;
       __syncthreads();   // the rows before are no longer in use
       for (int n = warp; n < blocks; n += kWeightWarps) {
-        const int r = 8 * n + g, at = p.h * a.head_rows + r0 + r;
-        const bool live = r < nrows;
-        const int h = at / a.n_q, qt = at - h * a.n_q;
-        const __nv_bfloat16* qr =
-            a.q + p.b * a.stride_b + h * a.stride_h + static_cast<int64_t>(qt) * a.stride_n;
-        uint32_t w[D / 8];
+        uint32_t w[kBlock / 8][kWords];
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const uint4 y = live ? *reinterpret_cast<const uint4*>(
-                                     qr + (PACKED ? t * (D / 4) + 8 * i : 32 * i + 8 * t))
-                               : make_uint4(0u, 0u, 0u, 0u);
-          w[4 * i] = y.x;
-          w[4 * i + 1] = y.y;
-          w[4 * i + 2] = y.z;
-          w[4 * i + 3] = y.w;
-        }
-        float c2 = a.scale_log2;
-        if constexpr (PACKED) {
-          int e = 0;
-          half_rows<D / 8>(w, &e);
-          c2 = score_factor(a.scale_log2 * f.k_descale, e);
+        for (int i = 0; i < kBlock / 8; ++i) {
+          const int r = kBlock * n + 8 * i + g, at = p.h * a.head_rows + r0 + r;
+          const bool live = r < nrows;
+          const float c2 = load_query<D, PACKED>(a, f, p.b, at, live, t, w[i]);
+          if (t == 0) rows[r] = row_info(a, f, p.b, p.len, at, live, c2);
         }
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s)
-          qf[(n * kSteps + s) * 32 + lane] = make_uint2(w[2 * s], w[2 * s + 1]);
-        if (t == 0) {
-          const float L = live ? f.lse[static_cast<int64_t>(p.b) * a.all_rows + at] : -INFINITY;
-          RowInfo& info = rows[r];
-          info.c2 = c2;
-          info.l2 = L == -INFINITY ? INFINITY : L * kLog2Of;
-          info.lim = !live || L == -INFINITY
-                         ? 0
-                         : (a.causal ? min(p.len, p.len - a.n_q + qt + 1) : p.len);
+        for (int s = 0; s < kSteps; ++s) {
+          const int at = (n * kSteps + s) * 32 + lane;
+          if constexpr (MANY)
+            reinterpret_cast<uint4*>(frag)[at] =
+                make_uint4(w[0][2 * s], w[1][2 * s], w[0][2 * s + 1], w[1][2 * s + 1]);
+          else
+            reinterpret_cast<uint2*>(frag)[at] = make_uint2(w[0][2 * s], w[0][2 * s + 1]);
         }
       }
       __syncthreads();
-      const bool ragged = (nrows & 7) != 0;
-      if (nu > 0) load_pages(p, 0, nu);
-      KeyPieces<D, PACKED> next[G];
-#pragma unroll
-      for (int i = 0; i < G; ++i)
-        if (nu > 0) load(p, i, next[i]);
-      for (int v0 = 0; v0 < 2 * nu; v0 += G) {
-        KeyPieces<D, PACKED> now[G];
-#pragma unroll
-        for (int i = 0; i < G; ++i) now[i] = next[i];
-        if (v0 + G < 2 * nu) {
-          if (((v0 + G) & 63) == 0) load_pages(p, (v0 + G) >> 1, nu);
-#pragma unroll
-          for (int i = 0; i < G; ++i) load(p, v0 + G + i, next[i]);
+      const bool ragged = nrows % kBlock != 0;
+      if (nv > 0) load_pages(p, 0, nv >> 2);
+      KeyPart<D, PACKED> part[kParts];
+      if (!MANY && nv > 0) load(p, 0, part);
+      for (int v = 0; v < nv; v += kParts) {
+        KeyPart<D, PACKED> now[kParts];
+        if constexpr (MANY) {
+          if ((v & 127) == 0 && v > 0) load_pages(p, v >> 2, nv >> 2);
+          load(p, v, part);
         }
 #pragma unroll
-        for (int i = 0; i < G; ++i) {
-          const int v = v0 + i;
-          const int k0 = (p.t0 + warp + kWeightWarps * (v >> 1)) * kWeightKeys + 16 * (v & 1);
-          if (k0 >= p.len) continue;
-          // lanes t = 0, 1 have keys g, g + 8 to write
-          const int mine = k0 + g + 8 * (t & 1);
-          const bool writes = t < 2 && mine < p.len;
-          float* to = f.weights + p.b * f.stride_b + p.h * f.stride_h + mine;
-          float before = 0.f;
-          if (writes && (f.add || r0 > 0)) before = *to;
-          uint32_t ka[kSteps][4];
-          fragments(now[i], ka);
-          const bool masked = ragged || k0 + 16 > (a.causal ? p.len - a.n_q + 1 : p.len);
-          float sum[2] = {0.f, 0.f};
+        for (int i = 0; i < kParts; ++i) now[i] = part[i];
+        if (!MANY && v + kParts < nv) {
+          if (((v + kParts) & 127) == 0) load_pages(p, (v + kParts) >> 2, nv >> 2);
+          load(p, v + kParts, part);
+        }
+        const int k0 = (p.t0 + warp + kWeightWarps * (v >> 2)) * kWeightKeys + 8 * (v & 3);
+        const bool masked =
+            ragged || k0 + 8 * kParts > (a.causal ? p.len - a.n_q + 1 : p.len);
+        float* to = f.weights + p.b * f.stride_b + p.h * f.stride_h + k0;
+        const bool add = f.add || r0 > 0;
+        if constexpr (MANY) {
+          uint32_t kb[4][kSteps][2];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) operands<D, PACKED>(now[i], kb[i]);
+          // lanes g = 0 ... 3 write keys 8 g + 2 t, + 1
+          const int mine = 8 * g + 2 * t;
+          float before[2] = {0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (add && g < 4 && k0 + mine + j < p.len) before[j] = to[mine + j];
+          float sum[4][2];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum[i][0] = sum[i][1] = 0.f;
           for (int n = 0; n < blocks; ++n) {
-            float c[4] = {0.f, 0.f, 0.f, 0.f};
+            float c[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0.f;
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
-              const uint2 b = qf[(n * kSteps + s) * 32 + lane];
-              if constexpr (PACKED) mma16816_half(c, ka[s], b.x, b.y);
-              else mma16816_bf16(c, ka[s], b.x, b.y);
+              const uint4 q = reinterpret_cast<const uint4*>(frag)[(n * kSteps + s) * 32 + lane];
+              const uint32_t qa[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if constexpr (PACKED) mma16816_half(c[i], qa, kb[i][s][0], kb[i][s][1]);
+                else mma16816_bf16(c[i], qa, kb[i][s][0], kb[i][s][1]);
+              }
             }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {   // rows g, g + 8
+              const RowInfo info = rows[16 * n + 8 * e + g];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  float x = ex2_approx(fmaf(c[i][2 * e + j], info.c2, -info.l2));
+                  if (masked && k0 + 8 * i + 2 * t + j >= info.lim) x = 0.f;
+                  sum[i][j] += x;
+                }
+            }
+          }
+          float out[2] = {0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const RowInfo info = rows[8 * n + 2 * t + j];
-              float p0 = ex2_approx(fmaf(c[j], info.c2, -info.l2));
-              float p1 = ex2_approx(fmaf(c[2 + j], info.c2, -info.l2));
-              if (masked) {
-                if (k0 + g >= info.lim) p0 = 0.f;
-                if (k0 + g + 8 >= info.lim) p1 = 0.f;
-              }
-              sum[0] += p0;
-              sum[1] += p1;
+              float x = sum[i][j];
+              x += __shfl_xor_sync(0xffffffffu, x, 4);
+              x += __shfl_xor_sync(0xffffffffu, x, 8);
+              x += __shfl_xor_sync(0xffffffffu, x, 16);
+              if (g == i) out[j] = x;
             }
-          }
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 1);
-            sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 2);
+          for (int j = 0; j < 2; ++j)
+            if (g < 4 && k0 + mine + j < p.len) to[mine + j] = before[j] + out[j];
+        } else {
+          // lanes t = 0, 1 have keys g, g + 8 of 16 to write
+          const int mine = g + 8 * (t & 1);
+#pragma unroll
+          for (int i = 0; i < kParts; i += 2) {
+            float before = 0.f, sum[2] = {0.f, 0.f};
+            const bool writes = t < 2 && k0 + mine + 8 * i < p.len;
+            if (add && writes) before = to[mine + 8 * i];
+            uint32_t kb[2][kSteps][2];
+            operands<D, PACKED>(now[i], kb[0]);
+            operands<D, PACKED>(now[i + 1], kb[1]);
+            for (int n = 0; n < blocks; ++n) {
+              float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int s = 0; s < kSteps; ++s) {
+                const uint2 q = reinterpret_cast<const uint2*>(frag)[(n * kSteps + s) * 32 + lane];
+                const uint32_t ka[4] = {kb[0][s][0], kb[1][s][0], kb[0][s][1], kb[1][s][1]};
+                if constexpr (PACKED) mma16816_half(c, ka, q.x, q.y);
+                else mma16816_bf16(c, ka, q.x, q.y);
+              }
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const RowInfo info = rows[8 * n + 2 * t + j];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {   // keys g, g + 8
+                  float x = ex2_approx(fmaf(c[2 * e + j], info.c2, -info.l2));
+                  if (masked && k0 + 8 * i + 8 * e + g >= info.lim) x = 0.f;
+                  sum[e] += x;
+                }
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
+              sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
+            }
+            if (writes) to[mine + 8 * i] = before + (t == 0 ? sum[0] : sum[1]);
           }
-          if (writes) *to = before + (t == 0 ? sum[0] : sum[1]);
         }
       }
     }
   }
 }
 
-template <int D, bool PACKED>
-cudaError_t launch_kind(const PagedArgs& a, const WeightArgs& f, int ctas, cudaStream_t s) {
+constexpr int kManyRows = 16;   // query rows of a head above which MANY is taken
+
+template <int D, bool PACKED, bool MANY>
+cudaError_t launch_rows(const PagedArgs& a, const WeightArgs& f, int ctas, cudaStream_t s) {
   const size_t bytes = f.pass_rows * (sizeof(RowInfo) + D * 2);
   static std::atomic<uint64_t> set_up{0};
   int dev = 0;
@@ -275,19 +357,26 @@ cudaError_t launch_kind(const PagedArgs& a, const WeightArgs& f, int ctas, cudaS
   cudaError_t e = needs_setup(set_up, &dev, &todo);
   if (e != cudaSuccess) return e;
   if (todo) {
-    e = cudaFuncSetAttribute(key_weights_kernel<D, PACKED>,
+    e = cudaFuncSetAttribute(key_weights_kernel<D, PACKED, MANY>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kWeightRows * (sizeof(RowInfo) + D * 2));
     if (e != cudaSuccess) return e;
     mark_done(set_up, dev);
   }
-  return launch_pdl(key_weights_kernel<D, PACKED>, dim3(ctas), dim3(kWeightThreads), bytes, s, a, f);
+  return launch_pdl(key_weights_kernel<D, PACKED, MANY>, dim3(ctas), dim3(kWeightThreads), bytes, s,
+                    a, f);
+}
+
+template <int D, bool PACKED>
+cudaError_t launch_kind(const PagedArgs& a, const WeightArgs& f, int ctas, cudaStream_t s) {
+  return a.head_rows > kManyRows ? launch_rows<D, PACKED, true>(a, f, ctas, s)
+                                 : launch_rows<D, PACKED, false>(a, f, ctas, s);
 }
 
 }  // namespace
 
 cudaError_t launch_key_weights(const PagedArgs& a, WeightArgs f, int ctas, cudaStream_t s) {
-  const int rows = (a.head_rows + 7) / 8 * 8;
+  const int rows = (a.head_rows + 15) / 16 * 16;
   f.pass_rows = rows < kWeightRows ? rows : kWeightRows;
   if (f.k == nullptr)
     return a.d == 64 ? launch_kind<64, true>(a, f, ctas, s) : launch_kind<128, true>(a, f, ctas, s);
