@@ -28,6 +28,7 @@ ATTN_STALL_BWD_COMPUTE = 2
 ATTN_STALL_PAGED_TILE = 3
 ATTN_STALL_PREFIX_SOFTMAX = 4
 ATTN_STALL_LATENT_SOFTMAX = 5
+ATTN_STALL_EVICT_READ = 8
 
 # every function the header declares, with its ctypes signature
 EXPORTS = {

@@ -78,11 +78,13 @@ struct EvictArgs {
   int n_pools;
   RowPool pools[kMaxPools];
   int buffer;                // bytes of a chunk, all pools
+  int stall;                 // kStallEvictRead: see attn_debug_stall
   int* status;
+  uint64_t timeout_ns;
 };
 
-__device__ void report(int* status, int code) {
-  if (atomicCAS(status, 0, code) == 0) atomicExch(status + 1, kSitePageIndex);
+__device__ void report(int* status, int code, int site) {
+  if (atomicCAS(status, 0, code) == 0) atomicExch(status + 1, site);
 }
 
 __device__ __forceinline__ bool in_range(int i, int n) {
@@ -168,7 +170,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const EvictAr
       for (int j = threadIdx.x; j < part; j += kSelectThreads) cache[j] = order_key(w[lo + j]);
   ok = ok && check_pages(a, i, old, len);   // (and the CTA's keys are there)
   const bool first = h == 0 && rank == 0 && threadIdx.x == 0;
-  if (first && !ok) report(a.status, kStatusPage);
+  if (first && !ok) report(a.status, kStatusPage, kSitePageIndex);
   if (first) {
     a.old_len[i] = ok && len < old ? old : -1;
     a.new_len[i] = len;
@@ -440,14 +442,15 @@ __global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const __grid_cons
       int32_t* read = a.read + static_cast<int64_t>(now.item) * a.chunks;
       // (The rows have arrived, so the flag needs no fence before it; and whoever
       // sees it set writes only after that.)
-      if (threadIdx.x == 0) atomicExch(read + now.c, 1);
+      // (An armed test stall: the first chunks never say so.)
+      if (threadIdx.x == 0 && !(a.stall != 0 && now.c == 0)) atomicExch(read + now.c, 1);
       // chunks in front of this one that have rows where it writes
       for (int q = now.from + static_cast<int>(threadIdx.x); q < now.until; q += kMoveThreads) {
         const volatile int32_t* flag = read + q;
         const uint64_t t0 = globaltimer_ns();
         for (uint32_t it = 1; *flag == 0; ++it)
-          if ((it & 63u) == 0 && globaltimer_ns() - t0 > kTimeoutNs) {
-            report(a.status, kStatusTimeout);
+          if ((it & 63u) == 0 && globaltimer_ns() - t0 > a.timeout_ns) {
+            report(a.status, kStatusTimeout, kSiteEvictRead);
             sh.give_up = 1;
             break;
           }
@@ -539,7 +542,7 @@ int check_evict(const attn_page_table* t, int32_t heads, int32_t n, const attn_r
   for (int i = 0; i < n_pools; ++i) {
     const attn_rows& p = pools[i];
     if (p.reserved != 0) return bad(ATTN_ERR_INVALID_ARG, "pools: reserved field must be 0");
-    if ((p.base == nullptr && t->num_pages > 0) || (reinterpret_cast<uintptr_t>(p.base) & 3u) != 0 ||
+    if ((p.base == nullptr && t->num_pages > 0 && heads > 0) || (reinterpret_cast<uintptr_t>(p.base) & 3u) != 0 ||
         p.row_bytes <= 0 || p.row_bytes % 4 != 0 || p.page_stride % 4 != 0 ||
         p.head_stride % 4 != 0 || p.row_stride % 4 != 0 || p.page_stride < 0 ||
         p.head_stride < 0 || p.row_stride < p.row_bytes)
@@ -705,6 +708,8 @@ attn_status attn_pages_evict(const attn_page_table* t, const attn_rows* pools, i
     at = (at + L.chunk * p.row_bytes + 15) / 16 * 16;
   }
   a.status = reinterpret_cast<int*>(ws);
+  a.timeout_ns = kTimeoutNs;
+  a.stall = take_stall(kStallEvictRead, &a.timeout_ns);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   // a CTA's part of the weights, if it fits
   const int64_t part = (cap + a.cluster * kSelectThreads - 1) / (a.cluster * kSelectThreads) *

@@ -39,6 +39,7 @@ using namespace sm103;
 namespace {
 
 constexpr float kLazy = 8.f;
+constexpr float kLn2 = 0.69314718f;
 constexpr float kNone = -3e38f;   // a row's maximum before its first key
 
 // NT: blocks of 8 query rows per warp; MT: warps that share a tile.
@@ -58,16 +59,20 @@ struct Fp4Cfg {
   static constexpr int kRedBytes = kRows * kRedStride * 4;   // of a slot
   static constexpr int kStages = NT == 1 && D == 128 ? 2 : MT == 2 || D == 64 ? 4 : 3;
   static constexpr int kRingBytes = kSlots * kStages * kTileBytes;
+  static constexpr int kQRows = MT == 1 ? 8 * NT * kWarps : kRows;   // with a segment per warp
   static constexpr int kQBytes = kSharedQ ? kRows * D * 2 : 0;
   static constexpr int kSmem = kRingBytes + 2 * kRedBytes + kQBytes;
   static_assert(kCtasPerSm * (kSmem + 1024 + 2560) <= 228 * 1024, "shared memory of an SM");
+  // (a warp to itself needs no `red`, and has Q there)
+  static_assert(!kSharedQ || kQRows * D * 2 <= 2 * kRedBytes + kQBytes, "Q of all warps");
 };
 
 template <int D, int NT, int MT>
 struct Fp4Shared {
   float m[Fp4Cfg<D, NT, MT>::kSlots][Fp4Cfg<D, NT, MT>::kRows];   // largest score, log2 units
   float l[Fp4Cfg<D, NT, MT>::kSlots][Fp4Cfg<D, NT, MT>::kRows];
-  float c2[Fp4Cfg<D, NT, MT>::kRows];   // (kSharedQ)
+  float c2[Fp4Cfg<D, NT, MT>::kQRows];   // (kSharedQ)
+  float L[Fp4Cfg<D, NT, MT>::kRows];     // of the CTA's rows, for the cluster
 };
 
 // 16 bytes to shared memory, asynchronously; zeros where nothing is `there`.
@@ -84,6 +89,13 @@ __device__ __forceinline__ void copies_commit() {
 template <int N>
 __device__ __forceinline__ void copies_wait_but() {   // all groups but the last N have landed
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void cluster_ld2(uint32_t addr, float* x) {
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+               : "=f"(x[0]), "=f"(x[1])
+               : "r"(addr)
+               : "memory");
 }
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {   // an 8 x 8 matrix of 16 bits
@@ -116,7 +128,14 @@ __device__ __forceinline__ const uint8_t* page_at(const uint8_t* base, int page,
   return base + static_cast<uint64_t>(static_cast<uint32_t>(page)) * static_cast<uint32_t>(step);
 }
 
-template <int D, int NT, int MT>
+// How the segments are given out.
+//   kSplit    the balanced split; what it cuts is merged by a second kernel
+//   kCluster  a segment per cluster of a.cluster CTAs (of one, perhaps), merged in
+//             shared memory
+//   kSolo     a segment per warp, which has nobody to merge with
+enum Fp4Mode { kSplit, kCluster, kSolo };
+
+template <int D, int NT, int MT, Fp4Mode MODE>
 __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>::kCtasPerSm)
     fp4_decode_kernel(const PagedArgs a, const Fp4Args f) {
   using C = Fp4Cfg<D, NT, MT>;
@@ -126,7 +145,7 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Fp4Shared<D, NT, MT> sh;
   float* red = reinterpret_cast<float*>(smem + C::kRingBytes);   // [2][kRows][kRedStride]
-  uint2* sq = reinterpret_cast<uint2*>(smem + C::kRingBytes + 2 * C::kRedBytes);
+  uint2* sq = reinterpret_cast<uint2*>(smem + C::kRingBytes + (MODE == kSolo ? 0 : 2 * C::kRedBytes));
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int slot = warp / MT, mt = warp % MT;
@@ -134,22 +153,26 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
   uint8_t* ring = smem + slot * ST * C::kTileBytes;
   grid_dep_wait();
   grid_dep_launch();
-  const PagedShare share =
-      paged_share<KT, C::kOverhead, kFp4MinUnits>(a, blockIdx.x, gridDim.x);
+  PagedShare share{};
+  if constexpr (MODE == kSplit)
+    share = paged_share<KT, C::kOverhead, kFp4MinUnits>(a, blockIdx.x, gridDim.x);
   MergeNote note{-1, 0, 0, 0};
   const bool small_pages = a.page_shift < 5;   // 16 keys: a tile lies in two
 
   // ---- the copies: tile u of this slot is tile t0 + slot + kSlots u of the
-  // piece; lane l holds the pages of tile 32 * (batch) + l
+  // piece (of a segment of its own: tile u); lane l holds the pages of tile 32 *
+  // (batch) + l
+  constexpr int kStep = MODE == kSolo ? 1 : kSlots;
+  const int first_tile = MODE == kSolo ? 0 : slot;
   int page_of[2] = {0, 0};
   auto slot_tiles = [&](const PagedPiece& p) {
-    const int n = p.t1 - p.t0 - slot;
-    return n > 0 ? (n + kSlots - 1) / kSlots : 0;
+    const int n = p.t1 - p.t0 - first_tile;
+    return n > 0 ? (n + kStep - 1) / kStep : 0;
   };
   auto load_pages = [&](const PagedPiece& p, int u0, int nu) {
     const int u = u0 + lane;
     if (u < nu) {
-      const int key = (p.t0 + slot + kSlots * u) * KT;
+      const int key = (p.t0 + first_tile + kStep * u) * KT;
       const int32_t* row = a.table + p.b * a.table_stride;
       page_of[0] = checked_page(row[key >> a.page_shift], a.num_pages, a.status);
       page_of[1] = !small_pages || key + 16 >= p.len
@@ -190,7 +213,7 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
     const uint8_t *k0, *v0, *s0, *k1, *v1;
     bool in1 = in0, s_in = in0;
     if (!small_pages) {
-      const uint32_t row = (p.t0 + slot + kSlots * u) * KT & ((1 << a.page_shift) - 1);
+      const uint32_t row = (p.t0 + first_tile + kStep * u) * KT & ((1 << a.page_shift) - 1);
       k0 = k1 = page_at(from_k, pg0, f.k.code_page) + row * (D / 2);
       v0 = v1 = page_at(from_v, pg0, f.v.code_page) + row * (D / 2);
       s0 = page_at(from_s, pg0, scale_page) + row * (D / kFp4Block);
@@ -226,13 +249,14 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
 
   // What a piece begins with, on its way early: its rows of Q (raw), its pages,
   // its first tiles.
+  constexpr bool kOwnQ = C::kSharedQ && MODE == kSolo;   // NT blocks, one after another
   constexpr int kQBlocks = C::kSharedQ ? 1 : NT;   // of 8 rows that this warp loads
   uint32_t qw[kQBlocks][D / 8];
-  auto fetch_q = [&](const PagedPiece& p) {
+  auto fetch_q = [&](const PagedPiece& p, int block) {   // (kSharedQ: this one)
     const int row0 = segment_row(a, p.h), nrows = segment_rows(a, p.h);
 #pragma unroll
     for (int n = 0; n < kQBlocks; ++n) {
-      const int r = (C::kSharedQ ? warp : mt * NT + n) * 8 + g;
+      const int r = (C::kSharedQ ? block : mt * NT + n) * 8 + g;
       const bool live = r < nrows;
       const int h = (row0 + r) / a.n_q, qt = row0 + r - h * a.n_q;
       const uint4* qr = reinterpret_cast<const uint4*>(
@@ -250,7 +274,7 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
   };
   auto fetch = [&](const PagedPiece& p) {
     const int nu = slot_tiles(p);
-    if constexpr (!C::kSharedQ) fetch_q(p);
+    if constexpr (!C::kSharedQ) fetch_q(p, 0);
     if (nu > 0) load_pages(p, 0, nu);
     sources(p);
     for (int u = 0; u < ST - 1; ++u) {
@@ -259,45 +283,58 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
     }
   };
 
-  PagedPiece p = paged_piece<KT, C::kOverhead>(a, share, share.b, 0, share.s);
+  const int rank = MODE == kCluster ? static_cast<int>(cluster_rank()) : 0;
+  PagedPiece p;
+  if constexpr (MODE == kSplit) {
+    p = paged_piece<KT, C::kOverhead>(a, share, share.b, 0, share.s);
+  } else {
+    const int segment = MODE == kSolo ? blockIdx.x * kSlots + slot : blockIdx.x / a.cluster;
+    const int b = segment / a.heads;
+    p.valid = false;
+    if (b < a.B) p = paged_part<KT>(a, b, segment - b * a.heads, rank, MODE == kSolo ? 1 : a.cluster);
+  }
   if (p.valid) fetch(p);
   while (p.valid) {   // (the same pieces in every warp)
     const int nu = slot_tiles(p);
     // Q^T fragments: row r = 8 n + g, columns of quarter t, as fp16 times 2^e
     const int row0 = segment_row(a, p.h), nrows = segment_rows(a, p.h);
     float c2[NT][2];                // what turns a score into log2 units, rows 2t, 2t + 1
-    float factor[kQBlocks];
-    if constexpr (C::kSharedQ) fetch_q(p);   // (late: the registers are O's until then)
-#pragma unroll
-    for (int n = 0; n < kQBlocks; ++n) {
-      int e;
-      half_rows<D / 8>(qw[n], &e);
-      factor[n] = score_factor(a.scale_log2 * f.k_descale, e);
-    }
     uint32_t qb[kQBlocks][kSteps][2];
+    if constexpr (C::kSharedQ) {   // (late: the registers are O's until then)
+      // the CTA's blocks, one a warp; of a segment of its own: all of them
+      uint2* to = sq + (kOwnQ ? warp * NT * kSteps * 32 : 0);
+#pragma unroll 1
+      for (int n = kOwnQ ? 0 : warp; n < (kOwnQ ? NT : warp + 1); ++n) {
+        fetch_q(p, n);
+        int e;
+        half_rows<D / 8>(qw[0], &e);
+        const float c = score_factor(a.scale_log2 * f.k_descale, e);
 #pragma unroll
-    for (int n = 0; n < kQBlocks; ++n)
-#pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        qb[n][i][0] = qw[n][2 * i];
-        qb[n][i][1] = qw[n][2 * i + 1];
+        for (int i = 0; i < kSteps; ++i)
+          to[(n * kSteps + i) * 32 + lane] = make_uint2(qw[0][2 * i], qw[0][2 * i + 1]);
+        if (t == 0) sh.c2[(kOwnQ ? warp * NT : 0) * 8 + n * 8 + g] = c;
       }
-    if constexpr (C::kSharedQ) {
-#pragma unroll
-      for (int i = 0; i < kSteps; ++i)
-        sq[(warp * kSteps + i) * 32 + lane] = make_uint2(qb[0][i][0], qb[0][i][1]);
-      if (t == 0) sh.c2[warp * 8 + g] = factor[0];
-      __syncthreads();
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) c2[n][i] = sh.c2[(mt * NT + n) * 8 + 2 * t + i];
-    } else {
+      if constexpr (kOwnQ) __syncwarp();
+      else __syncthreads();
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          c2[n][i] = __shfl_sync(0xffffffffu, factor[n], 4 * (2 * t + i));
+          c2[n][i] = sh.c2[((kOwnQ ? warp : mt) * NT + n) * 8 + 2 * t + i];
+    } else {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        int e;
+        half_rows<D / 8>(qw[n], &e);
+        const float c = score_factor(a.scale_log2 * f.k_descale, e);
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          qb[n][i][0] = qw[n][2 * i];
+          qb[n][i][1] = qw[n][2 * i + 1];
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) c2[n][i] = __shfl_sync(0xffffffffu, c, 4 * (2 * t + i));
+      }
     }
     auto limit = [&](int n, int i) {   // keys below it are allowed, row 2t + i of block n
       const int r = (mt * NT + n) * 8 + 2 * t + i, qt = (row0 + r) % a.n_q;
@@ -328,7 +365,7 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
       }
       copies_commit();
       const uint8_t *kc = at_k + stage, *vc = at_v + stage, *ks = at_ks + stage, *vs = at_vs + stage;
-      const int k0 = (p.t0 + slot + kSlots * u) * KT;
+      const int k0 = (p.t0 + first_tile + kStep * u) * KT;
       if (k0 + KT > p.len) {   // value rows past the end: their scales are zero
         const int from = (p.len - k0) * (D / kFp4Block) + lane;
         uint8_t* to = ring + stage + 2 * C::kCodeBytes + C::kScaleBytes;
@@ -383,7 +420,7 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             uint2 q;
-            if constexpr (C::kSharedQ) q = sq[((mt * NT + n) * kSteps + 2 * j + i) * 32 + lane];
+            if constexpr (C::kSharedQ) q = sq[(((kOwnQ ? warp : mt) * NT + n) * kSteps + 2 * j + i) * 32 + lane];
             else q = make_uint2(qb[n][2 * j + i][0], qb[n][2 * j + i][1]);
             mma16816_half(sc[0][n], ka[0], q.x, q.y);
             mma16816_half(sc[1][n], ka[1], q.x, q.y);
@@ -480,11 +517,15 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
       }
     }
     copies_wait_but<0>();
-    const PagedPiece next = paged_next<KT, C::kOverhead>(a, share, p);
-    slot_sync();   // the ring is free
-    if (next.valid) fetch(next);
+    PagedPiece next = p;
+    next.valid = false;
+    if constexpr (MODE == kSplit) {
+      next = paged_next<KT, C::kOverhead>(a, share, p);
+      slot_sync();   // the ring is free
+      if (next.valid) fetch(next);
+    }
 
-    // ---- the slots' states merged: m, l per row, then O through shared memory
+    // the sums over the lanes of equal t
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -495,6 +536,34 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
         // no keys; a row of NaN scores has seen some
         if (l[n][i] == 0.f) m[n][i] = -INFINITY;
         else if (l[n][i] != l[n][i]) m[n][i] = 0.f;
+      }
+    if constexpr (MODE == kSolo) {   // straight from the registers, 2 or 1 16-byte words a row
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = n * 8 + 2 * t + i;
+          if (r >= nrows) continue;
+          const int h = (row0 + r) / a.n_q, qt = row0 + r - h * a.n_q;
+          const float w = l[n][i] == 0.f ? 0.f : f.v_descale / l[n][i];
+          uint4* to = reinterpret_cast<uint4*>(a.o + p.b * a.stride_b + h * a.stride_h +
+                                               static_cast<int64_t>(qt) * a.stride_n + (D / 8) * g);
+          uint32_t x[kSteps];
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k) x[k] = pack_bf16x2(o[k][n][i] * w, o[k][n][2 + i] * w);
+#pragma unroll
+          for (int k = 0; k < kSteps / 4; ++k)
+            to[k] = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+          if (g == 0)
+            a.lse[static_cast<int64_t>(p.b) * a.all_rows + row0 + r] =
+                l[n][i] == 0.f ? -INFINITY : fmaf(m[n][i], kLn2, logf(l[n][i]));
+        }
+    } else {
+    // ---- the slots' states merged: m, l per row, then O through shared memory
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
         if (g == 0) {
           sh.m[slot][(mt * NT + n) * 8 + 2 * t + i] = m[n][i];
           sh.l[slot][(mt * NT + n) * 8 + 2 * t + i] = l[n][i];
@@ -528,9 +597,11 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
         }
       }
     const bool whole = p.whole();
-    if (p.t0 == 0 && !whole) note = paged_note<C::kOverhead>(share, p);
-    if (a.by_segment && p.t0 == 0 && threadIdx.x == 0)
-      a.notes[p.b * a.heads + p.h] = whole ? MergeNote{p.b, p.h, 0, -1} : note;
+    if constexpr (MODE == kSplit) {
+      if (p.t0 == 0 && !whole) note = paged_note<C::kOverhead>(share, p);
+      if (a.by_segment && p.t0 == 0 && threadIdx.x == 0)
+        a.notes[p.b * a.heads + p.h] = whole ? MergeNote{p.b, p.h, 0, -1} : note;
+    }
     const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (p.s < share.lo ? 0 : 1);
     // slots 0, 1 write, 2, 3 add, ...: the sum has a fixed order.  Column (D / 8) g +
     // 2 i + b of a row lies at 16 i + 2 g + b
@@ -573,9 +644,14 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
       float mx, L = 0.f;
       if (c == 0) {
         const float lt = total(r, &mx);
-        L = lt == 0.f ? -INFINITY : fmaf(mx, 0.69314718f, logf(lt));
+        L = lt == 0.f ? -INFINITY : fmaf(mx, kLn2, logf(lt));
       }
-      if (whole) {
+      if (MODE == kCluster && a.cluster > 1) {   // for the others (this thread's own place)
+        *reinterpret_cast<float2*>(&red[r * C::kRedStride + 2 * gg + 16 * k]) = make_float2(x[0], x[1]);
+        *reinterpret_cast<float2*>(&red[r * C::kRedStride + 2 * gg + 16 * k + 16]) =
+            make_float2(x[2], x[3]);
+        if (c == 0) sh.L[r] = L;
+      } else if (MODE == kCluster || whole) {
         const int h = (row0 + r) / a.n_q, qt = row0 + r - h * a.n_q;
         *reinterpret_cast<uint2*>(a.o + p.b * a.stride_b + h * a.stride_h +
                                   static_cast<int64_t>(qt) * a.stride_n + c) =
@@ -587,27 +663,73 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
         if (c == 0) a.part_l[part * a.rows + r] = L;
       }
     }
+    if constexpr (MODE == kCluster) {
+      if (a.cluster > 1) {   // each CTA of the cluster writes a part of the items
+        cluster_sync();
+        for (int e = rank * C::kThreads + threadIdx.x; e < nrows * (D / 4);
+             e += a.cluster * C::kThreads) {
+          const int r = e / (D / 4), c = 4 * (e - r * (D / 4));
+          const float* at = &red[r * C::kRedStride + 2 * (c / (D / 8)) + 16 * (c % (D / 8) / 2)];
+          float top = -INFINITY, sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int k = 0; k < a.cluster; ++k)
+            top = fmaxf(top, cluster_ld(cluster_addr(&sh.L[r], k)));
+          top = merge_base(top);
+          for (int k = 0; k < a.cluster; ++k) {
+            const float w = __expf(cluster_ld(cluster_addr(&sh.L[r], k)) - top);
+            float y[4];
+            cluster_ld2(cluster_addr(at, k), y);
+            cluster_ld2(cluster_addr(at + 16, k), y + 2);
+            sum += w;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = fmaf(w, y[i], x[i]);
+          }
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          const int h = (row0 + r) / a.n_q, qt = row0 + r - h * a.n_q;
+          *reinterpret_cast<uint2*>(a.o + p.b * a.stride_b + h * a.stride_h +
+                                    static_cast<int64_t>(qt) * a.stride_n + c) =
+              make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
+          if (c == 0)
+            a.lse[static_cast<int64_t>(p.b) * a.all_rows + row0 + r] =
+                sum == 0.f ? -INFINITY : top + logf(sum);
+        }
+        cluster_sync();   // the others have read this CTA's rows
+      }
+    }
     __syncthreads();   // red, m and l are free
+    }
     p = next;
   }
-  if (!a.by_segment && threadIdx.x == 0) a.notes[blockIdx.x] = note;
+  if (MODE == kSplit && !a.by_segment && threadIdx.x == 0) a.notes[blockIdx.x] = note;
 }
 
-template <int D, int NT, int MT>
-cudaError_t launch_rows(const PagedArgs& a, const Fp4Args& f, int ctas, cudaStream_t s) {
+template <int D, int NT, int MT, Fp4Mode MODE>
+cudaError_t launch_mode(const PagedArgs& a, const Fp4Args& f, int ctas, cudaStream_t s) {
   using C = Fp4Cfg<D, NT, MT>;
   static std::atomic<uint64_t> set_up{0};
   int dev = 0;
   bool todo = false;
   cudaError_t e = needs_setup(set_up, &dev, &todo);
   if (e != cudaSuccess) return e;
+  auto kernel = fp4_decode_kernel<D, NT, MT, MODE>;
   if (todo) {
-    e = cudaFuncSetAttribute(fp4_decode_kernel<D, NT, MT>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     mark_done(set_up, dev);
   }
-  return launch_pdl(fp4_decode_kernel<D, NT, MT>, dim3(ctas), dim3(C::kThreads), C::kSmem, s, a, f);
+  const unsigned segments = static_cast<unsigned>(a.B * a.heads);
+  if (MODE == kCluster)
+    return launch_clusters(kernel, dim3(segments * a.cluster), dim3(C::kThreads), C::kSmem,
+                           a.cluster, s, a, f);
+  const unsigned grid = MODE == kSolo ? (segments + C::kSlots - 1) / C::kSlots : ctas;
+  return launch_pdl(kernel, dim3(grid), dim3(C::kThreads), C::kSmem, s, a, f);
+}
+
+template <int D, int NT, int MT>
+cudaError_t launch_rows(const PagedArgs& a, const Fp4Args& f, int ctas, cudaStream_t s) {
+  if (a.cluster > 0) return launch_mode<D, NT, MT, kCluster>(a, f, ctas, s);
+  if constexpr (MT == 1)
+    if (a.cluster < 0) return launch_mode<D, NT, MT, kSolo>(a, f, ctas, s);
+  return launch_mode<D, NT, MT, kSplit>(a, f, ctas, s);
 }
 
 template <int D>

@@ -68,10 +68,26 @@ cudaError_t launch_fp4_store(const Fp4CopyArgs& a, cudaStream_t s);
 cudaError_t launch_fp4_load(const Fp4CopyArgs& a, cudaStream_t s);
 cudaError_t launch_fp4_decode(const PagedArgs& a, const Fp4Args& f, int ctas, cudaStream_t s);
 
-// Decode: key tiles of 32, the split's constants in such tiles.
+// Decode: key tiles of 32, and the constants of the split, in such tiles.  Swept on
+// whole steps (us; H = 32, 8 key/value heads, d = 128 unless said).
+// A segment's cost beside its tiles, 8 / 20 above 16 rows: 64 sequences of 0-16384
+// keys, 32 rows 286 / 245.
 constexpr int kFp4Keys = 32;
 constexpr int fp4_overhead(int rows) { return rows <= 16 ? 8 : 20; }
-constexpr int kFp4MinUnits = 6;
+constexpr int kFp4MinUnits = 6;       // units a CTA takes at least
+// Tiles (at full caches) from which on a segment takes more than one CTA: 100 keys
+// one CTA 4.5, two 6.2; 517 keys one 8.0, eight 6.4.
+constexpr int kFp4ClusterFrom = 8;
+// Tiles of a cluster's CTA at most: one sequence of 4096 keys, eight CTAs 8.8, the
+// balanced split 9.3; 8192 keys 11.8 and 10.7; 64 rows, 16 sequences of 1000-2000
+// keys 20.3 and 17.1.
+constexpr int fp4_cluster_tiles(int rows) { return rows <= 32 ? 24 : 12; }
+// Where there are more segments than CTAs at a time: tiles of a warp that has a
+// segment to itself (300 sequences of 300-600 keys a warp each 38.9, a CTA 45.8,
+// split 58.8; 200 of 600-1200 keys 68.2, 51.7, 60.8), and of a CTA (200 sequences
+// of 0-2000 keys 61.1, split 70.3).
+constexpr int kFp4SoloTiles = 24;
+constexpr int kFp4ManyTiles = 64;
 
 // CTAs of the decode kernel per SM at `rows` query rows of a segment: 16 warps of
 // up to 8 rows, 12 of 16, 8 of 32.

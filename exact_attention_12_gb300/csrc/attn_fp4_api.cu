@@ -65,15 +65,15 @@ attn_status check_pages(const attn_params* p, const attn_pages* g) {
   return ATTN_OK;
 }
 
-// A cache in 4 bits; one of no pages may be anywhere.
-attn_status check_cache(const attn_fp4* c, int num_pages) {
+// A cache in 4 bits; one of no pages or heads may be anywhere.
+attn_status check_cache(const attn_fp4* c, int heads, int num_pages) {
   if (c == nullptr) return fail(ATTN_ERR_INVALID_ARG, "cache is NULL");
   if (c->reserved != 0) return fail(ATTN_ERR_INVALID_ARG, "cache: reserved field must be 0");
   if (!(c->descale >= 0x1p-100f && c->descale <= 0x1p100f))
     return fail(ATTN_ERR_INVALID_ARG, "cache: descale must be between 2^-100 and 2^100");
   const void* ptrs[2] = {c->codes, c->scales};
   for (const void* ptr : ptrs)
-    if ((num_pages > 0 && ptr == nullptr) || (reinterpret_cast<uintptr_t>(ptr) & 15u) != 0)
+    if ((num_pages > 0 && heads > 0 && ptr == nullptr) || (reinterpret_cast<uintptr_t>(ptr) & 15u) != 0)
       return fail(ATTN_ERR_INVALID_ARG, "cache: codes and scales must be 16-byte aligned");
   const int64_t steps[4] = {c->code_page, c->code_head, c->scale_page, c->scale_head};
   for (int64_t s : steps)
@@ -156,6 +156,7 @@ struct Layout {
   size_t notes = 0, part_o = 0, part_l = 0, total = 0;
   int ctas = 0, n_notes = 0;
   bool by_segment = false;
+  int cluster = 0;   // CTAs of a segment's cluster; 0: the balanced split; -1: a warp a segment
   int heads = 0, blocks = 1, rows = 0, head_rows = 0;
 };
 
@@ -173,6 +174,17 @@ Layout decode_layout(const attn_params* p, int32_t n_q, const attn_pages* g) {
   const int64_t want = segments * (tiles + attn::fp4_overhead(L.rows)) / attn::kFp4MinUnits;
   L.ctas = static_cast<int>(most < want ? most : want);
   if (L.ctas < 1) L.ctas = 1;
+  // Short caches need no balance: a cluster per segment, of as many CTAs as the GPU
+  // holds at once and as have a tile for each of their warps, if that leaves each
+  // few tiles; a warp per segment where there are more segments than that.
+  int c = tiles < attn::kFp4ClusterFrom ? 1 : 8;
+  while (c > 1 && (4 * segments * c > 3 * most || 2 * c > tiles)) c /= 2;
+  if (segments > most) {
+    if (L.rows <= 32 && tiles <= attn::kFp4SoloTiles) L.cluster = -1;
+    else if (tiles <= attn::kFp4ManyTiles) L.cluster = 1;
+  } else if (tiles <= c * attn::fp4_cluster_tiles(L.rows)) {
+    L.cluster = c;
+  }
   L.by_segment = segments <= L.ctas;
   L.n_notes = L.by_segment ? static_cast<int>(segments) : L.ctas;
   size_t off = kHeaderBytes;
@@ -219,8 +231,8 @@ attn_status copy(const attn_params* p, const attn_pages* g, const int32_t* count
                  const void* v, const attn_fp4* kc, const attn_fp4* vc, void* ws, size_t ws_bytes,
                  void* stream, bool store) {
   attn_status st = check_pages(p, g);
-  if (st != ATTN_OK || (st = check_cache(kc, g->num_pages)) != ATTN_OK ||
-      (st = check_cache(vc, g->num_pages)) != ATTN_OK)
+  if (st != ATTN_OK || (st = check_cache(kc, p->H_kv, g->num_pages)) != ATTN_OK ||
+      (st = check_cache(vc, p->H_kv, g->num_pages)) != ATTN_OK)
     return st;
   if (p->N > (1 << 30)) return fail(ATTN_ERR_UNSUPPORTED, "more than 2^30 tokens");
   if (!good_strides({p->kv_stride_b, p->kv_stride_h, p->kv_stride_n}, p->d))
@@ -283,8 +295,8 @@ attn_status attn_decode_fp4(const attn_params* p, int32_t n_q, const attn_pages*
   attn_status st =
       check_step(p, n_q, pages, attn::kFp4Keys, attn::fp4_overhead(attn::kDecMaxRows),
                  attn::kDecMaxRows);
-  if (st != ATTN_OK || (st = check_cache(k, pages->num_pages)) != ATTN_OK ||
-      (st = check_cache(v, pages->num_pages)) != ATTN_OK)
+  if (st != ATTN_OK || (st = check_cache(k, kv_heads(p), pages->num_pages)) != ATTN_OK ||
+      (st = check_cache(v, kv_heads(p), pages->num_pages)) != ATTN_OK)
     return st;
   const Layout L = decode_layout(p, n_q, pages);
   if ((st = check_ws(ws, ws_bytes, L.total)) != ATTN_OK) return st;
@@ -302,6 +314,7 @@ attn_status attn_decode_fp4(const attn_params* p, int32_t n_q, const attn_pages*
   a.part_o = reinterpret_cast<float*>(w + L.part_o);
   a.part_l = reinterpret_cast<float*>(w + L.part_l);
   a.ctas = L.ctas;
+  a.cluster = L.cluster;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   attn::Fp4Args f{cache_of(k), cache_of(v), k->descale, v->descale};
   if (pages->num_pages == 0)   // no cache to point at, and none is read
@@ -309,7 +322,7 @@ attn_status attn_decode_fp4(const attn_params* p, int32_t n_q, const attn_pages*
         static_cast<uint8_t*>(const_cast<void*>(q));
   if ((st = launched(attn::launch_fp4_decode(a, f, L.ctas, s), "4-bit decode launch")) != ATTN_OK)
     return st;
-  if (L.ctas == 1) return ATTN_OK;   // one CTA cuts nothing
+  if (L.cluster != 0 || L.ctas == 1) return ATTN_OK;   // merged already; one CTA cuts nothing
   return launched(attn::launch_paged_merge(a, L.n_notes, L.ctas, s), "4-bit decode merge launch");
 }
 
@@ -323,7 +336,7 @@ attn_status attn_key_weights(const attn_params* p, int32_t n_q, const attn_pages
   if (st != ATTN_OK) return st;
   if (k_cache != nullptr) {
     if (k != nullptr) return fail(ATTN_ERR_INVALID_ARG, "give k or k_cache, not both");
-    if ((st = check_cache(k_cache, pages->num_pages)) != ATTN_OK) return st;
+    if ((st = check_cache(k_cache, kv_heads(p), pages->num_pages)) != ATTN_OK) return st;
   } else if (!good_strides({p->kv_stride_b, p->kv_stride_h, p->kv_stride_n}, p->d)) {
     return fail(ATTN_ERR_INVALID_ARG, "kv strides must be positive multiples of 8, the last >= d");
   }

@@ -74,7 +74,8 @@ enum StallSite : int {
   kStallBwdCompute = 2,
   kStallPagedTile = 3,
   kStallPrefixSoftmax = 4,
-  kStallLatentSoftmax = 5
+  kStallLatentSoftmax = 5,
+  kStallEvictRead = 8
 };
 
 // Device status code for a kernel that found its shared memory misaligned

@@ -147,7 +147,7 @@ enum PagedSite : int {
   kSitePrefixP, kSitePrefixFree, kSitePrefixDone,
   kSiteLatentTile = 70, kSiteLatentS, kSiteLatentP, kSiteLatentFree, kSiteLatentDone, kSiteLatentQ,
   kSiteLatentSmem,
-  kSitePageIndex = 80
+  kSitePageIndex = 80, kSiteEvictRead
 };
 
 // What the weights of a merge, e^(L_i - base), are taken against: the largest

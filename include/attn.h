@@ -518,7 +518,10 @@ attn_status attn_selftest_timeout(void* ws, uint64_t limit_ns, void* stream);
  *   ATTN_STALL_PREFIX_SOFTMAX  the shared prefix's kernel (attn_decode_paged
  *                           with shared_len > 0 and two sequences or more), as
  *                           the forward's;
- *   ATTN_STALL_LATENT_SOFTMAX  attn_decode_latent, as the forward's.
+ *   ATTN_STALL_LATENT_SOFTMAX  attn_decode_latent, as the forward's;
+ *   ATTN_STALL_EVICT_READ   attn_pages_evict: a head's first keys that move are
+ *                           never reported as read (the cache's state is then
+ *                           undefined).
  * The wait on that barrier then runs out; every wait of that launch
  * gives up after `limit_ns` (clamped to [1 ms, 2 s]).  The kernel drains its
  * copies and MMAs, frees its tensor memory and returns, and the status words
@@ -532,7 +535,8 @@ typedef enum {
   ATTN_STALL_BWD_COMPUTE = 2,
   ATTN_STALL_PAGED_TILE = 3,
   ATTN_STALL_PREFIX_SOFTMAX = 4,
-  ATTN_STALL_LATENT_SOFTMAX = 5
+  ATTN_STALL_LATENT_SOFTMAX = 5,
+  ATTN_STALL_EVICT_READ = 8
 } attn_stall;
 attn_status attn_debug_stall(int32_t which, uint64_t limit_ns);
 
