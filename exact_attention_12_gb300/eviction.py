@@ -7,18 +7,20 @@ import torch
 
 from ._abi import lib
 from .fp4 import _cache
-from .paged import _PAGES, _PARAMS, _bf16, _call, _f32, _list, _strides, _table, _table_args
+from .paged import _PAGES, _PARAMS, _bf16, _call, _empty, _f32, _i32, _list, _strides, _table, _table_args
 
 _ROWS = struct.Struct("@P3q2i").pack   # attn_rows as bytes
 
 
 def _weights(weights, rows, heads, keys, index):
-    if weights.dtype is not _f32 or weights.get_device() != index or weights.dim() != 3 \
-            or weights.shape[:2] != (rows, heads) or weights.shape[2] < keys \
-            or (weights.stride(2) != 1 and weights.shape[2] > 1):
+    shape = weights.shape
+    if weights.dtype is not _f32 or weights.get_device() != index or len(shape) != 3 \
+            or shape[0] != rows or shape[1] != heads or shape[2] < keys \
+            or (weights.stride(2) != 1 and shape[2] > 1):
         raise ValueError("weights must be fp32 [sequences, H_kv, at least max_pages * page_size] "
                          "on the tensors' device, contiguous along the last axis")
-    return weights.data_ptr(), weights.stride(0), weights.stride(1)
+    step, head, _ = weights.stride()
+    return weights.data_ptr(), step, head
 
 
 def attention_key_weights(q, k_pages, page_table, cache_lens, lse, weights, *, k_scales=None,
@@ -111,7 +113,7 @@ def pages_evict(pools, page_table, cache_lens, refs, weights, seqs, new_lens, *,
     b, m = _list(new_lens, refs.device, "new_lens")
     if n != m:
         raise ValueError("seqs and new_lens must have the same length")
-    slots = refs.new_empty((n, heads, weights.shape[2]))
+    slots = _empty((n, heads, weights.shape[2]), dtype=_i32, device=refs.device)
     c = lib()
     _call(c.attn_pages_evict, c.attn_pages_evict_workspace_size, (t, heads, n, rows, len(pools)),
           (t, rows, len(pools), heads, *w, weights.shape[2], a, b, n, recent, slots.data_ptr()),

@@ -14,7 +14,7 @@ import torch
 
 from .api import _FP8
 from ._abi import lib
-from .paged import _PAGES, _PARAMS, _bf16, _call, _empty_like, _i32, _lse, _strides, _table
+from .paged import _PAGES, _PARAMS, _bf16, _call, _empty, _empty_like, _i32, _lse, _strides, _table
 
 _FP4 = struct.Struct("@PP4qfi").pack   # attn_fp4 as bytes
 _u8 = torch.uint8
@@ -25,22 +25,23 @@ def _cache(codes, scales, descale, index, what):
     if codes.dtype is not _u8 or scales.dtype is not _FP8 \
             or not index == codes.get_device() == scales.get_device():
         raise TypeError(f"{what}: codes must be uint8 and scales float8_e4m3fn, on one device")
-    half, shape = codes.shape, scales.shape
-    if len(half) != 4 or len(shape) != 4 or half[:3] != shape[:3] or half[3] != 8 * shape[3]:
+    if codes.ndim != 4 or scales.ndim != 4:
+        raise ValueError(f"{what}: codes and scales must have four dimensions")
+    P, H, size, n = scales.shape
+    if codes.shape != (P, H, size, 8 * n):
         raise ValueError(f"{what}: codes must be [num_pages, H_kv, page_size, d / 2], scales "
                          "[num_pages, H_kv, page_size, d / 16]")
-    P, H, size, n = shape
     if codes.is_contiguous() and scales.is_contiguous():
         # (a cache without heads has no strides to speak of)
         head = size * n
         page = (H or 1) * head
-        steps = 8 * page, 8 * head, page, head
-    else:
-        cs, ss = _strides(codes), _strides(scales)
-        if (cs[2], ss[2]) != (8 * n, n) and size > 1:
-            raise ValueError(f"{what}: a head's rows of a page must follow one another")
-        steps = cs[0], cs[1], ss[0], ss[1]
-    return _FP4(codes.data_ptr(), scales.data_ptr(), *steps, descale, 0), (P, H, size, 16 * n)
+        return _FP4(codes.data_ptr(), scales.data_ptr(), 8 * page, 8 * head, page, head, descale,
+                    0), (P, H, size, 16 * n)
+    cs, ss = _strides(codes), _strides(scales)
+    if (cs[2], ss[2]) != (8 * n, n) and size > 1:
+        raise ValueError(f"{what}: a head's rows of a page must follow one another")
+    return _FP4(codes.data_ptr(), scales.data_ptr(), cs[0], cs[1], ss[0], ss[1], descale,
+                0), (P, H, size, 16 * n)
 
 
 def _both(k_codes, k_scales, v_codes, v_scales, k_descale, v_descale, index):
@@ -144,7 +145,7 @@ def pages_load_fp4(k_codes, k_scales, v_codes, v_scales, page_table, cache_lens,
     kc, vc, cache = _both(k_codes, k_scales, v_codes, v_scales, k_descale, v_descale, index)
     _, H_kv, _, d = cache
     B = page_table.shape[0]
-    k = k_codes.new_empty((B, H_kv, n, d), dtype=_bf16)
+    k = _empty((B, H_kv, n, d), dtype=_bf16, device=k_codes.device)
     v = _empty_like(k)
     p, g, m = _copy_args(B, n, ((H_kv or 1) * (n or 1) * d, (n or 1) * d, d), cache, page_table,
                          cache_lens, counts, index)

@@ -14,7 +14,7 @@ import torch
 
 from . import _abi
 from ._abi import check_status, lib
-from .api import workspace
+from .api import _workspaces, workspace
 
 # The C structures (attn_params, attn_pages, attn_page_table) as bytes, which
 # ctypes passes as a pointer: a third of the time of filling a ctypes.Structure.
@@ -51,7 +51,9 @@ def _call(fn, size_fn, size_args, args, device, ws, what):
             return _call(fn, size_fn, size_args, args, device, ws, what)
     stream = _stream(index)
     if ws is None:
-        w = workspace(device, 256)
+        w = _workspaces.get(("cuda", index))   # (what workspace() would look up)
+        if w is None:
+            w = workspace(device, 256)
         st = fn(*args, w.data_ptr(), w.numel(), stream)
         if st == _abi.ATTN_ERR_WORKSPACE:
             need = size_fn(*size_args) if size_fn else 256
@@ -68,7 +70,7 @@ def _call(fn, size_fn, size_args, args, device, ws, what):
 
 
 def _int32(t, index, dim, what):
-    if t.dtype is not _i32 or t.get_device() != index or t.dim() != dim \
+    if t.dtype is not _i32 or t.get_device() != index or t.ndim != dim \
             or not (t.is_contiguous() or t.stride(-1) == 1):
         raise ValueError(f"{what} must be a {dim}-dimensional int32 tensor on the tensors' device, "
                          "contiguous along its last axis")
