@@ -55,7 +55,16 @@ struct WeightArgs {
   int64_t stride_b, stride_h;      // of the weights
   int add;
   int pass_rows;                   // query rows of a pass, set by the launcher
+  int ring;                        // key tiles in shared memory, set by the launcher
+  int stall;                       // kStallWeightsSum: see attn_debug_stall
 };
+// Many rows (attn_weights_tile.cu); tk: the cache of bf16, boxes of min(128, page) rows.
+cudaError_t launch_key_weights_tile(const CUtensorMap& tk, const PagedArgs& a, const WeightArgs& f,
+                                    int ctas, cudaStream_t s);
+// Rows of a head above which it is taken: 8 sequences of 8192 keys, 4 heads, 24 rows
+// 18.3 us with it, 16.9 without; 40 rows 18.8 and 20.2; 128 rows 18.5 and 37.2.
+constexpr int kWeightTileRows = 32;
+constexpr int kWeightTileOverhead = 2;    // a segment's cost beside its 128-key tiles
 cudaError_t launch_key_weights(const PagedArgs& a, WeightArgs f, int ctas, cudaStream_t s);
 
 constexpr int kWeightKeys = 32;
@@ -143,6 +152,12 @@ __device__ __forceinline__ void mma16816_half(float* c, const uint32_t* a, uint3
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// e with top 2^e in [2^14, 2^15); 0 for an infinite top.
+__device__ __forceinline__ int row_exponent(float top) {
+  const int ef = static_cast<int>(__float_as_uint(top) >> 23);
+  return ef == 255 ? 0 : min(141 - ef, 127);
+}
+
 // A row of Q, W words of bf16 pairs in each of the four lanes of equal lane / 4,
 // as fp16 pairs times 2^e, with the row's largest element in [2^14, 2^15)
 // (an infinite row: as it is).
@@ -155,8 +170,7 @@ __device__ __forceinline__ void half_rows(uint32_t* w, int* e) {
                            fabsf(__uint_as_float(w[i] & 0xffff0000u))));
   top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  const int ef = static_cast<int>(__float_as_uint(top) >> 23);
-  *e = ef == 255 ? 0 : min(141 - ef, 127);
+  *e = row_exponent(top);
   const float up = ldexpf(1.f, *e);
 #pragma unroll
   for (int i = 0; i < W; ++i)

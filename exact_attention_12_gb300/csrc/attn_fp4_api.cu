@@ -12,6 +12,7 @@ namespace {
 using attn::PagedArgs;
 
 constexpr size_t kHeaderBytes = 256;
+constexpr uint64_t kTimeoutNs = 2000000000ull;
 
 attn_status fail(attn_status s, const char* msg) {
   return static_cast<attn_status>(attn::record_error(s, msg));
@@ -364,13 +365,28 @@ attn_status attn_key_weights(const attn_params* p, int32_t n_q, const attn_pages
   f.stride_b = weight_stride_b;
   f.stride_h = weight_stride_h;
   f.add = add != 0;
-  const int64_t tiles = (static_cast<int64_t>(p->N) + attn::kWeightKeys - 1) / attn::kWeightKeys;
-  const int64_t want = static_cast<int64_t>(a.B) * a.heads * (tiles + attn::kWeightOverhead) /
-                       attn::kWeightMinUnits;
-  const int64_t most = 2 * sm_count();
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool many = a.head_rows > attn::kWeightTileRows;
+  const int keys = many ? attn::kTile : attn::kWeightKeys;
+  const int overhead = many ? attn::kWeightTileOverhead : attn::kWeightOverhead;
+  const int64_t tiles = (static_cast<int64_t>(p->N) + keys - 1) / keys;
+  const int64_t want = static_cast<int64_t>(a.B) * a.heads * (tiles + overhead) /
+                       (many ? 1 : attn::kWeightMinUnits);
+  const int64_t most = (many ? 1 : 2) * sm_count();
   const int ctas = static_cast<int>(want < 1 ? 1 : (want < most ? want : most));
-  return launched(attn::launch_key_weights(a, f, ctas, static_cast<cudaStream_t>(stream)),
-                  "key weights launch");
+  if (!many) return launched(attn::launch_key_weights(a, f, ctas, s), "key weights launch");
+  CUtensorMap tk{};
+  if (k_cache == nullptr) {
+    st = static_cast<attn_status>(attn::encode_pages(
+        &tk, k, pages->num_pages < 1 ? 1 : pages->num_pages, kv_heads(p), pages->page_size, p->d,
+        p->kv_stride_b, p->kv_stride_h, p->kv_stride_n,
+        pages->page_size < attn::kTile ? pages->page_size : attn::kTile));
+    if (st != ATTN_OK) return st;
+  }
+  PagedArgs b = a;
+  b.timeout_ns = kTimeoutNs;
+  f.stall = attn::take_stall(attn::kStallWeightsSum, &b.timeout_ns);
+  return launched(attn::launch_key_weights_tile(tk, b, f, ctas, s), "key weights launch");
 }
 
 }  // extern "C"

@@ -75,7 +75,8 @@ enum StallSite : int {
   kStallPagedTile = 3,
   kStallPrefixSoftmax = 4,
   kStallLatentSoftmax = 5,
-  kStallEvictRead = 8
+  kStallEvictRead = 8,
+  kStallWeightsSum = 9
 };
 
 // Device status code for a kernel that found its shared memory misaligned

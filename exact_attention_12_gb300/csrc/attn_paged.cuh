@@ -147,7 +147,8 @@ enum PagedSite : int {
   kSitePrefixP, kSitePrefixFree, kSitePrefixDone,
   kSiteLatentTile = 70, kSiteLatentS, kSiteLatentP, kSiteLatentFree, kSiteLatentDone, kSiteLatentQ,
   kSiteLatentSmem,
-  kSitePageIndex = 80, kSiteEvictRead
+  kSitePageIndex = 80, kSiteEvictRead,
+  kSiteWeightsK = 85, kSiteWeightsS, kSiteWeightsFree, kSiteWeightsRing
 };
 
 // What the weights of a merge, e^(L_i - base), are taken against: the largest

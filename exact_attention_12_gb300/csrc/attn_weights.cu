@@ -1,4 +1,5 @@
-// The attention weight that cached keys receive from query rows.
+// The attention weight that cached keys receive from the few query rows of a decode
+// step (up to 32 of a key/value head; more: attn_weights_tile.cu).
 //
 // What it computes: for key j of sequence b and key/value head h
 //   W[j] = sum_r exp(c q_r k_j - L_r),
@@ -7,17 +8,17 @@
 // gathered, or replaces it.  With L known there is no softmax to carry along and
 // nothing to merge: one pass over the keys, each by one warp.
 //
-// Bound: HBM for the few rows of a decode step, 2 d + 8 bytes a key (9 d / 16 + 8
-// in 4 bits); for the hundred rows of an observation window the exponentials,
-// 16 a clock and SM, and the products as much.
-//   * 16 x 8 x 16 warp MMAs whose fragments of K come straight from global memory
-//     into registers (the sum over d may go in any order, so lane (g, t) takes
-//     16-byte pieces of its keys) and stay there for all rows;
-//   * Q's fragments lie in shared memory in the order in which a warp reads them,
-//     up to 256 rows at a time;
-//   * the sum over a key's rows is each lane's own until the last row, then a few
+// Bound: HBM, 2 d + 8 bytes a key (9 d / 16 + 8 in 4 bits).
+//   * 16 x 8 x 16 warp MMAs, 16 keys by 8 rows, S^T = K Q^T: no lane idle at 8
+//     rows.  K's fragments come straight from global memory into registers (the
+//     sum over d may go in any order, so lane (g, t) takes 16-byte pieces of its
+//     keys), the next keys' while these are worked on;
+//   * Q's fragments lie in shared memory in the order in which a warp reads them;
+//   * the sum over a key's rows is each lane's own until the last row, then two
 //     shuffles.
 // Keys in 4 bits are unpacked as in attn_fp4.cu (exactly, to fp16).
+// Measured: 16 sequences of 2048-8192 keys, 32 heads over 8, d = 128, 173 MB in 30 us
+// = 5.8 TB/s.
 #include "attn_fp4.cuh"
 
 namespace attn {
@@ -27,7 +28,6 @@ namespace {
 
 constexpr int kWeightWarps = 8;
 constexpr int kWeightThreads = 32 * kWeightWarps;
-constexpr int kWeightRows = 256;        // query rows of one pass at most
 
 struct RowInfo {
   float c2, l2;   // score -> log2 units; L in them (+inf where the row gives nothing)
@@ -150,22 +150,14 @@ __device__ __forceinline__ RowInfo row_info(const PagedArgs& a, const WeightArgs
   return info;
 }
 
-// MANY: enough rows that the products take longer than the keys' way here.
-//   few rows    16 keys by 8 rows an MMA, no lane idle up to 8 rows; the next
-//               keys are on their way meanwhile
-//   many rows   16 rows by 8 keys: the keys' fragments are then the registers as
-//               they were loaded (as the other operand every use put them together
-//               anew: 161 instructions for 32 keys by 8 rows, now 95); 32 keys at
-//               a time share what is read of Q
-template <int D, bool PACKED, bool MANY>
+template <int D, bool PACKED>
 __global__ void __launch_bounds__(kWeightThreads, 2)
     key_weights_kernel(const PagedArgs a, const WeightArgs f) {
   constexpr int kSteps = D / 16, kWords = D / 8;
-  constexpr int kBlock = MANY ? 16 : 8;            // query rows of an MMA
-  constexpr int kParts = MANY || PACKED ? 4 : 2;   // keys of a lane at a time, 8 apart
+  constexpr int kParts = PACKED ? 4 : 2;   // keys of a lane at a time, 8 apart
   extern __shared__ __align__(16) uint8_t smem[];
   RowInfo* rows = reinterpret_cast<RowInfo*>(smem);       // [f.pass_rows]
-  uint8_t* frag = smem + f.pass_rows * sizeof(RowInfo);   // Q: [rows / kBlock][kSteps][32]
+  uint2* qf = reinterpret_cast<uint2*>(smem + f.pass_rows * sizeof(RowInfo));   // [rows / 8][kSteps][32]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   grid_dep_wait();
@@ -204,182 +196,86 @@ __global__ void __launch_bounds__(kWeightThreads, 2)
        p.valid; p = paged_next<kWeightKeys, kWeightOverhead>(a, share, p)) {
     const int tiles = p.t1 - p.t0 - warp;
     const int nv = tiles > 0 ? (tiles + kWeightWarps - 1) / kWeightWarps * 4 : 0;
-    for (int r0 = 0; r0 < a.head_rows; r0 += f.pass_rows) {   // (one pass but for very many rows)
-      const int nrows = min(a.head_rows - r0, f.pass_rows), blocks = (nrows + kBlock - 1) / kBlock;
-      __syncthreads();   // the rows before are no longer in use
-      for (int n = warp; n < blocks; n += kWeightWarps) {
-        uint32_t w[kBlock / 8][kWords];
+    const int blocks = (a.head_rows + 7) / 8;
+    __syncthreads();   // the rows before are no longer in use
+    for (int n = warp; n < blocks; n += kWeightWarps) {
+      const int r = 8 * n + g, at = p.h * a.head_rows + r;
+      const bool live = r < a.head_rows;
+      uint32_t w[kWords];
+      const float c2 = load_query<D, PACKED>(a, f, p.b, at, live, t, w);
+      if (t == 0) rows[r] = row_info(a, f, p.b, p.len, at, live, c2);
 #pragma unroll
-        for (int i = 0; i < kBlock / 8; ++i) {
-          const int r = kBlock * n + 8 * i + g, at = p.h * a.head_rows + r0 + r;
-          const bool live = r < nrows;
-          const float c2 = load_query<D, PACKED>(a, f, p.b, at, live, t, w[i]);
-          if (t == 0) rows[r] = row_info(a, f, p.b, p.len, at, live, c2);
-        }
+      for (int s = 0; s < kSteps; ++s)
+        qf[(n * kSteps + s) * 32 + lane] = make_uint2(w[2 * s], w[2 * s + 1]);
+    }
+    __syncthreads();
+    const bool ragged = (a.head_rows & 7) != 0;
+    if (nv > 0) load_pages(p, 0, nv >> 2);
+    KeyPart<D, PACKED> next[kParts];
+    if (nv > 0) load(p, 0, next);
+    for (int v = 0; v < nv; v += kParts) {
+      KeyPart<D, PACKED> now[kParts];
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-          const int at = (n * kSteps + s) * 32 + lane;
-          if constexpr (MANY)
-            reinterpret_cast<uint4*>(frag)[at] =
-                make_uint4(w[0][2 * s], w[1][2 * s], w[0][2 * s + 1], w[1][2 * s + 1]);
-          else
-            reinterpret_cast<uint2*>(frag)[at] = make_uint2(w[0][2 * s], w[0][2 * s + 1]);
-        }
+      for (int i = 0; i < kParts; ++i) now[i] = next[i];
+      if (v + kParts < nv) {
+        if (((v + kParts) & 127) == 0) load_pages(p, (v + kParts) >> 2, nv >> 2);
+        load(p, v + kParts, next);
       }
-      __syncthreads();
-      const bool ragged = nrows % kBlock != 0;
-      if (nv > 0) load_pages(p, 0, nv >> 2);
-      KeyPart<D, PACKED> part[kParts];
-      if (!MANY && nv > 0) load(p, 0, part);
-      for (int v = 0; v < nv; v += kParts) {
-        KeyPart<D, PACKED> now[kParts];
-        if constexpr (MANY) {
-          if ((v & 127) == 0 && v > 0) load_pages(p, v >> 2, nv >> 2);
-          load(p, v, part);
-        }
+      const int k0 = (p.t0 + warp + kWeightWarps * (v >> 2)) * kWeightKeys + 8 * (v & 3);
+      const bool masked = ragged || k0 + 8 * kParts > (a.causal ? p.len - a.n_q + 1 : p.len);
+      float* to = f.weights + p.b * f.stride_b + p.h * f.stride_h + k0;
+      // lanes t = 0, 1 have keys g, g + 8 of 16 to write
+      const int mine = g + 8 * (t & 1);
 #pragma unroll
-        for (int i = 0; i < kParts; ++i) now[i] = part[i];
-        if (!MANY && v + kParts < nv) {
-          if (((v + kParts) & 127) == 0) load_pages(p, (v + kParts) >> 2, nv >> 2);
-          load(p, v + kParts, part);
-        }
-        const int k0 = (p.t0 + warp + kWeightWarps * (v >> 2)) * kWeightKeys + 8 * (v & 3);
-        const bool masked =
-            ragged || k0 + 8 * kParts > (a.causal ? p.len - a.n_q + 1 : p.len);
-        float* to = f.weights + p.b * f.stride_b + p.h * f.stride_h + k0;
-        const bool add = f.add || r0 > 0;
-        if constexpr (MANY) {
-          uint32_t kb[4][kSteps][2];
+      for (int i = 0; i < kParts; i += 2) {
+        float before = 0.f, sum[2] = {0.f, 0.f};
+        const bool writes = t < 2 && k0 + mine + 8 * i < p.len;
+        if (f.add && writes) before = to[mine + 8 * i];
+        uint32_t kb[2][kSteps][2];
+        operands<D, PACKED>(now[i], kb[0]);
+        operands<D, PACKED>(now[i + 1], kb[1]);
+        for (int n = 0; n < blocks; ++n) {
+          float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) operands<D, PACKED>(now[i], kb[i]);
-          // lanes g = 0 ... 3 write keys 8 g + 2 t, + 1
-          const int mine = 8 * g + 2 * t;
-          float before[2] = {0.f, 0.f};
+          for (int s = 0; s < kSteps; ++s) {
+            const uint2 q = qf[(n * kSteps + s) * 32 + lane];
+            const uint32_t ka[4] = {kb[0][s][0], kb[1][s][0], kb[0][s][1], kb[1][s][1]};
+            if constexpr (PACKED) mma16816_half(c, ka, q.x, q.y);
+            else mma16816_bf16(c, ka, q.x, q.y);
+          }
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            if (add && g < 4 && k0 + mine + j < p.len) before[j] = to[mine + j];
-          float sum[4][2];
+          for (int j = 0; j < 2; ++j) {
+            const RowInfo info = rows[8 * n + 2 * t + j];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sum[i][0] = sum[i][1] = 0.f;
-          for (int n = 0; n < blocks; ++n) {
-            float c[4][4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0.f;
-#pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
-              const uint4 q = reinterpret_cast<const uint4*>(frag)[(n * kSteps + s) * 32 + lane];
-              const uint32_t qa[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if constexpr (PACKED) mma16816_half(c[i], qa, kb[i][s][0], kb[i][s][1]);
-                else mma16816_bf16(c[i], qa, kb[i][s][0], kb[i][s][1]);
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {   // rows g, g + 8
-              const RowInfo info = rows[16 * n + 8 * e + g];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  float x = ex2_approx(fmaf(c[i][2 * e + j], info.c2, -info.l2));
-                  if (masked && k0 + 8 * i + 2 * t + j >= info.lim) x = 0.f;
-                  sum[i][j] += x;
-                }
+            for (int e = 0; e < 2; ++e) {   // keys g, g + 8
+              float x = ex2_approx(fmaf(c[2 * e + j], info.c2, -info.l2));
+              if (masked && k0 + 8 * i + 8 * e + g >= info.lim) x = 0.f;
+              sum[e] += x;
             }
           }
-          float out[2] = {0.f, 0.f};
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              float x = sum[i][j];
-              x += __shfl_xor_sync(0xffffffffu, x, 4);
-              x += __shfl_xor_sync(0xffffffffu, x, 8);
-              x += __shfl_xor_sync(0xffffffffu, x, 16);
-              if (g == i) out[j] = x;
-            }
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            if (g < 4 && k0 + mine + j < p.len) to[mine + j] = before[j] + out[j];
-        } else {
-          // lanes t = 0, 1 have keys g, g + 8 of 16 to write
-          const int mine = g + 8 * (t & 1);
-#pragma unroll
-          for (int i = 0; i < kParts; i += 2) {
-            float before = 0.f, sum[2] = {0.f, 0.f};
-            const bool writes = t < 2 && k0 + mine + 8 * i < p.len;
-            if (add && writes) before = to[mine + 8 * i];
-            uint32_t kb[2][kSteps][2];
-            operands<D, PACKED>(now[i], kb[0]);
-            operands<D, PACKED>(now[i + 1], kb[1]);
-            for (int n = 0; n < blocks; ++n) {
-              float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-              for (int s = 0; s < kSteps; ++s) {
-                const uint2 q = reinterpret_cast<const uint2*>(frag)[(n * kSteps + s) * 32 + lane];
-                const uint32_t ka[4] = {kb[0][s][0], kb[1][s][0], kb[0][s][1], kb[1][s][1]};
-                if constexpr (PACKED) mma16816_half(c, ka, q.x, q.y);
-                else mma16816_bf16(c, ka, q.x, q.y);
-              }
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const RowInfo info = rows[8 * n + 2 * t + j];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {   // keys g, g + 8
-                  float x = ex2_approx(fmaf(c[2 * e + j], info.c2, -info.l2));
-                  if (masked && k0 + 8 * i + 8 * e + g >= info.lim) x = 0.f;
-                  sum[e] += x;
-                }
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
-              sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
-            }
-            if (writes) to[mine + 8 * i] = before + (t == 0 ? sum[0] : sum[1]);
-          }
         }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
+          sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
+        }
+        if (writes) to[mine + 8 * i] = before + (t == 0 ? sum[0] : sum[1]);
       }
     }
   }
 }
 
-// Query rows of a head above which MANY is taken: 8 sequences of 8192 keys, 24 rows
-// 18.0 us with it, 16.9 without; 40 rows 20.2 and 20.2; 128 rows 31.1 and 37.2.
-constexpr int kManyRows = 32;
-
-template <int D, bool PACKED, bool MANY>
-cudaError_t launch_rows(const PagedArgs& a, const WeightArgs& f, int ctas, cudaStream_t s) {
-  const size_t bytes = f.pass_rows * (sizeof(RowInfo) + D * 2);
-  static std::atomic<uint64_t> set_up{0};
-  int dev = 0;
-  bool todo = false;
-  cudaError_t e = needs_setup(set_up, &dev, &todo);
-  if (e != cudaSuccess) return e;
-  if (todo) {
-    e = cudaFuncSetAttribute(key_weights_kernel<D, PACKED, MANY>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kWeightRows * (sizeof(RowInfo) + D * 2));
-    if (e != cudaSuccess) return e;
-    mark_done(set_up, dev);
-  }
-  return launch_pdl(key_weights_kernel<D, PACKED, MANY>, dim3(ctas), dim3(kWeightThreads), bytes, s,
-                    a, f);
-}
-
 template <int D, bool PACKED>
 cudaError_t launch_kind(const PagedArgs& a, const WeightArgs& f, int ctas, cudaStream_t s) {
-  return a.head_rows > kManyRows ? launch_rows<D, PACKED, true>(a, f, ctas, s)
-                                 : launch_rows<D, PACKED, false>(a, f, ctas, s);
+  // (up to kWeightTileRows rows: less than the shared memory every kernel may have)
+  const size_t bytes = f.pass_rows * (sizeof(RowInfo) + D * 2);
+  return launch_pdl(key_weights_kernel<D, PACKED>, dim3(ctas), dim3(kWeightThreads), bytes, s, a, f);
 }
 
 }  // namespace
 
 cudaError_t launch_key_weights(const PagedArgs& a, WeightArgs f, int ctas, cudaStream_t s) {
-  const int rows = (a.head_rows + 15) / 16 * 16;
-  f.pass_rows = rows < kWeightRows ? rows : kWeightRows;
+  f.pass_rows = (a.head_rows + 7) / 8 * 8;
   if (f.k == nullptr)
     return a.d == 64 ? launch_kind<64, true>(a, f, ctas, s) : launch_kind<128, true>(a, f, ctas, s);
   return a.d == 64 ? launch_kind<64, false>(a, f, ctas, s) : launch_kind<128, false>(a, f, ctas, s);

@@ -521,7 +521,9 @@ attn_status attn_selftest_timeout(void* ws, uint64_t limit_ns, void* stream);
  *   ATTN_STALL_LATENT_SOFTMAX  attn_decode_latent, as the forward's;
  *   ATTN_STALL_EVICT_READ   attn_pages_evict: a head's first keys that move are
  *                           never reported as read (the cache's state is then
- *                           undefined).
+ *                           undefined);
+ *   ATTN_STALL_WEIGHTS_SUM  attn_key_weights with many rows of a head: a warp
+ *                           never gives its first scores back.
  * The wait on that barrier then runs out; every wait of that launch
  * gives up after `limit_ns` (clamped to [1 ms, 2 s]).  The kernel drains its
  * copies and MMAs, frees its tensor memory and returns, and the status words
@@ -536,7 +538,8 @@ typedef enum {
   ATTN_STALL_PAGED_TILE = 3,
   ATTN_STALL_PREFIX_SOFTMAX = 4,
   ATTN_STALL_LATENT_SOFTMAX = 5,
-  ATTN_STALL_EVICT_READ = 8
+  ATTN_STALL_EVICT_READ = 8,
+  ATTN_STALL_WEIGHTS_SUM = 9
 } attn_stall;
 attn_status attn_debug_stall(int32_t which, uint64_t limit_ns);
 

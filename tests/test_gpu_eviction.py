@@ -125,6 +125,30 @@ def test_a_bad_page_of_keys_is_reported(ea):  # noqa: F811
     assert torch.all(w == 1)    # exp(0 - 0), the missing page's keys being zero
 
 
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("n_q", [10, 70])
+def test_a_stalled_sum_of_many_rows_ends_and_reports(ea, packed, n_q):  # noqa: F811
+    from exact_attention_12_gb300 import _abi
+    lib = _abi.lib()
+    z = dict(device="cuda")
+    P = 640      # tiles enough for every CTA's ring to come round
+    k = torch.zeros(P, 1, 128, 32 if packed else 64, dtype=torch.uint8 if packed else torch.bfloat16, **z)
+    kw = dict(k_scales=torch.zeros(P, 1, 128, 4, **z).to(E4M3)) if packed else {}
+    t, n = torch.arange(P, dtype=torch.int32, **z).view(1, P), _i([P * 128])
+    q = torch.zeros(1, 8, n_q, 64, dtype=torch.bfloat16, **z)
+    w, lse = torch.zeros(1, 1, P * 128, **z), torch.zeros(1, 8, n_q, **z)
+    ws = torch.zeros(256, dtype=torch.uint8, **z)
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert lib.attn_debug_stall(_abi.ATTN_STALL_WEIGHTS_SUM, 20_000_000) == _abi.ATTN_OK
+    ea.attention_key_weights(q, k, t, n, lse, w, causal=False, ws=ws, **kw)
+    assert lib.attn_check(ws.data_ptr(), stream) == _abi.ATTN_ERR_TIMEOUT
+    assert int(lib.attn_last_error().decode().rsplit("wait site", 1)[1]) in range(85, 89)
+    for _ in range(2):
+        ea.attention_key_weights(q, k, t, n, lse, w, causal=False, ws=ws, add=False, **kw)
+        assert lib.attn_check(ws.data_ptr(), stream) == _abi.ATTN_OK
+        assert torch.all(w == 8 * n_q)      # exp(0 - 0) of every row
+
+
 def test_weights_of_nothing(ea):  # noqa: F811
     z = dict(device="cuda", dtype=torch.bfloat16)
     k, w = torch.zeros(3, 2, 16, 64, **z), torch.ones(1, 2, 32, device="cuda")
