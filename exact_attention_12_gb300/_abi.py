@@ -30,6 +30,7 @@ ATTN_STALL_PREFIX_SOFTMAX = 4
 ATTN_STALL_LATENT_SOFTMAX = 5
 ATTN_STALL_EVICT_READ = 8
 ATTN_STALL_WEIGHTS_SUM = 9
+ATTN_STALL_FP4_VALUES = 10
 
 # every function the header declares, with its ctypes signature
 EXPORTS = {

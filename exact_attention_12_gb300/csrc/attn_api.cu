@@ -770,8 +770,8 @@ attn_status attn_decode(const attn_params* p, int32_t n_q, const void* q, const 
 }
 
 attn_status attn_debug_stall(int32_t which, uint64_t limit_ns) {
-  if ((which < ATTN_STALL_NONE || which > ATTN_STALL_LATENT_SOFTMAX) && which != ATTN_STALL_EVICT_READ &&
-      which != ATTN_STALL_WEIGHTS_SUM)
+  if ((which < ATTN_STALL_NONE || which > ATTN_STALL_LATENT_SOFTMAX) &&
+      (which < ATTN_STALL_EVICT_READ || which > ATTN_STALL_FP4_VALUES))
     return fail(ATTN_ERR_INVALID_ARG, "unknown stall %d", which);
   if (limit_ns < 1000000ull) limit_ns = 1000000ull;          // 1 ms
   if (limit_ns > kTimeoutNs) limit_ns = kTimeoutNs;          // 2 s

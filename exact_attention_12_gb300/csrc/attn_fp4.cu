@@ -123,11 +123,6 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
   }
 }
 
-// base + page * step, the step in 32 bits (the host sees to that).
-__device__ __forceinline__ const uint8_t* page_at(const uint8_t* base, int page, int64_t step) {
-  return base + static_cast<uint64_t>(static_cast<uint32_t>(page)) * static_cast<uint32_t>(step);
-}
-
 // How the segments are given out.
 //   kSplit    the balanced split; what it cuts is merged by a second kernel
 //   kCluster  a segment per cluster of a.cluster CTAs (of one, perhaps), merged in

@@ -98,6 +98,14 @@ constexpr int fp4_cluster_tiles(int rows) { return rows <= 32 ? 24 : 12; }
 constexpr int kFp4SoloTiles = 24;
 constexpr int kFp4ManyTiles = 64;
 
+// Above 32 rows, d = 128, the balanced split goes to attn_fp4_tile.cu (64 sequences of
+// 16384 keys, 4 heads, 64 rows 373 us, attn_fp4.cu 474; 32 rows 271 and 230): tiles of
+// 128 keys, and its own constants in such tiles.
+cudaError_t launch_fp4_tile(const PagedArgs& a, const Fp4Args& f, int ctas, cudaStream_t s);
+constexpr int kFp4TileOverhead = 4;
+constexpr int kFp4TileMinUnits = 5;
+constexpr bool fp4_in_tiles(int rows, int d) { return rows > 32 && d == 128; }
+
 // CTAs of the decode kernel per SM at `rows` query rows of a segment: 16 warps of
 // up to 8 rows, 12 of 16, 8 of 32.
 constexpr int fp4_ctas_per_sm(int rows) {
@@ -150,6 +158,11 @@ __device__ __forceinline__ void mma16816_half(float* c, const uint32_t* a, uint3
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// base + page * step, the step in 32 bits (the host sees to that).
+__device__ __forceinline__ const uint8_t* page_at(const uint8_t* base, int page, int64_t step) {
+  return base + static_cast<uint64_t>(static_cast<uint32_t>(page)) * static_cast<uint32_t>(step);
 }
 
 // e with top 2^e in [2^14, 2^15); 0 for an infinite top.

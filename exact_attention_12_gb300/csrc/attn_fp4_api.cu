@@ -156,7 +156,7 @@ bool empty(const attn_params* p) { return p->B == 0 || p->H == 0; }
 struct Layout {
   size_t notes = 0, part_o = 0, part_l = 0, total = 0;
   int ctas = 0, n_notes = 0;
-  bool by_segment = false;
+  bool by_segment = false, tiled = false;
   int cluster = 0;   // CTAs of a segment's cluster; 0: the balanced split; -1: a warp a segment
   int heads = 0, blocks = 1, rows = 0, head_rows = 0;
 };
@@ -169,12 +169,9 @@ Layout decode_layout(const attn_params* p, int32_t n_q, const attn_pages* g) {
   L.blocks = (L.head_rows + attn::kDecMaxRows - 1) / attn::kDecMaxRows;
   L.rows = L.blocks > 0 ? (L.head_rows + L.blocks - 1) / L.blocks : 0;
   L.heads = H_kv * L.blocks;
-  const int64_t most = attn::fp4_ctas_per_sm(L.rows) * sms;
+  int64_t most = attn::fp4_ctas_per_sm(L.rows) * sms;   // CTAs at a time
   const int64_t tiles = (static_cast<int64_t>(p->N) + attn::kFp4Keys - 1) / attn::kFp4Keys;
   const int64_t segments = static_cast<int64_t>(p->B) * L.heads;
-  const int64_t want = segments * (tiles + attn::fp4_overhead(L.rows)) / attn::kFp4MinUnits;
-  L.ctas = static_cast<int>(most < want ? most : want);
-  if (L.ctas < 1) L.ctas = 1;
   // Short caches need no balance: a cluster per segment, of as many CTAs as the GPU
   // holds at once and as have a tile for each of their warps, if that leaves each
   // few tiles; a warp per segment where there are more segments than that.
@@ -186,6 +183,16 @@ Layout decode_layout(const attn_params* p, int32_t n_q, const attn_pages* g) {
   } else if (tiles <= c * attn::fp4_cluster_tiles(L.rows)) {
     L.cluster = c;
   }
+  // the balanced split: CTAs that have the smallest share worth one at full caches
+  int64_t want = segments * (tiles + attn::fp4_overhead(L.rows)) / attn::kFp4MinUnits;
+  L.tiled = L.cluster == 0 && attn::fp4_in_tiles(L.rows, p->d);
+  if (L.tiled) {
+    most = sms;
+    want = segments * ((static_cast<int64_t>(p->N) + attn::kTile - 1) / attn::kTile +
+                       attn::kFp4TileOverhead) / attn::kFp4TileMinUnits;
+  }
+  L.ctas = static_cast<int>(most < want ? most : want);
+  if (L.ctas < 1) L.ctas = 1;
   L.by_segment = segments <= L.ctas;
   L.n_notes = L.by_segment ? static_cast<int>(segments) : L.ctas;
   size_t off = kHeaderBytes;
@@ -321,7 +328,13 @@ attn_status attn_decode_fp4(const attn_params* p, int32_t n_q, const attn_pages*
   if (pages->num_pages == 0)   // no cache to point at, and none is read
     f.k.codes = f.k.scales = f.v.codes = f.v.scales =
         static_cast<uint8_t*>(const_cast<void*>(q));
-  if ((st = launched(attn::launch_fp4_decode(a, f, L.ctas, s), "4-bit decode launch")) != ATTN_OK)
+  if (L.tiled) {
+    a.timeout_ns = kTimeoutNs;
+    a.stall = attn::take_stall(attn::kStallFp4Values, &a.timeout_ns);
+  }
+  if ((st = launched(L.tiled ? attn::launch_fp4_tile(a, f, L.ctas, s)
+                             : attn::launch_fp4_decode(a, f, L.ctas, s),
+                     "4-bit decode launch")) != ATTN_OK)
     return st;
   if (L.cluster != 0 || L.ctas == 1) return ATTN_OK;   // merged already; one CTA cuts nothing
   return launched(attn::launch_paged_merge(a, L.n_notes, L.ctas, s), "4-bit decode merge launch");

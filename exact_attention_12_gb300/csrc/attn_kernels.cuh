@@ -76,7 +76,8 @@ enum StallSite : int {
   kStallPrefixSoftmax = 4,
   kStallLatentSoftmax = 5,
   kStallEvictRead = 8,
-  kStallWeightsSum = 9
+  kStallWeightsSum = 9,
+  kStallFp4Values = 10
 };
 
 // Device status code for a kernel that found its shared memory misaligned

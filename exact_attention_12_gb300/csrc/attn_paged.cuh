@@ -148,7 +148,8 @@ enum PagedSite : int {
   kSiteLatentTile = 70, kSiteLatentS, kSiteLatentP, kSiteLatentFree, kSiteLatentDone, kSiteLatentQ,
   kSiteLatentSmem,
   kSitePageIndex = 80, kSiteEvictRead,
-  kSiteWeightsK = 85, kSiteWeightsS, kSiteWeightsFree, kSiteWeightsRing
+  kSiteWeightsK = 85, kSiteWeightsS, kSiteWeightsFree, kSiteWeightsRing,
+  kSiteFp4Q = 90, kSiteFp4K, kSiteFp4V, kSiteFp4S, kSiteFp4P, kSiteFp4Free, kSiteFp4Ring, kSiteFp4Done
 };
 
 // What the weights of a merge, e^(L_i - base), are taken against: the largest

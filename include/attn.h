@@ -523,7 +523,9 @@ attn_status attn_selftest_timeout(void* ws, uint64_t limit_ns, void* stream);
  *                           never reported as read (the cache's state is then
  *                           undefined);
  *   ATTN_STALL_WEIGHTS_SUM  attn_key_weights with many rows of a head: a warp
- *                           never gives its first scores back.
+ *                           never gives its first scores back;
+ *   ATTN_STALL_FP4_VALUES   attn_decode_fp4 with more than 16 rows of a head, d =
+ *                           128, long caches: the first values never arrive.
  * The wait on that barrier then runs out; every wait of that launch
  * gives up after `limit_ns` (clamped to [1 ms, 2 s]).  The kernel drains its
  * copies and MMAs, frees its tensor memory and returns, and the status words
@@ -539,7 +541,8 @@ typedef enum {
   ATTN_STALL_PREFIX_SOFTMAX = 4,
   ATTN_STALL_LATENT_SOFTMAX = 5,
   ATTN_STALL_EVICT_READ = 8,
-  ATTN_STALL_WEIGHTS_SUM = 9
+  ATTN_STALL_WEIGHTS_SUM = 9,
+  ATTN_STALL_FP4_VALUES = 10
 } attn_stall;
 attn_status attn_debug_stall(int32_t which, uint64_t limit_ns);
 
