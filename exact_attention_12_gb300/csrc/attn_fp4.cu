@@ -724,7 +724,8 @@ cudaError_t launch_rows(const PagedArgs& a, const Fp4Args& f, int ctas, cudaStre
   if (a.cluster > 0) return launch_mode<D, NT, MT, kCluster>(a, f, ctas, s);
   if constexpr (MT == 1)
     if (a.cluster < 0) return launch_mode<D, NT, MT, kSolo>(a, f, ctas, s);
-  return launch_mode<D, NT, MT, kSplit>(a, f, ctas, s);
+  if constexpr (!fp4_in_tiles(8 * NT * MT, D)) return launch_mode<D, NT, MT, kSplit>(a, f, ctas, s);
+  return cudaErrorInvalidValue;   // (launch_fp4_tile's)
 }
 
 template <int D>

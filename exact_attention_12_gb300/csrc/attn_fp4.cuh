@@ -98,9 +98,10 @@ constexpr int fp4_cluster_tiles(int rows) { return rows <= 32 ? 24 : 12; }
 constexpr int kFp4SoloTiles = 24;
 constexpr int kFp4ManyTiles = 64;
 
-// Above 32 rows, d = 128, the balanced split goes to attn_fp4_tile.cu (64 sequences of
-// 16384 keys, 4 heads, 64 rows 373 us, attn_fp4.cu 474; 32 rows 271 and 230): tiles of
-// 128 keys, and its own constants in such tiles.
+// Above 32 rows, d = 128, the balanced split goes to attn_fp4_tile.cu: tiles of 128 keys,
+// and its own constants in such tiles.  64 sequences of 16384 keys, 4 heads, 36 rows
+// 348 us, attn_fp4.cu 469; 64 rows 348 and 474; 32 rows 343 and 230, with 16 rows a
+// softmax group 252.
 cudaError_t launch_fp4_tile(const PagedArgs& a, const Fp4Args& f, int ctas, cudaStream_t s);
 constexpr int kFp4TileOverhead = 4;
 constexpr int kFp4TileMinUnits = 5;

@@ -219,7 +219,8 @@ def test_evict_refuses(lib, kw, status):
 
 def test_the_waits_can_be_stalled(lib):
     from exact_attention_12_gb300 import _abi
-    for which in (_abi.ATTN_STALL_EVICT_READ, _abi.ATTN_STALL_WEIGHTS_SUM, _abi.ATTN_STALL_NONE):
+    for which in (_abi.ATTN_STALL_EVICT_READ, _abi.ATTN_STALL_WEIGHTS_SUM, _abi.ATTN_STALL_FP4_VALUES,
+                  _abi.ATTN_STALL_NONE):
         assert lib.attn_debug_stall(which, 1) == _abi.ATTN_OK
 
 

@@ -11,6 +11,8 @@ bf16: |O - O*| <= (2^-11 + 2 L_MAX_ABS) sum_j P_j |V_j| + 2^-25 sum_j |V_j| + 2^
 with a hundredth on top for the products of these.
 """
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -220,6 +222,107 @@ def test_a_page_outside_the_cache_reads_as_zeros(ea, room):  # noqa: F811
     want = oracle.paged_decode(np64(q), fp4.decode(zero[0], zero[1], 1.0),
                                fp4.decode(zero[2], zero[3], 1.0), t, lens, 0.01)
     _hold(o, lse, want, 1e4)
+
+
+# ----------------------------------- decode: many rows, long tables, d = 128 --
+
+@pytest.mark.parametrize("page", [16, 32, 64, 256])
+@pytest.mark.parametrize("causal", [True, False])
+def test_page_sizes_of_many_rows(ea, page, causal):  # noqa: F811
+    # (causal: rows that attend nothing where n_q exceeds the sequence)
+    _decode(ea, [0, 1, 15, 16, 33, 127, 128, 129, 700, 2000], 24, 2, 4, 128, page, causal, seed=page,
+            room=WIDE)
+
+
+# 33 to 64 rows: both halves full, one of them part full; 72 in two blocks of 36
+@pytest.mark.parametrize("H,n_q", [(33, 1), (12, 4), (49, 1), (1, 64), (72, 1), (3, 24)])
+@pytest.mark.parametrize("layout", ["hnd", "nhd", "apart"])
+def test_many_rows_of_long_sequences(ea, H, n_q, layout):  # noqa: F811
+    _decode(ea, [30000, 5], H, 1, n_q, 128, 64, seed=H, layout=layout)
+
+
+def test_many_rows_of_many_sequences(ea):  # noqa: F811
+    # more segments than CTAs, pieces that end and begin inside a CTA, empty ones
+    rng = np.random.default_rng(12)
+    lens = [int(x) for x in rng.integers(0, 700, 170)]
+    lens[3] = lens[4] = lens[-1] = 0
+    lens[5] = 4100
+    _decode(ea, lens, 40, 1, 1, 128, 16, seed=12)
+
+
+@pytest.mark.parametrize("q_scale", [2.0 ** -60, 2.0 ** 70])
+def test_magnitudes_of_many_rows(ea, q_scale):  # noqa: F811
+    _decode(ea, [150, 33], 40, 1, 1, 128, 16, q_scale=q_scale, seed=4, room=WIDE)
+    _decode(ea, [150, 33], 40, 1, 1, 128, 16, k_descale=3e20, v_descale=2.0 ** -99, seed=4, room=WIDE)
+
+
+def test_large_scores_of_many_rows(ea):  # noqa: F811
+    # scores to +-100, over many tiles: maxima rise late, and O is scaled in place
+    _decode(ea, [2500, 64], 48, 1, 1, 128, 32, scale=3.0 * 0.25, seed=11, room=WIDE)
+
+
+def test_many_rows_some_of_them_no_numbers(ea):  # noqa: F811
+    rng = np.random.default_rng(5)
+    lens = [700, 40]
+    table, P = _table(rng, lens, 16, room=WIDE)
+    k, v = (_cache(rng, table, lens, P, 1, 16, 128) for _ in range(2))
+    q = torch.randn(2, 40, 1, 128, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    args = (*_on_gpu(*k), *_on_gpu(*v), torch.from_numpy(table).cuda(), _i(lens))
+    want, want_l = ea.attention_decode_fp4(q.cuda(), *args, scale=0.01)
+    odd = q.clone()
+    odd[0, 2, 0, 5], odd[0, 33, 0, 7] = float("nan"), float("nan")
+    odd[1, 3, 0, 9], odd[1, 39, 0, 100] = float("inf"), -float("inf")
+    o, lse = ea.attention_decode_fp4(odd.cuda(), *args, scale=0.01)
+    ea.check()
+    for b, h in ((0, 2), (0, 33), (1, 3), (1, 39)):
+        assert torch.isnan(o[b, h]).all() and torch.isnan(lse[b, h]).all()
+    keep = torch.ones(2, 40, dtype=torch.bool)
+    keep[0, 2] = keep[0, 33] = keep[1, 3] = keep[1, 39] = False
+    assert torch.equal(o.cpu()[keep], want.cpu()[keep])
+    assert torch.equal(lse.cpu()[keep], want_l.cpu()[keep])
+
+
+@pytest.mark.parametrize("page", [16, 64])
+def test_a_page_outside_the_cache_under_many_rows(ea, page):  # noqa: F811
+    from exact_attention_12_gb300 import AttnError
+    rng = np.random.default_rng(6)
+    lens = [700, 140]
+    table, P = _table(rng, lens, page, room=WIDE)
+    k, v = (_cache(rng, table, lens, P, 1, page, 128) for _ in range(2))
+    bad = table.copy()
+    bad[0, 2], bad[0, 7], bad[1, 1] = P, -5, 2 ** 31 - 1
+    q = torch.randn(2, 40, 1, 128, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    o, lse = ea.attention_decode_fp4(q.cuda(), *_on_gpu(*k), *_on_gpu(*v),
+                                     torch.from_numpy(bad).cuda(), _i(lens), scale=0.01)
+    with pytest.raises(AttnError) as e:
+        ea.check()
+    assert e.value.status == 6
+    zero = [np.concatenate([x, np.zeros_like(x[:1])]) for x in (*k, *v)]
+    t = np.where((bad < 0) | (bad >= P), P, bad)
+    want = oracle.paged_decode(np64(q), fp4.decode(zero[0], zero[1], 1.0),
+                               fp4.decode(zero[2], zero[3], 1.0), t, lens, 0.01)
+    _hold(o, lse, want, 1e5)
+
+
+def test_a_stalled_step_of_many_rows_ends_and_reports(ea):  # noqa: F811
+    from exact_attention_12_gb300 import _abi
+    lib = _abi.lib()
+    z = dict(device="cuda")
+    P = 640
+    codes = torch.full((P, 1, 128, 64), 0x22, dtype=torch.uint8, **z)       # ones
+    scales = torch.full((P, 1, 128, 8), 0x38, dtype=torch.uint8, **z).view(E4M3)
+    t, n = torch.arange(P, dtype=torch.int32, **z).view(1, P), _i([P * 128])
+    q = torch.zeros(1, 40, 1, 128, dtype=torch.bfloat16, **z)
+    ws = torch.zeros(1 << 24, dtype=torch.uint8, **z)
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert lib.attn_debug_stall(_abi.ATTN_STALL_FP4_VALUES, 20_000_000) == _abi.ATTN_OK
+    ea.attention_decode_fp4(q, codes, scales, codes, scales, t, n, ws=ws)
+    assert lib.attn_check(ws.data_ptr(), stream) == _abi.ATTN_ERR_TIMEOUT
+    assert int(lib.attn_last_error().decode().rsplit("wait site", 1)[1]) in range(90, 98)
+    for _ in range(2):
+        o, lse = ea.attention_decode_fp4(q, codes, scales, codes, scales, t, n, ws=ws)
+        assert lib.attn_check(ws.data_ptr(), stream) == _abi.ATTN_OK
+        assert torch.all(o == 1) and torch.all((lse - float(np.log(P * 128))).abs() <= L_MAX_ABS)
 
 
 def test_nothing_to_do(ea):  # noqa: F811
