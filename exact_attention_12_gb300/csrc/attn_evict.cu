@@ -551,6 +551,10 @@ int check_evict(const attn_page_table* t, int32_t heads, int32_t n, const attn_r
     total += p.row_bytes;
   }
   if (total > 32768) return bad(ATTN_ERR_UNSUPPORTED, "pools: more than 32768 bytes a row");
+  for (int i = 0; i < n_pools && heads > 0; ++i)
+    if ((t->num_pages > 1 && pools[i].page_stride < pools[i].row_bytes) ||
+        (heads > 1 && pools[i].head_stride < pools[i].row_bytes))
+      return bad(ATTN_ERR_INVALID_ARG, "pools: pages and heads must be apart");
   return ATTN_OK;
 }
 
@@ -646,9 +650,10 @@ attn_status attn_pages_evict(const attn_page_table* t, const attn_rows* pools, i
   if (st != ATTN_OK) return static_cast<attn_status>(st);
   if (recent < 0) return static_cast<attn_status>(bad(ATTN_ERR_INVALID_ARG, "recent is negative"));
   const int64_t cap = static_cast<int64_t>(t->max_pages) * t->page_size;
-  if (width < cap || weight_stride_row < 0 || weight_stride_head < 0)
+  if (width < cap || weight_stride_row < (t->rows > 1 ? cap : 0) ||
+      weight_stride_head < (heads > 1 ? cap : 0))
     return static_cast<attn_status>(
-        bad(ATTN_ERR_INVALID_ARG, "weights: width below max_pages * page_size, or negative stride"));
+        bad(ATTN_ERR_INVALID_ARG, "weights: width or strides below max_pages * page_size"));
   const EvictLayout L = evict_layout(t, heads, n, pools, n_pools);
   if (static_cast<int64_t>(n) * heads * L.chunks >= (int64_t{1} << 30))
     return static_cast<attn_status>(bad(ATTN_ERR_UNSUPPORTED, "more than 2^30 chunks to move"));

@@ -354,8 +354,8 @@ attn_status attn_key_weights(const attn_params* p, int32_t n_q, const attn_pages
   } else if (!good_strides({p->kv_stride_b, p->kv_stride_h, p->kv_stride_n}, p->d)) {
     return fail(ATTN_ERR_INVALID_ARG, "kv strides must be positive multiples of 8, the last >= d");
   }
-  if (weight_stride_b < 0 || weight_stride_h < 0)
-    return fail(ATTN_ERR_INVALID_ARG, "weights: negative stride");
+  if (weight_stride_b < (p->B > 1 ? p->N : 0) || weight_stride_h < (kv_heads(p) > 1 ? p->N : 0))
+    return fail(ATTN_ERR_INVALID_ARG, "weights: sequences and heads must be N entries apart at least");
   if ((st = check_ws(ws, ws_bytes, kHeaderBytes)) != ATTN_OK) return st;
   if (empty(p) || p->N == 0) return ATTN_OK;
   if (k_cache == nullptr && pages->num_pages == 0) k = q;   // no cache to point at

@@ -56,9 +56,10 @@
  * which attn_check() returns.
  *
  * CUDA graphs: attn_fwd, attn_bwd, the decode steps and the calls on paged
- * caches (attn_decode_paged, attn_decode_latent, attn_pages_*) neither
- * synchronise nor allocate, and every launch argument (tensor maps included) is passed by
- * value, so the calls can be captured into a CUDA graph and replayed.  Make
+ * caches (attn_decode_paged, _latent and _fp4, attn_key_weights, attn_pages_*)
+ * neither synchronise nor allocate, and every launch argument (tensor maps
+ * included) is passed by value, so the calls can be captured into a CUDA graph
+ * and replayed.  Make
  * one uncaptured call of each kind first: it sets the kernels' attributes.
  * The forward and backward kernels and those on paged caches are launched
  * with programmatic stream serialisation; each waits for the preceding work in
@@ -386,7 +387,7 @@ attn_status attn_decode_fp4(const attn_params* p, int32_t n_q, const attn_pages*
  *   k         [num_pages, H_kv, page_size, d] bf16 with the kv strides, or NULL and
  *   k_cache   a cache in 4 bits (then NULL otherwise)
  *   weights   fp32, weight_stride_b and weight_stride_h entries between sequences
- *             and heads, max_pages * page_size entries of a head at least
+ *             and heads, each max_pages * page_size at least (where there are two)
  * ws: 256 bytes. */
 attn_status attn_key_weights(const attn_params* p, int32_t n_q, const attn_pages* pages,
                              const void* q, const void* k, const attn_fp4* k_cache,
@@ -462,7 +463,7 @@ attn_status attn_pages_compact(const attn_page_table* t, const attn_pool* pools,
 
 /* A buffer of pages by its rows: row r of head h in page g is row_bytes bytes at
  * base + g * page_stride + h * head_stride + r * row_stride (bytes).  Everything a
- * multiple of 4; rows apart. */
+ * multiple of 4; rows, heads and pages apart. */
 typedef struct attn_rows {
   void* base;
   int64_t page_stride, head_stride, row_stride;
@@ -478,7 +479,7 @@ typedef struct attn_rows {
  * back as in attn_pages_free.  A sequence that is not longer than new_lens[i] stays
  * as it is.
  *   weights    fp32 [rows][heads][width], weight_stride_row and weight_stride_head
- *              entries apart, width >= max_pages * page_size
+ *              entries apart; these and width >= max_pages * page_size
  *   slots      device int32 [n][heads][width], output: slots[i][h][j] is where the
  *              key that is now in place j was before; -1 from the new length on,
  *              -2 throughout where a sequence was refused
@@ -524,7 +525,7 @@ attn_status attn_selftest_timeout(void* ws, uint64_t limit_ns, void* stream);
  *                           undefined);
  *   ATTN_STALL_WEIGHTS_SUM  attn_key_weights with many rows of a head: a warp
  *                           never gives its first scores back;
- *   ATTN_STALL_FP4_VALUES   attn_decode_fp4 with more than 16 rows of a head, d =
+ *   ATTN_STALL_FP4_VALUES   attn_decode_fp4 with more than 32 rows of a head, d =
  *                           128, long caches: the first values never arrive.
  * The wait on that barrier then runs out; every wait of that launch
  * gives up after `limit_ns` (clamped to [1 ms, 2 s]).  The kernel drains its

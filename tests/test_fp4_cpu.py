@@ -217,6 +217,35 @@ def test_evict_refuses(lib, kw, status):
     assert _evict(lib, n=0)[0] == 0 and _evict(lib, heads=0)[0] == 0 and _evict(lib)[1] > 256
 
 
+@pytest.mark.parametrize("kw", [dict(page_stride=0), dict(page_stride=124), dict(head_stride=0)])
+def test_evict_refuses_pools_that_overlap(lib, kw):
+    assert _evict(lib, **kw)[0] == 1
+    one = dict(num_pages=1) if "page_stride" in kw else dict(heads=1)
+    assert _evict(lib, **{**kw, **one, "n": 0})[0] == 0     # nothing to be apart from
+
+
+@pytest.mark.parametrize("row,head", [(0, 64), (128, 0), (63, 64), (128, 63), (0, 0)])
+def test_weights_that_overlap_are_refused(lib, row, head):
+    # (what expand() gives: several would add to one entry)
+    from exact_attention_12_gb300 import _abi
+    p, g, c, _ = _step(lib, B=2, N=64, max_pages=4, table_stride=4)
+    call = lambda: lib.attn_key_weights(  # noqa: E731
+        ctypes.byref(p), 1, ctypes.byref(g), FAKE, None, ctypes.byref(c), FAKE, FAKE, row, head, 1, FAKE,
+        256, None)
+    assert call() == 1 and b"apart" in lib.attn_last_error()
+    p.B = 0     # passes every check, and enqueues nothing, where only one is left
+    assert call() == (1 if head < 64 else 0)
+    t = _abi.AttnPageTable()
+    t.table = t.lens = t.refs = FAKE
+    t.table_stride = t.max_pages = 4
+    t.rows, t.page_size, t.num_pages = 2, 16, 8
+    call = lambda: lib.attn_pages_evict(  # noqa: E731
+        ctypes.byref(t), None, 0, 2, FAKE, row, head, 64, FAKE, FAKE, 0, 0, FAKE, FAKE, 1 << 20, None)
+    assert call() == 1 and b"strides" in lib.attn_last_error()
+    t.rows = 1
+    assert call() == (1 if head < 64 else 0)
+
+
 def test_the_waits_can_be_stalled(lib):
     from exact_attention_12_gb300 import _abi
     for which in (_abi.ATTN_STALL_EVICT_READ, _abi.ATTN_STALL_WEIGHTS_SUM, _abi.ATTN_STALL_FP4_VALUES,
