@@ -324,11 +324,13 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const EvictAr
   if (C > 1) cluster_sync();   // the others have read this CTA's counts
 }
 
+// (Rows lie scattered, and L2 fetches 128 bytes where it is not told otherwise: 4
+// sequences of 95000 4-bit keys 98 us, with 64 bytes 92.)
 __device__ __forceinline__ void copy_async(uint8_t* dst, const char* src, int unit) {
   const uint32_t d = smem_u32(dst);
   const uint64_t s = reinterpret_cast<uint64_t>(src);
-  if (unit == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(s) : "memory");
-  else if (unit == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(s) : "memory");
+  if (unit == 16) asm volatile("cp.async.cg.shared.global.L2::64B [%0], [%1], 16;" ::"r"(d), "l"(s) : "memory");
+  else if (unit == 8) asm volatile("cp.async.ca.shared.global.L2::64B [%0], [%1], 8;" ::"r"(d), "l"(s) : "memory");
   else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(s) : "memory");
 }
 
