@@ -100,8 +100,8 @@ constexpr int kFp4ManyTiles = 64;
 
 // Above 32 rows, d = 128, the balanced split goes to attn_fp4_tile.cu: tiles of 128 keys,
 // and its own constants in such tiles.  64 sequences of 16384 keys, 4 heads, 36 rows
-// 348 us, attn_fp4.cu 469; 64 rows 348 and 474; 32 rows 343 and 230, with 16 rows a
-// softmax group 252.
+// 299 us, attn_fp4.cu 469; 64 rows 303 and 474; 32 rows, with two tiles of 32 rows at a
+// time, 269 and 230.
 cudaError_t launch_fp4_tile(const PagedArgs& a, const Fp4Args& f, int ctas, cudaStream_t s);
 constexpr int kFp4TileOverhead = 4;
 constexpr int kFp4TileMinUnits = 5;

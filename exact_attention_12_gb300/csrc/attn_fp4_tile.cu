@@ -13,14 +13,14 @@
 //   O^T += V^T P^T   128 columns x rows; V and P lie as they were written, a key's
 //                    columns (rows) side by side, which tcgen05 takes as M- and
 //                    N-major operands
-//   warps 0-3, 4-7  Q, softmax, write-out, each of half of the rows
-//   warp 8       MMA issue, the next tile's S before this one's O
-//   warps 12-19  unpacking, four K and four V: four lanes a key, their 16 bytes of codes
+//   warps 0-15   Q, softmax, write-out: four groups of 16 rows each (two of 32: 348 us)
+//   warp 16      MMA issue, the next tile's S before this one's O
+//   warps 20-27  unpacking, four K and four V: four lanes a key, their 16 bytes of codes
 //                and two scales a tile ahead in registers and six in L2
-// 64 sequences of 16384 keys, 4 heads, 64 rows (604 MB): 348 us, 1.76 TB/s.  A tile takes
-// 6600 warp instructions, half of what an SM issues in that time, and 3000 clocks: two
-// tiles in flight do not cover the way from a score to its product.  The tensor cores
-// are busy for a seventh of it.
+// 64 sequences of 16384 keys, 4 heads, 64 rows (604 MB): 303 us, 2.0 TB/s; 2700 clocks a
+// tile.  Its 6600 warp instructions are 1650 of them, its way through shared memory
+// (unpacked values in, operands out) 1400, and the groups go from a score to its weight
+// in step; the tensor cores are busy for a sixth.  S and O from two issuing warps: 318.
 // Rounding and what may lie where no key is attended: as in attn_fp4.cu.
 #include "attn_fp4.cuh"
 
@@ -30,16 +30,16 @@ using namespace sm103;
 namespace {
 
 constexpr int kD = 128;
-constexpr int kSoftWarps = 4;                      // of a softmax group; there are two
-constexpr int kIssueWarp = 8, kUnpackWarp = 12;    // then four for K, four for V
+constexpr int kGroups = 4, kSoftWarps = 4;         // softmax groups; warps of one
+constexpr int kIssueWarp = 16, kUnpackWarp = 20;   // then four for K, four for V
 constexpr int kTileThreads = 32 * (kUnpackWarp + 8);
-// registers re-split between the five warpgroups after the start
-constexpr uint32_t kRegsLaunch = 96, kRegsSoft = 136, kRegsIssue = 48, kRegsUnpack = 80;
-static_assert(2 * kRegsSoft + kRegsIssue + 2 * kRegsUnpack <= 5 * kRegsLaunch,
+// registers re-split between the seven warpgroups after the start
+constexpr uint32_t kRegsLaunch = 72, kRegsSoft = 80, kRegsIssue = 40;
+static_assert(kGroups * kRegsSoft + kRegsIssue + 2 * kRegsLaunch <= 7 * kRegsLaunch,
               "register re-split exceeds the launch allocation");
 constexpr int kTileStages = 2;                     // of every ring
 constexpr int kRowsMax = 64;
-constexpr int kGroupRows = kRowsMax / 2;           // rows of a softmax group
+constexpr int kGroupRows = kRowsMax / kGroups;     // rows of a softmax group
 constexpr int kBox = kTile * 128;                  // 64 columns of 128 keys
 constexpr int kKeysBytes = kD / 64 * kBox;         // a tile's keys, or values
 constexpr int kQBox = kRowsMax * 128;
@@ -97,7 +97,7 @@ __device__ __forceinline__ float warp_max(float x) {
 
 // A group's rows of the warp's 32 lanes.
 __device__ __forceinline__ void tmem_read(uint32_t at, uint32_t* r) {
-  tmem_ld32(at, r);
+  tmem_ld16(at, r);
   tmem_wait_ld();
 }
 
@@ -122,11 +122,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_init(&ctl.vfull[s], 4);
       mbar_init(&ctl.vempty[s], 1);
       mbar_init(&ctl.sfull[s], 1);
-      mbar_init(&ctl.sempty[s], 2 * kSoftWarps);
-      mbar_init(&ctl.pfull[s], 2 * kSoftWarps);
+      mbar_init(&ctl.sempty[s], kGroups * kSoftWarps);
+      mbar_init(&ctl.pfull[s], kGroups * kSoftWarps);
       mbar_init(&ctl.pempty[s], 1);
     }
-    mbar_init(&ctl.qfull, 2 * kSoftWarps);
+    mbar_init(&ctl.qfull, kGroups * kSoftWarps);
     mbar_init(&ctl.final_bar, 1);
     fence_mbar_init();
   }
@@ -157,9 +157,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   uint32_t kt = 0;
   const int wg = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) / 128, 0);
 
-  if (wg >= 3) {
+  if (wg > kGroups) {
     // ------------------------------------------------------------ unpacking
-    regs_decrease<kRegsUnpack>();
     const bool values = warp >= kUnpackWarp + 4;
     const Fp4Cache& c = values ? f.v : f.k;
     uint64_t* full = values ? ctl.vfull : ctl.kfull;
@@ -269,7 +268,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         now = next;
       }
     }
-  } else if (wg == 2) {
+  } else if (wg == kGroups) {
     // --------------------------------------------------------------- MMA issue
     regs_decrease<kRegsIssue>();
     // One elected lane issues, in code that the whole warp runs, on values that the
@@ -505,6 +504,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
           }
         }
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);   // (two lanes a row)
         if (lane < kGroupRows) ctl.part[warp & 3][r0 + lane] = v[0];
       }
       group_sync();
