@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const EvictAr
   for (int k = threadIdx.x; k < 3 * kBins; k += kSelectThreads) (&sh.bins[0][0])[k] = 0;
   if constexpr (CACHED)
     if (len < old)
-#pragma unroll 4
+#pragma unroll 8
       for (int j = threadIdx.x; j < part; j += kSelectThreads) cache[j] = order_key(w[lo + j]);
   ok = ok && check_pages(a, i, old, len);   // (and the CTA's keys are there)
   const bool first = h == 0 && rank == 0 && threadIdx.x == 0;
