@@ -433,3 +433,105 @@ def test_a_serving_loop(ea, packed):  # noqa: F811
         held = sum(-(-x // size) for x in n_now)
         assert int((refs > 0).sum()) == held
     ea.check()
+
+
+@pytest.mark.parametrize("H", [4, 40])
+def test_pages_further_apart_than_32_bits(ea, H):  # noqa: F811
+    # the same calls on pages next to one another and on pages (of codes, scales and
+    # bf16 keys) 2.5 GiB apart give the same bits
+    page, P, apart = 64, 6, 5 << 29
+    big = torch.zeros(P * apart + (1 << 20), dtype=torch.uint8, device="cuda")
+    shapes = [(P, 1, page, 64), (P, 1, page, 8)] * 2 + [(P, 1, page, 256)]
+    far = [big[i << 17:].as_strided(s, (apart, page * s[3], s[3], 1)) for i, s in enumerate(shapes)]
+    near = [torch.zeros(s, dtype=torch.uint8, device="cuda") for s in shapes]
+    g = torch.Generator().manual_seed(H)
+    k, v = (torch.randn(1, 1, 300, 128, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    q = torch.randn(1, H, 1, 128, generator=g).to(torch.bfloat16).cuda()
+    keys = torch.randn(P, 1, page, 128, generator=g).to(torch.bfloat16).cuda()
+    table = torch.full((1, 320), -1, dtype=torch.int32, device="cuda")
+    table[0, :5] = _i([5, 0, 3, 1, 4])
+    out = []
+    for pools in (near, far):
+        t, lens, refs = table.clone(), _i([300]), _i([1, 1, 0, 1, 1, 1])
+        pools[4].copy_(keys.view(torch.uint8))
+        cache = [pools[0], pools[1].view(E4M3), pools[2], pools[3].view(E4M3)]
+        wide = pools[4].view(torch.bfloat16)
+        kw = dict(k_descale=2.0 ** -9, v_descale=2.0 ** -9)
+        w = torch.zeros(1, 1, 320 * page, device="cuda")
+        ea.pages_store_fp4(k, v, *cache, t, lens, **kw)
+        back = ea.pages_load_fp4(*cache, t, lens, 300, **kw)
+        step = ea.attention_decode_fp4(q, *cache, t, lens, **kw)
+        ea.attention_key_weights(q, cache[0], t, lens, step[1], w, k_scales=cache[1], k_descale=2.0 ** -9)
+        first = w.clone()
+        ea.attention_key_weights(q, wide, t, lens, step[1], w)
+        second = w.clone()
+        slots = ea.pages_evict([*cache, wide], t, lens, refs, w, _i([0]), _i([100]), recent=10,
+                               page_size=page)
+        ea.check()
+        out.append([*back, *step, first, second, slots, w, t, lens, refs,
+                    *(x.view(torch.uint8)[[5, 0]] for x in pools)])
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
+    assert out[0][0].abs().sum() > 0 and out[0][4].sum() > 0
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_a_captured_step_of_many_rows(ea, packed):  # noqa: F811
+    # decode (4 bits), the weights of 48 rows a head and an eviction in one graph, replayed
+    # with other queries and lengths on a stream of its own
+    page, P, B, d = 32, 90, 2, 128
+    rng, g = np.random.default_rng(3), torch.Generator().manual_seed(3)
+    table = torch.full((B, 600), -1, dtype=torch.int32)
+    table[:, :40] = torch.from_numpy(rng.permutation(P)[:80].reshape(B, 40).astype(np.int32))
+    codes = [torch.from_numpy(rng.integers(0, 256, (P, 1, page, d // 2), dtype=np.uint8)).cuda() for _ in range(2)]
+    scales = [torch.from_numpy(rng.integers(0x20, 0x50, (P, 1, page, d // 16), dtype=np.uint8)).cuda().view(E4M3)
+              for _ in range(2)]
+    cache = (codes[0], scales[0], codes[1], scales[1])
+    keys = torch.randn(P, 1, page, d, generator=g).to(torch.bfloat16).cuda()
+    pools = [*cache, keys]
+    start = [x.clone() for x in pools]
+    q = torch.zeros(B, 12, 4, d, dtype=torch.bfloat16, device="cuda")
+    t, lens, refs = table.cuda(), _i([0, 0]), _i([0] * P)
+    w, new, seqs = torch.zeros(B, 1, 600 * page, device="cuda"), _i([0, 0]), _i([0, 1])
+    ws = torch.zeros(1 << 24, dtype=torch.uint8, device="cuda")
+
+    def set_up(n, m, seed):
+        for x, y in zip(pools, start):
+            x.copy_(y)
+        q.copy_(torch.randn(q.shape, generator=torch.Generator().manual_seed(seed)) * 0.3)
+        lens.copy_(_i(n))
+        new.copy_(_i(m))
+        t.copy_(table)
+        for b in range(B):
+            t[b, -(-n[b] // page):] = -1
+        refs.zero_()
+        refs[t[t >= 0].long()] = 1
+        w.zero_()
+
+    def step():
+        o, lse = ea.attention_decode_fp4(q, *cache, t, lens, scale=0.02, k_descale=0.01, ws=ws)
+        ea.attention_key_weights(q, codes[0] if packed else keys, t, lens, lse, w, scale=0.02, ws=ws,
+                                 **(dict(k_scales=scales[0], k_descale=0.01) if packed else {}))
+        seen = w.clone()
+        return o, lse, seen, ea.pages_evict(pools, t, lens, refs, w, seqs, new, recent=7, page_size=page, ws=ws)
+
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        set_up([1000, 3], [500, 3], 0)
+        step()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            got = step()
+        for n, m, seed in (([1000, 77], [333, 20], 1), ([1, 1280], [5, 64], 2), ([0, 640], [0, 0], 3)):
+            set_up(n, m, seed)
+            graph.replay()
+            first = [x.clone() for x in (*got, t, lens, refs, w, *pools)]
+            set_up(n, m, seed)
+            again = [*step(), t, lens, refs, w, *pools]
+            for a, b in zip(first, again):
+                assert torch.equal(a.view(torch.uint8) if a.dtype is E4M3 else a,
+                                   b.view(torch.uint8) if b.dtype is E4M3 else b)
+            assert lens.tolist() == [min(x, y) for x, y in zip(n, m)]
+            stream.synchronize()
+            ea.check(ws=ws)
