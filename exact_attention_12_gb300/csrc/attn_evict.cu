@@ -4,27 +4,28 @@
 // `len`, each head keeps its last r = min(recent, len) keys and the len - r of the
 // others that have the largest weights, in their order, at the front.
 //
-// Three kernels:
+// Two kernels:
 //   1. select, a cluster of CTAs per (sequence, head): the weights as 32-bit keys
 //      in the order of the numbers; the (len - r)-th largest by three rounds of
 //      counting digits (11, 11, 10 bits), every CTA its own part, the counts
 //      added up through the cluster's shared memory; then where each kept key
-//      goes, by ballots and running counts.
+//      goes, by ballots and running counts, and its weight with it.
 //   2. move, in place.  Key j comes from slots[j] >= j, and slots ascends, so the
 //      keys are moved in chunks of T: a CTA reads a chunk's rows of all pools
 //      into shared memory, says so, waits until the chunks in front of it whose
 //      rows lie where it writes have been read too, and writes.  Chunks are given
 //      out by a ticket, front to back, so what a CTA waits for is always being
 //      worked on, whichever CTAs are resident; a row is read and written once,
-//      and what stays where it is is not touched.
-//   3. finish: pages that are left over go back, lengths and tables follow.
+//      and what stays where it is is not touched.  Behind the chunks a ticket for
+//      each sequence: once all its chunks have been read, its left-over pages go
+//      back, its length and table follow.
 //
 // Bound: HBM, the moved rows twice and the weights once; on a short cache the
-// three launches.
-// Measured (8 heads, d = 128): 32 sequences of 2048-8192 bf16 keys to 4096, 660 MB moved,
-// 156 us; 4 of 95000 4-bit keys to 24000, 91 us, of them 26 the selection and 50 the
-// moves, which read 230 MB for 110 of scattered rows of 64 and 8 bytes with 128-byte
-// fetches; one of 333 keys to 256, 15 us.
+// two launches.
+// Measured (8 heads, d = 128; 4 us of each are copies that put the state back): 32
+// sequences of 2048-8192 bf16 keys to 4096, 660 MB moved, 149 us; 4 of 95000 4-bit keys
+// to 24000, 87 us, of them 26 the selection; one of 333 keys to 256, 14 us.  With a
+// kernel of its own for the pages and the weights behind the new length: 156, 91, 16.
 #include <climits>
 #include <cstdio>
 
@@ -45,7 +46,6 @@ constexpr int kMoveThreads = 256;
 constexpr int kMoveBytes = 40960;         // of a chunk, all pools
 constexpr int kMaxChunk = 512;            // keys of a chunk
 constexpr int kMaxPools = 16;
-constexpr int kFinishThreads = 128;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
 struct RowPool {
@@ -77,7 +77,6 @@ struct EvictArgs {
   int32_t* bound;            // [n][heads][chunks + 1]: kept keys before slot c T
   int chunk, chunk_shift;    // T, a power of two
   int chunks;                // of a row of the table
-  int finish_parts;          // CTAs of the last kernel per head and entry
   int cluster;               // CTAs per (sequence, head) of the first kernel
   int n_pools;
   RowPool pools[kMaxPools];
@@ -100,6 +99,11 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   if (w != w) return 0xffffffffu;
   const uint32_t b = __float_as_uint(w + 0.f);   // (-0 is 0)
   return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// The weight of a key (-0 as 0, a NaN as a NaN).
+__device__ __forceinline__ float weight_of(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
 
 // Entry i of the list: its sequence's length, and the new one; whether they hold
@@ -149,7 +153,8 @@ __device__ __forceinline__ uint32_t cluster_ld_u32(uint32_t addr) {
   return x;
 }
 
-// CACHED: the CTA's part of the weights stays in shared memory.
+// CACHED: the CTA's part of the weights stays in shared memory, and the weights are
+// moved from there.
 template <bool CACHED>
 __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const EvictArgs a) {
   extern __shared__ __align__(16) uint32_t cache[];
@@ -165,13 +170,15 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const EvictAr
   const int per_warp = (old + C * kSelectThreads - 1) / (C * kSelectThreads) * 32;
   const int lo = rank * per_warp * kSelectWarps;
   const int part = max(0, min(per_warp * kSelectWarps, old - lo));
-  const float* w = ok ? a.weights + a.seqs[i] * a.weight_row + h * a.weight_head : nullptr;
+  float* w = ok ? a.weights + a.seqs[i] * a.weight_row + h * a.weight_head : nullptr;
   auto key_at = [&](int j) { return CACHED ? cache[j] : order_key(w[lo + j]); };
   for (int k = threadIdx.x; k < 3 * kBins; k += kSelectThreads) (&sh.bins[0][0])[k] = 0;
-  if constexpr (CACHED)
-    if (len < old)
+  if constexpr (CACHED) {
+    if (len < old) {
 #pragma unroll 8
       for (int j = threadIdx.x; j < part; j += kSelectThreads) cache[j] = order_key(w[lo + j]);
+    }
+  }
   ok = ok && check_pages(a, i, old, len);   // (and the CTA's keys are there)
   const bool first = h == 0 && rank == 0 && threadIdx.x == 0;
   if (first && !ok) report(a.status, kStatusPage, kSitePageIndex);
@@ -316,7 +323,10 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const EvictAr
     const int to = static_cast<int>(above + __popc(ups & low) + min(e, left));
     if (j < stop) {
       const int slot = lo + j;
-      if (up || (same && e < left)) slots[to] = slot;
+      if (up || (same && e < left)) {
+        slots[to] = slot;
+        if (CACHED && to != slot) w[to] = weight_of(cache[j]);   // (all parts are read)
+      }
       if ((slot & (a.chunk - 1)) == 0 && slot >> a.chunk_shift <= chunks)
         bound[slot >> a.chunk_shift] = to;
     }
@@ -325,6 +335,9 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const EvictAr
   }
   for (int c = (old + a.chunk - 1) / a.chunk + me; c <= chunks; c += all) bound[c] = len;
   for (int j = len + me; j < a.width; j += all) slots[j] = -1;
+  if constexpr (CACHED) {
+    for (int j = len + me; j < old; j += all) w[j] = 0.f;
+  }
   if (C > 1) cluster_sync();   // the others have read this CTA's counts
 }
 
@@ -342,7 +355,7 @@ __device__ __forceinline__ void copy_async(uint8_t* dst, const char* src, int un
 struct ChunkKeys {
   int page[2][kMaxChunk];    // of a key's old and new place
   int row[kMaxChunk];        // in the old page
-  float weight[kMaxChunk];
+  float weight[kMaxChunk];   // (WEIGHTS)
 };
 constexpr int kMoveEntries = 256;   // of the list that are kept at hand
 struct MoveShared {
@@ -351,6 +364,8 @@ struct MoveShared {
   int ticket, give_up;
 };
 
+// WEIGHTS: the weights are still where they were.
+template <bool WEIGHTS>
 __global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const __grid_constant__ EvictArgs a) {
   extern __shared__ __align__(16) uint8_t buffer[];
   __shared__ MoveShared sh;
@@ -373,7 +388,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const __grid_cons
   const int last = most * items;
 
   struct Chunk {
-    int item, c, h, first, count;   // count 0: nothing to move
+    int item, c, h, first, count;   // count 0: nothing to move; -1: entry `item` ends
     int from, until;                // chunks to wait for
     float* w;
   };
@@ -381,7 +396,11 @@ __global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const __grid_cons
   // read.
   auto look_up = [&](int ticket, int buf) {
     Chunk k{};
-    if (ticket >= last) return k;
+    if (ticket >= last) {
+      k.item = ticket - last;
+      k.count = -1;
+      return k;
+    }
     k.c = ticket / items;
     k.item = ticket - k.c * items;
     const int i = k.item / a.heads;
@@ -401,7 +420,9 @@ __global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const __grid_cons
       to.page[0][j] = table[from >> a.page_shift];
       to.page[1][j] = table[(k.first + j) >> a.page_shift];
       to.row[j] = from & ((1 << a.page_shift) - 1);
-      to.weight[j] = k.w[from];
+      if constexpr (WEIGHTS) {
+        to.weight[j] = k.w[from];
+      }
     }
     if (b1 == k.first + T) {   // every key so far is kept: it stays
       if (threadIdx.x == 0) a.read[static_cast<int64_t>(k.item) * a.chunks + k.c] = 1;
@@ -416,13 +437,51 @@ __global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const __grid_cons
     return pool.shift >= 0 ? e >> pool.shift : e / per;
   };
 
+  auto wait_read = [&](const volatile int32_t* flag) {
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 1; *flag == 0; ++it)
+      if ((it & 63u) == 0 && globaltimer_ns() - t0 > a.timeout_ns) {
+        report(a.status, kStatusTimeout, kSiteEvictRead);
+        sh.give_up = 1;
+        return;
+      }
+  };
+  // Entry i, all of whose chunks are taken: when they have been read, its pages behind
+  // the new length go back.
+  auto end_entry = [&](int i) {
+    const int old = a.old_len[i], len = a.new_len[i], seq = a.seqs[i];
+    if (old < 0) return;
+    const int chunks = (len + T - 1) >> a.chunk_shift;
+    for (int q = threadIdx.x; q < a.heads * chunks; q += kMoveThreads) {
+      const int h = q / chunks;
+      wait_read(a.read + (static_cast<int64_t>(i) * a.heads + h) * a.chunks + q - h * chunks);
+    }
+    __syncthreads();
+    if (sh.give_up) return;
+    const int size = 1 << a.page_shift;
+    int32_t* row = a.table + seq * a.table_stride;
+    const int held = (old + size - 1) >> a.page_shift;
+    for (int j = ((len + size - 1) >> a.page_shift) + static_cast<int>(threadIdx.x); j < held;
+         j += kMoveThreads) {
+      atomicSub(&a.refs[row[j]], 1);   // (checked by the first kernel)
+      row[j] = -1;
+    }
+    if (threadIdx.x == 0) a.lens[seq] = len;
+    if constexpr (WEIGHTS) {
+      for (int h = 0; h < a.heads; ++h) {
+        float* w = a.weights + seq * a.weight_row + h * a.weight_head;
+        for (int j = len + static_cast<int>(threadIdx.x); j < old; j += kMoveThreads) w[j] = 0.f;
+      }
+    }
+  };
+
   // One chunk's rows are on their way while the next one is looked up.
   __syncthreads();
   if (threadIdx.x == 0) sh.ticket = atomicAdd(a.ticket, 1);
   __syncthreads();
   int ticket = sh.ticket;
   Chunk now = look_up(ticket, 0);
-  for (int buf = 0; ticket < last; buf ^= 1) {
+  for (int buf = 0; ticket < last + a.n; buf ^= 1) {
     __syncthreads();   // its keys are there; the buffer is free; sh.ticket has been read
     int next_ticket = 0;
     if (threadIdx.x == 0) next_ticket = atomicAdd(a.ticket, 1);
@@ -451,16 +510,8 @@ __global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const __grid_cons
       // (An armed test stall: the first chunks never say so.)
       if (threadIdx.x == 0 && !(a.stall != 0 && now.c == 0)) atomicExch(read + now.c, 1);
       // chunks in front of this one that have rows where it writes
-      for (int q = now.from + static_cast<int>(threadIdx.x); q < now.until; q += kMoveThreads) {
-        const volatile int32_t* flag = read + q;
-        const uint64_t t0 = globaltimer_ns();
-        for (uint32_t it = 1; *flag == 0; ++it)
-          if ((it & 63u) == 0 && globaltimer_ns() - t0 > a.timeout_ns) {
-            report(a.status, kStatusTimeout, kSiteEvictRead);
-            sh.give_up = 1;
-            break;
-          }
-      }
+      for (int q = now.from + static_cast<int>(threadIdx.x); q < now.until; q += kMoveThreads)
+        wait_read(read + q);
       __syncthreads();
       if (sh.give_up) break;
       for (int k = 0; k < a.n_pools; ++k) {
@@ -477,36 +528,14 @@ __global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const __grid_cons
           else *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(from);
         }
       }
-      for (int j = threadIdx.x; j < now.count; j += kMoveThreads) now.w[now.first + j] = keys.weight[j];
+      if constexpr (WEIGHTS) {
+        for (int j = threadIdx.x; j < now.count; j += kMoveThreads) now.w[now.first + j] = keys.weight[j];
+      }
+    } else if (now.count < 0) {
+      end_entry(now.item);
+      if (sh.give_up) break;
     }
     now = next;
-  }
-}
-
-// CTA (head and part, entry): the weights behind the new length; the first also the
-// pages.
-__global__ void __launch_bounds__(kFinishThreads) finish_kernel(const EvictArgs a) {
-  grid_dep_wait();
-  grid_dep_launch();
-  for (int i = blockIdx.y; i < a.n; i += gridDim.y) {
-    const int old = a.old_len[i], len = a.new_len[i], h = blockIdx.x / a.finish_parts;
-    if (old < 0) continue;
-    const int seq = a.seqs[i];
-    float* w = a.weights + seq * a.weight_row + h * a.weight_head;
-    const int part = blockIdx.x - h * a.finish_parts;
-    for (int j = len + part * kFinishThreads + static_cast<int>(threadIdx.x); j < old;
-         j += a.finish_parts * kFinishThreads)
-      w[j] = 0.f;
-    if (blockIdx.x > 0) continue;
-    const int size = 1 << a.page_shift;
-    int32_t* row = a.table + seq * a.table_stride;
-    const int held = (old + size - 1) >> a.page_shift;
-    for (int j = ((len + size - 1) >> a.page_shift) + static_cast<int>(threadIdx.x); j < held;
-         j += kFinishThreads) {
-      atomicSub(&a.refs[row[j]], 1);   // (checked by the first kernel)
-      row[j] = -1;
-    }
-    if (threadIdx.x == 0) a.lens[seq] = len;
   }
 }
 
@@ -617,6 +646,7 @@ cudaError_t launch_select(const EvictArgs& a, size_t bytes, cudaStream_t s) {
   return launch_clusters(select_kernel<CACHED>, grid, dim3(kSelectThreads), bytes, a.cluster, s, a);
 }
 
+template <bool WEIGHTS>
 cudaError_t launch_move(const EvictArgs& a, cudaStream_t s) {
   static std::atomic<uint64_t> set_up{0};
   int dev = 0;
@@ -624,13 +654,13 @@ cudaError_t launch_move(const EvictArgs& a, cudaStream_t s) {
   cudaError_t e = needs_setup(set_up, &dev, &todo);
   if (e != cudaSuccess) return e;
   if (todo) {
-    e = cudaFuncSetAttribute(move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(move_kernel<WEIGHTS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kMoveBytes + 16 * kMaxPools);
     if (e != cudaSuccess) return e;
     mark_done(set_up, dev);
   }
   const int64_t work = static_cast<int64_t>(a.n) * a.heads * a.chunks, room = 4ll * multiprocessors();
-  return launch_pdl(move_kernel, dim3(static_cast<unsigned>(work < room ? work : room)),
+  return launch_pdl(move_kernel<WEIGHTS>, dim3(static_cast<unsigned>(work < room ? work : room)),
                     dim3(kMoveThreads), a.buffer, s, a);
 }
 
@@ -725,18 +755,10 @@ attn_status attn_pages_evict(const attn_page_table* t, const attn_rows* pools, i
   // a CTA's part of the weights, if it fits
   const int64_t part = (cap + a.cluster * kSelectThreads - 1) / (a.cluster * kSelectThreads) *
                        kSelectThreads * 4;
-  cudaError_t e = part <= 160 * 1024 ? launch_select<true>(a, static_cast<size_t>(part), s)
-                                     : launch_select<false>(a, 0, s);
-  if (e == cudaSuccess && cap > 0) e = launch_move(a, s);
-  a.finish_parts = 1;   // a few thousand weights each, while the GPU has room
-  while (a.finish_parts < 64 && cap > 4096ll * a.finish_parts &&
-         static_cast<int64_t>(n) * heads * a.finish_parts < 8ll * multiprocessors())
-    a.finish_parts *= 2;
-  if (e == cudaSuccess)
-    e = launch_pdl(finish_kernel,
-                   dim3(static_cast<unsigned>(heads * a.finish_parts),
-                        static_cast<unsigned>(n < 65535 ? n : 65535)),
-                   dim3(kFinishThreads), 0, s, a);
+  const bool cached = part <= 160 * 1024;
+  cudaError_t e = cached ? launch_select<true>(a, static_cast<size_t>(part), s)
+                         : launch_select<false>(a, 0, s);
+  if (e == cudaSuccess && cap > 0) e = cached ? launch_move<false>(a, s) : launch_move<true>(a, s);
   if (e == cudaSuccess) return ATTN_OK;
   char msg[256];
   snprintf(msg, sizeof(msg), "page evict launch: %s", cudaGetErrorString(e));

@@ -474,8 +474,8 @@ typedef struct attn_rows {
  * keys, every head by its own weights.  A head keeps its last
  * min(recent, new_lens[i]) keys and, of those before them, the ones with the
  * largest weights (of equal ones those in front; NaN counts as the largest); they keep
- * their order and move to the front, in every pool.  The weights move along, those
- * behind the new length become 0.  Pages that are no longer needed are given
+ * their order and move to the front, in every pool.  The weights move along (a -0 as 0,
+ * a NaN as some NaN), those behind the new length become 0.  Pages that are no longer needed are given
  * back as in attn_pages_free.  A sequence that is not longer than new_lens[i] stays
  * as it is.
  *   weights    fp32 [rows][heads][width], weight_stride_row and weight_stride_head
