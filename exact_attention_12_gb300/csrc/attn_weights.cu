@@ -113,8 +113,8 @@ __device__ __forceinline__ void operands(const KeyPart<D, PACKED>& x, uint32_t (
   }
 }
 
-// The quarter of a row of Q that goes with it, and what turns a score into log2
-// units.
+// The quarter of a row of Q that goes with it (zeros if not `live`), and what turns a
+// score into log2 units.
 template <int D, bool PACKED>
 __device__ __forceinline__ float load_query(const PagedArgs& a, const WeightArgs& f, int b, int at,
                                             bool live, int t, uint32_t* w) {
@@ -139,9 +139,8 @@ __device__ __forceinline__ float load_query(const PagedArgs& a, const WeightArgs
   return a.scale_log2;
 }
 
-__device__ __forceinline__ RowInfo row_info(const PagedArgs& a, const WeightArgs& f, int b, int len,
-                                            int at, bool live, float c2) {
-  const float L = live ? f.lse[static_cast<int64_t>(b) * a.all_rows + at] : -INFINITY;
+__device__ __forceinline__ RowInfo row_info(const PagedArgs& a, int len,
+                                            int at, float L, float c2) {
   RowInfo info;
   info.c2 = c2;
   info.l2 = L == -INFINITY ? INFINITY : L * kLog2Of;
@@ -200,10 +199,10 @@ __global__ void __launch_bounds__(kWeightThreads, 2)
     __syncthreads();   // the rows before are no longer in use
     for (int n = warp; n < blocks; n += kWeightWarps) {
       const int r = 8 * n + g, at = p.h * a.head_rows + r;
-      const bool live = r < a.head_rows;
-      uint32_t w[kWords];
-      const float c2 = load_query<D, PACKED>(a, f, p.b, at, live, t, w);
-      if (t == 0) rows[r] = row_info(a, f, p.b, p.len, at, live, c2);
+      const float L = r < a.head_rows ? f.lse[static_cast<int64_t>(p.b) * a.all_rows + at] : -INFINITY;
+      uint32_t w[kWords];   // (a row that gives nothing may hold anything)
+      const float c2 = load_query<D, PACKED>(a, f, p.b, at, L != -INFINITY, t, w);
+      if (t == 0) rows[r] = row_info(a, p.len, at, L, c2);
 #pragma unroll
       for (int s = 0; s < kSteps; ++s)
         qf[(n * kSteps + s) * 32 + lane] = make_uint2(w[2 * s], w[2 * s + 1]);

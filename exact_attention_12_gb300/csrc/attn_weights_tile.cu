@@ -134,7 +134,8 @@ __global__ void __launch_bounds__(TileCfg<D, PACKED>::kThreads, 1)
     for (int r0 = 0; ok && r0 < a.head_rows; r0 += f.pass_rows) {
       const int nrows = min(a.head_rows - r0, f.pass_rows);
       const int blocks = (nrows + kRowsAtOnce - 1) / kRowsAtOnce;
-      // ---- Q and its rows' limits; what lies past the last row is zero
+      // ---- Q and its rows' limits; a row that gives nothing and what lies past the last
+      // one is zero
       // (the scores of the pass before have all been read, so its products are complete)
       if (warp < kSumWarps) {
         for (int i = threadIdx.x; i < blocks * kRowsAtOnce * kPerRow; i += 32 * kSumWarps) {
@@ -179,6 +180,16 @@ __global__ void __launch_bounds__(TileCfg<D, PACKED>::kThreads, 1)
               gives ? (a.causal ? min(p.len, p.len - a.n_q + at % a.n_q + 1) : p.len) : 0;
         }
         copies_wait();
+        // a row that gives nothing may hold anything: zeros in its place (asking for L before
+        // the copies are made took 3 us more)
+        named_barrier_sync(2, 32 * kSumWarps);
+        for (int r = threadIdx.x; r < nrows; r += 32 * kSumWarps)
+          if (row_l[r] == -INFINITY) {
+            uint8_t* to = sQ + r / kRowsAtOnce * C::kTileBytes + r % kRowsAtOnce * 128;
+            for (int i = 0; i < kPerRow; ++i)
+              *reinterpret_cast<uint4*>(to + (i >> 3) * C::kBoxBytes + ((i & 7) << 4)) =
+                  make_uint4(0u, 0u, 0u, 0u);
+          }
         fence_proxy_async_smem();
       }
       // (the copies need not wait for Q)

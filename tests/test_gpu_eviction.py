@@ -114,6 +114,30 @@ def test_rows_that_attend_nothing_give_nothing(ea):  # noqa: F811
         assert torch.equal(again, w)
 
 
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("H", [9, 40, 130])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_of_minus_infinity_give_nothing_whatever_they_hold(ea, packed, H, d):  # noqa: F811
+    # rows that pad a batch: no logsumexp, and a q that nobody has written
+    g = torch.Generator().manual_seed(H)
+    rng = np.random.default_rng(H)
+    codes, scales = (torch.from_numpy(x).cuda() for x in
+                     _cache(rng, np.arange(12).reshape(1, 12), [700], 12, 1, 64, d))
+    keys = torch.randn(12, 1, 64, d, generator=g).to(torch.bfloat16).cuda()
+    kw = dict(k_scales=scales.view(E4M3), k_descale=2.0 ** -7) if packed else {}
+    q = torch.randn(1, H, 1, d, generator=g).to(torch.bfloat16)
+    lse = torch.randn(1, H, 1, generator=g) + 5
+    odd, some = q.clone(), lse.clone()
+    for h, x in ((1, float("nan")), (H // 2, float("inf")), (H - 1, -float("inf"))):
+        odd[0, h], some[0, h], q[0, h] = x, -float("inf"), 0
+    t, n = _i([list(range(12))]), _i([700])
+    got = [ea.attention_key_weights(x.cuda(), codes if packed else keys, t, n, some.cuda(),
+                                    torch.zeros(1, 1, 768, device="cuda"), scale=0.01, **kw) for x in (q, odd)]
+    ea.check()
+    assert torch.isfinite(got[0]).all() and got[0][0, 0, :700].min() > 0
+    assert torch.equal(*got)
+
+
 def test_a_bad_page_of_keys_is_reported(ea):  # noqa: F811
     from exact_attention_12_gb300 import AttnError
     k = torch.ones(2, 1, 16, 64, device="cuda", dtype=torch.bfloat16)
