@@ -17,10 +17,11 @@
 //   warp 16      MMA issue, the next tile's S before this one's O
 //   warps 20-27  unpacking, four K and four V: four lanes a key, their 16 bytes of codes
 //                and two scales a tile ahead in registers and six in L2
-// 64 sequences of 16384 keys, 4 heads, 64 rows (604 MB): 303 us, 2.0 TB/s; 2700 clocks a
-// tile.  Its 6600 warp instructions are 1650 of them, its way through shared memory
-// (unpacked values in, operands out) 1400, and the groups go from a score to its weight
-// in step; the tensor cores are busy for a sixth.  S and O from two issuing warps: 318.
+// 64 sequences of 16384 keys, 4 heads, 64 rows (604 MB): 303 us, 2.0 TB/s; 2900 clocks a
+// tile.  Its 7500 warp instructions take 65 % of the issue slots, its way through shared
+// memory (unpacked values in, operands out) 1400 clocks, and the groups go from a score
+// to its weight in step; the tensor cores are busy for a sixth.  S and O from two
+// issuing warps: 318.
 // Rounding and what may lie where no key is attended: as in attn_fp4.cu.
 #include "attn_fp4.cuh"
 
