@@ -699,8 +699,9 @@ attn_status attn_pages_evict(const attn_page_table* t, const attn_rows* pools, i
   if (ws_bytes < L.total)
     return static_cast<attn_status>(bad(ATTN_ERR_WORKSPACE, "workspace too small"));
   if (n == 0 || heads == 0) return ATTN_OK;
-  if (seqs == nullptr || new_lens == nullptr ||
-      (cap > 0 && (weights == nullptr || slots == nullptr)))
+  // (slots are written as far as `width`, without any page too)
+  if (seqs == nullptr || new_lens == nullptr || (cap > 0 && weights == nullptr) ||
+      (width > 0 && slots == nullptr))
     return static_cast<attn_status>(bad(ATTN_ERR_INVALID_ARG, "list, weights or slots is NULL"));
   char* w = static_cast<char*>(ws);
   auto ints = [&](size_t at) { return reinterpret_cast<int32_t*>(w + at); };
