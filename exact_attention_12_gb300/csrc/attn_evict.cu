@@ -190,7 +190,9 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const EvictAr
   int32_t* slots = a.slots + static_cast<int64_t>(item) * a.width;
   const int all = C * kSelectThreads, me = rank * kSelectThreads + static_cast<int>(threadIdx.x);
   if (!ok || len == old) {   // (the same in all CTAs of the cluster)
-    for (int j = me; j < a.width; j += all) slots[j] = ok ? (j < old ? j : -1) : -2;
+    // (64 bits: `width` may be as large as 32 hold)
+    for (int64_t j = me; j < a.width; j += all)
+      slots[j] = ok ? (j < old ? static_cast<int32_t>(j) : -1) : -2;
     return;
   }
   const int chunks = (len + a.chunk - 1) / a.chunk;
@@ -334,7 +336,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const EvictAr
     equal += __popc(sames);
   }
   for (int c = (old + a.chunk - 1) / a.chunk + me; c <= chunks; c += all) bound[c] = len;
-  for (int j = len + me; j < a.width; j += all) slots[j] = -1;
+  for (int64_t j = len + me; j < a.width; j += all) slots[j] = -1;
   if constexpr (CACHED) {
     for (int j = len + me; j < old; j += all) w[j] = 0.f;
   }
