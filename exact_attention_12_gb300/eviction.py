@@ -10,6 +10,7 @@ from .fp4 import _cache
 from .paged import _PAGES, _PARAMS, _bf16, _call, _empty, _f32, _i32, _list, _strides, _table, _table_args
 
 _ROWS = struct.Struct("@P3q2i").pack   # attn_rows as bytes
+_MOST = 2 ** 31 - 1   # what the library's 32-bit counts hold
 
 
 def _weights(weights, rows, heads, keys, index):
@@ -92,6 +93,9 @@ def pages_evict(pools, page_table, cache_lens, refs, weights, seqs, new_lens, *,
         raise ValueError("weights must be [rows, H_kv, keys]")
     heads = weights.shape[1]
     w = _weights(weights, page_table.shape[0], heads, page_table.shape[1] * page_size, index)
+    if weights.shape[2] > _MOST:
+        raise ValueError("weights: more than 2^31 - 1 keys")
+    recent = max(-1, min(recent, _MOST))   # (as many as there are; a negative one is refused)
     lead, rows = (P, heads, page_size), b""
     for x in pools:
         shape, n = x.shape, x.element_size()   # n: bytes of a row

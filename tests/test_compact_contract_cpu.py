@@ -4,8 +4,9 @@ without a GPU: what they refuse before anything is launched."""
 import ctypes
 
 import pytest
+import torch
 
-from tests.test_fp4_cpu import FAKE, lib  # noqa: F401
+from tests.test_fp4_cpu import FAKE, _Seen, _tensors, lib  # noqa: F401
 
 
 def _table(**kw):
@@ -30,3 +31,29 @@ def _evict(lib, t, weights=FAKE, row=128, head=64, width=64, slots=FAKE, n=1, po
 def test_an_eviction_without_slots_is_refused(lib, kw):  # noqa: F811
     # (a table without pages as well: every call writes slots as far as `width`)
     assert _evict(lib, _table(**kw), slots=None) == 1 and b"NULL" in lib.attn_last_error()
+
+
+# ---------------------------------------------------------------- binding --
+
+@pytest.mark.parametrize("recent,want", [(0, 0), (7, 7), (2 ** 31, 2 ** 31 - 1), (2 ** 32, 2 ** 31 - 1),
+                                         (2 ** 32 + 3, 2 ** 31 - 1), (2 ** 64, 2 ** 31 - 1), (-2 ** 32, -1),
+                                         (-2 ** 31 - 1, -1)])
+def test_recent_is_not_taken_modulo_32_bits(lib, monkeypatch, recent, want):  # noqa: F811
+    import exact_attention_12_gb300 as ea
+    seen, x = _Seen(monkeypatch), _tensors()
+    ea.pages_evict((x["kc"],), x["t"], x["lens"], x["refs"], x["w"], x["lens"][:1], x["lens"][:1],
+                   recent=recent, page_size=16)
+    assert ctypes.c_int32(seen.calls[0][1][11]).value == want
+
+
+def test_weights_wider_than_32_bits_count_are_refused(lib, monkeypatch):  # noqa: F811
+    import exact_attention_12_gb300 as ea
+    seen, x = _Seen(monkeypatch), _tensors()
+    call = lambda width: ea.pages_evict(  # noqa: E731
+        (), x["t"], x["lens"], x["refs"], torch.empty(2, 2, width, device="meta"), x["lens"][:0],
+        x["lens"][:0], page_size=16)
+    call(2 ** 31 - 1)
+    for width in (2 ** 31, 2 ** 32 + 64):
+        with pytest.raises(ValueError):
+            call(width)
+    assert len(seen.calls) == 1
