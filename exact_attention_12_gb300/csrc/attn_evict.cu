@@ -688,10 +688,11 @@ attn_status attn_pages_evict(const attn_page_table* t, const attn_rows* pools, i
   if (st != ATTN_OK) return static_cast<attn_status>(st);
   if (recent < 0) return static_cast<attn_status>(bad(ATTN_ERR_INVALID_ARG, "recent is negative"));
   const int64_t cap = static_cast<int64_t>(t->max_pages) * t->page_size;
-  if (width < cap || weight_stride_row < (t->rows > 1 ? cap : 0) ||
-      weight_stride_head < (heads > 1 ? cap : 0))
-    return static_cast<attn_status>(
-        bad(ATTN_ERR_INVALID_ARG, "weights: width or strides below max_pages * page_size"));
+  if (width < cap || weight_stride_row < 0 || weight_stride_head < 0 ||
+      !apart({{t->rows, weight_stride_row}, {heads, weight_stride_head}}, cap))
+    return static_cast<attn_status>(bad(
+        ATTN_ERR_INVALID_ARG,
+        "weights: width or strides below max_pages * page_size, or rows and heads not apart"));
   const EvictLayout L = evict_layout(t, heads, n, pools, n_pools);
   if (static_cast<int64_t>(n) * heads * L.chunks >= (int64_t{1} << 30))
     return static_cast<attn_status>(bad(ATTN_ERR_UNSUPPORTED, "more than 2^30 chunks to move"));

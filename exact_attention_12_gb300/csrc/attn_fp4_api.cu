@@ -1,6 +1,7 @@
 // Host side of the calls on caches in 4 bits (attn_pages_store_fp4,
 // attn_pages_load_fp4, attn_decode_fp4) and of attn_key_weights: argument checks,
 // workspace layout, launches.
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 
@@ -274,6 +275,24 @@ attn_status copy(const attn_params* p, const attn_pages* g, const int32_t* count
 
 }  // namespace
 
+namespace attn {
+
+bool apart(std::initializer_list<Axis> axes, int64_t extent) {
+  Axis live[kMaxAxes];
+  int n = 0;
+  for (const Axis& x : axes)
+    if (x.size > 1 && n < kMaxAxes) live[n++] = x;
+  std::sort(live, live + n, [](const Axis& x, const Axis& y) { return x.stride < y.stride; });
+  __int128 span = extent;
+  for (int i = 0; i < n; ++i) {
+    if (live[i].stride < span) return false;
+    span += static_cast<__int128>(live[i].size - 1) * live[i].stride;
+  }
+  return true;
+}
+
+}  // namespace attn
+
 extern "C" {
 
 attn_status attn_pages_store_fp4(const attn_params* p, const attn_pages* pages,
@@ -354,8 +373,9 @@ attn_status attn_key_weights(const attn_params* p, int32_t n_q, const attn_pages
   } else if (!good_strides({p->kv_stride_b, p->kv_stride_h, p->kv_stride_n}, p->d)) {
     return fail(ATTN_ERR_INVALID_ARG, "kv strides must be positive multiples of 8, the last >= d");
   }
-  if (weight_stride_b < (p->B > 1 ? p->N : 0) || weight_stride_h < (kv_heads(p) > 1 ? p->N : 0))
-    return fail(ATTN_ERR_INVALID_ARG, "weights: sequences and heads must be N entries apart at least");
+  if (weight_stride_b < 0 || weight_stride_h < 0 ||
+      !attn::apart({{p->B, weight_stride_b}, {kv_heads(p), weight_stride_h}}, p->N))
+    return fail(ATTN_ERR_INVALID_ARG, "weights: the N entries of sequences and heads must lie apart");
   if ((st = check_ws(ws, ws_bytes, kHeaderBytes)) != ATTN_OK) return st;
   if (empty(p) || p->N == 0) return ATTN_OK;
   if (k_cache == nullptr && pages->num_pages == 0) k = q;   // no cache to point at

@@ -6,6 +6,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <initializer_list>
 
 #include "attn_kernels.cuh"
 #include "sm103_async.cuh"
@@ -347,6 +348,15 @@ cudaError_t launch_prefix(const CUtensorMap& tk, const CUtensorMap& tv, const Pr
 cudaError_t launch_latent(const CUtensorMap& tc, const PagedArgs& a, int ctas, cudaStream_t s);
 cudaError_t launch_paged_merge(const PagedArgs& a, int notes, int ctas, cudaStream_t s);
 cudaError_t launch_paged_finish(const PagedArgs& a, int ctas, cudaStream_t s);
+
+// Whether a buffer's blocks of `extent` lie apart: the axes' sizes and strides (in the
+// extent's unit, >= 0; up to kMaxAxes), in any order.  Each axis has to step over all
+// that the axes of smaller strides span; one of size 1 or 0 steps over nothing.
+struct Axis {
+  int64_t size, stride;
+};
+constexpr int kMaxAxes = 4;
+bool apart(std::initializer_list<Axis> axes, int64_t extent);
 
 // Whether attn_debug_stall armed `which` for this launch; then its wait limit.
 bool take_stall(int which, uint64_t* limit_ns);

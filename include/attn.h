@@ -387,7 +387,7 @@ attn_status attn_decode_fp4(const attn_params* p, int32_t n_q, const attn_pages*
  *   k         [num_pages, H_kv, page_size, d] bf16 with the kv strides, or NULL and
  *   k_cache   a cache in 4 bits (then NULL otherwise)
  *   weights   fp32, weight_stride_b and weight_stride_h entries between sequences
- *             and heads, each max_pages * page_size at least (where there are two)
+ *             and heads; the max_pages * page_size entries of each lie apart
  * ws: 256 bytes. */
 attn_status attn_key_weights(const attn_params* p, int32_t n_q, const attn_pages* pages,
                              const void* q, const void* k, const attn_fp4* k_cache,
@@ -479,7 +479,8 @@ typedef struct attn_rows {
  * back as in attn_pages_free.  A sequence that is not longer than new_lens[i] stays
  * as it is.
  *   weights    fp32 [rows][heads][width], weight_stride_row and weight_stride_head
- *              entries apart; these and width >= max_pages * page_size
+ *              entries between rows and heads, the max_pages * page_size entries of
+ *              each lie apart; width >= max_pages * page_size
  *   slots      device int32 [n][heads][width], output: slots[i][h][j] is where the
  *              key that is now in place j was before; -1 from the new length on,
  *              -2 throughout where a sequence was refused

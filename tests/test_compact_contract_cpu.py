@@ -6,7 +6,7 @@ import ctypes
 import pytest
 import torch
 
-from tests.test_fp4_cpu import FAKE, _Seen, _tensors, lib  # noqa: F401
+from tests.test_fp4_cpu import FAKE, _Seen, _step, _tensors, lib  # noqa: F401
 
 
 def _table(**kw):
@@ -31,6 +31,23 @@ def _evict(lib, t, weights=FAKE, row=128, head=64, width=64, slots=FAKE, n=1, po
 def test_an_eviction_without_slots_is_refused(lib, kw):  # noqa: F811
     # (a table without pages as well: every call writes slots as far as `width`)
     assert _evict(lib, _table(**kw), slots=None) == 1 and b"NULL" in lib.attn_last_error()
+
+
+# What several sequences and heads would write to, row and head entries apart; 64 entries each,
+# 3 sequences, 2 heads.
+APART = [(128, 64), (64, 192), (1000, 64), (500, 3000), (129, 64), (64, 193)]
+SHARED = [(64, 64), (127, 64), (64, 191), (100, 100), (64, 128), (1 << 62, 63)]
+
+
+@pytest.mark.parametrize("row,head,ok", [(*x, True) for x in APART] + [(*x, False) for x in SHARED])
+def test_weights_of_one_place_are_refused(lib, row, head, ok):  # noqa: F811
+    p, g, c, _ = _step(lib, B=3, N=64, max_pages=4, table_stride=4)
+    # (without a workspace: what passes the checks of the weights is refused there)
+    st = lib.attn_key_weights(ctypes.byref(p), 1, ctypes.byref(g), FAKE, None, ctypes.byref(c), FAKE, FAKE,
+                              row, head, 1, None, 0, None)
+    assert st == (5 if ok else 1) and (ok or b"apart" in lib.attn_last_error())
+    assert _evict(lib, _table(rows=3), row=row, head=head, n=0) == (0 if ok else 1)
+    assert ok or b"apart" in lib.attn_last_error()
 
 
 # ---------------------------------------------------------------- binding --
