@@ -589,9 +589,9 @@ int check_evict(const attn_page_table* t, int32_t heads, int32_t n, const attn_r
   }
   if (total > 32768) return bad(ATTN_ERR_UNSUPPORTED, "pools: more than 32768 bytes a row");
   for (int i = 0; i < n_pools && heads > 0; ++i)
-    if ((t->num_pages > 1 && pools[i].page_stride < pools[i].row_bytes) ||
-        (heads > 1 && pools[i].head_stride < pools[i].row_bytes))
-      return bad(ATTN_ERR_INVALID_ARG, "pools: pages and heads must be apart");
+    if (!apart({{t->num_pages, pools[i].page_stride}, {heads, pools[i].head_stride},
+                {t->page_size, pools[i].row_stride}}, pools[i].row_bytes))
+      return bad(ATTN_ERR_INVALID_ARG, "pools: rows, heads and pages must lie apart");
   return ATTN_OK;
 }
 

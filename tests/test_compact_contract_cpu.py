@@ -50,6 +50,25 @@ def test_weights_of_one_place_are_refused(lib, row, head, ok):  # noqa: F811
     assert ok or b"apart" in lib.attn_last_error()
 
 
+# Page, head and row steps of pools with 3 pages, 2 heads, 16 rows of 128 bytes.
+POOLS = [((4096, 2048, 128), True), ((4096, 128, 256), True), ((128, 6144, 384), True),
+         ((5000, 2108, 132), True), ((1 << 40, 1 << 33, 1 << 20), True),
+         # (16 rows 132 apart take 15 * 132 + 128 = 2108)
+         ((5000, 2100, 132), False), ((128, 128, 128), False), ((4096, 1024, 128), False), ((2048, 4096, 128), False),
+         ((4096, 128, 128), False), ((4096, 2048, 256), False), ((256, 4096, 256), False)]
+
+
+@pytest.mark.parametrize("steps,ok", POOLS)
+def test_pools_whose_rows_share_memory_are_refused(lib, steps, ok):  # noqa: F811
+    from exact_attention_12_gb300 import _abi
+    pool = _abi.AttnRows(FAKE, *steps, 128, 0)
+    t = _table(num_pages=3)
+    assert _evict(lib, t, pools=(pool,), n=0) == (0 if ok else 1)
+    assert ok or b"apart" in lib.attn_last_error()
+    size = lib.attn_pages_evict_workspace_size(ctypes.byref(t), 2, 1, ctypes.byref(pool), 1)
+    assert (size > 256) is ok
+
+
 # ---------------------------------------------------------------- binding --
 
 @pytest.mark.parametrize("recent,want", [(0, 0), (7, 7), (2 ** 31, 2 ** 31 - 1), (2 ** 32, 2 ** 31 - 1),
