@@ -86,6 +86,15 @@ attn_status check_cache(const attn_fp4* c, int heads, int num_pages) {
   return ATTN_OK;
 }
 
+// (what is written to)
+attn_status check_apart(const attn_fp4* c, const attn_params* p, const attn_pages* g) {
+  const int64_t row = static_cast<int64_t>(g->page_size) * p->d;
+  if (attn::apart({{g->num_pages, c->code_page}, {p->H_kv, c->code_head}}, row / 2) &&
+      attn::apart({{g->num_pages, c->scale_page}, {p->H_kv, c->scale_head}}, row / attn::kFp4Block))
+    return ATTN_OK;
+  return fail(ATTN_ERR_INVALID_ARG, "cache: heads and pages must lie apart");
+}
+
 attn::Fp4Cache cache_of(const attn_fp4* c) {
   return attn::Fp4Cache{static_cast<uint8_t*>(c->codes), static_cast<uint8_t*>(c->scales),
                         c->code_page, c->code_head, c->scale_page, c->scale_head};
@@ -242,6 +251,8 @@ attn_status copy(const attn_params* p, const attn_pages* g, const int32_t* count
   attn_status st = check_pages(p, g);
   if (st != ATTN_OK || (st = check_cache(kc, p->H_kv, g->num_pages)) != ATTN_OK ||
       (st = check_cache(vc, p->H_kv, g->num_pages)) != ATTN_OK)
+    return st;
+  if (store && ((st = check_apart(kc, p, g)) != ATTN_OK || (st = check_apart(vc, p, g)) != ATTN_OK))
     return st;
   if (p->N > (1 << 30)) return fail(ATTN_ERR_UNSUPPORTED, "more than 2^30 tokens");
   if (!good_strides({p->kv_stride_b, p->kv_stride_h, p->kv_stride_n}, p->d))

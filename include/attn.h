@@ -331,7 +331,7 @@ attn_status attn_decode_latent(const attn_params* p, int32_t n_q, const attn_pag
  * key where bf16 has 2 d.  Codes and scales are two buffers of pages: codes
  * [num_pages][H_kv][page_size][d / 2], scales [num_pages][H_kv][page_size][d / 16];
  * a head's rows of a page follow one another without gaps, pages and heads may
- * be apart.  attn_pages_copy, _fork, _compact and _evict take them as pools.
+ * be apart (what is written to must not overlap).  attn_pages_copy, _fork, _compact and _evict take them as pools.
  * (The pages about attention have no counterpart.) */
 typedef struct attn_fp4 {
   void* codes;               /* 16-byte aligned, as is scales */

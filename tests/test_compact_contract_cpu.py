@@ -69,6 +69,27 @@ def test_pools_whose_rows_share_memory_are_refused(lib, steps, ok):  # noqa: F81
     assert (size > 256) is ok
 
 
+# Page and head bytes of codes and scales: 4 pages, 2 heads of 16 keys with 32 and 4 bytes.
+CACHES = [(dict(), True), (dict(code_page=512, code_head=2048, scale_page=64, scale_head=256), True),
+          (dict(code_page=512), False), (dict(code_head=496), False), (dict(code_page=1008), False),
+          (dict(scale_head=48), False), (dict(scale_page=64), False), (dict(code_page=512, code_head=2032), False)]
+
+
+@pytest.mark.parametrize("kw,ok", CACHES)
+@pytest.mark.parametrize("which", ["keys", "values"])
+def test_a_store_into_places_of_one_another_is_refused(lib, kw, ok, which):  # noqa: F811
+    p, g, c, _ = _step(lib, **kw)
+    good = _step(lib)[2]
+    pair = (c, good) if which == "keys" else (good, c)
+    # (without a workspace: what passes the checks of the cache is refused there)
+    st = lib.attn_pages_store_fp4(ctypes.byref(p), ctypes.byref(g), None, FAKE, FAKE,
+                                  *(ctypes.byref(x) for x in pair), None, 0, None)
+    assert st == (5 if ok else 1) and (ok or b"apart" in lib.attn_last_error())
+    # reading is free to
+    assert lib.attn_pages_load_fp4(ctypes.byref(p), ctypes.byref(g), None, *(ctypes.byref(x) for x in pair),
+                                   FAKE, FAKE, None, 0, None) == 5
+
+
 # ---------------------------------------------------------------- binding --
 
 @pytest.mark.parametrize("recent,want", [(0, 0), (7, 7), (2 ** 31, 2 ** 31 - 1), (2 ** 32, 2 ** 31 - 1),
