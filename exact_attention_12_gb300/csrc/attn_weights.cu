@@ -197,18 +197,21 @@ __global__ void __launch_bounds__(kWeightThreads, 2)
     const int nv = tiles > 0 ? (tiles + kWeightWarps - 1) / kWeightWarps * 4 : 0;
     const int blocks = (a.head_rows + 7) / 8;
     __syncthreads();   // the rows before are no longer in use
+    bool dead = false;
     for (int n = warp; n < blocks; n += kWeightWarps) {
       const int r = 8 * n + g, at = p.h * a.head_rows + r;
       const float L = r < a.head_rows ? f.lse[static_cast<int64_t>(p.b) * a.all_rows + at] : -INFINITY;
-      uint32_t w[kWords];   // (a row that gives nothing may hold anything)
-      const float c2 = load_query<D, PACKED>(a, f, p.b, at, L != -INFINITY, t, w);
+      dead = dead || L == -INFINITY;
+      uint32_t w[kWords];
+      const float c2 = load_query<D, PACKED>(a, f, p.b, at, r < a.head_rows, t, w);
       if (t == 0) rows[r] = row_info(a, p.len, at, L, c2);
 #pragma unroll
       for (int s = 0; s < kSteps; ++s)
         qf[(n * kSteps + s) * 32 + lane] = make_uint2(w[2 * s], w[2 * s + 1]);
     }
-    __syncthreads();
-    const bool ragged = (a.head_rows & 7) != 0;
+    // a row that gives nothing may hold anything, and an infinite key makes NaN of zeros as
+    // well: where there is one, what a row gives is chosen by its limit
+    const bool some_dead = __syncthreads_or(dead) != 0;
     if (nv > 0) load_pages(p, 0, nv >> 2);
     KeyPart<D, PACKED> next[kParts];
     if (nv > 0) load(p, 0, next);
@@ -221,7 +224,7 @@ __global__ void __launch_bounds__(kWeightThreads, 2)
         load(p, v + kParts, next);
       }
       const int k0 = (p.t0 + warp + kWeightWarps * (v >> 2)) * kWeightKeys + 8 * (v & 3);
-      const bool masked = ragged || k0 + 8 * kParts > (a.causal ? p.len - a.n_q + 1 : p.len);
+      const bool masked = some_dead || k0 + 8 * kParts > (a.causal ? p.len - a.n_q + 1 : p.len);
       float* to = f.weights + p.b * f.stride_b + p.h * f.stride_h + k0;
       // lanes t = 0, 1 have keys g, g + 8 of 16 to write
       const int mine = g + 8 * (t & 1);

@@ -61,6 +61,20 @@ __device__ __forceinline__ uint32_t idesc_half(int M, int N) {
   return (1u << 4) | ((static_cast<uint32_t>(N) >> 3) << 17) | ((static_cast<uint32_t>(M) >> 4) << 24);
 }
 
+// Whether x holds for any thread of the summing warps.
+__device__ __forceinline__ bool any_of_sums(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "barrier.cta.red.or.pred p, 2, %2, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(x ? 1u : 0u), "n"(32 * kSumWarps)
+      : "memory");
+  return r != 0;
+}
+
 // A position in a ring of n stages, over the whole kernel.
 struct RingAt {
   int stage = 0;
@@ -134,9 +148,11 @@ __global__ void __launch_bounds__(TileCfg<D, PACKED>::kThreads, 1)
     for (int r0 = 0; ok && r0 < a.head_rows; r0 += f.pass_rows) {
       const int nrows = min(a.head_rows - r0, f.pass_rows);
       const int blocks = (nrows + kRowsAtOnce - 1) / kRowsAtOnce;
-      // ---- Q and its rows' limits; a row that gives nothing and what lies past the last
-      // one is zero
+      // ---- Q and its rows' limits; what lies past the last row is zero.  A row that gives
+      // nothing may hold anything, and an infinite key makes NaN of zeros as well: where
+      // there is one, what a row gives is chosen by its limit.
       // (the scores of the pass before have all been read, so its products are complete)
+      bool some_dead = false;
       if (warp < kSumWarps) {
         for (int i = threadIdx.x; i < blocks * kRowsAtOnce * kPerRow; i += 32 * kSumWarps) {
           const int r = i / kPerRow, c8 = i % kPerRow, at = p.h * a.head_rows + r0 + r;
@@ -171,25 +187,18 @@ __global__ void __launch_bounds__(TileCfg<D, PACKED>::kThreads, 1)
           }
           if (PACKED && c8 == 0) row_c[r] = c2;
         }
+        bool dead = false;
         for (int r = threadIdx.x; r < blocks * kRowsAtOnce; r += 32 * kSumWarps) {
           const int at = p.h * a.head_rows + r0 + r;
           const float L = r < nrows ? f.lse[static_cast<int64_t>(p.b) * a.all_rows + at] : -INFINITY;
           const bool gives = L != -INFINITY;
+          dead = dead || (r < nrows && !gives);
           row_l[r] = gives ? -L * kLog2Of : -INFINITY;
           row_lim[r] =
               gives ? (a.causal ? min(p.len, p.len - a.n_q + at % a.n_q + 1) : p.len) : 0;
         }
+        some_dead = any_of_sums(dead);
         copies_wait();
-        // a row that gives nothing may hold anything: zeros in its place (asking for L before
-        // the copies are made took 3 us more)
-        named_barrier_sync(2, 32 * kSumWarps);
-        for (int r = threadIdx.x; r < nrows; r += 32 * kSumWarps)
-          if (row_l[r] == -INFINITY) {
-            uint8_t* to = sQ + r / kRowsAtOnce * C::kTileBytes + r % kRowsAtOnce * 128;
-            for (int i = 0; i < kPerRow; ++i)
-              *reinterpret_cast<uint4*>(to + (i >> 3) * C::kBoxBytes + ((i & 7) << 4)) =
-                  make_uint4(0u, 0u, 0u, 0u);
-          }
         fence_proxy_async_smem();
       }
       // (the copies need not wait for Q)
@@ -199,7 +208,8 @@ __global__ void __launch_bounds__(TileCfg<D, PACKED>::kThreads, 1)
         const int group = warp >> 2;
         RingAt& mine = s_at[0];
         const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        const int open = a.causal ? p.len - a.n_q + 1 : p.len;   // every row attends keys below it
+        // every row attends keys below it
+        const int open = some_dead ? 0 : a.causal ? p.len - a.n_q + 1 : p.len;
         const bool add = f.add || r0 > 0;
         for (int t = 0; ok && t < n; ++t, ++k_seen) {
           if ((k_seen & 1) != group) continue;
