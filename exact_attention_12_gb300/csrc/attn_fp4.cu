@@ -20,9 +20,10 @@
 //     before they are converted, two operations per four pairs;
 //   * P^T comes from S^T by movmatrix, without shared memory.
 // Q enters as fp16, scaled by a power of two per row so that its largest element
-// is in [2^14, 2^15): exact for elements down to 2^-31 of that one.  P is
-// rounded to fp16 (a relative 2^-11, of p below 2^-14 an absolute 2^-25), the row
-// sums are of the unrounded fp32 values, S, m, l, O are fp32.
+// is in [2^14, 2^15): exact for elements down to 2^-31 of that one.  P, up to 2^7 where a
+// maximum is taken, is rounded to fp16 (a relative 2^-11, of p below 2^-21 of the largest
+// an absolute 2^-32 of it), the row sums are of the unrounded fp32 values, S, m, l, O are
+// fp32.
 //
 // The keys of all sequences are divided evenly over the CTAs (attn_paged.cuh).
 // A slot (MT warps, 16 rows each; one warp up to 16 rows) streams its own 32-key
@@ -44,7 +45,6 @@ using namespace sm103;
 
 namespace {
 
-constexpr float kLazy = 8.f;
 constexpr float kLn2 = 0.69314718f;
 constexpr float kNone = -3e38f;   // a row's maximum before its first key
 
@@ -75,7 +75,7 @@ struct Fp4Cfg {
 
 template <int D, int NT, int MT>
 struct Fp4Shared {
-  float m[Fp4Cfg<D, NT, MT>::kSlots][Fp4Cfg<D, NT, MT>::kRows];   // largest score, log2 units
+  float m[Fp4Cfg<D, NT, MT>::kSlots][Fp4Cfg<D, NT, MT>::kRows];   // maximum taken, log2 units
   float l[Fp4Cfg<D, NT, MT>::kSlots][Fp4Cfg<D, NT, MT>::kRows];
   float c2[Fp4Cfg<D, NT, MT>::kQRows];   // (kSharedQ)
   float L[Fp4Cfg<D, NT, MT>::kRows];     // of the CTA's rows, for the cluster
@@ -441,15 +441,15 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
             }
           }
       }
-      // The maximum that the scores are taken against follows only where a score
-      // is 2^kLazy above it (P then stays below 2^kLazy, far inside fp16's range).
+      // The maximum that the scores are taken against follows only where P would pass
+      // 2^kPLazy.  (Rounded up: of scores so large that fp32 has no halves P stays there.)
       bool over = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float top = fmaxf(fmaxf(sc[0][n][i], sc[0][n][2 + i]), fmaxf(sc[1][n][i], sc[1][n][2 + i]));
-          over = over || fmaf(top, c2[n][i], -kLazy) > m[n][i];
+          over = over || __fmaf_ru(top, c2[n][i], -kPLazy) > m[n][i];
         }
       if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NT, MT>::kThreads, Fp4Cfg<D, NT, MT>
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            const float mn = fmaxf(m[n][i], top * c2[n][i]);
+            const float mn = fmaxf(m[n][i], fmaf(top, c2[n][i], -kPTop));
             const float alpha = ex2_approx(m[n][i] - mn);
             m[n][i] = mn;
             l[n][i] *= alpha;

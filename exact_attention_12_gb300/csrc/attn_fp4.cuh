@@ -73,6 +73,12 @@ constexpr int kWeightMinUnits = 16;
 
 constexpr float kLog2Of = 1.4426950408889634f;   // log2(e)
 
+// Decode: P is 2^(S c - m), m the row's maximum less kPTop, taken again only when a
+// score passes m by more than kPLazy: P reaches 2^15 (fp16's end is 2^16), so what fp16
+// cannot hold begins 2^32 below the maximum, not 2^25, and costs nothing.
+constexpr float kPTop = 7.f;
+constexpr float kPLazy = kPTop + 8.f;
+
 cudaError_t launch_fp4_store(const Fp4CopyArgs& a, cudaStream_t s);
 cudaError_t launch_fp4_load(const Fp4CopyArgs& a, cudaStream_t s);
 cudaError_t launch_fp4_decode(const PagedArgs& a, const Fp4Args& f, int ctas, cudaStream_t s);

@@ -48,7 +48,6 @@ constexpr int kQBytes = kD / 64 * kQBox;
 constexpr int kPBytes = kTile * 2 * kRowsMax;
 constexpr int kTileSmem = 1024 + kTileStages * (2 * kKeysBytes + kPBytes) + kQBytes;
 constexpr uint32_t kSCol = 0, kOCol = kTileStages * kRowsMax, kTmemCols = 256;
-constexpr float kLazyLimit = 8.f;
 constexpr float kNoScore = -3e38f;                 // a row's maximum before its first key
 constexpr int kAhead = 6;                          // tiles that are fetched into L2 ahead
 
@@ -413,7 +412,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int i = 0; i < kGroupRows; i += 2)
           most = max3f(most, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-        if (any_of_group(wg, most > kLazyLimit || !ok)) {
+        if (any_of_group(wg, most > kPLazy || !ok)) {
           if ((bad = any_of_group(wg, !ok))) break;
           // new maxima: of the tile's scores, row by row
           tmem_read(sc, s);
@@ -421,7 +420,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
           for (int i = 0; i < kGroupRows; ++i) {
             const float top = warp_max(
-                key < ctl.lim[r0 + i] ? __uint_as_float(s[i]) * ctl.c2[r0 + i] : -INFINITY);
+                key < ctl.lim[r0 + i] ? fmaf(__uint_as_float(s[i]), ctl.c2[r0 + i], -kPTop) : -INFINITY);
             if (lane == i) mine = top;
           }
           if (lane < kGroupRows) ctl.part[warp & 3][r0 + lane] = mine;

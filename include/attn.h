@@ -370,8 +370,10 @@ attn_status attn_pages_load_fp4(const attn_params* p, const attn_pages* pages,
 /* attn_decode_paged on such a cache (the kv strides of p are ignored, shared_len
  * must be 0): what it says of rows, masks, lengths and of values that are not
  * attended holds here.  Q and P enter the products in fp16, Q scaled by a power
- * of two per row; keys and values as they are.  S, L and O in fp32, O rounded
- * to bf16. */
+ * of two per row, P to be 2^7 where a row's maximum is taken: keys 2^32 below it
+ * begin to be lost.  Keys and values as they are.  S, L and O in fp32, O rounded
+ * to bf16.  Scores (scale q k) stay below 2^27 in magnitude; fp32 tells larger ones
+ * apart by 16 and more, which P does not reach. */
 size_t attn_decode_fp4_workspace_size(const attn_params* p, int32_t n_q, const attn_pages* pages);
 attn_status attn_decode_fp4(const attn_params* p, int32_t n_q, const attn_pages* pages,
                             const void* q, const attn_fp4* k, const attn_fp4* v, void* o,

@@ -5,9 +5,11 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_fp4 import E4M3
+from oracle import fp4, paged as oracle
+from tests.helpers import L_MAX_ABS, np64
+from tests.test_gpu_fp4 import E4M3, _cache, _on_gpu
 from tests.test_gpu_pages import _i
-from tests.test_gpu_paged import ea  # noqa: F401
+from tests.test_gpu_paged import WIDE, _table, ea  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -91,3 +93,63 @@ def test_a_head_of_dead_rows_gives_nothing_to_any_key(ea, rows, d, packed):  # n
     assert torch.isfinite(w[0, 1]).all() and (w[0, 1, :700] > start[0, 1, :700]).all()
     w = ea.attention_key_weights(q.cuda(), keys, t, n, lse.cuda(), start.clone(), scale=0.02, add=False, **kw)
     assert torch.all(w[0, 0, :700] == 0) and torch.equal(w[0, :, 700:], start[0, :, 700:])
+
+
+# ------------------------------------------------------------ 4-bit decode --
+
+# rows a head in one to four blocks of 8, two warps a tile, tcgen05 (a long table, d = 128)
+ROWS = [(1, 64, 0), (8, 128, 0), (16, 64, 0), (16, 128, WIDE), (32, 128, 0), (32, 64, WIDE), (40, 128, 0),
+        (40, 64, WIDE), (40, 128, WIDE), (64, 128, WIDE)]
+
+
+@pytest.mark.parametrize("gap", [20, 26, 28.5, 31])
+@pytest.mark.parametrize("rows,d,room", ROWS)
+def test_small_probabilities_count(ea, rows, d, room, gap):  # noqa: F811
+    """Every 32nd key has a score `gap` log2 units above the others, and a value of 0 where
+    theirs is 1: O is what the small probabilities add up to.  P has 11 bits down to 2^-21
+    of the row's largest, below that an absolute 2^-32 of it; L_MAX_ABS for the scores and
+    for L; O rounded to bf16."""
+    page, n = 64, 2048
+    P = n // page
+    codes = torch.full((P, 1, page, d // 2), 0x22, dtype=torch.uint8, device="cuda")    # ones
+    codes[:, :, ::32] = 0
+    scales = torch.full((P, 1, page, d // 16), 0x38, dtype=torch.uint8, device="cuda").view(E4M3)
+    q = torch.full((1, rows, 1, d), -1.0, dtype=torch.bfloat16, device="cuda")
+    table = torch.full((1, P + room // page), -1, dtype=torch.int32, device="cuda")
+    table[0, :P] = torch.arange(P)
+    o, lse = ea.attention_decode_fp4(q, codes, scales, codes, scales, table, _i([n]),
+                                     scale=gap * float(np.log(2)) / d)
+    ea.check()
+    tail = 31 * 2.0 ** -gap
+    want = tail / (1 + tail)
+    bound = 1.01 * ((2.0 ** -11 + 2 * L_MAX_ABS + 2.0 ** -8) * want + 31 * 2.0 ** -32)
+    assert (o.double() - want).abs().max().item() <= bound
+    assert (lse.double() - np.log(n / 32 * (1 + tail))).abs().max().item() <= L_MAX_ABS
+
+
+@pytest.mark.parametrize("rows,d,room", ROWS)
+@pytest.mark.parametrize("scale", [1e3, 1e5, 5e5])
+def test_scores_of_a_hundred_million(ea, rows, d, room, scale):  # noqa: F811
+    # (up to 2^27: a key is attended alone, the next score being far below)
+    n, page = 1024, 64
+    rng = np.random.default_rng(rows)
+    table, P = _table(rng, [n], page, room=room)
+    (kc, ks), (vc, vs) = (_cache(rng, table, [n], P, 1, page, d) for _ in range(2))
+    ks[...] = 0x38
+    q = torch.randn(1, rows, 1, d, generator=torch.Generator().manual_seed(rows)).to(torch.bfloat16)
+    o, lse = ea.attention_decode_fp4(q.cuda(), *_on_gpu(kc, ks), *_on_gpu(vc, vs),
+                                     torch.from_numpy(table).cuda(), _i([n]), scale=scale)
+    ea.check()
+    k, v = (oracle.gather(fp4.decode(c, s, 1.0), table[0], n)[0] for c, s in ((kc, ks), (vc, vs)))
+    s = np64(q)[0, :, 0] @ k.T * scale
+    first, second = np.sort(s)[:, -1], np.sort(s)[:, -2]
+    assert 30 * scale < first.min() and first.max() < 2.0 ** 27
+    # S is a sum of d exact products, truncated rather than rounded
+    off = 2 * (d + 8) * 2.0 ** -24 * scale * (np.abs(np64(q)[0, :, 0]) @ np.abs(k).T).max()
+    alone = first - second > 40 + 2 * off
+    assert alone.mean() > 0.7
+    want = v[s.argmax(1)]
+    # P and the sum are the same number, P rounded to fp16; O to bf16
+    far = np.abs(np64(o)[0, :, 0] - want) / (np.abs(want) + 1e-30)
+    assert far[alone].max() <= 1.01 * (2.0 ** -11 + 2.0 ** -8)
+    assert np.all(np.abs(np64(lse)[0, :, 0] - first) <= off + 2.0 ** -21 * first + 1)
