@@ -7,6 +7,7 @@ import torch
 
 from oracle import fp4, paged as oracle
 from tests.helpers import L_MAX_ABS, np64
+from tests.test_gpu_eviction import Evicting
 from tests.test_gpu_fp4 import E4M3, _cache, _on_gpu
 from tests.test_gpu_pages import _i
 from tests.test_gpu_paged import WIDE, _table, ea  # noqa: F401
@@ -93,6 +94,55 @@ def test_a_head_of_dead_rows_gives_nothing_to_any_key(ea, rows, d, packed):  # n
     assert torch.isfinite(w[0, 1]).all() and (w[0, 1, :700] > start[0, 1, :700]).all()
     w = ea.attention_key_weights(q.cuda(), keys, t, n, lse.cuda(), start.clone(), scale=0.02, add=False, **kw)
     assert torch.all(w[0, 0, :700] == 0) and torch.equal(w[0, :, 700:], start[0, :, 700:])
+
+
+@pytest.mark.parametrize("rows", [4, 40, 130, 600])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("page", [16, 64, 256])
+def test_bad_pages_of_keys_read_as_zeros_and_are_reported(ea, rows, d, packed, page):  # noqa: F811
+    keys, kw = _keys(packed, d, 1, rows, pages=768 // page + 1, page=page)
+    P = keys.shape[0]
+    for x in (keys, *(y for y in kw.values() if torch.is_tensor(y))):
+        x[P - 1].view(torch.uint8).zero_()
+    q = torch.randn(2, rows, 1, d, generator=torch.Generator().manual_seed(d)).to(torch.bfloat16).cuda()
+    lse = torch.full((2, rows, 1), 6.0, device="cuda")
+    table = torch.tensor([list(range(P - 1))] * 2, dtype=torch.int32)
+    bad, zero = table.clone(), table.clone()
+    for b, j, value in ((0, 0, -1), (0, (P - 1) // 2, 2 ** 31 - 1), (1, P - 2, P + 5)):
+        bad[b, j], zero[b, j] = value, P - 1
+    n = _i([730, 768])
+    got = []
+    for t, pages, fails in ((zero, P, False), (bad, P - 1, True)):
+        got.append(ea.attention_key_weights(
+            q, keys[:pages], t.cuda(), n, lse, torch.zeros(2, 1, 768, device="cuda"), scale=0.02,
+            **{k: x[:pages] if torch.is_tensor(x) else x for k, x in kw.items()}))
+        if fails:
+            with pytest.raises(ea.AttnError) as e:
+                ea.check()
+            assert e.value.status == 6
+        ea.check()
+    assert torch.equal(*got) and got[0][0, 0, :730].min() > 0
+
+
+# ---------------------------------------------------------------- eviction --
+
+def test_hundreds_of_sequences(ea):  # noqa: F811
+    # (more than the moves keep at hand)
+    rng = np.random.default_rng(14)
+    lens = [int(x) for x in rng.integers(0, 70, 320)]
+    e = Evicting(14, lens, 16, rows=330)
+    seqs = [int(x) for x in rng.permutation(320)[:300]]
+    e.evict(ea, seqs, [int(rng.integers(0, 60)) for _ in seqs], 6)
+    e.evict(ea, list(range(320)), [int(x) for x in rng.integers(0, 30, 320)], 0)
+
+
+# rows of 3, 8 and 32 KB: chunks of 8, 4 and one key
+@pytest.mark.parametrize("d", [770, 2048, 8192])
+def test_wide_rows(ea, d):  # noqa: F811
+    e = Evicting(d, [400, 33, 90], 16, d=d)
+    e.evict(ea, [2, 0, 1], [50, 213, 32], 9)
+    e.evict(ea, [0, 1], [1, 31], 0)
 
 
 # ------------------------------------------------------------ 4-bit decode --
