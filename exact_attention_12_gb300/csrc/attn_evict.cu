@@ -23,9 +23,15 @@
 // Bound: HBM, the moved rows twice and the weights once; on a short cache the
 // two launches.
 // Measured (8 heads, d = 128; 4 us of each are copies that put the state back): 32
-// sequences of 2048-8192 bf16 keys to 4096, 660 MB moved, 149 us; 4 of 95000 4-bit keys
-// to 24000, 87 us, of them 26 the selection; one of 333 keys to 256, 14 us.  With a
-// kernel of its own for the pages and the weights behind the new length: 156, 91, 16.
+// sequences of 2048-8192 bf16 keys to 4096, 656 MB moved (96 us at the copy rate), 149 us, of
+// them 22 the selection; 4 of 95000 4-bit keys to 24000, 87 us, of them 26 the selection;
+// one of 333 keys to 256, 14 us.  With a kernel of its own for the pages and the weights
+// behind the new length: 156, 91, 16.
+// The choice of variants goes by the room of the table and of the weights, as the lengths
+// are on the device: the 32 sequences with room for 40960, 65536, 131072 keys take 155, 159,
+// 172 us without those copies, 145 with room for their 8192 (slots are written as far as
+// the weights reach; from 40961 on the weights stay in global memory and the moves take
+// them along).  One sequence of 400000 keys to 100000, one head, d = 64: 123 us.
 #include <climits>
 #include <cstdio>
 
@@ -624,7 +630,9 @@ EvictLayout evict_layout(const attn_page_table* t, int heads, int n, const attn_
 }
 
 // CTAs per (sequence, head) of the first kernel: as many as leave each some
-// thousands of weights, while the GPU has room for them.
+// thousands of weights, while the GPU has room for them.  4096 / 1024 / 16384 weights: one
+// sequence of 8192 keys 24.1 / 22.7 / 25.2 us, 4 of 16384 69 / 70 / 77.  Two CTAs an SM / one /
+// six: 32 of 2048-8192 149 / 149 / 159, 4 of 95000 87 / 93 / 87.
 int select_cluster(int64_t cap, int64_t items) {
   int c = 1;
   while (c < kMaxCluster && cap > 4096ll * c && items * c * 2 <= 2 * multiprocessors()) c *= 2;

@@ -26,7 +26,7 @@
 // fp32.
 //
 // The keys of all sequences are divided evenly over the CTAs (attn_paged.cuh).
-// A slot (MT warps, 16 rows each; one warp up to 16 rows) streams its own 32-key
+// A slot (one warp up to 32 rows; above, two warps of 32 rows each) streams its own 32-key
 // tiles by 16-byte asynchronous copies through its own ring; what is no page
 // is filled with zeros.  Value rows past the end of a sequence may hold
 // anything: their scores are replaced, their values' scales are taken as zero.
@@ -35,7 +35,11 @@
 // rows, d = 128, 604 MB in 115 us = 5.2 TB/s; 16 rows 155 us; 32 rows 230 us.  16
 // sequences of 4096-8192 keys 31 us, floor 17; one of 517 keys 6.5 us.  At 4 rows 323
 // warp instructions for 16 keys take 62 % of the issue slots; at 32 rows 478, and the
-// warp MMAs half of the tensor cores' time, with eight warps on an SM.
+// warp MMAs half of the tensor cores' time, with eight warps on an SM.  d = 64: 64
+// sequences of 16384 keys, 4 heads, 32 rows 135 us, 33 to 64 rows 280 (every value is
+// unpacked once per 32 rows).  512 queries on 16384 keys, 8 heads, d = 128: 347 us, the
+// cache unpacked once per 64 rows (attn_fp4_tile.cu).  Spills of the balanced split at d =
+// 128: 144 bytes up to 16 rows (168 registers), 72 up to 32 (255), none up to 8.
 #include <type_traits>
 
 #include "attn_fp4.cuh"

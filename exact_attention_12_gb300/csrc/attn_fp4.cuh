@@ -64,9 +64,16 @@ cudaError_t launch_key_weights_tile(const CUtensorMap& tk, const PagedArgs& a, c
 // Rows of a head above which it is taken: 8 sequences of 8192 keys, 4 heads, 24 rows
 // 18.3 us with it, 16.9 without; 40 rows 18.8 and 20.2; 128 rows 18.5 and 37.2.
 constexpr int kWeightTileRows = 32;
-constexpr int kWeightTileOverhead = 2;    // a segment's cost beside its 128-key tiles
+// A segment's cost beside its 128-key tiles, 2 / 1 / 6: 64 sequences of 0-8192 keys, 64
+// rows 108 / 115 / 103 us; 200 of 0-1000 77 / 83 / 68; two of 16384, 128 rows 18.5 / 19.3 /
+// 17.5.
+constexpr int kWeightTileOverhead = 2;
 cudaError_t launch_key_weights(const PagedArgs& a, WeightArgs f, int ctas, cudaStream_t s);
 
+// Up to kWeightTileRows rows, in tiles of 32 keys.  A segment's cost beside them, 8 / 2 /
+// 20: 64 sequences of 0-8192 keys, 4 rows 93 / 101 / 92 us, one of 517 keys 7.3 / 8.5 / 6.9.
+// Units a CTA takes at least, 16 / 4 / 48: one of 517 keys 7.3 / 5.4 / 11.8, one of 4096
+// 7.1 / 6.0 / 12.2, long caches the same.
 constexpr int kWeightKeys = 32;
 constexpr int kWeightOverhead = 8;
 constexpr int kWeightMinUnits = 16;
@@ -89,7 +96,9 @@ cudaError_t launch_fp4_decode(const PagedArgs& a, const Fp4Args& f, int ctas, cu
 // keys, 32 rows 286 / 245.
 constexpr int kFp4Keys = 32;
 constexpr int fp4_overhead(int rows) { return rows <= 16 ? 8 : 20; }
-constexpr int kFp4MinUnits = 6;       // units a CTA takes at least
+// Units a CTA takes at least, 6 / 2 / 18 (room for 32768 keys): one sequence of 517 keys
+// 8.7 / 8.0 / 12.2, 4 of 4096 12.6 / 12.6 / 15.5.
+constexpr int kFp4MinUnits = 6;
 // Tiles (at full caches) from which on a segment takes more than one CTA: 100 keys
 // one CTA 4.5, two 6.2; 517 keys one 8.0, eight 6.4.
 constexpr int kFp4ClusterFrom = 8;
@@ -104,11 +113,15 @@ constexpr int fp4_cluster_tiles(int rows) { return rows <= 32 ? 24 : 12; }
 constexpr int kFp4SoloTiles = 24;
 constexpr int kFp4ManyTiles = 64;
 
-// Above 32 rows, d = 128, the balanced split goes to attn_fp4_tile.cu: tiles of 128 keys,
-// and its own constants in such tiles.  64 sequences of 16384 keys, 4 heads, 36 rows
+// Above 32 rows, d = 128, the balanced split goes to attn_fp4_tile.cu (which is written for
+// 128 columns, TMEM's lanes of O^T): tiles of 128 keys, and its own constants in such
+// tiles.  64 sequences of 16384 keys, 4 heads, 36 rows
 // 299 us, attn_fp4.cu 469; 64 rows 303 and 474; 32 rows, with two tiles of 32 rows at a
 // time, 269 and 230.
 cudaError_t launch_fp4_tile(const PagedArgs& a, const Fp4Args& f, int ctas, cudaStream_t s);
+// A segment's cost beside its tiles, 4 / 1 / 10: 64 sequences of 0-16384 keys, 64 rows 175 /
+// 204 / 176, 200 of 0-4000 166 / 191 / 171.  Units a CTA takes at least, 5 / 2 / 15: one of
+// 2000 keys, 64 rows 16.9 / 12.8 / 31.1, 64 of 0-16384 the same.
 constexpr int kFp4TileOverhead = 4;
 constexpr int kFp4TileMinUnits = 5;
 constexpr bool fp4_in_tiles(int rows, int d) { return rows > 32 && d == 128; }

@@ -161,7 +161,9 @@ __device__ __forceinline__ uint32_t quantised(const uint4& w, float descale, flo
   return codes;
 }
 
-constexpr int kAtOnce = 4;   // heads whose loads are on the way together
+// Heads whose loads are on the way together, 4 / 2 / 8: 8 prompts stored and loaded 92 /
+// 100 / 92 us, 64 tokens 4.9 / 4.5 / 5.5.
+constexpr int kAtOnce = 4;
 
 template <int D>
 __global__ void __launch_bounds__(kFp4Threads) fp4_store_kernel(const Fp4CopyArgs a, int tile_shift) {

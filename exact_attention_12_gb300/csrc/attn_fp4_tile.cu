@@ -18,7 +18,8 @@
 //   warps 20-27  unpacking, four K and four V: four lanes a key, their 16 bytes of codes
 //                and two scales a tile ahead in registers and six in L2
 // 64 sequences of 16384 keys, 4 heads, 64 rows (604 MB): 303 us, 2.0 TB/s; 2900 clocks a
-// tile.  Its 7500 warp instructions take 65 % of the issue slots, its way through shared
+// tile.  Its 7150 warp instructions take 67 % of the issue slots (136 bytes of spills at 72
+// registers), its way through shared
 // memory (unpacked values in, operands out) 1400 clocks, and the groups go from a score
 // to its weight in step; the tensor cores are busy for a sixth.  S and O from two
 // issuing warps: 318.

@@ -18,7 +18,8 @@
 //     shuffles.
 // Keys in 4 bits are unpacked as in attn_fp4.cu (exactly, to fp16).
 // Measured: 16 sequences of 2048-8192 keys, 32 heads over 8, d = 128, 173 MB in 30 us
-// = 5.8 TB/s.
+// = 5.8 TB/s; 16 of 8192 277 MB in 45 us, of a cache in 4 bits 84 MB in 29 us (floor 12):
+// the unpacking, for 4 rows.
 #include "attn_fp4.cuh"
 
 namespace attn {

@@ -331,8 +331,8 @@ attn_status attn_decode_latent(const attn_params* p, int32_t n_q, const attn_pag
  * key where bf16 has 2 d.  Codes and scales are two buffers of pages: codes
  * [num_pages][H_kv][page_size][d / 2], scales [num_pages][H_kv][page_size][d / 16];
  * a head's rows of a page follow one another without gaps, pages and heads may
- * be apart (what is written to must not overlap).  attn_pages_copy, _fork, _compact and _evict take them as pools.
- * (The pages about attention have no counterpart.) */
+ * be apart (what is written to must not overlap).  attn_pages_copy, _fork, _compact
+ * and _evict take them as pools.  (The pages about attention have no counterpart.) */
 typedef struct attn_fp4 {
   void* codes;               /* 16-byte aligned, as is scales */
   void* scales;
@@ -373,7 +373,8 @@ attn_status attn_pages_load_fp4(const attn_params* p, const attn_pages* pages,
  * of two per row, P to be 2^7 where a row's maximum is taken: keys 2^32 below it
  * begin to be lost.  Keys and values as they are.  S, L and O in fp32, O rounded
  * to bf16.  Scores (scale q k) stay below 2^27 in magnitude; fp32 tells larger ones
- * apart by 16 and more, which P does not reach. */
+ * apart by 16 and more, which P does not reach.  Limits as there, the last one
+ * being B * H_kv * ceil(rows / 64) * (p->N / 32 + 21) < 2^31. */
 size_t attn_decode_fp4_workspace_size(const attn_params* p, int32_t n_q, const attn_pages* pages);
 attn_status attn_decode_fp4(const attn_params* p, int32_t n_q, const attn_pages* pages,
                             const void* q, const attn_fp4* k, const attn_fp4* v, void* o,
@@ -385,7 +386,9 @@ attn_status attn_decode_fp4(const attn_params* p, int32_t n_q, const attn_pages*
  * added to weights[b, h, j] (add != 0) or written there, for j < key_lens[b];
  * further entries stay as they are.  Rows, masks and positions as in
  * attn_decode_paged, whose lse [B, H, n_q] this takes; a row with lse = -inf gives
- * nothing.  Summed in fp32 in an order that does not depend on timing.
+ * nothing, whatever its queries and the keys hold.  Summed in fp32 in an order that
+ * does not depend on timing.  Limits as there, rows in one piece: the last one is
+ * B * H_kv * (p->N / 32 + 9) < 2^31.
  *   k         [num_pages, H_kv, page_size, d] bf16 with the kv strides, or NULL and
  *   k_cache   a cache in 4 bits (then NULL otherwise)
  *   weights   fp32, weight_stride_b and weight_stride_h entries between sequences
